@@ -301,6 +301,173 @@ int32_t nvfp4_mla_stage_fp8(const int32_t* q_seq, const int32_t* topk_idx, int32
                             int64_t block_stride_bytes, float latent_scale, void* staged,
                             int32_t* staged_idx, int32_t* invalid_count, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Step planning: block tables and slot maps from request lengths.
+ *
+ * A serving step adds new_lens[s] tokens to sequence s. The pool's unused
+ * pages are kept on a stack: free_pages[0 .. *free_count) of
+ * free_pages[free_capacity], the top at the highest index. Each page belongs
+ * to one sequence. Both entry points are one launch, read nothing on the
+ * host and depend on the sizes only through their arguments, so a captured
+ * graph that holds them advances the state at every replay. They may not run
+ * at the same time as each other on the same stack or table.
+ *
+ * nvfp4_mla_plan_step: for sequence s of length L = seq_lens[s] with
+ * n = new_lens[s] tokens, ceil((L+n)/page_size) - ceil(L/page_size) pages
+ * are taken from the top of the stack, in sequence order, and entered into
+ * block_table[s] behind its ceil(L/page_size) pages. Requests are served
+ * whole and in order: once one does not find its pages, no later one that
+ * needs a page is served, and once one does not fit into max_tokens, no
+ * later one with tokens is. Invalid requests (n < 0, L < 0, L + n beyond
+ * max_blocks_per_seq pages) are refused and change nothing for the others.
+ *
+ *   new_lens     device int32 [num_seqs]
+ *   seq_lens     device int32 [num_seqs]: lengths before the step
+ *   num_seqs     1..NVFP4_MLA_MAX_PLAN_SEQS
+ *   block_table  device int32 [num_seqs, max_blocks_per_seq], updated; the
+ *                entries of the pages taken are written, no others
+ *   page_size    1..2^20, max_blocks_per_seq * page_size < 2^31
+ *   free_pages   device int32 [free_capacity], read only; free_capacity >= 0
+ *   free_count   device int32 [1] (clamped to 0..free_capacity)
+ *   max_tokens   >= 0: rows of seq_ids, positions and slots
+ *   seq_lens_out device int32 [num_seqs]: lengths after the step; may be
+ *                seq_lens itself
+ *   free_count_out device int32 [1]; may be free_count itself
+ *   seq_ids, positions  device int32 [max_tokens]: the step's tokens, packed
+ *                in sequence order; rows behind the last token get -1. They
+ *                are what nvfp4_mla_append, nvfp4_mla_index_append and
+ *                sparse_mla_select (as q_seq, q_pos) take
+ *   slots        nullable device int64 [max_tokens]: page * page_size + row,
+ *                -1 behind the last token or where the page id is negative
+ *   cu_tokens    nullable device int32 [num_seqs + 1]: first token of each
+ *                sequence, then the number of tokens
+ *   refused_count nullable device int32: += sequences with new_lens != 0
+ *                that were not served (atomicAdd; the caller zeroes it)
+ *
+ * nvfp4_mla_truncate: sequences with 0 <= keep_lens[s] < seq_lens[s] shrink
+ * to keep_lens[s] (0: the request ended); the others keep their length. The
+ * non-negative entries of block_table[s] from block ceil(keep/page_size) to
+ * block ceil(L/page_size) - 1 go back onto the stack, the first one (by
+ * sequence, then block) topmost: truncating to the lengths before a
+ * nvfp4_mla_plan_step restores that step's stack. The table is read only:
+ * entries past a sequence's length are stale until a step takes them anew.
+ * Pages that do not fit below free_capacity are dropped (the topmost ones)
+ * and counted.
+ *
+ *   keep_lens, seq_lens, seq_lens_out  device int32 [num_seqs]; seq_lens_out
+ *                may be seq_lens itself
+ *   block_table  device int32 [num_seqs, max_blocks_per_seq]
+ *   free_pages   device int32 [free_capacity], entries from *free_count on
+ *                are written
+ *   free_count, free_count_out  device int32 [1]; may be the same
+ *   dropped_count nullable device int32: += pages dropped
+ */
+#define NVFP4_MLA_MAX_PLAN_SEQS 16384
+
+int32_t nvfp4_mla_plan_step(const int32_t* new_lens, const int32_t* seq_lens, int32_t num_seqs,
+                            int32_t* block_table, int32_t max_blocks_per_seq, int32_t page_size,
+                            const int32_t* free_pages, int32_t free_capacity,
+                            const int32_t* free_count, int32_t max_tokens, int32_t* seq_lens_out,
+                            int32_t* free_count_out, int32_t* seq_ids, int32_t* positions,
+                            int64_t* slots, int32_t* cu_tokens, int32_t* refused_count,
+                            void* stream);
+
+int32_t nvfp4_mla_truncate(const int32_t* keep_lens, const int32_t* seq_lens, int32_t num_seqs,
+                           const int32_t* block_table, int32_t max_blocks_per_seq,
+                           int32_t page_size, int32_t* free_pages, int32_t free_capacity,
+                           const int32_t* free_count, int32_t* seq_lens_out,
+                           int32_t* free_count_out, int32_t* dropped_count, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The index-key cache: one 128-value key per token, by which
+ * sparse_mla_select scores it. It lives in a pool of its own with the
+ * block table of the latent cache: page p starts at byte
+ * p * block_stride_bytes and holds page_size * 64 bytes of E2M1 codes
+ * (element 2i of a row in the low nibble of its byte i), then page_size * 8
+ * bytes of E4M3 scales (one per 16 values). Encoding as for the latent
+ * values of an NVFP4 row: scale = E4M3(amax/6), code = nearest E2M1.
+ *
+ * nvfp4_mla_index_append: encode n_tok keys into their rows.
+ * nvfp4_mla_index_read: the values that the rows of n_tok tokens stand for
+ * (code * scale, exact in bf16); 0 for a token that does not resolve.
+ *
+ *   keys         device bf16 [n_tok, 128], row-major, 16-byte aligned; finite
+ *   seq_ids, positions  device int32 [n_tok]; a token with seq_ids = -1 is
+ *                padding (not written, not counted)
+ *   cache        device, 16-byte aligned
+ *   block_stride_bytes  multiple of 16, >= page_size * 72
+ *   page_size    even (the scales of a page start 16-byte aligned)
+ *   invalid_count nullable device int32: += tokens, other than padding,
+ *                that do not resolve to a row
+ * n_tok = 0 is a no-op. Two tokens that resolve to the same row race.
+ */
+#define NVFP4_MLA_INDEX_DIM 128
+#define NVFP4_MLA_INDEX_ROW_BYTES 72
+
+int32_t nvfp4_mla_index_append(const void* keys, const int32_t* seq_ids, const int32_t* positions,
+                               int32_t n_tok, const int32_t* block_table, int32_t num_seqs,
+                               int32_t max_blocks_per_seq, int32_t page_size, void* cache,
+                               int64_t num_blocks, int64_t block_stride_bytes,
+                               int32_t* invalid_count, void* stream);
+
+int32_t nvfp4_mla_index_read(const int32_t* seq_ids, const int32_t* positions, int32_t n_tok,
+                             const int32_t* block_table, int32_t num_seqs,
+                             int32_t max_blocks_per_seq, int32_t page_size, const void* cache,
+                             int64_t num_blocks, int64_t block_stride_bytes, void* keys,
+                             int32_t* invalid_count, void* stream);
+
+/*
+ * The selection that sparse_mla_decode attends to: the blocks of the context
+ * with the highest index scores, as positions.
+ *
+ * Query token t of sequence q_seq[t] at position q_pos[t] sees positions
+ * 0 .. q_pos[t] (at most max_blocks_per_seq * page_size of them). With q^ its
+ * index queries encoded as index rows are (E2M1 codes, one E4M3 scale per 16
+ * values) and k^ the stored keys,
+ *   score(t, s) = sum_j weights[t, j] * max(0, q^[t, j] . k^[s]);
+ * a NaN and a position whose page does not resolve count as -inf. The
+ * context is cut into blocks of select_block positions; a block's score is
+ * the highest of its visible positions. The first sink_blocks and the last
+ * recent_blocks visible blocks are always taken, then the highest scores up
+ * to num_select blocks in all, the lower index first where scores are equal.
+ * The choice is that of 64-bit arithmetic: scores computed in fp32 decide it
+ * only where they differ by more than their error bound.
+ *
+ *   q_index      device bf16 [num_q, num_heads, 128], 16-byte aligned, finite
+ *   weights      device fp32 [num_q, num_heads], finite
+ *   q_seq, q_pos device int32 [num_q]; a bad sequence or q_pos < 0 sees nothing
+ *   num_heads    1..128; num_q >= 0 (0 is a no-op)
+ *   block_table, num_seqs, max_blocks_per_seq, page_size  as above;
+ *                max_blocks_per_seq * page_size < 2^31
+ *   cache, num_blocks, block_stride_bytes  the index-key pool; every visible
+ *                row has been written by nvfp4_mla_index_append
+ *   select_block a power of two, 1..128
+ *   num_select   >= 1, num_select * select_block <= NVFP4_MLA_MAX_TOPK
+ *   sink_blocks, recent_blocks  >= 0, their sum <= num_select
+ *   topk_idx     device int32 [num_q, num_select * select_block]: the visible
+ *                positions of the chosen blocks, ascending, then -1. Every
+ *                entry is -2 (which sparse_mla_decode skips and counts) for
+ *                a launch in which a kernel's wait ran out
+ *                (nvfp4_mla_set_wait_limit)
+ *   workspace    device, 16-byte aligned, >= sparse_mla_select_workspace_size
+ *                bytes for the same sizes; contents need not be initialised.
+ *                Calls that can run at the same time need one each
+ * sparse_mla_select_workspace_size returns SIZE_MAX for an invalid shape.
+ * Large num_q is worked through in parts that share the workspace.
+ */
+size_t sparse_mla_select_workspace_size(int32_t num_q, int32_t num_heads,
+                                        int32_t max_blocks_per_seq, int32_t page_size,
+                                        int32_t select_block);
+
+int32_t sparse_mla_select(const void* q_index, const float* weights, const int32_t* q_seq,
+                          const int32_t* q_pos, int32_t num_q, int32_t num_heads,
+                          const int32_t* block_table, int32_t num_seqs,
+                          int32_t max_blocks_per_seq, int32_t page_size, const void* cache,
+                          int64_t num_blocks, int64_t block_stride_bytes, int32_t select_block,
+                          int32_t num_select, int32_t sink_blocks, int32_t recent_blocks,
+                          int32_t* topk_idx, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
 #ifdef __cplusplus
 } /* extern "C" */
 #endif

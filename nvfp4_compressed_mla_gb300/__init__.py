@@ -23,6 +23,8 @@ ROPE_DIM = 64
 ROW_NVFP4_352 = 0
 ROW_FP8_576 = 1
 ROW_BYTES = {ROW_NVFP4_352: 352, ROW_FP8_576: 576}
+INDEX_DIM = 128
+INDEX_ROW_BYTES = 72
 
 __all__ = [
     "LATENT_DIM", "ROPE_DIM", "ROW_NVFP4_352", "ROW_FP8_576", "ROW_BYTES", "NativeError",
@@ -30,7 +32,9 @@ __all__ = [
     "sparse_mla_decode_num_splits", "sparse_mla_decode_workspace_size", "sparse_mla_decode",
     "nvfp4_mla_set_wait_limit",
     "sparse_mla_merge_states", "nvfp4_mla_staged_rows_per_q", "nvfp4_mla_stage_fp8",
-    "staged_fp8_tables", "library_path",
+    "staged_fp8_tables", "INDEX_DIM", "INDEX_ROW_BYTES", "nvfp4_mla_plan_step",
+    "nvfp4_mla_truncate", "nvfp4_mla_index_append", "nvfp4_mla_index_read",
+    "sparse_mla_select_workspace_size", "sparse_mla_select", "library_path",
 ]
 
 
@@ -211,3 +215,199 @@ def staged_fp8_tables(num_q: int, topk: int, page_size: int, device) -> dict:
         "num_blocks": num_q * P,
         "block_stride_bytes": page_size * ROW_BYTES[ROW_FP8_576],
     }
+
+
+# ------------------------------------------------------------ step planning
+def _arg(t: torch.Tensor, name: str, dtype: torch.dtype, least: int, device: int) -> int:
+    """Device pointer of an argument with at least ``least`` values of ``dtype``."""
+    if t.dtype != dtype or t.numel() < least or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {least} values "
+                         f"on the current CUDA device")
+    return t.data_ptr()
+
+
+def _opt(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, least: int, device: int):
+    return None if t is None else _arg(t, name, dtype, least, device)
+
+
+def _table(t: torch.Tensor, device: int):
+    """Pointer, rows and columns of a block table."""
+    if t.dim() != 2:
+        raise ValueError("block_table must be [num_seqs, max_blocks_per_seq]")
+    return _arg(t, "block_table", torch.int32, 0, device), t.shape[0], t.shape[1]
+
+
+def _scratch(size: int, stream) -> torch.Tensor:
+    """A buffer that torch may hand out again once ``stream`` is past this call's work."""
+    if stream is None:
+        return torch.empty(size, dtype=torch.uint8, device="cuda")
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):
+        return torch.empty(size, dtype=torch.uint8, device="cuda")
+
+
+def nvfp4_mla_plan_step(new_lens: torch.Tensor, seq_lens: torch.Tensor, block_table: torch.Tensor,
+                        page_size: int, free_pages: torch.Tensor, free_count: torch.Tensor,
+                        max_tokens: int, seq_lens_out: Optional[torch.Tensor] = None,
+                        free_count_out: Optional[torch.Tensor] = None,
+                        seq_ids: Optional[torch.Tensor] = None,
+                        positions: Optional[torch.Tensor] = None,
+                        slots: Optional[torch.Tensor] = None,
+                        cu_tokens: Optional[torch.Tensor] = None,
+                        refused_count: Optional[torch.Tensor] = None, stream=None):
+    """Pages, block-table entries and token rows of a step that adds ``new_lens`` (int32
+    [num_seqs]) tokens; returns (seq_ids, positions, slots, cu_tokens).
+
+    ``block_table`` is updated; ``seq_lens`` and ``free_count`` too unless
+    ``seq_lens_out`` / ``free_count_out`` are given. The four results
+    (int32, int32, int64 [max_tokens], int32 [num_seqs + 1]) are allocated
+    with torch when not given.
+    """
+    dev, i32 = torch.cuda.current_device(), torch.int32
+    table, num_seqs, max_blocks = _table(block_table, dev)
+    rows = max(max_tokens, 0)
+    if seq_ids is None:
+        seq_ids = torch.empty(rows, dtype=i32, device=dev)
+    if positions is None:
+        positions = torch.empty(rows, dtype=i32, device=dev)
+    if slots is None:
+        slots = torch.empty(rows, dtype=torch.int64, device=dev)
+    if cu_tokens is None:
+        cu_tokens = torch.empty(num_seqs + 1, dtype=i32, device=dev)
+    lens_out = seq_lens if seq_lens_out is None else seq_lens_out
+    count_out = free_count if free_count_out is None else free_count_out
+    st = _lib().nvfp4_mla_plan_step(
+        _arg(new_lens, "new_lens", i32, num_seqs, dev),
+        _arg(seq_lens, "seq_lens", i32, num_seqs, dev), num_seqs, table, max_blocks, page_size,
+        _arg(free_pages, "free_pages", i32, 0, dev), free_pages.numel(),
+        _arg(free_count, "free_count", i32, 1, dev), max_tokens,
+        _arg(lens_out, "seq_lens_out", i32, num_seqs, dev),
+        _arg(count_out, "free_count_out", i32, 1, dev), _arg(seq_ids, "seq_ids", i32, rows, dev),
+        _arg(positions, "positions", i32, rows, dev),
+        _arg(slots, "slots", torch.int64, rows, dev),
+        _arg(cu_tokens, "cu_tokens", i32, num_seqs + 1, dev),
+        _opt(refused_count, "refused_count", i32, 1, dev), _stream(stream))
+    _check(st, "nvfp4_mla_plan_step")
+    return seq_ids, positions, slots, cu_tokens
+
+
+def nvfp4_mla_truncate(keep_lens: torch.Tensor, seq_lens: torch.Tensor, block_table: torch.Tensor,
+                       page_size: int, free_pages: torch.Tensor, free_count: torch.Tensor,
+                       seq_lens_out: Optional[torch.Tensor] = None,
+                       free_count_out: Optional[torch.Tensor] = None,
+                       dropped_count: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Shrink sequences to ``keep_lens`` (int32 [num_seqs]); their pages go onto ``free_pages``.
+
+    ``seq_lens`` and ``free_count`` are updated unless ``seq_lens_out`` /
+    ``free_count_out`` are given.
+    """
+    dev, i32 = torch.cuda.current_device(), torch.int32
+    table, num_seqs, max_blocks = _table(block_table, dev)
+    lens_out = seq_lens if seq_lens_out is None else seq_lens_out
+    count_out = free_count if free_count_out is None else free_count_out
+    st = _lib().nvfp4_mla_truncate(
+        _arg(keep_lens, "keep_lens", i32, num_seqs, dev),
+        _arg(seq_lens, "seq_lens", i32, num_seqs, dev), num_seqs, table, max_blocks, page_size,
+        _arg(free_pages, "free_pages", i32, 0, dev), free_pages.numel(),
+        _arg(free_count, "free_count", i32, 1, dev),
+        _arg(lens_out, "seq_lens_out", i32, num_seqs, dev),
+        _arg(count_out, "free_count_out", i32, 1, dev),
+        _opt(dropped_count, "dropped_count", i32, 1, dev), _stream(stream))
+    _check(st, "nvfp4_mla_truncate")
+
+
+# ------------------------------------------------- index-key cache and selection
+def _pool(cache: torch.Tensor, num_blocks: int, block_stride_bytes: int, device: int) -> int:
+    """Device pointer of a pool that holds num_blocks pages (the last one need not be padded)."""
+    if (not cache.is_contiguous() or cache.get_device() != device
+            or cache.numel() * cache.element_size() < num_blocks * block_stride_bytes):
+        raise ValueError("cache must be a contiguous tensor of num_blocks * block_stride_bytes "
+                         "bytes on the current CUDA device")
+    return cache.data_ptr()
+
+
+def nvfp4_mla_index_append(keys: torch.Tensor, seq_ids: torch.Tensor, positions: torch.Tensor,
+                           block_table: torch.Tensor, page_size: int, cache: torch.Tensor,
+                           num_blocks: int, block_stride_bytes: int,
+                           invalid_count: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Quantize index ``keys`` (bf16 [n,128]) into their rows of the index-key cache."""
+    dev, i32 = torch.cuda.current_device(), torch.int32
+    if keys.dim() != 2 or keys.shape[1] != INDEX_DIM:
+        raise ValueError("keys must be bf16 [n, 128]")
+    n = keys.shape[0]
+    table, num_seqs, max_blocks = _table(block_table, dev)
+    st = _lib().nvfp4_mla_index_append(
+        _arg(keys, "keys", torch.bfloat16, 0, dev), _arg(seq_ids, "seq_ids", i32, n, dev),
+        _arg(positions, "positions", i32, n, dev), n, table, num_seqs, max_blocks, page_size,
+        _pool(cache, num_blocks, block_stride_bytes, dev), num_blocks, block_stride_bytes,
+        _opt(invalid_count, "invalid_count", i32, 1, dev), _stream(stream))
+    _check(st, "nvfp4_mla_index_append")
+
+
+def nvfp4_mla_index_read(seq_ids: torch.Tensor, positions: torch.Tensor,
+                         block_table: torch.Tensor, page_size: int, cache: torch.Tensor,
+                         num_blocks: int, block_stride_bytes: int,
+                         keys: Optional[torch.Tensor] = None,
+                         invalid_count: Optional[torch.Tensor] = None, stream=None):
+    """The values (bf16 [n,128]) that the index rows of n tokens stand for."""
+    dev, i32 = torch.cuda.current_device(), torch.int32
+    n = seq_ids.numel()
+    if keys is None:
+        keys = torch.empty((n, INDEX_DIM), dtype=torch.bfloat16, device=dev)
+    table, num_seqs, max_blocks = _table(block_table, dev)
+    st = _lib().nvfp4_mla_index_read(
+        _arg(seq_ids, "seq_ids", i32, n, dev), _arg(positions, "positions", i32, n, dev), n,
+        table, num_seqs, max_blocks, page_size,
+        _pool(cache, num_blocks, block_stride_bytes, dev), num_blocks, block_stride_bytes,
+        _arg(keys, "keys", torch.bfloat16, n * INDEX_DIM, dev),
+        _opt(invalid_count, "invalid_count", i32, 1, dev), _stream(stream))
+    _check(st, "nvfp4_mla_index_read")
+    return keys
+
+
+def sparse_mla_select_workspace_size(num_q: int, num_heads: int, max_blocks: int, page_size: int,
+                                     select_block: int = 1) -> int:
+    n = int(_lib().sparse_mla_select_workspace_size(num_q, num_heads, max_blocks, page_size,
+                                                    select_block))
+    if n == (1 << 64) - 1:
+        raise ValueError("invalid selection shape")
+    return n
+
+
+def sparse_mla_select(q_index: torch.Tensor, weights: torch.Tensor, q_seq: torch.Tensor,
+                      q_pos: torch.Tensor, block_table: torch.Tensor, page_size: int,
+                      cache: torch.Tensor, num_blocks: int, block_stride_bytes: int,
+                      num_select: int, select_block: int = 1, sink_blocks: int = 0,
+                      recent_blocks: int = 0, topk_idx: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Positions of the ``num_select`` blocks of ``select_block`` tokens that score highest;
+    returns topk_idx (int32 [num_q, num_select * select_block]) for sparse_mla_decode.
+
+    ``topk_idx`` / ``workspace`` are allocated with torch when not given.
+    """
+    dev, i32 = torch.cuda.current_device(), torch.int32
+    if q_index.dim() != 3 or q_index.shape[2] != INDEX_DIM:
+        raise ValueError("q_index must be bf16 [num_q, num_heads, 128]")
+    num_q, H = q_index.shape[0], q_index.shape[1]
+    table, num_seqs, max_blocks = _table(block_table, dev)
+    width = max(num_select * select_block, 0)
+    if topk_idx is None:
+        topk_idx = torch.empty((num_q, width), dtype=i32, device=dev)
+    if workspace is None:
+        need = int(_lib().sparse_mla_select_workspace_size(num_q, H, max_blocks, page_size,
+                                                           select_block))
+        if need < 1 << 63:  # an invalid shape is refused below
+            workspace = _scratch(need, stream)
+    ws = None if workspace is None else workspace.numel() * workspace.element_size()
+    st = _lib().sparse_mla_select(
+        _arg(q_index, "q_index", torch.bfloat16, 0, dev),
+        _arg(weights, "weights", torch.float32, num_q * H, dev), _arg(q_seq, "q_seq", i32, num_q, dev),
+        _arg(q_pos, "q_pos", i32, num_q, dev), num_q, H, table, num_seqs, max_blocks, page_size,
+        _pool(cache, num_blocks, block_stride_bytes, dev), num_blocks, block_stride_bytes,
+        select_block, num_select, sink_blocks, recent_blocks,
+        _arg(topk_idx, "topk_idx", i32, num_q * width, dev),
+        None if workspace is None else _arg(workspace, "workspace", workspace.dtype, 0, dev),
+        ws or 0, _stream(stream))
+    _check(st, "sparse_mla_select")
+    return topk_idx

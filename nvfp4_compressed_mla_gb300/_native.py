@@ -32,6 +32,13 @@ SIGNATURES = {
     "nvfp4_mla_staged_rows_per_q": (I64, [I32, I32]),
     "nvfp4_mla_stage_fp8": (I32, [P, P, I32, I32, P, I32, I32, P, I32, P, I64, I64, F32, P, P,
                                   P, P]),
+    "nvfp4_mla_plan_step": (I32, [P, P, I32, P, I32, I32, P, I32, P, I32, P, P, P, P, P, P, P, P]),
+    "nvfp4_mla_truncate": (I32, [P, P, I32, P, I32, I32, P, I32, P, P, P, P, P]),
+    "nvfp4_mla_index_append": (I32, [P, P, P, I32, P, I32, I32, I32, P, I64, I64, P, P]),
+    "nvfp4_mla_index_read": (I32, [P, P, I32, P, I32, I32, I32, P, I64, I64, P, P, P]),
+    "sparse_mla_select_workspace_size": (SZ, [I32, I32, I32, I32, I32]),
+    "sparse_mla_select": (I32, [P, P, P, P, I32, I32, P, I32, I32, I32, P, I64, I64, I32, I32, I32,
+                                I32, P, P, SZ, P]),
 }
 
 

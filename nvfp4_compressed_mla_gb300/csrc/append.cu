@@ -29,17 +29,6 @@ __device__ __forceinline__ float div_scale(float x, float s, float inv_pow2) {
   return inv_pow2 != 0.f ? x * inv_pow2 : __fdiv_rn(x, s);
 }
 
-// E2M1 code of x under scale S > 0: nearest grid value of x/S, ties to the
-// even code, saturating at 6, sign from x. Decided by comparing |x| with
-// midpoint*S, products that are exact in fp32 (midpoints have <= 3
-// significant bits, E4M3 scales <= 4), so no quotient is rounded.
-__device__ __forceinline__ uint32_t e2m1_code(float x, float S) {
-  const float a = fabsf(x);
-  const uint32_t mag = (a > 0.25f * S) + (a >= 0.75f * S) + (a > 1.25f * S) +
-                       (a >= 1.75f * S) + (a > 2.5f * S) + (a >= 3.5f * S) + (a > 5.0f * S);
-  return mag | ((__float_as_uint(x) >> 31) << 3);
-}
-
 template <int kFmt>
 __global__ void __launch_bounds__(kAppendWarps * 32)
     append_kernel(const uint8_t* __restrict__ latent, const uint8_t* __restrict__ rope,

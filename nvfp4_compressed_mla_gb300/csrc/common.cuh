@@ -115,6 +115,17 @@ __device__ __forceinline__ uint4 ld_nc_v4(const void* p) {
   return r;
 }
 
+// E2M1 code of x under scale S > 0: nearest grid value of x/S, ties to the
+// even code, saturating at 6, sign from x. Decided by comparing |x| with
+// midpoint*S, products that are exact in fp32 (midpoints have <= 3
+// significant bits, E4M3 scales <= 4), so no quotient is rounded.
+__device__ __forceinline__ uint32_t e2m1_code(float x, float S) {
+  const float a = fabsf(x);
+  const uint32_t mag = (a > 0.25f * S) + (a >= 0.75f * S) + (a > 1.25f * S) +
+                       (a >= 1.75f * S) + (a > 2.5f * S) + (a >= 3.5f * S) + (a > 5.0f * S);
+  return mag | ((__float_as_uint(x) >> 31) << 3);
+}
+
 // Resolve logical position `pos` of sequence `b` to a byte offset in the
 // pool; -1 when it does not resolve. `len` < 0 skips the length check.
 __device__ __forceinline__ int64_t resolve_row(int32_t b, int32_t pos, int32_t len,

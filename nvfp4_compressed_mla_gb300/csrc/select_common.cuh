@@ -1,0 +1,54 @@
+// select_common.cuh -- what the two kernels of sparse_mla_select share.
+//
+// Kernel 1 writes fp32 scores (the highest of every `granule` = min(block, 32)
+// consecutive positions) and, per tile of 128 positions, the largest scale
+// byte among the keys; kernel 2 picks the blocks.
+#pragma once
+
+#include "index_common.cuh"
+
+namespace nvfp4_mla {
+
+constexpr int kScoreTile = 128;      // positions per tile of the score kernel
+constexpr int kMaxGranule = 32;      // positions behind one stored score
+constexpr int kStatusWords = 1024;   // one per CTA of the score kernel
+
+struct SelectParams {
+  const uint8_t* q_index;
+  const float* weights;
+  const int32_t* q_seq;
+  const int32_t* q_pos;
+  int32_t num_q, num_heads;
+  const int32_t* block_table;
+  int32_t num_seqs, max_blocks, page_size;
+  const uint8_t* cache;
+  int64_t num_blocks, block_stride;
+  int32_t block, num_select, sink, recent;
+  int32_t* topk_idx;
+  float* scores;      // [num_q, score_stride]
+  int64_t score_stride;
+  float* smax;        // [num_q, tiles]: largest key scale of each tile
+  int64_t tiles;
+  uint32_t* status;   // [kStatusWords]
+  int32_t score_ctas;
+  long long wait_cycles;
+};
+
+// Positions that query token t sees, 0 for none.
+__device__ __forceinline__ int32_t visible_positions(const SelectParams& p, int32_t t) {
+  const int32_t seq = __ldg(p.q_seq + t), pos = __ldg(p.q_pos + t);
+  if (seq < 0 || seq >= p.num_seqs || pos < 0) return 0;
+  const int64_t room = static_cast<int64_t>(p.max_blocks) * p.page_size;
+  return static_cast<int32_t>(min(static_cast<int64_t>(pos) + 1, room));
+}
+
+// Positions that have to be scored: none where every visible block is taken.
+__device__ __forceinline__ int32_t scored_positions(const SelectParams& p, int32_t t) {
+  const int32_t n = visible_positions(p, t);
+  const int64_t blocks = (static_cast<int64_t>(n) + p.block - 1) / p.block;
+  return blocks > p.num_select ? n : 0;
+}
+
+int32_t launch_scores(SelectParams& p, int num_sms, cudaStream_t stream);
+
+}  // namespace nvfp4_mla

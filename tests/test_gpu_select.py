@@ -1,0 +1,214 @@
+"""GPU: the selection against 64-bit scores and a stable sort. The chosen positions have to be
+equal: the operator decides as 64-bit arithmetic does, ties by the lower index."""
+import numpy as np
+import pytest
+import torch
+
+from tests import step_cases as sc
+from workloads.gen import bf16_from_f32
+
+pytestmark = pytest.mark.gpu
+
+
+def dev(a, dtype=None):
+    t = torch.from_numpy(np.ascontiguousarray(a))
+    return (t.view(dtype) if dtype is not None else t).to("cuda:0")
+
+
+class Case:
+    def __init__(self, seed, lens, per_seq, heads, page=64, pad=0, width=None, order=None):
+        rng = np.random.default_rng(seed)
+        self.page, self.stride = page, page * sc.ROW + pad
+        self.lens = np.asarray(lens)
+        self.table, _, self.blocks = sc.random_tables(rng, self.lens, page, 2, width)
+        self.pool = sc.random_pool(rng, self.blocks, page, self.stride)
+        seq = np.repeat(np.arange(len(lens)), per_seq)
+        pos = np.concatenate([np.arange(n - per_seq, n) for n in self.lens])
+        if order is not None:
+            seq, pos = seq[order], pos[order]
+        self.seq, self.pos = seq.astype(np.int32), pos.astype(np.int32)
+        self.q = bf16_from_f32(rng.standard_normal((len(seq), heads, 128)))
+        self.w = (rng.standard_normal((len(seq), heads)) / np.sqrt(heads)).astype(np.float32)
+
+    def ref(self, num, block=1, sink=0, recent=0):
+        return sc.select(self.q, self.w, self.seq, self.pos, self.table, self.page, self.pool,
+                         self.blocks, self.stride, num, block, sink, recent)
+
+    def device(self):
+        return (dev(self.q, torch.bfloat16), dev(self.w), dev(self.seq), dev(self.pos),
+                dev(self.table), self.page, dev(self.pool), self.blocks, self.stride)
+
+    def run(self, num, block=1, sink=0, recent=0, **kw):
+        import nvfp4_compressed_mla_gb300 as nm
+        out = nm.sparse_mla_select(*self.device(), num, select_block=block, sink_blocks=sink,
+                                   recent_blocks=recent, **kw)
+        torch.cuda.synchronize()
+        return out.cpu().numpy()
+
+    def check(self, num, block=1, sink=0, recent=0, **kw):
+        got, ref = self.run(num, block, sink, recent, **kw), self.ref(num, block, sink, recent)
+        bad = np.nonzero((got != ref).any(1))[0]
+        assert bad.size == 0, (bad[:5], got[bad[0]][:20], ref[bad[0]][:20])
+
+
+@pytest.mark.parametrize("heads", [1, 2, 16, 31, 32, 33, 64, 65, 100, 128])
+def test_head_counts(heads):
+    Case(heads, [700, 1, 129, 2000], 1, heads).check(100)
+
+
+@pytest.mark.parametrize("block", [1, 2, 4, 8, 16, 32, 64, 128])
+@pytest.mark.parametrize("sink,recent", [(0, 0), (1, 2), (0, 5)])
+def test_block_sizes(block, sink, recent):
+    Case(block, [block * 40 + 3, block * 9, 5 * block + 1, 1], 2, 8).check(6, block, sink, recent)
+
+
+@pytest.mark.parametrize("page,pad", [(2, 0), (16, 16), (48, 0), (64, 64 * 352), (128, 0), (1000, 0)])
+def test_page_sizes_and_strides(page, pad):
+    Case(page, [1500, 333], 1, 24, page=page, pad=pad).check(64)
+
+
+@pytest.mark.parametrize("per_seq", [1, 2, 3, 5, 15, 64])
+def test_several_query_tokens_of_a_sequence(per_seq):
+    Case(per_seq, [900, 40, 2100], per_seq, 32).check(128)
+
+
+def test_query_tokens_in_any_order():
+    rng = np.random.default_rng(3)
+    Case(3, [900, 1200, 500, 70], 9, 16, order=rng.permutation(36)).check(50)
+
+
+@pytest.mark.parametrize("num", [1, 2, 255, 256, 1000, 2047, 2999, 3000, 5000])
+def test_numbers_selected(num):
+    Case(num, [3000, 2999, 10], 1, 16).check(num)
+
+
+def test_lengths_around_a_tile():
+    Case(8, [1, 2, 127, 128, 129, 255, 256, 257, 383, 385], 1, 16).check(100)
+
+
+def test_long_context():
+    Case(11, [60011], 2, 64).check(2048)
+
+
+def test_a_table_wider_than_the_sequences():
+    Case(12, [300, 7], 1, 16, width=500).check(40)
+
+
+def test_query_tokens_that_see_nothing_or_past_the_table():
+    c = Case(13, [300, 500], 3, 16)
+    c.seq[0], c.pos[1], c.seq[2] = -1, -1, 2
+    c.pos[3] = 10 ** 6  # sees the whole table
+    c.pos[4] = 2 ** 31 - 1
+    c.check(40)
+    got = c.run(40)
+    assert (got[:3] == -1).all()
+
+
+def test_pages_that_do_not_resolve_rank_last():
+    c = Case(14, [900, 900], 1, 16)
+    c.table[0, 3], c.table[0, 5], c.table[1, 0] = -1, 10 ** 6, -1
+    c.table[1, 2:9] = -1
+    c.check(64)
+    c.check(700)  # some of them have to be taken: the lowest ones
+    c.check(5, 64)
+
+
+def test_equal_scores_go_to_the_lower_index():
+    c = Case(15, [1000, 1000, 1000], 1, 16)
+    c.w[0] = 0.0                      # every score 0
+    c.q[1] = 0
+    row = c.pool.reshape(c.blocks, c.stride)
+    one = row[:, :64].copy()[0], row[:, 64 * 64:64 * 64 + 8].copy()[0]
+    for b in c.table[2][:9]:          # sequence 2: the same key 576 times, then others
+        row[b, :64 * 64] = np.tile(one[0], 64)
+        row[b, 64 * 64:64 * sc.ROW] = np.tile(one[1], 64)
+    c.check(100)
+    c.check(700)
+    c.check(9, 64)
+
+
+def test_more_candidates_than_the_list_holds():
+    # one head: half of the scores are exactly 0, and the border lies among them
+    c = Case(16, [9000, 5000], 1, 1)
+    c.w[:] = 1.0
+    c.check(6000)
+    c = Case(17, [9000], 2, 2)
+    c.w[:] = -1.0
+    c.check(3000)
+    c.check(100, 32)
+
+
+def test_scores_next_to_each_other():
+    # keys that differ in one code of a small group: scores a few parts in 2^24 apart
+    rng = np.random.default_rng(18)
+    c = Case(18, [2000], 1, 64)
+    row = c.pool.reshape(c.blocks, c.stride)
+    base = rng.integers(0, 256, 64, dtype=np.uint8)
+    for b in c.table[0]:
+        codes = row[b, :64 * 64].reshape(64, 64)
+        codes[:] = base
+        codes[np.arange(64), 0] = rng.integers(0, 256, 64)
+        row[b, 64 * 64:64 * sc.ROW] = np.tile(np.array([1] + [126] * 7, np.uint8), 64)
+    c.check(500)
+    c.check(10, 16)
+
+
+def test_weights_and_keys_over_a_wide_range():
+    rng = np.random.default_rng(19)
+    c = Case(19, [3000, 3000], 1, 64)
+    c.w *= (10.0 ** rng.uniform(-6, 6, c.w.shape)).astype(np.float32)
+    c.q = bf16_from_f32(rng.standard_normal(c.q.shape) * 10.0 ** rng.uniform(-4, 2, c.q.shape))
+    c.check(300)
+    c.w *= np.float32(1e-38)  # subnormal weights among them
+    c.check(300)
+
+
+def test_workspace_of_the_stated_size_is_enough_and_its_contents_do_not_matter():
+    import nvfp4_compressed_mla_gb300 as nm
+    c = Case(20, [700, 1300], 5, 16)
+    n = nm.sparse_mla_select_workspace_size(10, 16, c.table.shape[1], 64, 4)
+    buf = torch.full((n + 256,), 255, dtype=torch.uint8, device="cuda:0")
+    got = c.run(20, 4, workspace=buf[:n])
+    assert bool((buf[n:] == 255).all())
+    assert np.array_equal(got, c.ref(20, 4))
+    with pytest.raises(nm.NativeError):
+        c.run(20, 4, workspace=buf[:n - 16])
+
+
+def test_replayed_graphs_that_share_a_workspace_in_order():
+    import nvfp4_compressed_mla_gb300 as nm
+    a, b = Case(21, [700, 1300], 1, 16), Case(22, [500, 90, 2000], 1, 64)
+    n = max(nm.sparse_mla_select_workspace_size(len(c.seq), c.q.shape[1], c.table.shape[1], 64)
+            for c in (a, b))
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda:0")
+    made = []
+    for c in (a, b):
+        args = c.device()
+        out = torch.empty((len(c.seq), 64), dtype=torch.int32, device="cuda:0")
+        nm.sparse_mla_select(*args, 64, topk_idx=out, workspace=ws)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            nm.sparse_mla_select(*args, 64, topk_idx=out, workspace=ws)
+        made.append((g, out, args, c.ref(64)))
+    for g, out, _, _ in made:
+        out.fill_(-9)
+    for g, _, _, _ in made * 3:
+        g.replay()
+    torch.cuda.synchronize()
+    for _, out, _, ref in made:
+        assert np.array_equal(out.cpu().numpy(), ref)
+
+
+def test_another_stream():
+    c = Case(23, [700, 1300], 2, 16)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = c.run(64, stream=s)
+    assert np.array_equal(got, c.ref(64))
+
+
+def test_results_repeat():
+    c = Case(24, [5000, 3000], 4, 64)
+    first = c.run(512)
+    for _ in range(5):
+        assert np.array_equal(c.run(512), first)
