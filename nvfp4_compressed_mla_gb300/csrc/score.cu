@@ -1,100 +1,586 @@
-// score.cu -- index scores of every visible position of every query token.
+// score.cu -- index scores of every visible position of every query token, on
+// the block-scaled FP4 tensor cores (tcgen05 kind::mxf4nvf4).
+//
+// Keys and queries are stored as the tensor cores take them (E2M1 codes, one
+// E4M3 scale per 16 values along the contraction), so nothing is dequantised:
+// per tile of 128 positions and query token, D = K Q^T (M = 128 positions,
+// N = heads, K = 128 in two steps), and the epilogue adds up
+// sum_j w_j max(0, D_j) in fp32, thread = position.
+//
+// The bound is HBM for one query token per sequence: 72 bytes a position
+// against 2 * 128 * heads FP4 flop. With several query tokens a sequence, a
+// tile is read once for up to `group` of them and the epilogue's fp32 work
+// (one max and one fma per position and head) bounds it.
+//
+// One persistent CTA per SM. All visible (tile, query token run) pairs form
+// one list, and each CTA takes a contiguous part of it of equal cost, so one
+// long sequence fills the device as well as many short ones. Runs are
+// consecutive query tokens of one sequence, at most `group` of them.
+//
+//   warps 0-7    epilogue: two sets of four; a set takes every other
+//                (tile, query token) unit, warp w the positions 32 (w % 4)..
+//   warps 8-11   key loads: warp w resolves its 32 positions through the block
+//                table (two tiles ahead) and copies their codes and scales
+//                with cp.async, six tiles in flight
+//   warp 12      issues the scale copies and MMAs
+//   warps 13-15  encode the next run's queries
+//
+// Every wait is bounded; when one runs out the CTA's roles unwind, what is in
+// flight is drained, and the CTA's status word says so.
+#include <math.h>
+
 #include "select_common.cuh"
+#include "tc_ptx.cuh"
 
 namespace nvfp4_mla {
 namespace {
 
-// One thread per position of a tile, the query's dequantised heads in shared
-// memory.
-__global__ void __launch_bounds__(kScoreTile) score_kernel(const SelectParams p) {
-  extern __shared__ float qv[];  // [num_heads][128]
-  __shared__ float wmax[4];
-  const int32_t t = blockIdx.y;
-  const int32_t seen = scored_positions(p, t);
-  const int32_t pos0 = blockIdx.x * kScoreTile;
-  if (pos0 >= seen) return;
-  const int tid = threadIdx.x, lane = tid & 31;
-  for (int g = tid; g < p.num_heads * kIndexScales; g += kScoreTile) {
-    const uint8_t* src = p.q_index +
-                         (static_cast<int64_t>(t) * p.num_heads * kIndexScales + g) * (2 * kGroup);
-    const uint4 a = ld_nc_v4(src), b = ld_nc_v4(src + 16);
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    uint32_t lo, hi, h[8];
-    float s;
-    quantize_group(w, lo, hi, s);
-    uint32_t x[4], y[4];
-    e2m1x8_to_f16x8(lo, x);
-    e2m1x8_to_f16x8(hi, y);
-    for (int i = 0; i < 4; ++i) h[i] = x[i], h[4 + i] = y[i];
-    for (int i = 0; i < 8; ++i) {
-      qv[g * kGroup + 2 * i] = f16_bits_to_f32(static_cast<uint16_t>(h[i])) * s;
-      qv[g * kGroup + 2 * i + 1] = f16_bits_to_f32(static_cast<uint16_t>(h[i] >> 16)) * s;
-    }
-  }
-  __syncthreads();
-  const int32_t pos = pos0 + tid;
-  float score = -INFINITY, smax = 0.f;
-  if (pos < seen) {
-    const IndexRow at = resolve_index_row(__ldg(p.q_seq + t), pos, p.block_table, p.num_seqs,
-                                          p.max_blocks, p.page_size, p.num_blocks,
-                                          p.block_stride);
-    if (at.page >= 0) {
-      const uint8_t* page = p.cache + at.page;
-      const uint8_t* sc = page + static_cast<int64_t>(p.page_size) * kIndexCodes +
-                          static_cast<int64_t>(at.row) * kIndexScales;
-      float k[kIndexDim];
-      for (int g = 0; g < kIndexScales; ++g) {
-        const uint2 c = __ldg(reinterpret_cast<const uint2*>(
-            page + static_cast<int64_t>(at.row) * kIndexCodes + g * 8));
-        const uint8_t byte = __ldg(sc + g) & 0x7Fu;
-        const float s = f16_bits_to_f32(static_cast<uint16_t>(e4m3x2_to_f16x2(byte)));
-        smax = fmaxf(smax, byte == 0x7Fu ? 448.f : s);
-        uint32_t x[4], y[4];
-        e2m1x8_to_f16x8(c.x, x);
-        e2m1x8_to_f16x8(c.y, y);
-        for (int i = 0; i < 4; ++i) {
-          k[g * kGroup + 2 * i] = f16_bits_to_f32(static_cast<uint16_t>(x[i])) * s;
-          k[g * kGroup + 2 * i + 1] = f16_bits_to_f32(static_cast<uint16_t>(x[i] >> 16)) * s;
-          k[g * kGroup + 8 + 2 * i] = f16_bits_to_f32(static_cast<uint16_t>(y[i])) * s;
-          k[g * kGroup + 8 + 2 * i + 1] = f16_bits_to_f32(static_cast<uint16_t>(y[i] >> 16)) * s;
-        }
-      }
-      float sum = 0.f;
-      for (int j = 0; j < p.num_heads; ++j) {
-        float d = 0.f;
-#pragma unroll
-        for (int i = 0; i < kIndexDim; ++i) d = fmaf(qv[j * kIndexDim + i], k[i], d);
-        d = d < 0.f ? 0.f : d;
-        sum = fmaf(__ldg(p.weights + static_cast<int64_t>(t) * p.num_heads + j), d, sum);
-      }
-      if (!(sum != sum)) score = sum + 0.f;
-    }
-  }
-  const int granule = min(p.block, kMaxGranule);
-  for (int d = 1; d < granule; d <<= 1)
-    score = fmaxf(score, __shfl_xor_sync(0xffffffffu, score, d));
-  if (pos < seen && pos % granule == 0)
-    p.scores[t * p.score_stride + pos / granule] = score;
-  for (int d = 16; d > 0; d >>= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, d));
-  if (lane == 0) wmax[tid >> 5] = smax;
-  __syncthreads();
-  if (tid == 0)
-    p.smax[t * p.tiles + blockIdx.x] = fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3]));
+constexpr int kScoreThreads = 512;
+constexpr int kEpiWarps = 8;
+constexpr int kLoadWarp0 = 8, kLoadWarps = 4;
+constexpr int kScoreMmaWarp = 12;
+constexpr int kQWarp0 = 13, kQWarps = 3;
+constexpr int kStages = 8;        // key tiles in shared memory
+constexpr int kInFlight = 6;      // key tiles whose copies are under way
+constexpr int kMaskRing = 32;     // resolved-position masks; more than the tiles between load and epilogue
+constexpr int kMaxGroup = 8;      // query tokens of a run
+constexpr int kTileCodes = kScoreTile * kIndexCodes;   // 8192, 64-byte swizzle
+constexpr int kTileScales = 1024;                      // two K halves of 128 x 4 scale bytes
+constexpr int kStageBytes = kTileCodes + kTileScales;
+constexpr int kMaskBytes = kMaskRing * 4 * 4;
+// A run's cost per tile: its query tokens' epilogues and the tile's load.
+constexpr int kLoadCost = 2;
+// Tensor memory columns: accumulator slots, then scales of Q, then of K.
+constexpr uint32_t kSfbCol = 384, kSfaCol = 448;
+
+// Instruction descriptor, kind::mxf4nvf4: E2M1 A (bit 7) and B (bit 10), both
+// K-major, E4M3 scales, N >> 3 at 17, M >> 4 at 24, K = 64.
+__host__ __device__ constexpr uint32_t score_idesc(int n) {
+  return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+__host__ __device__ constexpr int acc_slots(int chunks) {  // chunks of 32 heads
+  return chunks == 1 ? 8 : chunks == 2 ? 6 : chunks == 3 ? 4 : 3;
+}
+__host__ __device__ constexpr int max_group(int chunks) { return chunks <= 2 ? kMaxGroup : 4; }
+
+// K-major operand with 64-byte rows in 64-byte swizzle: 8-row groups of 512 bytes.
+__device__ __forceinline__ uint64_t sw64_desc(uint32_t addr) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) |
+         (static_cast<uint64_t>(512 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+         (static_cast<uint64_t>(4) << 61);
+}
+__device__ __forceinline__ uint32_t sw64_off(uint32_t row, uint32_t chunk) {
+  return row * 64u + ((chunk ^ ((row >> 1) & 3u)) << 4);
+}
+// 32 rows of 16 bytes without swizzle: 8-row groups of 128 bytes.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) |
+         (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
+}
+// Scale byte g (0..7) of row r (0..127): per K half, row r % 32 holds the four
+// bytes of rows r, r + 32, .. in turn.
+__device__ __forceinline__ uint32_t scale_off(uint32_t r, uint32_t g) {
+  return (g >> 2) * 512u + (r & 31u) * 16u + (r >> 5) * 4u + (g & 3u);
+}
+// 512 bytes of scales -> four columns of tensor memory, in all lane quadrants
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
+}
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %6, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], "
+      "[%5], p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+// 16 or 4 bytes, or zeros where `live` is false
+__device__ __forceinline__ void cp_async16_z(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(live ? 16u : 0u)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4_z(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+               "r"(live ? 4u : 0u)
+               : "memory");
+}
+template <int kPending>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+__device__ __forceinline__ float relu_nan(float x) {  // max(0, x), NaN stays NaN
+  float r;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ float sum2(uint64_t v) {
+  float lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+  return lo + hi;
+}
+// One warp's bounded wait: it leaves together.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t abort_addr,
+                                          long long limit) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_addr, limit)) != 0;
 }
 
-}  // namespace
+struct Bars {  // byte offsets in the control block
+  static constexpr int kFull = 0, kEmpty = kFull + 8 * kStages, kDFull = kEmpty + 8 * kStages,
+                       kDEmpty = kDFull + 64, kQFull = kDEmpty + 64, kQEmpty = kQFull + 16,
+                       kDrain = kQEmpty + 16, kTmem = kDrain + 8, kAbort = kTmem + 4,
+                       kStart = kAbort + 4, kEnd = kStart + 32;
+};
+static_assert(Bars::kStart % 8 == 0, "start words");
+constexpr int kCtl = kStages * kStageBytes + kMaskBytes;
+constexpr int kQBase = (kCtl + Bars::kEnd + 511) / 512 * 512;
 
-int32_t launch_scores(SelectParams& p, int num_sms, cudaStream_t stream) {
-  (void)num_sms;
-  p.score_ctas = 0;
-  const size_t smem = static_cast<size_t>(p.num_heads) * kIndexDim * 4;
-  if (cudaFuncSetAttribute(score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+__host__ __device__ constexpr int q_buffer_bytes(int heads_pad, int group) {
+  return (group * (heads_pad * kIndexCodes + kTileScales + heads_pad * 4) + 1023) / 1024 * 1024;
+}
+
+struct ScoreParams {
+  SelectParams s;
+  int32_t group;
+  int32_t ctas;
+};
+
+// The runs of query tokens whose tiles a CTA scores, walked by one warp. Lane
+// i holds query token i of the current run; the next run's words are loaded
+// while the current one is worked on.
+struct Walk {
+  int32_t q, count, seq, tiles, t0, t1;  // run; tiles t0 .. t1 - 1 are this CTA's
+  int32_t seen;                          // lane i: positions to score of token q + i
+  int64_t cost0, begin, end;
+  int32_t next_seq, next_pos;            // lane i: words of token next_q + i
+  int32_t next_q;
+
+  __device__ __forceinline__ void fetch(const ScoreParams& p, int32_t from) {
+    next_q = from;
+    const int32_t lane = threadIdx.x & 31;
+    const int64_t stop = min(static_cast<int64_t>(from / p.group + 1) * p.group,
+                             static_cast<int64_t>(p.s.num_q));
+    next_seq = next_pos = -1;
+    if (from + lane < stop) {
+      next_seq = __ldg(p.s.q_seq + from + lane);
+      next_pos = __ldg(p.s.q_pos + from + lane);
+    }
+  }
+  // Moves to the next run with tiles of this CTA; false when there is none.
+  __device__ __forceinline__ bool next(const ScoreParams& p) {
+    const int32_t lane = threadIdx.x & 31;
+    while (next_q < p.s.num_q && cost0 < end) {
+      q = next_q;
+      const int32_t lim = min(p.group - q % p.group, p.s.num_q - q);
+      seq = __shfl_sync(0xffffffffu, next_seq, 0);
+      const uint32_t same = __ballot_sync(0xffffffffu, lane < lim && next_seq == seq);
+      count = __ffs(~same) - 1;  // leading lanes; lim < 32
+      seen = lane < count ? scored_positions_of(p.s, seq, next_pos) : 0;
+      fetch(p, q + count);
+      const int32_t most = static_cast<int32_t>(__reduce_max_sync(0xffffffffu, seen));
+      tiles = (most + kScoreTile - 1) / kScoreTile;
+      const int64_t w = count + kLoadCost;
+      const int64_t from = begin - cost0, to = end - cost0;
+      t0 = from <= 0 ? 0 : static_cast<int32_t>(min((from + w - 1) / w, int64_t{tiles}));
+      t1 = static_cast<int32_t>(min((to + w - 1) / w, int64_t{tiles}));
+      cost0 += tiles * w;
+      if (t0 < t1) return true;
+    }
+    return false;
+  }
+};
+
+template <int kChunks>
+__global__ void __launch_bounds__(kScoreThreads, 1)
+    score_kernel(const __grid_constant__ ScoreParams p) {
+  constexpr int kHeads = 32 * kChunks;
+  constexpr int kSlots = acc_slots(kChunks);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t base = smem_u32(smem);
+  const uint32_t ctl = base + kCtl;
+  const uint32_t abort_addr = ctl + Bars::kAbort;
+  auto bar = [ctl](int kind, int i) { return ctl + static_cast<uint32_t>(kind + 8 * i); };
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const long long lim = p.s.wait_cycles;
+
+  // ---- this CTA's part of the list
+  __shared__ int64_t warp_cost[kScoreThreads / 32];
+  const int32_t groups = (p.s.num_q + p.group - 1) / p.group;
+  const int32_t per = (groups + kScoreThreads - 1) / kScoreThreads;
+  const int32_t g_from = min(tid * per, groups), g_to = min(g_from + per, groups);
+  auto runs = [&](auto&& each) {  // the runs of this thread's groups, in order
+    for (int32_t q = g_from * p.group; q < min(g_to * p.group, p.s.num_q);) {
+      const int32_t stop = min((q / p.group + 1) * p.group, p.s.num_q);
+      const int32_t seq = __ldg(p.s.q_seq + q);
+      int32_t most = 0, n = 0;
+      do {
+        most = max(most, scored_positions_of(p.s, seq, __ldg(p.s.q_pos + q + n)));
+        ++n;
+      } while (q + n < stop && __ldg(p.s.q_seq + q + n) == seq);
+      each(q, static_cast<int64_t>((most + kScoreTile - 1) / kScoreTile) * (n + kLoadCost));
+      q += n;
+    }
+  };
+  int64_t mine = 0;
+  runs([&](int32_t, int64_t cost) { mine += cost; });
+  int64_t upto = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t o = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += o;
+  }
+  if (lane == 31) warp_cost[warp] = upto;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(bar(Bars::kFull, i), kLoadWarps);
+      mbar_init(bar(Bars::kEmpty, i), 1);
+    }
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(bar(Bars::kDFull, i), 1);
+      mbar_init(bar(Bars::kDEmpty, i), 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(Bars::kQFull, i), kQWarps);
+      mbar_init(bar(Bars::kQEmpty, i), kEpiWarps + 1);
+    }
+    mbar_init(bar(Bars::kDrain, 0), 1);
+    st_shared_u32(abort_addr, 0);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  int64_t total = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < kScoreThreads / 32; ++w) {
+    if (w < warp) before += warp_cost[w];
+    total += warp_cost[w];
+  }
+  const int64_t begin = total * blockIdx.x / p.ctas, end = total * (blockIdx.x + 1) / p.ctas;
+  if (begin == end) {
+    if (tid == 0) p.s.status[blockIdx.x] = 0;
+    return;
+  }
+  before += upto - mine;
+  if (before <= begin && begin < before + mine) {
+    int64_t at = before;
+    runs([&](int32_t q, int64_t cost) {
+      if (at <= begin && begin < at + cost) {
+        *reinterpret_cast<int64_t*>(smem + kCtl + Bars::kStart) = at;
+        *reinterpret_cast<int32_t*>(smem + kCtl + Bars::kStart + 8) = q;
+      }
+      at += cost;
+    });
+  }
+  if (warp == kScoreMmaWarp) tmem_alloc(ctl + Bars::kTmem);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ld_shared_u32(ctl + Bars::kTmem);
+  Walk walk;
+  walk.cost0 = *reinterpret_cast<const int64_t*>(smem + kCtl + Bars::kStart);
+  walk.begin = begin;
+  walk.end = end;
+  walk.fetch(p, *reinterpret_cast<const int32_t*>(smem + kCtl + Bars::kStart + 8));
+
+  const int q_bytes = q_buffer_bytes(kHeads, p.group);
+  auto q_codes = [&](int buf) { return base + kQBase + buf * q_bytes; };
+  auto q_scales = [&](int buf) { return q_codes(buf) + p.group * kHeads * kIndexCodes; };
+  auto q_weights = [&](int buf) { return q_scales(buf) + p.group * kTileScales; };
+
+  if (warp < kEpiWarps) {
+    // ------------------------------------------------------------ epilogue
+    const int set = warp >> 2, quad = warp & 3;
+    const uint32_t lanes = static_cast<uint32_t>(quad) << 21;  // lane 32 * quad
+    const int granule = min(p.s.block, kMaxGranule);
+    const int shift = __ffs(granule) - 1;
+    uint32_t unit = 0, tile_no = 0, run = 0;
+    bool ok = true;
+    while (ok && walk.next(p)) {
+      const int buf = run & 1;
+      ok = warp_wait(bar(Bars::kQFull, buf), (run >> 1) & 1u, abort_addr, lim);
+      for (int32_t tile = walk.t0; ok && tile < walk.t1; ++tile, ++tile_no) {
+        const int32_t pos = tile * kScoreTile + quad * 32 + lane;
+        for (int i = 0; i < walk.count; ++i, ++unit) {
+          if ((unit & 1u) != static_cast<uint32_t>(set)) continue;
+          const uint32_t slot = unit % kSlots;
+          ok = warp_wait(bar(Bars::kDFull, slot), (unit / kSlots) & 1u, abort_addr, lim);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t d = tmem + lanes + slot * kHeads;
+          const uint32_t w = q_weights(buf) + i * kHeads * 4;
+          uint64_t acc[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int c0 = 0; c0 < kChunks; c0 += 2) {  // 64 columns in registers at a time
+            uint32_t v[2][32];
+            tmem_ld32(d + 32 * c0, v[0]);
+            if (c0 + 1 < kChunks) tmem_ld32(d + 32 * c0 + 32, v[1]);
+            tmem_ld_wait();
+            if (c0 + 2 >= kChunks) {  // the slot has been read
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(Bars::kDEmpty, slot));
+            }
+#pragma unroll
+            for (int c = 0; c < 2 && c0 + c < kChunks; ++c) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                uint64_t w0, w1;
+                asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
+                             : "=l"(w0), "=l"(w1)
+                             : "r"(w + (32 * (c0 + c) + j) * 4));
+                fma2(acc[(j >> 1) & 3],
+                     pack2(relu_nan(__uint_as_float(v[c][j])),
+                           relu_nan(__uint_as_float(v[c][j + 1]))),
+                     w0);
+                fma2(acc[((j >> 1) & 3) + 1],
+                     pack2(relu_nan(__uint_as_float(v[c][j + 2])),
+                           relu_nan(__uint_as_float(v[c][j + 3]))),
+                     w1);
+              }
+            }
+          }
+          float score = (sum2(acc[0]) + sum2(acc[1])) + (sum2(acc[2]) + sum2(acc[3]));
+          const uint32_t mask =
+              ld_shared_u32(base + kStages * kStageBytes + ((tile_no % kMaskRing) * 4 + quad) * 4);
+          const int32_t seen = __shfl_sync(0xffffffffu, walk.seen, i);
+          const bool live = pos < seen;
+          score = live && (mask >> lane & 1u) && score == score ? score + 0.f : -INFINITY;
+          for (int s = 1; s < granule; s <<= 1)
+            score = fmaxf(score, __shfl_xor_sync(0xffffffffu, score, s));
+          if (live && (pos & (granule - 1)) == 0)
+            p.s.scores[(walk.q + i) * p.s.score_stride + (pos >> shift)] = score;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(Bars::kQEmpty, buf));
+      ++run;
+    }
+  } else if (warp < kLoadWarp0 + kLoadWarps) {
+    // ----------------------------------------------------------- key loads
+    const int part = warp - kLoadWarp0;
+    struct Entry {
+      int32_t page, row;  // page -1: nothing to load
+      bool live;
+    };
+    int32_t tile = 0;
+    bool more = walk.next(p);
+    if (more) tile = walk.t0;
+    // Lane l keeps the (run, tile) of the l-th tile of every 32.
+    int32_t info_q = 0, info_tile = 0, fetched = 0;
+    auto fetch = [&](Entry& e) {
+      e.page = -1;
+      e.row = 0;
+      e.live = more;
+      if (!more) return;
+      if (lane == fetched % 32) info_q = walk.q, info_tile = tile;
+      ++fetched;
+      const int32_t pos = tile * kScoreTile + part * 32 + lane;
+      const int32_t most = static_cast<int32_t>(__reduce_max_sync(0xffffffffu, walk.seen));
+      if (pos < most) {
+        const int32_t lb = pos / p.s.page_size;
+        e.row = pos - lb * p.s.page_size;
+        e.page = __ldg(p.s.block_table + static_cast<int64_t>(walk.seq) * p.s.max_blocks + lb);
+      }
+      if (++tile == walk.t1) {
+        more = walk.next(p);
+        tile = walk.t0;
+      }
+    };
+    auto publish = [&](uint32_t it) {  // this warp's rows of tile `it` have landed
+      const uint32_t stage = it % kStages;
+      const uint32_t sc = base + stage * kStageBytes + kTileCodes + lane * 16 + part * 4;
+      uint32_t top = __vmaxu4(ld_shared_u32(sc) & 0x7F7F7F7Fu, ld_shared_u32(sc + 512) & 0x7F7F7F7Fu);
+      top = __vmaxu4(top, top >> 16);
+      top = __vmaxu4(top, top >> 8) & 0xFFu;
+      top = __reduce_max_sync(0xffffffffu, top);
+      const int32_t q = __shfl_sync(0xffffffffu, info_q, it % 32);
+      const int32_t t = __shfl_sync(0xffffffffu, info_tile, it % 32);
+      fence_proxy_async_cta();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(Bars::kFull, stage));
+        reinterpret_cast<uint8_t*>(p.s.smax + q * p.s.tiles + t)[part] =
+            static_cast<uint8_t>(min(top, 0x7Eu));
+      }
+    };
+    Entry e0, e1, e2;
+    fetch(e0);
+    fetch(e1);
+    uint32_t it = 0;
+    bool ok = true;
+    for (; e0.live; ++it) {
+      fetch(e2);
+      const uint32_t stage = it % kStages;
+      ok = warp_wait(bar(Bars::kEmpty, stage), ((it / kStages) & 1u) ^ 1u, abort_addr, lim);
+      if (!ok) break;
+      const uint32_t dst = base + stage * kStageBytes;
+      const bool live = e0.page >= 0 && e0.page < p.s.num_blocks;
+      const uint32_t mask = __ballot_sync(0xffffffffu, live);
+      if (lane == 0)
+        st_shared_u32(base + kStages * kStageBytes + ((it % kMaskRing) * 4 + part) * 4, mask);
+      const int64_t page = live ? static_cast<int64_t>(e0.page) * p.s.block_stride : 0;
+      const int64_t codes = page + static_cast<int64_t>(e0.row) * kIndexCodes;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // eight rows each, four lanes a row
+        const int r = i * 8 + (lane >> 2);
+        const int64_t at = __shfl_sync(0xffffffffu, codes, r);
+        cp_async16_z(dst + sw64_off(part * 32 + r, lane & 3), p.s.cache + at + (lane & 3) * 16,
+                     (mask >> r) & 1u);
+      }
+      const uint8_t* sc = p.s.cache + page + static_cast<int64_t>(p.s.page_size) * kIndexCodes +
+                          static_cast<int64_t>(e0.row) * kIndexScales;
+      const uint32_t sd = dst + kTileCodes + lane * 16 + part * 4;
+      cp_async4_z(sd, sc, live);
+      cp_async4_z(sd + 512, sc + 4, live);
+      cp_async_commit();
+      if (it >= kInFlight) {
+        cp_async_wait<kInFlight>();
+        publish(it - kInFlight);
+      }
+      e0 = e1;
+      e1 = e2;
+    }
+    cp_async_wait<0>();
+    if (ok)
+      for (uint32_t k = it > kInFlight ? it - kInFlight : 0; k < it; ++k) publish(k);
+  } else if (warp == kScoreMmaWarp) {
+    // ---------------------------------------------------------- MMA issue
+    constexpr uint32_t idesc = score_idesc(kHeads);
+    uint32_t unit = 0, it = 0, run = 0;
+    bool ok = true;
+    while (ok && walk.next(p)) {
+      const int buf = run & 1;
+      ok = warp_wait(bar(Bars::kQFull, buf), (run >> 1) & 1u, abort_addr, lim);
+      if (!ok) break;
+      tc_fence_after();
+      if (lane == 0)
+        for (int i = 0; i < walk.count; ++i)
+          for (int h = 0; h < 2; ++h)
+            copy_scales(tmem + kSfbCol + i * 8 + h * 4,
+                        scale_desc(q_scales(buf) + i * kTileScales + h * 512));
+      for (int32_t tile = walk.t0; ok && tile < walk.t1; ++tile, ++it) {
+        const uint32_t stage = it % kStages;
+        ok = warp_wait(bar(Bars::kFull, stage), (it / kStages) & 1u, abort_addr, lim);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t src = base + stage * kStageBytes;
+        const uint32_t sfa = tmem + kSfaCol + (it & 1u) * 8;
+        if (lane == 0)
+          for (int h = 0; h < 2; ++h)
+            copy_scales(sfa + h * 4, scale_desc(src + kTileCodes + h * 512));
+        for (int i = 0; i < walk.count; ++i, ++unit) {
+          const uint32_t slot = unit % kSlots;
+          ok = warp_wait(bar(Bars::kDEmpty, slot), ((unit / kSlots) & 1u) ^ 1u, abort_addr, lim);
+          if (!ok) break;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t b = q_codes(buf) + i * kHeads * kIndexCodes;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              mma_fp4(tmem + slot * kHeads, sw64_desc(src + 32 * h), sw64_desc(b + 32 * h), idesc,
+                      sfa + h * 4, tmem + kSfbCol + i * 8 + h * 4, h);
+            mma_commit(bar(Bars::kDFull, slot));
+          }
+          __syncwarp();
+        }
+        if (lane == 0) mma_commit(bar(Bars::kEmpty, stage));
+        __syncwarp();
+      }
+      if (lane == 0) mma_commit(bar(Bars::kQEmpty, buf));
+      __syncwarp();
+      ++run;
+    }
+    // everything this thread issued has completed before the CTA ends
+    if (lane == 0) {
+      mma_commit(bar(Bars::kDrain, 0));
+      const long long t0 = clock64();
+      while (!mbar_test(bar(Bars::kDrain, 0), 0) && clock64() - t0 < (1ll << 31)) {
+      }
+    }
+    __syncwarp();
+  } else {
+    // ----------------------------------------------------- encode queries
+    const int qt = tid - kQWarp0 * 32;
+    uint32_t run = 0;
+    bool ok = true;
+    while (ok && walk.next(p)) {
+      const int buf = run & 1;
+      ok = warp_wait(bar(Bars::kQEmpty, buf), ((run >> 1) & 1u) ^ 1u, abort_addr, lim);
+      if (!ok) break;
+      for (int x = qt; x < walk.count * kHeads * kIndexScales; x += kQWarps * 32) {
+        const int g = x % kIndexScales, row = x / kIndexScales;  // row = token * kHeads + head
+        const int i = row / kHeads, h = row % kHeads;
+        uint32_t lo = 0, hi = 0, sc = 0;
+        float weight = 0.f;
+        if (h < p.s.num_heads) {
+          const int64_t head = static_cast<int64_t>(walk.q + i) * p.s.num_heads + h;
+          const uint8_t* src = p.s.q_index + head * (kIndexDim * 2) + g * (2 * kGroup);
+          const uint4 a = ld_nc_v4(src), b = ld_nc_v4(src + 16);
+          const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+          float s;
+          sc = quantize_group(v, lo, hi, s);
+          if (g == 0) weight = __ldg(p.s.weights + head);
+        }
+        const uint32_t at = q_codes(buf) + sw64_off(row, g >> 1) + (g & 1) * 8;
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(lo), "r"(hi) : "memory");
+        asm volatile("st.shared.u8 [%0], %1;" ::"r"(q_scales(buf) + i * kTileScales + scale_off(h, g)),
+                     "r"(sc)
+                     : "memory");
+        if (g == 0)
+          st_shared_u32(q_weights(buf) + row * 4, __float_as_uint(weight));
+      }
+      fence_proxy_async_cta();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(Bars::kQFull, buf));
+      ++run;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kScoreMmaWarp) tmem_dealloc(tmem);
+  if (tid == 0) p.s.status[blockIdx.x] = ld_shared_u32(abort_addr);
+}
+
+template <int kChunks>
+int32_t launch_chunks(const ScoreParams& p, cudaStream_t stream) {
+  const size_t smem = kQBase + 2 * static_cast<size_t>(q_buffer_bytes(32 * kChunks, p.group));
+  if (cudaFuncSetAttribute(score_kernel<kChunks>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem)) != cudaSuccess) {
     cudaGetLastError();
     return NVFP4_MLA_ERR_LAUNCH;
   }
-  score_kernel<<<dim3(static_cast<unsigned>(p.tiles), p.num_q), kScoreTile, smem, stream>>>(p);
+  score_kernel<kChunks><<<p.ctas, kScoreThreads, smem, stream>>>(p);
   return launch_status();
+}
+
+}  // namespace
+
+int32_t launch_scores(SelectParams& s, int num_sms, cudaStream_t stream) {
+  ScoreParams p;
+  const int chunks = (s.num_heads + 31) / 32;
+  // Query tokens of a sequence share its key tiles: runs as long as there are
+  // tokens per sequence, on average, and shared memory for their queries.
+  const int32_t mean = s.num_q / s.num_seqs;
+  const int32_t most = max_group(chunks);
+  p.group = s.group = mean < 1 ? 1 : mean > most ? most : mean;
+  p.ctas = s.score_ctas = num_sms < kStatusWords ? num_sms : kStatusWords;
+  p.s = s;
+  switch (chunks) {
+    case 1: return launch_chunks<1>(p, stream);
+    case 2: return launch_chunks<2>(p, stream);
+    case 3: return launch_chunks<3>(p, stream);
+    default: return launch_chunks<4>(p, stream);
+  }
 }
 
 }  // namespace nvfp4_mla

@@ -12,7 +12,7 @@
 // The bound: a dot product's terms sum up, in magnitude, to at most
 // 6 smax * |q^_j|_1 with smax the largest scale of the visible keys, so with
 // M = 6 smax * sum_j |w_j| |q^_j|_1 the fp32 score is off by at most
-// (kDotError + (heads + 4) 2^-24) M.
+// (kDotError + (heads / 8 + 8) 2^-24) M: heads are summed up in eight parts.
 #include <math.h>
 
 #include "select_common.cuh"
@@ -26,9 +26,9 @@ namespace {
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kListCap = 1024;  // candidates ranked from shared memory
-// Relative error of one fp32 dot product of 128 terms: sequential sums of up
-// to 128 products round 127 times.
-constexpr double kDotError = 128.0 / 16777216.0;
+// Error of a dot product on the tensor cores, relative to the sum of its
+// terms' magnitudes.
+constexpr double kDotError = 64.0 / 16777216.0;
 
 // Ordered integers: a < b as floats iff key(a) < key(b); no NaN, -0 = +0.
 __device__ __forceinline__ uint32_t key32(float a) {
@@ -196,8 +196,9 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
   const int32_t t = blockIdx.x;
   const int64_t width = static_cast<int64_t>(p.num_select) * p.block;
   int32_t* out = p.topk_idx + t * width;
-  const int32_t seen = visible_positions(p, t);
-  const int32_t blocks = static_cast<int32_t>((static_cast<int64_t>(seen) + p.block - 1) / p.block);
+  const int32_t seq = __ldg(p.q_seq + t);
+  const int32_t seen = visible_positions(p, seq, __ldg(p.q_pos + t));
+  const int32_t blocks = blocks_of_positions(seen, p.block);
 
   if (tid == 0) sh.failed = 0;
   __syncthreads();
@@ -214,7 +215,6 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     return;
   }
 
-  const int32_t seq = __ldg(p.q_seq + t);
   const int granule = min(p.block, kMaxGranule);
   const int per = p.block / granule;
   const int32_t granules = (seen + granule - 1) / granule;
@@ -269,10 +269,15 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
       if (g % kIndexScales == 0) sh.w[g / kIndexScales] = w;
       m += static_cast<double>(fabsf(w)) * (0.5 * mag) * static_cast<double>(s);
     }
-    float smax = 0.f;
+    int32_t lead = t;  // first token of t's run
+    while (lead % p.group != 0 && __ldg(p.q_seq + lead - 1) == seq) --lead;
+    uint32_t top = 0;
     const int32_t tiles = (seen + kScoreTile - 1) / kScoreTile;
     for (int32_t i = tid; i < tiles; i += kSelThreads)
-      smax = fmaxf(smax, __ldcg(p.smax + t * p.tiles + i));
+      top = __vmaxu4(top, __ldcg(p.smax + lead * p.tiles + i));
+    top = __vmaxu4(top, top >> 16);
+    top = __vmaxu4(top, top >> 8) & 0xFFu;
+    float smax = scale_value(top);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
       m += __shfl_xor_sync(0xffffffffu, m, d);
@@ -290,7 +295,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     m *= 6.0 * static_cast<double>(smax);
     // rounded up to fp32; the last term covers products below the smallest
     // normal fp32
-    const double eps = m == 0.0 ? 0.0 : m * (kDotError + (p.num_heads + 4) / 16777216.0) + 1e-40;
+    const double eps = m == 0.0 ? 0.0 : m * (kDotError + (p.num_heads / 8 + 8) / 16777216.0) + 1e-40;
     const float eps2 = __double2float_ru(2.0 * eps);
     // A score of -inf comes from a NaN or a page that does not resolve, not
     // from rounding, unless fp32 overflowed.
@@ -521,7 +526,7 @@ extern "C" int32_t sparse_mla_select(const void* q_index, const float* weights,
     p.topk_idx = topk_idx + static_cast<int64_t>(q0) * num_select * select_block;
     p.scores = static_cast<float*>(workspace);
     p.score_stride = w.score_stride;
-    p.smax = p.scores + w.score_stride * w.chunk;
+    p.smax = reinterpret_cast<uint32_t*>(p.scores + w.score_stride * w.chunk);
     p.tiles = w.tiles;
     p.status = reinterpret_cast<uint32_t*>(p.smax + w.tiles * w.chunk);
     p.wait_cycles = decode_wait_cycles();

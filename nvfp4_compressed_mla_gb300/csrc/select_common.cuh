@@ -27,26 +27,35 @@ struct SelectParams {
   int32_t* topk_idx;
   float* scores;      // [num_q, score_stride]
   int64_t score_stride;
-  float* smax;        // [num_q, tiles]: largest key scale of each tile
+  // [num_q, tiles]: the largest key scale byte of each tile's quarters, in the
+  // row of the first query token of a run (consecutive tokens of one sequence
+  // inside an aligned group of `group`)
+  uint32_t* smax;
   int64_t tiles;
+  int32_t group;
   uint32_t* status;   // [kStatusWords]
   int32_t score_ctas;
   long long wait_cycles;
 };
 
-// Positions that query token t sees, 0 for none.
-__device__ __forceinline__ int32_t visible_positions(const SelectParams& p, int32_t t) {
-  const int32_t seq = __ldg(p.q_seq + t), pos = __ldg(p.q_pos + t);
+// Positions that a query token at `pos` of sequence `seq` sees, 0 for none.
+__device__ __forceinline__ int32_t visible_positions(const SelectParams& p, int32_t seq,
+                                                     int32_t pos) {
   if (seq < 0 || seq >= p.num_seqs || pos < 0) return 0;
   const int64_t room = static_cast<int64_t>(p.max_blocks) * p.page_size;
   return static_cast<int32_t>(min(static_cast<int64_t>(pos) + 1, room));
 }
 
+__device__ __forceinline__ int32_t blocks_of_positions(int32_t positions, int32_t block) {
+  const int shift = __ffs(block) - 1;  // a power of two
+  return static_cast<int32_t>((static_cast<int64_t>(positions) + block - 1) >> shift);
+}
+
 // Positions that have to be scored: none where every visible block is taken.
-__device__ __forceinline__ int32_t scored_positions(const SelectParams& p, int32_t t) {
-  const int32_t n = visible_positions(p, t);
-  const int64_t blocks = (static_cast<int64_t>(n) + p.block - 1) / p.block;
-  return blocks > p.num_select ? n : 0;
+__device__ __forceinline__ int32_t scored_positions_of(const SelectParams& p, int32_t seq,
+                                                       int32_t pos) {
+  const int32_t n = visible_positions(p, seq, pos);
+  return blocks_of_positions(n, p.block) > p.num_select ? n : 0;
 }
 
 int32_t launch_scores(SelectParams& p, int num_sms, cudaStream_t stream);
