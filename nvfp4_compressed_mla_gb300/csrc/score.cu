@@ -19,15 +19,19 @@
 //
 //   warps 0-7    epilogue: two sets of four; a set takes every other
 //                (tile, query token) unit, warp w the positions 32 (w % 4)..
-//   warps 8-11   key loads: warp w resolves its 32 positions through the block
-//                table (two tiles ahead) and copies their codes and scales
-//                with cp.async, six tiles in flight
+//   warp 8       key loads: resolves a tile's pages through the block table
+//                (two tiles ahead) and copies codes (tensor copies, swizzled on
+//                the way) and scales, up to eight tiles in flight
+//   warps 9-11   take turns in laying out a tile's scales for the tensor cores
+//   (pages that do not cut tiles into whole 8-row groups: warps 8-11 copy row
+//   by row with cp.async instead)
 //   warp 12      issues the scale copies and MMAs
 //   warps 13-15  encode the next run's queries
 //
 // Every wait is bounded; when one runs out the CTA's roles unwind, what is in
 // flight is drained, and the CTA's status word says so.
 #include <math.h>
+#include <string.h>
 
 #include "select_common.cuh"
 #include "tc_ptx.cuh"
@@ -38,6 +42,7 @@ namespace {
 constexpr int kScoreThreads = 512;
 constexpr int kEpiWarps = 8;
 constexpr int kLoadWarp0 = 8, kLoadWarps = 4;
+constexpr int kScaleWarp0 = 9, kScaleWarps = 3;  // with tensor copies
 constexpr int kScoreMmaWarp = 12;
 constexpr int kQWarp0 = 13, kQWarps = 3;
 constexpr int kStages = 8;        // key tiles in shared memory
@@ -46,7 +51,8 @@ constexpr int kMaskRing = 32;     // resolved-position masks; more than the tile
 constexpr int kMaxGroup = 8;      // query tokens of a run
 constexpr int kTileCodes = kScoreTile * kIndexCodes;   // 8192, 64-byte swizzle
 constexpr int kTileScales = 1024;                      // two K halves of 128 x 4 scale bytes
-constexpr int kStageBytes = kTileCodes + kTileScales;
+// a stage: codes, scales as laid out for the tensor cores, scales as stored
+constexpr int kStageBytes = kTileCodes + 2 * kTileScales;
 constexpr int kMaskBytes = kMaskRing * 4 * 4;
 // A run's cost per tile: its query tokens' epilogues and the tile's load.
 constexpr int kLoadCost = 2;
@@ -136,7 +142,8 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_
 }
 
 struct Bars {  // byte offsets in the control block
-  static constexpr int kFull = 0, kEmpty = kFull + 8 * kStages, kDFull = kEmpty + 8 * kStages,
+  static constexpr int kFull = 0, kEmpty = kFull + 8 * kStages, kRaw = kEmpty + 8 * kStages,
+                       kDFull = kRaw + 8 * kStages,
                        kDEmpty = kDFull + 64, kQFull = kDEmpty + 64, kQEmpty = kQFull + 16,
                        kDrain = kQEmpty + 16, kTmem = kDrain + 8, kAbort = kTmem + 4,
                        kStart = kAbort + 4, kEnd = kStart + 32;
@@ -153,7 +160,28 @@ struct ScoreParams {
   SelectParams s;
   int32_t group;
   int32_t ctas;
+  int32_t seg_rows;  // rows of a tensor copy; 0: copies row by row
 };
+
+// one box of a 3-D tensor map at (0, y, z)
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm, int32_t y,
+                                            int32_t z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(0), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+// Largest byte of a word, as the low byte.
+__device__ __forceinline__ uint32_t top_byte(uint32_t v) {
+  v = __vmaxu4(v, v >> 16);
+  return __vmaxu4(v, v >> 8) & 0xFFu;
+}
 
 // The runs of query tokens whose tiles a CTA scores, walked by one warp. Lane
 // i holds query token i of the current run; the next run's words are loaded
@@ -202,7 +230,7 @@ struct Walk {
 
 template <int kChunks>
 __global__ void __launch_bounds__(kScoreThreads, 1)
-    score_kernel(const __grid_constant__ ScoreParams p) {
+    score_kernel(const __grid_constant__ ScoreParams p, const __grid_constant__ CUtensorMap codes_map) {
   constexpr int kHeads = 32 * kChunks;
   constexpr int kSlots = acc_slots(kChunks);
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -242,7 +270,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   if (lane == 31) warp_cost[warp] = upto;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(bar(Bars::kFull, i), kLoadWarps);
+      mbar_init(bar(Bars::kFull, i), p.seg_rows > 0 ? 1 : kLoadWarps);
+      mbar_init(bar(Bars::kRaw, i), 1);
       mbar_init(bar(Bars::kEmpty, i), 1);
     }
     for (int i = 0; i < kSlots; ++i) {
@@ -364,8 +393,115 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       if (lane == 0) mbar_arrive(bar(Bars::kQEmpty, buf));
       ++run;
     }
+  } else if (p.seg_rows > 0 && warp == kLoadWarp0) {
+    // ------------------------------------------- key loads, tensor copies
+    const int segs = kScoreTile / p.seg_rows;
+    struct Entry {
+      int32_t page, row, limit;  // lane's segment; rows of the tile in use
+      bool live;
+    };
+    int32_t tile = 0;
+    bool more = walk.next(p);
+    if (more) tile = walk.t0;
+    auto fetch = [&](Entry& e) {
+      e.page = -1;
+      e.row = e.limit = 0;
+      e.live = more;
+      if (!more) return;
+      e.limit = static_cast<int32_t>(__reduce_max_sync(0xffffffffu, walk.seen)) - tile * kScoreTile;
+      if (lane < segs && lane * p.seg_rows < e.limit) {
+        const int32_t pos = tile * kScoreTile + lane * p.seg_rows;
+        const int32_t lb = pos / p.s.page_size;
+        e.row = pos - lb * p.s.page_size;
+        e.page = __ldg(p.s.block_table + static_cast<int64_t>(walk.seq) * p.s.max_blocks + lb);
+      }
+      if (++tile == walk.t1) {
+        more = walk.next(p);
+        tile = walk.t0;
+      }
+    };
+    const int seg_shift = __ffs(p.seg_rows) - 1;
+    Entry e0, e1, e2;
+    fetch(e0);
+    fetch(e1);
+    uint32_t it = 0;
+    bool ok = true;
+    for (; e0.live; ++it) {
+      fetch(e2);
+      const uint32_t stage = it % kStages;
+      ok = warp_wait(bar(Bars::kEmpty, stage), ((it / kStages) & 1u) ^ 1u, abort_addr, lim);
+      if (!ok) break;
+      const uint32_t dst = base + stage * kStageBytes;
+      const bool live = e0.page >= 0 && e0.page < p.s.num_blocks;
+      const uint32_t found = __ballot_sync(0xffffffffu, live);
+      uint32_t mask[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = i * 32 + lane;
+        mask[i] = __ballot_sync(0xffffffffu, r < e0.limit && (found >> (r >> seg_shift) & 1u));
+      }
+      if (lane == 0) {
+        st_shared_v4(base + kStages * kStageBytes + (it % kMaskRing) * 16, mask[0], mask[1],
+                     mask[2], mask[3]);
+        mbar_arrive_tx(bar(Bars::kRaw, stage),
+                       kTileCodes + __popc(found) * p.seg_rows * kIndexScales);
+      }
+      __syncwarp();
+      if (lane < segs) {  // a page that does not resolve: past the pool, zeros
+        tma_load_3d(dst + lane * p.seg_rows * kIndexCodes, &codes_map, e0.row,
+                    live ? e0.page : static_cast<int32_t>(p.s.num_blocks), bar(Bars::kRaw, stage));
+        if (live)
+          bulk_g2s(dst + kTileCodes + kTileScales + lane * p.seg_rows * kIndexScales,
+                   p.s.cache + static_cast<int64_t>(e0.page) * p.s.block_stride +
+                       static_cast<int64_t>(p.s.page_size) * kIndexCodes +
+                       static_cast<int64_t>(e0.row) * kIndexScales,
+                   p.seg_rows * kIndexScales, bar(Bars::kRaw, stage));
+      }
+      e0 = e1;
+      e1 = e2;
+    }
+    if (!ok)  // copies in flight land before the CTA ends
+      for (uint32_t k = it > kStages ? it - kStages : 0; k < it; ++k) {
+        const long long t0 = clock64();
+        while (!mbar_test(bar(Bars::kRaw, k % kStages), (k / kStages) & 1u) &&
+               clock64() - t0 < (1ll << 31)) {
+        }
+      }
+  } else if (p.seg_rows > 0 && warp < kScaleWarp0 + kScaleWarps) {
+    // ------------------------------------------- scales, tensor copies
+    uint32_t it = 0;
+    bool ok = true;
+    while (ok && walk.next(p)) {
+      for (int32_t tile = walk.t0; ok && tile < walk.t1; ++tile, ++it) {
+        if (it % kScaleWarps != static_cast<uint32_t>(warp - kScaleWarp0)) continue;
+        const uint32_t stage = it % kStages;
+        ok = warp_wait(bar(Bars::kRaw, stage), (it / kStages) & 1u, abort_addr, lim);
+        if (!ok) break;
+        const uint4 mask = ld_shared_v4(base + kStages * kStageBytes + (it % kMaskRing) * 16);
+        const uint32_t to = base + stage * kStageBytes + kTileCodes + lane * 16;
+        const uint32_t from = base + stage * kStageBytes + kTileCodes + kTileScales + lane * 8;
+        uint2 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[i] = ld_shared_v2(from + i * 256);
+          const uint32_t m = i == 0 ? mask.x : i == 1 ? mask.y : i == 2 ? mask.z : mask.w;
+          if (!(m >> lane & 1u)) v[i] = make_uint2(0, 0);
+        }
+        st_shared_v4(to, v[0].x, v[1].x, v[2].x, v[3].x);
+        st_shared_v4(to + 512, v[0].y, v[1].y, v[2].y, v[3].y);
+        fence_proxy_async_cta();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(Bars::kFull, stage));
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          top = __vmaxu4(top, __vmaxu4(v[i].x & 0x7F7F7F7Fu, v[i].y & 0x7F7F7F7Fu));
+        top = __reduce_max_sync(0xffffffffu, top_byte(top));
+        if (lane == 0) p.s.smax[walk.q * p.s.tiles + tile] = min(top, 0x7Eu);
+      }
+    }
   } else if (warp < kLoadWarp0 + kLoadWarps) {
-    // ----------------------------------------------------------- key loads
+    // ---------------------------------------------- key loads, row by row
     const int part = warp - kLoadWarp0;
     struct Entry {
       int32_t page, row;  // page -1: nothing to load
@@ -398,10 +534,9 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     auto publish = [&](uint32_t it) {  // this warp's rows of tile `it` have landed
       const uint32_t stage = it % kStages;
       const uint32_t sc = base + stage * kStageBytes + kTileCodes + lane * 16 + part * 4;
-      uint32_t top = __vmaxu4(ld_shared_u32(sc) & 0x7F7F7F7Fu, ld_shared_u32(sc + 512) & 0x7F7F7F7Fu);
-      top = __vmaxu4(top, top >> 16);
-      top = __vmaxu4(top, top >> 8) & 0xFFu;
-      top = __reduce_max_sync(0xffffffffu, top);
+      const uint32_t top = __reduce_max_sync(
+          0xffffffffu, top_byte(__vmaxu4(ld_shared_u32(sc) & 0x7F7F7F7Fu,
+                                         ld_shared_u32(sc + 512) & 0x7F7F7F7Fu)));
       const int32_t q = __shfl_sync(0xffffffffu, info_q, it % 32);
       const int32_t t = __shfl_sync(0xffffffffu, info_tile, it % 32);
       fence_proxy_async_cta();
@@ -469,7 +604,9 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
                         scale_desc(q_scales(buf) + i * kTileScales + h * 512));
       for (int32_t tile = walk.t0; ok && tile < walk.t1; ++tile, ++it) {
         const uint32_t stage = it % kStages;
-        ok = warp_wait(bar(Bars::kFull, stage), (it / kStages) & 1u, abort_addr, lim);
+        ok = warp_wait(bar(Bars::kFull, stage), (it / kStages) & 1u, abort_addr, lim) &&
+             (p.seg_rows == 0 ||
+              warp_wait(bar(Bars::kRaw, stage), (it / kStages) & 1u, abort_addr, lim));
         if (!ok) break;
         tc_fence_after();
         const uint32_t src = base + stage * kStageBytes;
@@ -551,15 +688,38 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   if (tid == 0) p.s.status[blockIdx.x] = ld_shared_u32(abort_addr);
 }
 
+// The pool's codes as rows of 64 bytes, in 64-byte swizzle; false where a tile
+// of 128 positions is not made of whole pieces of pages with whole 8-row groups.
+bool codes_tensor(const SelectParams& s, CUtensorMap* map, int32_t* seg_rows) {
+  const int32_t P = s.page_size;
+  *seg_rows = 0;
+  if (P % 8 != 0 || (P < kScoreTile ? kScoreTile % P : P % kScoreTile) != 0) return false;
+  EncodeTiledFn enc = encode_tiled();
+  if (enc == nullptr || s.num_blocks >= INT32_MAX || s.block_stride >= (int64_t{1} << 40))
+    return false;
+  const cuuint32_t rows = static_cast<cuuint32_t>(P < kScoreTile ? P : kScoreTile);
+  const cuuint64_t dims[3] = {kIndexCodes, static_cast<cuuint64_t>(P),
+                              static_cast<cuuint64_t>(s.num_blocks)};
+  const cuuint64_t strides[2] = {kIndexCodes, static_cast<cuuint64_t>(s.block_stride)};
+  const cuuint32_t box[3] = {kIndexCodes, rows, 1};
+  const cuuint32_t es[3] = {1, 1, 1};
+  if (enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(s.cache), dims, strides, box,
+          es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return false;
+  *seg_rows = static_cast<int32_t>(rows);
+  return true;
+}
+
 template <int kChunks>
-int32_t launch_chunks(const ScoreParams& p, cudaStream_t stream) {
+int32_t launch_chunks(const ScoreParams& p, const CUtensorMap& map, cudaStream_t stream) {
   const size_t smem = kQBase + 2 * static_cast<size_t>(q_buffer_bytes(32 * kChunks, p.group));
   if (cudaFuncSetAttribute(score_kernel<kChunks>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem)) != cudaSuccess) {
     cudaGetLastError();
     return NVFP4_MLA_ERR_LAUNCH;
   }
-  score_kernel<kChunks><<<p.ctas, kScoreThreads, smem, stream>>>(p);
+  score_kernel<kChunks><<<p.ctas, kScoreThreads, smem, stream>>>(p, map);
   return launch_status();
 }
 
@@ -575,11 +735,14 @@ int32_t launch_scores(SelectParams& s, int num_sms, cudaStream_t stream) {
   p.group = s.group = mean < 1 ? 1 : mean > most ? most : mean;
   p.ctas = s.score_ctas = num_sms < kStatusWords ? num_sms : kStatusWords;
   p.s = s;
+  CUtensorMap map;
+  memset(&map, 0, sizeof(map));
+  codes_tensor(s, &map, &p.seg_rows);
   switch (chunks) {
-    case 1: return launch_chunks<1>(p, stream);
-    case 2: return launch_chunks<2>(p, stream);
-    case 3: return launch_chunks<3>(p, stream);
-    default: return launch_chunks<4>(p, stream);
+    case 1: return launch_chunks<1>(p, map, stream);
+    case 2: return launch_chunks<2>(p, map, stream);
+    case 3: return launch_chunks<3>(p, map, stream);
+    default: return launch_chunks<4>(p, map, stream);
   }
 }
 

@@ -2,6 +2,10 @@
 // proxy fences, bulk copies, tensor memory, tcgen05 and bounded waits.
 #pragma once
 
+#include <cuda.h>
+
+#include <mutex>
+
 #include "common.cuh"
 
 namespace nvfp4_mla {
@@ -291,6 +295,26 @@ __device__ __forceinline__ bool wait_bar_hot(uint32_t bar, uint32_t parity, uint
       return false;
     }
   }
+}
+
+// ------------------------------------------------------------ host side
+// cuTensorMapEncodeTiled, looked up once through the runtime
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(f);
+  });
+  return fn;
 }
 
 }  // namespace
