@@ -438,7 +438,7 @@ int32_t nvfp4_mla_index_read(const int32_t* seq_ids, const int32_t* positions, i
  *   q_seq, q_pos device int32 [num_q]; a bad sequence or q_pos < 0 sees nothing
  *   num_heads    1..128; num_q >= 0 (0 is a no-op)
  *   block_table, num_seqs, max_blocks_per_seq, page_size  as above;
- *                max_blocks_per_seq * page_size < 2^31
+ *                max_blocks_per_seq * page_size <= 2^31 - 512
  *   cache, num_blocks, block_stride_bytes  the index-key pool; every visible
  *                row has been written by nvfp4_mla_index_append
  *   select_block a power of two, 1..128

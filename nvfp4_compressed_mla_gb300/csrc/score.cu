@@ -17,15 +17,22 @@
 // long sequence fills the device as well as many short ones. Runs are
 // consecutive query tokens of one sequence, at most `group` of them.
 //
+// Positions go through in steps of one or two tiles (two where 64 heads or
+// fewer leave room in tensor memory): each role is one or a few warps whose
+// handshakes and address arithmetic cost hundreds of cycles a step, however
+// large the step is.
+//
 //   warps 0-7    epilogue: two sets of four; a set takes every other
-//                (tile, query token) unit, warp w the positions 32 (w % 4)..
-//   warp 8       key loads: resolves a tile's pages through the block table
-//                (two tiles ahead) and copies codes (tensor copies, swizzled on
-//                the way) and scales, up to eight tiles in flight
-//   warps 9-11   take turns in laying out a tile's scales for the tensor cores
+//                (step, query token) unit, warp w the positions 32 (w % 4)..
+//                of each tile
+//   warp 8       copies the steps' codes: resolves the pages through the block
+//                table (two steps ahead), one tensor copy per page, swizzled on
+//                the way; all stages in flight
+//   warps 9-11   take turns in loading a step's scales (one turn ahead) and
+//                laying them out in tensor memory
 //   (pages that do not cut tiles into whole 8-row groups: warps 8-11 copy row
 //   by row with cp.async instead)
-//   warp 12      issues the scale copies and MMAs
+//   warp 12      issues the MMAs
 //   warps 13-15  encode the next run's queries
 //
 // Every wait is bounded; when one runs out the CTA's roles unwind, what is in
@@ -45,18 +52,20 @@ constexpr int kLoadWarp0 = 8, kLoadWarps = 4;
 constexpr int kScaleWarp0 = 9, kScaleWarps = 3;  // with tensor copies
 constexpr int kScoreMmaWarp = 12;
 constexpr int kQWarp0 = 13, kQWarps = 3;
-constexpr int kStages = 8;        // key tiles in shared memory
-constexpr int kInFlight = 6;      // key tiles whose copies are under way
-constexpr int kMaskRing = 32;     // resolved-position masks; more than the tiles between load and epilogue
+constexpr int kStageTiles = 8;    // key tiles in shared memory
+constexpr int kMaxStages = kStageTiles;
+// Resolved-position masks of the last tiles; more than there can be between a
+// step's scales and its epilogue (the stages and the accumulator slots).
+constexpr int kMaskRing = 32;
 constexpr int kMaxGroup = 8;      // query tokens of a run
 constexpr int kTileCodes = kScoreTile * kIndexCodes;   // 8192, 64-byte swizzle
 constexpr int kTileScales = 1024;                      // two K halves of 128 x 4 scale bytes
-// a stage: codes, scales as laid out for the tensor cores, scales as stored
-constexpr int kStageBytes = kTileCodes + 2 * kTileScales;
+constexpr int kTileBytes = kTileCodes + kTileScales;
 constexpr int kMaskBytes = kMaskRing * 4 * 4;
-// A run's cost per tile: its query tokens' epilogues and the tile's load.
+// A run's cost per step: its query tokens' epilogues and the step's load.
 constexpr int kLoadCost = 2;
-// Tensor memory columns: accumulator slots, then scales of Q, then of K.
+// Tensor memory columns: accumulator slots, then scales of Q, then of K (one
+// set per stage).
 constexpr uint32_t kSfbCol = 384, kSfaCol = 448;
 
 // Instruction descriptor, kind::mxf4nvf4: E2M1 A (bit 7) and B (bit 10), both
@@ -64,8 +73,11 @@ constexpr uint32_t kSfbCol = 384, kSfaCol = 448;
 __host__ __device__ constexpr uint32_t score_idesc(int n) {
   return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
 }
-__host__ __device__ constexpr int acc_slots(int chunks) {  // chunks of 32 heads
-  return chunks == 1 ? 8 : chunks == 2 ? 6 : chunks == 3 ? 4 : 3;
+// For `chunks` of 32 heads: tiles of a step, and accumulator slots of a step's
+// tiles for one query token.
+__host__ __device__ constexpr int step_tiles(int chunks) { return chunks <= 2 ? 2 : 1; }
+__host__ __device__ constexpr int acc_slots(int chunks) {
+  return 384 / (32 * chunks * step_tiles(chunks));
 }
 __host__ __device__ constexpr int max_group(int chunks) { return chunks <= 2 ? kMaxGroup : 4; }
 
@@ -122,6 +134,9 @@ __device__ __forceinline__ float relu_nan(float x) {  // max(0, x), NaN stays Na
   asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(x));
   return r;
 }
+// 2 max(0, x), exact, NaN stays NaN: an addition, where the maximum takes the
+// slower integer pipe; the epilogue uses one for half of the heads each.
+__device__ __forceinline__ float twice_relu(float x) { return x + fabsf(x); }
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
@@ -135,21 +150,38 @@ __device__ __forceinline__ float sum2(uint64_t v) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
   return lo + hi;
 }
+// True in one lane of the warp, the same one every time; the compiler knows
+// that it is one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
 // One warp's bounded wait: it leaves together.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t abort_addr,
                                           long long limit) {
   return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_addr, limit)) != 0;
 }
 
+// Bounded wait at the end, whether the CTA aborts or not.
+__device__ __noinline__ void drain(uint32_t bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_test(bar, parity) && clock64() - t0 < (1ll << 31)) {
+  }
+}
+
 struct Bars {  // byte offsets in the control block
-  static constexpr int kFull = 0, kEmpty = kFull + 8 * kStages, kRaw = kEmpty + 8 * kStages,
-                       kDFull = kRaw + 8 * kStages,
+  static constexpr int kFull = 0, kEmpty = kFull + 8 * kMaxStages,
+                       kDFull = kEmpty + 8 * kMaxStages,
                        kDEmpty = kDFull + 64, kQFull = kDEmpty + 64, kQEmpty = kQFull + 16,
-                       kDrain = kQEmpty + 16, kTmem = kDrain + 8, kAbort = kTmem + 4,
+                       kDrain = kQEmpty + 16, kScaleDrain = kDrain + 8,
+                       kTmem = kScaleDrain + 8 * kScaleWarps, kAbort = kTmem + 4,
                        kStart = kAbort + 4, kEnd = kStart + 32;
 };
 static_assert(Bars::kStart % 8 == 0, "start words");
-constexpr int kCtl = kStages * kStageBytes + kMaskBytes;
+constexpr int kMasks = kStageTiles * kTileBytes;
+constexpr int kCtl = kMasks + kMaskBytes;
 constexpr int kQBase = (kCtl + Bars::kEnd + 511) / 512 * 512;
 
 __host__ __device__ constexpr int q_buffer_bytes(int heads_pad, int group) {
@@ -160,7 +192,8 @@ struct ScoreParams {
   SelectParams s;
   int32_t group;
   int32_t ctas;
-  int32_t seg_rows;  // rows of a tensor copy; 0: copies row by row
+  int32_t seg_rows;    // rows of a tensor copy; 0: copies row by row
+  int32_t page_shift;  // log2 of the page size, -1 if it is no power of two
 };
 
 // one box of a 3-D tensor map at (0, y, z)
@@ -183,12 +216,13 @@ __device__ __forceinline__ uint32_t top_byte(uint32_t v) {
   return __vmaxu4(v, v >> 8) & 0xFFu;
 }
 
-// The runs of query tokens whose tiles a CTA scores, walked by one warp. Lane
+// The runs of query tokens whose steps a CTA scores, walked by one warp. Lane
 // i holds query token i of the current run; the next run's words are loaded
 // while the current one is worked on.
 struct Walk {
-  int32_t q, count, seq, tiles, t0, t1;  // run; tiles t0 .. t1 - 1 are this CTA's
+  int32_t q, count, seq, t0, t1;         // run; steps t0 .. t1 - 1 are this CTA's
   int32_t seen;                          // lane i: positions to score of token q + i
+  int32_t most;                          // the highest of them
   int64_t cost0, begin, end;
   int32_t next_seq, next_pos;            // lane i: words of token next_q + i
   int32_t next_q;
@@ -204,7 +238,8 @@ struct Walk {
       next_pos = __ldg(p.s.q_pos + from + lane);
     }
   }
-  // Moves to the next run with tiles of this CTA; false when there is none.
+  // Moves to the next run with steps of this CTA; false when there is none.
+  template <int kStep>
   __device__ __forceinline__ bool next(const ScoreParams& p) {
     const int32_t lane = threadIdx.x & 31;
     while (next_q < p.s.num_q && cost0 < end) {
@@ -215,13 +250,13 @@ struct Walk {
       count = __ffs(~same) - 1;  // leading lanes; lim < 32
       seen = lane < count ? scored_positions_of(p.s, seq, next_pos) : 0;
       fetch(p, q + count);
-      const int32_t most = static_cast<int32_t>(__reduce_max_sync(0xffffffffu, seen));
-      tiles = (most + kScoreTile - 1) / kScoreTile;
+      most = static_cast<int32_t>(__reduce_max_sync(0xffffffffu, seen));
+      const int32_t steps = (most + kStep - 1) / kStep;
       const int64_t w = count + kLoadCost;
       const int64_t from = begin - cost0, to = end - cost0;
-      t0 = from <= 0 ? 0 : static_cast<int32_t>(min((from + w - 1) / w, int64_t{tiles}));
-      t1 = static_cast<int32_t>(min((to + w - 1) / w, int64_t{tiles}));
-      cost0 += tiles * w;
+      t0 = from <= 0 ? 0 : static_cast<int32_t>(min((from + w - 1) / w, int64_t{steps}));
+      t1 = static_cast<int32_t>(min((to + w - 1) / w, int64_t{steps}));
+      cost0 += steps * w;
       if (t0 < t1) return true;
     }
     return false;
@@ -233,6 +268,11 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     score_kernel(const __grid_constant__ ScoreParams p, const __grid_constant__ CUtensorMap codes_map) {
   constexpr int kHeads = 32 * kChunks;
   constexpr int kSlots = acc_slots(kChunks);
+  constexpr int kTiles = step_tiles(kChunks);  // of a step
+  constexpr int kStep = kTiles * kScoreTile;
+  constexpr int kStages = kStageTiles / kTiles;
+  constexpr int kStageBytes = kTiles * kTileBytes;  // tile by tile: codes, then scales
+  constexpr uint32_t kSlotCols = kTiles * kHeads;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
   const uint32_t ctl = base + kCtl;
@@ -255,7 +295,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
         most = max(most, scored_positions_of(p.s, seq, __ldg(p.s.q_pos + q + n)));
         ++n;
       } while (q + n < stop && __ldg(p.s.q_seq + q + n) == seq);
-      each(q, static_cast<int64_t>((most + kScoreTile - 1) / kScoreTile) * (n + kLoadCost));
+      each(q, static_cast<int64_t>((most + kStep - 1) / kStep) * (n + kLoadCost));
       q += n;
     }
   };
@@ -270,8 +310,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   if (lane == 31) warp_cost[warp] = upto;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(bar(Bars::kFull, i), p.seg_rows > 0 ? 1 : kLoadWarps);
-      mbar_init(bar(Bars::kRaw, i), 1);
+      mbar_init(bar(Bars::kFull, i), p.seg_rows > 0 ? 2 : kLoadWarps);
       mbar_init(bar(Bars::kEmpty, i), 1);
     }
     for (int i = 0; i < kSlots; ++i) {
@@ -283,6 +322,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       mbar_init(bar(Bars::kQEmpty, i), kEpiWarps + 1);
     }
     mbar_init(bar(Bars::kDrain, 0), 1);
+    for (int i = 0; i < kScaleWarps; ++i) mbar_init(bar(Bars::kScaleDrain, i), 1);
     st_shared_u32(abort_addr, 0);
     fence_mbar_init();
   }
@@ -331,62 +371,67 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(quad) << 21;  // lane 32 * quad
     const int granule = min(p.s.block, kMaxGranule);
     const int shift = __ffs(granule) - 1;
-    uint32_t unit = 0, tile_no = 0, run = 0;
+    uint32_t first = 0, step_no = 0, run = 0;  // first: number of the step's first unit
     bool ok = true;
-    while (ok && walk.next(p)) {
+    while (ok && walk.next<kStep>(p)) {
       const int buf = run & 1;
       ok = warp_wait(bar(Bars::kQFull, buf), (run >> 1) & 1u, abort_addr, lim);
-      for (int32_t tile = walk.t0; ok && tile < walk.t1; ++tile, ++tile_no) {
-        const int32_t pos = tile * kScoreTile + quad * 32 + lane;
-        for (int i = 0; i < walk.count; ++i, ++unit) {
-          if ((unit & 1u) != static_cast<uint32_t>(set)) continue;
-          const uint32_t slot = unit % kSlots;
+      float* out = p.s.scores + walk.q * p.s.score_stride;
+      const uint8_t* weights = smem + (q_weights(buf) - base);
+      for (int32_t step = walk.t0; ok && step < walk.t1; ++step, ++step_no, first += walk.count) {
+        const int32_t pos0 = step * kStep + quad * 32 + lane;
+        for (int i = static_cast<int>((step_no ^ set) & 1u); i < walk.count; i += 2) {
+          const uint32_t unit = first + i, slot = unit % kSlots;
+          const int32_t seen = __shfl_sync(0xffffffffu, walk.seen, i);
           ok = warp_wait(bar(Bars::kDFull, slot), (unit / kSlots) & 1u, abort_addr, lim);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t d = tmem + lanes + slot * kHeads;
-          const uint32_t w = q_weights(buf) + i * kHeads * 4;
-          uint64_t acc[4] = {0, 0, 0, 0};
+          const auto* w = reinterpret_cast<const ulonglong2*>(weights + i * kHeads * 4);
+#pragma unroll 1
+          for (int tile = 0; tile < kTiles; ++tile) {
+            const uint32_t mask = ld_shared_u32(
+                base + kMasks + (((step_no * kTiles + tile) % kMaskRing) * 4 + quad) * 4);
+            const uint32_t d = tmem + lanes + slot * kSlotCols + tile * kHeads;
+            uint64_t acc[4] = {0, 0, 0, 0};
 #pragma unroll
-          for (int c0 = 0; c0 < kChunks; c0 += 2) {  // 64 columns in registers at a time
-            uint32_t v[2][32];
-            tmem_ld32(d + 32 * c0, v[0]);
-            if (c0 + 1 < kChunks) tmem_ld32(d + 32 * c0 + 32, v[1]);
-            tmem_ld_wait();
-            if (c0 + 2 >= kChunks) {  // the slot has been read
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar(Bars::kDEmpty, slot));
-            }
+            for (int c0 = 0; c0 < kChunks; c0 += 2) {  // 64 columns in registers at a time
+              uint32_t v[2][32];
+              tmem_ld32(d + 32 * c0, v[0]);
+              if (c0 + 1 < kChunks) tmem_ld32(d + 32 * c0 + 32, v[1]);
+              tmem_ld_wait();
+              if (c0 + 2 >= kChunks && tile == kTiles - 1) {  // the slot has been read
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(Bars::kDEmpty, slot));
+              }
 #pragma unroll
-            for (int c = 0; c < 2 && c0 + c < kChunks; ++c) {
+              for (int c = 0; c < 2 && c0 + c < kChunks; ++c) {
 #pragma unroll
-              for (int j = 0; j < 32; j += 4) {
-                uint64_t w0, w1;
-                asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
-                             : "=l"(w0), "=l"(w1)
-                             : "r"(w + (32 * (c0 + c) + j) * 4));
-                fma2(acc[(j >> 1) & 3],
-                     pack2(relu_nan(__uint_as_float(v[c][j])),
-                           relu_nan(__uint_as_float(v[c][j + 1]))),
-                     w0);
-                fma2(acc[((j >> 1) & 3) + 1],
-                     pack2(relu_nan(__uint_as_float(v[c][j + 2])),
-                           relu_nan(__uint_as_float(v[c][j + 3]))),
-                     w1);
+                for (int j = 0; j < 32; j += 4) {
+                  const ulonglong2 wj = w[(32 * (c0 + c) + j) / 4];  // four weights
+                  fma2(acc[(j >> 2) & 1],
+                       pack2(relu_nan(__uint_as_float(v[c][j])),
+                             relu_nan(__uint_as_float(v[c][j + 1]))),
+                       wj.x);
+                  fma2(acc[2 + ((j >> 2) & 1)],
+                       pack2(twice_relu(__uint_as_float(v[c][j + 2])),
+                             twice_relu(__uint_as_float(v[c][j + 3]))),
+                       wj.y);
+                }
               }
             }
+            float score =
+                fmaf(sum2(acc[2]) + sum2(acc[3]), 0.5f, sum2(acc[0]) + sum2(acc[1]));
+            const int32_t pos = pos0 + tile * kScoreTile;
+            const bool live = pos < seen;
+            score = live && (mask >> lane & 1u) && score == score ? score + 0.f : -INFINITY;
+            if (granule > 1) {
+              for (int s = 1; s < granule; s <<= 1)
+                score = fmaxf(score, __shfl_xor_sync(0xffffffffu, score, s));
+            }
+            if (live && (pos & (granule - 1)) == 0)
+              out[i * p.s.score_stride + (pos >> shift)] = score;
           }
-          float score = (sum2(acc[0]) + sum2(acc[1])) + (sum2(acc[2]) + sum2(acc[3]));
-          const uint32_t mask =
-              ld_shared_u32(base + kStages * kStageBytes + ((tile_no % kMaskRing) * 4 + quad) * 4);
-          const int32_t seen = __shfl_sync(0xffffffffu, walk.seen, i);
-          const bool live = pos < seen;
-          score = live && (mask >> lane & 1u) && score == score ? score + 0.f : -INFINITY;
-          for (int s = 1; s < granule; s <<= 1)
-            score = fmaxf(score, __shfl_xor_sync(0xffffffffu, score, s));
-          if (live && (pos & (granule - 1)) == 0)
-            p.s.scores[(walk.q + i) * p.s.score_stride + (pos >> shift)] = score;
         }
       }
       __syncwarp();
@@ -394,158 +439,224 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       ++run;
     }
   } else if (p.seg_rows > 0 && warp == kLoadWarp0) {
-    // ------------------------------------------- key loads, tensor copies
-    const int segs = kScoreTile / p.seg_rows;
+    // ------------------------------------------------ codes, tensor copies
+    const int segs = kStep / p.seg_rows;  // lane i resolves and copies piece i of a step
+    const int32_t past = static_cast<int32_t>(p.s.num_blocks);
     struct Entry {
-      int32_t page, row, limit;  // lane's segment; rows of the tile in use
+      int32_t page, row;
       bool live;
     };
-    int32_t tile = 0;
-    bool more = walk.next(p);
-    if (more) tile = walk.t0;
-    auto fetch = [&](Entry& e) {
-      e.page = -1;
-      e.row = e.limit = 0;
-      e.live = more;
-      if (!more) return;
-      e.limit = static_cast<int32_t>(__reduce_max_sync(0xffffffffu, walk.seen)) - tile * kScoreTile;
-      if (lane < segs && lane * p.seg_rows < e.limit) {
-        const int32_t pos = tile * kScoreTile + lane * p.seg_rows;
-        const int32_t lb = pos / p.s.page_size;
-        e.row = pos - lb * p.s.page_size;
-        e.page = __ldg(p.s.block_table + static_cast<int64_t>(walk.seq) * p.s.max_blocks + lb);
-      }
-      if (++tile == walk.t1) {
-        more = walk.next(p);
-        tile = walk.t0;
-      }
-    };
-    const int seg_shift = __ffs(p.seg_rows) - 1;
-    Entry e0, e1, e2;
-    fetch(e0);
-    fetch(e1);
-    uint32_t it = 0;
-    bool ok = true;
-    for (; e0.live; ++it) {
-      fetch(e2);
-      const uint32_t stage = it % kStages;
-      ok = warp_wait(bar(Bars::kEmpty, stage), ((it / kStages) & 1u) ^ 1u, abort_addr, lim);
-      if (!ok) break;
-      const uint32_t dst = base + stage * kStageBytes;
-      const bool live = e0.page >= 0 && e0.page < p.s.num_blocks;
-      const uint32_t found = __ballot_sync(0xffffffffu, live);
-      uint32_t mask[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = i * 32 + lane;
-        mask[i] = __ballot_sync(0xffffffffu, r < e0.limit && (found >> (r >> seg_shift) & 1u));
-      }
-      if (lane == 0) {
-        st_shared_v4(base + kStages * kStageBytes + (it % kMaskRing) * 16, mask[0], mask[1],
-                     mask[2], mask[3]);
-        mbar_arrive_tx(bar(Bars::kRaw, stage),
-                       kTileCodes + __popc(found) * p.seg_rows * kIndexScales);
-      }
-      __syncwarp();
-      if (lane < segs) {  // a page that does not resolve: past the pool, zeros
-        tma_load_3d(dst + lane * p.seg_rows * kIndexCodes, &codes_map, e0.row,
-                    live ? e0.page : static_cast<int32_t>(p.s.num_blocks), bar(Bars::kRaw, stage));
-        if (live)
-          bulk_g2s(dst + kTileCodes + kTileScales + lane * p.seg_rows * kIndexScales,
-                   p.s.cache + static_cast<int64_t>(e0.page) * p.s.block_stride +
-                       static_cast<int64_t>(p.s.page_size) * kIndexCodes +
-                       static_cast<int64_t>(e0.row) * kIndexScales,
-                   p.seg_rows * kIndexScales, bar(Bars::kRaw, stage));
-      }
-      e0 = e1;
-      e1 = e2;
-    }
-    if (!ok)  // copies in flight land before the CTA ends
-      for (uint32_t k = it > kStages ? it - kStages : 0; k < it; ++k) {
-        const long long t0 = clock64();
-        while (!mbar_test(bar(Bars::kRaw, k % kStages), (k / kStages) & 1u) &&
-               clock64() - t0 < (1ll << 31)) {
-        }
-      }
-  } else if (p.seg_rows > 0 && warp < kScaleWarp0 + kScaleWarps) {
-    // ------------------------------------------- scales, tensor copies
-    uint32_t it = 0;
-    bool ok = true;
-    while (ok && walk.next(p)) {
-      for (int32_t tile = walk.t0; ok && tile < walk.t1; ++tile, ++it) {
-        if (it % kScaleWarps != static_cast<uint32_t>(warp - kScaleWarp0)) continue;
-        const uint32_t stage = it % kStages;
-        ok = warp_wait(bar(Bars::kRaw, stage), (it / kStages) & 1u, abort_addr, lim);
-        if (!ok) break;
-        const uint4 mask = ld_shared_v4(base + kStages * kStageBytes + (it % kMaskRing) * 16);
-        const uint32_t to = base + stage * kStageBytes + kTileCodes + lane * 16;
-        const uint32_t from = base + stage * kStageBytes + kTileCodes + kTileScales + lane * 8;
-        uint2 v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[i] = ld_shared_v2(from + i * 256);
-          const uint32_t m = i == 0 ? mask.x : i == 1 ? mask.y : i == 2 ? mask.z : mask.w;
-          if (!(m >> lane & 1u)) v[i] = make_uint2(0, 0);
-        }
-        st_shared_v4(to, v[0].x, v[1].x, v[2].x, v[3].x);
-        st_shared_v4(to + 512, v[0].y, v[1].y, v[2].y, v[3].y);
-        fence_proxy_async_cta();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(Bars::kFull, stage));
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          top = __vmaxu4(top, __vmaxu4(v[i].x & 0x7F7F7F7Fu, v[i].y & 0x7F7F7F7Fu));
-        top = __reduce_max_sync(0xffffffffu, top_byte(top));
-        if (lane == 0) p.s.smax[walk.q * p.s.tiles + tile] = min(top, 0x7Eu);
-      }
-    }
-  } else if (warp < kLoadWarp0 + kLoadWarps) {
-    // ---------------------------------------------- key loads, row by row
-    const int part = warp - kLoadWarp0;
-    struct Entry {
-      int32_t page, row;  // page -1: nothing to load
-      bool live;
-    };
-    int32_t tile = 0;
-    bool more = walk.next(p);
-    if (more) tile = walk.t0;
-    // Lane l keeps the (run, tile) of the l-th tile of every 32.
-    int32_t info_q = 0, info_tile = 0, fetched = 0;
+    int32_t step = 0;
+    bool more = walk.next<kStep>(p);
+    if (more) step = walk.t0;
     auto fetch = [&](Entry& e) {
       e.page = -1;
       e.row = 0;
       e.live = more;
       if (!more) return;
-      if (lane == fetched % 32) info_q = walk.q, info_tile = tile;
-      ++fetched;
-      const int32_t pos = tile * kScoreTile + part * 32 + lane;
-      const int32_t most = static_cast<int32_t>(__reduce_max_sync(0xffffffffu, walk.seen));
-      if (pos < most) {
-        const int32_t lb = pos / p.s.page_size;
+      const int32_t pos = step * kStep + lane * p.seg_rows;
+      if (lane < segs && pos < walk.most) {
+        const int32_t lb = p.page_shift >= 0 ? pos >> p.page_shift : pos / p.s.page_size;
         e.row = pos - lb * p.s.page_size;
         e.page = __ldg(p.s.block_table + static_cast<int64_t>(walk.seq) * p.s.max_blocks + lb);
       }
-      if (++tile == walk.t1) {
-        more = walk.next(p);
-        tile = walk.t0;
+      if (++step == walk.t1) {
+        more = walk.next<kStep>(p);
+        step = walk.t0;
       }
     };
-    auto publish = [&](uint32_t it) {  // this warp's rows of tile `it` have landed
+    const bool issuer = elect_one();
+    // piece i's rows go to row i * seg_rows of the step's tiles
+    const uint32_t piece = static_cast<uint32_t>(p.seg_rows) * kIndexCodes;
+    Entry e0, e1, e2;
+    fetch(e0);
+    fetch(e1);
+    uint32_t it = 0;
+    bool ok = true;
+    for (; e0.live; ++it) {
+      fetch(e2);
       const uint32_t stage = it % kStages;
-      const uint32_t sc = base + stage * kStageBytes + kTileCodes + lane * 16 + part * 4;
-      const uint32_t top = __reduce_max_sync(
-          0xffffffffu, top_byte(__vmaxu4(ld_shared_u32(sc) & 0x7F7F7F7Fu,
-                                         ld_shared_u32(sc + 512) & 0x7F7F7F7Fu)));
-      const int32_t q = __shfl_sync(0xffffffffu, info_q, it % 32);
-      const int32_t t = __shfl_sync(0xffffffffu, info_tile, it % 32);
+      ok = warp_wait(bar(Bars::kEmpty, stage), ((it / kStages) & 1u) ^ 1u, abort_addr, lim);
+      if (!ok) break;
+      const uint32_t full = bar(Bars::kFull, stage);
+      if (issuer) mbar_arrive_tx(full, kTiles * kTileCodes);
+      // a page that does not resolve: past the pool, zeros
+      const int32_t page =
+          static_cast<uint32_t>(e0.page) < static_cast<uint32_t>(past) ? e0.page : past;
+      uint32_t dst = base + stage * kStageBytes;
+      for (int i = 0; i < segs; ++i) {
+        const int32_t z = __shfl_sync(0xffffffffu, page, i);
+        const int32_t y = __shfl_sync(0xffffffffu, e0.row, i);
+        if (issuer) tma_load_3d(dst, &codes_map, y, z, full);
+        dst += piece;
+        if (kTiles > 1 && (i + 1) * p.seg_rows == kScoreTile) dst += kTileScales;
+      }
+      e0 = e1;
+      e1 = e2;
+    }
+    __syncwarp();
+    if (!ok) {
+      // Copies in flight land before the CTA ends: this lane stands in for the
+      // scale warps on stages that they have left.
+      for (uint32_t k = it > kStages ? it - kStages : 0; k < it; ++k) {
+        if (lane == 0) mbar_arrive(bar(Bars::kFull, k % kStages));
+        drain(bar(Bars::kFull, k % kStages), (k / kStages) & 1u);
+      }
+    }
+  } else if (p.seg_rows > 0 && warp < kScaleWarp0 + kScaleWarps) {
+    // ----------------------------------------------- scales, tensor copies
+    // Lane l has rows l, l + 32, .. of the step: their scales are one 16-byte
+    // line of each K half's layout.
+    constexpr int kRows = kStep / 32;
+    const bool issuer = elect_one();
+    const int64_t scale_at = static_cast<int64_t>(p.s.page_size) * kIndexCodes;
+    struct Turn {  // a step of this warp's: its scales, zeros for rows not in use
+      uint2 v[kRows];
+      uint32_t valid;  // bit i: row l + 32 i resolves
+      int32_t q, step;
+      uint32_t it;
+      bool live;
+    };
+    int32_t step = 0;
+    uint32_t it = 0, wait = warp - kScaleWarp0;  // steps until this warp's next
+    bool more = walk.next<kStep>(p);
+    if (more) step = walk.t0;
+    auto fetch = [&](Turn& u) {
+      while (more && wait > 0) {
+        const int32_t skip = min(static_cast<int32_t>(wait), walk.t1 - step);
+        step += skip, it += skip, wait -= skip;
+        if (step == walk.t1) {
+          more = walk.next<kStep>(p);
+          step = walk.t0;
+        }
+      }
+      u.live = more;
+      if (!more) return;
+      u.q = walk.q, u.step = step, u.it = it, u.valid = 0;
+      const int32_t* table = p.s.block_table + static_cast<int64_t>(walk.seq) * p.s.max_blocks;
+      int32_t page[kRows], row[kRows];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int32_t pos = step * kStep + i * 32 + lane;
+        const int32_t lb = p.page_shift >= 0 ? pos >> p.page_shift : pos / p.s.page_size;
+        row[i] = pos - lb * p.s.page_size;
+        page[i] = pos < walk.most ? __ldg(table + lb) : -1;
+      }
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        u.v[i] = make_uint2(0, 0);
+        if (page[i] >= 0 && page[i] < p.s.num_blocks) {
+          u.valid |= 1u << i;
+          u.v[i] = __ldg(reinterpret_cast<const uint2*>(
+              p.s.cache + page[i] * p.s.block_stride + scale_at + row[i] * kIndexScales));
+        }
+      }
+      ++it, wait = kScaleWarps - 1;
+      if (++step == walk.t1) {
+        more = walk.next<kStep>(p);
+        step = walk.t0;
+      }
+    };
+    Turn now, then;
+    fetch(now);
+    bool ok = true;
+    while (now.live) {
+      fetch(then);
+      const uint32_t stage = now.it % kStages;
+      ok = warp_wait(bar(Bars::kEmpty, stage), ((now.it / kStages) & 1u) ^ 1u, abort_addr, lim);
+      if (!ok) break;
+      uint32_t top = 0;
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        const uint2* v = now.v + 4 * t;
+        const uint32_t to = base + stage * kStageBytes + t * kTileBytes + kTileCodes + lane * 16;
+        st_shared_v4(to, v[0].x, v[1].x, v[2].x, v[3].x);
+        st_shared_v4(to + 512, v[0].y, v[1].y, v[2].y, v[3].y);
+        uint32_t mask[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          mask[i] = __ballot_sync(0xffffffffu, now.valid >> (4 * t + i) & 1u);
+          top = __vmaxu4(top, __vmaxu4(v[i].x & 0x7F7F7F7Fu, v[i].y & 0x7F7F7F7Fu));
+        }
+        if (issuer)
+          st_shared_v4(base + kMasks + ((now.it * kTiles + t) % kMaskRing) * 16, mask[0], mask[1],
+                       mask[2], mask[3]);
+      }
       fence_proxy_async_cta();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar(Bars::kFull, stage));
-        reinterpret_cast<uint8_t*>(p.s.smax + q * p.s.tiles + t)[part] =
-            static_cast<uint8_t>(min(top, 0x7Eu));
+      if (issuer) {  // into tensor memory; the stage is full when they are there
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            copy_scales(tmem + kSfaCol + (stage * kTiles + t) * 8 + h * 4,
+                        scale_desc(base + stage * kStageBytes + t * kTileBytes + kTileCodes +
+                                   h * 512));
+        mma_commit(bar(Bars::kFull, stage));
       }
+      top = __reduce_max_sync(0xffffffffu, top_byte(top));
+      if (lane < kTiles) p.s.smax[now.q * p.s.tiles + now.step * kTiles + lane] = min(top, 0x7Eu);
+      now = then;
+    }
+    if (issuer) {  // scale copies of an aborted CTA have completed
+      mma_commit(bar(Bars::kScaleDrain, warp - kScaleWarp0));
+      drain(bar(Bars::kScaleDrain, warp - kScaleWarp0), 0);
+    }
+    __syncwarp();
+  } else if (warp < kLoadWarp0 + kLoadWarps) {
+    // ---------------------------------------------- key loads, row by row
+    // Warp w has rows 32 w .. of each tile; a step's copies are one group.
+    constexpr int kInFlight = kStages - 2;
+    const int part = warp - kLoadWarp0;
+    int32_t step = 0;
+    bool more = walk.next<kStep>(p);
+    if (more) step = walk.t0;
+    // Lane l keeps the run and step of the l-th step of every 32.
+    int32_t info_q = 0, info_step = 0;
+    struct Entry {
+      int32_t page[kTiles], row[kTiles];
+      bool live;
+    };
+    uint32_t fetched = 0;
+    auto fetch = [&](Entry& e) {
+      e.live = more;
+      if (!more) return;
+      if (lane == fetched % 32) info_q = walk.q, info_step = step;
+      ++fetched;
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        const int32_t pos = step * kStep + t * kScoreTile + part * 32 + lane;
+        const int32_t lb = pos / p.s.page_size;
+        e.row[t] = pos - lb * p.s.page_size;
+        e.page[t] = pos < walk.most
+                        ? __ldg(p.s.block_table +
+                                static_cast<int64_t>(walk.seq) * p.s.max_blocks + lb)
+                        : -1;
+      }
+      if (++step == walk.t1) {
+        more = walk.next<kStep>(p);
+        step = walk.t0;
+      }
+    };
+    auto publish = [&](uint32_t it) {  // this warp's rows of step `it` have landed
+      const uint32_t stage = it % kStages;
+      uint32_t top = 0;
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        const uint32_t sc =
+            base + stage * kStageBytes + t * kTileBytes + kTileCodes + lane * 16 + part * 4;
+        top = __vmaxu4(top, __vmaxu4(ld_shared_u32(sc) & 0x7F7F7F7Fu,
+                                     ld_shared_u32(sc + 512) & 0x7F7F7F7Fu));
+      }
+      top = __reduce_max_sync(0xffffffffu, top_byte(top));
+      const int32_t q = __shfl_sync(0xffffffffu, info_q, it % 32);
+      const int32_t at = __shfl_sync(0xffffffffu, info_step, it % 32) * kTiles;
+      fence_proxy_async_cta();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(Bars::kFull, stage));
+      if (lane < kTiles)
+        reinterpret_cast<uint8_t*>(p.s.smax + q * p.s.tiles + at + lane)[part] =
+            static_cast<uint8_t>(min(top, 0x7Eu));
     };
     Entry e0, e1, e2;
     fetch(e0);
@@ -557,25 +668,28 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       const uint32_t stage = it % kStages;
       ok = warp_wait(bar(Bars::kEmpty, stage), ((it / kStages) & 1u) ^ 1u, abort_addr, lim);
       if (!ok) break;
-      const uint32_t dst = base + stage * kStageBytes;
-      const bool live = e0.page >= 0 && e0.page < p.s.num_blocks;
-      const uint32_t mask = __ballot_sync(0xffffffffu, live);
-      if (lane == 0)
-        st_shared_u32(base + kStages * kStageBytes + ((it % kMaskRing) * 4 + part) * 4, mask);
-      const int64_t page = live ? static_cast<int64_t>(e0.page) * p.s.block_stride : 0;
-      const int64_t codes = page + static_cast<int64_t>(e0.row) * kIndexCodes;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {  // eight rows each, four lanes a row
-        const int r = i * 8 + (lane >> 2);
-        const int64_t at = __shfl_sync(0xffffffffu, codes, r);
-        cp_async16_z(dst + sw64_off(part * 32 + r, lane & 3), p.s.cache + at + (lane & 3) * 16,
-                     (mask >> r) & 1u);
+      for (int t = 0; t < kTiles; ++t) {
+        const uint32_t dst = base + stage * kStageBytes + t * kTileBytes;
+        const bool live = e0.page[t] >= 0 && e0.page[t] < p.s.num_blocks;
+        const uint32_t mask = __ballot_sync(0xffffffffu, live);
+        if (lane == 0)
+          st_shared_u32(base + kMasks + (((it * kTiles + t) % kMaskRing) * 4 + part) * 4, mask);
+        const int64_t page = live ? e0.page[t] * p.s.block_stride : 0;
+        const int64_t codes = page + static_cast<int64_t>(e0.row[t]) * kIndexCodes;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // eight rows each, four lanes a row
+          const int r = i * 8 + (lane >> 2);
+          const int64_t at = __shfl_sync(0xffffffffu, codes, r);
+          cp_async16_z(dst + sw64_off(part * 32 + r, lane & 3), p.s.cache + at + (lane & 3) * 16,
+                       (mask >> r) & 1u);
+        }
+        const uint8_t* sc = p.s.cache + page + static_cast<int64_t>(p.s.page_size) * kIndexCodes +
+                            static_cast<int64_t>(e0.row[t]) * kIndexScales;
+        const uint32_t sd = dst + kTileCodes + lane * 16 + part * 4;
+        cp_async4_z(sd, sc, live);
+        cp_async4_z(sd + 512, sc + 4, live);
       }
-      const uint8_t* sc = p.s.cache + page + static_cast<int64_t>(p.s.page_size) * kIndexCodes +
-                          static_cast<int64_t>(e0.row) * kIndexScales;
-      const uint32_t sd = dst + kTileCodes + lane * 16 + part * 4;
-      cp_async4_z(sd, sc, live);
-      cp_async4_z(sd + 512, sc + 4, live);
       cp_async_commit();
       if (it >= kInFlight) {
         cp_async_wait<kInFlight>();
@@ -590,58 +704,63 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   } else if (warp == kScoreMmaWarp) {
     // ---------------------------------------------------------- MMA issue
     constexpr uint32_t idesc = score_idesc(kHeads);
-    uint32_t unit = 0, it = 0, run = 0;
+    uint32_t it = 0, run = 0, slot = 0, phase = 0;
     bool ok = true;
-    while (ok && walk.next(p)) {
+    const bool issuer = elect_one();
+    while (ok && walk.next<kStep>(p)) {
       const int buf = run & 1;
       ok = warp_wait(bar(Bars::kQFull, buf), (run >> 1) & 1u, abort_addr, lim);
       if (!ok) break;
       tc_fence_after();
-      if (lane == 0)
+      if (issuer) {
         for (int i = 0; i < walk.count; ++i)
           for (int h = 0; h < 2; ++h)
             copy_scales(tmem + kSfbCol + i * 8 + h * 4,
                         scale_desc(q_scales(buf) + i * kTileScales + h * 512));
-      for (int32_t tile = walk.t0; ok && tile < walk.t1; ++tile, ++it) {
-        const uint32_t stage = it % kStages;
-        ok = warp_wait(bar(Bars::kFull, stage), (it / kStages) & 1u, abort_addr, lim) &&
-             (p.seg_rows == 0 ||
-              warp_wait(bar(Bars::kRaw, stage), (it / kStages) & 1u, abort_addr, lim));
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t src = base + stage * kStageBytes;
-        const uint32_t sfa = tmem + kSfaCol + (it & 1u) * 8;
-        if (lane == 0)
-          for (int h = 0; h < 2; ++h)
-            copy_scales(sfa + h * 4, scale_desc(src + kTileCodes + h * 512));
-        for (int i = 0; i < walk.count; ++i, ++unit) {
-          const uint32_t slot = unit % kSlots;
-          ok = warp_wait(bar(Bars::kDEmpty, slot), ((unit / kSlots) & 1u) ^ 1u, abort_addr, lim);
+        const uint64_t q0 = sw64_desc(q_codes(buf));
+        for (int32_t step = walk.t0; ok && step < walk.t1; ++step, ++it) {
+          const uint32_t stage = it % kStages;
+          ok = wait_bar(bar(Bars::kFull, stage), (it / kStages) & 1u, abort_addr, lim);
           if (!ok) break;
           tc_fence_after();
-          if (lane == 0) {
-            const uint32_t b = q_codes(buf) + i * kHeads * kIndexCodes;
+          const uint32_t src = base + stage * kStageBytes;
+          const uint32_t sfa = tmem + kSfaCol + stage * kTiles * 8;
+          if (p.seg_rows == 0) {  // copies row by row: the scales are still in shared memory
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              mma_fp4(tmem + slot * kHeads, sw64_desc(src + 32 * h), sw64_desc(b + 32 * h), idesc,
-                      sfa + h * 4, tmem + kSfbCol + i * 8 + h * 4, h);
-            mma_commit(bar(Bars::kDFull, slot));
+            for (int t = 0; t < kTiles; ++t) {
+              copy_scales(sfa + 8 * t, scale_desc(src + t * kTileBytes + kTileCodes));
+              copy_scales(sfa + 8 * t + 4, scale_desc(src + t * kTileBytes + kTileCodes + 512));
+            }
           }
-          __syncwarp();
+          const uint64_t a = sw64_desc(src);
+          for (int i = 0; i < walk.count; ++i) {
+            ok = wait_bar(bar(Bars::kDEmpty, slot), phase ^ 1u, abort_addr, lim);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t d = tmem + slot * kSlotCols;
+            // a descriptor's address counts 16 bytes; a K step is 32 bytes
+            const uint64_t b = q0 + i * (kHeads * kIndexCodes / 16);
+            const uint32_t sfb = tmem + kSfbCol + i * 8;
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+              const uint64_t at = a + t * (kTileBytes / 16);
+              mma_fp4(d + t * kHeads, at, b, idesc, sfa + 8 * t, sfb, 0);
+              mma_fp4(d + t * kHeads, at + 2, b + 2, idesc, sfa + 8 * t + 4, sfb + 4, 1);
+            }
+            mma_commit(bar(Bars::kDFull, slot));
+            if (++slot == kSlots) slot = 0, phase ^= 1u;
+          }
+          mma_commit(bar(Bars::kEmpty, stage));
         }
-        if (lane == 0) mma_commit(bar(Bars::kEmpty, stage));
-        __syncwarp();
+        mma_commit(bar(Bars::kQEmpty, buf));
       }
-      if (lane == 0) mma_commit(bar(Bars::kQEmpty, buf));
-      __syncwarp();
+      ok = __all_sync(0xffffffffu, ok);
       ++run;
     }
     // everything this thread issued has completed before the CTA ends
-    if (lane == 0) {
+    if (issuer) {
       mma_commit(bar(Bars::kDrain, 0));
-      const long long t0 = clock64();
-      while (!mbar_test(bar(Bars::kDrain, 0), 0) && clock64() - t0 < (1ll << 31)) {
-      }
+      drain(bar(Bars::kDrain, 0), 0);
     }
     __syncwarp();
   } else {
@@ -649,7 +768,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     const int qt = tid - kQWarp0 * 32;
     uint32_t run = 0;
     bool ok = true;
-    while (ok && walk.next(p)) {
+    while (ok && walk.next<kStep>(p)) {
       const int buf = run & 1;
       ok = warp_wait(bar(Bars::kQEmpty, buf), ((run >> 1) & 1u) ^ 1u, abort_addr, lim);
       if (!ok) break;
@@ -738,6 +857,9 @@ int32_t launch_scores(SelectParams& s, int num_sms, cudaStream_t stream) {
   CUtensorMap map;
   memset(&map, 0, sizeof(map));
   codes_tensor(s, &map, &p.seg_rows);
+  p.page_shift = -1;
+  for (int i = 0; i <= 20; ++i)
+    if (s.page_size == 1 << i) p.page_shift = i;
   switch (chunks) {
     case 1: return launch_chunks<1>(p, map, stream);
     case 2: return launch_chunks<2>(p, map, stream);

@@ -441,7 +441,7 @@ bool plan_workspace(int32_t num_q, int32_t num_heads, int32_t max_blocks, int32_
                     int32_t block, Workspace& w) {
   if (num_q < 0 || num_heads < 1 || num_heads > NVFP4_MLA_MAX_HEADS || max_blocks < 1 ||
       page_size < 1 || page_size > (1 << 20) || page_size % 2 != 0 ||
-      static_cast<int64_t>(max_blocks) * page_size > INT32_MAX || block < 1 ||
+      static_cast<int64_t>(max_blocks) * page_size > INT32_MAX - 511 || block < 1 ||
       block > kScoreTile || (block & (block - 1)) != 0)
     return false;
   const int64_t room = static_cast<int64_t>(max_blocks) * page_size;

@@ -114,7 +114,7 @@ def test_select_workspace(lib):
     one, many = size(1, 16, 1000, 64, 1), size(10 ** 6, 16, 1000, 64, 1)
     assert 64000 * 4 <= one < many <= 1 << 30     # a large batch shares a bounded workspace
     assert size(1, 16, 1000, 64, 64) < one        # one score for 32 positions
-    assert size(1, 128, (1 << 31) // 64 - 1, 64, 1) < 1 << 34
+    assert size(1, 128, (1 << 31) // 64 - 8, 64, 1) < 1 << 34
 
 
 def test_valid_arguments_without_gpu_report_device(lib):
