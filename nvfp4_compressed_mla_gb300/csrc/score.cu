@@ -205,11 +205,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm,
       "l"(reinterpret_cast<uint64_t>(tm)), "r"(0), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
-  return v;
-}
 // Largest byte of a word, as the low byte.
 __device__ __forceinline__ uint32_t top_byte(uint32_t v) {
   v = __vmaxu4(v, v >> 16);
@@ -280,6 +275,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   auto bar = [ctl](int kind, int i) { return ctl + static_cast<uint32_t>(kind + 8 * i); };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long lim = p.s.wait_cycles;
+  // The selection may take the SMs that fall idle; it waits for this grid.
+  cudaTriggerProgrammaticLaunchCompletion();
 
   // ---- this CTA's part of the list
   __shared__ int64_t warp_cost[kScoreThreads / 32];

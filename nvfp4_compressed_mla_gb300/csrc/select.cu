@@ -4,15 +4,25 @@
 // of block i, e_i its exact one and |a_i - e_i| <= eps for every i, let T be
 // the k-th largest a. The k-th largest e then lies within eps of T, so a block
 // with a_i > T + 2 eps is in and one with a_i < T - 2 eps is out; what lies
-// between (mostly T's block alone) is scored again exactly: codes are small
-// integers and the product of two E4M3 scales has 8 significant bits, so a dot
-// product of 128 terms is an exact double (multiples of 2^-20 below 2^31), and
-// only the weighted sum over the heads rounds, to 53 bits.
+// between (mostly T's block and a few neighbours) is scored again: codes are
+// small integers and the product of two E4M3 scales has 8 significant bits, so
+// a dot product of 128 terms is an exact 51-bit integer. Summed up over the
+// heads in fp32 that gives an interval around e_i a thousand times narrower
+// than 2 eps; blocks whose intervals still overlap at the border are summed up
+// in fp64, which this part runs at 1/64 of its fp32 rate.
 //
 // The bound: a dot product's terms sum up, in magnitude, to at most
 // 6 smax * |q^_j|_1 with smax the largest scale of the visible keys, so with
 // M = 6 smax * sum_j |w_j| |q^_j|_1 the fp32 score is off by at most
 // (kDotError + (heads / 8 + 8) 2^-24) M: heads are summed up in eight parts.
+//
+// One CTA per query token holds the scores of all blocks in shared memory
+// where they fit (32768). Longer rows: a sample of 4096 scores gives a
+// threshold that a little more than k of them pass, one sweep collects those
+// that do (a cluster of CTAs shares the sweep where there are few query
+// tokens), and the choice is made among them. Where a sweep collects too few
+// or too many, and for a border among equal scores, the general form reads the
+// scores from memory in every step.
 #include <math.h>
 
 #include "select_common.cuh"
@@ -23,14 +33,24 @@ long long decode_wait_cycles();
 
 namespace {
 
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kListCap = 1024;  // candidates ranked from shared memory
+constexpr int kBins = 2048;
+constexpr int kSample = 4096;
+constexpr int kListMax = 16384;          // collected scores of a long row
+constexpr int kDenseMax = 2 * kListMax;  // scores held without their indexes
+constexpr int kMaxCluster = 8;
 // Error of a dot product on the tensor cores, relative to the sum of its
-// terms' magnitudes.
-constexpr double kDotError = 64.0 / 16777216.0;
+// terms' magnitudes: 2.9 x 2^-24 is the most measured over 5e5 dot products,
+// with scales up to 2^15 apart.
+constexpr double kDotError = 16.0 / 16777216.0;
+// Error of an fp32 sum over the heads of exact dot products, relative to
+// sum_j |w_j| D_j: two roundings of each D, at most four terms and
+// five shuffles in a chain, and those of the bound itself.
+constexpr float kSumError = 16.0f / 16777216.0f;
+constexpr float kTiny = 1e-42f;  // products below the smallest normal fp32 round by less
 
-// Ordered integers: a < b as floats iff key(a) < key(b); no NaN, -0 = +0.
+// Ordered integers: a < b as floats iff key(a) < key(b); -0 = +0. The keys of
+// NaNs mark blocks whose fate is known.
+constexpr uint32_t kIn = 0xFFFFFFFFu, kTie = 0xFFFFFFFEu, kOut = 0u;
 __device__ __forceinline__ uint32_t key32(float a) {
   const uint32_t u = __float_as_uint(a + 0.f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
@@ -49,384 +69,768 @@ __device__ __forceinline__ int32_t twice_e2m1(uint32_t code) {
   const int32_t m = static_cast<int32_t>((0xC8643210u >> (4 * (code & 7u))) & 15u);
   return code & 8u ? -m : m;
 }
-// Eight codes of a word -> two words of four signed bytes.
-__device__ __forceinline__ void expand_codes(uint32_t w, uint32_t& a, uint32_t& b) {
-  a = b = 0;
+// Four codes -> four signed bytes.
+__device__ __forceinline__ uint32_t expand_codes(uint32_t w) {
+  uint32_t a = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 4; ++i)
     a |= (static_cast<uint32_t>(twice_e2m1(w >> (4 * i))) & 0xFFu) << (8 * i);
-    b |= (static_cast<uint32_t>(twice_e2m1(w >> (4 * i + 16))) & 0xFFu) << (8 * i);
-  }
+  return a;
+}
+// An E4M3 scale byte as an integer m * 2^s, in units of 2^-9: m | s << 8.
+__device__ __forceinline__ uint32_t scale_parts(uint32_t byte) {
+  const uint32_t e = byte >> 3 & 15u, m = byte & 7u;
+  return e != 0 ? (8u + m) | (e - 1) << 8 : m;
 }
 __device__ __forceinline__ float scale_value(uint32_t byte) {
   return f16_bits_to_f32(static_cast<uint16_t>(e4m3x2_to_f16x2(static_cast<uint16_t>(byte))));
 }
 
+constexpr int kHeadWords = 33;  // 32 words of codes; one more keeps lanes' heads in different banks
+constexpr int kHeadScales = 9;
+
+template <int kThreads>
 struct SelShared {
-  uint32_t q_codes[NVFP4_MLA_MAX_HEADS * kIndexScales * 4];  // signed bytes, twice the values
-  float q_scale[NVFP4_MLA_MAX_HEADS * kIndexScales];
+  static constexpr int kWarps = kThreads / 32;
+  static constexpr int kCands = kThreads;  // candidates ranked from shared memory
+  uint32_t q_codes[NVFP4_MLA_MAX_HEADS * kHeadWords];  // signed bytes, twice the values
+  uint32_t q_scale[NVFP4_MLA_MAX_HEADS * kHeadScales];
   float w[NVFP4_MLA_MAX_HEADS];
-  uint32_t hist[256];
-  uint64_t cand_key[kListCap];
-  int32_t cand[kListCap];
-  double red[kSelWarps];
-  float redf[kSelWarps];
-  int32_t warp_sum[kSelWarps];
-  int32_t warp_sum2[kSelWarps];
-  uint32_t pick, rest, cand_n, in_n, failed;
+  uint32_t hist[kBins];
+  uint64_t cand_key[kCands];              // fp64 score, as a key
+  uint32_t cand_lo[kCands], cand_hi[kCands];  // interval around the exact score, as keys
+  int32_t cand[kCands];                   // position in the row of keys
+  double red[kWarps];
+  uint32_t redu[kWarps], redv[kWarps];
+  int32_t sum_a[kWarps], sum_b[kWarps];
+  uint32_t pick, rest, n, failed;
 };
 
-__device__ __forceinline__ float block_score(const SelectParams& p, const float* row, int32_t b,
-                                             int per, int32_t granules) {
-  float a = __ldcg(row + static_cast<int64_t>(b) * per);
-  for (int i = 1; i < per; ++i)
-    if (static_cast<int64_t>(b) * per + i < granules)
-      a = fmaxf(a, __ldcg(row + static_cast<int64_t>(b) * per + i));
-  return a;
-}
+struct SelectConfig {
+  int32_t room;  // keys that the dynamic shared memory behind SelShared holds
+};
 
-// Exact score of position `pos` as an ordered key, by one warp.
-__device__ uint64_t exact_key(const SelectParams& p, const SelShared& sh, int32_t seq,
-                              int32_t pos) {
-  const int lane = threadIdx.x & 31;
-  const IndexRow at = resolve_index_row(seq, pos, p.block_table, p.num_seqs, p.max_blocks,
-                                        p.page_size, p.num_blocks, p.block_stride);
-  if (at.page < 0) return kLowest64;
-  const uint8_t* page = p.cache + at.page;
-  const int g = lane & 7;
-  const uint2 c = __ldg(reinterpret_cast<const uint2*>(
-      page + static_cast<int64_t>(at.row) * kIndexCodes + g * 8));
-  const float ks = scale_value(__ldg(page + static_cast<int64_t>(p.page_size) * kIndexCodes +
-                                     static_cast<int64_t>(at.row) * kIndexScales + g) &
-                               0x7Fu);
-  uint32_t k[4];
-  expand_codes(c.x, k[0], k[1]);
-  expand_codes(c.y, k[2], k[3]);
-  double sum = 0.0;
-  for (int j0 = 0; j0 < p.num_heads; j0 += 4) {  // four heads, eight lanes each
-    const int j = j0 + (lane >> 3);
-    double d = 0.0;
-    if (j < p.num_heads) {
-      const uint32_t* q = sh.q_codes + (j * kIndexScales + g) * 4;
-      int dot = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        dot = __dp4a(static_cast<int>(q[i]), static_cast<int>(k[i]), dot);
-      d = static_cast<double>(dot) * 0.25 *
-          static_cast<double>(ks * sh.q_scale[j * kIndexScales + g]);
-    }
-    d += __shfl_xor_sync(0xffffffffu, d, 1);
-    d += __shfl_xor_sync(0xffffffffu, d, 2);
-    d += __shfl_xor_sync(0xffffffffu, d, 4);
-    if (j < p.num_heads) sum += static_cast<double>(sh.w[j]) * (d < 0.0 ? 0.0 : d);
-  }
-  sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-  sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-  return sum != sum ? kLowest64 : key64(sum);
-}
-
-// Exact key of block b, by one warp.
-__device__ uint64_t exact_block_key(const SelectParams& p, const SelShared& sh, int32_t seq,
-                                    int32_t b, int32_t seen) {
-  uint64_t best = 0;
-  const int64_t first = static_cast<int64_t>(b) * p.block;
-  for (int64_t pos = first; pos < first + p.block && pos < seen; ++pos) {
-    const uint64_t k = exact_key(p, sh, seq, static_cast<int32_t>(pos));
-    best = best > k ? best : k;
-  }
-  return best;
-}
-
-__device__ __forceinline__ int block_sum(int v, int32_t* warp_sum) {
+// ------------------------------------------------------------- block helpers
+template <int kThreads>
+__device__ __forceinline__ int block_sum(int v, int32_t* sums) {
   v = __reduce_add_sync(0xffffffffu, v);
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = v;
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = v;
   __syncthreads();
-  return __reduce_add_sync(0xffffffffu, warp_sum[threadIdx.x & 31]);
+  const int lane = threadIdx.x & 31;
+  return __reduce_add_sync(0xffffffffu, lane < kThreads / 32 ? sums[lane] : 0);
 }
 
-// Threads with v set before this one, over the block; `total` gets all of them.
-__device__ __forceinline__ int block_rank(bool v, int32_t* warp_sum, int& total) {
+// Sum of v over the threads before this one; `total` gets that over all.
+template <int kThreads>
+__device__ __forceinline__ int block_before(int v, int32_t* sums, int& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t m = __ballot_sync(0xffffffffu, v);
-  __syncthreads();
-  if (lane == 0) warp_sum[warp] = __popc(m);
-  __syncthreads();
-  int w = warp_sum[lane];
+  int upto = v;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += o;
+  }
+  __syncthreads();
+  if (lane == 31) sums[warp] = upto;
+  __syncthreads();
+  int w = lane < kThreads / 32 ? sums[lane] : 0;
+#pragma unroll
+  for (int d = 1; d < kThreads / 32; d <<= 1) {
     const int o = __shfl_up_sync(0xffffffffu, w, d);
     if (lane >= d) w += o;
   }
-  total = __shfl_sync(0xffffffffu, w, 31);
+  total = __shfl_sync(0xffffffffu, w, kThreads / 32 - 1);
   const int before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
-  return (warp > 0 ? before : 0) + __popc(m & ((1u << lane) - 1));
+  return (warp > 0 ? before : 0) + upto - v;
 }
 
-// With hist[256] filled: the digit of the `rank`-th largest value (rank >= 1)
-// and its rank among the values with that digit. One warp.
-__device__ __forceinline__ void find_digit(SelShared& sh, uint32_t rank) {
-  const int lane = threadIdx.x & 31;
-  uint32_t c[8], mine = 0;
+// With hist filled: the bin of the `rank`-th largest value (rank >= 1) into
+// sh.pick and its rank among that bin's values into sh.rest.
+template <int kThreads>
+__device__ __forceinline__ void find_bin(SelShared<kThreads>& sh, uint32_t rank) {
+  constexpr int kPer = kBins / kThreads;
+  const int top = kBins - 1 - static_cast<int>(threadIdx.x) * kPer;  // this thread's highest bin
+  uint32_t c[kPer];
+  int mine = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) mine += c[i] = sh.hist[255 - (lane * 8 + i)];
-  uint32_t upto = mine;
+  for (int i = 0; i < kPer; ++i) mine += c[i] = sh.hist[top - i];
+  int total;
+  uint32_t before = block_before<kThreads>(mine, sh.sum_a, total);
+  if (before < rank && rank <= before + mine) {
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const uint32_t o = __shfl_up_sync(0xffffffffu, upto, d);
-    if (lane >= d) upto += o;
-  }
-  uint32_t before = upto - mine;
-  if (before < rank && rank <= upto) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (before < rank && rank <= before + c[i]) {
-        sh.pick = 255 - (lane * 8 + i);
-        sh.rest = rank - before;
-      }
+    for (int i = 0; i < kPer; ++i) {
+      if (before < rank && rank <= before + c[i]) sh.pick = top - i, sh.rest = rank - before;
       before += c[i];
     }
   }
+  __syncthreads();
 }
 
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p) {
-  extern __shared__ uint8_t raw[];
-  SelShared& sh = *reinterpret_cast<SelShared*>(raw);
+// The `rank`-th largest of `count` keys: a histogram over their range, then
+// over the bin that holds it, until a bin is one value (three levels for fp32
+// keys, which differ in 22 to 32 bits). each(f) calls f with this thread's
+// share of the keys, and the whole block goes through it; `rank` becomes the
+// rank among the equal ones.
+template <int kThreads, typename Key, typename Each>
+__device__ __forceinline__ Key kth_largest(SelShared<kThreads>& sh, Key lowest, Key highest,
+                                           uint32_t& rank, Each&& each) {
+  Key base = lowest, width = highest - lowest;  // keys base .. base + width are in question
+  while (true) {
+    const int bits = width == 0 ? 0 : sizeof(Key) == 8
+                                          ? 64 - __clzll(static_cast<long long>(width))
+                                          : 32 - __clz(static_cast<int>(width));
+    const int shift = bits > 11 ? bits - 11 : 0;
+    for (int i = threadIdx.x; i < kBins; i += kThreads) sh.hist[i] = 0;
+    __syncthreads();
+    each([&](Key k) {
+      if (k >= base && k - base <= width) atomicAdd(&sh.hist[(k - base) >> shift], 1u);
+    });
+    __syncthreads();
+    find_bin<kThreads>(sh, rank);
+    base += static_cast<Key>(sh.pick) << shift;
+    rank = sh.rest;
+    __syncthreads();
+    if (shift == 0) return base;
+    width = (Key{1} << shift) - 1;
+  }
+}
+
+// Lowest and highest of the keys that each() goes through.
+template <int kThreads, typename Each>
+__device__ __forceinline__ void key_range(SelShared<kThreads>& sh, uint32_t& lowest,
+                                          uint32_t& highest, Each&& each) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t lo = 0xFFFFFFFFu, hi = 0;
+  each([&](uint32_t k) { lo = min(lo, k), hi = max(hi, k); });
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  __syncthreads();
+  if (lane == 0) sh.redu[warp] = lo, sh.redv[warp] = hi;
+  __syncthreads();
+  constexpr int kW = kThreads / 32;
+  lowest = __reduce_min_sync(0xffffffffu, sh.redu[lane % kW]);
+  highest = __reduce_max_sync(0xffffffffu, sh.redv[lane % kW]);
+}
+
+// ------------------------------------------------------------ exact scores
+// One position's dot products with all heads as exact integers in units of
+// 2^-20, lane = head, 32 heads at a time, and their weighted sum: in fp32 with
+// an error bound, or in fp64. One warp.
+struct TokenScore {
+  float value, error;
+  double exact;
+  bool none;  // -inf: a NaN, or a page that does not resolve
+};
+template <bool kExact, typename Shared>
+__device__ __forceinline__ TokenScore score_token(const SelectParams& p, const Shared& sh,
+                                                  int32_t seq, int32_t pos) {
+  const int lane = threadIdx.x & 31;
+  TokenScore r = {0.f, 0.f, 0.0, true};
+  const IndexRow at = resolve_index_row(seq, pos, p.block_table, p.num_seqs, p.max_blocks,
+                                        p.page_size, p.num_blocks, p.block_stride);
+  if (at.page < 0) return r;
+  const uint8_t* page = p.cache + at.page;
+  const uint32_t mine = expand_codes(__ldg(reinterpret_cast<const uint16_t*>(
+      page + static_cast<int64_t>(at.row) * kIndexCodes + lane * 2)));
+  const uint32_t byte = __ldg(page + static_cast<int64_t>(p.page_size) * kIndexCodes +
+                              static_cast<int64_t>(at.row) * kIndexScales + (lane & 7)) &
+                        0x7Fu;
+  if (__any_sync(0xffffffffu, byte == 0x7Fu)) return r;
+  r.none = false;
+  const uint32_t parts = scale_parts(byte);
+  for (int j0 = 0; j0 < p.num_heads; j0 += 32) {
+    const int j = min(j0 + lane, p.num_heads - 1);
+    const uint32_t* q = sh.q_codes + j * kHeadWords;
+    int64_t d = 0;
+#pragma unroll
+    for (int g = 0; g < kIndexScales; ++g) {
+      int dot = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        dot = __dp4a(static_cast<int>(q[4 * g + i]),
+                     static_cast<int>(__shfl_sync(0xffffffffu, mine, 4 * g + i)), dot);
+      const uint32_t ks = __shfl_sync(0xffffffffu, parts, g);
+      const uint32_t qs = sh.q_scale[j * kHeadScales + g];
+      dot *= static_cast<int>((ks & 255u) * (qs & 255u));
+      d += static_cast<int64_t>(dot) << ((ks >> 8) + (qs >> 8));
+    }
+    if (d < 0 || j0 + lane >= p.num_heads) d = 0;
+    if (kExact) {
+      // most weights of zero dot products need no fp64
+      if (__any_sync(0xffffffffu, d > 0))
+        r.exact += static_cast<double>(sh.w[j]) * (static_cast<double>(d) * 0x1p-20);
+    } else {
+      const float f = fmaf(static_cast<float>(static_cast<int32_t>(d >> 24)), 16777216.f,
+                           static_cast<float>(static_cast<int32_t>(d & 0xFFFFFF))) *
+                      0x1p-20f;
+      r.value = fmaf(sh.w[j], f, r.value);
+      r.error = fmaf(fabsf(sh.w[j]), f, r.error);
+      if (f > 0.f && sh.w[j] != 0.f) r.error += kTiny;  // never 0 by underflow
+    }
+  }
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+    if (kExact) {
+      r.exact += __shfl_xor_sync(0xffffffffu, r.exact, s);
+    } else {
+      r.value += __shfl_xor_sync(0xffffffffu, r.value, s);
+      r.error += __shfl_xor_sync(0xffffffffu, r.error, s);
+    }
+  }
+  if (kExact) {
+    r.none = r.exact != r.exact;
+  } else {
+    r.error = r.error == 0.f ? 0.f : __fadd_ru(__fmul_ru(r.error, kSumError), kTiny);
+    r.none = r.value != r.value;
+  }
+  return r;
+}
+template <typename Shared>
+__device__ __forceinline__ uint64_t exact_key(const SelectParams& p, const Shared& sh, int32_t seq,
+                                              int32_t pos) {
+  const TokenScore r = score_token<true>(p, sh, seq, pos);
+  return r.none ? kLowest64 : key64(r.exact);
+}
+
+// ------------------------------------------------------------- the choice
+// Who is in, in terms of a row's keys: above `hi`, and of those at lo .. hi
+// the first `ties` by index.
+struct Border {
+  uint32_t lo, hi;
+  int32_t ties;
+};
+
+// The border of the k highest of the `count` keys of a row. `row` gives keys
+// by position and their blocks, and takes marks (kIn, kTie, kOut).
+template <int kThreads, typename Row>
+__device__ __forceinline__ Border choose(const SelectParams& p, SelShared<kThreads>& sh,
+                                         const Row& row, int32_t count, int32_t k, int32_t seq,
+                                         int32_t seen, double m) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int32_t t = blockIdx.x;
+  constexpr int kWarps = kThreads / 32;
+  auto each = [&](auto&& f) {
+    for (int32_t i = tid; i < count; i += kThreads) f(row.key(i));
+  };
+  uint32_t lowest, highest, rank = k;
+  key_range(sh, lowest, highest, each);
+  const uint32_t tk = kth_largest<kThreads, uint32_t>(sh, lowest, highest, rank, each);
+  const float T = unkey32(tk);
+  const double eps =
+      m == 0.0 ? 0.0 : m * (kDotError + (p.num_heads / 8 + 8) / 16777216.0) + 1e-40;
+  const float eps2 = __double2float_ru(2.0 * eps);
+  // A score of -inf comes from a NaN or a page that does not resolve, not from
+  // rounding, unless fp32 overflowed.
+  const bool bounded = m < 1e37;
+  if (bounded && (eps2 == 0.f || T == -INFINITY)) return {tk, tk, static_cast<int32_t>(rank)};
+  const uint32_t lo = bounded ? key32(__fadd_rd(T, -eps2)) : 1u;
+  const uint32_t hi = bounded ? key32(__fadd_ru(T, eps2)) : kTie - 1;
+
+  if (tid == 0) sh.n = 0;
+  __syncthreads();
+  int in = 0;
+  for (int32_t i = tid; i < count; i += kThreads) {
+    const uint32_t key = row.key(i);
+    if (key > hi) {
+      ++in;
+    } else if (key >= lo) {
+      const uint32_t c = atomicAdd(&sh.n, 1u);
+      if (c < SelShared<kThreads>::kCands) sh.cand[c] = i;
+    }
+  }
+  in = block_sum<kThreads>(in, sh.sum_a);
+  const int32_t cands = static_cast<int32_t>(sh.n);
+  int32_t want = k - in;  // 1 <= want <= cands
+  if (cands == want) return {lo, hi, INT32_MAX};  // all of them
+
+  const int shift = __ffs(p.block) - 1;
+  if (cands <= SelShared<kThreads>::kCands) {
+    for (int i = tid; i < cands; i += kThreads)
+      sh.cand_key[i] = 0, sh.cand_lo[i] = sh.cand_hi[i] = 0;
+    __syncthreads();
+    for (int i = warp; i < cands << shift; i += kWarps) {
+      const int c = i >> shift;
+      const int64_t pos = static_cast<int64_t>(row.block(sh.cand[c])) * p.block + (i & (p.block - 1));
+      if (pos >= seen) continue;
+      const TokenScore r = score_token<false>(p, sh, seq, static_cast<int32_t>(pos));
+      if (lane == 0) {
+        atomicMax(&sh.cand_lo[c], key32(r.none ? -INFINITY : __fsub_rd(r.value, r.error)));
+        atomicMax(&sh.cand_hi[c], key32(r.none ? -INFINITY : __fadd_ru(r.value, r.error)));
+      }
+    }
+    __syncthreads();
+    // Known by their intervals: in where fewer than `want` others can be
+    // above, out where `want` others are. sh.cand_key: 0 open, 1 in, 2 out.
+    int sure = 0;
+    for (int i = tid; i < cands; i += kThreads) {
+      int can = 0, are = 0;
+      for (int j = 0; j < cands; ++j) {
+        can += j != i && sh.cand_hi[j] >= sh.cand_lo[i];
+        are += sh.cand_lo[j] > sh.cand_hi[i];
+      }
+      const int state = can < want ? 1 : are >= want ? 2 : 0;
+      sh.cand_key[i] = state;
+      if (state != 0) row.mark(sh.cand[i], state == 1 ? kIn : kOut);
+      sure += state == 1;
+    }
+    want -= block_sum<kThreads>(sure, sh.sum_a);
+    // The best of the others by their fp64 scores.
+    if (want > 0) {
+      for (int i = tid; i < cands; i += kThreads) sh.cand_lo[i] = sh.cand_key[i] == 0 ? 1u : 0u;
+      __syncthreads();
+      for (int i = tid; i < cands; i += kThreads) sh.cand_key[i] = 0;
+      __syncthreads();
+      for (int i = warp; i < cands << shift; i += kWarps) {
+        const int c = i >> shift;
+        if (sh.cand_lo[c] == 0) continue;
+        const int64_t pos = static_cast<int64_t>(row.block(sh.cand[c])) * p.block + (i & (p.block - 1));
+        if (pos >= seen) continue;
+        const uint64_t key = exact_key(p, sh, seq, static_cast<int32_t>(pos));
+        if (lane == 0)
+          atomicMax(reinterpret_cast<unsigned long long*>(&sh.cand_key[c]),
+                    static_cast<unsigned long long>(key));
+      }
+      __syncthreads();
+      for (int i = tid; i < cands; i += kThreads) {
+        if (sh.cand_lo[i] == 0) continue;
+        const uint64_t key = sh.cand_key[i];
+        const int32_t b = row.block(sh.cand[i]);
+        int better = 0;
+        for (int j = 0; j < cands; ++j)
+          better += sh.cand_lo[j] != 0 &&
+                    (sh.cand_key[j] > key || (sh.cand_key[j] == key && row.block(sh.cand[j]) < b));
+        row.mark(sh.cand[i], better < want ? kIn : kOut);
+      }
+    } else {
+      for (int i = tid; i < cands; i += kThreads)
+        if (sh.cand_key[i] == 0) row.mark(sh.cand[i], kOut);
+    }
+    __syncthreads();
+    return {lo, hi, 0};
+  }
+
+  // Too many to list (a border among equal scores): the want-th largest fp64
+  // score, computed anew in each step, then a mark for each candidate.
+  auto exact = [&](int32_t i) {  // one warp
+    uint64_t best = 0;
+    const int64_t first = static_cast<int64_t>(row.block(i)) * p.block;
+    for (int64_t pos = first; pos < first + p.block && pos < seen; ++pos) {
+      const uint64_t e = exact_key(p, sh, seq, static_cast<int32_t>(pos));
+      best = best > e ? best : e;
+    }
+    return best;
+  };
+  auto each_exact = [&](auto&& f) {
+    for (int32_t i = warp; i < count; i += kWarps) {
+      const uint32_t key = row.key(i);
+      if (key < lo || key > hi) continue;
+      const uint64_t e = exact(i);
+      if (lane == 0) f(e);
+    }
+  };
+  rank = want;
+  const uint64_t edge = kth_largest<kThreads, uint64_t>(sh, uint64_t{0}, ~uint64_t{0}, rank,
+                                                        each_exact);
+  for (int32_t i = warp; i < count; i += kWarps) {
+    const uint32_t key = row.key(i);
+    if (key < lo || key > hi) continue;
+    const uint64_t e = exact(i);
+    __syncwarp();
+    if (lane == 0) row.mark(i, e > edge ? kIn : e == edge ? kTie : kOut);
+    __syncwarp();
+  }
+  __syncthreads();
+  return {lo, hi, static_cast<int32_t>(rank)};
+}
+
+// ------------------------------------------------------------------- rows
+// A row's scores in memory: a block's is the highest of its `per` stored ones.
+struct MemoryRow {
+  float* scores;
+  int32_t b0, per, granules;
+  __device__ __forceinline__ int32_t block(int32_t i) const { return b0 + i; }
+  __device__ __forceinline__ uint32_t key(int32_t i) const {
+    const int64_t at = static_cast<int64_t>(b0 + i) * per;
+    float a = __ldcg(scores + at);
+    const uint32_t u = __float_as_uint(a);
+    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return u & 0x80000000u ? ~u : u | 0x80000000u;  // a mark
+    for (int g = 1; g < per; ++g)
+      if (at + g < granules) a = fmaxf(a, __ldcg(scores + at + g));
+    return key32(a);
+  }
+  __device__ __forceinline__ void mark(int32_t i, uint32_t m) const {
+    scores[static_cast<int64_t>(b0 + i) * per] =
+        __uint_as_float(m == kOut ? 0xFFFFFFFFu : m & 0x7FFFFFFFu);
+  }
+};
+struct DenseRow {  // shared memory, all blocks from b0 on
+  uint32_t* keys;
+  int32_t b0;
+  __device__ __forceinline__ int32_t block(int32_t i) const { return b0 + i; }
+  __device__ __forceinline__ uint32_t key(int32_t i) const { return keys[i]; }
+  __device__ __forceinline__ void mark(int32_t i, uint32_t m) const { keys[i] = m; }
+};
+struct ListRow {  // shared memory, some blocks in any order
+  uint32_t* keys;
+  int32_t* blocks;
+  __device__ __forceinline__ int32_t block(int32_t i) const { return blocks[i]; }
+  __device__ __forceinline__ uint32_t key(int32_t i) const { return keys[i]; }
+  __device__ __forceinline__ void mark(int32_t i, uint32_t m) const { keys[i] = m; }
+};
+
+// Output rows of a query token: every block's first position is written in
+// order, the others follow from it.
+template <int kThreads>
+__device__ __forceinline__ void expand_blocks(const SelectParams& p, int32_t* out, int64_t width,
+                                              int32_t seen) {
+  if (p.block == 1) return;
+  __syncthreads();
+  for (int64_t i = threadIdx.x; i < width; i += kThreads) {
+    const int off = static_cast<int>(i % p.block);
+    if (off == 0) continue;
+    const int32_t pos = __ldcg(out + (i - off)) + off;
+    out[i] = pos < seen ? pos : -1;
+  }
+}
+
+// Blocks in order, `row` holding those from p.sink on.
+template <int kThreads, typename Row>
+__device__ __forceinline__ void emit_row(const SelectParams& p, SelShared<kThreads>& sh,
+                                         const Row& row, const Border& border, int32_t blocks,
+                                         int32_t* out) {
+  int32_t done = 0, ties = 0;
+  for (int32_t c0 = 0; c0 < blocks; c0 += kThreads) {
+    const int32_t b = c0 + static_cast<int32_t>(threadIdx.x);
+    bool in = b < blocks && (b < p.sink || b >= blocks - p.recent), tie = false;
+    if (b < blocks && !in) {
+      const uint32_t key = row.key(b - p.sink);
+      tie = key == kTie || (key >= border.lo && key <= border.hi);
+      in = key > border.hi && !tie;
+    }
+    int total;
+    if (border.ties > 0) {
+      const int before = block_before<kThreads>(tie, sh.sum_a, total);
+      in = in || (tie && before < border.ties - ties);
+      ties += total;
+    }
+    const int before = block_before<kThreads>(in, sh.sum_b, total);
+    if (in) out[static_cast<int64_t>(done + before) * p.block] = b * p.block;
+    done += total;
+  }
+}
+
+__device__ __forceinline__ uint32_t sel_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t sel_ctas() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void sel_cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n"
+               "barrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+__device__ __forceinline__ uint32_t in_rank(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+
+// The long row: this CTA's share of the keys that are at least `floor`, into
+// the list; returns how many there are (some may not have fitted).
+template <int kThreads>
+__device__ __forceinline__ int32_t collect(SelShared<kThreads>& sh, const MemoryRow& row,
+                                           int32_t from, int32_t to, uint32_t floor,
+                                           uint32_t* keys, int32_t* blocks) {
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) sh.n = 0;
+  __syncthreads();
+  constexpr int kFlight = 8;  // loads in flight per thread
+  for (int32_t i0 = from; i0 < to; i0 += kThreads * kFlight) {
+    uint32_t key[kFlight];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      const int64_t i = static_cast<int64_t>(i0) + u * kThreads + threadIdx.x;
+      key[u] = i < to ? row.key(static_cast<int32_t>(i)) : 0u;
+    }
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      const bool hit = key[u] >= floor;
+      const uint32_t hits = __ballot_sync(0xffffffffu, hit);
+      if (hits == 0) continue;
+      uint32_t at = 0;
+      if (lane == 0) at = atomicAdd(&sh.n, static_cast<uint32_t>(__popc(hits)));
+      at = __shfl_sync(0xffffffffu, at, 0) + __popc(hits & ((1u << lane) - 1));
+      if (hit && at < kListMax) {
+        keys[at] = key[u];
+        blocks[at] = row.block(i0 + u * kThreads + static_cast<int32_t>(threadIdx.x));
+      }
+    }
+  }
+  __syncthreads();
+  return static_cast<int32_t>(sh.n);
+}
+
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads)
+    select_kernel(const SelectParams p, const SelectConfig cfg) {
+  using Shared = SelShared<kThreads>;
+  constexpr int kWarps = kThreads / 32;
+  extern __shared__ __align__(16) uint8_t raw[];
+  Shared& sh = *reinterpret_cast<Shared*>(raw);
+  uint32_t* keys = reinterpret_cast<uint32_t*>(raw + sizeof(Shared));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t ctas = sel_ctas(), rank = sel_rank();
+  const int32_t t = blockIdx.x / ctas;
   const int64_t width = static_cast<int64_t>(p.num_select) * p.block;
   int32_t* out = p.topk_idx + t * width;
   const int32_t seq = __ldg(p.q_seq + t);
   const int32_t seen = visible_positions(p, seq, __ldg(p.q_pos + t));
   const int32_t blocks = blocks_of_positions(seen, p.block);
+  const bool all = blocks <= p.num_select;
 
-  if (tid == 0) sh.failed = 0;
-  __syncthreads();
-  for (int i = tid; i < p.score_ctas; i += kSelThreads)
-    if (__ldcg(p.status + i) != 0) sh.failed = 1;
-  __syncthreads();
-  if (sh.failed) {
-    for (int64_t i = tid; i < width; i += kSelThreads) out[i] = -2;
-    return;
-  }
-  if (blocks <= p.num_select) {  // all of them
-    for (int64_t i = tid; i < width; i += kSelThreads)
-      out[i] = i < seen ? static_cast<int32_t>(i) : -1;
-    return;
-  }
-
-  const int granule = min(p.block, kMaxGranule);
-  const int per = p.block / granule;
-  const int32_t granules = (seen + granule - 1) / granule;
-  float* row = p.scores + t * p.score_stride;
-  // The forced blocks are at both ends: k of the n between them are chosen.
-  const int32_t b0 = p.sink, n = blocks - p.sink - p.recent;
-  const int32_t k = p.num_select - p.sink - p.recent;
-
-  float lo = INFINITY, hi = INFINITY;  // in: > hi; in question: lo .. hi
-  int32_t ties = 0;                    // chosen ones of those at lo == hi, by index
-  if (k > 0) {
-    // k-th largest score
-    uint32_t prefix = 0, rank = k;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) sh.hist[tid] = 0;
-      __syncthreads();
-      for (int32_t i = tid; i < n; i += kSelThreads) {
-        const uint32_t key = key32(block_score(p, row, b0 + i, per, granules));
-        if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8)))
-          atomicAdd(&sh.hist[(key >> shift) & 255u], 1u);
-      }
-      __syncthreads();
-      if (warp == 0) find_digit(sh, rank);
-      __syncthreads();
-      prefix |= sh.pick << shift;
-      rank = sh.rest;
-      __syncthreads();
-    }
-    const float T = unkey32(prefix);
-
-    // the heads as integers, and the error bound
-    double m = 0.0;
-    for (int g = tid; g < p.num_heads * kIndexScales; g += kSelThreads) {
+  // The heads as integers, and their part of the error bound: nothing that
+  // the score kernel writes.
+  double m = 0.0;
+  if (!all) {
+    for (int g = tid; g < p.num_heads * kIndexScales; g += kThreads) {
       const uint8_t* src =
           p.q_index + (static_cast<int64_t>(t) * p.num_heads * kIndexScales + g) * (2 * kGroup);
       const uint4 a = ld_nc_v4(src), b = ld_nc_v4(src + 16);
       const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      uint32_t c0, c1;
+      const int j = g / kIndexScales, part = g % kIndexScales;
+      uint32_t c[2];
       float s;
-      quantize_group(v, c0, c1, s);
-      uint32_t e[4];
-      expand_codes(c0, e[0], e[1]);
-      expand_codes(c1, e[2], e[3]);
+      sh.q_scale[j * kHeadScales + part] = scale_parts(quantize_group(v, c[0], c[1], s));
       int mag = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        sh.q_codes[g * 4 + i] = e[i];
-        mag = __dp4a(static_cast<int>(__vabs4(e[i])), 0x01010101, mag);
+        const uint32_t e = expand_codes(c[i >> 1] >> (16 * (i & 1)));
+        sh.q_codes[j * kHeadWords + part * 4 + i] = e;
+        mag = __dp4a(static_cast<int>(__vabs4(e)), 0x01010101, mag);
       }
-      sh.q_scale[g] = s;
-      const float w = __ldg(p.weights + static_cast<int64_t>(t) * p.num_heads + g / kIndexScales);
-      if (g % kIndexScales == 0) sh.w[g / kIndexScales] = w;
-      m += static_cast<double>(fabsf(w)) * (0.5 * mag) * static_cast<double>(s);
+      const float w = __ldg(p.weights + static_cast<int64_t>(t) * p.num_heads + j);
+      if (part == 0) sh.w[j] = w;
+      m += static_cast<double>(fabsf(w) * (0.5f * mag * s));
     }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m += __shfl_xor_sync(0xffffffffu, m, d);
+    if (lane == 0) sh.red[warp] = m;
+  }
+  if (tid == 0) sh.failed = 0;
+  __syncthreads();
+  cudaGridDependencySynchronize();  // the scores are there
+  for (int i = tid; i < p.score_ctas; i += kThreads)
+    if (__ldcg(p.status + i) != 0) sh.failed = 1;
+  __syncthreads();
+  if (sh.failed || all) {
+    if (rank == 0)
+      for (int64_t i = tid; i < width; i += kThreads)
+        out[i] = sh.failed ? -2 : i < seen ? static_cast<int32_t>(i) : -1;
+    return;
+  }
+
+  // The forced blocks are at both ends: k of the n between them are chosen.
+  const int granule = min(p.block, kMaxGranule);
+  const MemoryRow row = {p.scores + t * p.score_stride, p.sink, p.block / granule,
+                         (seen + granule - 1) / granule};
+  const int32_t n = blocks - p.sink - p.recent;
+  const int32_t k = p.num_select - p.sink - p.recent;
+  if (k == 0) {
+    if (rank == 0) {
+      emit_row<kThreads>(p, sh, row, Border{kTie, kTie, 0}, blocks, out);
+      expand_blocks<kThreads>(p, out, width, seen);
+    }
+    return;
+  }
+  {
     int32_t lead = t;  // first token of t's run
     while (lead % p.group != 0 && __ldg(p.q_seq + lead - 1) == seq) --lead;
     uint32_t top = 0;
     const int32_t tiles = (seen + kScoreTile - 1) / kScoreTile;
-    for (int32_t i = tid; i < tiles; i += kSelThreads)
+    for (int32_t i = tid; i < tiles; i += kThreads)
       top = __vmaxu4(top, __ldcg(p.smax + lead * p.tiles + i));
     top = __vmaxu4(top, top >> 16);
-    top = __vmaxu4(top, top >> 8) & 0xFFu;
-    float smax = scale_value(top);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      m += __shfl_xor_sync(0xffffffffu, m, d);
-      smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, d));
-    }
-    if (lane == 0) sh.red[warp] = m, sh.redf[warp] = smax;
+    top = __reduce_max_sync(0xffffffffu, __vmaxu4(top, top >> 8) & 0xFFu);
+    if (lane == 0) sh.redu[warp] = top;
     __syncthreads();
-    m = sh.red[lane];
-    smax = sh.redf[lane];
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      m += __shfl_xor_sync(0xffffffffu, m, d);
-      smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, d));
+    m = 0.0;
+    for (int w = 0; w < kWarps; ++w) {
+      m += sh.red[w];
+      top = max(top, sh.redu[w]);
     }
-    m *= 6.0 * static_cast<double>(smax);
-    // rounded up to fp32; the last term covers products below the smallest
-    // normal fp32
-    const double eps = m == 0.0 ? 0.0 : m * (kDotError + (p.num_heads / 8 + 8) / 16777216.0) + 1e-40;
-    const float eps2 = __double2float_ru(2.0 * eps);
-    // A score of -inf comes from a NaN or a page that does not resolve, not
-    // from rounding, unless fp32 overflowed.
-    const bool bounded = m < 1e37;
-    if (bounded && (eps2 == 0.f || T == -INFINITY)) {
-      lo = hi = T;
-      ties = static_cast<int32_t>(rank);
-    } else {
-      lo = bounded ? __fadd_rd(T, -eps2) : -INFINITY;
-      hi = bounded ? __fadd_ru(T, eps2) : INFINITY;
-      // candidates
-      if (tid == 0) sh.cand_n = 0;
-      __syncthreads();
-      int in = 0;
-      for (int32_t i = tid; i < n; i += kSelThreads) {
-        const float a = block_score(p, row, b0 + i, per, granules);
-        if (a > hi) {
-          ++in;
-        } else if (a >= lo) {
-          const uint32_t c = atomicAdd(&sh.cand_n, 1u);
-          if (c < kListCap) sh.cand[c] = b0 + i;
-        }
-      }
-      in = block_sum(in, sh.warp_sum);
-      const int32_t cands = static_cast<int32_t>(sh.cand_n);
-      const int32_t want = k - in;  // 1 <= want <= cands
-      if (cands == want) {
-        ties = want;  // all of them
-      } else if (cands <= kListCap) {
-        for (int i = tid; i < cands; i += kSelThreads) sh.cand_key[i] = 0;
-        __syncthreads();
-        for (int64_t i = warp; i < static_cast<int64_t>(cands) * p.block; i += kSelWarps) {
-          const int c = static_cast<int>(i / p.block);
-          const int64_t pos = static_cast<int64_t>(sh.cand[c]) * p.block + i % p.block;
-          if (pos >= seen) continue;
-          const uint64_t key = exact_key(p, sh, seq, static_cast<int32_t>(pos));
-          if (lane == 0)
-            atomicMax(reinterpret_cast<unsigned long long*>(&sh.cand_key[c]),
-                      static_cast<unsigned long long>(key));
-        }
-        __syncthreads();
-        for (int i = tid; i < cands; i += kSelThreads) {
-          const uint64_t key = sh.cand_key[i];
-          const int32_t b = sh.cand[i];
-          int better = 0;
-          for (int j = 0; j < cands; ++j)
-            better += sh.cand_key[j] > key || (sh.cand_key[j] == key && sh.cand[j] < b);
-          float* at = row + static_cast<int64_t>(b) * per;
-          for (int g = 0; g < per && static_cast<int64_t>(b) * per + g < granules; ++g)
-            at[g] = better < want ? INFINITY : -INFINITY;
-        }
-        hi = fminf(hi, 3.402823466e38f);  // below +inf, the chosen ones' mark
-        __syncthreads();
-      } else {
-        // Too many to list: radix selection on the exact keys, computed anew
-        // for each digit; then candidates above the border become +inf, those
-        // on it NaN-free ties at the largest finite value, the others -inf.
-        uint64_t edge = 0;
-        uint32_t left = want;
-        for (int shift = 56; shift >= 0; shift -= 8) {
-          if (tid < 256) sh.hist[tid] = 0;
-          __syncthreads();
-          for (int32_t i = warp; i < n; i += kSelWarps) {
-            const float a = block_score(p, row, b0 + i, per, granules);
-            if (!(a >= lo && a <= hi)) continue;
-            const uint64_t key = exact_block_key(p, sh, seq, b0 + i, seen);
-            if (lane == 0 && (shift == 56 || (key >> (shift + 8)) == (edge >> (shift + 8))))
-              atomicAdd(&sh.hist[(key >> shift) & 255u], 1u);
-          }
-          __syncthreads();
-          if (warp == 0) find_digit(sh, left);
-          __syncthreads();
-          edge |= static_cast<uint64_t>(sh.pick) << shift;
-          left = sh.rest;
-          __syncthreads();
-        }
-        for (int32_t i = warp; i < n; i += kSelWarps) {
-          const float a = block_score(p, row, b0 + i, per, granules);
-          if (a > hi) {
-            // in: above any tie
-          } else if (!(a >= lo)) {
-            continue;
-          }
-          const uint64_t key = a > hi ? ~0ull : exact_block_key(p, sh, seq, b0 + i, seen);
-          __syncwarp();
-          if (lane == 0) {
-            float* at = row + static_cast<int64_t>(b0 + i) * per;
-            for (int g = 0; g < per && static_cast<int64_t>(b0 + i) * per + g < granules; ++g)
-              at[g] = key > edge ? INFINITY : key == edge ? 3.402823466e38f : -INFINITY;
-          }
-          __syncwarp();
-        }
-        lo = hi = 3.402823466e38f;
-        ties = static_cast<int32_t>(left);
-        __syncthreads();
-      }
-    }
+    // (1 + 2^-20): its fp32 products were rounded
+    m *= 6.000006 * static_cast<double>(scale_value(top));
+    __syncthreads();
   }
 
-  // Blocks in order: chosen ones get the next row of the output. A block is in
-  // above hi, and among the first `ties` at lo .. hi.
-  int32_t done = 0, ties_seen = 0;
-  for (int32_t c0 = 0; c0 < blocks; c0 += kSelThreads) {
-    const int32_t b = c0 + tid;
-    const bool forced = b < blocks && (b < p.sink || b >= blocks - p.recent);
-    bool in = forced, tie = false;
-    if (b < blocks && !forced && k > 0) {
-      const float a = block_score(p, row, b, per, granules);
-      in = a > hi;
-      tie = !in && a >= lo;
-    }
-    int total;
-    if (ties > 0) {
-      const int r = block_rank(tie, sh.warp_sum, total);
-      in = in || (tie && ties_seen + r < ties);
-      ties_seen += total;
-    }
-    const int r = block_rank(in, sh.warp_sum2, total);
-    if (in) out[static_cast<int64_t>(done + r) * p.block] = b * p.block;
-    done += total;
+  if (n <= cfg.room) {
+    const DenseRow dense = {keys, p.sink};
+    for (int32_t i = tid; i < n; i += kThreads) keys[i] = row.key(i);
+    __syncthreads();
+    const Border border = choose<kThreads>(p, sh, dense, n, k, seq, seen, m);
+    emit_row<kThreads>(p, sh, dense, border, blocks, out);
+    expand_blocks<kThreads>(p, out, width, seen);
+    return;
   }
-  __syncthreads();
-  // Each block's first position is in place: the others follow from it.
-  if (p.block > 1) {
-    for (int64_t i = tid; i < width; i += kSelThreads) {
-      const int off = static_cast<int>(i % p.block);
-      if (off == 0) continue;
-      const int32_t pos = __ldcg(out + (i - off)) + off;
-      out[i] = pos < seen ? pos : -1;
+
+  if constexpr (kThreads == 1024) {
+    // A threshold that about k + 4 sqrt(k) scores pass, by a sample's share.
+    int32_t* list_blocks = reinterpret_cast<int32_t*>(keys + kListMax);
+    const float share = static_cast<float>(k) * kSample / static_cast<float>(n);
+    uint32_t from_top = static_cast<uint32_t>(share + 4.f * sqrtf(share) + 8.f);
+    const float expect = static_cast<float>(from_top) * n / kSample;
+    bool listed = cfg.room >= kDenseMax && expect < 0.9f * kListMax && blocks <= 64 * kListMax;
+    if (listed) {
+      for (int32_t i = tid; i < kSample; i += kThreads)
+        keys[i] = row.key(static_cast<int32_t>(static_cast<int64_t>(i) * n / kSample));
+      __syncthreads();
+      auto each = [&](auto&& f) {
+        for (int32_t i = tid; i < kSample; i += kThreads) f(keys[i]);
+      };
+      uint32_t lowest, highest;
+      key_range(sh, lowest, highest, each);
+      const uint32_t floor = kth_largest<kThreads, uint32_t>(sh, lowest, highest, from_top, each);
+      const int32_t per = (n + static_cast<int32_t>(ctas) - 1) / static_cast<int32_t>(ctas);
+      const int32_t from = min(static_cast<int32_t>(rank) * per, n);
+      const int32_t mine =
+          collect<kThreads>(sh, row, from, min(from + per, n), floor, keys, list_blocks);
+      int32_t count = mine;
+      if (ctas > 1) {  // the lists go behind one another into rank 0's
+        if (tid == 0) sh.sum_a[0] = mine;
+        sel_cluster_sync();
+        int32_t before = 0;
+        count = 0;
+        for (uint32_t r = 0; r < ctas; ++r) {
+          int32_t c;
+          asm volatile("ld.shared::cluster.s32 %0, [%1];"
+                       : "=r"(c)
+                       : "r"(in_rank(smem_u32(&sh.sum_a[0]), r))
+                       : "memory");
+          if (r < rank) before += c;
+          count += c;
+        }
+        if (rank > 0 && count <= kListMax) {
+          const uint32_t to_keys = in_rank(smem_u32(keys), 0);
+          const uint32_t to_blocks = in_rank(smem_u32(list_blocks), 0);
+          for (int32_t i = tid; i < mine; i += kThreads) {
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to_keys + 4u * (before + i)),
+                         "r"(keys[i])
+                         : "memory");
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to_blocks + 4u * (before + i)),
+                         "r"(list_blocks[i])
+                         : "memory");
+          }
+        }
+        sel_cluster_sync();
+      }
+      if (rank > 0) return;
+      listed = count <= kListMax && count >= k;
+      if (listed) {
+        const ListRow list = {keys, list_blocks};
+        const Border border = choose<kThreads>(p, sh, list, count, k, seq, seen, m);
+        // What lies at the border has to have passed the threshold; the first
+        // ones of a tie cannot be told in a list.
+        listed = border.lo >= floor && (border.ties == 0 || border.ties == INT32_MAX);
+        if (listed) {
+          // the chosen ones as bits, in the list's place
+          constexpr int kPer = kListMax / kThreads;
+          int32_t mine_in[kPer];
+#pragma unroll
+          for (int u = 0; u < kPer; ++u) {
+            const int32_t i = u * kThreads + tid;
+            mine_in[u] = -1;
+            if (i < count) {
+              const uint32_t key = keys[i];
+              if (key > border.hi || (border.ties > 0 && key >= border.lo))
+                mine_in[u] = list_blocks[i];
+            }
+          }
+          __syncthreads();
+          const int32_t words = (blocks + 31) / 32;
+          for (int32_t i = tid; i < words; i += kThreads) keys[i] = 0;
+          __syncthreads();
+#pragma unroll
+          for (int u = 0; u < kPer; ++u)
+            if (mine_in[u] >= 0) atomicOr(&keys[mine_in[u] >> 5], 1u << (mine_in[u] & 31));
+          for (int32_t i = tid; i < p.sink + p.recent; i += kThreads) {
+            const int32_t b = i < p.sink ? i : blocks - 1 - (i - p.sink);
+            atomicOr(&keys[b >> 5], 1u << (b & 31));
+          }
+          __syncthreads();
+          // a warp's share of the words, 32 at a time
+          const int32_t share_words = ((words + kWarps - 1) / kWarps + 31) / 32 * 32;
+          const int32_t w0 = min(warp * share_words, words), w1 = min(w0 + share_words, words);
+          int bits = 0;
+          for (int32_t i = w0 + lane; i < w1; i += 32) bits += __popc(keys[i]);
+          bits = __reduce_add_sync(0xffffffffu, bits);
+          int total;
+          int at = block_before<kThreads>(lane == 0 ? bits : 0, sh.sum_a, total);
+          at = __shfl_sync(0xffffffffu, at, 0);
+          for (int32_t i0 = w0; i0 < w1; i0 += 32) {
+            uint32_t word = i0 + lane < w1 ? keys[i0 + lane] : 0u;
+            int upto = __popc(word);
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+              const int o = __shfl_up_sync(0xffffffffu, upto, d);
+              if (lane >= d) upto += o;
+            }
+            int64_t slot = at + upto - __popc(word);
+            at += __shfl_sync(0xffffffffu, upto, 31);
+            for (; word != 0; word &= word - 1)
+              out[slot++ * p.block] = ((i0 + lane) * 32 + __ffs(word) - 1) * p.block;
+          }
+          expand_blocks<kThreads>(p, out, width, seen);
+          return;
+        }
+      }
+      __syncthreads();
     }
+    if (rank > 0) return;
+    const Border border = choose<kThreads>(p, sh, row, n, k, seq, seen, m);
+    emit_row<kThreads>(p, sh, row, border, blocks, out);
+    expand_blocks<kThreads>(p, out, width, seen);
   }
+}
+
+template <int kThreads>
+int32_t launch_select(const SelectParams& p, int32_t most_blocks, int num_sms,
+                      cudaStream_t stream) {
+  SelectConfig cfg;
+  cfg.room = most_blocks < kDenseMax ? most_blocks : kDenseMax;
+  int ctas = 1;  // a cluster per query token where the rows are long and the device is not full
+  if (most_blocks > kDenseMax)
+    while (ctas < kMaxCluster && p.num_q * ctas * 2 <= num_sms) ctas *= 2;
+  const size_t smem = sizeof(SelShared<kThreads>) + 4 * static_cast<size_t>(cfg.room);
+  if (cudaFuncSetAttribute(select_kernel<kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess) {
+    cudaGetLastError();
+    return NVFP4_MLA_ERR_LAUNCH;
+  }
+  cudaLaunchConfig_t launch = {};
+  launch.gridDim = dim3(static_cast<unsigned>(p.num_q) * ctas);
+  launch.blockDim = dim3(kThreads);
+  launch.dynamicSmemBytes = smem;
+  launch.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  // starts as the score kernel's CTAs end; it waits for the scores itself
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  launch.attrs = attr;
+  launch.numAttrs = 2;
+  if (cudaLaunchKernelEx(&launch, select_kernel<kThreads>, p, cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return NVFP4_MLA_ERR_LAUNCH;
+  }
+  return NVFP4_MLA_OK;
 }
 
 struct Workspace {
@@ -497,11 +901,6 @@ extern "C" int32_t sparse_mla_select(const void* q_index, const float* weights,
   if (!aligned16(workspace)) return NVFP4_MLA_ERR_ALIGN;
   int dev = 0, sms = 0;
   if (int32_t st = current_device_checked(&dev, &sms)) return st;
-  if (cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(sizeof(SelShared))) != cudaSuccess) {
-    cudaGetLastError();
-    return NVFP4_MLA_ERR_LAUNCH;
-  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   for (int32_t q0 = 0; q0 < num_q; q0 += w.chunk) {
     SelectParams p = {};
@@ -531,8 +930,13 @@ extern "C" int32_t sparse_mla_select(const void* q_index, const float* weights,
     p.status = reinterpret_cast<uint32_t*>(p.smax + w.tiles * w.chunk);
     p.wait_cycles = decode_wait_cycles();
     if (int32_t st = launch_scores(p, sms, s)) return st;
-    select_kernel<<<p.num_q, kSelThreads, sizeof(SelShared), s>>>(p);
-    if (int32_t st = launch_status()) return st;
+    const int32_t most_blocks = static_cast<int32_t>(
+        (static_cast<int64_t>(max_blocks_per_seq) * page_size + select_block - 1) / select_block);
+    // Many query tokens with short rows: several small CTAs share an SM.
+    const bool small = most_blocks <= 4096 && p.num_q > 2 * sms;
+    if (int32_t st = small ? launch_select<256>(p, most_blocks, sms, s)
+                           : launch_select<1024>(p, most_blocks, sms, s))
+      return st;
   }
   return NVFP4_MLA_OK;
 }
