@@ -14,7 +14,7 @@
 // The bound: a dot product's terms sum up, in magnitude, to at most
 // 6 smax * |q^_j|_1 with smax the largest scale of the visible keys, so with
 // M = 6 smax * sum_j |w_j| |q^_j|_1 the fp32 score is off by at most
-// (kDotError + (heads / 8 + 8) 2^-24) M: heads are summed up in eight parts.
+// (kDotError + (heads / 8 + 4) 2^-24) M: heads are summed up in eight parts.
 //
 // One CTA per query token holds the scores of all blocks in shared memory
 // where they fit (32768). Longer rows: a sample of 4096 scores gives a
@@ -35,13 +35,14 @@ namespace {
 
 constexpr int kBins = 2048;
 constexpr int kSample = 4096;
-constexpr int kListMax = 16384;          // collected scores of a long row
-constexpr int kDenseMax = 2 * kListMax;  // scores held without their indexes
+// Keys that a CTA holds: all of a row's, or the keys and blocks of half as
+// many collected ones, or a bit for each of 32 times as many blocks.
+constexpr int kRoom = 16384, kWideRoom = 32768;
 constexpr int kMaxCluster = 8;
 // Error of a dot product on the tensor cores, relative to the sum of its
 // terms' magnitudes: 2.9 x 2^-24 is the most measured over 5e5 dot products,
 // with scales up to 2^15 apart.
-constexpr double kDotError = 16.0 / 16777216.0;
+constexpr float kDotError = 8.0f / 16777216.0f;
 // Error of an fp32 sum over the heads of exact dot products, relative to
 // sum_j |w_j| D_j: two roundings of each D, at most four terms and
 // five shuffles in a chain, and those of the bound itself.
@@ -100,7 +101,7 @@ struct SelShared {
   uint64_t cand_key[kCands];              // fp64 score, as a key
   uint32_t cand_lo[kCands], cand_hi[kCands];  // interval around the exact score, as keys
   int32_t cand[kCands];                   // position in the row of keys
-  double red[kWarps];
+  float red[kWarps];
   uint32_t redu[kWarps], redv[kWarps];
   int32_t sum_a[kWarps], sum_b[kWarps];
   uint32_t pick, rest, n, failed;
@@ -171,12 +172,12 @@ __device__ __forceinline__ void find_bin(SelShared<kThreads>& sh, uint32_t rank)
 // over the bin that holds it, until a bin is one value (three levels for fp32
 // keys, which differ in 22 to 32 bits). each(f) calls f with this thread's
 // share of the keys, and the whole block goes through it; `rank` becomes the
-// rank among the equal ones.
-template <int kThreads, typename Key, typename Each>
+// rank among the equal ones. With fewer levels the lower edge of the last bin.
+template <int kThreads, typename Key, int kLevels = 8, typename Each>
 __device__ __forceinline__ Key kth_largest(SelShared<kThreads>& sh, Key lowest, Key highest,
                                            uint32_t& rank, Each&& each) {
   Key base = lowest, width = highest - lowest;  // keys base .. base + width are in question
-  while (true) {
+  for (int level = 1;; ++level) {
     const int bits = width == 0 ? 0 : sizeof(Key) == 8
                                           ? 64 - __clzll(static_cast<long long>(width))
                                           : 32 - __clz(static_cast<int>(width));
@@ -191,7 +192,7 @@ __device__ __forceinline__ Key kth_largest(SelShared<kThreads>& sh, Key lowest, 
     base += static_cast<Key>(sh.pick) << shift;
     rank = sh.rest;
     __syncthreads();
-    if (shift == 0) return base;
+    if (shift == 0 || level == kLevels) return base;
     width = (Key{1} << shift) - 1;
   }
 }
@@ -306,7 +307,7 @@ struct Border {
 template <int kThreads, typename Row>
 __device__ __forceinline__ Border choose(const SelectParams& p, SelShared<kThreads>& sh,
                                          const Row& row, int32_t count, int32_t k, int32_t seq,
-                                         int32_t seen, double m) {
+                                         int32_t seen, float m) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kWarps = kThreads / 32;
   auto each = [&](auto&& f) {
@@ -316,12 +317,13 @@ __device__ __forceinline__ Border choose(const SelectParams& p, SelShared<kThrea
   key_range(sh, lowest, highest, each);
   const uint32_t tk = kth_largest<kThreads, uint32_t>(sh, lowest, highest, rank, each);
   const float T = unkey32(tk);
-  const double eps =
-      m == 0.0 ? 0.0 : m * (kDotError + (p.num_heads / 8 + 8) / 16777216.0) + 1e-40;
-  const float eps2 = __double2float_ru(2.0 * eps);
+  const float eps2 =
+      m == 0.f ? 0.f
+               : __fadd_ru(__fmul_ru(m, 2.0f * (kDotError + (p.num_heads / 8 + 4) / 16777216.0f)),
+                           kTiny);
   // A score of -inf comes from a NaN or a page that does not resolve, not from
   // rounding, unless fp32 overflowed.
-  const bool bounded = m < 1e37;
+  const bool bounded = m < 1e37f;
   if (bounded && (eps2 == 0.f || T == -INFINITY)) return {tk, tk, static_cast<int32_t>(rank)};
   const uint32_t lo = bounded ? key32(__fadd_rd(T, -eps2)) : 1u;
   const uint32_t hi = bounded ? key32(__fadd_ru(T, eps2)) : kTie - 1;
@@ -486,7 +488,7 @@ __device__ __forceinline__ void expand_blocks(const SelectParams& p, int32_t* ou
   if (p.block == 1) return;
   __syncthreads();
   for (int64_t i = threadIdx.x; i < width; i += kThreads) {
-    const int off = static_cast<int>(i % p.block);
+    const int off = static_cast<int>(i) & (p.block - 1);
     if (off == 0) continue;
     const int32_t pos = __ldcg(out + (i - off)) + off;
     out[i] = pos < seen ? pos : -1;
@@ -540,34 +542,62 @@ __device__ __forceinline__ uint32_t in_rank(uint32_t addr, uint32_t rank) {
   return a;
 }
 
-// The long row: this CTA's share of the keys that are at least `floor`, into
-// the list; returns how many there are (some may not have fitted).
+// The long row: this CTA's share from .. to - 1 of the keys that are at least
+// `floor`, into the list of `cap` entries; returns how many there are (some
+// may not have fitted). `from` is a multiple of 4.
 template <int kThreads>
 __device__ __forceinline__ int32_t collect(SelShared<kThreads>& sh, const MemoryRow& row,
                                            int32_t from, int32_t to, uint32_t floor,
-                                           uint32_t* keys, int32_t* blocks) {
+                                           uint32_t* keys, int32_t* blocks, int32_t cap) {
   const int lane = threadIdx.x & 31;
   if (threadIdx.x == 0) sh.n = 0;
   __syncthreads();
-  constexpr int kFlight = 8;  // loads in flight per thread
-  for (int32_t i0 = from; i0 < to; i0 += kThreads * kFlight) {
-    uint32_t key[kFlight];
+  constexpr int kQuads = 4;  // 16 keys of a thread at a time
+  // one stored score a block, 16-byte aligned: four at once
+  const bool vec = row.per == 1 && row.b0 % 4 == 0;
+  for (int32_t i0 = from; i0 < to; i0 += kThreads * 4 * kQuads) {
+    uint32_t key[4 * kQuads];
+    uint32_t hits = 0;
+    if (vec && i0 + kThreads * 4 * kQuads <= to) {
+      float4 v[kQuads];
 #pragma unroll
-    for (int u = 0; u < kFlight; ++u) {
-      const int64_t i = static_cast<int64_t>(i0) + u * kThreads + threadIdx.x;
-      key[u] = i < to ? row.key(static_cast<int32_t>(i)) : 0u;
+      for (int u = 0; u < kQuads; ++u)
+        v[u] = __ldcg(reinterpret_cast<const float4*>(row.scores + row.b0 + i0) + u * kThreads +
+                      threadIdx.x);
+#pragma unroll
+      for (int u = 0; u < kQuads; ++u) {
+        key[4 * u] = key32(v[u].x), key[4 * u + 1] = key32(v[u].y);
+        key[4 * u + 2] = key32(v[u].z), key[4 * u + 3] = key32(v[u].w);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < 4 * kQuads; ++u) {
+        const int64_t i = static_cast<int64_t>(i0) + (u >> 2) * kThreads * 4 + threadIdx.x * 4 + (u & 3);
+        key[u] = i < to ? row.key(static_cast<int32_t>(i)) : 0u;
+      }
     }
 #pragma unroll
-    for (int u = 0; u < kFlight; ++u) {
-      const bool hit = key[u] >= floor;
-      const uint32_t hits = __ballot_sync(0xffffffffu, hit);
-      if (hits == 0) continue;
-      uint32_t at = 0;
-      if (lane == 0) at = atomicAdd(&sh.n, static_cast<uint32_t>(__popc(hits)));
-      at = __shfl_sync(0xffffffffu, at, 0) + __popc(hits & ((1u << lane) - 1));
-      if (hit && at < kListMax) {
-        keys[at] = key[u];
-        blocks[at] = row.block(i0 + u * kThreads + static_cast<int32_t>(threadIdx.x));
+    for (int u = 0; u < 4 * kQuads; ++u) hits |= (key[u] >= floor ? 1u : 0u) << u;
+    const int mine = __popc(hits);
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += o;
+    }
+    uint32_t at = 0;
+    if (lane == 31 && upto > 0) at = atomicAdd(&sh.n, static_cast<uint32_t>(upto));
+    at = __shfl_sync(0xffffffffu, at, 31) + upto - mine;
+    if (hits != 0) {
+#pragma unroll
+      for (int u = 0; u < 4 * kQuads; ++u) {
+        if ((hits >> u & 1u) == 0) continue;
+        if (at < static_cast<uint32_t>(cap)) {
+          keys[at] = key[u];
+          blocks[at] = row.block(i0 + (u >> 2) * kThreads * 4 + static_cast<int32_t>(threadIdx.x) * 4 +
+                                 (u & 3));
+        }
+        ++at;
       }
     }
   }
@@ -576,7 +606,7 @@ __device__ __forceinline__ int32_t collect(SelShared<kThreads>& sh, const Memory
 }
 
 template <int kThreads>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     select_kernel(const SelectParams p, const SelectConfig cfg) {
   using Shared = SelShared<kThreads>;
   constexpr int kWarps = kThreads / 32;
@@ -595,7 +625,7 @@ __global__ void __launch_bounds__(kThreads)
 
   // The heads as integers, and their part of the error bound: nothing that
   // the score kernel writes.
-  double m = 0.0;
+  float m = 0.f;
   if (!all) {
     for (int g = tid; g < p.num_heads * kIndexScales; g += kThreads) {
       const uint8_t* src =
@@ -615,7 +645,8 @@ __global__ void __launch_bounds__(kThreads)
       }
       const float w = __ldg(p.weights + static_cast<int64_t>(t) * p.num_heads + j);
       if (part == 0) sh.w[j] = w;
-      m += static_cast<double>(fabsf(w) * (0.5f * mag * s));
+      m = fmaf(fabsf(w), 0.5f * mag * s, m);
+      if (mag > 0 && w != 0.f) m += kTiny;  // never 0 by underflow
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) m += __shfl_xor_sync(0xffffffffu, m, d);
@@ -658,13 +689,12 @@ __global__ void __launch_bounds__(kThreads)
     top = __reduce_max_sync(0xffffffffu, __vmaxu4(top, top >> 8) & 0xFFu);
     if (lane == 0) sh.redu[warp] = top;
     __syncthreads();
-    m = 0.0;
-    for (int w = 0; w < kWarps; ++w) {
-      m += sh.red[w];
-      top = max(top, sh.redu[w]);
-    }
-    // (1 + 2^-20): its fp32 products were rounded
-    m *= 6.000006 * static_cast<double>(scale_value(top));
+    m = lane < kWarps ? sh.red[lane] : 0.f;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m += __shfl_xor_sync(0xffffffffu, m, d);
+    top = __reduce_max_sync(0xffffffffu, lane < kWarps ? sh.redu[lane] : 0u);
+    // a little more than 6: the sum's own rounding
+    m = __fmul_ru(m, 6.001f * scale_value(top));
     __syncthreads();
   }
 
@@ -678,13 +708,14 @@ __global__ void __launch_bounds__(kThreads)
     return;
   }
 
-  if constexpr (kThreads == 1024) {
+  if constexpr (kThreads > 256) {
     // A threshold that about k + 4 sqrt(k) scores pass, by a sample's share.
-    int32_t* list_blocks = reinterpret_cast<int32_t*>(keys + kListMax);
+    const int32_t cap = cfg.room / 2;
+    int32_t* list_blocks = reinterpret_cast<int32_t*>(keys + cap);
     const float share = static_cast<float>(k) * kSample / static_cast<float>(n);
     uint32_t from_top = static_cast<uint32_t>(share + 4.f * sqrtf(share) + 8.f);
     const float expect = static_cast<float>(from_top) * n / kSample;
-    bool listed = cfg.room >= kDenseMax && expect < 0.9f * kListMax && blocks <= 64 * kListMax;
+    bool listed = expect < 0.9f * cap && blocks <= 32 * cfg.room;
     if (listed) {
       for (int32_t i = tid; i < kSample; i += kThreads)
         keys[i] = row.key(static_cast<int32_t>(static_cast<int64_t>(i) * n / kSample));
@@ -694,11 +725,15 @@ __global__ void __launch_bounds__(kThreads)
       };
       uint32_t lowest, highest;
       key_range(sh, lowest, highest, each);
-      const uint32_t floor = kth_largest<kThreads, uint32_t>(sh, lowest, highest, from_top, each);
-      const int32_t per = (n + static_cast<int32_t>(ctas) - 1) / static_cast<int32_t>(ctas);
+      // Two levels leave the threshold within 2^-14 or so of its value; one
+      // would not, as keys are spaced like exponents and scores of both signs
+      // spread over nearly all of them.
+      const uint32_t floor =
+          kth_largest<kThreads, uint32_t, 2>(sh, lowest, highest, from_top, each);
+      const int32_t per = ((n + static_cast<int32_t>(ctas) - 1) / static_cast<int32_t>(ctas) + 3) / 4 * 4;
       const int32_t from = min(static_cast<int32_t>(rank) * per, n);
       const int32_t mine =
-          collect<kThreads>(sh, row, from, min(from + per, n), floor, keys, list_blocks);
+          collect<kThreads>(sh, row, from, min(from + per, n), floor, keys, list_blocks, cap);
       int32_t count = mine;
       if (ctas > 1) {  // the lists go behind one another into rank 0's
         if (tid == 0) sh.sum_a[0] = mine;
@@ -714,7 +749,7 @@ __global__ void __launch_bounds__(kThreads)
           if (r < rank) before += c;
           count += c;
         }
-        if (rank > 0 && count <= kListMax) {
+        if (rank > 0 && count <= cap) {
           const uint32_t to_keys = in_rank(smem_u32(keys), 0);
           const uint32_t to_blocks = in_rank(smem_u32(list_blocks), 0);
           for (int32_t i = tid; i < mine; i += kThreads) {
@@ -729,7 +764,7 @@ __global__ void __launch_bounds__(kThreads)
         sel_cluster_sync();
       }
       if (rank > 0) return;
-      listed = count <= kListMax && count >= k;
+      listed = count <= cap && count >= k;
       if (listed) {
         const ListRow list = {keys, list_blocks};
         const Border border = choose<kThreads>(p, sh, list, count, k, seq, seen, m);
@@ -738,7 +773,7 @@ __global__ void __launch_bounds__(kThreads)
         listed = border.lo >= floor && (border.ties == 0 || border.ties == INT32_MAX);
         if (listed) {
           // the chosen ones as bits, in the list's place
-          constexpr int kPer = kListMax / kThreads;
+          constexpr int kPer = (kThreads == 1024 ? kWideRoom : kRoom) / 2 / kThreads;
           int32_t mine_in[kPer];
 #pragma unroll
           for (int u = 0; u < kPer; ++u) {
@@ -801,9 +836,9 @@ template <int kThreads>
 int32_t launch_select(const SelectParams& p, int32_t most_blocks, int num_sms,
                       cudaStream_t stream) {
   SelectConfig cfg;
-  cfg.room = most_blocks < kDenseMax ? most_blocks : kDenseMax;
+  cfg.room = most_blocks <= kRoom ? most_blocks : most_blocks <= 32 * kRoom ? kRoom : kWideRoom;
   int ctas = 1;  // a cluster per query token where the rows are long and the device is not full
-  if (most_blocks > kDenseMax)
+  if (most_blocks > kWideRoom)
     while (ctas < kMaxCluster && p.num_q * ctas * 2 <= num_sms) ctas *= 2;
   const size_t smem = sizeof(SelShared<kThreads>) + 4 * static_cast<size_t>(cfg.room);
   if (cudaFuncSetAttribute(select_kernel<kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -932,11 +967,13 @@ extern "C" int32_t sparse_mla_select(const void* q_index, const float* weights,
     if (int32_t st = launch_scores(p, sms, s)) return st;
     const int32_t most_blocks = static_cast<int32_t>(
         (static_cast<int64_t>(max_blocks_per_seq) * page_size + select_block - 1) / select_block);
-    // Many query tokens with short rows: several small CTAs share an SM.
-    const bool small = most_blocks <= 4096 && p.num_q > 2 * sms;
-    if (int32_t st = small ? launch_select<256>(p, most_blocks, sms, s)
-                           : launch_select<1024>(p, most_blocks, sms, s))
-      return st;
+    // Where there are more query tokens than SMs, smaller CTAs share an SM: one's
+    // barriers and loads pass while another works.
+    const bool many = p.num_q > 2 * sms;
+    const int32_t st = many && most_blocks <= 4096          ? launch_select<256>(p, most_blocks, sms, s)
+                       : many && most_blocks <= 32 * kRoom ? launch_select<512>(p, most_blocks, sms, s)
+                                                           : launch_select<1024>(p, most_blocks, sms, s);
+    if (st != NVFP4_MLA_OK) return st;
   }
   return NVFP4_MLA_OK;
 }
