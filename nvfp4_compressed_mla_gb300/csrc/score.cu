@@ -30,8 +30,8 @@
 //                the way; all stages in flight
 //   warps 9-11   take turns in loading a step's scales (one turn ahead) and
 //                laying them out in tensor memory
-//   (pages that do not cut tiles into whole 8-row groups: warps 8-11 copy row
-//   by row with cp.async instead)
+//   (page sizes that are no power of two or below 8: warps 8-11 copy row by row
+//   with cp.async instead)
 //   warp 12      issues the MMAs
 //   warps 13-15  encode the next run's queries
 //
@@ -193,7 +193,7 @@ struct ScoreParams {
   int32_t group;
   int32_t ctas;
   int32_t seg_rows;    // rows of a tensor copy; 0: copies row by row
-  int32_t page_shift;  // log2 of the page size, -1 if it is no power of two
+  int32_t page_shift;  // log2 of the page size (tensor copies)
 };
 
 // one box of a 3-D tensor map at (0, y, z)
@@ -205,53 +205,70 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm,
       "l"(reinterpret_cast<uint64_t>(tm)), "r"(0), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
-// Largest byte of a word, as the low byte.
-__device__ __forceinline__ uint32_t top_byte(uint32_t v) {
-  v = __vmaxu4(v, v >> 16);
-  return __vmaxu4(v, v >> 8) & 0xFFu;
-}
+// Largest of the low seven bits of bytes (E4M3 scales without a sign), in two
+// words of two 16-bit values, which one instruction compares.
+struct TopByte {
+  uint32_t even = 0, odd = 0;
+  __device__ __forceinline__ void add(uint32_t v) {
+    even = __vmaxu2(even, v & 0x007F007Fu);
+    odd = __vmaxu2(odd, (v >> 8) & 0x007F007Fu);
+  }
+  __device__ __forceinline__ uint32_t of_warp() const {  // at most 448
+    const uint32_t m = __vmaxu2(even, odd);
+    return min(__reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16)), 0x7Eu);
+  }
+};
+
+// A CTA's part of the list of steps: from step start_t of the run that begins
+// with query token start_q to step end_t - 1 of that which begins with end_q.
+struct Part {
+  int32_t start_q, start_t, end_q, end_t;
+};
 
 // The runs of query tokens whose steps a CTA scores, walked by one warp. Lane
 // i holds query token i of the current run; the next run's words are loaded
-// while the current one is worked on.
+// while the current one is worked on. Every role has a copy of this code, so
+// it holds no division.
 struct Walk {
-  int32_t q, count, seq, t0, t1;         // run; steps t0 .. t1 - 1 are this CTA's
-  int32_t seen;                          // lane i: positions to score of token q + i
-  int32_t most;                          // the highest of them
-  int64_t cost0, begin, end;
-  int32_t next_seq, next_pos;            // lane i: words of token next_q + i
-  int32_t next_q;
+  int32_t q, count, seq, t0, t1;  // run; steps t0 .. t1 - 1 are this CTA's
+  int32_t seen;                   // lane i: positions to score of token q + i
+  int32_t most;                   // the highest of them
+  int32_t next_q, next_t;
+  int32_t next_seq, next_pos;     // lane i: words of token next_q + i
+  int32_t next_lim;               // query tokens from next_q to the end of its group
+  int32_t end_q, end_t;
 
-  __device__ __forceinline__ void fetch(const ScoreParams& p, int32_t from) {
-    next_q = from;
+  __device__ __forceinline__ void load(const ScoreParams& p) {
     const int32_t lane = threadIdx.x & 31;
-    const int64_t stop = min(static_cast<int64_t>(from / p.group + 1) * p.group,
-                             static_cast<int64_t>(p.s.num_q));
     next_seq = next_pos = -1;
-    if (from + lane < stop) {
-      next_seq = __ldg(p.s.q_seq + from + lane);
-      next_pos = __ldg(p.s.q_pos + from + lane);
+    if (lane < next_lim) {
+      next_seq = __ldg(p.s.q_seq + next_q + lane);
+      next_pos = __ldg(p.s.q_pos + next_q + lane);
     }
+  }
+  __device__ __forceinline__ void begin(const ScoreParams& p, const Part& part) {
+    next_q = part.start_q, next_t = part.start_t;
+    end_q = part.end_q, end_t = part.end_t;
+    next_lim = min(p.group - next_q % p.group, p.s.num_q - next_q);
+    load(p);
   }
   // Moves to the next run with steps of this CTA; false when there is none.
   template <int kStep>
   __device__ __forceinline__ bool next(const ScoreParams& p) {
     const int32_t lane = threadIdx.x & 31;
-    while (next_q < p.s.num_q && cost0 < end) {
+#pragma unroll 1
+    while (next_q <= end_q && next_lim > 0) {
       q = next_q;
-      const int32_t lim = min(p.group - q % p.group, p.s.num_q - q);
       seq = __shfl_sync(0xffffffffu, next_seq, 0);
-      const uint32_t same = __ballot_sync(0xffffffffu, lane < lim && next_seq == seq);
-      count = __ffs(~same) - 1;  // leading lanes; lim < 32
-      seen = lane < count ? scored_positions_of(p.s, seq, next_pos) : 0;
-      fetch(p, q + count);
+      const uint32_t same = __ballot_sync(0xffffffffu, lane < next_lim && next_seq == seq);
+      count = __ffs(~same) - 1;  // leading lanes; next_lim < 32
+      seen = lane < count ? scored_positions(p.s, seq, next_pos) : 0;
+      next_q += count, next_lim -= count;
+      if (next_lim == 0) next_lim = min(p.group, p.s.num_q - next_q);
+      load(p);
       most = static_cast<int32_t>(__reduce_max_sync(0xffffffffu, seen));
-      const int32_t steps = (most + kStep - 1) / kStep;
-      const int64_t w = count + kLoadCost;
-      const int64_t from = begin - cost0, to = end - cost0;
-      t0 = from <= 0 ? 0 : static_cast<int32_t>(min((from + w - 1) / w, int64_t{steps}));
-      t1 = static_cast<int32_t>(min((to + w - 1) / w, int64_t{steps}));
-      cost0 += steps * w;
+      t0 = next_t, next_t = 0;
+      t1 = q == end_q ? end_t : (most + (kStep - 1)) / kStep;
       if (t0 < t1) return true;
     }
     return false;
@@ -284,20 +301,21 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   const int32_t per = (groups + kScoreThreads - 1) / kScoreThreads;
   const int32_t g_from = min(tid * per, groups), g_to = min(g_from + per, groups);
   auto runs = [&](auto&& each) {  // the runs of this thread's groups, in order
+#pragma unroll 1
     for (int32_t q = g_from * p.group; q < min(g_to * p.group, p.s.num_q);) {
       const int32_t stop = min((q / p.group + 1) * p.group, p.s.num_q);
       const int32_t seq = __ldg(p.s.q_seq + q);
       int32_t most = 0, n = 0;
       do {
-        most = max(most, scored_positions_of(p.s, seq, __ldg(p.s.q_pos + q + n)));
+        most = max(most, scored_positions(p.s, seq, __ldg(p.s.q_pos + q + n)));
         ++n;
       } while (q + n < stop && __ldg(p.s.q_seq + q + n) == seq);
-      each(q, static_cast<int64_t>((most + kStep - 1) / kStep) * (n + kLoadCost));
+      each(q, static_cast<int64_t>((most + kStep - 1) / kStep) * (n + kLoadCost), n + kLoadCost);
       q += n;
     }
   };
   int64_t mine = 0;
-  runs([&](int32_t, int64_t cost) { mine += cost; });
+  runs([&](int32_t, int64_t cost, int32_t) { mine += cost; });
   int64_t upto = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -306,21 +324,27 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   }
   if (lane == 31) warp_cost[warp] = upto;
   if (tid == 0) {
+#pragma unroll 1
     for (int i = 0; i < kStages; ++i) {
       mbar_init(bar(Bars::kFull, i), p.seg_rows > 0 ? 2 : kLoadWarps);
       mbar_init(bar(Bars::kEmpty, i), 1);
     }
+#pragma unroll 1
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(bar(Bars::kDFull, i), 1);
       mbar_init(bar(Bars::kDEmpty, i), 4);
     }
+#pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(Bars::kQFull, i), kQWarps);
       mbar_init(bar(Bars::kQEmpty, i), kEpiWarps + 1);
     }
     mbar_init(bar(Bars::kDrain, 0), 1);
+#pragma unroll 1
     for (int i = 0; i < kScaleWarps; ++i) mbar_init(bar(Bars::kScaleDrain, i), 1);
     st_shared_u32(abort_addr, 0);
+    // no end inside the list: the last CTA's
+    reinterpret_cast<Part*>(smem + kCtl + Bars::kStart)->end_q = INT32_MAX;
     fence_mbar_init();
   }
   __syncthreads();
@@ -335,14 +359,16 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     if (tid == 0) p.s.status[blockIdx.x] = 0;
     return;
   }
+  Part* part = reinterpret_cast<Part*>(smem + kCtl + Bars::kStart);
   before += upto - mine;
-  if (before <= begin && begin < before + mine) {
+  if ((before <= begin && begin < before + mine) || (before <= end && end < before + mine)) {
     int64_t at = before;
-    runs([&](int32_t q, int64_t cost) {
-      if (at <= begin && begin < at + cost) {
-        *reinterpret_cast<int64_t*>(smem + kCtl + Bars::kStart) = at;
-        *reinterpret_cast<int32_t*>(smem + kCtl + Bars::kStart + 8) = q;
-      }
+    runs([&](int32_t q, int64_t cost, int32_t w) {
+      // a step belongs to the CTA in whose share of the cost it starts
+      if (at <= begin && begin < at + cost)
+        part->start_q = q, part->start_t = static_cast<int32_t>((begin - at + w - 1) / w);
+      if (at <= end && end < at + cost)
+        part->end_q = q, part->end_t = static_cast<int32_t>((end - at + w - 1) / w);
       at += cost;
     });
   }
@@ -352,10 +378,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   tc_fence_after();
   const uint32_t tmem = ld_shared_u32(ctl + Bars::kTmem);
   Walk walk;
-  walk.cost0 = *reinterpret_cast<const int64_t*>(smem + kCtl + Bars::kStart);
-  walk.begin = begin;
-  walk.end = end;
-  walk.fetch(p, *reinterpret_cast<const int32_t*>(smem + kCtl + Bars::kStart + 8));
+  walk.begin(p, *part);
 
   const int q_bytes = q_buffer_bytes(kHeads, p.group);
   auto q_codes = [&](int buf) { return base + kQBase + buf * q_bytes; };
@@ -370,13 +393,16 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     const int shift = __ffs(granule) - 1;
     uint32_t first = 0, step_no = 0, run = 0;  // first: number of the step's first unit
     bool ok = true;
+#pragma unroll 1
     while (ok && walk.next<kStep>(p)) {
       const int buf = run & 1;
       ok = warp_wait(bar(Bars::kQFull, buf), (run >> 1) & 1u, abort_addr, lim);
       float* out = p.s.scores + walk.q * p.s.score_stride;
       const uint8_t* weights = smem + (q_weights(buf) - base);
+#pragma unroll 1
       for (int32_t step = walk.t0; ok && step < walk.t1; ++step, ++step_no, first += walk.count) {
         const int32_t pos0 = step * kStep + quad * 32 + lane;
+#pragma unroll 1
         for (int i = static_cast<int>((step_no ^ set) & 1u); i < walk.count; i += 2) {
           const uint32_t unit = first + i, slot = unit % kSlots;
           const int32_t seen = __shfl_sync(0xffffffffu, walk.seen, i);
@@ -384,50 +410,59 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
           if (!ok) break;
           tc_fence_after();
           const auto* w = reinterpret_cast<const ulonglong2*>(weights + i * kHeads * 4);
+          // 32 columns at a time: the next ones are on their way from tensor
+          // memory while these are summed up.
+          constexpr int kParts = kTiles * kChunks;
+          const uint32_t d = tmem + lanes + slot * kSlotCols;
+          uint32_t v[2][32];
+          uint64_t acc[4] = {0, 0, 0, 0};
+          tmem_ld32(d, v[0]);
 #pragma unroll 1
-          for (int tile = 0; tile < kTiles; ++tile) {
-            const uint32_t mask = ld_shared_u32(
-                base + kMasks + (((step_no * kTiles + tile) % kMaskRing) * 4 + quad) * 4);
-            const uint32_t d = tmem + lanes + slot * kSlotCols + tile * kHeads;
-            uint64_t acc[4] = {0, 0, 0, 0};
+          for (int x0 = 0; x0 < kParts; x0 += 2) {
 #pragma unroll
-            for (int c0 = 0; c0 < kChunks; c0 += 2) {  // 64 columns in registers at a time
-              uint32_t v[2][32];
-              tmem_ld32(d + 32 * c0, v[0]);
-              if (c0 + 1 < kChunks) tmem_ld32(d + 32 * c0 + 32, v[1]);
+            for (int y = 0; y < 2; ++y) {
+              const int x = x0 + y;  // 32 columns x of the slot
+              if (kParts % 2 != 0 && x >= kParts) break;
               tmem_ld_wait();
-              if (c0 + 2 >= kChunks && tile == kTiles - 1) {  // the slot has been read
+              if (x + 1 < kParts) {
+                tmem_ld32(d + 32 * (x + 1), v[y ^ 1]);
+              } else {  // the slot has been read
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(Bars::kDEmpty, slot));
               }
+              const int c = kChunks == 1 ? 0 : kChunks == 2 ? y : x % kChunks;
 #pragma unroll
-              for (int c = 0; c < 2 && c0 + c < kChunks; ++c) {
-#pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                  const ulonglong2 wj = w[(32 * (c0 + c) + j) / 4];  // four weights
-                  fma2(acc[(j >> 2) & 1],
-                       pack2(relu_nan(__uint_as_float(v[c][j])),
-                             relu_nan(__uint_as_float(v[c][j + 1]))),
-                       wj.x);
-                  fma2(acc[2 + ((j >> 2) & 1)],
-                       pack2(twice_relu(__uint_as_float(v[c][j + 2])),
-                             twice_relu(__uint_as_float(v[c][j + 3]))),
-                       wj.y);
-                }
+              for (int j = 0; j < 32; j += 4) {
+                const ulonglong2 wj = w[(32 * c + j) / 4];  // four weights
+                fma2(acc[(j >> 2) & 1],
+                     pack2(relu_nan(__uint_as_float(v[y][j])),
+                           relu_nan(__uint_as_float(v[y][j + 1]))),
+                     wj.x);
+                fma2(acc[2 + ((j >> 2) & 1)],
+                     pack2(twice_relu(__uint_as_float(v[y][j + 2])),
+                           twice_relu(__uint_as_float(v[y][j + 3]))),
+                     wj.y);
               }
+              if (c != kChunks - 1) continue;
+              // all heads of a tile
+              const int tile = kChunks == 1 ? x : kChunks == 2 ? x0 / 2 : 0;
+              const uint32_t mask = ld_shared_u32(
+                  base + kMasks + (((step_no * kTiles + tile) % kMaskRing) * 4 + quad) * 4);
+              float score =
+                  fmaf(sum2(acc[2]) + sum2(acc[3]), 0.5f, sum2(acc[0]) + sum2(acc[1]));
+              acc[0] = acc[1] = acc[2] = acc[3] = 0;
+              const int32_t pos = pos0 + tile * kScoreTile;
+              const bool live = pos < seen;
+              score = live && (mask >> lane & 1u) && score == score ? score + 0.f : -INFINITY;
+              if (granule > 1) {
+#pragma unroll 1
+                for (int s = 1; s < granule; s <<= 1)
+                  score = fmaxf(score, __shfl_xor_sync(0xffffffffu, score, s));
+              }
+              if (live && (pos & (granule - 1)) == 0)
+                out[i * p.s.score_stride + (pos >> shift)] = score;
             }
-            float score =
-                fmaf(sum2(acc[2]) + sum2(acc[3]), 0.5f, sum2(acc[0]) + sum2(acc[1]));
-            const int32_t pos = pos0 + tile * kScoreTile;
-            const bool live = pos < seen;
-            score = live && (mask >> lane & 1u) && score == score ? score + 0.f : -INFINITY;
-            if (granule > 1) {
-              for (int s = 1; s < granule; s <<= 1)
-                score = fmaxf(score, __shfl_xor_sync(0xffffffffu, score, s));
-            }
-            if (live && (pos & (granule - 1)) == 0)
-              out[i * p.s.score_stride + (pos >> shift)] = score;
           }
         }
       }
@@ -444,34 +479,41 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       bool live;
     };
     int32_t step = 0;
-    bool more = walk.next<kStep>(p);
-    if (more) step = walk.t0;
+    walk.t1 = 0;
+    bool more = true;
     auto fetch = [&](Entry& e) {
+      if (more && step == walk.t1) {
+        more = walk.next<kStep>(p);
+        step = walk.t0;
+      }
       e.page = -1;
       e.row = 0;
       e.live = more;
       if (!more) return;
       const int32_t pos = step * kStep + lane * p.seg_rows;
       if (lane < segs && pos < walk.most) {
-        const int32_t lb = p.page_shift >= 0 ? pos >> p.page_shift : pos / p.s.page_size;
-        e.row = pos - lb * p.s.page_size;
+        const int32_t lb = pos >> p.page_shift;
+        e.row = pos - (lb << p.page_shift);
         e.page = __ldg(p.s.block_table + static_cast<int64_t>(walk.seq) * p.s.max_blocks + lb);
       }
-      if (++step == walk.t1) {
-        more = walk.next<kStep>(p);
-        step = walk.t0;
-      }
+      ++step;
     };
     const bool issuer = elect_one();
     // piece i's rows go to row i * seg_rows of the step's tiles
     const uint32_t piece = static_cast<uint32_t>(p.seg_rows) * kIndexCodes;
     Entry e0, e1, e2;
-    fetch(e0);
-    fetch(e1);
+    e0.live = e1.live = false;
     uint32_t it = 0;
     bool ok = true;
-    for (; e0.live; ++it) {
+#pragma unroll 1
+    for (int ahead = 2; ahead > 0 || e0.live;) {  // pages are looked up two steps ahead
       fetch(e2);
+      if (ahead > 0) {
+        --ahead;
+        e0 = e1;
+        e1 = e2;
+        continue;
+      }
       const uint32_t stage = it % kStages;
       ok = warp_wait(bar(Bars::kEmpty, stage), ((it / kStages) & 1u) ^ 1u, abort_addr, lim);
       if (!ok) break;
@@ -481,6 +523,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       const int32_t page =
           static_cast<uint32_t>(e0.page) < static_cast<uint32_t>(past) ? e0.page : past;
       uint32_t dst = base + stage * kStageBytes;
+#pragma unroll 1
       for (int i = 0; i < segs; ++i) {
         const int32_t z = __shfl_sync(0xffffffffu, page, i);
         const int32_t y = __shfl_sync(0xffffffffu, e0.row, i);
@@ -490,11 +533,13 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       }
       e0 = e1;
       e1 = e2;
+      ++it;
     }
     __syncwarp();
     if (!ok) {
       // Copies in flight land before the CTA ends: this lane stands in for the
       // scale warps on stages that they have left.
+#pragma unroll 1
       for (uint32_t k = it > kStages ? it - kStages : 0; k < it; ++k) {
         if (lane == 0) mbar_arrive(bar(Bars::kFull, k % kStages));
         drain(bar(Bars::kFull, k % kStages), (k / kStages) & 1u);
@@ -515,17 +560,17 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       bool live;
     };
     int32_t step = 0;
-    uint32_t it = 0, wait = warp - kScaleWarp0;  // steps until this warp's next
-    bool more = walk.next<kStep>(p);
-    if (more) step = walk.t0;
+    int32_t it = 0, wait = warp - kScaleWarp0;  // steps until this warp's next
+    walk.t1 = 0;
+    bool more = true;
     auto fetch = [&](Turn& u) {
-      while (more && wait > 0) {
-        const int32_t skip = min(static_cast<int32_t>(wait), walk.t1 - step);
+#pragma unroll 1
+      while (more) {
+        const int32_t skip = min(wait, walk.t1 - step);
         step += skip, it += skip, wait -= skip;
-        if (step == walk.t1) {
-          more = walk.next<kStep>(p);
-          step = walk.t0;
-        }
+        if (step < walk.t1) break;
+        more = walk.next<kStep>(p);
+        step = walk.t0;
       }
       u.live = more;
       if (!more) return;
@@ -535,8 +580,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         const int32_t pos = step * kStep + i * 32 + lane;
-        const int32_t lb = p.page_shift >= 0 ? pos >> p.page_shift : pos / p.s.page_size;
-        row[i] = pos - lb * p.s.page_size;
+        const int32_t lb = pos >> p.page_shift;
+        row[i] = pos - (lb << p.page_shift);
         page[i] = pos < walk.most ? __ldg(table + lb) : -1;
       }
 #pragma unroll
@@ -548,21 +593,22 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
               p.s.cache + page[i] * p.s.block_stride + scale_at + row[i] * kIndexScales));
         }
       }
-      ++it, wait = kScaleWarps - 1;
-      if (++step == walk.t1) {
-        more = walk.next<kStep>(p);
-        step = walk.t0;
-      }
+      ++step, ++it, wait = kScaleWarps - 1;
     };
     Turn now, then;
-    fetch(now);
+    now.live = false;
     bool ok = true;
-    while (now.live) {
+#pragma unroll 1
+    for (bool first = true; first || now.live; first = false) {
       fetch(then);
+      if (first) {
+        now = then;
+        continue;
+      }
       const uint32_t stage = now.it % kStages;
       ok = warp_wait(bar(Bars::kEmpty, stage), ((now.it / kStages) & 1u) ^ 1u, abort_addr, lim);
       if (!ok) break;
-      uint32_t top = 0;
+      TopByte top;
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) {
         const uint2* v = now.v + 4 * t;
@@ -573,7 +619,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           mask[i] = __ballot_sync(0xffffffffu, now.valid >> (4 * t + i) & 1u);
-          top = __vmaxu4(top, __vmaxu4(v[i].x & 0x7F7F7F7Fu, v[i].y & 0x7F7F7F7Fu));
+          top.add(v[i].x);
+          top.add(v[i].y);
         }
         if (issuer)
           st_shared_v4(base + kMasks + ((now.it * kTiles + t) % kMaskRing) * 16, mask[0], mask[1],
@@ -591,8 +638,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
                                    h * 512));
         mma_commit(bar(Bars::kFull, stage));
       }
-      top = __reduce_max_sync(0xffffffffu, top_byte(top));
-      if (lane < kTiles) p.s.smax[now.q * p.s.tiles + now.step * kTiles + lane] = min(top, 0x7Eu);
+      const uint32_t most = top.of_warp();
+      if (lane < kTiles) p.s.smax[now.q * p.s.tiles + now.step * kTiles + lane] = most;
       now = then;
     }
     if (issuer) {  // scale copies of an aborted CTA have completed
@@ -606,8 +653,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     constexpr int kInFlight = kStages - 2;
     const int part = warp - kLoadWarp0;
     int32_t step = 0;
-    bool more = walk.next<kStep>(p);
-    if (more) step = walk.t0;
+    walk.t1 = 0;
+    bool more = true;
     // Lane l keeps the run and step of the l-th step of every 32.
     int32_t info_q = 0, info_step = 0;
     struct Entry {
@@ -616,6 +663,10 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     };
     uint32_t fetched = 0;
     auto fetch = [&](Entry& e) {
+      if (more && step == walk.t1) {
+        more = walk.next<kStep>(p);
+        step = walk.t0;
+      }
       e.live = more;
       if (!more) return;
       if (lane == fetched % 32) info_q = walk.q, info_step = step;
@@ -630,22 +681,19 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
                                 static_cast<int64_t>(walk.seq) * p.s.max_blocks + lb)
                         : -1;
       }
-      if (++step == walk.t1) {
-        more = walk.next<kStep>(p);
-        step = walk.t0;
-      }
+      ++step;
     };
     auto publish = [&](uint32_t it) {  // this warp's rows of step `it` have landed
       const uint32_t stage = it % kStages;
-      uint32_t top = 0;
+      TopByte top;
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) {
         const uint32_t sc =
             base + stage * kStageBytes + t * kTileBytes + kTileCodes + lane * 16 + part * 4;
-        top = __vmaxu4(top, __vmaxu4(ld_shared_u32(sc) & 0x7F7F7F7Fu,
-                                     ld_shared_u32(sc + 512) & 0x7F7F7F7Fu));
+        top.add(ld_shared_u32(sc));
+        top.add(ld_shared_u32(sc + 512));
       }
-      top = __reduce_max_sync(0xffffffffu, top_byte(top));
+      const uint32_t most = top.of_warp();
       const int32_t q = __shfl_sync(0xffffffffu, info_q, it % 32);
       const int32_t at = __shfl_sync(0xffffffffu, info_step, it % 32) * kTiles;
       fence_proxy_async_cta();
@@ -653,15 +701,21 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       if (lane == 0) mbar_arrive(bar(Bars::kFull, stage));
       if (lane < kTiles)
         reinterpret_cast<uint8_t*>(p.s.smax + q * p.s.tiles + at + lane)[part] =
-            static_cast<uint8_t>(min(top, 0x7Eu));
+            static_cast<uint8_t>(most);
     };
     Entry e0, e1, e2;
-    fetch(e0);
-    fetch(e1);
+    e0.live = e1.live = false;
     uint32_t it = 0;
     bool ok = true;
-    for (; e0.live; ++it) {
+#pragma unroll 1
+    for (int ahead = 2; ahead > 0 || e0.live;) {
       fetch(e2);
+      if (ahead > 0) {
+        --ahead;
+        e0 = e1;
+        e1 = e2;
+        continue;
+      }
       const uint32_t stage = it % kStages;
       ok = warp_wait(bar(Bars::kEmpty, stage), ((it / kStages) & 1u) ^ 1u, abort_addr, lim);
       if (!ok) break;
@@ -694,27 +748,34 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       }
       e0 = e1;
       e1 = e2;
+      ++it;
     }
     cp_async_wait<0>();
-    if (ok)
+    if (ok) {
+#pragma unroll 1
       for (uint32_t k = it > kInFlight ? it - kInFlight : 0; k < it; ++k) publish(k);
+    }
   } else if (warp == kScoreMmaWarp) {
     // ---------------------------------------------------------- MMA issue
     constexpr uint32_t idesc = score_idesc(kHeads);
     uint32_t it = 0, run = 0, slot = 0, phase = 0;
     bool ok = true;
     const bool issuer = elect_one();
+#pragma unroll 1
     while (ok && walk.next<kStep>(p)) {
       const int buf = run & 1;
       ok = warp_wait(bar(Bars::kQFull, buf), (run >> 1) & 1u, abort_addr, lim);
       if (!ok) break;
       tc_fence_after();
       if (issuer) {
+#pragma unroll 1
         for (int i = 0; i < walk.count; ++i)
+#pragma unroll 1
           for (int h = 0; h < 2; ++h)
             copy_scales(tmem + kSfbCol + i * 8 + h * 4,
                         scale_desc(q_scales(buf) + i * kTileScales + h * 512));
         const uint64_t q0 = sw64_desc(q_codes(buf));
+#pragma unroll 1
         for (int32_t step = walk.t0; ok && step < walk.t1; ++step, ++it) {
           const uint32_t stage = it % kStages;
           ok = wait_bar(bar(Bars::kFull, stage), (it / kStages) & 1u, abort_addr, lim);
@@ -730,6 +791,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
             }
           }
           const uint64_t a = sw64_desc(src);
+#pragma unroll 1
           for (int i = 0; i < walk.count; ++i) {
             ok = wait_bar(bar(Bars::kDEmpty, slot), phase ^ 1u, abort_addr, lim);
             if (!ok) break;
@@ -765,10 +827,12 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     const int qt = tid - kQWarp0 * 32;
     uint32_t run = 0;
     bool ok = true;
+#pragma unroll 1
     while (ok && walk.next<kStep>(p)) {
       const int buf = run & 1;
       ok = warp_wait(bar(Bars::kQEmpty, buf), ((run >> 1) & 1u) ^ 1u, abort_addr, lim);
       if (!ok) break;
+#pragma unroll 1
       for (int x = qt; x < walk.count * kHeads * kIndexScales; x += kQWarps * 32) {
         const int g = x % kIndexScales, row = x / kIndexScales;  // row = token * kHeads + head
         const int i = row / kHeads, h = row % kHeads;
@@ -804,12 +868,13 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   if (tid == 0) p.s.status[blockIdx.x] = ld_shared_u32(abort_addr);
 }
 
-// The pool's codes as rows of 64 bytes, in 64-byte swizzle; false where a tile
-// of 128 positions is not made of whole pieces of pages with whole 8-row groups.
+// The pool's codes as rows of 64 bytes, in 64-byte swizzle; false where the
+// page size is no power of two or below 8: a tile of 128 positions is then not
+// made of pieces of pages with whole 8-row groups.
 bool codes_tensor(const SelectParams& s, CUtensorMap* map, int32_t* seg_rows) {
   const int32_t P = s.page_size;
   *seg_rows = 0;
-  if (P % 8 != 0 || (P < kScoreTile ? kScoreTile % P : P % kScoreTile) != 0) return false;
+  if (P < 8 || (P & (P - 1)) != 0) return false;
   EncodeTiledFn enc = encode_tiled();
   if (enc == nullptr || s.num_blocks >= INT32_MAX || s.block_stride >= (int64_t{1} << 40))
     return false;
@@ -854,9 +919,8 @@ int32_t launch_scores(SelectParams& s, int num_sms, cudaStream_t stream) {
   CUtensorMap map;
   memset(&map, 0, sizeof(map));
   codes_tensor(s, &map, &p.seg_rows);
-  p.page_shift = -1;
-  for (int i = 0; i <= 20; ++i)
-    if (s.page_size == 1 << i) p.page_shift = i;
+  p.page_shift = 0;
+  while (p.page_shift < 20 && 1 << p.page_shift < s.page_size) ++p.page_shift;
   switch (chunks) {
     case 1: return launch_chunks<1>(p, map, stream);
     case 2: return launch_chunks<2>(p, map, stream);

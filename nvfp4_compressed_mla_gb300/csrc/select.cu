@@ -620,8 +620,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   int32_t* out = p.topk_idx + t * width;
   const int32_t seq = __ldg(p.q_seq + t);
   const int32_t seen = visible_positions(p, seq, __ldg(p.q_pos + t));
-  const int32_t blocks = blocks_of_positions(seen, p.block);
-  const bool all = blocks <= p.num_select;
+  const int32_t blocks = (seen + (p.block - 1)) >> (__ffs(p.block) - 1);
+  const bool all = seen <= p.take_all;
 
   // The heads as integers, and their part of the error bound: nothing that
   // the score kernel writes.
@@ -957,6 +957,8 @@ extern "C" int32_t sparse_mla_select(const void* q_index, const float* weights,
     p.num_select = num_select;
     p.sink = sink_blocks;
     p.recent = recent_blocks;
+    p.room = max_blocks_per_seq * page_size;
+    p.take_all = num_select * select_block;
     p.topk_idx = topk_idx + static_cast<int64_t>(q0) * num_select * select_block;
     p.scores = static_cast<float*>(workspace);
     p.score_stride = w.score_stride;

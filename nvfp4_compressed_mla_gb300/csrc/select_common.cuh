@@ -24,6 +24,8 @@ struct SelectParams {
   const uint8_t* cache;
   int64_t num_blocks, block_stride;
   int32_t block, num_select, sink, recent;
+  int32_t room;       // positions of a table's row: max_blocks * page_size
+  int32_t take_all;   // num_select * block: up to here every visible position is taken
   int32_t* topk_idx;
   float* scores;      // [num_q, score_stride]
   int64_t score_stride;
@@ -41,21 +43,14 @@ struct SelectParams {
 // Positions that a query token at `pos` of sequence `seq` sees, 0 for none.
 __device__ __forceinline__ int32_t visible_positions(const SelectParams& p, int32_t seq,
                                                      int32_t pos) {
-  if (seq < 0 || seq >= p.num_seqs || pos < 0) return 0;
-  const int64_t room = static_cast<int64_t>(p.max_blocks) * p.page_size;
-  return static_cast<int32_t>(min(static_cast<int64_t>(pos) + 1, room));
-}
-
-__device__ __forceinline__ int32_t blocks_of_positions(int32_t positions, int32_t block) {
-  const int shift = __ffs(block) - 1;  // a power of two
-  return static_cast<int32_t>((static_cast<int64_t>(positions) + block - 1) >> shift);
+  return seq >= 0 && seq < p.num_seqs && pos >= 0 ? min(pos, p.room - 1) + 1 : 0;
 }
 
 // Positions that have to be scored: none where every visible block is taken.
-__device__ __forceinline__ int32_t scored_positions_of(const SelectParams& p, int32_t seq,
-                                                       int32_t pos) {
+__device__ __forceinline__ int32_t scored_positions(const SelectParams& p, int32_t seq,
+                                                    int32_t pos) {
   const int32_t n = visible_positions(p, seq, pos);
-  return blocks_of_positions(n, p.block) > p.num_select ? n : 0;
+  return n > p.take_all ? n : 0;
 }
 
 int32_t launch_scores(SelectParams& p, int num_sms, cudaStream_t stream);
