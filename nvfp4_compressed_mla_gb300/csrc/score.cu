@@ -22,18 +22,18 @@
 // handshakes and address arithmetic cost hundreds of cycles a step, however
 // large the step is.
 //
-//   warps 0-7    epilogue: two sets of four; a set takes every other
+//   warps 0-11   epilogue: three sets of four; a set takes every third
 //                (step, query token) unit, warp w the positions 32 (w % 4)..
 //                of each tile
-//   warp 8       copies the steps' codes: resolves the pages through the block
+//   warp 12      copies the steps' codes: resolves the pages through the block
 //                table (two steps ahead), one tensor copy per page, swizzled on
 //                the way; all stages in flight
-//   warps 9-11   take turns in loading a step's scales (one turn ahead) and
+//   warps 13-15  take turns in loading a step's scales (one turn ahead) and
 //                laying them out in tensor memory
-//   (page sizes that are no power of two or below 8: warps 8-11 copy row by row
+//   (page sizes that are no power of two or below 8: warps 12-15 copy row by row
 //   with cp.async instead)
-//   warp 12      issues the MMAs
-//   warps 13-15  encode the next run's queries
+//   warp 17      issues the MMAs
+//   warps 16, 18, 19  encode the next run's queries
 //
 // Every wait is bounded; when one runs out the CTA's roles unwind, what is in
 // flight is drained, and the CTA's status word says so.
@@ -46,12 +46,12 @@
 namespace nvfp4_mla {
 namespace {
 
-constexpr int kScoreThreads = 512;
-constexpr int kEpiWarps = 8;
-constexpr int kLoadWarp0 = 8, kLoadWarps = 4;
-constexpr int kScaleWarp0 = 9, kScaleWarps = 3;  // with tensor copies
-constexpr int kScoreMmaWarp = 12;
-constexpr int kQWarp0 = 13, kQWarps = 3;
+constexpr int kScoreThreads = 640;
+constexpr int kEpiSets = 3, kEpiWarps = 4 * kEpiSets;
+constexpr int kLoadWarp0 = 12, kLoadWarps = 4;
+constexpr int kScaleWarp0 = 13, kScaleWarps = 3;  // with tensor copies
+constexpr int kScoreMmaWarp = 17;                 // not on the loads' sub-partition
+constexpr int kQWarp0 = 16, kQWarps = 3;          // and the last two
 constexpr int kStageTiles = 8;    // key tiles in shared memory
 constexpr int kMaxStages = kStageTiles;
 // Resolved-position masks of the last tiles; more than there can be between a
@@ -128,6 +128,17 @@ __device__ __forceinline__ void cp_async4_z(uint32_t dst, const void* src, bool 
 template <int kPending>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+// 16 consecutive TMEM columns of this thread's lane
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
 }
 __device__ __forceinline__ float relu_nan(float x) {  // max(0, x), NaN stays NaN
   float r;
@@ -283,6 +294,9 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   constexpr int kTiles = step_tiles(kChunks);  // of a step
   constexpr int kStep = kTiles * kScoreTile;
   constexpr int kStages = kStageTiles / kTiles;
+  // A set waits for a slot's phase by its parity: it must not come to a slot
+  // before the slot's last unit is there.
+  static_assert(kSlots >= kEpiSets, "a slot for each set");
   constexpr int kStageBytes = kTiles * kTileBytes;  // tile by tile: codes, then scales
   constexpr uint32_t kSlotCols = kTiles * kHeads;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -387,11 +401,12 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
 
   if (warp < kEpiWarps) {
     // ------------------------------------------------------------ epilogue
-    const int set = warp >> 2, quad = warp & 3;
+    const uint32_t set = warp >> 2, quad = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(quad) << 21;  // lane 32 * quad
     const int granule = min(p.s.block, kMaxGranule);
     const int shift = __ffs(granule) - 1;
     uint32_t first = 0, step_no = 0, run = 0;  // first: number of the step's first unit
+    int next = set;                            // units from there to this set's next
     bool ok = true;
 #pragma unroll 1
     while (ok && walk.next<kStep>(p)) {
@@ -402,69 +417,73 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
 #pragma unroll 1
       for (int32_t step = walk.t0; ok && step < walk.t1; ++step, ++step_no, first += walk.count) {
         const int32_t pos0 = step * kStep + quad * 32 + lane;
+        int i = next;
 #pragma unroll 1
-        for (int i = static_cast<int>((step_no ^ set) & 1u); i < walk.count; i += 2) {
+        for (; i < walk.count; i += kEpiSets) {
           const uint32_t unit = first + i, slot = unit % kSlots;
           const int32_t seen = __shfl_sync(0xffffffffu, walk.seen, i);
           ok = warp_wait(bar(Bars::kDFull, slot), (unit / kSlots) & 1u, abort_addr, lim);
           if (!ok) break;
           tc_fence_after();
           const auto* w = reinterpret_cast<const ulonglong2*>(weights + i * kHeads * 4);
-          // 32 columns at a time: the next ones are on their way from tensor
-          // memory while these are summed up.
-          constexpr int kParts = kTiles * kChunks;
+          // 16 heads at a time, of all the step's tiles: a weight's way from
+          // shared memory into 32 lanes' registers is what bounds this loop,
+          // so each one is used for every tile.
           const uint32_t d = tmem + lanes + slot * kSlotCols;
-          uint32_t v[2][32];
-          uint64_t acc[4] = {0, 0, 0, 0};
-          tmem_ld32(d, v[0]);
-#pragma unroll 1
-          for (int x0 = 0; x0 < kParts; x0 += 2) {
+          uint64_t acc[kTiles][4];
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const int x = x0 + y;  // 32 columns x of the slot
-              if (kParts % 2 != 0 && x >= kParts) break;
-              tmem_ld_wait();
-              if (x + 1 < kParts) {
-                tmem_ld32(d + 32 * (x + 1), v[y ^ 1]);
-              } else {  // the slot has been read
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(Bars::kDEmpty, slot));
-              }
-              const int c = kChunks == 1 ? 0 : kChunks == 2 ? y : x % kChunks;
-#pragma unroll
-              for (int j = 0; j < 32; j += 4) {
-                const ulonglong2 wj = w[(32 * c + j) / 4];  // four weights
-                fma2(acc[(j >> 2) & 1],
-                     pack2(relu_nan(__uint_as_float(v[y][j])),
-                           relu_nan(__uint_as_float(v[y][j + 1]))),
-                     wj.x);
-                fma2(acc[2 + ((j >> 2) & 1)],
-                     pack2(twice_relu(__uint_as_float(v[y][j + 2])),
-                           twice_relu(__uint_as_float(v[y][j + 3]))),
-                     wj.y);
-              }
-              if (c != kChunks - 1) continue;
-              // all heads of a tile
-              const int tile = kChunks == 1 ? x : kChunks == 2 ? x0 / 2 : 0;
-              const uint32_t mask = ld_shared_u32(
-                  base + kMasks + (((step_no * kTiles + tile) % kMaskRing) * 4 + quad) * 4);
-              float score =
-                  fmaf(sum2(acc[2]) + sum2(acc[3]), 0.5f, sum2(acc[0]) + sum2(acc[1]));
-              acc[0] = acc[1] = acc[2] = acc[3] = 0;
-              const int32_t pos = pos0 + tile * kScoreTile;
-              const bool live = pos < seen;
-              score = live && (mask >> lane & 1u) && score == score ? score + 0.f : -INFINITY;
-              if (granule > 1) {
+          for (int t = 0; t < kTiles; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0;
 #pragma unroll 1
-                for (int s = 1; s < granule; s <<= 1)
-                  score = fmaxf(score, __shfl_xor_sync(0xffffffffu, score, s));
+          for (int c = 0; c < kHeads; c += 16) {
+            uint32_t v[kTiles][16];
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) tmem_ld16(d + t * kHeads + c, v[t]);
+            ulonglong2 wj[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) wj[j] = w[c / 4 + j];  // four weights
+            tmem_ld_wait();
+            if (c + 16 == kHeads) {  // the slot has been read
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(Bars::kDEmpty, slot));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+              for (int t = 0; t < kTiles; ++t) {
+                fma2(acc[t][j & 1],
+                     pack2(relu_nan(__uint_as_float(v[t][4 * j])),
+                           relu_nan(__uint_as_float(v[t][4 * j + 1]))),
+                     wj[j].x);
+                fma2(acc[t][2 + (j & 1)],
+                     pack2(twice_relu(__uint_as_float(v[t][4 * j + 2])),
+                           twice_relu(__uint_as_float(v[t][4 * j + 3]))),
+                     wj[j].y);
               }
-              if (live && (pos & (granule - 1)) == 0)
-                out[i * p.s.score_stride + (pos >> shift)] = score;
             }
           }
+          float* row = out + i * p.s.score_stride;
+          const uint32_t masks = base + kMasks + quad * 4;
+          uint32_t mask[kTiles];
+#pragma unroll
+          for (int t = 0; t < kTiles; ++t)
+            mask[t] = ld_shared_u32(masks + ((step_no * kTiles + t) % kMaskRing) * 16);
+#pragma unroll
+          for (int t = 0; t < kTiles; ++t) {
+            float score =
+                fmaf(sum2(acc[t][2]) + sum2(acc[t][3]), 0.5f, sum2(acc[t][0]) + sum2(acc[t][1]));
+            const int32_t pos = pos0 + t * kScoreTile;
+            const bool live = pos < seen;
+            score = live && (mask[t] >> lane & 1u) && score == score ? score + 0.f : -INFINITY;
+            if (granule > 1) {
+#pragma unroll 1
+              for (int s = 1; s < granule; s <<= 1)
+                score = fmaxf(score, __shfl_xor_sync(0xffffffffu, score, s));
+            }
+            if (live && (pos & (granule - 1)) == 0) row[pos >> shift] = score;
+          }
         }
+        next = i - walk.count;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(Bars::kQEmpty, buf));
@@ -552,18 +571,83 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     constexpr int kRows = kStep / 32;
     const bool issuer = elect_one();
     const int64_t scale_at = static_cast<int64_t>(p.s.page_size) * kIndexCodes;
-    struct Turn {  // a step of this warp's: its scales, zeros for rows not in use
-      uint2 v[kRows];
-      uint32_t valid;  // bit i: row l + 32 i resolves
-      int32_t q, step;
+    struct Turn {  // a step of this warp's
+      int32_t q, seq, most, step;
       uint32_t it;
+      int32_t page;  // lane l: page l of those that the step touches, from `first` on
+      int32_t first;
       bool live;
     };
+    const int32_t step_pages = max(kStep >> p.page_shift, 1);
     int32_t step = 0;
     int32_t it = 0, wait = warp - kScaleWarp0;  // steps until this warp's next
     walk.t1 = 0;
     bool more = true;
-    auto fetch = [&](Turn& u) {
+    Turn then, now;
+    then.live = now.live = false;
+    uint2 vals[kRows];    // now's scales, zeros for rows not in use
+    uint32_t valid = 0;   // bit i: row l + 32 i resolves
+    bool ok = true;
+    // A turn's page ids are loaded two turns ahead, its scales one. Nothing is
+    // in flight at the fence, which would wait for it.
+#pragma unroll 1
+    for (int ahead = 2; ahead > 0 || now.live; --ahead) {
+      if (ahead <= 0) {
+        const uint32_t stage = now.it % kStages;
+        ok = warp_wait(bar(Bars::kEmpty, stage), ((now.it / kStages) & 1u) ^ 1u, abort_addr, lim);
+        if (!ok) break;
+        TopByte top;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          const uint2* v = vals + 4 * t;
+          const uint32_t to = base + stage * kStageBytes + t * kTileBytes + kTileCodes + lane * 16;
+          st_shared_v4(to, v[0].x, v[1].x, v[2].x, v[3].x);
+          st_shared_v4(to + 512, v[0].y, v[1].y, v[2].y, v[3].y);
+          uint32_t mask[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            mask[i] = __ballot_sync(0xffffffffu, valid >> (4 * t + i) & 1u);
+            top.add(v[i].x);
+            top.add(v[i].y);
+          }
+          if (issuer)
+            st_shared_v4(base + kMasks + ((now.it * kTiles + t) % kMaskRing) * 16, mask[0], mask[1],
+                         mask[2], mask[3]);
+        }
+        fence_proxy_async_cta();
+        __syncwarp();
+        if (issuer) {  // into tensor memory; the stage is full when they are there
+#pragma unroll
+          for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              copy_scales(tmem + kSfaCol + (stage * kTiles + t) * 8 + h * 4,
+                          scale_desc(base + stage * kStageBytes + t * kTileBytes + kTileCodes +
+                                     h * 512));
+          mma_commit(bar(Bars::kFull, stage));
+        }
+        const uint32_t most = top.of_warp();
+        if (lane < kTiles) p.s.smax[now.q * p.s.tiles + now.step * kTiles + lane] = most;
+      }
+      // the next turn's scales
+      now = then;
+      if (now.live) {
+        valid = 0;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          const int32_t pos = now.step * kStep + i * 32 + lane;
+          const int32_t lb = pos >> p.page_shift;
+          const int32_t page = __shfl_sync(0xffffffffu, now.page, lb - now.first);
+          vals[i] = make_uint2(0, 0);
+          if (pos < now.most && page >= 0 && page < p.s.num_blocks) {
+            valid |= 1u << i;
+            vals[i] = __ldg(reinterpret_cast<const uint2*>(
+                p.s.cache + page * p.s.block_stride + scale_at +
+                (pos - (lb << p.page_shift)) * kIndexScales));
+          }
+        }
+      }
+      // the page ids of the one after it
 #pragma unroll 1
       while (more) {
         const int32_t skip = min(wait, walk.t1 - step);
@@ -572,75 +656,17 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
         more = walk.next<kStep>(p);
         step = walk.t0;
       }
-      u.live = more;
-      if (!more) return;
-      u.q = walk.q, u.step = step, u.it = it, u.valid = 0;
-      const int32_t* table = p.s.block_table + static_cast<int64_t>(walk.seq) * p.s.max_blocks;
-      int32_t page[kRows], row[kRows];
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const int32_t pos = step * kStep + i * 32 + lane;
-        const int32_t lb = pos >> p.page_shift;
-        row[i] = pos - (lb << p.page_shift);
-        page[i] = pos < walk.most ? __ldg(table + lb) : -1;
+      then.live = more;
+      if (more) {
+        then.q = walk.q, then.seq = walk.seq, then.most = walk.most;
+        then.step = step, then.it = it;
+        then.first = (step * kStep) >> p.page_shift;
+        then.page = -1;
+        if (lane < step_pages && (then.first + lane) << p.page_shift < walk.most)
+          then.page = __ldg(p.s.block_table + static_cast<int64_t>(walk.seq) * p.s.max_blocks +
+                            then.first + lane);
+        ++step, ++it, wait = kScaleWarps - 1;
       }
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        u.v[i] = make_uint2(0, 0);
-        if (page[i] >= 0 && page[i] < p.s.num_blocks) {
-          u.valid |= 1u << i;
-          u.v[i] = __ldg(reinterpret_cast<const uint2*>(
-              p.s.cache + page[i] * p.s.block_stride + scale_at + row[i] * kIndexScales));
-        }
-      }
-      ++step, ++it, wait = kScaleWarps - 1;
-    };
-    Turn now, then;
-    now.live = false;
-    bool ok = true;
-#pragma unroll 1
-    for (bool first = true; first || now.live; first = false) {
-      fetch(then);
-      if (first) {
-        now = then;
-        continue;
-      }
-      const uint32_t stage = now.it % kStages;
-      ok = warp_wait(bar(Bars::kEmpty, stage), ((now.it / kStages) & 1u) ^ 1u, abort_addr, lim);
-      if (!ok) break;
-      TopByte top;
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t) {
-        const uint2* v = now.v + 4 * t;
-        const uint32_t to = base + stage * kStageBytes + t * kTileBytes + kTileCodes + lane * 16;
-        st_shared_v4(to, v[0].x, v[1].x, v[2].x, v[3].x);
-        st_shared_v4(to + 512, v[0].y, v[1].y, v[2].y, v[3].y);
-        uint32_t mask[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          mask[i] = __ballot_sync(0xffffffffu, now.valid >> (4 * t + i) & 1u);
-          top.add(v[i].x);
-          top.add(v[i].y);
-        }
-        if (issuer)
-          st_shared_v4(base + kMasks + ((now.it * kTiles + t) % kMaskRing) * 16, mask[0], mask[1],
-                       mask[2], mask[3]);
-      }
-      fence_proxy_async_cta();
-      __syncwarp();
-      if (issuer) {  // into tensor memory; the stage is full when they are there
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            copy_scales(tmem + kSfaCol + (stage * kTiles + t) * 8 + h * 4,
-                        scale_desc(base + stage * kStageBytes + t * kTileBytes + kTileCodes +
-                                   h * 512));
-        mma_commit(bar(Bars::kFull, stage));
-      }
-      const uint32_t most = top.of_warp();
-      if (lane < kTiles) p.s.smax[now.q * p.s.tiles + now.step * kTiles + lane] = most;
-      now = then;
     }
     if (issuer) {  // scale copies of an aborted CTA have completed
       mma_commit(bar(Bars::kScaleDrain, warp - kScaleWarp0));
@@ -824,7 +850,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     __syncwarp();
   } else {
     // ----------------------------------------------------- encode queries
-    const int qt = tid - kQWarp0 * 32;
+    const int qt = (warp == kQWarp0 ? 0 : warp - kQWarp0 - 1) * 32 + lane;
     uint32_t run = 0;
     bool ok = true;
 #pragma unroll 1

@@ -212,3 +212,57 @@ def test_results_repeat():
     first = c.run(512)
     for _ in range(5):
         assert np.array_equal(c.run(512), first)
+
+
+def reference_on_device(c, num, block=1, sink=0, recent=0):
+    """The same definition in torch, fp64, for sizes past the Python loops."""
+    nib = torch.tensor(np.concatenate([sc.GRID, -sc.GRID]), device="cuda:0")
+    pool = dev(c.pool).view(c.blocks, c.stride)
+    codes = pool[:, :c.page * 64].reshape(c.blocks, c.page, 64)
+    scale = pool[:, c.page * 64:c.page * sc.ROW].reshape(c.blocks, c.page, 8)
+    v = nib[torch.stack([codes & 15, codes >> 4], -1).long()].view(c.blocks, c.page, 8, 16)
+    keys = (v * scale.view(torch.float8_e4m3fn).double()[..., None]).view(c.blocks, c.page, 128)
+    out = np.full((len(c.seq), num * block), -1, np.int32)
+    q = torch.from_numpy(sc.values(*sc.quantize(c.q))).to("cuda:0")
+    w = dev(c.w).double()
+    for t in range(len(c.seq)):
+        seen = int(c.pos[t]) + 1
+        k = keys[torch.from_numpy(c.table[c.seq[t]][:sc.blocks_of(seen, c.page)]).long().to("cuda:0")]
+        score = torch.relu(k.reshape(-1, 128)[:seen] @ q[t].T) @ w[t]
+        nb = sc.blocks_of(seen, block)
+        best = torch.nn.functional.pad(score, (0, nb * block - seen), value=-np.inf)
+        best = best.view(nb, block).amax(1)
+        idx = torch.arange(nb, device="cuda:0")
+        best[(idx < sink) | (idx >= nb - recent)] = np.inf
+        chosen = torch.sort(best, descending=True, stable=True).indices[:num].sort().values
+        pos = (chosen[:, None] * block + torch.arange(block, device="cuda:0")).reshape(-1)
+        pos = pos[pos < seen].cpu().numpy()
+        out[t, :len(pos)] = pos
+    return out
+
+
+# every CTA of the score kernel goes many times round its stages and slots
+@pytest.mark.parametrize("seqs,length,per_seq,heads,num,block,page", [
+    (40, 40000, 1, 64, 2048, 1, 64), (40, 30000, 1, 32, 512, 4, 64), (20, 40000, 1, 128, 1000, 1, 16),
+    (20, 40000, 1, 96, 32, 64, 256), (6, 30000, 15, 64, 2048, 1, 64), (4, 20000, 64, 64, 64, 16, 64),
+    (30, 40000, 1, 64, 700, 1, 48), (4, 20000, 32, 128, 300, 1, 96), (3, 20000, 200, 24, 128, 16, 64),
+    (1, 600000, 1, 16, 2048, 1, 64), (330, 3000, 1, 64, 16, 64, 64), (400, 20000, 1, 16, 256, 1, 64),
+])
+def test_sizes_that_fill_the_device(seqs, length, per_seq, heads, num, block, page):
+    rng = np.random.default_rng(seqs + length)
+    lens = rng.integers(length * 9 // 10, length + 1, seqs)
+    c = Case.__new__(Case)
+    c.page, c.stride, c.lens = page, page * sc.ROW, lens
+    c.table, _, c.blocks = sc.random_tables(rng, lens, page, 2)
+    c.pool = rng.integers(0, 256, c.blocks * c.stride, dtype=np.uint8)
+    rows = c.pool.reshape(c.blocks, c.stride)
+    scales = rng.integers(0x28, 0x48, (c.blocks, page * 8), dtype=np.uint8)
+    rows[:, page * 64:] = scales
+    seq = np.repeat(np.arange(seqs), per_seq)
+    pos = np.concatenate([np.arange(n - per_seq, n) for n in lens])
+    c.seq, c.pos = seq.astype(np.int32), pos.astype(np.int32)
+    c.q = bf16_from_f32(rng.standard_normal((len(seq), heads, 128)))
+    c.w = (rng.standard_normal((len(seq), heads)) / np.sqrt(heads)).astype(np.float32)
+    got, ref = c.run(num, block), reference_on_device(c, num, block)
+    bad = np.nonzero((got != ref).any(1))[0]
+    assert bad.size == 0, (bad.size, bad[:5], got[bad[0]][:20], ref[bad[0]][:20])
