@@ -17,23 +17,25 @@
 // long sequence fills the device as well as many short ones. Runs are
 // consecutive query tokens of one sequence, at most `group` of them.
 //
-// Positions go through in steps of one or two tiles (two where 64 heads or
-// fewer leave room in tensor memory): each role is one or a few warps whose
+// Positions go through in steps of 256: each role is one or a few warps whose
 // handshakes and address arithmetic cost hundreds of cycles a step, however
-// large the step is.
+// large the step is. Two neighbouring rows of a page are one 128-byte line in
+// shared memory, as tensor copies take time per line: the MMA's row R holds
+// position 2 R in the line's first 64 bytes and 2 R + 1 in the others, and a
+// step's two tiles are its even and its odd positions.
 //
 //   warps 0-11   epilogue: three sets of four; a set takes every third
-//                (step, query token) unit, warp w the positions 32 (w % 4)..
-//                of each tile
+//                (step, query token) unit, warp w the rows 32 (w % 4).. of both
+//                tiles (more than 64 heads: two sets, one tile after the other)
 //   warp 12      copies the steps' codes: resolves the pages through the block
 //                table (two steps ahead), one tensor copy per page, swizzled on
 //                the way; all stages in flight
-//   warps 13-15  take turns in loading a step's scales (one turn ahead) and
+//   warps 13-16  take turns in loading a step's scales (one turn ahead) and
 //                laying them out in tensor memory
-//   (page sizes that are no power of two or below 8: warps 12-15 copy row by row
+//   (page sizes that are no power of two or below 16: warps 12-15 copy row by row
 //   with cp.async instead)
 //   warp 17      issues the MMAs
-//   warps 16, 18, 19  encode the next run's queries
+//   warps 18, 19  encode the next run's queries
 //
 // Every wait is bounded; when one runs out the CTA's roles unwind, what is in
 // flight is drained, and the CTA's status word says so.
@@ -47,38 +49,48 @@ namespace nvfp4_mla {
 namespace {
 
 constexpr int kScoreThreads = 640;
-constexpr int kEpiSets = 3, kEpiWarps = 4 * kEpiSets;
+constexpr int kEpiWarps = 12;
 constexpr int kLoadWarp0 = 12, kLoadWarps = 4;
-constexpr int kScaleWarp0 = 13, kScaleWarps = 3;  // with tensor copies
+constexpr int kScaleWarp0 = 13, kScaleWarps = 4;  // with tensor copies
 constexpr int kScoreMmaWarp = 17;                 // not on the loads' sub-partition
-constexpr int kQWarp0 = 16, kQWarps = 3;          // and the last two
-constexpr int kStageTiles = 8;    // key tiles in shared memory
-constexpr int kMaxStages = kStageTiles;
+constexpr int kQWarp0 = 18, kQWarps = 2;
+constexpr int kMaxStages = 7;     // steps in shared memory
 // Resolved-position masks of the last tiles; more than there can be between a
 // step's scales and its epilogue (the stages and the accumulator slots).
 constexpr int kMaskRing = 32;
 constexpr int kMaxGroup = 8;      // query tokens of a run
-constexpr int kTileCodes = kScoreTile * kIndexCodes;   // 8192, 64-byte swizzle
+constexpr int kStep = 256;                             // positions
+constexpr int kStepTiles = kStep / kScoreTile;         // 2
+constexpr int kStepCodes = kStep * kIndexCodes;        // 128 lines of 128 bytes, 128-byte swizzle
 constexpr int kTileScales = 1024;                      // two K halves of 128 x 4 scale bytes
-constexpr int kTileBytes = kTileCodes + kTileScales;
+constexpr int kStageBytes = kStepCodes + kStepTiles * kTileScales;
 constexpr int kMaskBytes = kMaskRing * 4 * 4;
 // A run's cost per step: its query tokens' epilogues and the step's load.
 constexpr int kLoadCost = 2;
-// Tensor memory columns: accumulator slots, then scales of Q, then of K (one
-// set per stage).
-constexpr uint32_t kSfbCol = 384, kSfaCol = 448;
+// Tensor memory columns: accumulator slots, then scales of Q (eight per query
+// token of a run), then of K (eight per tile of a stage).
+constexpr uint32_t kSfbCol = 384;
+// Stages of a run's length: what tensor memory holds scales for. A stage's
+// round (copies under way, MMAs, release) takes several thousand cycles, so
+// the copies in flight set the rate.
+__host__ __device__ constexpr int stage_count(int group) {
+  return (static_cast<int>(kTmemCols - kSfbCol) / 8 - group) / kStepTiles;
+}
 
 // Instruction descriptor, kind::mxf4nvf4: E2M1 A (bit 7) and B (bit 10), both
 // K-major, E4M3 scales, N >> 3 at 17, M >> 4 at 24, K = 64.
 __host__ __device__ constexpr uint32_t score_idesc(int n) {
   return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
 }
-// For `chunks` of 32 heads: tiles of a step, and accumulator slots of a step's
-// tiles for one query token.
-__host__ __device__ constexpr int step_tiles(int chunks) { return chunks <= 2 ? 2 : 1; }
+// For `chunks` of 32 heads: tiles of an accumulator slot, slots, and sets of
+// epilogue warps. A set waits for a slot's phase by its parity, so it must not
+// come to a slot before the slot's last content is there: with s sets, the
+// contents of the s - 1 units between two of its own fit into the slots.
+__host__ __device__ constexpr int slot_tiles(int chunks) { return chunks <= 2 ? 2 : 1; }
 __host__ __device__ constexpr int acc_slots(int chunks) {
-  return 384 / (32 * chunks * step_tiles(chunks));
+  return 384 / (32 * chunks * slot_tiles(chunks));
 }
+__host__ __device__ constexpr int epi_sets(int chunks) { return chunks <= 2 ? 3 : 2; }
 __host__ __device__ constexpr int max_group(int chunks) { return chunks <= 2 ? kMaxGroup : 4; }
 
 // K-major operand with 64-byte rows in 64-byte swizzle: 8-row groups of 512 bytes.
@@ -86,6 +98,17 @@ __device__ __forceinline__ uint64_t sw64_desc(uint32_t addr) {
   return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) |
          (static_cast<uint64_t>(512 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
          (static_cast<uint64_t>(4) << 61);
+}
+// The same with 128-byte rows in 128-byte swizzle: 8-row groups of 1024 bytes.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t addr) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+         (static_cast<uint64_t>(2) << 61);
+}
+// 16-byte chunk (0..3) of position x of a step.
+__device__ __forceinline__ uint32_t code_off(uint32_t x, uint32_t chunk) {
+  const uint32_t line = x >> 1;
+  return line * 128u + ((((x & 1u) * 4u + chunk) ^ (line & 7u)) << 4);
 }
 __device__ __forceinline__ uint32_t sw64_off(uint32_t row, uint32_t chunk) {
   return row * 64u + ((chunk ^ ((row >> 1) & 3u)) << 4);
@@ -191,9 +214,8 @@ struct Bars {  // byte offsets in the control block
                        kStart = kAbort + 4, kEnd = kStart + 32;
 };
 static_assert(Bars::kStart % 8 == 0, "start words");
-constexpr int kMasks = kStageTiles * kTileBytes;
-constexpr int kCtl = kMasks + kMaskBytes;
-constexpr int kQBase = (kCtl + Bars::kEnd + 511) / 512 * 512;
+constexpr int kCtl = kMaskBytes;  // the control block follows the masks
+constexpr int kStageBase = (kCtl + Bars::kEnd + 1023) / 1024 * 1024;  // stages, then two Q buffers
 
 __host__ __device__ constexpr int q_buffer_bytes(int heads_pad, int group) {
   return (group * (heads_pad * kIndexCodes + kTileScales + heads_pad * 4) + 1023) / 1024 * 1024;
@@ -203,6 +225,7 @@ struct ScoreParams {
   SelectParams s;
   int32_t group;
   int32_t ctas;
+  int32_t stages;
   int32_t seg_rows;    // rows of a tensor copy; 0: copies row by row
   int32_t page_shift;  // log2 of the page size (tensor copies)
 };
@@ -216,17 +239,31 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm,
       "l"(reinterpret_cast<uint64_t>(tm)), "r"(0), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
-// Largest of the low seven bits of bytes (E4M3 scales without a sign), in two
-// words of two 16-bit values, which one instruction compares.
+// Largest of the bytes (E4M3 scales, positive) of words, in the high bytes of
+// 16-bit values, two of which one instruction compares.
 struct TopByte {
   uint32_t even = 0, odd = 0;
   __device__ __forceinline__ void add(uint32_t v) {
-    even = __vmaxu2(even, v & 0x007F007Fu);
-    odd = __vmaxu2(odd, (v >> 8) & 0x007F007Fu);
+    even = __vmaxu2(even, v << 8);
+    odd = __vmaxu2(odd, v);
   }
   __device__ __forceinline__ uint32_t of_warp() const {  // at most 448
     const uint32_t m = __vmaxu2(even, odd);
-    return min(__reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16)), 0x7Eu);
+    return min(__reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16)) >> 8, 0x7Eu);
+  }
+};
+
+// A place in the ring of stages and the parity of its round.
+struct Ring {
+  uint32_t stage = 0, phase = 0, stages;
+  __device__ __forceinline__ explicit Ring(uint32_t n) : stages(n) {}
+  __device__ __forceinline__ void advance(uint32_t steps) {  // at most `stages`
+    stage += steps;
+    if (stage >= stages) stage -= stages, phase ^= 1u;
+  }
+  __device__ __forceinline__ void back() {
+    if (stage == 0) stage = stages, phase ^= 1u;
+    --stage;
   }
 };
 
@@ -264,7 +301,6 @@ struct Walk {
     load(p);
   }
   // Moves to the next run with steps of this CTA; false when there is none.
-  template <int kStep>
   __device__ __forceinline__ bool next(const ScoreParams& p) {
     const int32_t lane = threadIdx.x & 31;
 #pragma unroll 1
@@ -291,16 +327,14 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     score_kernel(const __grid_constant__ ScoreParams p, const __grid_constant__ CUtensorMap codes_map) {
   constexpr int kHeads = 32 * kChunks;
   constexpr int kSlots = acc_slots(kChunks);
-  constexpr int kTiles = step_tiles(kChunks);  // of a step
-  constexpr int kStep = kTiles * kScoreTile;
-  constexpr int kStages = kStageTiles / kTiles;
-  // A set waits for a slot's phase by its parity: it must not come to a slot
-  // before the slot's last unit is there.
-  static_assert(kSlots >= kEpiSets, "a slot for each set");
-  constexpr int kStageBytes = kTiles * kTileBytes;  // tile by tile: codes, then scales
-  constexpr uint32_t kSlotCols = kTiles * kHeads;
+  constexpr int kSlotTiles = slot_tiles(kChunks);
+  constexpr int kSets = epi_sets(kChunks);
+  constexpr int kUnitSlots = kStepTiles / kSlotTiles;  // a unit is a step and a query token
+  static_assert(kSlots >= (kSets - 1) * kUnitSlots + 1 && 4 * kSets <= kEpiWarps, "slots");
+  constexpr uint32_t kSlotCols = kSlotTiles * kHeads;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
+  const uint32_t stage0 = base + kStageBase;
   const uint32_t ctl = base + kCtl;
   const uint32_t abort_addr = ctl + Bars::kAbort;
   auto bar = [ctl](int kind, int i) { return ctl + static_cast<uint32_t>(kind + 8 * i); };
@@ -339,7 +373,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   if (lane == 31) warp_cost[warp] = upto;
   if (tid == 0) {
 #pragma unroll 1
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < p.stages; ++i) {
       mbar_init(bar(Bars::kFull, i), p.seg_rows > 0 ? 2 : kLoadWarps);
       mbar_init(bar(Bars::kEmpty, i), 1);
     }
@@ -395,95 +429,106 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   walk.begin(p, *part);
 
   const int q_bytes = q_buffer_bytes(kHeads, p.group);
-  auto q_codes = [&](int buf) { return base + kQBase + buf * q_bytes; };
+  const uint32_t q_base = stage0 + p.stages * kStageBytes;
+  const uint32_t sfa_col = kSfbCol + 8 * p.group;
+  auto q_codes = [&](int buf) { return q_base + buf * q_bytes; };
   auto q_scales = [&](int buf) { return q_codes(buf) + p.group * kHeads * kIndexCodes; };
   auto q_weights = [&](int buf) { return q_scales(buf) + p.group * kTileScales; };
 
   if (warp < kEpiWarps) {
     // ------------------------------------------------------------ epilogue
-    const uint32_t set = warp >> 2, quad = warp & 3;
+    const uint32_t set = warp >> 2, quad = warp & 3;  // a set past kSets has no units
     const uint32_t lanes = static_cast<uint32_t>(quad) << 21;  // lane 32 * quad
     const int granule = min(p.s.block, kMaxGranule);
     const int shift = __ffs(granule) - 1;
     uint32_t first = 0, step_no = 0, run = 0;  // first: number of the step's first unit
-    int next = set;                            // units from there to this set's next
+    int next = set < kSets ? set : INT32_MAX;  // units from there to this set's next
     bool ok = true;
 #pragma unroll 1
-    while (ok && walk.next<kStep>(p)) {
+    while (ok && walk.next(p)) {
       const int buf = run & 1;
       ok = warp_wait(bar(Bars::kQFull, buf), (run >> 1) & 1u, abort_addr, lim);
       float* out = p.s.scores + walk.q * p.s.score_stride;
       const uint8_t* weights = smem + (q_weights(buf) - base);
 #pragma unroll 1
       for (int32_t step = walk.t0; ok && step < walk.t1; ++step, ++step_no, first += walk.count) {
-        const int32_t pos0 = step * kStep + quad * 32 + lane;
+        const int32_t pos = step * kStep + 2 * (static_cast<int32_t>(quad) * 32 + lane);
         int i = next;
 #pragma unroll 1
-        for (; i < walk.count; i += kEpiSets) {
-          const uint32_t unit = first + i, slot = unit % kSlots;
+        for (; i < walk.count; i += kSets) {
           const int32_t seen = __shfl_sync(0xffffffffu, walk.seen, i);
-          ok = warp_wait(bar(Bars::kDFull, slot), (unit / kSlots) & 1u, abort_addr, lim);
-          if (!ok) break;
-          tc_fence_after();
           const auto* w = reinterpret_cast<const ulonglong2*>(weights + i * kHeads * 4);
-          // 16 heads at a time, of all the step's tiles: a weight's way from
-          // shared memory into 32 lanes' registers is what bounds this loop,
-          // so each one is used for every tile.
-          const uint32_t d = tmem + lanes + slot * kSlotCols;
-          uint64_t acc[kTiles][4];
+          float score[kStepTiles];  // of positions pos, pos + 1
 #pragma unroll
-          for (int t = 0; t < kTiles; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0;
+          for (int u = 0; u < kUnitSlots; ++u) {
+            const uint32_t n = (first + i) * kUnitSlots + u, slot = n % kSlots;
+            ok = warp_wait(bar(Bars::kDFull, slot), (n / kSlots) & 1u, abort_addr, lim);
+            if (!ok) break;
+            tc_fence_after();
+            // 16 heads at a time, of all the slot's tiles: a weight's way from
+            // shared memory into 32 lanes' registers is what bounds this loop,
+            // so each one is used for every tile.
+            const uint32_t d = tmem + lanes + slot * kSlotCols;
+            uint64_t acc[kSlotTiles][4];
+#pragma unroll
+            for (int t = 0; t < kSlotTiles; ++t)
+              acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0;
 #pragma unroll 1
-          for (int c = 0; c < kHeads; c += 16) {
-            uint32_t v[kTiles][16];
+            for (int c = 0; c < kHeads; c += 16) {
+              uint32_t v[kSlotTiles][16];
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t) tmem_ld16(d + t * kHeads + c, v[t]);
-            ulonglong2 wj[4];
+              for (int t = 0; t < kSlotTiles; ++t) tmem_ld16(d + t * kHeads + c, v[t]);
+              ulonglong2 wj[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) wj[j] = w[c / 4 + j];  // four weights
-            tmem_ld_wait();
-            if (c + 16 == kHeads) {  // the slot has been read
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar(Bars::kDEmpty, slot));
-            }
+              for (int j = 0; j < 4; ++j) wj[j] = w[c / 4 + j];  // four weights
+              tmem_ld_wait();
+              if (c + 16 == kHeads) {  // the slot has been read
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(Bars::kDEmpty, slot));
+              }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+              for (int j = 0; j < 4; ++j) {
 #pragma unroll
-              for (int t = 0; t < kTiles; ++t) {
-                fma2(acc[t][j & 1],
-                     pack2(relu_nan(__uint_as_float(v[t][4 * j])),
-                           relu_nan(__uint_as_float(v[t][4 * j + 1]))),
-                     wj[j].x);
-                fma2(acc[t][2 + (j & 1)],
-                     pack2(twice_relu(__uint_as_float(v[t][4 * j + 2])),
-                           twice_relu(__uint_as_float(v[t][4 * j + 3]))),
-                     wj[j].y);
+                for (int t = 0; t < kSlotTiles; ++t) {
+                  fma2(acc[t][j & 1],
+                       pack2(relu_nan(__uint_as_float(v[t][4 * j])),
+                             relu_nan(__uint_as_float(v[t][4 * j + 1]))),
+                       wj[j].x);
+                  fma2(acc[t][2 + (j & 1)],
+                       pack2(twice_relu(__uint_as_float(v[t][4 * j + 2])),
+                             twice_relu(__uint_as_float(v[t][4 * j + 3]))),
+                       wj[j].y);
+                }
               }
             }
+#pragma unroll
+            for (int t = 0; t < kSlotTiles; ++t)
+              score[u * kSlotTiles + t] = fmaf(sum2(acc[t][2]) + sum2(acc[t][3]), 0.5f,
+                                               sum2(acc[t][0]) + sum2(acc[t][1]));
+          }
+          if (!ok) break;
+#pragma unroll
+          for (int t = 0; t < kStepTiles; ++t) {
+            const uint32_t mask =
+                ld_shared_u32(base + ((step_no * kStepTiles + t) % kMaskRing * 4 + quad) * 4);
+            const bool real =
+                pos + t < seen && (mask >> lane & 1u) && score[t] == score[t];
+            score[t] = real ? score[t] + 0.f : -INFINITY;
           }
           float* row = out + i * p.s.score_stride;
-          const uint32_t masks = base + kMasks + quad * 4;
-          uint32_t mask[kTiles];
-#pragma unroll
-          for (int t = 0; t < kTiles; ++t)
-            mask[t] = ld_shared_u32(masks + ((step_no * kTiles + t) % kMaskRing) * 16);
-#pragma unroll
-          for (int t = 0; t < kTiles; ++t) {
-            float score =
-                fmaf(sum2(acc[t][2]) + sum2(acc[t][3]), 0.5f, sum2(acc[t][0]) + sum2(acc[t][1]));
-            const int32_t pos = pos0 + t * kScoreTile;
-            const bool live = pos < seen;
-            score = live && (mask[t] >> lane & 1u) && score == score ? score + 0.f : -INFINITY;
-            if (granule > 1) {
+          const bool live = pos < seen;  // the row has room for both positions
+          if (granule == 1) {
+            if (live) *reinterpret_cast<float2*>(row + pos) = make_float2(score[0], score[1]);
+          } else {
+            float m = fmaxf(score[0], score[1]);
 #pragma unroll 1
-              for (int s = 1; s < granule; s <<= 1)
-                score = fmaxf(score, __shfl_xor_sync(0xffffffffu, score, s));
-            }
-            if (live && (pos & (granule - 1)) == 0) row[pos >> shift] = score;
+            for (int s = 1; s < granule / 2; s <<= 1)
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+            if (live && (pos & (granule - 1)) == 0) row[pos >> shift] = m;
           }
         }
-        next = i - walk.count;
+        if (set < kSets) next = i - walk.count;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(Bars::kQEmpty, buf));
@@ -502,7 +547,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     bool more = true;
     auto fetch = [&](Entry& e) {
       if (more && step == walk.t1) {
-        more = walk.next<kStep>(p);
+        more = walk.next(p);
         step = walk.t0;
       }
       e.page = -1;
@@ -512,17 +557,17 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       const int32_t pos = step * kStep + lane * p.seg_rows;
       if (lane < segs && pos < walk.most) {
         const int32_t lb = pos >> p.page_shift;
-        e.row = pos - (lb << p.page_shift);
+        e.row = (pos - (lb << p.page_shift)) / 2;  // a line holds two
         e.page = __ldg(p.s.block_table + static_cast<int64_t>(walk.seq) * p.s.max_blocks + lb);
       }
       ++step;
     };
     const bool issuer = elect_one();
-    // piece i's rows go to row i * seg_rows of the step's tiles
     const uint32_t piece = static_cast<uint32_t>(p.seg_rows) * kIndexCodes;
     Entry e0, e1, e2;
     e0.live = e1.live = false;
-    uint32_t it = 0;
+    Ring at(p.stages);
+    uint32_t issued = 0;
     bool ok = true;
 #pragma unroll 1
     for (int ahead = 2; ahead > 0 || e0.live;) {  // pages are looked up two steps ahead
@@ -533,47 +578,59 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
         e1 = e2;
         continue;
       }
-      const uint32_t stage = it % kStages;
-      ok = warp_wait(bar(Bars::kEmpty, stage), ((it / kStages) & 1u) ^ 1u, abort_addr, lim);
+      ok = warp_wait(bar(Bars::kEmpty, at.stage), at.phase ^ 1u, abort_addr, lim);
       if (!ok) break;
-      const uint32_t full = bar(Bars::kFull, stage);
-      if (issuer) mbar_arrive_tx(full, kTiles * kTileCodes);
+      const uint32_t full = bar(Bars::kFull, at.stage);
+      if (issuer) mbar_arrive_tx(full, kStepCodes);
       // a page that does not resolve: past the pool, zeros
       const int32_t page =
           static_cast<uint32_t>(e0.page) < static_cast<uint32_t>(past) ? e0.page : past;
-      uint32_t dst = base + stage * kStageBytes;
+      const uint32_t dst = stage0 + at.stage * kStageBytes;
 #pragma unroll 1
-      for (int i = 0; i < segs; ++i) {
-        const int32_t z = __shfl_sync(0xffffffffu, page, i);
-        const int32_t y = __shfl_sync(0xffffffffu, e0.row, i);
-        if (issuer) tma_load_3d(dst, &codes_map, y, z, full);
-        dst += piece;
-        if (kTiles > 1 && (i + 1) * p.seg_rows == kScoreTile) dst += kTileScales;
+      for (int i0 = 0; i0 < segs; i0 += 4) {
+        int32_t z[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          z[i] = __shfl_sync(0xffffffffu, page, i0 + i);
+          y[i] = __shfl_sync(0xffffffffu, e0.row, i0 + i);
+        }
+        if (issuer) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (i0 + i < segs) tma_load_3d(dst + (i0 + i) * piece, &codes_map, y[i], z[i], full);
+          }
+        }
+        __syncwarp();
       }
       e0 = e1;
       e1 = e2;
-      ++it;
+      at.advance(1);
+      ++issued;
     }
     __syncwarp();
     if (!ok) {
       // Copies in flight land before the CTA ends: this lane stands in for the
       // scale warps on stages that they have left.
 #pragma unroll 1
-      for (uint32_t k = it > kStages ? it - kStages : 0; k < it; ++k) {
-        if (lane == 0) mbar_arrive(bar(Bars::kFull, k % kStages));
-        drain(bar(Bars::kFull, k % kStages), (k / kStages) & 1u);
+      for (uint32_t k = min(issued, static_cast<uint32_t>(p.stages)); k > 0; --k) {
+        at.back();
+        if (lane == 0) mbar_arrive(bar(Bars::kFull, at.stage));
+        drain(bar(Bars::kFull, at.stage), at.phase);
       }
     }
   } else if (p.seg_rows > 0 && warp < kScaleWarp0 + kScaleWarps) {
     // ----------------------------------------------- scales, tensor copies
-    // Lane l has rows l, l + 32, .. of the step: their scales are one 16-byte
-    // line of each K half's layout.
-    constexpr int kRows = kStep / 32;
+    // Lane l has lines l, l + 32, .. of the step: the scales of each tile's
+    // rows l, l + 32, .. are one 16-byte line of each K half's layout.
+    constexpr int kLines = kScoreTile / 32;
     const bool issuer = elect_one();
-    const int64_t scale_at = static_cast<int64_t>(p.s.page_size) * kIndexCodes;
+    const uint8_t* scales = p.s.cache + static_cast<int64_t>(p.s.page_size) * kIndexCodes;
+    const uint32_t stride = static_cast<uint32_t>(p.s.block_stride);
+    const uint32_t in_page = static_cast<uint32_t>(p.s.page_size) - 1;
     struct Turn {  // a step of this warp's
-      int32_t q, seq, most, step;
-      uint32_t it;
+      int32_t q, most, step;
+      uint32_t it;  // number of the step among the CTA's
+      uint32_t stage, phase;
       int32_t page;  // lane l: page l of those that the step touches, from `first` on
       int32_t first;
       bool live;
@@ -581,70 +638,84 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     const int32_t step_pages = max(kStep >> p.page_shift, 1);
     int32_t step = 0;
     int32_t it = 0, wait = warp - kScaleWarp0;  // steps until this warp's next
+    Ring at(p.stages);
     walk.t1 = 0;
     bool more = true;
     Turn then, now;
     then.live = now.live = false;
-    uint2 vals[kRows];    // now's scales, zeros for rows not in use
-    uint32_t valid = 0;   // bit i: row l + 32 i resolves
+    uint4 vals[kLines];   // now's scales, of an even and an odd position
+    uint32_t valid = 0;   // bit t + 2 i: position t of line l + 32 i resolves
     bool ok = true;
     // A turn's page ids are loaded two turns ahead, its scales one. Nothing is
     // in flight at the fence, which would wait for it.
 #pragma unroll 1
     for (int ahead = 2; ahead > 0 || now.live; --ahead) {
       if (ahead <= 0) {
-        const uint32_t stage = now.it % kStages;
-        ok = warp_wait(bar(Bars::kEmpty, stage), ((now.it / kStages) & 1u) ^ 1u, abort_addr, lim);
+        const uint32_t stage = now.stage;
+        ok = warp_wait(bar(Bars::kEmpty, stage), now.phase ^ 1u, abort_addr, lim);
         if (!ok) break;
-        TopByte top;
+        const bool whole = __all_sync(0xffffffffu, valid == (1u << 2 * kLines) - 1);
+        if (!whole) {
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-          const uint2* v = vals + 4 * t;
-          const uint32_t to = base + stage * kStageBytes + t * kTileBytes + kTileCodes + lane * 16;
-          st_shared_v4(to, v[0].x, v[1].x, v[2].x, v[3].x);
-          st_shared_v4(to + 512, v[0].y, v[1].y, v[2].y, v[3].y);
-          uint32_t mask[4];
+          for (int i = 0; i < kLines; ++i) {
+            if (!(valid >> 2 * i & 1u)) vals[i].x = vals[i].y = 0;
+            if (!(valid >> 2 * i & 2u)) vals[i].z = vals[i].w = 0;
+          }
+        }
+        const uint32_t to = stage0 + stage * kStageBytes + kStepCodes + lane * 16;
+        st_shared_v4(to, vals[0].x, vals[1].x, vals[2].x, vals[3].x);
+        st_shared_v4(to + 512, vals[0].y, vals[1].y, vals[2].y, vals[3].y);
+        st_shared_v4(to + 1024, vals[0].z, vals[1].z, vals[2].z, vals[3].z);
+        st_shared_v4(to + 1536, vals[0].w, vals[1].w, vals[2].w, vals[3].w);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            mask[i] = __ballot_sync(0xffffffffu, valid >> (4 * t + i) & 1u);
-            top.add(v[i].x);
-            top.add(v[i].y);
+        for (int t = 0; t < kStepTiles; ++t) {
+          uint32_t mask[kLines] = {~0u, ~0u, ~0u, ~0u};
+          if (!whole) {
+#pragma unroll
+            for (int i = 0; i < kLines; ++i)
+              mask[i] = __ballot_sync(0xffffffffu, valid >> (2 * i + t) & 1u);
           }
           if (issuer)
-            st_shared_v4(base + kMasks + ((now.it * kTiles + t) % kMaskRing) * 16, mask[0], mask[1],
+            st_shared_v4(base + (now.it * kStepTiles + t) % kMaskRing * 16, mask[0], mask[1],
                          mask[2], mask[3]);
         }
+        TopByte top;
+#pragma unroll
+        for (int i = 0; i < kLines; ++i)
+          top.add(vals[i].x), top.add(vals[i].y), top.add(vals[i].z), top.add(vals[i].w);
         fence_proxy_async_cta();
         __syncwarp();
         if (issuer) {  // into tensor memory; the stage is full when they are there
 #pragma unroll
-          for (int t = 0; t < kTiles; ++t)
+          for (int t = 0; t < kStepTiles; ++t)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-              copy_scales(tmem + kSfaCol + (stage * kTiles + t) * 8 + h * 4,
-                          scale_desc(base + stage * kStageBytes + t * kTileBytes + kTileCodes +
+              copy_scales(tmem + sfa_col + (stage * kStepTiles + t) * 8 + h * 4,
+                          scale_desc(stage0 + stage * kStageBytes + kStepCodes + t * kTileScales +
                                      h * 512));
           mma_commit(bar(Bars::kFull, stage));
         }
         const uint32_t most = top.of_warp();
-        if (lane < kTiles) p.s.smax[now.q * p.s.tiles + now.step * kTiles + lane] = most;
+        if (lane < kStepTiles) p.s.smax[now.q * p.s.tiles + now.step * kStepTiles + lane] = most;
       }
       // the next turn's scales
       now = then;
       if (now.live) {
         valid = 0;
+        // Positions that do not resolve or are not in use read some of page 0.
+        const uint32_t mine =
+            static_cast<uint32_t>(now.page) < static_cast<uint32_t>(p.s.num_blocks) ? now.page : ~0u;
+        const uint32_t pos0 = static_cast<uint32_t>(now.step) * kStep + 2 * lane;
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-          const int32_t pos = now.step * kStep + i * 32 + lane;
-          const int32_t lb = pos >> p.page_shift;
-          const int32_t page = __shfl_sync(0xffffffffu, now.page, lb - now.first);
-          vals[i] = make_uint2(0, 0);
-          if (pos < now.most && page >= 0 && page < p.s.num_blocks) {
-            valid |= 1u << i;
-            vals[i] = __ldg(reinterpret_cast<const uint2*>(
-                p.s.cache + page * p.s.block_stride + scale_at +
-                (pos - (lb << p.page_shift)) * kIndexScales));
-          }
+        for (int i = 0; i < kLines; ++i) {
+          const uint32_t pos = pos0 + i * 64;
+          const uint32_t page =
+              __shfl_sync(0xffffffffu, mine, (pos >> p.page_shift) - static_cast<uint32_t>(now.first));
+          const uint8_t* from = scales + static_cast<uint64_t>(page != ~0u ? page : 0u) * stride +
+                                (pos & in_page) * kIndexScales;
+          vals[i] = __ldg(reinterpret_cast<const uint4*>(from));
+          const uint32_t most = page != ~0u ? now.most : 0u;
+          valid |= (pos < most ? 1u << 2 * i : 0u) | (pos + 1 < most ? 2u << 2 * i : 0u);
         }
       }
       // the page ids of the one after it
@@ -652,20 +723,22 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       while (more) {
         const int32_t skip = min(wait, walk.t1 - step);
         step += skip, it += skip, wait -= skip;
+        at.advance(skip);
         if (step < walk.t1) break;
-        more = walk.next<kStep>(p);
+        more = walk.next(p);
         step = walk.t0;
       }
       then.live = more;
       if (more) {
-        then.q = walk.q, then.seq = walk.seq, then.most = walk.most;
-        then.step = step, then.it = it;
+        then.q = walk.q, then.most = walk.most;
+        then.step = step, then.it = it, then.stage = at.stage, then.phase = at.phase;
         then.first = (step * kStep) >> p.page_shift;
         then.page = -1;
         if (lane < step_pages && (then.first + lane) << p.page_shift < walk.most)
           then.page = __ldg(p.s.block_table + static_cast<int64_t>(walk.seq) * p.s.max_blocks +
                             then.first + lane);
         ++step, ++it, wait = kScaleWarps - 1;
+        at.advance(1);
       }
     }
     if (issuer) {  // scale copies of an aborted CTA have completed
@@ -675,8 +748,10 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     __syncwarp();
   } else if (warp < kLoadWarp0 + kLoadWarps) {
     // ---------------------------------------------- key loads, row by row
-    // Warp w has rows 32 w .. of each tile; a step's copies are one group.
-    constexpr int kInFlight = kStages - 2;
+    // Warp w has positions 64 w .. of a step, two a lane; a step's copies are
+    // one group.
+    constexpr int kInFlight = 2;
+    static_assert(stage_count(kMaxGroup) > kInFlight, "stages");
     const int part = warp - kLoadWarp0;
     int32_t step = 0;
     walk.t1 = 0;
@@ -684,13 +759,13 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     // Lane l keeps the run and step of the l-th step of every 32.
     int32_t info_q = 0, info_step = 0;
     struct Entry {
-      int32_t page[kTiles], row[kTiles];
+      int32_t page[2], row[2];
       bool live;
     };
     uint32_t fetched = 0;
     auto fetch = [&](Entry& e) {
       if (more && step == walk.t1) {
-        more = walk.next<kStep>(p);
+        more = walk.next(p);
         step = walk.t0;
       }
       e.live = more;
@@ -698,35 +773,40 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       if (lane == fetched % 32) info_q = walk.q, info_step = step;
       ++fetched;
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t) {
-        const int32_t pos = step * kStep + t * kScoreTile + part * 32 + lane;
+      for (int u = 0; u < 2; ++u) {
+        const int32_t pos = step * kStep + part * 64 + u * 32 + lane;
         const int32_t lb = pos / p.s.page_size;
-        e.row[t] = pos - lb * p.s.page_size;
-        e.page[t] = pos < walk.most
+        e.row[u] = pos - lb * p.s.page_size;
+        e.page[u] = pos < walk.most
                         ? __ldg(p.s.block_table +
                                 static_cast<int64_t>(walk.seq) * p.s.max_blocks + lb)
                         : -1;
       }
       ++step;
     };
-    auto publish = [&](uint32_t it) {  // this warp's rows of step `it` have landed
-      const uint32_t stage = it % kStages;
+    // Where the scales of this lane's position 32 u + lane of the part are.
+    auto scales_at = [&](uint32_t stage, int u) {
+      return stage0 + stage * kStageBytes + kStepCodes + (lane & 1) * kTileScales +
+             (u * 16 + (lane >> 1)) * 16 + part * 4;
+    };
+    Ring at(p.stages), done(p.stages);
+    auto publish = [&](uint32_t it) {  // this warp's positions of step `it` have landed
+      const uint32_t stage = done.stage;
+      done.advance(1);
       TopByte top;
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t) {
-        const uint32_t sc =
-            base + stage * kStageBytes + t * kTileBytes + kTileCodes + lane * 16 + part * 4;
-        top.add(ld_shared_u32(sc));
-        top.add(ld_shared_u32(sc + 512));
+      for (int u = 0; u < 2; ++u) {
+        top.add(ld_shared_u32(scales_at(stage, u)));
+        top.add(ld_shared_u32(scales_at(stage, u) + 512));
       }
       const uint32_t most = top.of_warp();
       const int32_t q = __shfl_sync(0xffffffffu, info_q, it % 32);
-      const int32_t at = __shfl_sync(0xffffffffu, info_step, it % 32) * kTiles;
+      const int32_t tile = __shfl_sync(0xffffffffu, info_step, it % 32) * kStepTiles;
       fence_proxy_async_cta();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(Bars::kFull, stage));
-      if (lane < kTiles)
-        reinterpret_cast<uint8_t*>(p.s.smax + q * p.s.tiles + at + lane)[part] =
+      if (lane < kStepTiles)
+        reinterpret_cast<uint8_t*>(p.s.smax + q * p.s.tiles + tile + lane)[part] =
             static_cast<uint8_t>(most);
     };
     Entry e0, e1, e2;
@@ -742,30 +822,36 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
         e1 = e2;
         continue;
       }
-      const uint32_t stage = it % kStages;
-      ok = warp_wait(bar(Bars::kEmpty, stage), ((it / kStages) & 1u) ^ 1u, abort_addr, lim);
+      const uint32_t stage = at.stage;
+      ok = warp_wait(bar(Bars::kEmpty, stage), at.phase ^ 1u, abort_addr, lim);
       if (!ok) break;
+      at.advance(1);
+      uint32_t found[2];
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t) {
-        const uint32_t dst = base + stage * kStageBytes + t * kTileBytes;
-        const bool live = e0.page[t] >= 0 && e0.page[t] < p.s.num_blocks;
-        const uint32_t mask = __ballot_sync(0xffffffffu, live);
-        if (lane == 0)
-          st_shared_u32(base + kMasks + (((it * kTiles + t) % kMaskRing) * 4 + part) * 4, mask);
-        const int64_t page = live ? e0.page[t] * p.s.block_stride : 0;
-        const int64_t codes = page + static_cast<int64_t>(e0.row[t]) * kIndexCodes;
+      for (int u = 0; u < 2; ++u) {
+        const bool live = e0.page[u] >= 0 && e0.page[u] < p.s.num_blocks;
+        found[u] = __ballot_sync(0xffffffffu, live);
+        const int64_t page = live ? e0.page[u] * p.s.block_stride : 0;
+        const int64_t codes = page + static_cast<int64_t>(e0.row[u]) * kIndexCodes;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // eight rows each, four lanes a row
+        for (int i = 0; i < 4; ++i) {  // eight positions each, four lanes a position
           const int r = i * 8 + (lane >> 2);
-          const int64_t at = __shfl_sync(0xffffffffu, codes, r);
-          cp_async16_z(dst + sw64_off(part * 32 + r, lane & 3), p.s.cache + at + (lane & 3) * 16,
-                       (mask >> r) & 1u);
+          const int64_t from = __shfl_sync(0xffffffffu, codes, r);
+          cp_async16_z(stage0 + stage * kStageBytes + code_off(part * 64 + u * 32 + r, lane & 3),
+                       p.s.cache + from + (lane & 3) * 16, (found[u] >> r) & 1u);
         }
         const uint8_t* sc = p.s.cache + page + static_cast<int64_t>(p.s.page_size) * kIndexCodes +
-                            static_cast<int64_t>(e0.row[t]) * kIndexScales;
-        const uint32_t sd = dst + kTileCodes + lane * 16 + part * 4;
-        cp_async4_z(sd, sc, live);
-        cp_async4_z(sd + 512, sc + 4, live);
+                            static_cast<int64_t>(e0.row[u]) * kIndexScales;
+        cp_async4_z(scales_at(stage, u), sc, live);
+        cp_async4_z(scales_at(stage, u) + 512, sc + 4, live);
+      }
+#pragma unroll
+      for (int t = 0; t < kStepTiles; ++t) {  // lane l: position 2 l + t of the part
+        const uint32_t x = 2 * lane + t;
+        const uint32_t mask =
+            __ballot_sync(0xffffffffu, (x < 32 ? found[0] : found[1]) >> (x & 31u) & 1u);
+        if (lane == 0)
+          st_shared_u32(base + ((it * kStepTiles + t) % kMaskRing * 4 + part) * 4, mask);
       }
       cp_async_commit();
       if (it >= kInFlight) {
@@ -784,11 +870,12 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   } else if (warp == kScoreMmaWarp) {
     // ---------------------------------------------------------- MMA issue
     constexpr uint32_t idesc = score_idesc(kHeads);
-    uint32_t it = 0, run = 0, slot = 0, phase = 0;
+    uint32_t run = 0, slot = 0, phase = 0;
+    Ring at(p.stages);
     bool ok = true;
     const bool issuer = elect_one();
 #pragma unroll 1
-    while (ok && walk.next<kStep>(p)) {
+    while (ok && walk.next(p)) {
       const int buf = run & 1;
       ok = warp_wait(bar(Bars::kQFull, buf), (run >> 1) & 1u, abort_addr, lim);
       if (!ok) break;
@@ -802,38 +889,43 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
                         scale_desc(q_scales(buf) + i * kTileScales + h * 512));
         const uint64_t q0 = sw64_desc(q_codes(buf));
 #pragma unroll 1
-        for (int32_t step = walk.t0; ok && step < walk.t1; ++step, ++it) {
-          const uint32_t stage = it % kStages;
-          ok = wait_bar(bar(Bars::kFull, stage), (it / kStages) & 1u, abort_addr, lim);
+        for (int32_t step = walk.t0; ok && step < walk.t1; ++step) {
+          const uint32_t stage = at.stage;
+          ok = wait_bar(bar(Bars::kFull, stage), at.phase, abort_addr, lim);
           if (!ok) break;
+          at.advance(1);
           tc_fence_after();
-          const uint32_t src = base + stage * kStageBytes;
-          const uint32_t sfa = tmem + kSfaCol + stage * kTiles * 8;
+          const uint32_t src = stage0 + stage * kStageBytes;
+          const uint32_t sfa = tmem + sfa_col + stage * kStepTiles * 8;
           if (p.seg_rows == 0) {  // copies row by row: the scales are still in shared memory
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
-              copy_scales(sfa + 8 * t, scale_desc(src + t * kTileBytes + kTileCodes));
-              copy_scales(sfa + 8 * t + 4, scale_desc(src + t * kTileBytes + kTileCodes + 512));
-            }
+            for (int x = 0; x < 2 * kStepTiles; ++x)
+              copy_scales(sfa + 4 * x, scale_desc(src + kStepCodes + 512 * x));
           }
-          const uint64_t a = sw64_desc(src);
+          const uint64_t a = sw128_desc(src);
 #pragma unroll 1
           for (int i = 0; i < walk.count; ++i) {
-            ok = wait_bar(bar(Bars::kDEmpty, slot), phase ^ 1u, abort_addr, lim);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t d = tmem + slot * kSlotCols;
-            // a descriptor's address counts 16 bytes; a K step is 32 bytes
+            // a descriptor's address counts 16 bytes; a K step is 32 bytes, and
+            // a tile's rows are one half of the 128-byte lines
             const uint64_t b = q0 + i * (kHeads * kIndexCodes / 16);
             const uint32_t sfb = tmem + kSfbCol + i * 8;
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
-              const uint64_t at = a + t * (kTileBytes / 16);
-              mma_fp4(d + t * kHeads, at, b, idesc, sfa + 8 * t, sfb, 0);
-              mma_fp4(d + t * kHeads, at + 2, b + 2, idesc, sfa + 8 * t + 4, sfb + 4, 1);
+            for (int u = 0; u < kUnitSlots; ++u) {
+              ok = wait_bar(bar(Bars::kDEmpty, slot), phase ^ 1u, abort_addr, lim);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t d = tmem + slot * kSlotCols;
+#pragma unroll
+              for (int t = 0; t < kSlotTiles; ++t) {
+                const int tile = u * kSlotTiles + t;
+                mma_fp4(d + t * kHeads, a + 4 * tile, b, idesc, sfa + 8 * tile, sfb, 0);
+                mma_fp4(d + t * kHeads, a + 4 * tile + 2, b + 2, idesc, sfa + 8 * tile + 4, sfb + 4,
+                        1);
+              }
+              mma_commit(bar(Bars::kDFull, slot));
+              if (++slot == kSlots) slot = 0, phase ^= 1u;
             }
-            mma_commit(bar(Bars::kDFull, slot));
-            if (++slot == kSlots) slot = 0, phase ^= 1u;
+            if (!ok) break;
           }
           mma_commit(bar(Bars::kEmpty, stage));
         }
@@ -848,13 +940,13 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       drain(bar(Bars::kDrain, 0), 0);
     }
     __syncwarp();
-  } else {
+  } else if (warp >= kQWarp0) {
     // ----------------------------------------------------- encode queries
-    const int qt = (warp == kQWarp0 ? 0 : warp - kQWarp0 - 1) * 32 + lane;
+    const int qt = tid - kQWarp0 * 32;
     uint32_t run = 0;
     bool ok = true;
 #pragma unroll 1
-    while (ok && walk.next<kStep>(p)) {
+    while (ok && walk.next(p)) {
       const int buf = run & 1;
       ok = warp_wait(bar(Bars::kQEmpty, buf), ((run >> 1) & 1u) ^ 1u, abort_addr, lim);
       if (!ok) break;
@@ -894,33 +986,34 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   if (tid == 0) p.s.status[blockIdx.x] = ld_shared_u32(abort_addr);
 }
 
-// The pool's codes as rows of 64 bytes, in 64-byte swizzle; false where the
-// page size is no power of two or below 8: a tile of 128 positions is then not
-// made of pieces of pages with whole 8-row groups.
+// The pool's codes as lines of 128 bytes (two rows), in 128-byte swizzle; false
+// where the page size is no power of two or below 16: a step is then not made
+// of pieces of pages with whole groups of eight lines.
 bool codes_tensor(const SelectParams& s, CUtensorMap* map, int32_t* seg_rows) {
   const int32_t P = s.page_size;
   *seg_rows = 0;
-  if (P < 8 || (P & (P - 1)) != 0) return false;
+  if (P < 16 || (P & (P - 1)) != 0) return false;
   EncodeTiledFn enc = encode_tiled();
-  if (enc == nullptr || s.num_blocks >= INT32_MAX || s.block_stride >= (int64_t{1} << 40))
-    return false;
-  const cuuint32_t rows = static_cast<cuuint32_t>(P < kScoreTile ? P : kScoreTile);
-  const cuuint64_t dims[3] = {kIndexCodes, static_cast<cuuint64_t>(P),
+  if (enc == nullptr || s.num_blocks >= INT32_MAX || s.block_stride > UINT32_MAX) return false;
+  const int32_t rows = P < kStep ? P : kStep;
+  const cuuint64_t dims[3] = {2 * kIndexCodes, static_cast<cuuint64_t>(P / 2),
                               static_cast<cuuint64_t>(s.num_blocks)};
-  const cuuint64_t strides[2] = {kIndexCodes, static_cast<cuuint64_t>(s.block_stride)};
-  const cuuint32_t box[3] = {kIndexCodes, rows, 1};
+  const cuuint64_t strides[2] = {2 * kIndexCodes, static_cast<cuuint64_t>(s.block_stride)};
+  const cuuint32_t box[3] = {2 * kIndexCodes, static_cast<cuuint32_t>(rows / 2), 1};
   const cuuint32_t es[3] = {1, 1, 1};
   if (enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(s.cache), dims, strides, box,
-          es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+          es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return false;
-  *seg_rows = static_cast<int32_t>(rows);
+  *seg_rows = rows;
   return true;
 }
 
 template <int kChunks>
 int32_t launch_chunks(const ScoreParams& p, const CUtensorMap& map, cudaStream_t stream) {
-  const size_t smem = kQBase + 2 * static_cast<size_t>(q_buffer_bytes(32 * kChunks, p.group));
+  const size_t smem = kStageBase +
+                      static_cast<size_t>(p.stages) * kStageBytes +
+                      2 * static_cast<size_t>(q_buffer_bytes(32 * kChunks, p.group));
   if (cudaFuncSetAttribute(score_kernel<kChunks>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem)) != cudaSuccess) {
     cudaGetLastError();
@@ -940,6 +1033,7 @@ int32_t launch_scores(SelectParams& s, int num_sms, cudaStream_t stream) {
   const int32_t mean = s.num_q / s.num_seqs;
   const int32_t most = max_group(chunks);
   p.group = s.group = mean < 1 ? 1 : mean > most ? most : mean;
+  p.stages = stage_count(p.group);
   p.ctas = s.score_ctas = num_sms < kStatusWords ? num_sms : kStatusWords;
   p.s = s;
   CUtensorMap map;
