@@ -27,15 +27,18 @@
 //   warps 0-11   epilogue: three sets of four; a set takes every third
 //                (step, query token) unit, warp w the rows 32 (w % 4).. of both
 //                tiles (more than 64 heads: two sets, one tile after the other)
-//   warp 12      copies the steps' codes: resolves the pages through the block
-//                table (two steps ahead), one tensor copy per page, swizzled on
-//                the way; all stages in flight
-//   warps 13-16  take turns in loading a step's scales (one turn ahead) and
+//   warps 12, 13 copy the codes of every other step: resolve the pages through
+//                the block table (two turns ahead), one tensor copy per page,
+//                swizzled on the way; all stages in flight
+//   warps 14-17  take turns in loading a step's scales (one turn ahead) and
 //                laying them out in tensor memory
 //   (page sizes that are no power of two or below 16: warps 12-15 copy row by row
 //   with cp.async instead)
-//   warp 17      issues the MMAs
-//   warps 18, 19  encode the next run's queries
+//   warps 18, 19 issue the MMAs of every other step (more than 64 heads: warp 18
+//                alone); warp 18 copies the next run's queries meanwhile
+//
+// A first kernel encodes the queries, once for all CTAs that score a run, into
+// images of what the MMAs and the epilogue read of them.
 //
 // Every wait is bounded; when one runs out the CTA's roles unwind, what is in
 // flight is drained, and the CTA's status word says so.
@@ -51,14 +54,13 @@ namespace {
 constexpr int kScoreThreads = 640;
 constexpr int kEpiWarps = 12;
 constexpr int kLoadWarp0 = 12, kLoadWarps = 4;
-constexpr int kScaleWarp0 = 13, kScaleWarps = 4;  // with tensor copies
-constexpr int kScoreMmaWarp = 17;                 // not on the loads' sub-partition
-constexpr int kQWarp0 = 18, kQWarps = 2;
+constexpr int kCopyWarps = 2, kScaleWarp0 = 14, kScaleWarps = 4;  // with tensor copies
+constexpr int kMmaWarp0 = 18;
 constexpr int kMaxStages = 7;     // steps in shared memory
 // Resolved-position masks of the last tiles; more than there can be between a
 // step's scales and its epilogue (the stages and the accumulator slots).
 constexpr int kMaskRing = 32;
-constexpr int kMaxGroup = 8;      // query tokens of a run
+constexpr int kMaxGroup = 4;      // query tokens of a run
 constexpr int kStep = 256;                             // positions
 constexpr int kStepTiles = kStep / kScoreTile;         // 2
 constexpr int kStepCodes = kStep * kIndexCodes;        // 128 lines of 128 bytes, 128-byte swizzle
@@ -68,13 +70,16 @@ constexpr int kMaskBytes = kMaskRing * 4 * 4;
 // A run's cost per step: its query tokens' epilogues and the step's load.
 constexpr int kLoadCost = 2;
 // Tensor memory columns: accumulator slots, then scales of Q (eight per query
-// token of a run), then of K (eight per tile of a stage).
+// token of a run, a set for each MMA warp), then of K (eight per tile of a
+// stage).
 constexpr uint32_t kSfbCol = 384;
 // Stages of a run's length: what tensor memory holds scales for. A stage's
 // round (copies under way, MMAs, release) takes several thousand cycles, so
 // the copies in flight set the rate.
-__host__ __device__ constexpr int stage_count(int group) {
-  return (static_cast<int>(kTmemCols - kSfbCol) / 8 - group) / kStepTiles;
+__host__ __device__ constexpr int mma_warps(int chunks) { return chunks <= 2 ? 2 : 1; }
+__host__ __device__ constexpr int stage_count(int chunks, int group) {
+  const int n = (static_cast<int>(kTmemCols - kSfbCol) / 8 - mma_warps(chunks) * group) / kStepTiles;
+  return n < kMaxStages ? n : kMaxStages;
 }
 
 // Instruction descriptor, kind::mxf4nvf4: E2M1 A (bit 7) and B (bit 10), both
@@ -84,14 +89,14 @@ __host__ __device__ constexpr uint32_t score_idesc(int n) {
 }
 // For `chunks` of 32 heads: tiles of an accumulator slot, slots, and sets of
 // epilogue warps. A set waits for a slot's phase by its parity, so it must not
-// come to a slot before the slot's last content is there: with s sets, the
+// come to a slot before the slot's last content is there: a slot is one set's
+// (64 heads or fewer), or units complete in order and, with s sets, the
 // contents of the s - 1 units between two of its own fit into the slots.
 __host__ __device__ constexpr int slot_tiles(int chunks) { return chunks <= 2 ? 2 : 1; }
 __host__ __device__ constexpr int acc_slots(int chunks) {
   return 384 / (32 * chunks * slot_tiles(chunks));
 }
 __host__ __device__ constexpr int epi_sets(int chunks) { return chunks <= 2 ? 3 : 2; }
-__host__ __device__ constexpr int max_group(int chunks) { return chunks <= 2 ? kMaxGroup : 4; }
 
 // K-major operand with 64-byte rows in 64-byte swizzle: 8-row groups of 512 bytes.
 __device__ __forceinline__ uint64_t sw64_desc(uint32_t addr) {
@@ -209,7 +214,7 @@ struct Bars {  // byte offsets in the control block
   static constexpr int kFull = 0, kEmpty = kFull + 8 * kMaxStages,
                        kDFull = kEmpty + 8 * kMaxStages,
                        kDEmpty = kDFull + 64, kQFull = kDEmpty + 64, kQEmpty = kQFull + 16,
-                       kDrain = kQEmpty + 16, kScaleDrain = kDrain + 8,
+                       kDrain = kQEmpty + 16, kTurn = kDrain + 16, kScaleDrain = kTurn + 16,
                        kTmem = kScaleDrain + 8 * kScaleWarps, kAbort = kTmem + 4,
                        kStart = kAbort + 4, kEnd = kStart + 32;
 };
@@ -217,8 +222,39 @@ static_assert(Bars::kStart % 8 == 0, "start words");
 constexpr int kCtl = kMaskBytes;  // the control block follows the masks
 constexpr int kStageBase = (kCtl + Bars::kEnd + 1023) / 1024 * 1024;  // stages, then two Q buffers
 
-__host__ __device__ constexpr int q_buffer_bytes(int heads_pad, int group) {
-  return (group * (heads_pad * kIndexCodes + kTileScales + heads_pad * 4) + 1023) / 1024 * 1024;
+constexpr int kImageLine = 512;  // images as lines, for tensor copies
+// A query token's image: codes in 64-byte swizzle, scales, weights (zeros past
+// num_heads), whole swizzle atoms.
+__host__ __device__ constexpr int image_scales(int heads_pad) { return heads_pad * kIndexCodes; }
+__host__ __device__ constexpr int image_weights(int heads_pad) {
+  return image_scales(heads_pad) + kTileScales;
+}
+__host__ __device__ constexpr int image_bytes(int heads_pad) {
+  return (image_weights(heads_pad) + heads_pad * 4 + kImageLine - 1) / kImageLine * kImageLine;
+}
+
+// One thread per group of 16 values; a CTA per query token.
+__global__ void __launch_bounds__(NVFP4_MLA_MAX_HEADS* kIndexScales)
+    encode_kernel(const uint8_t* __restrict__ q_index, const float* __restrict__ weights,
+                  int32_t num_heads, int32_t heads_pad, uint8_t* __restrict__ images) {
+  cudaTriggerProgrammaticLaunchCompletion();
+  const int64_t t = blockIdx.x;
+  const int g = threadIdx.x % kIndexScales, h = threadIdx.x / kIndexScales;
+  uint32_t lo = 0, hi = 0, sc = 0;
+  float weight = 0.f;
+  if (h < num_heads) {
+    const int64_t head = t * num_heads + h;
+    const uint8_t* src = q_index + head * (kIndexDim * 2) + g * (2 * kGroup);
+    const uint4 a = ld_nc_v4(src), b = ld_nc_v4(src + 16);
+    const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    float s;
+    sc = quantize_group(v, lo, hi, s);
+    if (g == 0) weight = __ldg(weights + head);
+  }
+  uint8_t* image = images + t * image_bytes(heads_pad);
+  *reinterpret_cast<uint2*>(image + sw64_off(h, g >> 1) + (g & 1) * 8) = make_uint2(lo, hi);
+  image[image_scales(heads_pad) + scale_off(h, g)] = static_cast<uint8_t>(sc);
+  if (g == 0) *reinterpret_cast<float*>(image + image_weights(heads_pad) + h * 4) = weight;
 }
 
 struct ScoreParams {
@@ -230,6 +266,15 @@ struct ScoreParams {
   int32_t page_shift;  // log2 of the page size (tensor copies)
 };
 
+// one box of a 2-D tensor map at (x, y)
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* tm, int32_t x,
+                                            int32_t y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
 // one box of a 3-D tensor map at (0, y, z)
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm, int32_t y,
                                             int32_t z, uint32_t bar) {
@@ -322,9 +367,37 @@ struct Walk {
   }
 };
 
+// One of `warps` warps that take turns at a CTA's steps.
+struct Turns {
+  int32_t step = 0, wait, stride;  // wait: steps until this warp's next
+  uint32_t it = 0;                 // number of the step among the CTA's
+  Ring at;
+  __device__ __forceinline__ Turns(int32_t first, int32_t warps, uint32_t stages)
+      : wait(first), stride(warps), at(stages) {}
+  // Goes on to this warp's next step; false when there is none. Before the
+  // first call walk.t1 is 0.
+  __device__ __forceinline__ bool next(Walk& walk, const ScoreParams& p) {
+#pragma unroll 1
+    while (true) {
+      const int32_t skip = min(wait, walk.t1 - step);
+      step += skip, it += skip, wait -= skip;
+      at.advance(skip);
+      if (step < walk.t1) return true;
+      if (!walk.next(p)) return false;
+      step = walk.t0;
+    }
+  }
+  __device__ __forceinline__ void done() {
+    ++step, ++it, wait = stride - 1;
+    at.advance(1);
+  }
+};
+
 template <int kChunks>
 __global__ void __launch_bounds__(kScoreThreads, 1)
-    score_kernel(const __grid_constant__ ScoreParams p, const __grid_constant__ CUtensorMap codes_map) {
+    score_kernel(const __grid_constant__ ScoreParams p,
+                 const __grid_constant__ CUtensorMap codes_map,
+                 const __grid_constant__ CUtensorMap image_map) {
   constexpr int kHeads = 32 * kChunks;
   constexpr int kSlots = acc_slots(kChunks);
   constexpr int kSlotTiles = slot_tiles(kChunks);
@@ -332,6 +405,10 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   constexpr int kUnitSlots = kStepTiles / kSlotTiles;  // a unit is a step and a query token
   static_assert(kSlots >= (kSets - 1) * kUnitSlots + 1 && 4 * kSets <= kEpiWarps, "slots");
   constexpr uint32_t kSlotCols = kSlotTiles * kHeads;
+  constexpr int kMmaWarps = mma_warps(kChunks);
+  // with two issuing threads, whose MMAs need not complete in order
+  static_assert(kMmaWarps == 1 || kSlots % kSets == 0, "slots of one set each");
+  constexpr uint32_t kImage = image_bytes(kHeads);
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
   const uint32_t stage0 = base + kStageBase;
@@ -340,9 +417,6 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   auto bar = [ctl](int kind, int i) { return ctl + static_cast<uint32_t>(kind + 8 * i); };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long lim = p.s.wait_cycles;
-  // The selection may take the SMs that fall idle; it waits for this grid.
-  cudaTriggerProgrammaticLaunchCompletion();
-
   // ---- this CTA's part of the list
   __shared__ int64_t warp_cost[kScoreThreads / 32];
   const int32_t groups = (p.s.num_q + p.group - 1) / p.group;
@@ -384,10 +458,13 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     }
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(Bars::kQFull, i), kQWarps);
-      mbar_init(bar(Bars::kQEmpty, i), kEpiWarps + 1);
+      mbar_init(bar(Bars::kQFull, i), 1);
+      mbar_init(bar(Bars::kQEmpty, i), kEpiWarps + kMmaWarps);
     }
-    mbar_init(bar(Bars::kDrain, 0), 1);
+    for (int i = 0; i < kMmaWarps; ++i) {
+      mbar_init(bar(Bars::kDrain, i), 1);
+      mbar_init(bar(Bars::kTurn, i), 1);
+    }
 #pragma unroll 1
     for (int i = 0; i < kScaleWarps; ++i) mbar_init(bar(Bars::kScaleDrain, i), 1);
     st_shared_u32(abort_addr, 0);
@@ -420,7 +497,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       at += cost;
     });
   }
-  if (warp == kScoreMmaWarp) tmem_alloc(ctl + Bars::kTmem);
+  if (warp == kMmaWarp0) tmem_alloc(ctl + Bars::kTmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -428,12 +505,14 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   Walk walk;
   walk.begin(p, *part);
 
-  const int q_bytes = q_buffer_bytes(kHeads, p.group);
+  // The queries are encoded; the selection may take the SMs that fall idle (it
+  // waits for this grid).
+  cudaGridDependencySynchronize();
+  cudaTriggerProgrammaticLaunchCompletion();
+
   const uint32_t q_base = stage0 + p.stages * kStageBytes;
-  const uint32_t sfa_col = kSfbCol + 8 * p.group;
-  auto q_codes = [&](int buf) { return q_base + buf * q_bytes; };
-  auto q_scales = [&](int buf) { return q_codes(buf) + p.group * kHeads * kIndexCodes; };
-  auto q_weights = [&](int buf) { return q_scales(buf) + p.group * kTileScales; };
+  const uint32_t sfa_col = kSfbCol + 8 * kMmaWarps * p.group;
+  auto q_image = [&](int buf) { return q_base + static_cast<uint32_t>(buf * p.group) * kImage; };
 
   if (warp < kEpiWarps) {
     // ------------------------------------------------------------ epilogue
@@ -449,7 +528,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       const int buf = run & 1;
       ok = warp_wait(bar(Bars::kQFull, buf), (run >> 1) & 1u, abort_addr, lim);
       float* out = p.s.scores + walk.q * p.s.score_stride;
-      const uint8_t* weights = smem + (q_weights(buf) - base);
+      const uint8_t* weights = smem + (q_image(buf) - base) + image_weights(kHeads);
 #pragma unroll 1
       for (int32_t step = walk.t0; ok && step < walk.t1; ++step, ++step_no, first += walk.count) {
         const int32_t pos = step * kStep + 2 * (static_cast<int32_t>(quad) * 32 + lane);
@@ -457,7 +536,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
 #pragma unroll 1
         for (; i < walk.count; i += kSets) {
           const int32_t seen = __shfl_sync(0xffffffffu, walk.seen, i);
-          const auto* w = reinterpret_cast<const ulonglong2*>(weights + i * kHeads * 4);
+          const auto* w = reinterpret_cast<const ulonglong2*>(weights + i * kImage);
           float score[kStepTiles];  // of positions pos, pos + 1
 #pragma unroll
           for (int u = 0; u < kUnitSlots; ++u) {
@@ -534,7 +613,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       if (lane == 0) mbar_arrive(bar(Bars::kQEmpty, buf));
       ++run;
     }
-  } else if (p.seg_rows > 0 && warp == kLoadWarp0) {
+  } else if (p.seg_rows > 0 && warp < kLoadWarp0 + kCopyWarps) {
     // ------------------------------------------------ codes, tensor copies
     const int segs = kStep / p.seg_rows;  // lane i resolves and copies piece i of a step
     const int32_t past = static_cast<int32_t>(p.s.num_blocks);
@@ -542,36 +621,30 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       int32_t page, row;
       bool live;
     };
-    int32_t step = 0;
+    Turns turns(warp - kLoadWarp0, kCopyWarps, p.stages);
     walk.t1 = 0;
-    bool more = true;
-    auto fetch = [&](Entry& e) {
-      if (more && step == walk.t1) {
-        more = walk.next(p);
-        step = walk.t0;
-      }
-      e.page = -1;
-      e.row = 0;
-      e.live = more;
-      if (!more) return;
-      const int32_t pos = step * kStep + lane * p.seg_rows;
-      if (lane < segs && pos < walk.most) {
-        const int32_t lb = pos >> p.page_shift;
-        e.row = (pos - (lb << p.page_shift)) / 2;  // a line holds two
-        e.page = __ldg(p.s.block_table + static_cast<int64_t>(walk.seq) * p.s.max_blocks + lb);
-      }
-      ++step;
-    };
     const bool issuer = elect_one();
     const uint32_t piece = static_cast<uint32_t>(p.seg_rows) * kIndexCodes;
     Entry e0, e1, e2;
     e0.live = e1.live = false;
     Ring at(p.stages);
+    at.advance(warp - kLoadWarp0);
     uint32_t issued = 0;
     bool ok = true;
 #pragma unroll 1
-    for (int ahead = 2; ahead > 0 || e0.live;) {  // pages are looked up two steps ahead
-      fetch(e2);
+    for (int ahead = 2; ahead > 0 || e0.live;) {  // pages are looked up two turns ahead
+      e2.page = -1;
+      e2.row = 0;
+      e2.live = turns.next(walk, p);
+      if (e2.live) {
+        const int32_t pos = turns.step * kStep + lane * p.seg_rows;
+        if (lane < segs && pos < walk.most) {
+          const int32_t lb = pos >> p.page_shift;
+          e2.row = (pos - (lb << p.page_shift)) / 2;  // a line holds two
+          e2.page = __ldg(p.s.block_table + static_cast<int64_t>(walk.seq) * p.s.max_blocks + lb);
+        }
+        turns.done();
+      }
       if (ahead > 0) {
         --ahead;
         e0 = e1;
@@ -604,16 +677,15 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       }
       e0 = e1;
       e1 = e2;
-      at.advance(1);
+      at.advance(kCopyWarps);
       ++issued;
     }
     __syncwarp();
     if (!ok) {
       // Copies in flight land before the CTA ends: this lane stands in for the
       // scale warps on stages that they have left.
-#pragma unroll 1
-      for (uint32_t k = min(issued, static_cast<uint32_t>(p.stages)); k > 0; --k) {
-        at.back();
+      for (uint32_t k = min(issued, (p.stages + kCopyWarps - 1u) / kCopyWarps); k > 0; --k) {
+        for (int i = 0; i < kCopyWarps; ++i) at.back();
         if (lane == 0) mbar_arrive(bar(Bars::kFull, at.stage));
         drain(bar(Bars::kFull, at.stage), at.phase);
       }
@@ -636,11 +708,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       bool live;
     };
     const int32_t step_pages = max(kStep >> p.page_shift, 1);
-    int32_t step = 0;
-    int32_t it = 0, wait = warp - kScaleWarp0;  // steps until this warp's next
-    Ring at(p.stages);
+    Turns turns(warp - kScaleWarp0, kScaleWarps, p.stages);
     walk.t1 = 0;
-    bool more = true;
     Turn then, now;
     then.live = now.live = false;
     uint4 vals[kLines];   // now's scales, of an even and an odd position
@@ -719,26 +788,17 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
         }
       }
       // the page ids of the one after it
-#pragma unroll 1
-      while (more) {
-        const int32_t skip = min(wait, walk.t1 - step);
-        step += skip, it += skip, wait -= skip;
-        at.advance(skip);
-        if (step < walk.t1) break;
-        more = walk.next(p);
-        step = walk.t0;
-      }
-      then.live = more;
-      if (more) {
+      then.live = turns.next(walk, p);
+      if (then.live) {
         then.q = walk.q, then.most = walk.most;
-        then.step = step, then.it = it, then.stage = at.stage, then.phase = at.phase;
-        then.first = (step * kStep) >> p.page_shift;
+        then.step = turns.step, then.it = turns.it;
+        then.stage = turns.at.stage, then.phase = turns.at.phase;
+        then.first = (turns.step * kStep) >> p.page_shift;
         then.page = -1;
         if (lane < step_pages && (then.first + lane) << p.page_shift < walk.most)
           then.page = __ldg(p.s.block_table + static_cast<int64_t>(walk.seq) * p.s.max_blocks +
                             then.first + lane);
-        ++step, ++it, wait = kScaleWarps - 1;
-        at.advance(1);
+        turns.done();
       }
     }
     if (issuer) {  // scale copies of an aborted CTA have completed
@@ -751,7 +811,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     // Warp w has positions 64 w .. of a step, two a lane; a step's copies are
     // one group.
     constexpr int kInFlight = 2;
-    static_assert(stage_count(kMaxGroup) > kInFlight, "stages");
+    static_assert(stage_count(kChunks, kMaxGroup) > kInFlight, "stages");
     const int part = warp - kLoadWarp0;
     int32_t step = 0;
     walk.t1 = 0;
@@ -867,33 +927,62 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
 #pragma unroll 1
       for (uint32_t k = it > kInFlight ? it - kInFlight : 0; k < it; ++k) publish(k);
     }
-  } else if (warp == kScoreMmaWarp) {
+  } else if (warp >= kMmaWarp0 && warp < kMmaWarp0 + kMmaWarps) {
     // ---------------------------------------------------------- MMA issue
     constexpr uint32_t idesc = score_idesc(kHeads);
-    uint32_t run = 0, slot = 0, phase = 0;
+    const int which = warp - kMmaWarp0;
+    const uint32_t sfb0 = tmem + kSfbCol + static_cast<uint32_t>(which * p.group) * 8;
+    uint32_t run = 0;
+    uint32_t first = 0;  // number of the step's first unit
+    int32_t wait = which;
+    uint32_t turn = 0;   // steps of this warp's
     Ring at(p.stages);
     bool ok = true;
     const bool issuer = elect_one();
+    // The first of these warps copies the queries, a run ahead of the MMAs.
+    Walk ahead = walk;
+    uint32_t copied = 0;  // runs
+    auto copy_queries = [&]() {
+      const uint32_t bytes = static_cast<uint32_t>(ahead.count) * kImage;
+      const uint32_t to = bar(Bars::kQFull, copied & 1u);
+      mbar_arrive_tx(to, bytes);
+#pragma unroll 1
+      for (int i = 0; i < ahead.count; ++i)
+        tma_load_2d(q_image(copied & 1u) + i * kImage, &image_map, 0,
+                    (ahead.q + i) * static_cast<int32_t>(kImage / kImageLine), to);
+      ++copied;
+    };
+    if (which == 0 && ahead.next(p) && issuer) copy_queries();
 #pragma unroll 1
     while (ok && walk.next(p)) {
       const int buf = run & 1;
+      bool pending = which == 0 && ahead.next(p);
       ok = warp_wait(bar(Bars::kQFull, buf), (run >> 1) & 1u, abort_addr, lim);
       if (!ok) break;
       tc_fence_after();
+      const uint32_t image = q_image(buf);
       if (issuer) {
 #pragma unroll 1
         for (int i = 0; i < walk.count; ++i)
-#pragma unroll 1
           for (int h = 0; h < 2; ++h)
-            copy_scales(tmem + kSfbCol + i * 8 + h * 4,
-                        scale_desc(q_scales(buf) + i * kTileScales + h * 512));
-        const uint64_t q0 = sw64_desc(q_codes(buf));
+            copy_scales(sfb0 + i * 8 + h * 4,
+                        scale_desc(image + i * kImage + image_scales(kHeads) + h * 512));
+        const uint64_t q0 = sw64_desc(image);
 #pragma unroll 1
-        for (int32_t step = walk.t0; ok && step < walk.t1; ++step) {
+        for (int32_t step = walk.t0; step < walk.t1; ++step, first += walk.count, at.advance(1)) {
+          if (pending &&
+              mbar_ready(bar(Bars::kQEmpty, copied & 1u), ((copied >> 1) & 1u) ^ 1u)) {
+            copy_queries();
+            pending = false;
+          }
+          if (wait > 0) {  // the other warp's
+            --wait;
+            continue;
+          }
+          wait = kMmaWarps - 1;
           const uint32_t stage = at.stage;
           ok = wait_bar(bar(Bars::kFull, stage), at.phase, abort_addr, lim);
           if (!ok) break;
-          at.advance(1);
           tc_fence_after();
           const uint32_t src = stage0 + stage * kStageBytes;
           const uint32_t sfa = tmem + sfa_col + stage * kStepTiles * 8;
@@ -903,15 +992,23 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
               copy_scales(sfa + 4 * x, scale_desc(src + kStepCodes + 512 * x));
           }
           const uint64_t a = sw128_desc(src);
+          // Steps are issued in order, which the parities of the slots rely on:
+          // after the other warp's step before this one.
+          if (kMmaWarps > 1 && (which > 0 || turn > 0)) {
+            ok = wait_bar(bar(Bars::kTurn, which), (turn - (which == 0)) & 1u, abort_addr, lim);
+            if (!ok) break;
+          }
+          ++turn;
 #pragma unroll 1
           for (int i = 0; i < walk.count; ++i) {
             // a descriptor's address counts 16 bytes; a K step is 32 bytes, and
             // a tile's rows are one half of the 128-byte lines
-            const uint64_t b = q0 + i * (kHeads * kIndexCodes / 16);
-            const uint32_t sfb = tmem + kSfbCol + i * 8;
+            const uint64_t b = q0 + i * (kImage / 16);
+            const uint32_t sfb = sfb0 + i * 8;
 #pragma unroll
             for (int u = 0; u < kUnitSlots; ++u) {
-              ok = wait_bar(bar(Bars::kDEmpty, slot), phase ^ 1u, abort_addr, lim);
+              const uint32_t n = (first + i) * kUnitSlots + u, slot = n % kSlots;
+              ok = wait_bar(bar(Bars::kDEmpty, slot), ((n / kSlots) & 1u) ^ 1u, abort_addr, lim);
               if (!ok) break;
               tc_fence_after();
               const uint32_t d = tmem + slot * kSlotCols;
@@ -923,66 +1020,38 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
                         1);
               }
               mma_commit(bar(Bars::kDFull, slot));
-              if (++slot == kSlots) slot = 0, phase ^= 1u;
             }
             if (!ok) break;
           }
+          if (!ok) break;
+          if (kMmaWarps > 1) mbar_arrive(bar(Bars::kTurn, which ^ 1));
           mma_commit(bar(Bars::kEmpty, stage));
         }
         mma_commit(bar(Bars::kQEmpty, buf));
+        if (pending && ok) {
+          ok = wait_bar(bar(Bars::kQEmpty, copied & 1u), ((copied >> 1) & 1u) ^ 1u, abort_addr, lim);
+          if (ok) copy_queries();
+        }
       }
       ok = __all_sync(0xffffffffu, ok);
       ++run;
     }
+    if (issuer) {  // copies of an aborted CTA have landed
+#pragma unroll 1
+      for (uint32_t k = copied > 2 ? copied - 2 : 0; k < copied; ++k)
+        drain(bar(Bars::kQFull, k & 1u), (k >> 1) & 1u);
+    }
     // everything this thread issued has completed before the CTA ends
     if (issuer) {
-      mma_commit(bar(Bars::kDrain, 0));
-      drain(bar(Bars::kDrain, 0), 0);
+      mma_commit(bar(Bars::kDrain, which));
+      drain(bar(Bars::kDrain, which), 0);
     }
     __syncwarp();
-  } else if (warp >= kQWarp0) {
-    // ----------------------------------------------------- encode queries
-    const int qt = tid - kQWarp0 * 32;
-    uint32_t run = 0;
-    bool ok = true;
-#pragma unroll 1
-    while (ok && walk.next(p)) {
-      const int buf = run & 1;
-      ok = warp_wait(bar(Bars::kQEmpty, buf), ((run >> 1) & 1u) ^ 1u, abort_addr, lim);
-      if (!ok) break;
-#pragma unroll 1
-      for (int x = qt; x < walk.count * kHeads * kIndexScales; x += kQWarps * 32) {
-        const int g = x % kIndexScales, row = x / kIndexScales;  // row = token * kHeads + head
-        const int i = row / kHeads, h = row % kHeads;
-        uint32_t lo = 0, hi = 0, sc = 0;
-        float weight = 0.f;
-        if (h < p.s.num_heads) {
-          const int64_t head = static_cast<int64_t>(walk.q + i) * p.s.num_heads + h;
-          const uint8_t* src = p.s.q_index + head * (kIndexDim * 2) + g * (2 * kGroup);
-          const uint4 a = ld_nc_v4(src), b = ld_nc_v4(src + 16);
-          const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-          float s;
-          sc = quantize_group(v, lo, hi, s);
-          if (g == 0) weight = __ldg(p.s.weights + head);
-        }
-        const uint32_t at = q_codes(buf) + sw64_off(row, g >> 1) + (g & 1) * 8;
-        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(lo), "r"(hi) : "memory");
-        asm volatile("st.shared.u8 [%0], %1;" ::"r"(q_scales(buf) + i * kTileScales + scale_off(h, g)),
-                     "r"(sc)
-                     : "memory");
-        if (g == 0)
-          st_shared_u32(q_weights(buf) + row * 4, __float_as_uint(weight));
-      }
-      fence_proxy_async_cta();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(Bars::kQFull, buf));
-      ++run;
-    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kScoreMmaWarp) tmem_dealloc(tmem);
+  if (warp == kMmaWarp0) tmem_dealloc(tmem);
   if (tid == 0) p.s.status[blockIdx.x] = ld_shared_u32(abort_addr);
 }
 
@@ -1011,19 +1080,53 @@ bool codes_tensor(const SelectParams& s, CUtensorMap* map, int32_t* seg_rows) {
 
 template <int kChunks>
 int32_t launch_chunks(const ScoreParams& p, const CUtensorMap& map, cudaStream_t stream) {
-  const size_t smem = kStageBase +
-                      static_cast<size_t>(p.stages) * kStageBytes +
-                      2 * static_cast<size_t>(q_buffer_bytes(32 * kChunks, p.group));
+  CUtensorMap images;  // a box is a query token's image
+  {
+    EncodeTiledFn enc = encode_tiled();
+    constexpr int kLines = image_bytes(32 * kChunks) / kImageLine;
+    const cuuint64_t dims[2] = {kImageLine / 4, static_cast<cuuint64_t>(p.s.num_q) * kLines};
+    const cuuint64_t strides[1] = {kImageLine};
+    const cuuint32_t box[2] = {kImageLine / 4, kLines};
+    const cuuint32_t es[2] = {1, 1};
+    if (enc == nullptr ||
+        enc(&images, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, p.s.images, dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return NVFP4_MLA_ERR_LAUNCH;
+  }
+  constexpr int kImage = image_bytes(32 * kChunks);
+  const size_t smem = kStageBase + static_cast<size_t>(p.stages) * kStageBytes +
+                      2 * static_cast<size_t>(p.group) * kImage;
   if (cudaFuncSetAttribute(score_kernel<kChunks>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem)) != cudaSuccess) {
     cudaGetLastError();
     return NVFP4_MLA_ERR_LAUNCH;
   }
-  score_kernel<kChunks><<<p.ctas, kScoreThreads, smem, stream>>>(p, map);
-  return launch_status();
+  encode_kernel<<<p.s.num_q, 32 * kChunks * kIndexScales, 0, stream>>>(
+      p.s.q_index, p.s.weights, p.s.num_heads, 32 * kChunks, p.s.images);
+  if (int32_t st = launch_status()) return st;
+  cudaLaunchConfig_t launch = {};
+  launch.gridDim = dim3(p.ctas);
+  launch.blockDim = dim3(kScoreThreads);
+  launch.dynamicSmemBytes = smem;
+  launch.stream = stream;
+  cudaLaunchAttribute attr[1];  // sets itself up while the queries are encoded
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  launch.attrs = attr;
+  launch.numAttrs = 1;
+  if (cudaLaunchKernelEx(&launch, score_kernel<kChunks>, p, map, images) != cudaSuccess) {
+    cudaGetLastError();
+    return NVFP4_MLA_ERR_LAUNCH;
+  }
+  return NVFP4_MLA_OK;
 }
 
 }  // namespace
+
+size_t query_image_bytes(int32_t num_heads) {
+  return static_cast<size_t>(image_bytes((num_heads + 31) / 32 * 32));
+}
 
 int32_t launch_scores(SelectParams& s, int num_sms, cudaStream_t stream) {
   ScoreParams p;
@@ -1031,9 +1134,8 @@ int32_t launch_scores(SelectParams& s, int num_sms, cudaStream_t stream) {
   // Query tokens of a sequence share its key tiles: runs as long as there are
   // tokens per sequence, on average, and shared memory for their queries.
   const int32_t mean = s.num_q / s.num_seqs;
-  const int32_t most = max_group(chunks);
-  p.group = s.group = mean < 1 ? 1 : mean > most ? most : mean;
-  p.stages = stage_count(p.group);
+  p.group = s.group = mean < 1 ? 1 : mean > kMaxGroup ? kMaxGroup : mean;
+  p.stages = stage_count(chunks, p.group);
   p.ctas = s.score_ctas = num_sms < kStatusWords ? num_sms : kStatusWords;
   p.s = s;
   CUtensorMap map;

@@ -480,11 +480,14 @@ struct ListRow {  // shared memory, some blocks in any order
   __device__ __forceinline__ void mark(int32_t i, uint32_t m) const { keys[i] = m; }
 };
 
-// Output rows of a query token: every block's first position is written in
-// order, the others follow from it.
+// Output row of a query token: the first positions of its `chosen` blocks are
+// written in order, the others follow from them.
 template <int kThreads>
 __device__ __forceinline__ void expand_blocks(const SelectParams& p, int32_t* out, int64_t width,
-                                              int32_t seen) {
+                                              int32_t seen, int32_t chosen) {
+  // never fewer than num_select; the row is whole all the same
+  for (int64_t i = static_cast<int64_t>(chosen) * p.block + threadIdx.x; i < width; i += kThreads)
+    out[i] = -1;
   if (p.block == 1) return;
   __syncthreads();
   for (int64_t i = threadIdx.x; i < width; i += kThreads) {
@@ -497,7 +500,7 @@ __device__ __forceinline__ void expand_blocks(const SelectParams& p, int32_t* ou
 
 // Blocks in order, `row` holding those from p.sink on.
 template <int kThreads, typename Row>
-__device__ __forceinline__ void emit_row(const SelectParams& p, SelShared<kThreads>& sh,
+__device__ __forceinline__ int32_t emit_row(const SelectParams& p, SelShared<kThreads>& sh,
                                          const Row& row, const Border& border, int32_t blocks,
                                          int32_t* out) {
   int32_t done = 0, ties = 0;
@@ -516,9 +519,11 @@ __device__ __forceinline__ void emit_row(const SelectParams& p, SelShared<kThrea
       ties += total;
     }
     const int before = block_before<kThreads>(in, sh.sum_b, total);
-    if (in) out[static_cast<int64_t>(done + before) * p.block] = b * p.block;
+    if (in && done + before < p.num_select)
+      out[static_cast<int64_t>(done + before) * p.block] = b * p.block;
     done += total;
   }
+  return min(done, p.num_select);
 }
 
 __device__ __forceinline__ uint32_t sel_rank() {
@@ -673,8 +678,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   const int32_t k = p.num_select - p.sink - p.recent;
   if (k == 0) {
     if (rank == 0) {
-      emit_row<kThreads>(p, sh, row, Border{kTie, kTie, 0}, blocks, out);
-      expand_blocks<kThreads>(p, out, width, seen);
+      const int32_t chosen = emit_row<kThreads>(p, sh, row, Border{kTie, kTie, 0}, blocks, out);
+      expand_blocks<kThreads>(p, out, width, seen, chosen);
     }
     return;
   }
@@ -703,8 +708,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     for (int32_t i = tid; i < n; i += kThreads) keys[i] = row.key(i);
     __syncthreads();
     const Border border = choose<kThreads>(p, sh, dense, n, k, seq, seen, m);
-    emit_row<kThreads>(p, sh, dense, border, blocks, out);
-    expand_blocks<kThreads>(p, out, width, seen);
+    const int32_t chosen = emit_row<kThreads>(p, sh, dense, border, blocks, out);
+    expand_blocks<kThreads>(p, out, width, seen, chosen);
     return;
   }
 
@@ -816,10 +821,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
             }
             int64_t slot = at + upto - __popc(word);
             at += __shfl_sync(0xffffffffu, upto, 31);
-            for (; word != 0; word &= word - 1)
+            for (; word != 0 && slot < p.num_select; word &= word - 1)
               out[slot++ * p.block] = ((i0 + lane) * 32 + __ffs(word) - 1) * p.block;
           }
-          expand_blocks<kThreads>(p, out, width, seen);
+          expand_blocks<kThreads>(p, out, width, seen, min(total, p.num_select));
           return;
         }
       }
@@ -827,8 +832,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     }
     if (rank > 0) return;
     const Border border = choose<kThreads>(p, sh, row, n, k, seq, seen, m);
-    emit_row<kThreads>(p, sh, row, border, blocks, out);
-    expand_blocks<kThreads>(p, out, width, seen);
+    const int32_t chosen = emit_row<kThreads>(p, sh, row, border, blocks, out);
+    expand_blocks<kThreads>(p, out, width, seen, chosen);
   }
 }
 
@@ -887,7 +892,7 @@ bool plan_workspace(int32_t num_q, int32_t num_heads, int32_t max_blocks, int32_
   const int64_t granule = block < kMaxGranule ? block : kMaxGranule;
   w.score_stride = ((room + granule - 1) / granule + 3) / 4 * 4;
   w.tiles = ((room + kScoreTile - 1) / kScoreTile + 3) / 4 * 4;
-  w.per_q = static_cast<size_t>(w.score_stride + w.tiles) * 4;
+  w.per_q = static_cast<size_t>(w.score_stride + w.tiles) * 4 + query_image_bytes(num_heads);
   size_t fit = kWorkspaceGoal / w.per_q;
   if (fit < 1) fit = 1;
   if (fit > 32768) fit = 32768;
@@ -960,7 +965,8 @@ extern "C" int32_t sparse_mla_select(const void* q_index, const float* weights,
     p.room = max_blocks_per_seq * page_size;
     p.take_all = num_select * select_block;
     p.topk_idx = topk_idx + static_cast<int64_t>(q0) * num_select * select_block;
-    p.scores = static_cast<float*>(workspace);
+    p.images = static_cast<uint8_t*>(workspace);
+    p.scores = reinterpret_cast<float*>(p.images + query_image_bytes(num_heads) * w.chunk);
     p.score_stride = w.score_stride;
     p.smax = reinterpret_cast<uint32_t*>(p.scores + w.score_stride * w.chunk);
     p.tiles = w.tiles;

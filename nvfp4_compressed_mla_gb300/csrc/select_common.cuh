@@ -27,6 +27,7 @@ struct SelectParams {
   int32_t room;       // positions of a table's row: max_blocks * page_size
   int32_t take_all;   // num_select * block: up to here every visible position is taken
   int32_t* topk_idx;
+  uint8_t* images;    // [num_q] images of the encoded queries
   float* scores;      // [num_q, score_stride]
   int64_t score_stride;
   // [num_q, tiles]: the largest key scale byte of each tile's quarters, in the
@@ -52,6 +53,9 @@ __device__ __forceinline__ int32_t scored_positions(const SelectParams& p, int32
   const int32_t n = visible_positions(p, seq, pos);
   return n > p.take_all ? n : 0;
 }
+
+// Bytes of a query token's image.
+size_t query_image_bytes(int32_t num_heads);
 
 int32_t launch_scores(SelectParams& p, int num_sms, cudaStream_t stream);
 
