@@ -87,14 +87,15 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
   return f16_bits_to_f32(static_cast<uint16_t>(e4m3x2_to_f16x2(static_cast<uint16_t>(byte))));
 }
 
+constexpr int kHeadWords = 33;  // 32 words of codes; one more keeps lanes' heads in different banks
+constexpr int kHeadScales = 9;
+
 template <int kThreads>
 struct SelShared {
   static constexpr int kWarps = kThreads / 32;
   static constexpr int kCands = kThreads;  // candidates ranked from shared memory
-  uint4 q_codes[kIndexScales][NVFP4_MLA_MAX_HEADS];  // groups as signed bytes, twice the values
-  uint4 k_codes[kWarps][kIndexScales];               // a warp's position
-  uint32_t q_scale[kIndexScales][NVFP4_MLA_MAX_HEADS];
-  uint32_t k_scale[kWarps][kIndexScales];
+  uint32_t q_codes[NVFP4_MLA_MAX_HEADS * kHeadWords];  // signed bytes, twice the values
+  uint32_t q_scale[NVFP4_MLA_MAX_HEADS * kHeadScales];
   float w[NVFP4_MLA_MAX_HEADS];
   uint32_t hist[kBins];
   uint64_t cand_key[kCands];              // fp64 score, as a key
@@ -108,45 +109,6 @@ struct SelShared {
 
 struct SelectConfig {
   int32_t room;  // keys that the dynamic shared memory behind SelShared holds
-};
-
-extern __shared__ __align__(16) uint8_t select_smem[];
-template <int kThreads>
-__device__ __forceinline__ SelShared<kThreads>& shared() {
-  return *reinterpret_cast<SelShared<kThreads>*>(select_smem);
-}
-
-// The keys of a query token's blocks, in one of three places. One piece of
-// code works on all of them, and rare paths are calls: a CTA goes through most
-// of this file once, and what it executes comes through the instruction cache
-// only then.
-struct Row {
-  uint32_t* keys;    // shared memory: of all blocks from b0 on, or of `blocks`
-  int32_t* blocks;   // shared memory, in any order, or null
-  float* scores;     // without `keys`: memory; a block has the highest of `per`
-  int32_t b0, per, granules;
-  __device__ __forceinline__ int32_t block(int32_t i) const {
-    return blocks != nullptr ? blocks[i] : b0 + i;
-  }
-  __device__ __forceinline__ uint32_t load(int32_t i) const {
-    const int64_t at = static_cast<int64_t>(b0 + i) * per;
-    float a = __ldcg(scores + at);
-    const uint32_t u = __float_as_uint(a);
-    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return u & 0x80000000u ? ~u : u | 0x80000000u;  // a mark
-#pragma unroll 1
-    for (int g = 1; g < per; ++g)
-      if (at + g < granules) a = fmaxf(a, __ldcg(scores + at + g));
-    return key32(a);
-  }
-  __device__ __forceinline__ uint32_t key(int32_t i) const {
-    return keys != nullptr ? keys[i] : load(i);
-  }
-  __device__ __forceinline__ void mark(int32_t i, uint32_t m) const {
-    if (keys != nullptr) keys[i] = m;
-    else
-      scores[static_cast<int64_t>(b0 + i) * per] =
-          __uint_as_float(m == kOut ? 0xFFFFFFFFu : m & 0x7FFFFFFFu);
-  }
 };
 
 // ------------------------------------------------------------- block helpers
@@ -206,21 +168,20 @@ __device__ __forceinline__ void find_bin(SelShared<kThreads>& sh, uint32_t rank)
   __syncthreads();
 }
 
-// The `rank`-th largest of the keys that each(f) gives to f, `lowest` to
-// highest: a histogram over their range, then over the bin that holds it, until
-// a bin is one value (three levels for fp32 keys, which differ in 22 to 32
-// bits). `rank` becomes the rank among the equal ones.
-template <int kThreads, typename Key, typename Each>
-__device__ __forceinline__ Key kth_largest(Key lowest, Key highest, uint32_t& rank, Each&& each) {
-  SelShared<kThreads>& sh = shared<kThreads>();
+// The `rank`-th largest of `count` keys: a histogram over their range, then
+// over the bin that holds it, until a bin is one value (three levels for fp32
+// keys, which differ in 22 to 32 bits). each(f) calls f with this thread's
+// share of the keys, and the whole block goes through it; `rank` becomes the
+// rank among the equal ones. With fewer levels the lower edge of the last bin.
+template <int kThreads, typename Key, int kLevels = 8, typename Each>
+__device__ __forceinline__ Key kth_largest(SelShared<kThreads>& sh, Key lowest, Key highest,
+                                           uint32_t& rank, Each&& each) {
   Key base = lowest, width = highest - lowest;  // keys base .. base + width are in question
-#pragma unroll 1
-  while (true) {
+  for (int level = 1;; ++level) {
     const int bits = width == 0 ? 0 : sizeof(Key) == 8
                                           ? 64 - __clzll(static_cast<long long>(width))
                                           : 32 - __clz(static_cast<int>(width));
     const int shift = bits > 11 ? bits - 11 : 0;
-#pragma unroll 1
     for (int i = threadIdx.x; i < kBins; i += kThreads) sh.hist[i] = 0;
     __syncthreads();
     each([&](Key k) {
@@ -231,80 +192,26 @@ __device__ __forceinline__ Key kth_largest(Key lowest, Key highest, uint32_t& ra
     base += static_cast<Key>(sh.pick) << shift;
     rank = sh.rest;
     __syncthreads();
-    if (shift == 0) return base;
+    if (shift == 0 || level == kLevels) return base;
     width = (Key{1} << shift) - 1;
   }
 }
 
-// The `rank`-th largest of the first `count` keys of a row; `rank` becomes the
-// rank among the equal ones. A histogram linear in the scores leaves a few of
-// them in the bin in question, which are ranked one by one; where it does not
-// (scores of very different size, many equal ones) the histograms of the keys
-// above follow.
-template <int kThreads>
-__device__ __noinline__ uint32_t kth_of_row(const Row row, int32_t count, uint32_t& rank) {
-  SelShared<kThreads>& sh = shared<kThreads>();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kW = kThreads / 32;
-  const uint32_t low = key32(-INFINITY);
-  uint32_t lo = 0xFFFFFFFFu, hi = 0;  // of the scores above -inf
-#pragma unroll 4
-  for (int32_t i = tid; i < count; i += kThreads) {
-    const uint32_t k = row.key(i);
-    lo = min(lo, k > low ? k : 0xFFFFFFFFu), hi = max(hi, k);
-  }
+// Lowest and highest of the keys that each() goes through.
+template <int kThreads, typename Each>
+__device__ __forceinline__ void key_range(SelShared<kThreads>& sh, uint32_t& lowest,
+                                          uint32_t& highest, Each&& each) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t lo = 0xFFFFFFFFu, hi = 0;
+  each([&](uint32_t k) { lo = min(lo, k), hi = max(hi, k); });
   lo = __reduce_min_sync(0xffffffffu, lo);
   hi = __reduce_max_sync(0xffffffffu, hi);
   __syncthreads();
   if (lane == 0) sh.redu[warp] = lo, sh.redv[warp] = hi;
-#pragma unroll 1
-  for (int i = tid; i < kBins; i += kThreads) sh.hist[i] = 0;
-  if (tid == 0) sh.n = 0;
   __syncthreads();
-  lo = __reduce_min_sync(0xffffffffu, sh.redu[lane % kW]);
-  hi = __reduce_max_sync(0xffffffffu, sh.redv[lane % kW]);
-  const float bottom = unkey32(lo), range = unkey32(hi) - bottom;
-  if (lo < hi && range < 3e38f && range > 1e-30f) {
-    const float scale = 2047.0f / range;
-    // rounds the same way for every score: never a lower bin for a higher one
-    auto bin = [&](uint32_t k) {
-      return k <= low ? 0 : min(static_cast<int>((unkey32(k) - bottom) * scale), kBins - 1);
-    };
-#pragma unroll 4
-    for (int32_t i = tid; i < count; i += kThreads) atomicAdd(&sh.hist[bin(row.key(i))], 1u);
-    __syncthreads();
-    find_bin<kThreads>(sh, rank);
-    const int pick = static_cast<int>(sh.pick);
-    const uint32_t within = sh.rest;
-    const int c = static_cast<int>(sh.hist[pick]);
-    if (c <= SelShared<kThreads>::kCands) {
-#pragma unroll 4
-      for (int32_t i = tid; i < count; i += kThreads) {
-        const uint32_t k = row.key(i);
-        if (bin(k) == pick) sh.cand_lo[atomicAdd(&sh.n, 1u)] = k;
-      }
-      __syncthreads();
-#pragma unroll 1
-      for (int i = tid; i < c; i += kThreads) {
-        const uint32_t k = sh.cand_lo[i];
-        uint32_t above = 0, equal = 0;
-#pragma unroll 4
-        for (int j = 0; j < c; ++j) {
-          above += sh.cand_lo[j] > k;
-          equal += sh.cand_lo[j] == k;
-        }
-        if (above < within && within <= above + equal) sh.pick = k, sh.rest = within - above;
-      }
-      __syncthreads();
-      rank = sh.rest;
-      return sh.pick;
-    }
-    __syncthreads();
-  }
-  return kth_largest<kThreads, uint32_t>(0u, hi, rank, [&](auto&& f) {
-#pragma unroll 1
-    for (int32_t i = tid; i < count; i += kThreads) f(row.key(i));
-  });
+  constexpr int kW = kThreads / 32;
+  lowest = __reduce_min_sync(0xffffffffu, sh.redu[lane % kW]);
+  highest = __reduce_max_sync(0xffffffffu, sh.redv[lane % kW]);
 }
 
 // ------------------------------------------------------------ exact scores
@@ -316,15 +223,14 @@ struct TokenScore {
   double exact;
   bool none;  // -inf: a NaN, or a page that does not resolve
 };
-template <bool kExact, int kThreads>
-__device__ __noinline__ TokenScore score_token(const SelectParams& p, int32_t seq, int32_t pos) {
-  SelShared<kThreads>& sh = shared<kThreads>();
+template <bool kExact, typename Shared>
+__device__ __forceinline__ TokenScore score_token(const SelectParams& p, const Shared& sh,
+                                                  int32_t seq, int32_t pos) {
   const int lane = threadIdx.x & 31;
   TokenScore r = {0.f, 0.f, 0.0, true};
   const IndexRow at = resolve_index_row(seq, pos, p.block_table, p.num_seqs, p.max_blocks,
                                         p.page_size, p.num_blocks, p.block_stride);
   if (at.page < 0) return r;
-  const int warp = threadIdx.x >> 5;
   const uint8_t* page = p.cache + at.page;
   const uint32_t mine = expand_codes(__ldg(reinterpret_cast<const uint16_t*>(
       page + static_cast<int64_t>(at.row) * kIndexCodes + lane * 2)));
@@ -333,22 +239,20 @@ __device__ __noinline__ TokenScore score_token(const SelectParams& p, int32_t se
                         0x7Fu;
   if (__any_sync(0xffffffffu, byte == 0x7Fu)) return r;
   r.none = false;
-  __syncwarp();
-  reinterpret_cast<uint32_t*>(sh.k_codes[warp])[lane] = mine;
-  if (lane < kIndexScales) sh.k_scale[warp][lane] = scale_parts(byte);
-  __syncwarp();
-#pragma unroll 1
+  const uint32_t parts = scale_parts(byte);
   for (int j0 = 0; j0 < p.num_heads; j0 += 32) {
     const int j = min(j0 + lane, p.num_heads - 1);
+    const uint32_t* q = sh.q_codes + j * kHeadWords;
     int64_t d = 0;
 #pragma unroll
     for (int g = 0; g < kIndexScales; ++g) {
-      const uint4 q = sh.q_codes[g][j], k = sh.k_codes[warp][g];
-      int dot = __dp4a(static_cast<int>(q.x), static_cast<int>(k.x), 0);
-      dot = __dp4a(static_cast<int>(q.y), static_cast<int>(k.y), dot);
-      dot = __dp4a(static_cast<int>(q.z), static_cast<int>(k.z), dot);
-      dot = __dp4a(static_cast<int>(q.w), static_cast<int>(k.w), dot);
-      const uint32_t ks = sh.k_scale[warp][g], qs = sh.q_scale[g][j];
+      int dot = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        dot = __dp4a(static_cast<int>(q[4 * g + i]),
+                     static_cast<int>(__shfl_sync(0xffffffffu, mine, 4 * g + i)), dot);
+      const uint32_t ks = __shfl_sync(0xffffffffu, parts, g);
+      const uint32_t qs = sh.q_scale[j * kHeadScales + g];
       dot *= static_cast<int>((ks & 255u) * (qs & 255u));
       d += static_cast<int64_t>(dot) << ((ks >> 8) + (qs >> 8));
     }
@@ -383,9 +287,10 @@ __device__ __noinline__ TokenScore score_token(const SelectParams& p, int32_t se
   }
   return r;
 }
-template <int kThreads>
-__device__ __forceinline__ uint64_t exact_key(const SelectParams& p, int32_t seq, int32_t pos) {
-  const TokenScore r = score_token<true, kThreads>(p, seq, pos);
+template <typename Shared>
+__device__ __forceinline__ uint64_t exact_key(const SelectParams& p, const Shared& sh, int32_t seq,
+                                              int32_t pos) {
+  const TokenScore r = score_token<true>(p, sh, seq, pos);
   return r.none ? kLowest64 : key64(r.exact);
 }
 
@@ -397,59 +302,20 @@ struct Border {
   int32_t ties;
 };
 
-// Too many candidates (keys lo .. hi) to list, as at a border among equal
-// scores: the want-th largest fp64 score, computed anew in each step, then a
-// mark for each candidate.
-template <int kThreads>
-__device__ __noinline__ Border choose_exact(const SelectParams& p, const Row row, int32_t count,
-                                            uint32_t want, int32_t seq, int32_t seen, uint32_t lo,
-                                            uint32_t hi) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int kWarps = kThreads / 32;
-  auto exact = [&](int32_t i) {  // one warp
-    uint64_t best = 0;
-    const int64_t first = static_cast<int64_t>(row.block(i)) * p.block;
-#pragma unroll 1
-    for (int64_t pos = first; pos < first + p.block && pos < seen; ++pos) {
-      const uint64_t e = exact_key<kThreads>(p, seq, static_cast<int32_t>(pos));
-      best = best > e ? best : e;
-    }
-    return best;
-  };
-  uint32_t rank = want;
-  const uint64_t edge = kth_largest<kThreads, uint64_t>(
-      uint64_t{0}, ~uint64_t{0}, rank, [&](auto&& f) {
-#pragma unroll 1
-        for (int32_t i = warp; i < count; i += kWarps) {
-          const uint32_t key = row.key(i);
-          if (key < lo || key > hi) continue;
-          const uint64_t e = exact(i);
-          if (lane == 0) f(e);
-        }
-      });
-#pragma unroll 1
-  for (int32_t i = warp; i < count; i += kWarps) {
-    const uint32_t key = row.key(i);
-    if (key < lo || key > hi) continue;
-    const uint64_t e = exact(i);
-    __syncwarp();
-    if (lane == 0) row.mark(i, e > edge ? kIn : e == edge ? kTie : kOut);
-    __syncwarp();
-  }
-  __syncthreads();
-  return {lo, hi, static_cast<int32_t>(rank)};
-}
-
 // The border of the k highest of the `count` keys of a row. `row` gives keys
 // by position and their blocks, and takes marks (kIn, kTie, kOut).
-template <int kThreads>
-__device__ __noinline__ Border choose(const SelectParams& p, const Row row, int32_t count,
-                                      int32_t k, int32_t seq, int32_t seen, float m) {
-  SelShared<kThreads>& sh = shared<kThreads>();
+template <int kThreads, typename Row>
+__device__ __forceinline__ Border choose(const SelectParams& p, SelShared<kThreads>& sh,
+                                         const Row& row, int32_t count, int32_t k, int32_t seq,
+                                         int32_t seen, float m) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kWarps = kThreads / 32;
-  uint32_t rank = k;
-  const uint32_t tk = kth_of_row<kThreads>(row, count, rank);
+  auto each = [&](auto&& f) {
+    for (int32_t i = tid; i < count; i += kThreads) f(row.key(i));
+  };
+  uint32_t lowest, highest, rank = k;
+  key_range(sh, lowest, highest, each);
+  const uint32_t tk = kth_largest<kThreads, uint32_t>(sh, lowest, highest, rank, each);
   const float T = unkey32(tk);
   const float eps2 =
       m == 0.f ? 0.f
@@ -465,7 +331,6 @@ __device__ __noinline__ Border choose(const SelectParams& p, const Row row, int3
   if (tid == 0) sh.n = 0;
   __syncthreads();
   int in = 0;
-#pragma unroll 1
   for (int32_t i = tid; i < count; i += kThreads) {
     const uint32_t key = row.key(i);
     if (key > hi) {
@@ -482,16 +347,14 @@ __device__ __noinline__ Border choose(const SelectParams& p, const Row row, int3
 
   const int shift = __ffs(p.block) - 1;
   if (cands <= SelShared<kThreads>::kCands) {
-#pragma unroll 1
     for (int i = tid; i < cands; i += kThreads)
       sh.cand_key[i] = 0, sh.cand_lo[i] = sh.cand_hi[i] = 0;
     __syncthreads();
-#pragma unroll 1
     for (int i = warp; i < cands << shift; i += kWarps) {
       const int c = i >> shift;
       const int64_t pos = static_cast<int64_t>(row.block(sh.cand[c])) * p.block + (i & (p.block - 1));
       if (pos >= seen) continue;
-      const TokenScore r = score_token<false, kThreads>(p, seq, static_cast<int32_t>(pos));
+      const TokenScore r = score_token<false>(p, sh, seq, static_cast<int32_t>(pos));
       if (lane == 0) {
         atomicMax(&sh.cand_lo[c], key32(r.none ? -INFINITY : __fsub_rd(r.value, r.error)));
         atomicMax(&sh.cand_hi[c], key32(r.none ? -INFINITY : __fadd_ru(r.value, r.error)));
@@ -501,10 +364,8 @@ __device__ __noinline__ Border choose(const SelectParams& p, const Row row, int3
     // Known by their intervals: in where fewer than `want` others can be
     // above, out where `want` others are. sh.cand_key: 0 open, 1 in, 2 out.
     int sure = 0;
-#pragma unroll 1
     for (int i = tid; i < cands; i += kThreads) {
       int can = 0, are = 0;
-#pragma unroll 1
       for (int j = 0; j < cands; ++j) {
         can += j != i && sh.cand_hi[j] >= sh.cand_lo[i];
         are += sh.cand_lo[j] > sh.cand_hi[i];
@@ -517,38 +378,32 @@ __device__ __noinline__ Border choose(const SelectParams& p, const Row row, int3
     want -= block_sum<kThreads>(sure, sh.sum_a);
     // The best of the others by their fp64 scores.
     if (want > 0) {
-#pragma unroll 1
       for (int i = tid; i < cands; i += kThreads) sh.cand_lo[i] = sh.cand_key[i] == 0 ? 1u : 0u;
       __syncthreads();
-#pragma unroll 1
       for (int i = tid; i < cands; i += kThreads) sh.cand_key[i] = 0;
       __syncthreads();
-#pragma unroll 1
       for (int i = warp; i < cands << shift; i += kWarps) {
         const int c = i >> shift;
         if (sh.cand_lo[c] == 0) continue;
         const int64_t pos = static_cast<int64_t>(row.block(sh.cand[c])) * p.block + (i & (p.block - 1));
         if (pos >= seen) continue;
-        const uint64_t key = exact_key<kThreads>(p, seq, static_cast<int32_t>(pos));
+        const uint64_t key = exact_key(p, sh, seq, static_cast<int32_t>(pos));
         if (lane == 0)
           atomicMax(reinterpret_cast<unsigned long long*>(&sh.cand_key[c]),
                     static_cast<unsigned long long>(key));
       }
       __syncthreads();
-#pragma unroll 1
       for (int i = tid; i < cands; i += kThreads) {
         if (sh.cand_lo[i] == 0) continue;
         const uint64_t key = sh.cand_key[i];
         const int32_t b = row.block(sh.cand[i]);
         int better = 0;
-#pragma unroll 1
         for (int j = 0; j < cands; ++j)
           better += sh.cand_lo[j] != 0 &&
                     (sh.cand_key[j] > key || (sh.cand_key[j] == key && row.block(sh.cand[j]) < b));
         row.mark(sh.cand[i], better < want ? kIn : kOut);
       }
     } else {
-#pragma unroll 1
       for (int i = tid; i < cands; i += kThreads)
         if (sh.cand_key[i] == 0) row.mark(sh.cand[i], kOut);
     }
@@ -556,76 +411,119 @@ __device__ __noinline__ Border choose(const SelectParams& p, const Row row, int3
     return {lo, hi, 0};
   }
 
-  return choose_exact<kThreads>(p, row, count, want, seq, seen, lo, hi);
+  // Too many to list (a border among equal scores): the want-th largest fp64
+  // score, computed anew in each step, then a mark for each candidate.
+  auto exact = [&](int32_t i) {  // one warp
+    uint64_t best = 0;
+    const int64_t first = static_cast<int64_t>(row.block(i)) * p.block;
+    for (int64_t pos = first; pos < first + p.block && pos < seen; ++pos) {
+      const uint64_t e = exact_key(p, sh, seq, static_cast<int32_t>(pos));
+      best = best > e ? best : e;
+    }
+    return best;
+  };
+  auto each_exact = [&](auto&& f) {
+    for (int32_t i = warp; i < count; i += kWarps) {
+      const uint32_t key = row.key(i);
+      if (key < lo || key > hi) continue;
+      const uint64_t e = exact(i);
+      if (lane == 0) f(e);
+    }
+  };
+  rank = want;
+  const uint64_t edge = kth_largest<kThreads, uint64_t>(sh, uint64_t{0}, ~uint64_t{0}, rank,
+                                                        each_exact);
+  for (int32_t i = warp; i < count; i += kWarps) {
+    const uint32_t key = row.key(i);
+    if (key < lo || key > hi) continue;
+    const uint64_t e = exact(i);
+    __syncwarp();
+    if (lane == 0) row.mark(i, e > edge ? kIn : e == edge ? kTie : kOut);
+    __syncwarp();
+  }
+  __syncthreads();
+  return {lo, hi, static_cast<int32_t>(rank)};
 }
 
-// The end of an output row behind `chosen` blocks. There are never fewer than
-// num_select; the row is whole all the same.
+// ------------------------------------------------------------------- rows
+// A row's scores in memory: a block's is the highest of its `per` stored ones.
+struct MemoryRow {
+  float* scores;
+  int32_t b0, per, granules;
+  __device__ __forceinline__ int32_t block(int32_t i) const { return b0 + i; }
+  __device__ __forceinline__ uint32_t key(int32_t i) const {
+    const int64_t at = static_cast<int64_t>(b0 + i) * per;
+    float a = __ldcg(scores + at);
+    const uint32_t u = __float_as_uint(a);
+    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return u & 0x80000000u ? ~u : u | 0x80000000u;  // a mark
+    for (int g = 1; g < per; ++g)
+      if (at + g < granules) a = fmaxf(a, __ldcg(scores + at + g));
+    return key32(a);
+  }
+  __device__ __forceinline__ void mark(int32_t i, uint32_t m) const {
+    scores[static_cast<int64_t>(b0 + i) * per] =
+        __uint_as_float(m == kOut ? 0xFFFFFFFFu : m & 0x7FFFFFFFu);
+  }
+};
+struct DenseRow {  // shared memory, all blocks from b0 on
+  uint32_t* keys;
+  int32_t b0;
+  __device__ __forceinline__ int32_t block(int32_t i) const { return b0 + i; }
+  __device__ __forceinline__ uint32_t key(int32_t i) const { return keys[i]; }
+  __device__ __forceinline__ void mark(int32_t i, uint32_t m) const { keys[i] = m; }
+};
+struct ListRow {  // shared memory, some blocks in any order
+  uint32_t* keys;
+  int32_t* blocks;
+  __device__ __forceinline__ int32_t block(int32_t i) const { return blocks[i]; }
+  __device__ __forceinline__ uint32_t key(int32_t i) const { return keys[i]; }
+  __device__ __forceinline__ void mark(int32_t i, uint32_t m) const { keys[i] = m; }
+};
+
+// Output row of a query token: the first positions of its `chosen` blocks are
+// written in order, the others follow from them.
 template <int kThreads>
-__device__ __forceinline__ void fill_row(const SelectParams& p, int32_t* out, int64_t width,
-                                         int32_t chosen) {
-#pragma unroll 1
+__device__ __forceinline__ void expand_blocks(const SelectParams& p, int32_t* out, int64_t width,
+                                              int32_t seen, int32_t chosen) {
+  // never fewer than num_select; the row is whole all the same
   for (int64_t i = static_cast<int64_t>(chosen) * p.block + threadIdx.x; i < width; i += kThreads)
     out[i] = -1;
+  if (p.block == 1) return;
+  __syncthreads();
+  for (int64_t i = threadIdx.x; i < width; i += kThreads) {
+    const int off = static_cast<int>(i) & (p.block - 1);
+    if (off == 0) continue;
+    const int32_t pos = __ldcg(out + (i - off)) + off;
+    out[i] = pos < seen ? pos : -1;
+  }
 }
 
-// The positions of the chosen blocks in order, `row` holding the blocks from
-// p.sink on; returns how many were chosen. A warp has consecutive blocks: it
-// counts, learns what comes before it, and writes.
-template <int kThreads>
-__device__ __noinline__ int32_t emit_row(const SelectParams& p, const Row row, const Border border,
-                                         int32_t blocks, int32_t seen, int32_t* out) {
-  SelShared<kThreads>& sh = shared<kThreads>();
-  constexpr int kWarps = kThreads / 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int32_t share = ((blocks + kWarps - 1) / kWarps + 31) / 32 * 32;
-  const int32_t from = min(warp * share, blocks), to = min(from + share, blocks);
-  auto state = [&](int32_t b, bool& tie) {
-    tie = false;
-    if (b >= to) return false;
-    if (b < p.sink || b >= blocks - p.recent) return true;
-    const uint32_t key = row.key(b - p.sink);
-    tie = key == kTie || (key >= border.lo && key <= border.hi);
-    return key > border.hi && !tie;
-  };
-  int sure = 0, ties = 0;
-#pragma unroll 2
-  for (int32_t b0 = from; b0 < to; b0 += 32) {
-    bool tie;
-    const bool in = state(b0 + lane, tie);
-    sure += __popc(__ballot_sync(0xffffffffu, in));
-    ties += __popc(__ballot_sync(0xffffffffu, tie));
-  }
-  int total;
-  int32_t tie_at = block_before<kThreads>(lane == 0 ? ties : 0, sh.sum_a, total);
-  tie_at = __shfl_sync(0xffffffffu, tie_at, 0);
-  const int taken = max(0, min(ties, border.ties - tie_at));
-  int32_t at = block_before<kThreads>(lane == 0 ? sure + taken : 0, sh.sum_b, total);
-  at = __shfl_sync(0xffffffffu, at, 0);
-#pragma unroll 1
-  for (int32_t b0 = from; b0 < to; b0 += 32) {
-    bool tie;
-    bool in = state(b0 + lane, tie);
-    const uint32_t tied = __ballot_sync(0xffffffffu, tie);
-    in = in || (tie && tie_at + __popc(tied & ((1u << lane) - 1)) < border.ties);
-    tie_at += __popc(tied);
-    uint32_t chosen = __ballot_sync(0xffffffffu, in);
-    if (p.block == 1) {
-      const int32_t slot = at + __popc(chosen & ((1u << lane) - 1));
-      if (in && slot < p.num_select) out[slot] = b0 + lane;
-      at += __popc(chosen);
-    } else {
-#pragma unroll 1
-      for (; chosen != 0; chosen &= chosen - 1, ++at) {
-        if (at >= p.num_select) break;
-        const int32_t pos = (b0 + __ffs(chosen) - 1) * p.block;
-#pragma unroll 1
-        for (int32_t i = lane; i < p.block; i += 32)
-          out[static_cast<int64_t>(at) * p.block + i] = pos + i < seen ? pos + i : -1;
-      }
+// Blocks in order, `row` holding those from p.sink on.
+template <int kThreads, typename Row>
+__device__ __forceinline__ int32_t emit_row(const SelectParams& p, SelShared<kThreads>& sh,
+                                         const Row& row, const Border& border, int32_t blocks,
+                                         int32_t* out) {
+  int32_t done = 0, ties = 0;
+  for (int32_t c0 = 0; c0 < blocks; c0 += kThreads) {
+    const int32_t b = c0 + static_cast<int32_t>(threadIdx.x);
+    bool in = b < blocks && (b < p.sink || b >= blocks - p.recent), tie = false;
+    if (b < blocks && !in) {
+      const uint32_t key = row.key(b - p.sink);
+      tie = key == kTie || (key >= border.lo && key <= border.hi);
+      in = key > border.hi && !tie;
     }
+    int total;
+    if (border.ties > 0) {
+      const int before = block_before<kThreads>(tie, sh.sum_a, total);
+      in = in || (tie && before < border.ties - ties);
+      ties += total;
+    }
+    const int before = block_before<kThreads>(in, sh.sum_b, total);
+    if (in && done + before < p.num_select)
+      out[static_cast<int64_t>(done + before) * p.block] = b * p.block;
+    done += total;
   }
-  return min(total, p.num_select);
+  return min(done, p.num_select);
 }
 
 __device__ __forceinline__ uint32_t sel_rank() {
@@ -653,48 +551,38 @@ __device__ __forceinline__ uint32_t in_rank(uint32_t addr, uint32_t rank) {
 // `floor`, into the list of `cap` entries; returns how many there are (some
 // may not have fitted). `from` is a multiple of 4.
 template <int kThreads>
-__device__ __forceinline__ int32_t collect(SelShared<kThreads>& sh, const Row& row,
+__device__ __forceinline__ int32_t collect(SelShared<kThreads>& sh, const MemoryRow& row,
                                            int32_t from, int32_t to, uint32_t floor,
                                            uint32_t* keys, int32_t* blocks, int32_t cap) {
   const int lane = threadIdx.x & 31;
   if (threadIdx.x == 0) sh.n = 0;
   __syncthreads();
-  constexpr int kQuads = 2;                       // 8 scores of a thread at a time,
-  constexpr int kChunk = kThreads * 4 * kQuads;   // the next 8 on their way
-  const float least = unkey32(floor);
+  constexpr int kQuads = 4;  // 16 keys of a thread at a time
   // one stored score a block, 16-byte aligned: four at once
   const bool vec = row.per == 1 && row.b0 % 4 == 0;
-  const float* base = row.scores + row.b0;
-  auto fetch = [&](float4 (&v)[kQuads], int32_t i0) {
+  for (int32_t i0 = from; i0 < to; i0 += kThreads * 4 * kQuads) {
+    uint32_t key[4 * kQuads];
+    uint32_t hits = 0;
+    if (vec && i0 + kThreads * 4 * kQuads <= to) {
+      float4 v[kQuads];
 #pragma unroll
-    for (int u = 0; u < kQuads; ++u) {
-      const int64_t i = static_cast<int64_t>(i0) + (u * kThreads + threadIdx.x) * 4;
-      if (vec && i + 4 <= to) {
-        v[u] = __ldcg(reinterpret_cast<const float4*>(base + i));
-      } else {
-        v[u].x = i < to ? unkey32(row.load(static_cast<int32_t>(i))) : -INFINITY;
-        v[u].y = i + 1 < to ? unkey32(row.load(static_cast<int32_t>(i + 1))) : -INFINITY;
-        v[u].z = i + 2 < to ? unkey32(row.load(static_cast<int32_t>(i + 2))) : -INFINITY;
-        v[u].w = i + 3 < to ? unkey32(row.load(static_cast<int32_t>(i + 3))) : -INFINITY;
+      for (int u = 0; u < kQuads; ++u)
+        v[u] = __ldcg(reinterpret_cast<const float4*>(row.scores + row.b0 + i0) + u * kThreads +
+                      threadIdx.x);
+#pragma unroll
+      for (int u = 0; u < kQuads; ++u) {
+        key[4 * u] = key32(v[u].x), key[4 * u + 1] = key32(v[u].y);
+        key[4 * u + 2] = key32(v[u].z), key[4 * u + 3] = key32(v[u].w);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < 4 * kQuads; ++u) {
+        const int64_t i = static_cast<int64_t>(i0) + (u >> 2) * kThreads * 4 + threadIdx.x * 4 + (u & 3);
+        key[u] = i < to ? row.key(static_cast<int32_t>(i)) : 0u;
       }
     }
-  };
-  float4 next[kQuads];
-  fetch(next, from);
-#pragma unroll 1
-  for (int32_t i0 = from; i0 < to; i0 += kChunk) {
-    float v[4 * kQuads];
 #pragma unroll
-    for (int u = 0; u < kQuads; ++u)
-      v[4 * u] = next[u].x, v[4 * u + 1] = next[u].y, v[4 * u + 2] = next[u].z,
-            v[4 * u + 3] = next[u].w;
-    if (to - i0 > kChunk) fetch(next, i0 + kChunk);
-    uint32_t hits = 0;
-#pragma unroll
-    for (int u = 0; u < 4 * kQuads; ++u) {
-      const int32_t i = i0 + (u >> 2) * kThreads * 4 + static_cast<int32_t>(threadIdx.x) * 4 + (u & 3);
-      hits |= (v[u] >= least && i < to ? 1u : 0u) << u;
-    }
+    for (int u = 0; u < 4 * kQuads; ++u) hits |= (key[u] >= floor ? 1u : 0u) << u;
     const int mine = __popc(hits);
     int upto = mine;
 #pragma unroll
@@ -710,7 +598,7 @@ __device__ __forceinline__ int32_t collect(SelShared<kThreads>& sh, const Row& r
       for (int u = 0; u < 4 * kQuads; ++u) {
         if ((hits >> u & 1u) == 0) continue;
         if (at < static_cast<uint32_t>(cap)) {
-          keys[at] = key32(v[u]);
+          keys[at] = key[u];
           blocks[at] = row.block(i0 + (u >> 2) * kThreads * 4 + static_cast<int32_t>(threadIdx.x) * 4 +
                                  (u & 3));
         }
@@ -724,11 +612,12 @@ __device__ __forceinline__ int32_t collect(SelShared<kThreads>& sh, const Row& r
 
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
-    select_kernel(const __grid_constant__ SelectParams p, const SelectConfig cfg) {
+    select_kernel(const SelectParams p, const SelectConfig cfg) {
   using Shared = SelShared<kThreads>;
   constexpr int kWarps = kThreads / 32;
-  Shared& sh = shared<kThreads>();
-  uint32_t* keys = reinterpret_cast<uint32_t*>(select_smem + sizeof(Shared));
+  extern __shared__ __align__(16) uint8_t raw[];
+  Shared& sh = *reinterpret_cast<Shared*>(raw);
+  uint32_t* keys = reinterpret_cast<uint32_t*>(raw + sizeof(Shared));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t ctas = sel_ctas(), rank = sel_rank();
   const int32_t t = blockIdx.x / ctas;
@@ -743,7 +632,6 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   // the score kernel writes.
   float m = 0.f;
   if (!all) {
-#pragma unroll 1
     for (int g = tid; g < p.num_heads * kIndexScales; g += kThreads) {
       const uint8_t* src =
           p.q_index + (static_cast<int64_t>(t) * p.num_heads * kIndexScales + g) * (2 * kGroup);
@@ -752,14 +640,14 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
       const int j = g / kIndexScales, part = g % kIndexScales;
       uint32_t c[2];
       float s;
-      sh.q_scale[part][j] = scale_parts(quantize_group(v, c[0], c[1], s));
-      const uint4 e = make_uint4(expand_codes(c[0]), expand_codes(c[0] >> 16), expand_codes(c[1]),
-                                 expand_codes(c[1] >> 16));
-      sh.q_codes[part][j] = e;
-      int mag = __dp4a(static_cast<int>(__vabs4(e.x)), 0x01010101, 0);
-      mag = __dp4a(static_cast<int>(__vabs4(e.y)), 0x01010101, mag);
-      mag = __dp4a(static_cast<int>(__vabs4(e.z)), 0x01010101, mag);
-      mag = __dp4a(static_cast<int>(__vabs4(e.w)), 0x01010101, mag);
+      sh.q_scale[j * kHeadScales + part] = scale_parts(quantize_group(v, c[0], c[1], s));
+      int mag = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t e = expand_codes(c[i >> 1] >> (16 * (i & 1)));
+        sh.q_codes[j * kHeadWords + part * 4 + i] = e;
+        mag = __dp4a(static_cast<int>(__vabs4(e)), 0x01010101, mag);
+      }
       const float w = __ldg(p.weights + static_cast<int64_t>(t) * p.num_heads + j);
       if (part == 0) sh.w[j] = w;
       m = fmaf(fabsf(w), 0.5f * mag * s, m);
@@ -772,13 +660,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   if (tid == 0) sh.failed = 0;
   __syncthreads();
   cudaGridDependencySynchronize();  // the scores are there
-#pragma unroll 1
   for (int i = tid; i < p.score_ctas; i += kThreads)
     if (__ldcg(p.status + i) != 0) sh.failed = 1;
   __syncthreads();
   if (sh.failed || all) {
     if (rank == 0)
-#pragma unroll 1
       for (int64_t i = tid; i < width; i += kThreads)
         out[i] = sh.failed ? -2 : i < seen ? static_cast<int32_t>(i) : -1;
     return;
@@ -786,24 +672,22 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
 
   // The forced blocks are at both ends: k of the n between them are chosen.
   const int granule = min(p.block, kMaxGranule);
-  const Row row = {nullptr, nullptr, p.scores + t * p.score_stride, p.sink, p.block / granule,
-                   (seen + granule - 1) / granule};
+  const MemoryRow row = {p.scores + t * p.score_stride, p.sink, p.block / granule,
+                         (seen + granule - 1) / granule};
   const int32_t n = blocks - p.sink - p.recent;
   const int32_t k = p.num_select - p.sink - p.recent;
   if (k == 0) {
     if (rank == 0) {
-      const int32_t chosen = emit_row<kThreads>(p, row, Border{kTie, kTie, 0}, blocks, seen, out);
-      fill_row<kThreads>(p, out, width, chosen);
+      const int32_t chosen = emit_row<kThreads>(p, sh, row, Border{kTie, kTie, 0}, blocks, out);
+      expand_blocks<kThreads>(p, out, width, seen, chosen);
     }
     return;
   }
   {
     int32_t lead = t;  // first token of t's run
-#pragma unroll 1
     while (lead % p.group != 0 && __ldg(p.q_seq + lead - 1) == seq) --lead;
     uint32_t top = 0;
     const int32_t tiles = (seen + kScoreTile - 1) / kScoreTile;
-#pragma unroll 1
     for (int32_t i = tid; i < tiles; i += kThreads)
       top = __vmaxu4(top, __ldcg(p.smax + lead * p.tiles + i));
     top = __vmaxu4(top, top >> 16);
@@ -820,14 +704,12 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   }
 
   if (n <= cfg.room) {
-    Row dense = row;
-    dense.keys = keys;
-#pragma unroll 4
-    for (int32_t i = tid; i < n; i += kThreads) keys[i] = row.load(i);
+    const DenseRow dense = {keys, p.sink};
+    for (int32_t i = tid; i < n; i += kThreads) keys[i] = row.key(i);
     __syncthreads();
-    const Border border = choose<kThreads>(p, dense, n, k, seq, seen, m);
-    const int32_t chosen = emit_row<kThreads>(p, dense, border, blocks, seen, out);
-    fill_row<kThreads>(p, out, width, chosen);
+    const Border border = choose<kThreads>(p, sh, dense, n, k, seq, seen, m);
+    const int32_t chosen = emit_row<kThreads>(p, sh, dense, border, blocks, out);
+    expand_blocks<kThreads>(p, out, width, seen, chosen);
     return;
   }
 
@@ -840,13 +722,19 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     const float expect = static_cast<float>(from_top) * n / kSample;
     bool listed = expect < 0.9f * cap && blocks <= 32 * cfg.room;
     if (listed) {
-#pragma unroll 1
       for (int32_t i = tid; i < kSample; i += kThreads)
-        keys[i] = row.load(static_cast<int32_t>(static_cast<int64_t>(i) * n / kSample));
+        keys[i] = row.key(static_cast<int32_t>(static_cast<int64_t>(i) * n / kSample));
       __syncthreads();
-      Row sample = row;
-      sample.keys = keys;
-      const uint32_t floor = kth_of_row<kThreads>(sample, kSample, from_top);
+      auto each = [&](auto&& f) {
+        for (int32_t i = tid; i < kSample; i += kThreads) f(keys[i]);
+      };
+      uint32_t lowest, highest;
+      key_range(sh, lowest, highest, each);
+      // Two levels leave the threshold within 2^-14 or so of its value; one
+      // would not, as keys are spaced like exponents and scores of both signs
+      // spread over nearly all of them.
+      const uint32_t floor =
+          kth_largest<kThreads, uint32_t, 2>(sh, lowest, highest, from_top, each);
       const int32_t per = ((n + static_cast<int32_t>(ctas) - 1) / static_cast<int32_t>(ctas) + 3) / 4 * 4;
       const int32_t from = min(static_cast<int32_t>(rank) * per, n);
       const int32_t mine =
@@ -857,7 +745,6 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
         sel_cluster_sync();
         int32_t before = 0;
         count = 0;
-#pragma unroll 1
         for (uint32_t r = 0; r < ctas; ++r) {
           int32_t c;
           asm volatile("ld.shared::cluster.s32 %0, [%1];"
@@ -870,7 +757,6 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
         if (rank > 0 && count <= cap) {
           const uint32_t to_keys = in_rank(smem_u32(keys), 0);
           const uint32_t to_blocks = in_rank(smem_u32(list_blocks), 0);
-#pragma unroll 1
           for (int32_t i = tid; i < mine; i += kThreads) {
             asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to_keys + 4u * (before + i)),
                          "r"(keys[i])
@@ -885,9 +771,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
       if (rank > 0) return;
       listed = count <= cap && count >= k;
       if (listed) {
-        Row list = row;
-        list.keys = keys, list.blocks = list_blocks;
-        const Border border = choose<kThreads>(p, list, count, k, seq, seen, m);
+        const ListRow list = {keys, list_blocks};
+        const Border border = choose<kThreads>(p, sh, list, count, k, seq, seen, m);
         // What lies at the border has to have passed the threshold; the first
         // ones of a tie cannot be told in a list.
         listed = border.lo >= floor && (border.ties == 0 || border.ties == INT32_MAX);
@@ -907,13 +792,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
           }
           __syncthreads();
           const int32_t words = (blocks + 31) / 32;
-#pragma unroll 1
           for (int32_t i = tid; i < words; i += kThreads) keys[i] = 0;
           __syncthreads();
 #pragma unroll
           for (int u = 0; u < kPer; ++u)
             if (mine_in[u] >= 0) atomicOr(&keys[mine_in[u] >> 5], 1u << (mine_in[u] & 31));
-#pragma unroll 1
           for (int32_t i = tid; i < p.sink + p.recent; i += kThreads) {
             const int32_t b = i < p.sink ? i : blocks - 1 - (i - p.sink);
             atomicOr(&keys[b >> 5], 1u << (b & 31));
@@ -923,13 +806,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
           const int32_t share_words = ((words + kWarps - 1) / kWarps + 31) / 32 * 32;
           const int32_t w0 = min(warp * share_words, words), w1 = min(w0 + share_words, words);
           int bits = 0;
-#pragma unroll 1
           for (int32_t i = w0 + lane; i < w1; i += 32) bits += __popc(keys[i]);
           bits = __reduce_add_sync(0xffffffffu, bits);
           int total;
           int at = block_before<kThreads>(lane == 0 ? bits : 0, sh.sum_a, total);
           at = __shfl_sync(0xffffffffu, at, 0);
-#pragma unroll 1
           for (int32_t i0 = w0; i0 < w1; i0 += 32) {
             uint32_t word = i0 + lane < w1 ? keys[i0 + lane] : 0u;
             int upto = __popc(word);
@@ -940,24 +821,19 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
             }
             int64_t slot = at + upto - __popc(word);
             at += __shfl_sync(0xffffffffu, upto, 31);
-#pragma unroll 1
-            for (; word != 0 && slot < p.num_select; word &= word - 1, ++slot) {
-              const int32_t pos = ((i0 + lane) * 32 + __ffs(word) - 1) * p.block;
-#pragma unroll 1
-              for (int32_t i = 0; i < p.block; ++i)
-                out[slot * p.block + i] = pos + i < seen ? pos + i : -1;
-            }
+            for (; word != 0 && slot < p.num_select; word &= word - 1)
+              out[slot++ * p.block] = ((i0 + lane) * 32 + __ffs(word) - 1) * p.block;
           }
-          fill_row<kThreads>(p, out, width, min(total, p.num_select));
+          expand_blocks<kThreads>(p, out, width, seen, min(total, p.num_select));
           return;
         }
       }
       __syncthreads();
     }
     if (rank > 0) return;
-    const Border border = choose<kThreads>(p, row, n, k, seq, seen, m);
-    const int32_t chosen = emit_row<kThreads>(p, row, border, blocks, seen, out);
-    fill_row<kThreads>(p, out, width, chosen);
+    const Border border = choose<kThreads>(p, sh, row, n, k, seq, seen, m);
+    const int32_t chosen = emit_row<kThreads>(p, sh, row, border, blocks, out);
+    expand_blocks<kThreads>(p, out, width, seen, chosen);
   }
 }
 
