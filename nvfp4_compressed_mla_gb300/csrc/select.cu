@@ -498,32 +498,54 @@ __device__ __forceinline__ void expand_blocks(const SelectParams& p, int32_t* ou
   }
 }
 
-// Blocks in order, `row` holding those from p.sink on.
+// The first positions of the chosen blocks in order, `row` holding the blocks
+// from p.sink on; returns how many were chosen. A warp has consecutive blocks:
+// it counts, learns what comes before it, and writes.
 template <int kThreads, typename Row>
 __device__ __forceinline__ int32_t emit_row(const SelectParams& p, SelShared<kThreads>& sh,
-                                         const Row& row, const Border& border, int32_t blocks,
-                                         int32_t* out) {
-  int32_t done = 0, ties = 0;
-  for (int32_t c0 = 0; c0 < blocks; c0 += kThreads) {
-    const int32_t b = c0 + static_cast<int32_t>(threadIdx.x);
-    bool in = b < blocks && (b < p.sink || b >= blocks - p.recent), tie = false;
-    if (b < blocks && !in) {
-      const uint32_t key = row.key(b - p.sink);
-      tie = key == kTie || (key >= border.lo && key <= border.hi);
-      in = key > border.hi && !tie;
-    }
-    int total;
-    if (border.ties > 0) {
-      const int before = block_before<kThreads>(tie, sh.sum_a, total);
-      in = in || (tie && before < border.ties - ties);
-      ties += total;
-    }
-    const int before = block_before<kThreads>(in, sh.sum_b, total);
-    if (in && done + before < p.num_select)
-      out[static_cast<int64_t>(done + before) * p.block] = b * p.block;
-    done += total;
+                                            const Row& row, const Border& border, int32_t blocks,
+                                            int32_t* out) {
+  constexpr int kWarps = kThreads / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int32_t share = ((blocks + kWarps - 1) / kWarps + 31) / 32 * 32;
+  const int32_t from = min(warp * share, blocks), to = min(from + share, blocks);
+  auto state = [&](int32_t b, bool& tie) {
+    tie = false;
+    if (b >= to) return false;
+    if (b < p.sink || b >= blocks - p.recent) return true;
+    const uint32_t key = row.key(b - p.sink);
+    tie = key == kTie || (key >= border.lo && key <= border.hi);
+    return key > border.hi && !tie;
+  };
+  int sure = 0, ties = 0;
+  for (int32_t b0 = from; b0 < to; b0 += 32) {
+    bool tie;
+    const bool in = state(b0 + lane, tie);
+    sure += __popc(__ballot_sync(0xffffffffu, in));
+    ties += __popc(__ballot_sync(0xffffffffu, tie));
   }
-  return min(done, p.num_select);
+  int total;
+  int32_t tie_at = 0;
+  if (border.ties > 0) {
+    tie_at = block_before<kThreads>(lane == 0 ? ties : 0, sh.sum_a, total);
+    tie_at = __shfl_sync(0xffffffffu, tie_at, 0);
+  }
+  const int taken = max(0, min(ties, border.ties - tie_at));
+  int32_t at = block_before<kThreads>(lane == 0 ? sure + taken : 0, sh.sum_b, total);
+  at = __shfl_sync(0xffffffffu, at, 0);
+  for (int32_t b0 = from; b0 < to; b0 += 32) {
+    bool tie;
+    bool in = state(b0 + lane, tie);
+    const uint32_t tied = __ballot_sync(0xffffffffu, tie);
+    in = in || (tie && tie_at + __popc(tied & ((1u << lane) - 1)) < border.ties);
+    tie_at += __popc(tied);
+    const uint32_t chosen = __ballot_sync(0xffffffffu, in);
+    const int32_t slot = at + __popc(chosen & ((1u << lane) - 1));
+    if (in && slot < p.num_select)
+      out[static_cast<int64_t>(slot) * p.block] = (b0 + lane) * p.block;
+    at += __popc(chosen);
+  }
+  return min(total, p.num_select);
 }
 
 __device__ __forceinline__ uint32_t sel_rank() {
@@ -557,7 +579,7 @@ __device__ __forceinline__ int32_t collect(SelShared<kThreads>& sh, const Memory
   const int lane = threadIdx.x & 31;
   if (threadIdx.x == 0) sh.n = 0;
   __syncthreads();
-  constexpr int kQuads = 4;  // 16 keys of a thread at a time
+  constexpr int kQuads = 2;  // 8 keys of a thread at a time
   // one stored score a block, 16-byte aligned: four at once
   const bool vec = row.per == 1 && row.b0 % 4 == 0;
   for (int32_t i0 = from; i0 < to; i0 += kThreads * 4 * kQuads) {
