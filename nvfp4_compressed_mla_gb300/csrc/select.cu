@@ -87,15 +87,20 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
   return f16_bits_to_f32(static_cast<uint16_t>(e4m3x2_to_f16x2(static_cast<uint16_t>(byte))));
 }
 
-constexpr int kHeadWords = 33;  // 32 words of codes; one more keeps lanes' heads in different banks
-constexpr int kHeadScales = 9;
+constexpr int kTokens = 4;                     // that a warp scores at a time
+template <int kN>
+struct Count {
+  static constexpr int value = kN;
+};
+constexpr int kStageWords = kTokens * (32 + 8);  // their codes and scales
 
 template <int kThreads>
 struct SelShared {
   static constexpr int kWarps = kThreads / 32;
   static constexpr int kCands = kThreads;  // candidates ranked from shared memory
-  uint32_t q_codes[NVFP4_MLA_MAX_HEADS * kHeadWords];  // signed bytes, twice the values
-  uint32_t q_scale[NVFP4_MLA_MAX_HEADS * kHeadScales];
+  uint4 q_codes[kIndexScales][NVFP4_MLA_MAX_HEADS];  // signed bytes, twice the values
+  uint4 stage[kWarps][kStageWords / 4];
+  uint16_t q_scale[kIndexScales][NVFP4_MLA_MAX_HEADS];
   float w[NVFP4_MLA_MAX_HEADS];
   uint32_t hist[kBins];
   uint64_t cand_key[kCands];              // fp64 score, as a key
@@ -215,83 +220,124 @@ __device__ __forceinline__ void key_range(SelShared<kThreads>& sh, uint32_t& low
 }
 
 // ------------------------------------------------------------ exact scores
-// One position's dot products with all heads as exact integers in units of
-// 2^-20, lane = head, 32 heads at a time, and their weighted sum: in fp32 with
-// an error bound, or in fp64. One warp.
+// Dot products of `n` consecutive positions (1 .. kTok) with all heads as
+// exact integers in units of 2^-20, lane = head, 32 heads at a time, and their
+// weighted sums: in fp32 with an error bound, or in fp64. One warp; the keys go
+// through shared memory, where a 16-byte broadcast serves 16 codes, and the
+// heads' codes are read once for all the positions.
 struct TokenScore {
   float value, error;
   double exact;
   bool none;  // -inf: a NaN, or a page that does not resolve
 };
-template <bool kExact, typename Shared>
-__device__ __forceinline__ TokenScore score_token(const SelectParams& p, const Shared& sh,
-                                                  int32_t seq, int32_t pos) {
+template <bool kExact, int kTok, int kThreads>
+__device__ __forceinline__ void score_tokens(const SelectParams& p, SelShared<kThreads>& sh,
+                                             int32_t seq, int32_t pos, int n,
+                                             TokenScore (&r)[kTok]) {
   const int lane = threadIdx.x & 31;
-  TokenScore r = {0.f, 0.f, 0.0, true};
-  const IndexRow at = resolve_index_row(seq, pos, p.block_table, p.num_seqs, p.max_blocks,
-                                        p.page_size, p.num_blocks, p.block_stride);
-  if (at.page < 0) return r;
-  const uint8_t* page = p.cache + at.page;
-  const uint32_t mine = expand_codes(__ldg(reinterpret_cast<const uint16_t*>(
-      page + static_cast<int64_t>(at.row) * kIndexCodes + lane * 2)));
-  const uint32_t byte = __ldg(page + static_cast<int64_t>(p.page_size) * kIndexCodes +
-                              static_cast<int64_t>(at.row) * kIndexScales + (lane & 7)) &
-                        0x7Fu;
-  if (__any_sync(0xffffffffu, byte == 0x7Fu)) return r;
-  r.none = false;
-  const uint32_t parts = scale_parts(byte);
+  uint4* codes = sh.stage[threadIdx.x >> 5];
+  uint32_t* scales = reinterpret_cast<uint32_t*>(codes + kTokens * 8);
+  const IndexRow at =
+      resolve_index_row(seq, pos + min(lane & (kTok - 1), n - 1), p.block_table, p.num_seqs,
+                        p.max_blocks, p.page_size, p.num_blocks, p.block_stride);
+  uint32_t word[kTok], byte[kTok];
+#pragma unroll
+  for (int t = 0; t < kTok; ++t) {
+    const int64_t page = __shfl_sync(0xffffffffu, static_cast<int64_t>(at.page), t);
+    const int64_t row = __shfl_sync(0xffffffffu, at.row, t);
+    word[t] = 0, byte[t] = 0x7Fu;
+    if (t < n && page >= 0) {
+      const uint8_t* base = p.cache + page;
+      word[t] = __ldg(reinterpret_cast<const uint16_t*>(base + row * kIndexCodes + lane * 2));
+      byte[t] = __ldg(base + static_cast<int64_t>(p.page_size) * kIndexCodes + row * kIndexScales +
+                      (lane & 7)) &
+                0x7Fu;
+    }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int t = 0; t < kTok; ++t) {
+    r[t] = {0.f, 0.f, 0.0, __any_sync(0xffffffffu, byte[t] == 0x7Fu) != 0};
+    if (t < n) {
+      reinterpret_cast<uint32_t*>(codes)[t * 32 + lane] = expand_codes(word[t]);
+      if (lane < 8) scales[t * 8 + lane] = scale_parts(byte[t]);
+    }
+  }
+  __syncwarp();
+#pragma unroll 1
   for (int j0 = 0; j0 < p.num_heads; j0 += 32) {
     const int j = min(j0 + lane, p.num_heads - 1);
-    const uint32_t* q = sh.q_codes + j * kHeadWords;
-    int64_t d = 0;
-#pragma unroll
+    int64_t d[kTok] = {};
+#pragma unroll(kTok == 1 ? kIndexScales : 2)
     for (int g = 0; g < kIndexScales; ++g) {
-      int dot = 0;
+      const uint4 q = sh.q_codes[g][j];
+      const uint32_t qs = sh.q_scale[g][j];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        dot = __dp4a(static_cast<int>(q[4 * g + i]),
-                     static_cast<int>(__shfl_sync(0xffffffffu, mine, 4 * g + i)), dot);
-      const uint32_t ks = __shfl_sync(0xffffffffu, parts, g);
-      const uint32_t qs = sh.q_scale[j * kHeadScales + g];
-      dot *= static_cast<int>((ks & 255u) * (qs & 255u));
-      d += static_cast<int64_t>(dot) << ((ks >> 8) + (qs >> 8));
+      for (int t = 0; t < kTok; ++t) {
+        if (t >= n) break;
+        const uint4 k = codes[t * 8 + g];
+        const uint32_t ks = scales[t * 8 + g];
+        int dot = __dp4a(static_cast<int>(q.x), static_cast<int>(k.x), 0);
+        dot = __dp4a(static_cast<int>(q.y), static_cast<int>(k.y), dot);
+        dot = __dp4a(static_cast<int>(q.z), static_cast<int>(k.z), dot);
+        dot = __dp4a(static_cast<int>(q.w), static_cast<int>(k.w), dot);
+        dot *= static_cast<int>((ks & 255u) * (qs & 255u));
+        d[t] += static_cast<int64_t>(dot) << ((ks >> 8) + (qs >> 8));
+      }
     }
-    if (d < 0 || j0 + lane >= p.num_heads) d = 0;
-    if (kExact) {
-      // most weights of zero dot products need no fp64
-      if (__any_sync(0xffffffffu, d > 0))
-        r.exact += static_cast<double>(sh.w[j]) * (static_cast<double>(d) * 0x1p-20);
-    } else {
-      const float f = fmaf(static_cast<float>(static_cast<int32_t>(d >> 24)), 16777216.f,
-                           static_cast<float>(static_cast<int32_t>(d & 0xFFFFFF))) *
-                      0x1p-20f;
-      r.value = fmaf(sh.w[j], f, r.value);
-      r.error = fmaf(fabsf(sh.w[j]), f, r.error);
-      if (f > 0.f && sh.w[j] != 0.f) r.error += kTiny;  // never 0 by underflow
+    const float w = sh.w[j];
+#pragma unroll
+    for (int t = 0; t < kTok; ++t) {
+      if (t >= n) break;
+      if (d[t] < 0 || j0 + lane >= p.num_heads) d[t] = 0;
+      if (kExact) {
+        // most weights of zero dot products need no fp64
+        if (__any_sync(0xffffffffu, d[t] > 0))
+          r[t].exact += static_cast<double>(w) * (static_cast<double>(d[t]) * 0x1p-20);
+      } else {
+        const float f = fmaf(static_cast<float>(static_cast<int32_t>(d[t] >> 24)), 16777216.f,
+                             static_cast<float>(static_cast<int32_t>(d[t] & 0xFFFFFF))) *
+                        0x1p-20f;
+        r[t].value = fmaf(w, f, r[t].value);
+        r[t].error = fmaf(fabsf(w), f, r[t].error);
+        if (f > 0.f && w != 0.f) r[t].error += kTiny;  // never 0 by underflow
+      }
     }
   }
 #pragma unroll
-  for (int s = 16; s > 0; s >>= 1) {
+  for (int t = 0; t < kTok; ++t) {
+    if (t >= n) break;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) {
+      if (kExact) {
+        r[t].exact += __shfl_xor_sync(0xffffffffu, r[t].exact, s);
+      } else {
+        r[t].value += __shfl_xor_sync(0xffffffffu, r[t].value, s);
+        r[t].error += __shfl_xor_sync(0xffffffffu, r[t].error, s);
+      }
+    }
     if (kExact) {
-      r.exact += __shfl_xor_sync(0xffffffffu, r.exact, s);
+      r[t].none = r[t].none || r[t].exact != r[t].exact;
     } else {
-      r.value += __shfl_xor_sync(0xffffffffu, r.value, s);
-      r.error += __shfl_xor_sync(0xffffffffu, r.error, s);
+      r[t].error = r[t].error == 0.f ? 0.f : __fadd_ru(__fmul_ru(r[t].error, kSumError), kTiny);
+      r[t].none = r[t].none || r[t].value != r[t].value;
     }
   }
-  if (kExact) {
-    r.none = r.exact != r.exact;
-  } else {
-    r.error = r.error == 0.f ? 0.f : __fadd_ru(__fmul_ru(r.error, kSumError), kTiny);
-    r.none = r.value != r.value;
-  }
-  return r;
 }
-template <typename Shared>
-__device__ __forceinline__ uint64_t exact_key(const SelectParams& p, const Shared& sh, int32_t seq,
-                                              int32_t pos) {
-  const TokenScore r = score_token<true>(p, sh, seq, pos);
-  return r.none ? kLowest64 : key64(r.exact);
+// The highest fp64 score of `n` consecutive positions, as a key.
+template <int kTok, int kThreads>
+__device__ __forceinline__ uint64_t exact_key(const SelectParams& p, SelShared<kThreads>& sh,
+                                              int32_t seq, int32_t pos, int n) {
+  TokenScore r[kTok];
+  score_tokens<true, kTok>(p, sh, seq, pos, n, r);
+  uint64_t best = 0;
+#pragma unroll
+  for (int t = 0; t < kTok; ++t) {
+    if (t >= n) break;
+    const uint64_t key = r[t].none ? kLowest64 : key64(r[t].exact);
+    best = best > key ? best : key;
+  }
+  return best;
 }
 
 // ------------------------------------------------------------- the choice
@@ -306,8 +352,8 @@ struct Border {
 // by position and their blocks, and takes marks (kIn, kTie, kOut).
 template <int kThreads, typename Row>
 __device__ __forceinline__ Border choose(const SelectParams& p, SelShared<kThreads>& sh,
-                                         const Row& row, int32_t count, int32_t k, int32_t seq,
-                                         int32_t seen, float m) {
+                                         const Row& row, const float* scores, int32_t count,
+                                         int32_t k, int32_t seq, int32_t seen, float m) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kWarps = kThreads / 32;
   auto each = [&](auto&& f) {
@@ -345,21 +391,51 @@ __device__ __forceinline__ Border choose(const SelectParams& p, SelShared<kThrea
   int32_t want = k - in;  // 1 <= want <= cands
   if (cands == want) return {lo, hi, INT32_MAX};  // all of them
 
-  const int shift = __ffs(p.block) - 1;
+  // A warp's piece of a candidate: consecutive positions. None of a granule
+  // whose stored score is more than eps2 below the block's can be its highest.
+  const int per_piece = min(p.block, kTokens), piece_shift = __ffs(p.block / per_piece) - 1;
+  const int granule = min(p.block, kMaxGranule);
+  auto piece = [&](int i, int& c, int32_t& pos) {  // how many positions
+    c = i >> piece_shift;
+    const int off = (i & ((1 << piece_shift) - 1)) * per_piece;
+    const int64_t b = row.block(sh.cand[c]), first = b * p.block + off;
+    if (first >= seen) return 0;
+    pos = static_cast<int32_t>(first);
+    if (granule < p.block && bounded &&
+        __ldcg(scores + b * (p.block / granule) + off / granule) <
+            __fadd_rd(unkey32(row.key(sh.cand[c])), -eps2))
+      return 0;
+    return min(per_piece, seen - pos);
+  };
   if (cands <= SelShared<kThreads>::kCands) {
     for (int i = tid; i < cands; i += kThreads)
       sh.cand_key[i] = 0, sh.cand_lo[i] = sh.cand_hi[i] = 0;
     __syncthreads();
-    for (int i = warp; i < cands << shift; i += kWarps) {
-      const int c = i >> shift;
-      const int64_t pos = static_cast<int64_t>(row.block(sh.cand[c])) * p.block + (i & (p.block - 1));
-      if (pos >= seen) continue;
-      const TokenScore r = score_token<false>(p, sh, seq, static_cast<int32_t>(pos));
-      if (lane == 0) {
-        atomicMax(&sh.cand_lo[c], key32(r.none ? -INFINITY : __fsub_rd(r.value, r.error)));
-        atomicMax(&sh.cand_hi[c], key32(r.none ? -INFINITY : __fadd_ru(r.value, r.error)));
+    auto rescore = [&](auto tokens) {
+      constexpr int kTok = decltype(tokens)::value;
+#pragma unroll 1
+      for (int i = warp; i < cands << piece_shift; i += kWarps) {
+        int c;
+        int32_t pos;
+        const int of = piece(i, c, pos);
+        if (of == 0) continue;
+        TokenScore r[kTok];
+        score_tokens<false, kTok>(p, sh, seq, pos, of, r);
+        float low = -INFINITY, high = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < kTok; ++t) {
+          if (t >= of) break;
+          if (r[t].none) continue;
+          low = fmaxf(low, __fsub_rd(r[t].value, r[t].error));
+          high = fmaxf(high, __fadd_ru(r[t].value, r[t].error));
+        }
+        if (lane == 0) {
+          atomicMax(&sh.cand_lo[c], key32(low));
+          atomicMax(&sh.cand_hi[c], key32(high));
+        }
       }
-    }
+    };
+    if (p.block == 1) rescore(Count<1>{}); else rescore(Count<kTokens>{});
     __syncthreads();
     // Known by their intervals: in where fewer than `want` others can be
     // above, out where `want` others are. sh.cand_key: 0 open, 1 in, 2 out.
@@ -382,12 +458,15 @@ __device__ __forceinline__ Border choose(const SelectParams& p, SelShared<kThrea
       __syncthreads();
       for (int i = tid; i < cands; i += kThreads) sh.cand_key[i] = 0;
       __syncthreads();
-      for (int i = warp; i < cands << shift; i += kWarps) {
-        const int c = i >> shift;
-        if (sh.cand_lo[c] == 0) continue;
-        const int64_t pos = static_cast<int64_t>(row.block(sh.cand[c])) * p.block + (i & (p.block - 1));
-        if (pos >= seen) continue;
-        const uint64_t key = exact_key(p, sh, seq, static_cast<int32_t>(pos));
+#pragma unroll 1
+      for (int i = warp; i < cands << piece_shift; i += kWarps) {
+        if (sh.cand_lo[i >> piece_shift] == 0) continue;
+        int c;
+        int32_t pos;
+        const int of = piece(i, c, pos);
+        if (of == 0) continue;
+        const uint64_t key = p.block == 1 ? exact_key<1>(p, sh, seq, pos, 1)
+                                          : exact_key<kTokens>(p, sh, seq, pos, of);
         if (lane == 0)
           atomicMax(reinterpret_cast<unsigned long long*>(&sh.cand_key[c]),
                     static_cast<unsigned long long>(key));
@@ -416,8 +495,9 @@ __device__ __forceinline__ Border choose(const SelectParams& p, SelShared<kThrea
   auto exact = [&](int32_t i) {  // one warp
     uint64_t best = 0;
     const int64_t first = static_cast<int64_t>(row.block(i)) * p.block;
-    for (int64_t pos = first; pos < first + p.block && pos < seen; ++pos) {
-      const uint64_t e = exact_key(p, sh, seq, static_cast<int32_t>(pos));
+    for (int64_t pos = first; pos < first + p.block && pos < seen; pos += per_piece) {
+      const uint64_t e = exact_key<kTokens>(p, sh, seq, static_cast<int32_t>(pos),
+                                            min(per_piece, seen - static_cast<int32_t>(pos)));
       best = best > e ? best : e;
     }
     return best;
@@ -662,14 +742,15 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
       const int j = g / kIndexScales, part = g % kIndexScales;
       uint32_t c[2];
       float s;
-      sh.q_scale[j * kHeadScales + part] = scale_parts(quantize_group(v, c[0], c[1], s));
+      sh.q_scale[part][j] = static_cast<uint16_t>(scale_parts(quantize_group(v, c[0], c[1], s)));
       int mag = 0;
+      uint32_t e[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t e = expand_codes(c[i >> 1] >> (16 * (i & 1)));
-        sh.q_codes[j * kHeadWords + part * 4 + i] = e;
-        mag = __dp4a(static_cast<int>(__vabs4(e)), 0x01010101, mag);
+        e[i] = expand_codes(c[i >> 1] >> (16 * (i & 1)));
+        mag = __dp4a(static_cast<int>(__vabs4(e[i])), 0x01010101, mag);
       }
+      sh.q_codes[part][j] = make_uint4(e[0], e[1], e[2], e[3]);
       const float w = __ldg(p.weights + static_cast<int64_t>(t) * p.num_heads + j);
       if (part == 0) sh.w[j] = w;
       m = fmaf(fabsf(w), 0.5f * mag * s, m);
@@ -729,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     const DenseRow dense = {keys, p.sink};
     for (int32_t i = tid; i < n; i += kThreads) keys[i] = row.key(i);
     __syncthreads();
-    const Border border = choose<kThreads>(p, sh, dense, n, k, seq, seen, m);
+    const Border border = choose<kThreads>(p, sh, dense, row.scores, n, k, seq, seen, m);
     const int32_t chosen = emit_row<kThreads>(p, sh, dense, border, blocks, out);
     expand_blocks<kThreads>(p, out, width, seen, chosen);
     return;
@@ -742,7 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     const float share = static_cast<float>(k) * kSample / static_cast<float>(n);
     uint32_t from_top = static_cast<uint32_t>(share + 4.f * sqrtf(share) + 8.f);
     const float expect = static_cast<float>(from_top) * n / kSample;
-    bool listed = expect < 0.9f * cap && blocks <= 32 * cfg.room;
+    bool listed = expect < 0.9f * cap && (blocks + 127) / 128 * 4 <= cfg.room;
     if (listed) {
       for (int32_t i = tid; i < kSample; i += kThreads)
         keys[i] = row.key(static_cast<int32_t>(static_cast<int64_t>(i) * n / kSample));
@@ -794,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
       listed = count <= cap && count >= k;
       if (listed) {
         const ListRow list = {keys, list_blocks};
-        const Border border = choose<kThreads>(p, sh, list, count, k, seq, seen, m);
+        const Border border = choose<kThreads>(p, sh, list, row.scores, count, k, seq, seen, m);
         // What lies at the border has to have passed the threshold; the first
         // ones of a tie cannot be told in a list.
         listed = border.lo >= floor && (border.ties == 0 || border.ties == INT32_MAX);
@@ -806,6 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
           for (int u = 0; u < kPer; ++u) {
             const int32_t i = u * kThreads + tid;
             mine_in[u] = -1;
+            if (u * kThreads >= count) continue;
             if (i < count) {
               const uint32_t key = keys[i];
               if (key > border.hi || (border.ties > 0 && key >= border.lo))
@@ -813,38 +895,46 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
             }
           }
           __syncthreads();
-          const int32_t words = (blocks + 31) / 32;
-          for (int32_t i = tid; i < words; i += kThreads) keys[i] = 0;
+          uint4* bits4 = reinterpret_cast<uint4*>(keys);
+          const int32_t quads = (blocks + 127) / 128;
+          for (int32_t i = tid; i < quads; i += kThreads) bits4[i] = make_uint4(0, 0, 0, 0);
           __syncthreads();
 #pragma unroll
           for (int u = 0; u < kPer; ++u)
-            if (mine_in[u] >= 0) atomicOr(&keys[mine_in[u] >> 5], 1u << (mine_in[u] & 31));
+            if (u * kThreads < count && mine_in[u] >= 0) atomicOr(&keys[mine_in[u] >> 5], 1u << (mine_in[u] & 31));
           for (int32_t i = tid; i < p.sink + p.recent; i += kThreads) {
             const int32_t b = i < p.sink ? i : blocks - 1 - (i - p.sink);
             atomicOr(&keys[b >> 5], 1u << (b & 31));
           }
           __syncthreads();
-          // a warp's share of the words, 32 at a time
-          const int32_t share_words = ((words + kWarps - 1) / kWarps + 31) / 32 * 32;
-          const int32_t w0 = min(warp * share_words, words), w1 = min(w0 + share_words, words);
+          // a warp's share of the bits, 32 lanes x 128 at a time
+          const int32_t share4 = ((quads + kWarps - 1) / kWarps + 31) / 32 * 32;
+          const int32_t w0 = min(warp * share4, quads), w1 = min(w0 + share4, quads);
           int bits = 0;
-          for (int32_t i = w0 + lane; i < w1; i += 32) bits += __popc(keys[i]);
+          for (int32_t i = w0 + lane; i < w1; i += 32) {
+            const uint4 v = bits4[i];
+            bits += __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w);
+          }
           bits = __reduce_add_sync(0xffffffffu, bits);
           int total;
           int at = block_before<kThreads>(lane == 0 ? bits : 0, sh.sum_a, total);
           at = __shfl_sync(0xffffffffu, at, 0);
           for (int32_t i0 = w0; i0 < w1; i0 += 32) {
-            uint32_t word = i0 + lane < w1 ? keys[i0 + lane] : 0u;
-            int upto = __popc(word);
+            const uint4 v = i0 + lane < w1 ? bits4[i0 + lane] : make_uint4(0, 0, 0, 0);
+            const int mine_bits = __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w);
+            int upto = mine_bits;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
               const int o = __shfl_up_sync(0xffffffffu, upto, d);
               if (lane >= d) upto += o;
             }
-            int64_t slot = at + upto - __popc(word);
+            int64_t slot = at + upto - mine_bits;
             at += __shfl_sync(0xffffffffu, upto, 31);
-            for (; word != 0 && slot < p.num_select; word &= word - 1)
-              out[slot++ * p.block] = ((i0 + lane) * 32 + __ffs(word) - 1) * p.block;
+            const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              for (uint32_t left = word[u]; left != 0 && slot < p.num_select; left &= left - 1)
+                out[slot++ * p.block] = (((i0 + lane) * 4 + u) * 32 + __ffs(left) - 1) * p.block;
           }
           expand_blocks<kThreads>(p, out, width, seen, min(total, p.num_select));
           return;
@@ -853,7 +943,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
       __syncthreads();
     }
     if (rank > 0) return;
-    const Border border = choose<kThreads>(p, sh, row, n, k, seq, seen, m);
+    const Border border = choose<kThreads>(p, sh, row, row.scores, n, k, seq, seen, m);
     const int32_t chosen = emit_row<kThreads>(p, sh, row, border, blocks, out);
     expand_blocks<kThreads>(p, out, width, seen, chosen);
   }
