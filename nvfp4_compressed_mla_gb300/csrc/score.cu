@@ -216,9 +216,33 @@ struct Bars {  // byte offsets in the control block
                        kDEmpty = kDFull + 64, kQFull = kDEmpty + 64, kQEmpty = kQFull + 16,
                        kDrain = kQEmpty + 16, kTurn = kDrain + 16, kScaleDrain = kTurn + 16,
                        kTmem = kScaleDrain + 8 * kScaleWarps, kAbort = kTmem + 4,
-                       kStart = kAbort + 4, kEnd = kStart + 32;
+                       kStart = kAbort + 4,
+                       // steps that each copying warp has issued, and each scale
+                       // warp committed, when it ends
+                       kIssued = kStart + 32, kCommitted = kIssued + 4 * kCopyWarps,
+                       kEnd = kCommitted + 4 * kScaleWarps;
 };
 static_assert(Bars::kStart % 8 == 0, "start words");
+// An aborted CTA's code copies land before it ends. Every role has ended: no
+// one else arrives at the stages any more, except for scale commits under way,
+// which are counted. Step n is copy warp n % kCopyWarps' and scale warp
+// n % kScaleWarps'. A stage is issued once its last content has been used, so
+// only the newest `stages` steps can be in flight; a stage that is copied and
+// has no scales lacks exactly the scale warp's arrival.
+__device__ __noinline__ void drain_codes(uint32_t ctl, uint32_t stages) {
+  uint32_t end = 0;  // behind the newest step that was issued
+  for (uint32_t w = 0; w < kCopyWarps; ++w) {
+    const uint32_t n = ld_shared_u32(ctl + Bars::kIssued + 4 * w);
+    if (n > 0) end = max(end, w + (n - 1) * kCopyWarps + 1);
+  }
+  for (uint32_t n = end > stages ? end - stages : 0; n < end; ++n) {
+    if (n / kCopyWarps >= ld_shared_u32(ctl + Bars::kIssued + 4 * (n % kCopyWarps))) continue;
+    const uint32_t full = ctl + Bars::kFull + 8 * (n % stages);
+    if (n / kScaleWarps >= ld_shared_u32(ctl + Bars::kCommitted + 4 * (n % kScaleWarps)))
+      mbar_arrive(full);
+    drain(full, (n / stages) & 1u);
+  }
+}
 constexpr int kCtl = kMaskBytes;  // the control block follows the masks
 constexpr int kStageBase = (kCtl + Bars::kEnd + 1023) / 1024 * 1024;  // stages, then two Q buffers
 
@@ -305,10 +329,6 @@ struct Ring {
   __device__ __forceinline__ void advance(uint32_t steps) {  // at most `stages`
     stage += steps;
     if (stage >= stages) stage -= stages, phase ^= 1u;
-  }
-  __device__ __forceinline__ void back() {
-    if (stage == 0) stage = stages, phase ^= 1u;
-    --stage;
   }
 };
 
@@ -481,6 +501,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   }
   const int64_t begin = total * blockIdx.x / p.ctas, end = total * (blockIdx.x + 1) / p.ctas;
   if (begin == end) {
+    cudaGridDependencySynchronize();  // this grid does not end before the encoding
     if (tid == 0) p.s.status[blockIdx.x] = 0;
     return;
   }
@@ -680,16 +701,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       at.advance(kCopyWarps);
       ++issued;
     }
-    __syncwarp();
-    if (!ok) {
-      // Copies in flight land before the CTA ends: this lane stands in for the
-      // scale warps on stages that they have left.
-      for (uint32_t k = min(issued, (p.stages + kCopyWarps - 1u) / kCopyWarps); k > 0; --k) {
-        for (int i = 0; i < kCopyWarps; ++i) at.back();
-        if (lane == 0) mbar_arrive(bar(Bars::kFull, at.stage));
-        drain(bar(Bars::kFull, at.stage), at.phase);
-      }
-    }
+    if (lane == 0) st_shared_u32(ctl + Bars::kIssued + 4 * (warp - kLoadWarp0), issued);
   } else if (p.seg_rows > 0 && warp < kScaleWarp0 + kScaleWarps) {
     // ----------------------------------------------- scales, tensor copies
     // Lane l has lines l, l + 32, .. of the step: the scales of each tile's
@@ -714,6 +726,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     then.live = now.live = false;
     uint4 vals[kLines];   // now's scales, of an even and an odd position
     uint32_t valid = 0;   // bit t + 2 i: position t of line l + 32 i resolves
+    uint32_t committed = 0;
     bool ok = true;
     // A turn's page ids are loaded two turns ahead, its scales one. Nothing is
     // in flight at the fence, which would wait for it.
@@ -764,6 +777,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
                                      h * 512));
           mma_commit(bar(Bars::kFull, stage));
         }
+        ++committed;
         const uint32_t most = top.of_warp();
         if (lane < kStepTiles) p.s.smax[now.q * p.s.tiles + now.step * kStepTiles + lane] = most;
       }
@@ -801,6 +815,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
         turns.done();
       }
     }
+    if (lane == 0) st_shared_u32(ctl + Bars::kCommitted + 4 * (warp - kScaleWarp0), committed);
     if (issuer) {  // scale copies of an aborted CTA have completed
       mma_commit(bar(Bars::kScaleDrain, warp - kScaleWarp0));
       drain(bar(Bars::kScaleDrain, warp - kScaleWarp0), 0);
@@ -1051,6 +1066,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (p.seg_rows > 0 && tid == 32 * kLoadWarp0 && ld_shared_u32(abort_addr) != 0)
+    drain_codes(ctl, static_cast<uint32_t>(p.stages));
   if (warp == kMmaWarp0) tmem_dealloc(tmem);
   if (tid == 0) p.s.status[blockIdx.x] = ld_shared_u32(abort_addr);
 }

@@ -266,3 +266,102 @@ def test_sizes_that_fill_the_device(seqs, length, per_seq, heads, num, block, pa
     got, ref = c.run(num, block), reference_on_device(c, num, block)
     bad = np.nonzero((got != ref).any(1))[0]
     assert bad.size == 0, (bad.size, bad[:5], got[bad[0]][:20], ref[bad[0]][:20])
+
+
+def test_more_query_tokens_than_the_workspace_takes_at_a_time():
+    import nvfp4_compressed_mla_gb300 as nm
+    c = Case(23, [700, 333], 80, 16, width=8192)
+    per_q = nm.sparse_mla_select_workspace_size(1, 16, 8192, 64)
+    n = nm.sparse_mla_select_workspace_size(160, 16, 8192, 64)
+    assert n < 140 * per_q  # parts of fewer than 160
+    c.check(40)
+
+
+def test_on_a_stream_of_its_own():
+    c = Case(24, [700, 2000], 3, 16)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    import nvfp4_compressed_mla_gb300 as nm
+    args = c.device()
+    torch.cuda.synchronize()
+    a = nm.sparse_mla_select(*args, 64, stream=side)
+    with torch.cuda.stream(side):
+        b = nm.sparse_mla_select(*args, 64)
+    e = nm.sparse_mla_select(*args, 64, stream=side.cuda_stream)
+    side.synchronize()
+    for got in (a, b, e):
+        assert np.array_equal(got.cpu().numpy(), c.ref(64))
+
+
+def test_two_calls_at_once():
+    cases = [Case(25, [9000, 2000], 1, 64), Case(26, [3000, 100, 7000], 2, 32)]
+    import nvfp4_compressed_mla_gb300 as nm
+    args, refs = [c.device() for c in cases], [c.ref(256) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(nm.sparse_mla_select(*args[i], 256))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert np.array_equal(g.cpu().numpy(), refs[i])
+
+
+def test_python_arguments_that_are_refused():
+    import nvfp4_compressed_mla_gb300 as nm
+    c = Case(27, [300, 40], 1, 16)
+    args = c.device()
+
+    def bad(i, t):
+        a = list(args)
+        a[i] = t
+        with pytest.raises(ValueError):
+            nm.sparse_mla_select(*a, 16)
+
+    q, w, seq, pos, table, _, pool = args[:7]
+    bad(0, q.float())                       # type
+    bad(0, q[:, :, :64])                    # width
+    bad(0, q.cpu())                         # device
+    bad(0, q.transpose(0, 1))               # strides
+    bad(1, w[:, :8])
+    bad(1, w.double())
+    bad(2, seq[:1])                         # too few
+    bad(3, pos.long())
+    bad(4, table.view(-1))
+    bad(4, table.cpu())
+    bad(6, pool[:-1])                       # a page short
+    with pytest.raises(ValueError):
+        nm.sparse_mla_select(*args, 16, topk_idx=torch.empty((2, 15), dtype=torch.int32, device="cuda"))
+    for kw in (dict(select_block=3), dict(select_block=256), dict(sink_blocks=-1),
+               dict(sink_blocks=9, recent_blocks=8)):
+        with pytest.raises(nm.NativeError):
+            nm.sparse_mla_select(*args, 16, **kw)
+    with pytest.raises(nm.NativeError):
+        nm.sparse_mla_select(*args, 0)
+    assert np.array_equal(c.run(16), c.ref(16))
+
+
+# page 64: tensor copies; page 48: copies row by row
+@pytest.mark.parametrize("page", [64, 48])
+@pytest.mark.parametrize("heads,per_seq", [(16, 1), (64, 4), (128, 2)])
+def test_waits_that_run_out_give_minus_two_and_the_next_launch_is_correct(page, heads, per_seq):
+    import nvfp4_compressed_mla_gb300 as nm
+    # ten steps or more an SM, so that stages are taken a second time: a long
+    # sequence that has the same pages again and again
+    c = Case(28, [4000, 333], per_seq, heads, page=page)
+    c.table = np.tile(c.table[:, :4000 // page], (1, 100))
+    c.pos[:per_seq] += c.table.shape[1] * page - 4000
+    args = c.device()
+    want = nm.sparse_mla_select(*args, 64).clone()
+    nm.nvfp4_mla_set_wait_limit(200)
+    try:
+        for _ in range(3):
+            got = nm.sparse_mla_select(*args, 64)
+            torch.cuda.synchronize()
+            assert bool((got == -2).all()), "no wait ran out under a 200-cycle bound"
+    finally:
+        nm.nvfp4_mla_set_wait_limit(0)
+    assert torch.equal(nm.sparse_mla_select(*args, 64), want)
