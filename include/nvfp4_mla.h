@@ -336,7 +336,8 @@ int32_t nvfp4_mla_stage_fp8(const int32_t* q_seq, const int32_t* topk_idx, int32
  *   seq_ids, positions  device int32 [max_tokens]: the step's tokens, packed
  *                in sequence order; rows behind the last token get -1. They
  *                are what nvfp4_mla_append, nvfp4_mla_index_append and
- *                sparse_mla_select (as q_seq, q_pos) take
+ *                sparse_mla_select (as q_seq, q_pos) take (nvfp4_mla_append
+ *                adds the rows behind the last token to its invalid_count)
  *   slots        nullable device int64 [max_tokens]: page * page_size + row,
  *                -1 behind the last token or where the page id is negative
  *   cu_tokens    nullable device int32 [num_seqs + 1]: first token of each
