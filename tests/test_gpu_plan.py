@@ -80,6 +80,30 @@ def test_plan_long_prompt_and_idle_sequences():
     assert_same(run_plan(new, lens, table, 64, free, len(free), 131072), ref)
 
 
+@pytest.mark.parametrize("page", [1, 3, 7, 48, 1000, 2 ** 20 - 1, 2 ** 20])
+@pytest.mark.parametrize("tokens", [3000, 12000])  # one CTA, a cluster
+def test_plan_page_sizes_and_lengths_up_to_the_last_token(page, tokens):
+    rng = np.random.default_rng(page)
+    width = min((2 ** 31 - 1) // page, 2047)
+    room = width * page
+    lens = np.minimum([0, page, page * 5 + 1, 2 * page - 1, room - 700, room - 900], room)
+    lens = np.maximum(lens, 0).astype(np.int32)
+    new = np.minimum([300, 1, 700, 2, 700, 901], room - lens).astype(np.int32)
+    new[5] = room - lens[5] + 1  # one too many
+    if tokens > 3000:
+        new[2] = min(9000, room - int(lens[2]))
+    table, free, _ = sc.random_tables(rng, lens, page, 4000, width)
+    ref = sc.plan_step(new, lens, table, page, free, len(free), tokens)
+    assert ref["refused"] >= 1
+    assert_same(run_plan(new, lens, table, page, free, len(free), tokens), ref)
+    after = ref["seq_lens"]
+    stack = np.concatenate([free[:ref["free_count"]], np.full(9000, -7, np.int32)])
+    back = sc.truncate(lens, after, ref["table"], page, stack, ref["free_count"])
+    got = run_truncate(lens, after, ref["table"], page, stack, ref["free_count"])
+    assert_same(got, back)
+    assert np.array_equal(back["free_pages"][:len(free)], free)
+
+
 def test_plan_nothing_to_do_and_no_rows():
     rng = np.random.default_rng(2)
     lens = rng.integers(0, 500, 40).astype(np.int32)
