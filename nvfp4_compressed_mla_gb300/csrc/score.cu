@@ -308,6 +308,9 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm,
       "l"(reinterpret_cast<uint64_t>(tm)), "r"(0), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
+__device__ __forceinline__ void prefetch_l2(const void* at) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+}
 // Largest of the bytes (E4M3 scales, positive) of words, in the high bytes of
 // 16-bit values, two of which one instruction compares.
 struct TopByte {
@@ -722,16 +725,17 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     const int32_t step_pages = max(kStep >> p.page_shift, 1);
     Turns turns(warp - kScaleWarp0, kScaleWarps, p.stages);
     walk.t1 = 0;
-    Turn then, now;
-    then.live = now.live = false;
+    Turn later, then, now;
+    later.live = then.live = now.live = false;
     uint4 vals[kLines];   // now's scales, of an even and an odd position
     uint32_t valid = 0;   // bit t + 2 i: position t of line l + 32 i resolves
     uint32_t committed = 0;
     bool ok = true;
-    // A turn's page ids are loaded two turns ahead, its scales one. Nothing is
-    // in flight at the fence, which would wait for it.
+    // A turn's page ids are loaded three turns ahead, its scales fetched into L2
+    // two and loaded one turn ahead. Nothing is in flight at the fence, which
+    // would wait for it.
 #pragma unroll 1
-    for (int ahead = 2; ahead > 0 || now.live; --ahead) {
+    for (int ahead = 3; ahead > 0 || now.live; --ahead) {
       if (ahead <= 0) {
         const uint32_t stage = now.stage;
         ok = warp_wait(bar(Bars::kEmpty, stage), now.phase ^ 1u, abort_addr, lim);
@@ -801,17 +805,27 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
           valid |= (pos < most ? 1u << 2 * i : 0u) | (pos + 1 < most ? 2u << 2 * i : 0u);
         }
       }
-      // the page ids of the one after it
-      then.live = turns.next(walk, p);
+      // the scales of the one after it, a line of 16 rows a lane
+      then = later;
       if (then.live) {
-        then.q = walk.q, then.most = walk.most;
-        then.step = turns.step, then.it = turns.it;
-        then.stage = turns.at.stage, then.phase = turns.at.phase;
-        then.first = (turns.step * kStep) >> p.page_shift;
-        then.page = -1;
-        if (lane < step_pages && (then.first + lane) << p.page_shift < walk.most)
-          then.page = __ldg(p.s.block_table + static_cast<int64_t>(walk.seq) * p.s.max_blocks +
-                            then.first + lane);
+        constexpr uint32_t kRows = 128 / kIndexScales;
+        const uint32_t pos = static_cast<uint32_t>(then.step) * kStep + lane % (kStep / kRows) * kRows;
+        const uint32_t page = __shfl_sync(0xffffffffu, then.page,
+                                          (pos >> p.page_shift) - static_cast<uint32_t>(then.first));
+        if (lane < kStep / kRows && page < static_cast<uint32_t>(p.s.num_blocks))
+          prefetch_l2(scales + static_cast<uint64_t>(page) * stride + (pos & in_page) * kIndexScales);
+      }
+      // the page ids of the one after that
+      later.live = turns.next(walk, p);
+      if (later.live) {
+        later.q = walk.q, later.most = walk.most;
+        later.step = turns.step, later.it = turns.it;
+        later.stage = turns.at.stage, later.phase = turns.at.phase;
+        later.first = (turns.step * kStep) >> p.page_shift;
+        later.page = -1;
+        if (lane < step_pages && (later.first + lane) << p.page_shift < walk.most)
+          later.page = __ldg(p.s.block_table + static_cast<int64_t>(walk.seq) * p.s.max_blocks +
+                             later.first + lane);
         turns.done();
       }
     }
