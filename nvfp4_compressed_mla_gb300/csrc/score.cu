@@ -157,24 +157,17 @@ template <int kPending>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
-// 16 consecutive TMEM columns of this thread's lane
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+// 8 consecutive TMEM columns of this thread's lane
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15}, [%16];"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
+        "=r"(r[7])
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ float relu_nan(float x) {  // max(0, x), NaN stays NaN
-  float r;
-  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(x));
-  return r;
-}
-// 2 max(0, x), exact, NaN stays NaN: an addition, where the maximum takes the
-// slower integer pipe; the epilogue uses one for half of the heads each.
+// 2 max(0, x), exact, NaN stays NaN: an addition; the maximum takes the slower
+// integer pipe.
 __device__ __forceinline__ float twice_relu(float x) { return x + fabsf(x); }
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
   uint64_t r;
@@ -568,47 +561,56 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
             ok = warp_wait(bar(Bars::kDFull, slot), (n / kSlots) & 1u, abort_addr, lim);
             if (!ok) break;
             tc_fence_after();
-            // 16 heads at a time, of all the slot's tiles: a weight's way from
-            // shared memory into 32 lanes' registers is what bounds this loop,
-            // so each one is used for every tile.
+            // 8 heads at a time, of all the slot's tiles: a weight's way from
+            // shared memory into 32 lanes' registers costs as much as its use,
+            // so each one is used for every tile. The next ones are loaded
+            // while these are worked on.
             const uint32_t d = tmem + lanes + slot * kSlotCols;
             uint64_t acc[kSlotTiles][4];
 #pragma unroll
             for (int t = 0; t < kSlotTiles; ++t)
               acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0;
+            uint32_t v[2][kSlotTiles][8];
+            ulonglong2 wj[2][2];
+            auto fetch = [&](int to, int c) {
+#pragma unroll
+              for (int t = 0; t < kSlotTiles; ++t) tmem_ld8(d + t * kHeads + c, v[to][t]);
+              wj[to][0] = w[c / 4], wj[to][1] = w[c / 4 + 1];
+            };
+            fetch(0, 0);
 #pragma unroll 1
             for (int c = 0; c < kHeads; c += 16) {
-              uint32_t v[kSlotTiles][16];
 #pragma unroll
-              for (int t = 0; t < kSlotTiles; ++t) tmem_ld16(d + t * kHeads + c, v[t]);
-              ulonglong2 wj[4];
+              for (int h = 0; h < 2; ++h) {
+                tmem_ld_wait();
+                if (h == 0) {
+                  fetch(1, c + 8);
+                } else if (c + 16 < kHeads) {
+                  fetch(0, c + 16);
+                } else {  // the slot has been read
+                  tc_fence_before();
+                  __syncwarp();
+                  if (lane == 0) mbar_arrive(bar(Bars::kDEmpty, slot));
+                }
 #pragma unroll
-              for (int j = 0; j < 4; ++j) wj[j] = w[c / 4 + j];  // four weights
-              tmem_ld_wait();
-              if (c + 16 == kHeads) {  // the slot has been read
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(Bars::kDEmpty, slot));
-              }
+                for (int j = 0; j < 2; ++j) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-#pragma unroll
-                for (int t = 0; t < kSlotTiles; ++t) {
-                  fma2(acc[t][j & 1],
-                       pack2(relu_nan(__uint_as_float(v[t][4 * j])),
-                             relu_nan(__uint_as_float(v[t][4 * j + 1]))),
-                       wj[j].x);
-                  fma2(acc[t][2 + (j & 1)],
-                       pack2(twice_relu(__uint_as_float(v[t][4 * j + 2])),
-                             twice_relu(__uint_as_float(v[t][4 * j + 3]))),
-                       wj[j].y);
+                  for (int t = 0; t < kSlotTiles; ++t) {
+                    const uint32_t* x = v[h][t] + 4 * j;
+                    fma2(acc[t][j],
+                         pack2(twice_relu(__uint_as_float(x[0])), twice_relu(__uint_as_float(x[1]))),
+                         wj[h][j].x);
+                    fma2(acc[t][2 + j],
+                         pack2(twice_relu(__uint_as_float(x[2])), twice_relu(__uint_as_float(x[3]))),
+                         wj[h][j].y);
+                  }
                 }
               }
             }
 #pragma unroll
             for (int t = 0; t < kSlotTiles; ++t)
-              score[u * kSlotTiles + t] = fmaf(sum2(acc[t][2]) + sum2(acc[t][3]), 0.5f,
-                                               sum2(acc[t][0]) + sum2(acc[t][1]));
+              score[u * kSlotTiles + t] = ((sum2(acc[t][2]) + sum2(acc[t][3])) +
+                                           (sum2(acc[t][0]) + sum2(acc[t][1]))) * 0.5f;
           }
           if (!ok) break;
 #pragma unroll
