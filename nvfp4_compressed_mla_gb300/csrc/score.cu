@@ -538,6 +538,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     const int granule = min(p.s.block, kMaxGranule);
     const int shift = __ffs(granule) - 1;
     uint32_t first = 0, step_no = 0, run = 0;  // first: number of the step's first unit
+    uint32_t done = 0;  // units of this set
     int next = set < kSets ? set : INT32_MAX;  // units from there to this set's next
     bool ok = true;
 #pragma unroll 1
@@ -555,12 +556,26 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
           const int32_t seen = __shfl_sync(0xffffffffu, walk.seen, i);
           const auto* w = reinterpret_cast<const ulonglong2*>(weights + i * kImage);
           float score[kStepTiles];  // of positions pos, pos + 1
+          uint32_t mask[kStepTiles];
 #pragma unroll
           for (int u = 0; u < kUnitSlots; ++u) {
-            const uint32_t n = (first + i) * kUnitSlots + u, slot = n % kSlots;
-            ok = warp_wait(bar(Bars::kDFull, slot), (n / kSlots) & 1u, abort_addr, lim);
+            uint32_t slot, parity;
+            if constexpr (kUnitSlots == 1 && kSlots % kSets == 0) {  // every kSets-th slot is this set's
+              slot = set + kSets * (done % (kSlots / kSets));
+              parity = done / (kSlots / kSets) & 1u;
+            } else {
+              const uint32_t n = (first + i) * kUnitSlots + u;
+              slot = n % kSlots;
+              parity = n / kSlots & 1u;
+            }
+            ok = warp_wait(bar(Bars::kDFull, slot), parity, abort_addr, lim);
             if (!ok) break;
             tc_fence_after();
+            if (u == 0) {
+#pragma unroll
+              for (int t = 0; t < kStepTiles; ++t)
+                mask[t] = ld_shared_u32(base + ((step_no * kStepTiles + t) % kMaskRing * 4 + quad) * 4);
+            }
             // 8 heads at a time, of all the slot's tiles: a weight's way from
             // shared memory into 32 lanes' registers costs as much as its use,
             // so each one is used for every tile. The next ones are loaded
@@ -613,12 +628,10 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
                                            (sum2(acc[t][0]) + sum2(acc[t][1]))) * 0.5f;
           }
           if (!ok) break;
+          ++done;
 #pragma unroll
           for (int t = 0; t < kStepTiles; ++t) {
-            const uint32_t mask =
-                ld_shared_u32(base + ((step_no * kStepTiles + t) % kMaskRing * 4 + quad) * 4);
-            const bool real =
-                pos + t < seen && (mask >> lane & 1u) && score[t] == score[t];
+            const bool real = pos + t < seen && (mask[t] >> lane & 1u) && score[t] == score[t];
             score[t] = real ? score[t] + 0.f : -INFINITY;
           }
           float* row = out + i * p.s.score_stride;
@@ -627,9 +640,11 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
             if (live) *reinterpret_cast<float2*>(row + pos) = make_float2(score[0], score[1]);
           } else {
             float m = fmaxf(score[0], score[1]);
-#pragma unroll 1
-            for (int s = 1; s < granule / 2; s <<= 1)
-              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+#pragma unroll
+            for (int s = 1; s < kMaxGranule / 2; s <<= 1) {
+              const float o = __shfl_xor_sync(0xffffffffu, m, s);
+              if (s < granule / 2) m = fmaxf(m, o);
+            }
             if (live && (pos & (granule - 1)) == 0) row[pos >> shift] = m;
           }
         }
