@@ -63,6 +63,9 @@ __device__ __forceinline__ uint64_t key64(double a) {
   const uint64_t u = static_cast<uint64_t>(__double_as_longlong(a + 0.0));
   return u >> 63 ? ~u : u | (1ull << 63);
 }
+__device__ __forceinline__ uint32_t load_volatile(const uint32_t* at) {
+  return *static_cast<const volatile uint32_t*>(at);
+}
 constexpr uint64_t kLowest64 = 0x000FFFFFFFFFFFFFull;  // key64(-inf)
 
 // An E2M1 code as an integer: twice its value.
@@ -324,6 +327,21 @@ __device__ __forceinline__ void score_tokens(const SelectParams& p, SelShared<kT
     }
   }
 }
+// Raises the bounds of a block's highest score by those of `n` consecutive
+// positions.
+template <int kTok, int kThreads>
+__device__ __forceinline__ void widen(const SelectParams& p, SelShared<kThreads>& sh, int32_t seq,
+                                      int32_t pos, int n, float& low, float& high) {
+  TokenScore r[kTok];
+  score_tokens<false, kTok>(p, sh, seq, pos, n, r);
+#pragma unroll
+  for (int t = 0; t < kTok; ++t) {
+    if (t >= n) break;
+    if (r[t].none) continue;
+    low = fmaxf(low, __fsub_rd(r[t].value, r[t].error));
+    high = fmaxf(high, __fadd_ru(r[t].value, r[t].error));
+  }
+}
 // The highest fp64 score of `n` consecutive positions, as a key.
 template <int kTok, int kThreads>
 __device__ __forceinline__ uint64_t exact_key(const SelectParams& p, SelShared<kThreads>& sh,
@@ -347,6 +365,90 @@ struct Border {
   uint32_t lo, hi;
   int32_t ties;
 };
+
+// The border where more scores lie next to it than can be listed, mostly among
+// equal ones: the want-th largest of the keys lo .. hi.
+template <int kThreads, typename Row>
+__device__ __forceinline__ Border choose_unlisted(const SelectParams& p, SelShared<kThreads>& sh,
+                                               const Row& row, int32_t count, int32_t want,
+                                               int32_t seq, int32_t seen, uint32_t lo,
+                                               uint32_t hi) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kWarps = kThreads / 32;
+  const int per_piece = min(p.block, kTokens);
+  auto pieces = [&](int32_t i, auto&& each) {  // until each() is false; one warp
+    const int64_t first = static_cast<int64_t>(row.block(i)) * p.block;
+#pragma unroll 1
+    for (int64_t pos = first; pos < first + p.block && pos < seen; pos += per_piece)
+      if (!each(static_cast<int32_t>(pos), min(per_piece, seen - static_cast<int32_t>(pos)))) break;
+  };
+  // Scores of 0 are exact in fp32: where the border lies among them, one pass
+  // tells who is above and who is equal.
+  const bool capped =
+      __syncthreads_or(tid < p.num_heads && sh.w[min(tid, p.num_heads - 1)] > 0.f) == 0;
+  if (lo <= key32(0.f) && key32(0.f) <= hi) {
+    int above = 0, equal = 0, open = 0;
+#pragma unroll 1
+    for (int32_t i = warp; i < count; i += kWarps) {
+      const uint32_t key = row.key(i);
+      if (key < lo || key > hi) continue;
+      float low = -INFINITY, high = -INFINITY;
+      pieces(i, [&](int32_t pos, int of) {
+        widen<kTokens>(p, sh, seq, pos, of, low, high);
+        return !(capped && low == 0.f);
+      });
+      if (capped) high = fminf(high, 0.f);
+      __syncwarp();
+      const bool in = low > 0.f, out = high < 0.f, tie = low == 0.f && high == 0.f;
+      if (lane == 0) {
+        above += in, equal += tie, open += !(in || out || tie);
+        if (in || out || tie) row.mark(i, in ? kIn : tie ? kTie : kOut);
+      }
+      __syncwarp();
+    }
+    above = block_sum<kThreads>(above, sh.sum_a);
+    equal = block_sum<kThreads>(equal, sh.sum_a);
+    open = block_sum<kThreads>(open, sh.sum_a);
+    if (open == 0 && above < want && want <= above + equal) return {lo, hi, want - above};
+  }
+
+  // The want-th largest fp64 score, computed anew in each step, then a mark for
+  // each candidate. Marks are candidates' from before.
+  auto candidate = [&](int32_t i) {
+    const uint32_t key = row.key(i);
+    return (key >= lo && key <= hi) || key == kIn || key == kTie || key == kOut;
+  };
+  auto exact = [&](int32_t i) {  // one warp
+    uint64_t best = 0;
+    pieces(i, [&](int32_t pos, int of) {
+      const uint64_t e = exact_key<kTokens>(p, sh, seq, pos, of);
+      best = best > e ? best : e;
+      return true;
+    });
+    return best;
+  };
+  auto each_exact = [&](auto&& f) {
+#pragma unroll 1
+    for (int32_t i = warp; i < count; i += kWarps) {
+      if (!candidate(i)) continue;
+      const uint64_t e = exact(i);
+      if (lane == 0) f(e);
+    }
+  };
+  uint32_t rank = want;
+  const uint64_t edge = kth_largest<kThreads, uint64_t>(sh, uint64_t{0}, ~uint64_t{0}, rank,
+                                                        each_exact);
+#pragma unroll 1
+  for (int32_t i = warp; i < count; i += kWarps) {
+    if (!candidate(i)) continue;
+    const uint64_t e = exact(i);
+    __syncwarp();
+    if (lane == 0) row.mark(i, e > edge ? kIn : e == edge ? kTie : kOut);
+    __syncwarp();
+  }
+  __syncthreads();
+  return {lo, hi, static_cast<int32_t>(rank)};
+}
 
 // The border of the k highest of the `count` keys of a row. `row` gives keys
 // by position and their blocks, and takes marks (kIn, kTie, kOut).
@@ -396,8 +498,10 @@ __device__ __forceinline__ Border choose(const SelectParams& p, SelShared<kThrea
   const int per_piece = min(p.block, kTokens), piece_shift = __ffs(p.block / per_piece) - 1;
   const int granule = min(p.block, kMaxGranule);
   auto piece = [&](int i, int& c, int32_t& pos) {  // how many positions
-    c = i >> piece_shift;
-    const int off = (i & ((1 << piece_shift) - 1)) * per_piece;
+    // the candidates' first pieces, then their second ones, ..
+    const int part = piece_shift == 0 ? 0 : i / cands;
+    c = i - part * cands;
+    const int off = part * per_piece;
     const int64_t b = row.block(sh.cand[c]), first = b * p.block + off;
     if (first >= seen) return 0;
     pos = static_cast<int32_t>(first);
@@ -410,7 +514,9 @@ __device__ __forceinline__ Border choose(const SelectParams& p, SelShared<kThrea
   if (cands <= SelShared<kThreads>::kCands) {
     for (int i = tid; i < cands; i += kThreads)
       sh.cand_key[i] = 0, sh.cand_lo[i] = sh.cand_hi[i] = 0;
-    __syncthreads();
+    // Without a positive weight no score is above 0, and a block that has one
+    // of 0 is known.
+    const bool capped = __syncthreads_or(tid < p.num_heads && sh.w[min(tid, p.num_heads - 1)] > 0.f) == 0;
     auto rescore = [&](auto tokens) {
       constexpr int kTok = decltype(tokens)::value;
 #pragma unroll 1
@@ -419,16 +525,11 @@ __device__ __forceinline__ Border choose(const SelectParams& p, SelShared<kThrea
         int32_t pos;
         const int of = piece(i, c, pos);
         if (of == 0) continue;
-        TokenScore r[kTok];
-        score_tokens<false, kTok>(p, sh, seq, pos, of, r);
+        if (capped && __shfl_sync(0xffffffffu, load_volatile(&sh.cand_lo[c]), 0) == key32(0.f))
+          continue;
         float low = -INFINITY, high = -INFINITY;
-#pragma unroll
-        for (int t = 0; t < kTok; ++t) {
-          if (t >= of) break;
-          if (r[t].none) continue;
-          low = fmaxf(low, __fsub_rd(r[t].value, r[t].error));
-          high = fmaxf(high, __fadd_ru(r[t].value, r[t].error));
-        }
+        widen<kTok>(p, sh, seq, pos, of, low, high);
+        if (capped) high = fminf(high, 0.f);
         if (lane == 0) {
           atomicMax(&sh.cand_lo[c], key32(low));
           atomicMax(&sh.cand_hi[c], key32(high));
@@ -452,19 +553,22 @@ __device__ __forceinline__ Border choose(const SelectParams& p, SelShared<kThrea
       sure += state == 1;
     }
     want -= block_sum<kThreads>(sure, sh.sum_a);
-    // The best of the others by their fp64 scores.
+    // The best of the others by their fp64 scores, which an interval of one
+    // value gives too. sh.cand_hi: 0 known, 1 to be scored, 2 open and exact.
     if (want > 0) {
-      for (int i = tid; i < cands; i += kThreads) sh.cand_lo[i] = sh.cand_key[i] == 0 ? 1u : 0u;
-      __syncthreads();
-      for (int i = tid; i < cands; i += kThreads) sh.cand_key[i] = 0;
+      for (int i = tid; i < cands; i += kThreads) {
+        const uint32_t low = sh.cand_lo[i];
+        const bool exact = low == sh.cand_hi[i];
+        sh.cand_hi[i] = sh.cand_key[i] != 0 ? 0u : exact ? 2u : 1u;
+        sh.cand_key[i] = exact ? key64(static_cast<double>(unkey32(low))) : 0u;
+      }
       __syncthreads();
 #pragma unroll 1
       for (int i = warp; i < cands << piece_shift; i += kWarps) {
-        if (sh.cand_lo[i >> piece_shift] == 0) continue;
         int c;
         int32_t pos;
         const int of = piece(i, c, pos);
-        if (of == 0) continue;
+        if (of == 0 || sh.cand_hi[c] != 1) continue;
         const uint64_t key = p.block == 1 ? exact_key<1>(p, sh, seq, pos, 1)
                                           : exact_key<kTokens>(p, sh, seq, pos, of);
         if (lane == 0)
@@ -473,12 +577,12 @@ __device__ __forceinline__ Border choose(const SelectParams& p, SelShared<kThrea
       }
       __syncthreads();
       for (int i = tid; i < cands; i += kThreads) {
-        if (sh.cand_lo[i] == 0) continue;
+        if (sh.cand_hi[i] == 0) continue;
         const uint64_t key = sh.cand_key[i];
         const int32_t b = row.block(sh.cand[i]);
         int better = 0;
         for (int j = 0; j < cands; ++j)
-          better += sh.cand_lo[j] != 0 &&
+          better += sh.cand_hi[j] != 0 &&
                     (sh.cand_key[j] > key || (sh.cand_key[j] == key && row.block(sh.cand[j]) < b));
         row.mark(sh.cand[i], better < want ? kIn : kOut);
       }
@@ -490,39 +594,7 @@ __device__ __forceinline__ Border choose(const SelectParams& p, SelShared<kThrea
     return {lo, hi, 0};
   }
 
-  // Too many to list (a border among equal scores): the want-th largest fp64
-  // score, computed anew in each step, then a mark for each candidate.
-  auto exact = [&](int32_t i) {  // one warp
-    uint64_t best = 0;
-    const int64_t first = static_cast<int64_t>(row.block(i)) * p.block;
-    for (int64_t pos = first; pos < first + p.block && pos < seen; pos += per_piece) {
-      const uint64_t e = exact_key<kTokens>(p, sh, seq, static_cast<int32_t>(pos),
-                                            min(per_piece, seen - static_cast<int32_t>(pos)));
-      best = best > e ? best : e;
-    }
-    return best;
-  };
-  auto each_exact = [&](auto&& f) {
-    for (int32_t i = warp; i < count; i += kWarps) {
-      const uint32_t key = row.key(i);
-      if (key < lo || key > hi) continue;
-      const uint64_t e = exact(i);
-      if (lane == 0) f(e);
-    }
-  };
-  rank = want;
-  const uint64_t edge = kth_largest<kThreads, uint64_t>(sh, uint64_t{0}, ~uint64_t{0}, rank,
-                                                        each_exact);
-  for (int32_t i = warp; i < count; i += kWarps) {
-    const uint32_t key = row.key(i);
-    if (key < lo || key > hi) continue;
-    const uint64_t e = exact(i);
-    __syncwarp();
-    if (lane == 0) row.mark(i, e > edge ? kIn : e == edge ? kTie : kOut);
-    __syncwarp();
-  }
-  __syncthreads();
-  return {lo, hi, static_cast<int32_t>(rank)};
+  return choose_unlisted<kThreads>(p, sh, row, count, want, seq, seen, lo, hi);
 }
 
 // ------------------------------------------------------------------- rows

@@ -365,3 +365,33 @@ def test_waits_that_run_out_give_minus_two_and_the_next_launch_is_correct(page, 
     finally:
         nm.nvfp4_mla_set_wait_limit(0)
     assert torch.equal(nm.sparse_mla_select(*args, 64), want)
+
+
+@pytest.mark.parametrize("heads,block,num,lens", [
+    (1, 1, 50, [9000, 2592, 40]), (1, 1, 6000, [9000, 2592]), (1, 128, 4, [5240, 2000, 5239]),
+    (4, 16, 14, [2592, 2591, 700]), (3, 4, 100, [9000, 333]), (1, 64, 30, [9000]),
+    (2, 1, 2048, [70000]), (1, 2, 3000, [40000]),
+])
+def test_weights_of_one_sign(heads, block, num, lens):
+    # without a positive weight the highest scores are zeros, and ties go to the lower index
+    c = Case(heads * block + num, lens, 2, heads)
+    c.w = -np.abs(c.w) - np.float32(1e-3)
+    c.check(num, block)
+    c.check(num, block, min(2, num // 2), min(1, num // 2))
+    c.w = -c.w  # the lowest scores are zeros
+    c.check(num, block)
+
+
+@pytest.mark.parametrize("block,num", [(1, 700), (1, 5000), (8, 60), (128, 5)])
+def test_scores_that_cancel(block, num):
+    # two equal heads with opposite weights: every score is 0, by a sum that fp32 bounds but
+    # does not settle, or by dot products that are all 0
+    c = Case(29, [9000, 1300], 2, 2)
+    c.q[:, 1] = c.q[:, 0]
+    c.w[:, 0], c.w[:, 1] = 0.7, -0.7
+    c.check(num, block)
+    # and a third head that tells some of them apart
+    d = Case(30, [9000, 1300], 2, 3)
+    d.q[:, 1] = d.q[:, 0]
+    d.w[:, 0], d.w[:, 1], d.w[:, 2] = 0.7, -0.7, 1e-9
+    d.check(num, block)
