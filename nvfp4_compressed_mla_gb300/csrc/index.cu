@@ -8,6 +8,9 @@
 // bytes of codes, one scale byte; the eight scale bytes of a token go through
 // one lane as one 8-byte word. HBM-bound for a chunk of tokens (256 + 72
 // bytes each), launch-bound for a step of a few.
+// Measured (GB300, device time): 66 tokens 2.5 us to write and 2.1 to read back;
+// 32768 tokens 6.0 us (10.7 MB, 1.8 TB/s: the chain of block-table, key and row
+// accesses of a single wave of CTAs) and 4.2 us (2.6 TB/s).
 #include "index_common.cuh"
 
 namespace nvfp4_mla {

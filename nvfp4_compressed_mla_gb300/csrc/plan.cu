@@ -9,7 +9,12 @@
 // The plan's prefix sums are computed by every CTA of the cluster over all
 // sequences, which costs less than exchanging partial sums; its in-place
 // updates wait for the cluster barrier behind which nobody reads the old
-// lengths any more.
+// lengths any more. With many token rows their index arithmetic bounds it
+// (eight SMs work on them).
+//
+// Measured (GB300, device time): 66 rows of 66 sequences 5.4 us, 131072 rows of
+// 1021 sequences 16.5 us (2.1 MB, 0.3 us at the copy rate); drafts of 66
+// sequences taken back 4.6 us, a quarter of 1021 sequences released 11.5 us.
 #include "common.cuh"
 
 namespace nvfp4_mla {
@@ -449,7 +454,7 @@ extern "C" int32_t nvfp4_mla_truncate(const int32_t* keep_lens, const int32_t* s
   const TruncateParams p = {keep_lens,  seq_lens,      num_seqs,   block_table,  max_blocks_per_seq,
                             page_division(page_size), free_pages, free_capacity, free_count, seq_lens_out,
                             free_count_out, dropped_count};
-  const int ctas = num_seqs > kPlanWarps ? kMaxCluster : 1;  // a warp per sequence
+  const int ctas = num_seqs > kPlanWarps ? kMaxCluster : 1;  // a warp per sequence, as far as 256
   return launch_cluster(truncate_kernel, p, ctas, 4u * static_cast<size_t>(num_seqs),
                         static_cast<cudaStream_t>(stream));
 }
