@@ -187,7 +187,8 @@ int32_t sparse_mla_decode(const void* q_latent, const void* q_rope, const int32_
  * tensor memory and writes NaN to its outputs and LSE (or workspace
  * partials), so a stalled launch ends with a visible result instead of
  * holding its SMs. 0 restores the default of 2^31 cycles (about a second).
- * Process-wide; applies to decode launches enqueued after the call. A bound
+ * Process-wide; applies to decode launches enqueued after the call, and to
+ * those of sparse_mla_select, whose rows are then -2. A bound
  * shorter than a healthy launch's waits makes healthy launches fail, which
  * is how the failure path is tested. Returns NVFP4_MLA_ERR_VALUE if
  * cycles < 0. This is this library's choice; the post has no counterpart.
