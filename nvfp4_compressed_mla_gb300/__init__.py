@@ -318,12 +318,15 @@ def nvfp4_mla_truncate(keep_lens: torch.Tensor, seq_lens: torch.Tensor, block_ta
 
 
 # ------------------------------------------------- index-key cache and selection
-def _pool(cache: torch.Tensor, num_blocks: int, block_stride_bytes: int, device: int) -> int:
-    """Device pointer of a pool that holds num_blocks pages (the last one need not be padded)."""
+def _pool(cache: torch.Tensor, num_blocks: int, block_stride_bytes: int, page_size: int,
+          device: int) -> int:
+    """Device pointer of a pool that holds num_blocks pages; it may end with the last page's rows
+    (a layer's view of a pool that interleaves several)."""
+    least = (num_blocks - 1) * block_stride_bytes + page_size * INDEX_ROW_BYTES
     if (not cache.is_contiguous() or cache.get_device() != device
-            or cache.numel() * cache.element_size() < num_blocks * block_stride_bytes):
-        raise ValueError("cache must be a contiguous tensor of num_blocks * block_stride_bytes "
-                         "bytes on the current CUDA device")
+            or cache.numel() * cache.element_size() < least):
+        raise ValueError("cache must be a contiguous tensor that reaches to the end of page "
+                         "num_blocks - 1, on the current CUDA device")
     return cache.data_ptr()
 
 
@@ -340,7 +343,7 @@ def nvfp4_mla_index_append(keys: torch.Tensor, seq_ids: torch.Tensor, positions:
     st = _lib().nvfp4_mla_index_append(
         _arg(keys, "keys", torch.bfloat16, 0, dev), _arg(seq_ids, "seq_ids", i32, n, dev),
         _arg(positions, "positions", i32, n, dev), n, table, num_seqs, max_blocks, page_size,
-        _pool(cache, num_blocks, block_stride_bytes, dev), num_blocks, block_stride_bytes,
+        _pool(cache, num_blocks, block_stride_bytes, page_size, dev), num_blocks, block_stride_bytes,
         _opt(invalid_count, "invalid_count", i32, 1, dev), _stream(stream))
     _check(st, "nvfp4_mla_index_append")
 
@@ -359,7 +362,7 @@ def nvfp4_mla_index_read(seq_ids: torch.Tensor, positions: torch.Tensor,
     st = _lib().nvfp4_mla_index_read(
         _arg(seq_ids, "seq_ids", i32, n, dev), _arg(positions, "positions", i32, n, dev), n,
         table, num_seqs, max_blocks, page_size,
-        _pool(cache, num_blocks, block_stride_bytes, dev), num_blocks, block_stride_bytes,
+        _pool(cache, num_blocks, block_stride_bytes, page_size, dev), num_blocks, block_stride_bytes,
         _arg(keys, "keys", torch.bfloat16, n * INDEX_DIM, dev),
         _opt(invalid_count, "invalid_count", i32, 1, dev), _stream(stream))
     _check(st, "nvfp4_mla_index_read")
@@ -404,7 +407,7 @@ def sparse_mla_select(q_index: torch.Tensor, weights: torch.Tensor, q_seq: torch
         _arg(q_index, "q_index", torch.bfloat16, 0, dev),
         _arg(weights, "weights", torch.float32, num_q * H, dev), _arg(q_seq, "q_seq", i32, num_q, dev),
         _arg(q_pos, "q_pos", i32, num_q, dev), num_q, H, table, num_seqs, max_blocks, page_size,
-        _pool(cache, num_blocks, block_stride_bytes, dev), num_blocks, block_stride_bytes,
+        _pool(cache, num_blocks, block_stride_bytes, page_size, dev), num_blocks, block_stride_bytes,
         select_block, num_select, sink_blocks, recent_blocks,
         _arg(topk_idx, "topk_idx", i32, num_q * width, dev),
         None if workspace is None else _arg(workspace, "workspace", workspace.dtype, 0, dev),

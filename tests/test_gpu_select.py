@@ -395,3 +395,44 @@ def test_scores_that_cancel(block, num):
     d.q[:, 1] = d.q[:, 0]
     d.w[:, 0], d.w[:, 1], d.w[:, 2] = 0.7, -0.7, 1e-9
     d.check(num, block)
+
+
+@pytest.mark.parametrize("page", [64, 48])
+def test_a_layer_of_a_pool_that_holds_several(page):
+    # page p of layer l at (p * layers + l) pages: the last layer's last page ends the pool
+    import nvfp4_compressed_mla_gb300 as nm
+    layers, bytes_ = 3, page * sc.ROW
+    cases = [Case(31, [900, 1300], 2, 16, page=page) for _ in range(layers)]
+    pool = torch.empty(cases[0].blocks * layers * bytes_, dtype=torch.uint8, device="cuda:0")
+    whole = pool.view(cases[0].blocks, layers, bytes_)
+    for i, c in enumerate(cases):
+        c.pool = sc.random_pool(np.random.default_rng(40 + i), c.blocks, page, bytes_)
+        whole[:, i] = dev(c.pool).view(c.blocks, bytes_)
+    for i, c in enumerate(cases):
+        a = c.device()
+        view = pool[i * bytes_:]
+        got = nm.sparse_mla_select(*a[:6], view, c.blocks, layers * bytes_, 40)
+        assert np.array_equal(got.cpu().numpy(), c.ref(40))
+        keys = torch.randn((1, 128), device="cuda:0").bfloat16()
+        at = [dev(np.array([x], np.int32)) for x in (1, 1299)]
+        nm.nvfp4_mla_index_append(keys, *at, a[4], page, view, c.blocks, layers * bytes_)
+        k = nm.nvfp4_mla_index_read(*at, a[4], page, view, c.blocks, layers * bytes_)
+        codes, scales = sc.quantize(keys.view(torch.int16).cpu().numpy().view(np.uint16))
+        assert np.array_equal(k.float().cpu().numpy(), sc.values(codes, scales))
+        with pytest.raises(ValueError):  # a byte short of the last page's end
+            nm.sparse_mla_select(*a[:6], pool[i * bytes_:pool.numel() - (layers - 1 - i) * bytes_ - 1],
+                                 c.blocks, layers * bytes_, 40)
+
+
+@pytest.mark.parametrize("page", [64, 48])
+def test_pages_past_4_gib(page):
+    import nvfp4_compressed_mla_gb300 as nm
+    c = Case(32, [1500, 700], 3, 32, page=page)
+    stride = (160 << 20) + 16
+    pool = torch.empty(c.blocks * stride, dtype=torch.uint8, device="cuda:0")
+    assert pool.numel() > 5 << 30
+    pool.view(c.blocks, stride)[:, :page * sc.ROW] = dev(c.pool).view(c.blocks, -1)
+    a = c.device()
+    for block, num in ((1, 50), (16, 6)):
+        got = nm.sparse_mla_select(*a[:6], pool, c.blocks, stride, num, block)
+        assert np.array_equal(got.cpu().numpy(), c.ref(num, block))
