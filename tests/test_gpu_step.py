@@ -139,3 +139,18 @@ def test_steps_of_a_server(captured, num, block):
     # nvfp4_mla_append counts every token that does not resolve, padding among them
     assert int(s.d["bad"]) == padding and int(s.d["index_bad"]) == 0
     assert int(s.d["refused"]) == 1
+
+
+def test_the_stream_that_a_call_takes():
+    import nvfp4_compressed_mla_gb300 as nm
+    assert nm._stream(None) == torch.cuda.current_stream().cuda_stream
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        assert nm._stream(None) == side.cuda_stream
+        with torch.cuda.stream(torch.cuda.default_stream()):
+            assert nm._stream(None) == torch.cuda.default_stream().cuda_stream
+    assert nm._stream(side) == side.cuda_stream == nm._stream(side.cuda_stream)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        assert nm._stream(None) == torch.cuda.current_stream().cuda_stream
+        torch.zeros(1, device="cuda:0")
