@@ -391,23 +391,35 @@ __device__ __forceinline__ Border choose_unlisted(const SelectParams& p, SelShar
       __syncthreads_or(tid < p.num_heads && sh.w[min(tid, p.num_heads - 1)] > 0.f) == 0;
   if (lo <= key32(0.f) && key32(0.f) <= hi) {
     int above = 0, equal = 0, open = 0;
+    int zeros = 0;     // capped: found so far by all warps, and
+    bool sure = true;  // nothing undecided before them
 #pragma unroll 1
-    for (int32_t i = warp; i < count; i += kWarps) {
-      const uint32_t key = row.key(i);
-      if (key < lo || key > hi) continue;
-      float low = -INFINITY, high = -INFINITY;
-      pieces(i, [&](int32_t pos, int of) {
-        widen<kTokens>(p, sh, seq, pos, of, low, high);
-        return !(capped && low == 0.f);
-      });
-      if (capped) high = fminf(high, 0.f);
-      __syncwarp();
-      const bool in = low > 0.f, out = high < 0.f, tie = low == 0.f && high == 0.f;
-      if (lane == 0) {
-        above += in, equal += tie, open += !(in || out || tie);
-        if (in || out || tie) row.mark(i, in ? kIn : tie ? kTie : kOut);
+    for (int32_t i0 = 0; i0 < count; i0 += kWarps) {
+      const int32_t i = i0 + warp;
+      const uint32_t key = i < count ? row.key(i) : kOut;
+      bool tie = false, unknown = false;
+      if (key >= lo && key <= hi) {
+        float low = -INFINITY, high = -INFINITY;
+        pieces(i, [&](int32_t pos, int of) {
+          widen<kTokens>(p, sh, seq, pos, of, low, high);
+          return !(capped && low == 0.f);
+        });
+        if (capped) high = fminf(high, 0.f);
+        __syncwarp();
+        const bool in = low > 0.f, out = high < 0.f;
+        tie = low == 0.f && high == 0.f;
+        unknown = !(in || out || tie);
+        if (lane == 0) {
+          above += in, equal += tie, open += unknown;
+          if (!unknown) row.mark(i, in ? kIn : tie ? kTie : kOut);
+        }
+        __syncwarp();
       }
-      __syncwarp();
+      if (capped) {  // nothing is above 0: the first zeros are chosen, and the later ones ..
+        zeros += __syncthreads_count(lane == 0 && tie);
+        sure = __syncthreads_or(unknown) == 0 && sure;
+        if (sure && zeros >= want) return {lo, hi, want};  // .. need no look
+      }
     }
     above = block_sum<kThreads>(above, sh.sum_a);
     equal = block_sum<kThreads>(equal, sh.sum_a);
