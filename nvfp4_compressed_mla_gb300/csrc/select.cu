@@ -873,11 +873,12 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
                          (seen + granule - 1) / granule};
   const int32_t n = blocks - p.sink - p.recent;
   const int32_t k = p.num_select - p.sink - p.recent;
+  // A cluster is launched for what the table can hold; a row without a long
+  // sweep is one CTA's.
+  if (rank > 0 && (k == 0 || n <= cfg.room)) return;
   if (k == 0) {
-    if (rank == 0) {
-      const int32_t chosen = emit_row<kThreads>(p, sh, row, Border{kTie, kTie, 0}, blocks, out);
-      expand_blocks<kThreads>(p, out, width, seen, chosen);
-    }
+    const int32_t chosen = emit_row<kThreads>(p, sh, row, Border{kTie, kTie, 0}, blocks, out);
+    expand_blocks<kThreads>(p, out, width, seen, chosen);
     return;
   }
   {

@@ -1,0 +1,24 @@
+"""GPU: the selection where sizes, tables and weights reach their limits, against 64-bit scores and
+a stable sort. The chosen positions have to be equal."""
+import numpy as np
+import pytest
+
+from tests.test_gpu_select import Case
+
+pytestmark = pytest.mark.gpu
+
+
+# Tables of more than 32768 blocks: a cluster of CTAs a query token, whose row may be short.
+@pytest.mark.parametrize("lens,per_seq,num,block,sink,recent", [
+    ([900], 1, 40, 1, 0, 0), ([900, 5, 2000], 3, 64, 1, 0, 0), ([900, 1300], 2, 10, 1, 3, 7),
+    ([2600, 40], 1, 9, 16, 1, 2), ([2600, 3000], 19, 9, 16, 0, 0), ([900, 17000], 1, 100, 1, 0, 0),
+])
+def test_short_rows_of_a_wide_table(lens, per_seq, num, block, sink, recent):
+    c = Case(sum(lens) + num, lens, per_seq, 16)
+    ref = c.ref(num, block, sink, recent)
+    wide = np.full((len(lens), 16384), -1, np.int32)
+    wide[:, :c.table.shape[1]] = c.table
+    c.table = wide
+    got = c.run(num, block, sink, recent)
+    bad = np.nonzero((got != ref).any(1))[0]
+    assert bad.size == 0, (bad[:5], got[bad[0]][:20], ref[bad[0]][:20])
