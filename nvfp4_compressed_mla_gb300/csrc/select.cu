@@ -621,22 +621,27 @@ __device__ __forceinline__ Border choose(const SelectParams& p, SelShared<kThrea
 
 // ------------------------------------------------------------------- rows
 // A row's scores in memory: a block's is the highest of its `per` stored ones.
+// A mark is a NaN's word in the place of a block's first score. It is loaded as
+// a word: a float on its way through the compiler need not keep a NaN's payload,
+// and a float load here was seen to lose it.
 struct MemoryRow {
   float* scores;
   int32_t b0, per, granules;
   __device__ __forceinline__ int32_t block(int32_t i) const { return b0 + i; }
+  __device__ __forceinline__ uint32_t* word(int64_t at) const {
+    return reinterpret_cast<uint32_t*>(scores) + at;
+  }
   __device__ __forceinline__ uint32_t key(int32_t i) const {
     const int64_t at = static_cast<int64_t>(b0 + i) * per;
-    float a = __ldcg(scores + at);
-    const uint32_t u = __float_as_uint(a);
-    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return u & 0x80000000u ? ~u : u | 0x80000000u;  // a mark
+    const uint32_t u = __ldcg(word(at));
+    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return u >> 31 ? ~u : u | 0x80000000u;  // a mark
+    float a = __uint_as_float(u);
     for (int g = 1; g < per; ++g)
       if (at + g < granules) a = fmaxf(a, __ldcg(scores + at + g));
     return key32(a);
   }
   __device__ __forceinline__ void mark(int32_t i, uint32_t m) const {
-    scores[static_cast<int64_t>(b0 + i) * per] =
-        __uint_as_float(m == kOut ? 0xFFFFFFFFu : m & 0x7FFFFFFFu);
+    *word(static_cast<int64_t>(b0 + i) * per) = m == kOut ? 0xFFFFFFFFu : m & 0x7FFFFFFFu;
   }
 };
 struct DenseRow {  // shared memory, all blocks from b0 on

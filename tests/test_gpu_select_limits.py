@@ -22,3 +22,23 @@ def test_short_rows_of_a_wide_table(lens, per_seq, num, block, sink, recent):
     got = c.run(num, block, sink, recent)
     bad = np.nonzero((got != ref).any(1))[0]
     assert bad.size == 0, (bad[:5], got[bad[0]][:20], ref[bad[0]][:20])
+
+
+# Few different keys, so that thousands of blocks tie at the border, in rows that shared memory does
+# not hold: each step reads the scores, and the marks of what is decided, from memory.
+@pytest.mark.parametrize("length,keys,heads,num,block,per_seq", [
+    (20000, 8, 16, 3000, 1, 1), (20000, 8, 16, 6000, 1, 2), (20011, 3, 1, 2048, 1, 1),
+    (70000, 16, 64, 2048, 1, 1), (40000, 5, 8, 5001, 2, 1), (70000, 4, 16, 4000, 4, 3),
+])
+@pytest.mark.parametrize("sink,recent", [(0, 0), (2, 3)])
+def test_ties_in_rows_that_shared_memory_does_not_hold(length, keys, heads, num, block, per_seq,
+                                                       sink, recent):
+    c = Case(length + keys, [length], per_seq, heads)
+    rng = np.random.default_rng(keys)
+    pages = c.pool.reshape(c.blocks, c.stride)
+    codes, scales = pages[0, :64 * 64].reshape(64, 64), pages[0, 64 * 64:64 * 72].reshape(64, 8)
+    for p in range(1, c.blocks):
+        pick = rng.integers(0, keys, 64)
+        pages[p, :64 * 64] = codes[pick].reshape(-1)
+        pages[p, 64 * 64:64 * 72] = scales[pick].reshape(-1)
+    c.check(num, block, sink, recent)
