@@ -238,6 +238,8 @@ __device__ __forceinline__ void key_range(SelShared<kThreads>& sh, uint32_t& low
 // weighted sums: in fp32 with an error bound, or in fp64. One warp; the keys go
 // through shared memory, where a 16-byte broadcast serves 16 codes, and the
 // heads' codes are read once for all the positions.
+// Where the fp32 sum of the magnitudes overflows (or a weight is not finite), the error
+// is not finite, and the value says nothing.
 struct TokenScore {
   float value, error;
   double exact;
@@ -333,12 +335,11 @@ __device__ __forceinline__ void score_tokens(const SelectParams& p, SelShared<kT
       r[t].none = r[t].none || r[t].exact != r[t].exact;
     } else {
       r[t].error = r[t].error == 0.f ? 0.f : __fadd_ru(__fmul_ru(r[t].error, kSumError), kTiny);
-      r[t].none = r[t].none || r[t].value != r[t].value;
     }
   }
 }
 // Raises the bounds of a block's highest score by those of `n` consecutive
-// positions.
+// positions. A score that fp32 does not bound may be anything: fp64 tells.
 template <int kTok, int kThreads>
 __device__ __forceinline__ void widen(const SelectParams& p, SelShared<kThreads>& sh, int32_t seq,
                                       int32_t pos, int n, float& low, float& high) {
@@ -348,8 +349,12 @@ __device__ __forceinline__ void widen(const SelectParams& p, SelShared<kThreads>
   for (int t = 0; t < kTok; ++t) {
     if (t >= n) break;
     if (r[t].none) continue;
-    low = fmaxf(low, __fsub_rd(r[t].value, r[t].error));
-    high = fmaxf(high, __fadd_ru(r[t].value, r[t].error));
+    if (r[t].error < INFINITY) {
+      low = fmaxf(low, __fsub_rd(r[t].value, r[t].error));
+      high = fmaxf(high, __fadd_ru(r[t].value, r[t].error));
+    } else {
+      high = INFINITY;
+    }
   }
 }
 // The highest fp64 score of `n` consecutive positions, as a key.

@@ -42,3 +42,39 @@ def test_ties_in_rows_that_shared_memory_does_not_hold(length, keys, heads, num,
         pages[p, :64 * 64] = codes[pick].reshape(-1)
         pages[p, 64 * 64:64 * 72] = scales[pick].reshape(-1)
     c.check(num, block, sink, recent)
+
+
+# Sums over the heads that pass the largest fp32 number, downwards, upwards or both ways: fp32
+# settles nothing, and fp64 decides. At most as many blocks as the list of candidates holds; more;
+# rows that are sampled first.
+@pytest.mark.parametrize("size", [1e35, 2e37, 3e38])
+@pytest.mark.parametrize("signs", ["negative", "positive", "both"])
+@pytest.mark.parametrize("lens,per_seq,heads,num,block", [
+    ([700, 900], 1, 64, 100, 1), ([700, 300], 2, 3, 100, 1), ([2600, 1300], 1, 16, 9, 16),
+    ([2600, 700], 1, 33, 5, 64), ([5000], 1, 16, 300, 1), ([5000], 1, 8, 700, 4),
+    ([20000], 1, 4, 512, 1),
+])
+def test_weights_whose_sums_pass_fp32(size, signs, lens, per_seq, heads, num, block):
+    c = Case(len(signs) + heads, lens, per_seq, heads)
+    rng = np.random.default_rng(heads)
+    w = size * rng.uniform(0.5, 1.0, c.w.shape)
+    c.w = {"negative": -w, "positive": w,
+           "both": w * rng.choice([-1.0, 1.0], w.shape)}[signs].astype(np.float32)
+    assert np.isfinite(c.w).all()
+    c.check(num, block)
+
+
+def test_equal_large_weights_choose_by_score():
+    c = Case(50, [700], 1, 64)
+    c.w[:] = np.float32(-2e37)
+    assert not np.array_equal(c.ref(100)[0], np.arange(100))
+    c.check(100)
+
+
+def test_pages_that_do_not_resolve_rank_last_beside_large_weights():
+    c = Case(51, [900, 900], 1, 16)
+    c.w = (np.sign(c.w) * 2e37).astype(np.float32)
+    c.table[0, 3], c.table[1, 2:9] = -1, 10 ** 6
+    c.check(64)
+    c.check(860)  # some of them have to be taken
+    c.check(5, 64)
