@@ -1143,11 +1143,24 @@ bool codes_tensor(const SelectParams& s, CUtensorMap* map, int32_t* seg_rows) {
 }
 
 template <int kChunks>
-int32_t launch_chunks(const ScoreParams& p, const CUtensorMap& map, cudaStream_t stream) {
+int32_t launch_chunks(ScoreParams& p, cudaStream_t stream) {
+  constexpr int kImage = image_bytes(32 * kChunks);
+  const size_t smem = kStageBase + static_cast<size_t>(p.stages) * kStageBytes +
+                      2 * static_cast<size_t>(p.group) * kImage;
+  // Before the tensor maps: this call binds the device's context to the host
+  // thread, which may have made no other yet, and the driver's encoder needs it.
+  if (cudaFuncSetAttribute(score_kernel<kChunks>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess) {
+    cudaGetLastError();
+    return NVFP4_MLA_ERR_LAUNCH;
+  }
+  CUtensorMap map;
+  memset(&map, 0, sizeof(map));
+  codes_tensor(p.s, &map, &p.seg_rows);
   CUtensorMap images;  // a box is a query token's image
   {
     EncodeTiledFn enc = encode_tiled();
-    constexpr int kLines = image_bytes(32 * kChunks) / kImageLine;
+    constexpr int kLines = kImage / kImageLine;
     const cuuint64_t dims[2] = {kImageLine / 4, static_cast<cuuint64_t>(p.s.num_q) * kLines};
     const cuuint64_t strides[1] = {kImageLine};
     const cuuint32_t box[2] = {kImageLine / 4, kLines};
@@ -1157,14 +1170,6 @@ int32_t launch_chunks(const ScoreParams& p, const CUtensorMap& map, cudaStream_t
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return NVFP4_MLA_ERR_LAUNCH;
-  }
-  constexpr int kImage = image_bytes(32 * kChunks);
-  const size_t smem = kStageBase + static_cast<size_t>(p.stages) * kStageBytes +
-                      2 * static_cast<size_t>(p.group) * kImage;
-  if (cudaFuncSetAttribute(score_kernel<kChunks>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess) {
-    cudaGetLastError();
-    return NVFP4_MLA_ERR_LAUNCH;
   }
   encode_kernel<<<p.s.num_q, 32 * kChunks * kIndexScales, 0, stream>>>(
       p.s.q_index, p.s.weights, p.s.num_heads, 32 * kChunks, p.s.images);
@@ -1202,16 +1207,13 @@ int32_t launch_scores(SelectParams& s, int num_sms, cudaStream_t stream) {
   p.stages = stage_count(chunks, p.group);
   p.ctas = s.score_ctas = num_sms < kStatusWords ? num_sms : kStatusWords;
   p.s = s;
-  CUtensorMap map;
-  memset(&map, 0, sizeof(map));
-  codes_tensor(s, &map, &p.seg_rows);
   p.page_shift = 0;
   while (p.page_shift < 20 && 1 << p.page_shift < s.page_size) ++p.page_shift;
   switch (chunks) {
-    case 1: return launch_chunks<1>(p, map, stream);
-    case 2: return launch_chunks<2>(p, map, stream);
-    case 3: return launch_chunks<3>(p, map, stream);
-    default: return launch_chunks<4>(p, map, stream);
+    case 1: return launch_chunks<1>(p, stream);
+    case 2: return launch_chunks<2>(p, stream);
+    case 3: return launch_chunks<3>(p, stream);
+    default: return launch_chunks<4>(p, stream);
   }
 }
 
