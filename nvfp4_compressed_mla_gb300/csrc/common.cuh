@@ -22,6 +22,7 @@ static_assert(kPayloadBytes + kLatent / kGroup + kRope == kNvfp4Row, "352-byte N
 static_assert(kLatent + kRope == kFp8Row, "576-byte FP8 row");
 
 // ------------------------------------------------------------ host side
+constexpr size_t kMaxSharedBytes = 227 * 1024;  // of a CTA
 // Current device, checked to be an sm_103 part; caches the SM count.
 int32_t current_device_checked(int* device, int* num_sms);
 bool aligned16(const void* p);

@@ -23,6 +23,9 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kMaxCluster = 8;  // largest portable cluster
+// Dynamic shared memory a sequence, beside the 256 bytes of a scan's sums.
+constexpr size_t kPlanBytes = 12, kTruncateBytes = 4;
+static_assert(kPlanBytes * NVFP4_MLA_MAX_PLAN_SEQS + 256 <= kMaxSharedBytes, "shared memory");
 
 __device__ __forceinline__ uint32_t cta_rank() {
   uint32_t r;
@@ -369,13 +372,17 @@ __global__ void __launch_bounds__(kPlanThreads) truncate_kernel(const TruncatePa
   }
 }
 
+// With `per_seq` bytes of shared memory a sequence. The kernel's limit is the
+// process's: calls of other threads rely on it, so that it is the same one in
+// every call that needs it.
 template <typename Params>
-int32_t launch_cluster(void (*kernel)(Params), const Params& p, int ctas, size_t smem,
+int32_t launch_cluster(void (*kernel)(Params), const Params& p, int ctas, size_t per_seq,
                        cudaStream_t stream) {
+  const size_t smem = per_seq * static_cast<size_t>(p.num_seqs);
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                            cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess) {
+                           static_cast<int>(per_seq * NVFP4_MLA_MAX_PLAN_SEQS)) != cudaSuccess) {
     cudaGetLastError();
     return NVFP4_MLA_ERR_LAUNCH;
   }
@@ -431,10 +438,9 @@ extern "C" int32_t nvfp4_mla_plan_step(
   // a warp takes 128 rows at a time: 131072 rows of 1021 sequences 16.5 us, 25.3
   // with 32. With few rows that leaves warps idle: 66 rows 5.2 us with 32 a
   // warp, 6.2 with 128.
-  const size_t smem = 12u * static_cast<size_t>(num_seqs);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return max_tokens > 4 * kPlanThreads ? launch_cluster(plan_kernel<4>, p, kMaxCluster, smem, s)
-                                       : launch_cluster(plan_kernel<1>, p, 1, smem, s);
+  return max_tokens > 4 * kPlanThreads ? launch_cluster(plan_kernel<4>, p, kMaxCluster, kPlanBytes, s)
+                                       : launch_cluster(plan_kernel<1>, p, 1, kPlanBytes, s);
 }
 
 extern "C" int32_t nvfp4_mla_truncate(const int32_t* keep_lens, const int32_t* seq_lens,
@@ -455,6 +461,6 @@ extern "C" int32_t nvfp4_mla_truncate(const int32_t* keep_lens, const int32_t* s
                             page_division(page_size), free_pages, free_capacity, free_count, seq_lens_out,
                             free_count_out, dropped_count};
   const int ctas = num_seqs > kPlanWarps ? kMaxCluster : 1;  // a warp per sequence, as far as 256
-  return launch_cluster(truncate_kernel, p, ctas, 4u * static_cast<size_t>(num_seqs),
+  return launch_cluster(truncate_kernel, p, ctas, kTruncateBytes,
                         static_cast<cudaStream_t>(stream));
 }

@@ -1119,6 +1119,18 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   if (tid == 0) p.s.status[blockIdx.x] = ld_shared_u32(abort_addr);
 }
 
+// Dynamic shared memory of score_kernel<chunks> with runs of up to `group`.
+constexpr size_t score_smem(int chunks, int group) {
+  return kStageBase + static_cast<size_t>(stage_count(chunks, group)) * kStageBytes +
+         2 * static_cast<size_t>(group) * image_bytes(32 * chunks);
+}
+constexpr size_t most_score_smem(int chunks) {
+  size_t most = 0;
+  for (int group = 1; group <= kMaxGroup; ++group)
+    most = score_smem(chunks, group) > most ? score_smem(chunks, group) : most;
+  return most;
+}
+
 // The pool's codes as lines of 128 bytes (two rows), in 128-byte swizzle; false
 // where the page size is no power of two or below 16: a step is then not made
 // of pieces of pages with whole groups of eight lines.
@@ -1145,12 +1157,15 @@ bool codes_tensor(const SelectParams& s, CUtensorMap* map, int32_t* seg_rows) {
 template <int kChunks>
 int32_t launch_chunks(ScoreParams& p, cudaStream_t stream) {
   constexpr int kImage = image_bytes(32 * kChunks);
-  const size_t smem = kStageBase + static_cast<size_t>(p.stages) * kStageBytes +
-                      2 * static_cast<size_t>(p.group) * kImage;
-  // Before the tensor maps: this call binds the device's context to the host
-  // thread, which may have made no other yet, and the driver's encoder needs it.
+  const size_t smem = score_smem(kChunks, p.group);
+  constexpr size_t kMost = most_score_smem(kChunks);
+  static_assert(kMost + 1024 <= kMaxSharedBytes, "shared memory");  // 1024 static ones
+  // The limit is the process's: calls of other threads rely on it, so that it is
+  // the same one in every call. Before the tensor maps: this call binds the
+  // device's context to the host thread, which may have made no other yet, and
+  // the driver's encoder needs it.
   if (cudaFuncSetAttribute(score_kernel<kChunks>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess) {
+                           static_cast<int>(kMost)) != cudaSuccess) {
     cudaGetLastError();
     return NVFP4_MLA_ERR_LAUNCH;
   }

@@ -1054,6 +1054,12 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   }
 }
 
+// Largest room that launch_select<kThreads> is called with or takes.
+constexpr int kSmallRoom = 4096;
+constexpr int most_room(int threads) {
+  return threads == 256 ? kSmallRoom : threads == 512 ? kRoom : kWideRoom;
+}
+
 template <int kThreads>
 int32_t launch_select(const SelectParams& p, int32_t most_blocks, int num_sms,
                       cudaStream_t stream) {
@@ -1066,8 +1072,13 @@ int32_t launch_select(const SelectParams& p, int32_t most_blocks, int num_sms,
   if (most_blocks > kWideRoom)
     while (ctas < kMaxCluster && p.num_q * ctas * 2 <= num_sms) ctas *= 2;
   const size_t smem = sizeof(SelShared<kThreads>) + 4 * static_cast<size_t>(cfg.room);
-  if (cudaFuncSetAttribute(select_kernel<kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess) {
+  // The limit is the process's: calls of other threads rely on it, so that it is
+  // the same one in every call.
+  constexpr size_t kMost = sizeof(SelShared<kThreads>) + 4 * static_cast<size_t>(most_room(kThreads));
+  static_assert(kMost <= kMaxSharedBytes, "shared memory");
+  if (smem > kMost ||
+      cudaFuncSetAttribute(select_kernel<kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(kMost)) != cudaSuccess) {
     cudaGetLastError();
     return NVFP4_MLA_ERR_LAUNCH;
   }
@@ -1202,7 +1213,7 @@ extern "C" int32_t sparse_mla_select(const void* q_index, const float* weights,
     // was longer then). 66
     // rows of 146000: 76 us with 512, 54 with 1024.
     const bool many = p.num_q > 2 * sms;
-    const int32_t st = many && most_blocks <= 4096          ? launch_select<256>(p, most_blocks, sms, s)
+    const int32_t st = many && most_blocks <= kSmallRoom   ? launch_select<256>(p, most_blocks, sms, s)
                        : many && most_blocks <= 32 * kRoom ? launch_select<512>(p, most_blocks, sms, s)
                                                            : launch_select<1024>(p, most_blocks, sms, s);
     if (st != NVFP4_MLA_OK) return st;
