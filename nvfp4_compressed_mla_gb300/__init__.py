@@ -3,6 +3,9 @@
 Thin Python binding over the C ABI declared in ``include/nvfp4_mla.h``:
 the functions below carry the C entry points' names and only marshal
 arguments (torch tensors -> device pointers, the current CUDA stream).
+With ``stream`` a call runs on that stream instead (a torch stream or a
+handle): the caller orders it after what writes the arguments and before
+what reads the results. Buffers that the call allocates are that stream's.
 Every step of the computation runs in the library's CUDA kernels; if the
 library is missing or the device is not an sm_103 part the calls raise.
 
@@ -74,6 +77,33 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _launch_stream(stream) -> torch.cuda.Stream:
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    # torch would take the default stream's handle, 0, for none and make a new stream
+    return torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+
+
+def _scratch(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """A buffer of the launch stream: torch may hand out its memory again once ``stream`` is past
+    what was enqueued on it, and it holds nothing that other streams' pending work still reads."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_launch_stream(stream)):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _result(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """The same for what a call returns, which the current stream will read: when it is dropped,
+    its memory waits for the current stream's work too."""
+    t = _scratch(shape, dtype, device, stream)
+    if stream is not None:
+        here = torch.cuda.current_stream(t.device)
+        if here.cuda_stream != _launch_stream(stream).cuda_stream:
+            t.record_stream(here)
+    return t
+
+
 def _check(status: int, where: str) -> None:
     if status != 0:
         raise NativeError(status, where)
@@ -137,13 +167,13 @@ def sparse_mla_decode(q_latent: torch.Tensor, q_rope: torch.Tensor, q_seq: torch
     topk = topk_idx.shape[1]
     dev = q_latent.device
     if out is None:
-        out = torch.empty((num_q, H, LATENT_DIM), device=dev,
-                          dtype=torch.float32 if out_fp32 else torch.bfloat16)
+        out = _result((num_q, H, LATENT_DIM), torch.float32 if out_fp32 else torch.bfloat16, dev,
+                      stream)
     if lse is None:
-        lse = torch.empty((num_q, H), device=dev, dtype=torch.float32)
+        lse = _result((num_q, H), torch.float32, dev, stream)
     need = sparse_mla_decode_workspace_size(num_q, H, topk, num_splits) if num_q else 0
     if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+        workspace = _scratch(need, torch.uint8, dev, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = _lib().sparse_mla_decode(
         _ptr(q_latent), _ptr(q_rope), _ptr(q_seq), _ptr(topk_idx), num_q, H, topk,
@@ -163,10 +193,10 @@ def sparse_mla_merge_states(part_out: torch.Tensor, part_lse: torch.Tensor,
     P, num_q, H = part_out.shape[0], part_out.shape[1], part_out.shape[2]
     dev = part_out.device
     if out is None:
-        out = torch.empty((num_q, H, LATENT_DIM), device=dev,
-                          dtype=torch.float32 if out_fp32 else torch.bfloat16)
+        out = _result((num_q, H, LATENT_DIM), torch.float32 if out_fp32 else torch.bfloat16, dev,
+                      stream)
     if lse is None:
-        lse = torch.empty((num_q, H), device=dev, dtype=torch.float32)
+        lse = _result((num_q, H), torch.float32, dev, stream)
     st = _lib().sparse_mla_merge_states(_ptr(part_out), _ptr(part_lse), P, num_q, H, _ptr(out),
                                         1 if out_fp32 else 0, _ptr(lse), _stream(stream))
     _check(st, "sparse_mla_merge_states")
@@ -196,10 +226,9 @@ def nvfp4_mla_stage_fp8(q_seq: torch.Tensor, topk_idx: torch.Tensor, block_table
     dev = topk_idx.device
     R = nvfp4_mla_staged_rows_per_q(topk, page_size)
     if staged is None:
-        staged = torch.empty(max(num_q * R * ROW_BYTES[ROW_FP8_576], 16), dtype=torch.uint8,
-                             device=dev)
+        staged = _result(max(num_q * R * ROW_BYTES[ROW_FP8_576], 16), torch.uint8, dev, stream)
     if staged_idx is None:
-        staged_idx = torch.empty((num_q, topk), dtype=torch.int32, device=dev)
+        staged_idx = _result((num_q, topk), torch.int32, dev, stream)
     st = _lib().nvfp4_mla_stage_fp8(
         _ptr(q_seq), _ptr(topk_idx), num_q, topk, _ptr(block_table), block_table.shape[0],
         block_table.shape[1], _ptr(seq_lens), page_size, _ptr(cache), num_blocks,
@@ -243,16 +272,6 @@ def _table(t: torch.Tensor, device: int):
     return _arg(t, "block_table", torch.int32, 0, device), t.shape[0], t.shape[1]
 
 
-def _scratch(size: int, stream) -> torch.Tensor:
-    """A buffer that torch may hand out again once ``stream`` is past this call's work."""
-    if stream is None:
-        return torch.empty(size, dtype=torch.uint8, device="cuda")
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream))
-    with torch.cuda.stream(stream):
-        return torch.empty(size, dtype=torch.uint8, device="cuda")
-
-
 def nvfp4_mla_plan_step(new_lens: torch.Tensor, seq_lens: torch.Tensor, block_table: torch.Tensor,
                         page_size: int, free_pages: torch.Tensor, free_count: torch.Tensor,
                         max_tokens: int, seq_lens_out: Optional[torch.Tensor] = None,
@@ -274,13 +293,13 @@ def nvfp4_mla_plan_step(new_lens: torch.Tensor, seq_lens: torch.Tensor, block_ta
     table, num_seqs, max_blocks = _table(block_table, dev)
     rows = max(max_tokens, 0)
     if seq_ids is None:
-        seq_ids = torch.empty(rows, dtype=i32, device=dev)
+        seq_ids = _result(rows, i32, dev, stream)
     if positions is None:
-        positions = torch.empty(rows, dtype=i32, device=dev)
+        positions = _result(rows, i32, dev, stream)
     if slots is None:
-        slots = torch.empty(rows, dtype=torch.int64, device=dev)
+        slots = _result(rows, torch.int64, dev, stream)
     if cu_tokens is None:
-        cu_tokens = torch.empty(num_seqs + 1, dtype=i32, device=dev)
+        cu_tokens = _result(num_seqs + 1, i32, dev, stream)
     lens_out = seq_lens if seq_lens_out is None else seq_lens_out
     count_out = free_count if free_count_out is None else free_count_out
     st = _lib().nvfp4_mla_plan_step(
@@ -363,7 +382,7 @@ def nvfp4_mla_index_read(seq_ids: torch.Tensor, positions: torch.Tensor,
     dev, i32 = torch.cuda.current_device(), torch.int32
     n = seq_ids.numel()
     if keys is None:
-        keys = torch.empty((n, INDEX_DIM), dtype=torch.bfloat16, device=dev)
+        keys = _result((n, INDEX_DIM), torch.bfloat16, dev, stream)
     table, num_seqs, max_blocks = _table(block_table, dev)
     st = _lib().nvfp4_mla_index_read(
         _arg(seq_ids, "seq_ids", i32, n, dev), _arg(positions, "positions", i32, n, dev), n,
@@ -402,12 +421,12 @@ def sparse_mla_select(q_index: torch.Tensor, weights: torch.Tensor, q_seq: torch
     table, num_seqs, max_blocks = _table(block_table, dev)
     width = max(num_select * select_block, 0)
     if topk_idx is None:
-        topk_idx = torch.empty((num_q, width), dtype=i32, device=dev)
+        topk_idx = _result((num_q, width), i32, dev, stream)
     if workspace is None:
         need = int(_lib().sparse_mla_select_workspace_size(num_q, H, max_blocks, page_size,
                                                            select_block))
         if need < 1 << 63:  # an invalid shape is refused below
-            workspace = _scratch(need, stream)
+            workspace = _scratch(need, torch.uint8, dev, stream)
     ws = None if workspace is None else workspace.numel() * workspace.element_size()
     st = _lib().sparse_mla_select(
         _arg(q_index, "q_index", torch.bfloat16, 0, dev),
