@@ -664,14 +664,11 @@ struct ListRow {  // shared memory, some blocks in any order
   __device__ __forceinline__ void mark(int32_t i, uint32_t m) const { keys[i] = m; }
 };
 
-// Output row of a query token: the first positions of its `chosen` blocks are
+// Output row of a query token: the first positions of its num_select blocks are
 // written in order, the others follow from them.
 template <int kThreads>
 __device__ __forceinline__ void expand_blocks(const SelectParams& p, int32_t* out, int64_t width,
-                                              int32_t seen, int32_t chosen) {
-  // never fewer than num_select; the row is whole all the same
-  for (int64_t i = static_cast<int64_t>(chosen) * p.block + threadIdx.x; i < width; i += kThreads)
-    out[i] = -1;
+                                              int32_t seen) {
   if (p.block == 1) return;
   __syncthreads();
   for (int64_t i = threadIdx.x; i < width; i += kThreads) {
@@ -683,12 +680,12 @@ __device__ __forceinline__ void expand_blocks(const SelectParams& p, int32_t* ou
 }
 
 // The first positions of the chosen blocks in order, `row` holding the blocks
-// from p.sink on; returns how many were chosen. A warp has consecutive blocks:
-// it counts, learns what comes before it, and writes.
+// from p.sink on: num_select ones, as there are more blocks than that. A warp has
+// consecutive blocks: it counts, learns what comes before it, and writes.
 template <int kThreads, typename Row>
-__device__ __forceinline__ int32_t emit_row(const SelectParams& p, SelShared<kThreads>& sh,
-                                            const Row& row, const Border& border, int32_t blocks,
-                                            int32_t* out) {
+__device__ __forceinline__ void emit_row(const SelectParams& p, SelShared<kThreads>& sh,
+                                         const Row& row, const Border& border, int32_t blocks,
+                                         int32_t* out) {
   constexpr int kWarps = kThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int32_t share = ((blocks + kWarps - 1) / kWarps + 31) / 32 * 32;
@@ -729,7 +726,6 @@ __device__ __forceinline__ int32_t emit_row(const SelectParams& p, SelShared<kTh
       out[static_cast<int64_t>(slot) * p.block] = (b0 + lane) * p.block;
     at += __popc(chosen);
   }
-  return min(total, p.num_select);
 }
 
 __device__ __forceinline__ uint32_t sel_rank() {
@@ -887,8 +883,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   // sweep is one CTA's.
   if (rank > 0 && (k == 0 || n <= cfg.room)) return;
   if (k == 0) {
-    const int32_t chosen = emit_row<kThreads>(p, sh, row, Border{kTie, kTie, 0}, blocks, out);
-    expand_blocks<kThreads>(p, out, width, seen, chosen);
+    emit_row<kThreads>(p, sh, row, Border{kTie, kTie, 0}, blocks, out);
+    expand_blocks<kThreads>(p, out, width, seen);
     return;
   }
   {
@@ -916,8 +912,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     for (int32_t i = tid; i < n; i += kThreads) keys[i] = row.key(i);
     __syncthreads();
     const Border border = choose<kThreads>(p, sh, dense, row.scores, n, k, seq, seen, m);
-    const int32_t chosen = emit_row<kThreads>(p, sh, dense, border, blocks, out);
-    expand_blocks<kThreads>(p, out, width, seen, chosen);
+    emit_row<kThreads>(p, sh, dense, border, blocks, out);
+    expand_blocks<kThreads>(p, out, width, seen);
     return;
   }
 
@@ -1041,7 +1037,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
               for (uint32_t left = word[u]; left != 0 && slot < p.num_select; left &= left - 1)
                 out[slot++ * p.block] = (((i0 + lane) * 4 + u) * 32 + __ffs(left) - 1) * p.block;
           }
-          expand_blocks<kThreads>(p, out, width, seen, min(total, p.num_select));
+          expand_blocks<kThreads>(p, out, width, seen);
           return;
         }
       }
@@ -1049,8 +1045,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     }
     if (rank > 0) return;
     const Border border = choose<kThreads>(p, sh, row, row.scores, n, k, seq, seen, m);
-    const int32_t chosen = emit_row<kThreads>(p, sh, row, border, blocks, out);
-    expand_blocks<kThreads>(p, out, width, seen, chosen);
+    emit_row<kThreads>(p, sh, row, border, blocks, out);
+    expand_blocks<kThreads>(p, out, width, seen);
   }
 }
 
