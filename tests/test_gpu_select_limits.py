@@ -3,7 +3,9 @@ a stable sort. The chosen positions have to be equal."""
 import numpy as np
 import pytest
 
-from tests.test_gpu_select import Case
+from tests import step_cases as sc
+from tests.test_gpu_select import Case, reference_on_device
+from workloads.gen import bf16_from_f32
 
 pytestmark = pytest.mark.gpu
 
@@ -78,3 +80,43 @@ def test_pages_that_do_not_resolve_rank_last_beside_large_weights():
     c.check(64)
     c.check(860)  # some of them have to be taken
     c.check(5, 64)
+
+
+def long_case(length, per_seq, heads, keys=None):
+    """One sequence of random codes, or of few different keys under weights that are powers of two:
+    their scores are exact in any order of summation, and thousands of them are equal."""
+    rng = np.random.default_rng(length + per_seq)
+    c = Case.__new__(Case)
+    c.page, c.stride, c.lens = 64, 64 * sc.ROW, np.array([length])
+    c.table, _, c.blocks = sc.random_tables(rng, c.lens, 64, 2)
+    rows = np.empty((c.blocks, c.stride), np.uint8)
+    n = c.blocks * 64 if keys is None else keys
+    codes = rng.integers(0, 256, (n, 64), dtype=np.uint8)
+    scales = rng.integers(0x28, 0x48, (n, 8), dtype=np.uint8)
+    pick = np.arange(n) if keys is None else rng.integers(0, keys, c.blocks * 64)
+    rows[:, :64 * 64] = codes[pick].reshape(c.blocks, -1)
+    rows[:, 64 * 64:] = scales[pick].reshape(c.blocks, -1)
+    c.pool = rows.reshape(-1)
+    c.seq = np.zeros(per_seq, np.int32)
+    c.pos = np.arange(length - per_seq, length).astype(np.int32)
+    c.q = bf16_from_f32(rng.standard_normal((per_seq, heads, 128)))
+    c.w = (rng.standard_normal((per_seq, heads)) / np.sqrt(heads)).astype(np.float32)
+    if keys is not None:
+        c.w = (2.0 ** rng.integers(-2, 2, c.w.shape) * np.sign(c.w)).astype(np.float32)
+    return c
+
+
+# More chosen than a list has room for; rows of more blocks than the list's place has bits; several
+# stored scores a block in a row that shared memory does not hold; the smaller CTAs of many tokens.
+@pytest.mark.parametrize("length,per_seq,heads,num,block,keys", [
+    (131072, 2, 16, 16384, 1, None), (131072, 1, 16, 65536, 1, None), (70000, 1, 4, 7000, 1, None),
+    (70000, 1, 4, 7000, 1, 9), (131072, 1, 16, 16384, 4, 30),
+    (1048576, 1, 4, 2048, 1, None), (1048577, 1, 4, 2048, 1, None), (1200003, 2, 4, 2048, 1, None),
+    (1100003, 1, 4, 30, 64, None), (1100003, 1, 2, 400, 64, 3000), (2200001, 1, 2, 100, 128, 9000),
+    (17000, 320, 8, 300, 1, 12), (17000, 320, 8, 9000, 1, None),
+])
+def test_long_rows_of_every_form(length, per_seq, heads, num, block, keys):
+    c = long_case(length, per_seq, heads, keys)
+    got, ref = c.run(num, block), reference_on_device(c, num, block)
+    bad = np.nonzero((got != ref).any(1))[0]
+    assert bad.size == 0, (bad.size, bad[:5], got[bad[0]][:20], ref[bad[0]][:20])
