@@ -387,7 +387,13 @@ int32_t nvfp4_mla_truncate(const int32_t* keep_lens, const int32_t* seq_lens, in
  * p * block_stride_bytes and holds page_size * 64 bytes of E2M1 codes
  * (element 2i of a row in the low nibble of its byte i), then page_size * 8
  * bytes of E4M3 scales (one per 16 values). Encoding as for the latent
- * values of an NVFP4 row: scale = E4M3(amax/6), code = nearest E2M1.
+ * values of an NVFP4 row: scale = E4M3(amax/6), code = nearest E2M1. There is
+ * no scale beside it, and none for the index queries, which are encoded the
+ * same way: groups of 16 whose largest magnitude is above 2688 saturate,
+ * below 6 * 2^-6 their scales lose bits, and up to 6 * 2^-10 they become
+ * zeros. A caller whose keys or queries leave that range scales them first; a
+ * power of two common to all keys, or to all queries, does not change the
+ * choice.
  *
  * nvfp4_mla_index_append: encode n_tok keys into their rows.
  * nvfp4_mla_index_read: the values that the rows of n_tok tokens stand for
@@ -433,7 +439,10 @@ int32_t nvfp4_mla_index_read(const int32_t* seq_ids, const int32_t* positions, i
  * recent_blocks visible blocks are always taken, then the highest scores up
  * to num_select blocks in all, the lower index first where scores are equal.
  * The choice is that of 64-bit arithmetic: scores computed in fp32 decide it
- * only where they differ by more than their error bound.
+ * only where they differ by more than their error bound, and not at all where
+ * they could overflow. One part of the bound is measured and not derived: the
+ * tensor cores' own sum of a dot product is taken to be off by at most
+ * 8 * 2^-24 of its terms' magnitudes (2.9 * 2^-24 was the most seen in 5e5).
  *
  *   q_index      device bf16 [num_q, num_heads, 128], 16-byte aligned, finite
  *   weights      device fp32 [num_q, num_heads], finite
