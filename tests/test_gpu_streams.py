@@ -121,7 +121,7 @@ def test_a_result_that_the_current_stream_still_reads_is_not_handed_out_again():
     torch.cuda.synchronize()
     out = nm.sparse_mla_select(*args, 64, stream=side)
     torch.cuda.current_stream().wait_stream(side)
-    torch.cuda._sleep(40_000_000)   # about 20 ms, behind which the result is read
+    torch.cuda._sleep(400_000_000)  # about 0.2 s, behind which the result is read
     kept = out.clone()
     at = out.data_ptr()
     del out
