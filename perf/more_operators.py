@@ -207,7 +207,8 @@ def prepare(case, seed):
         st.update(src=src.int(), dst=dst.int(), fork_lens=lens[src].int(), pools=[])
         for row in (NVFP4_ROW, INDEX_ROW):  # the latent pool and the index keys' pool of a layer
             st["pools"].append((torch.randint(0, 256, (blocks * P * row,), generator=g, device=DEV, dtype=torch.uint8), P * row))
-        st.update(copy_src=torch.empty(S * k, device=DEV, dtype=i32), copy_dst=torch.empty(S * k, device=DEV, dtype=i32))
+        for name in ("shared", "copy_src", "copy_dst"):
+            st[name] = torch.empty(S * k, device=DEV, dtype=i32)
     elif case["op"] == "release":
         # prompt s and its samples s * k .. s * k + k - 1, all of them sequences with answers of their own
         k = case["samples"]
@@ -347,8 +348,8 @@ def _plain_fork(st):
     for pool, size in st["pools"]:
         _copy_plain(pool, size, copy_src, copy_dst)
     return {"block_table": new_table, "seq_lens": new_lens, "page_shares": new_shares,
-            "free_count": (count - need.sum()).int(), "copy_src": copy_src, "copy_dst": copy_dst,
-            "latent": st["pools"][0][0], "index": st["pools"][1][0]}
+            "free_count": (count - need.sum()).int(), "shared_blocks": torch.where(ok, full, -1).int(),
+            "copy_src": copy_src, "copy_dst": copy_dst, "latent": st["pools"][0][0], "index": st["pools"][1][0]}
 
 
 def _plain_release(st):
@@ -437,12 +438,13 @@ def _own(st):
     outs = {"page_shares_out": st["shares_out"], "free_count_out": st["count_out"]}
     if case["op"] == "fork":
         nm.nvfp4_mla_fork(st["src"], st["dst"], st["fork_lens"], st["lens"], st["table"], P, st["shares"], st["free"],
-                          st["count"], seq_lens_out=st["lens_out"], copy_src=st["copy_src"], copy_dst=st["copy_dst"], **outs)
+                          st["count"], seq_lens_out=st["lens_out"], shared_blocks=st["shared"], copy_src=st["copy_src"],
+                          copy_dst=st["copy_dst"], **outs)
         for pool, size in st["pools"]:
             nm.nvfp4_mla_copy_pages(st["copy_src"], st["copy_dst"], pool, blocks, size, size)
         return {"block_table": st["table"], "seq_lens": st["lens_out"], "page_shares": st["shares_out"],
-                "free_count": st["count_out"], "copy_src": st["copy_src"], "copy_dst": st["copy_dst"],
-                "latent": st["pools"][0][0], "index": st["pools"][1][0]}
+                "free_count": st["count_out"], "shared_blocks": st["shared"], "copy_src": st["copy_src"],
+                "copy_dst": st["copy_dst"], "latent": st["pools"][0][0], "index": st["pools"][1][0]}
     if case["op"] == "release":
         nm.nvfp4_mla_release(st["keep"], st["lens"], st["table"], P, st["shares"], st["free"], st["count"],
                              seq_lens_out=st["lens_out"], **outs)
