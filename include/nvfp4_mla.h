@@ -479,6 +479,108 @@ int32_t sparse_mla_select(const void* q_index, const float* weights, const int32
                           int32_t* topk_idx, void* workspace, size_t workspace_bytes,
                           void* stream);
 
+/* ------------------------------------------------------------------------
+ * Pages that several sequences share: parallel samples, beams, common
+ * prompts. page_shares[p] (device int32 [num_blocks]) is the number of
+ * sequences that hold page p beyond the first: 0 for a free page and for a
+ * page of one sequence, so that nvfp4_mla_plan_step works on such a pool as
+ * it is. A sequence holds a page at most once. Only whole pages are shared,
+ * and nothing appends to a whole page. A pool with shared pages is shrunk
+ * with nvfp4_mla_release; nvfp4_mla_truncate knows of no sharing.
+ *
+ * Arguments that all of them have are those of nvfp4_mla_plan_step. The
+ * *_out buffers may be the inputs themselves. Page ids outside
+ * [0, num_blocks) in a table or on the stack are never followed. Calls on the
+ * same state may not run at the same time as each other.
+ *
+ * nvfp4_mla_fork: for i = 0 .. num_forks - 1, sequence dst_seqs[i] becomes
+ * the first fork_lens[i] tokens of src_seqs[i]: it gets the entries of the
+ * whole pages (whose shares rise by one) and, where fork_lens[i] is no
+ * multiple of page_size, a page from the top of the stack, in the order of i,
+ * into which the caller copies the partly used one (copy_src[i] to
+ * copy_dst[i], nvfp4_mla_copy_pages) in every pool that the table serves.
+ * The lengths and tables are those before the call. A fork is refused, and
+ * changes nothing, unless both sequences exist, 0 <= fork_lens[i] <= the
+ * source's length and what the table holds, dst has length 0 and no earlier
+ * i has the same dst; and once one does not find its page, no later one
+ * that needs a page is served. src_seqs[i] = -1 is padding.
+ *
+ *   src_seqs, dst_seqs, fork_lens  device int32 [num_forks],
+ *                0 <= num_forks <= NVFP4_MLA_MAX_PLAN_SEQS
+ *   block_table  updated: entries of the dst sequences
+ *   shared_blocks device int32 [num_forks]: pages that fork i shares, -1 for
+ *                a refused one and for padding
+ *   copy_src, copy_dst  device int32 [num_forks]: the page to copy, or -1, -1
+ *   refused_count nullable device int32: += refused forks
+ *
+ * nvfp4_mla_release: nvfp4_mla_truncate for such a pool. The released entries
+ * of sequence s are those of blocks ceil(keep/page_size) ..
+ * ceil(L/page_size) - 1; each takes one off its page's shares, and a page
+ * whose last holder drops it goes back onto the stack, in the place of the
+ * first entry (by sequence, then block) of this call that dropped it, the
+ * first such topmost. A cut that would leave the sequence with a part of a
+ * page that was shared before the call is refused, whole (fork at that
+ * length instead).
+ *   refused_count nullable device int32: += refused cuts
+ *
+ * nvfp4_mla_compact: pages move down, so that a pool's upper end becomes
+ * free. With u_0 > u_1 > ... the pages that tables hold (their first
+ * ceil(L/page_size) entries) and f_0 < f_1 < ... the pages of the stack that no
+ * table holds, u_i becomes f_i for i < max_moves as long as f_i < u_i. Tables
+ * and shares follow; the stack becomes the free pages after the moves, the
+ * lowest on top. Pages that neither a table nor the stack holds stay. The
+ * caller copies copy_src[i] to copy_dst[i] in every pool; until then the old
+ * table is the one to read with (block_table_out may be another buffer).
+ *   max_moves    >= 0
+ *   block_table_out device int32 [num_seqs, max_blocks_per_seq], all of it
+ *                written if it is another buffer
+ *   free_pages_out device int32 [free_capacity]; the entries below the new
+ *                count are written
+ *   copy_src, copy_dst  device int32 [max_moves]; -1, -1 behind the last move
+ *   pages_end    nullable device int32 [1]: one above the highest page held
+ *                after the moves
+ *   workspace    device, 16-byte aligned, >= nvfp4_mla_compact_workspace_size
+ *                bytes; contents need not be initialised. That size is
+ *                SIZE_MAX for num_blocks < 1
+ *
+ * nvfp4_mla_copy_pages: page copy_src[i] to page copy_dst[i] of one pool,
+ * page_bytes from the start of each (a multiple of 16, at most
+ * block_stride_bytes). Pairs with a -1 are skipped; pairs with any other
+ * page outside [0, num_blocks) are skipped and counted into invalid_count.
+ * No page may be the target of two pairs, or target of one and source of
+ * another.
+ */
+int32_t nvfp4_mla_fork(const int32_t* src_seqs, const int32_t* dst_seqs, const int32_t* fork_lens,
+                       int32_t num_forks, const int32_t* seq_lens, int32_t num_seqs,
+                       int32_t* block_table, int32_t max_blocks_per_seq, int32_t page_size,
+                       const int32_t* page_shares, int32_t num_blocks, const int32_t* free_pages,
+                       int32_t free_capacity, const int32_t* free_count, int32_t* seq_lens_out,
+                       int32_t* page_shares_out, int32_t* free_count_out, int32_t* shared_blocks,
+                       int32_t* copy_src, int32_t* copy_dst, int32_t* refused_count, void* stream);
+
+int32_t nvfp4_mla_release(const int32_t* keep_lens, const int32_t* seq_lens, int32_t num_seqs,
+                          const int32_t* block_table, int32_t max_blocks_per_seq,
+                          int32_t page_size, const int32_t* page_shares, int32_t num_blocks,
+                          int32_t* free_pages, int32_t free_capacity, const int32_t* free_count,
+                          int32_t* seq_lens_out, int32_t* page_shares_out, int32_t* free_count_out,
+                          int32_t* dropped_count, int32_t* refused_count, void* stream);
+
+size_t nvfp4_mla_compact_workspace_size(int32_t num_blocks);
+
+int32_t nvfp4_mla_compact(const int32_t* seq_lens, int32_t num_seqs, const int32_t* block_table,
+                          int32_t max_blocks_per_seq, int32_t page_size,
+                          const int32_t* page_shares, int32_t num_blocks,
+                          const int32_t* free_pages, int32_t free_capacity,
+                          const int32_t* free_count, int32_t max_moves, int32_t* block_table_out,
+                          int32_t* page_shares_out, int32_t* free_pages_out,
+                          int32_t* free_count_out, int32_t* copy_src, int32_t* copy_dst,
+                          int32_t* pages_end, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+int32_t nvfp4_mla_copy_pages(const int32_t* copy_src, const int32_t* copy_dst, int32_t num_copies,
+                             void* cache, int64_t num_blocks, int64_t block_stride_bytes,
+                             int64_t page_bytes, int32_t* invalid_count, void* stream);
+
 #ifdef __cplusplus
 } /* extern "C" */
 #endif

@@ -37,7 +37,8 @@ __all__ = [
     "sparse_mla_merge_states", "nvfp4_mla_staged_rows_per_q", "nvfp4_mla_stage_fp8",
     "staged_fp8_tables", "INDEX_DIM", "INDEX_ROW_BYTES", "nvfp4_mla_plan_step",
     "nvfp4_mla_truncate", "nvfp4_mla_index_append", "nvfp4_mla_index_read",
-    "sparse_mla_select_workspace_size", "sparse_mla_select", "library_path",
+    "sparse_mla_select_workspace_size", "sparse_mla_select", "nvfp4_mla_fork", "nvfp4_mla_release",
+    "nvfp4_mla_compact_workspace_size", "nvfp4_mla_compact", "nvfp4_mla_copy_pages", "library_path",
 ]
 
 
@@ -344,10 +345,10 @@ def nvfp4_mla_truncate(keep_lens: torch.Tensor, seq_lens: torch.Tensor, block_ta
 
 # ------------------------------------------------- index-key cache and selection
 def _pool(cache: torch.Tensor, num_blocks: int, block_stride_bytes: int, page_size: int,
-          device: int) -> int:
+          device: int, row_bytes: int = INDEX_ROW_BYTES) -> int:
     """Device pointer of a pool that holds num_blocks pages; it may end with the last page's rows
     (a layer's view of a pool that interleaves several)."""
-    least = (num_blocks - 1) * block_stride_bytes + page_size * INDEX_ROW_BYTES
+    least = (num_blocks - 1) * block_stride_bytes + page_size * row_bytes
     if (not cache.is_contiguous() or cache.get_device() != device
             or cache.numel() * cache.element_size() < least):
         raise ValueError("cache must be a contiguous tensor that reaches to the end of page "
@@ -439,3 +440,149 @@ def sparse_mla_select(q_index: torch.Tensor, weights: torch.Tensor, q_seq: torch
         ws or 0, _stream(stream))
     _check(st, "sparse_mla_select")
     return topk_idx
+
+
+# --------------------------------------------------------------- shared pages
+def nvfp4_mla_fork(src_seqs: torch.Tensor, dst_seqs: torch.Tensor, fork_lens: torch.Tensor,
+                   seq_lens: torch.Tensor, block_table: torch.Tensor, page_size: int,
+                   page_shares: torch.Tensor, free_pages: torch.Tensor, free_count: torch.Tensor,
+                   seq_lens_out: Optional[torch.Tensor] = None,
+                   page_shares_out: Optional[torch.Tensor] = None,
+                   free_count_out: Optional[torch.Tensor] = None,
+                   shared_blocks: Optional[torch.Tensor] = None,
+                   copy_src: Optional[torch.Tensor] = None, copy_dst: Optional[torch.Tensor] = None,
+                   refused_count: Optional[torch.Tensor] = None, stream=None):
+    """Sequences ``dst_seqs`` become the first ``fork_lens`` tokens of ``src_seqs`` (int32
+    [num_forks]) and share their whole pages; returns (shared_blocks, copy_src, copy_dst).
+
+    ``copy_src`` / ``copy_dst`` are the pages to copy with nvfp4_mla_copy_pages. ``page_shares``
+    (int32 [num_blocks]) counts a page's holders beyond the first. ``block_table`` is updated;
+    ``seq_lens``, ``page_shares`` and ``free_count`` too unless the ``*_out`` buffers are given.
+    """
+    dev, i32 = torch.cuda.current_device(), torch.int32
+    table, num_seqs, max_blocks = _table(block_table, dev)
+    n, num_blocks = src_seqs.numel(), page_shares.numel()
+    if shared_blocks is None:
+        shared_blocks = _result(n, i32, dev, stream)
+    if copy_src is None:
+        copy_src = _result(n, i32, dev, stream)
+    if copy_dst is None:
+        copy_dst = _result(n, i32, dev, stream)
+    lens_out = seq_lens if seq_lens_out is None else seq_lens_out
+    shares_out = page_shares if page_shares_out is None else page_shares_out
+    count_out = free_count if free_count_out is None else free_count_out
+    st = _lib().nvfp4_mla_fork(
+        _arg(src_seqs, "src_seqs", i32, n, dev), _arg(dst_seqs, "dst_seqs", i32, n, dev),
+        _arg(fork_lens, "fork_lens", i32, n, dev), n, _arg(seq_lens, "seq_lens", i32, num_seqs, dev),
+        num_seqs, table, max_blocks, page_size, _arg(page_shares, "page_shares", i32, 0, dev),
+        num_blocks, _arg(free_pages, "free_pages", i32, 0, dev), free_pages.numel(),
+        _arg(free_count, "free_count", i32, 1, dev),
+        _arg(lens_out, "seq_lens_out", i32, num_seqs, dev),
+        _arg(shares_out, "page_shares_out", i32, num_blocks, dev),
+        _arg(count_out, "free_count_out", i32, 1, dev),
+        _arg(shared_blocks, "shared_blocks", i32, n, dev), _arg(copy_src, "copy_src", i32, n, dev),
+        _arg(copy_dst, "copy_dst", i32, n, dev), _opt(refused_count, "refused_count", i32, 1, dev),
+        _stream(stream))
+    _check(st, "nvfp4_mla_fork")
+    return shared_blocks, copy_src, copy_dst
+
+
+def nvfp4_mla_release(keep_lens: torch.Tensor, seq_lens: torch.Tensor, block_table: torch.Tensor,
+                      page_size: int, page_shares: torch.Tensor, free_pages: torch.Tensor,
+                      free_count: torch.Tensor, seq_lens_out: Optional[torch.Tensor] = None,
+                      page_shares_out: Optional[torch.Tensor] = None,
+                      free_count_out: Optional[torch.Tensor] = None,
+                      dropped_count: Optional[torch.Tensor] = None,
+                      refused_count: Optional[torch.Tensor] = None, stream=None) -> None:
+    """nvfp4_mla_truncate for sequences that share pages: a page goes onto ``free_pages`` when its
+    last holder drops it.
+
+    ``seq_lens``, ``page_shares`` and ``free_count`` are updated unless the ``*_out`` buffers are
+    given.
+    """
+    dev, i32 = torch.cuda.current_device(), torch.int32
+    table, num_seqs, max_blocks = _table(block_table, dev)
+    num_blocks = page_shares.numel()
+    lens_out = seq_lens if seq_lens_out is None else seq_lens_out
+    shares_out = page_shares if page_shares_out is None else page_shares_out
+    count_out = free_count if free_count_out is None else free_count_out
+    st = _lib().nvfp4_mla_release(
+        _arg(keep_lens, "keep_lens", i32, num_seqs, dev),
+        _arg(seq_lens, "seq_lens", i32, num_seqs, dev), num_seqs, table, max_blocks, page_size,
+        _arg(page_shares, "page_shares", i32, 0, dev), num_blocks,
+        _arg(free_pages, "free_pages", i32, 0, dev), free_pages.numel(),
+        _arg(free_count, "free_count", i32, 1, dev),
+        _arg(lens_out, "seq_lens_out", i32, num_seqs, dev),
+        _arg(shares_out, "page_shares_out", i32, num_blocks, dev),
+        _arg(count_out, "free_count_out", i32, 1, dev),
+        _opt(dropped_count, "dropped_count", i32, 1, dev),
+        _opt(refused_count, "refused_count", i32, 1, dev), _stream(stream))
+    _check(st, "nvfp4_mla_release")
+
+
+def nvfp4_mla_compact_workspace_size(num_blocks: int) -> int:
+    n = int(_lib().nvfp4_mla_compact_workspace_size(num_blocks))
+    if n == (1 << 64) - 1:
+        raise ValueError("invalid number of pages")
+    return n
+
+
+def nvfp4_mla_compact(seq_lens: torch.Tensor, block_table: torch.Tensor, page_size: int,
+                      page_shares: torch.Tensor, free_pages: torch.Tensor,
+                      free_count: torch.Tensor, max_moves: int,
+                      block_table_out: Optional[torch.Tensor] = None,
+                      page_shares_out: Optional[torch.Tensor] = None,
+                      free_pages_out: Optional[torch.Tensor] = None,
+                      free_count_out: Optional[torch.Tensor] = None,
+                      copy_src: Optional[torch.Tensor] = None,
+                      copy_dst: Optional[torch.Tensor] = None,
+                      pages_end: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None):
+    """Up to ``max_moves`` of the highest pages in use become the lowest free ones; returns
+    (copy_src, copy_dst), the pages to copy with nvfp4_mla_copy_pages (-1 behind the last move).
+
+    ``block_table``, ``page_shares``, ``free_pages`` and ``free_count`` are updated unless the
+    ``*_out`` buffers are given.
+    """
+    dev, i32 = torch.cuda.current_device(), torch.int32
+    table, num_seqs, max_blocks = _table(block_table, dev)
+    num_blocks, moves = page_shares.numel(), max(max_moves, 0)
+    if copy_src is None:
+        copy_src = _result(moves, i32, dev, stream)
+    if copy_dst is None:
+        copy_dst = _result(moves, i32, dev, stream)
+    if workspace is None and num_blocks > 0:
+        workspace = _scratch(nvfp4_mla_compact_workspace_size(num_blocks), torch.uint8, dev, stream)
+    table_out = block_table if block_table_out is None else block_table_out
+    shares_out = page_shares if page_shares_out is None else page_shares_out
+    pages_out = free_pages if free_pages_out is None else free_pages_out
+    count_out = free_count if free_count_out is None else free_count_out
+    st = _lib().nvfp4_mla_compact(
+        _arg(seq_lens, "seq_lens", i32, num_seqs, dev), num_seqs, table, max_blocks, page_size,
+        _arg(page_shares, "page_shares", i32, 0, dev), num_blocks,
+        _arg(free_pages, "free_pages", i32, 0, dev), free_pages.numel(),
+        _arg(free_count, "free_count", i32, 1, dev), max_moves,
+        _arg(table_out, "block_table_out", i32, num_seqs * max_blocks, dev),
+        _arg(shares_out, "page_shares_out", i32, num_blocks, dev),
+        _arg(pages_out, "free_pages_out", i32, free_pages.numel(), dev),
+        _arg(count_out, "free_count_out", i32, 1, dev), _arg(copy_src, "copy_src", i32, moves, dev),
+        _arg(copy_dst, "copy_dst", i32, moves, dev), _opt(pages_end, "pages_end", i32, 1, dev),
+        None if workspace is None else _arg(workspace, "workspace", workspace.dtype, 0, dev),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "nvfp4_mla_compact")
+    return copy_src, copy_dst
+
+
+def nvfp4_mla_copy_pages(copy_src: torch.Tensor, copy_dst: torch.Tensor, cache: torch.Tensor,
+                         num_blocks: int, block_stride_bytes: int, page_bytes: int,
+                         invalid_count: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Copy the first ``page_bytes`` of pages ``copy_src`` to pages ``copy_dst`` (int32 [n]; pairs
+    with a -1 are skipped) of a pool."""
+    dev, i32 = torch.cuda.current_device(), torch.int32
+    n = copy_src.numel()
+    st = _lib().nvfp4_mla_copy_pages(
+        _arg(copy_src, "copy_src", i32, n, dev), _arg(copy_dst, "copy_dst", i32, n, dev), n,
+        _pool(cache, num_blocks, block_stride_bytes, 1, dev, page_bytes), num_blocks,
+        block_stride_bytes, page_bytes, _opt(invalid_count, "invalid_count", i32, 1, dev),
+        _stream(stream))
+    _check(st, "nvfp4_mla_copy_pages")

@@ -39,6 +39,13 @@ SIGNATURES = {
     "sparse_mla_select_workspace_size": (SZ, [I32, I32, I32, I32, I32]),
     "sparse_mla_select": (I32, [P, P, P, P, I32, I32, P, I32, I32, I32, P, I64, I64, I32, I32, I32,
                                 I32, P, P, SZ, P]),
+    "nvfp4_mla_fork": (I32, [P, P, P, I32, P, I32, P, I32, I32, P, I32, P, I32, P, P, P, P, P, P, P,
+                             P, P]),
+    "nvfp4_mla_release": (I32, [P, P, I32, P, I32, I32, P, I32, P, I32, P, P, P, P, P, P, P]),
+    "nvfp4_mla_compact_workspace_size": (SZ, [I32]),
+    "nvfp4_mla_compact": (I32, [P, I32, P, I32, I32, P, I32, P, I32, P, I32, P, P, P, P, P, P, P, P,
+                                SZ, P]),
+    "nvfp4_mla_copy_pages": (I32, [P, P, I32, P, I64, I64, I64, P, P]),
 }
 
 

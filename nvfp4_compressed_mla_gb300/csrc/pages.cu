@@ -1,0 +1,752 @@
+// pages.cu -- pages that several sequences share: forking, releasing, compacting and copying.
+//
+// page_shares[p] counts the holders of page p beyond the first, so that a free
+// page and a page with one holder both have 0 and nvfp4_mla_plan_step, which
+// hands out pages that have one, needs no knowledge of it. A fork shares whole
+// pages only and copies a partly filled last page, so no sequence ever appends
+// to a page that another one reads.
+//
+// All four work on metadata of a few kilobytes to a few megabytes and are bound
+// by latency (dependent loads, launches, barriers), but for the copy of pages,
+// which is bound by HBM: it reads and writes each page once.
+#include "plan_common.cuh"
+
+namespace nvfp4_mla {
+namespace {
+
+constexpr int kRowThreads = 256;      // CTAs that walk rows of a table
+constexpr int kRowChunk = 1024;       // entries of a row that such a CTA takes at a time
+constexpr int kCopyVecs = 4;          // 16-byte vectors that a copying thread has under way
+
+// ------------------------------------------------------------------------- fork
+struct ForkParams {
+  const int32_t* src_seqs;
+  const int32_t* dst_seqs;
+  const int32_t* fork_lens;
+  int32_t num_forks;
+  const int32_t* seq_lens;
+  int32_t num_seqs;
+  int32_t* block_table;
+  int32_t max_blocks;
+  PageSize page;
+  const int32_t* page_shares;
+  int32_t num_blocks;
+  const int32_t* free_pages;
+  int32_t free_capacity;
+  const int32_t* free_count;
+  int32_t* seq_lens_out;
+  int32_t* page_shares_out;
+  int32_t* free_count_out;
+  int32_t* shared_blocks;
+  int32_t* copy_src;
+  int32_t* copy_dst;
+  int32_t* refused_count;
+};
+
+__device__ __forceinline__ void copy_ints(const int32_t* __restrict__ from, int32_t* __restrict__ to,
+                                          int64_t n, int64_t first, int64_t stride) {
+  for (int64_t i = first; i < n; i += 4 * stride) {
+    int32_t v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i + u * stride < n) v[u] = __ldg(from + i + u * stride);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i + u * stride < n) to[i + u * stride] = v[u];
+  }
+}
+
+// CTA 0 decides which forks are served (one prefix sum over the fresh pages
+// that they need) and writes all but the shared entries; the other CTAs copy
+// the counts of holders where those go to another buffer.
+__global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkParams p) {
+  extern __shared__ int32_t claim[];  // [num_seqs] first fork that names the sequence as its dst
+  __shared__ int64_t sums[32];
+  const int tid = threadIdx.x;
+  cudaTriggerProgrammaticLaunchCompletion();
+  if (blockIdx.x > 0) {
+    copy_ints(p.page_shares, p.page_shares_out, p.num_blocks,
+              static_cast<int64_t>(blockIdx.x - 1) * kPlanThreads + tid,
+              static_cast<int64_t>(gridDim.x - 1) * kPlanThreads);
+    return;
+  }
+  // an ordinary load: the count may be replaced below
+  const int32_t free_now = min(max(*p.free_count, 0), p.free_capacity);
+  for (int s = tid; s < p.num_seqs; s += kPlanThreads) claim[s] = p.num_forks;
+  __syncthreads();
+  for (int i = tid; i < p.num_forks; i += kPlanThreads) {
+    const int32_t dst = __ldg(p.dst_seqs + i);
+    if (__ldg(p.src_seqs + i) != -1 && dst >= 0 && dst < p.num_seqs) atomicMin(claim + dst, i);
+  }
+  __syncthreads();
+  const int64_t room = static_cast<int64_t>(p.max_blocks) * p.page.size;
+  int64_t asked = 0;
+  int taken = 0, refused = 0;
+  for (int i0 = 0; i0 < p.num_forks; i0 += kPlanThreads) {
+    const int i = i0 + tid;
+    const bool here = i < p.num_forks;
+    const int32_t src = here ? __ldg(p.src_seqs + i) : -1;
+    const int32_t dst = here ? __ldg(p.dst_seqs + i) : -1;
+    const int32_t len = here ? __ldg(p.fork_lens + i) : 0;
+    bool ok = src >= 0 && src < p.num_seqs && dst >= 0 && dst < p.num_seqs && len >= 0 &&
+              len <= room && claim[min(max(dst, 0), p.num_seqs - 1)] == i;
+    // ordinary loads: the lengths may be replaced below
+    ok = ok && len <= p.seq_lens[src] && p.seq_lens[dst] == 0;
+    const int32_t full = ok ? p.page.block(len) : 0;
+    const bool need = ok && len != full * p.page.size;
+    const int64_t rank = block_scan(need ? 1 : 0, asked, sums);
+    ok = ok && (!need || rank <= free_now);
+    int32_t from = -1, to = -1;
+    if (ok && need) {
+      ++taken;
+      to = __ldg(p.free_pages + (free_now - rank));
+      from = p.block_table[static_cast<int64_t>(src) * p.max_blocks + full];
+      p.block_table[static_cast<int64_t>(dst) * p.max_blocks + full] = to;
+    }
+    if (from < 0 || from >= p.num_blocks || to < 0 || to >= p.num_blocks) from = to = -1;
+    if (here) {
+      p.shared_blocks[i] = ok ? full : -1;
+      p.copy_src[i] = from;
+      p.copy_dst[i] = to;
+      if (!ok && src != -1) ++refused;
+    }
+  }
+  __syncthreads();  // every length has been read
+  if (p.seq_lens_out != p.seq_lens) {
+    for (int s = tid; s < p.num_seqs; s += kPlanThreads) p.seq_lens_out[s] = p.seq_lens[s];
+    __syncthreads();
+  }
+  for (int i = tid; i < p.num_forks; i += kPlanThreads)  // a thread's own results
+    if (p.shared_blocks[i] >= 0) p.seq_lens_out[__ldg(p.dst_seqs + i)] = __ldg(p.fork_lens + i);
+  int64_t all = 0;
+  block_scan(taken, all, sums);
+  if (tid == 0) *p.free_count_out = free_now - static_cast<int32_t>(all);
+  if (p.refused_count != nullptr && refused > 0) atomicAdd(p.refused_count, refused);
+}
+
+// The shared entries, 1024 of a fork at a time, and their pages' holders.
+__global__ void __launch_bounds__(kRowThreads) fork_share_kernel(const ForkParams p, int32_t chunks) {
+  cudaGridDependencySynchronize();
+  const int64_t units = static_cast<int64_t>(p.num_forks) * chunks;
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int32_t i = static_cast<int32_t>(u / chunks);
+    const int32_t b0 = static_cast<int32_t>(u - static_cast<int64_t>(i) * chunks) * kRowChunk;
+    const int32_t full = __ldcg(p.shared_blocks + i);
+    if (full <= b0) continue;
+    const int32_t* from = p.block_table + static_cast<int64_t>(__ldg(p.src_seqs + i)) * p.max_blocks;
+    int32_t* to = p.block_table + static_cast<int64_t>(__ldg(p.dst_seqs + i)) * p.max_blocks;
+    int32_t page[kRowChunk / kRowThreads];
+#pragma unroll
+    for (int k = 0; k < kRowChunk / kRowThreads; ++k) {
+      const int32_t b = b0 + k * kRowThreads + threadIdx.x;
+      page[k] = b < full ? from[b] : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kRowChunk / kRowThreads; ++k) {
+      const int32_t b = b0 + k * kRowThreads + threadIdx.x;
+      if (b < full) to[b] = page[k];
+      if (page[k] >= 0 && page[k] < p.num_blocks) atomicAdd(p.page_shares_out + page[k], 1);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------- release
+struct ReleaseParams {
+  const int32_t* keep_lens;
+  const int32_t* seq_lens;
+  int32_t num_seqs;
+  const int32_t* block_table;
+  int32_t max_blocks;
+  PageSize page;
+  const int32_t* page_shares;
+  int32_t num_blocks;
+  int32_t* free_pages;
+  int32_t free_capacity;
+  const int32_t* free_count;
+  int32_t* seq_lens_out;
+  int32_t* page_shares_out;
+  int32_t* free_count_out;
+  int32_t* dropped_count;
+  int32_t* refused_count;
+};
+
+constexpr int kReleaseUnits = 4096;  // beside one a sequence
+constexpr int kReleaseFlight = 8;    // entries of a lane under way
+constexpr int kReleaseChunk = 32 * kReleaseFlight;
+constexpr int kReleaseMark = 1 << 20;
+constexpr size_t kReleaseBytes = 12;  // of shared memory a sequence, beside the units' 4 each
+static_assert(kReleaseBytes * NVFP4_MLA_MAX_PLAN_SEQS + 4 * kReleaseUnits + 512 <= kMaxSharedBytes,
+              "shared memory");
+
+// One cluster. The released entries are cut into units of (at least) 256, at
+// most kReleaseUnits and one a sequence, which the warps take in turn:
+//   1. every entry takes one off its page's count; a page whose count falls
+//      below 0 has lost its last holder;
+//   2. the first sequence that dropped such a page marks it with its number
+//      (the lowest, by an atomic minimum below all counts): that entry is the
+//      one that returns the page, whatever the order of the atomics was;
+//   3. the units' returned pages are counted, summed up and pushed.
+__global__ void __launch_bounds__(kPlanThreads) release_kernel(const ReleaseParams p) {
+  extern __shared__ int32_t dyn[];
+  int32_t* begin = dyn;                  // [num_seqs] first released block
+  int32_t* unit_end = dyn + p.num_seqs;  // [num_seqs] entries, then units up to and with sequence s
+  int32_t* counts = unit_end + p.num_seqs;  // [num_seqs + kReleaseUnits] pages of a unit, then sums
+  __shared__ int64_t sums[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = cta_rank(), ctas = cluster_size();
+  const int32_t free_now = min(max(*p.free_count, 0), p.free_capacity);
+
+  int64_t entries = 0;
+  int refused = 0;
+  for (int s0 = 0; s0 < p.num_seqs; s0 += kPlanThreads) {
+    const int s = s0 + tid;
+    int32_t b0 = 0, b1 = 0;
+    bool cut = false;
+    if (s < p.num_seqs) {
+      const int32_t len = p.seq_lens[s], keep = __ldg(p.keep_lens + s);
+      cut = keep >= 0 && keep < len;
+      if (cut) {
+        const int32_t inner = p.page.block(keep);
+        if (keep != inner * p.page.size && inner < p.max_blocks) {
+          const int32_t page = __ldg(p.block_table + static_cast<int64_t>(s) * p.max_blocks + inner);
+          // an ordinary load: the counts may be replaced behind the barrier
+          if (page >= 0 && page < p.num_blocks && p.page_shares[page] > 0) {
+            cut = false;
+            ++refused;
+          }
+        }
+        if (cut) {
+          b0 = p.page.blocks(keep);
+          b1 = max(min(p.page.blocks(len), p.max_blocks), b0);
+        }
+      }
+      begin[s] = cut ? b0 : -1;
+      unit_end[s] = b1 - b0;
+    }
+    block_scan(b1 - b0, entries, sums);
+  }
+  const int64_t chunk =
+      max((entries + kReleaseUnits - 1) / kReleaseUnits + kReleaseChunk - 1, int64_t{kReleaseChunk}) /
+      kReleaseChunk * kReleaseChunk;
+  int64_t units_so_far = 0;
+  for (int s0 = 0; s0 < p.num_seqs; s0 += kPlanThreads) {
+    const int s = s0 + tid;
+    const int64_t to = block_scan(s < p.num_seqs ? (unit_end[s] + chunk - 1) / chunk : 0, units_so_far, sums);
+    if (s < p.num_seqs) unit_end[s] = static_cast<int32_t>(to);
+  }
+  const int units = static_cast<int>(units_so_far);
+  if (p.page_shares_out != p.page_shares)
+    copy_ints(p.page_shares, p.page_shares_out, p.num_blocks,
+              static_cast<int64_t>(rank) * kPlanThreads + tid, static_cast<int64_t>(ctas) * kPlanThreads);
+  if (rank == 0 && p.refused_count != nullptr && refused > 0) atomicAdd(p.refused_count, refused);
+  cluster_barrier();  // the counts may change now; the units are in every CTA's shared memory
+
+  // f(s, pages of 8 x 32 entries (-1: none)) for each round of a unit
+  auto walk = [&](int u, auto&& f) {
+    int s;
+    {  // the sequence: the first whose units end behind u
+      int lo = 0, hi = p.num_seqs;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (unit_end[mid] <= u) lo = mid + 1;
+        else hi = mid;
+      }
+      s = lo;
+    }
+    const int32_t first = s > 0 ? unit_end[s - 1] : 0;
+    const int64_t b1 = min(p.page.blocks(p.seq_lens[s]), p.max_blocks);
+    int64_t b = begin[s] + (u - first) * chunk;
+    const int64_t end = min(b + chunk, b1);
+    const int32_t* row = p.block_table + static_cast<int64_t>(s) * p.max_blocks;
+    for (; b < end; b += kReleaseChunk) {
+      int32_t page[kReleaseFlight];
+#pragma unroll
+      for (int k = 0; k < kReleaseFlight; ++k) {
+        const int64_t at = b + 32 * k + lane;
+        page[k] = at < end ? __ldg(row + at) : -1;
+        if (page[k] >= p.num_blocks) page[k] = -1;
+      }
+      f(s, page);
+    }
+  };
+  const int first_unit = static_cast<int>(rank) * kPlanWarps + warp;
+  const int stride = static_cast<int>(ctas) * kPlanWarps;
+
+  for (int u = first_unit; u < units; u += stride)
+    walk(u, [&](int, const int32_t(&page)[kReleaseFlight]) {
+#pragma unroll
+      for (int k = 0; k < kReleaseFlight; ++k)
+        if (page[k] >= 0) atomicAdd(p.page_shares_out + page[k], -1);
+    });
+  cluster_barrier();
+  for (int u = first_unit; u < units; u += stride)
+    walk(u, [&](int s, const int32_t(&page)[kReleaseFlight]) {
+      int32_t held[kReleaseFlight];
+#pragma unroll
+      for (int k = 0; k < kReleaseFlight; ++k)
+        held[k] = page[k] >= 0 ? __ldcg(p.page_shares_out + page[k]) : 0;
+#pragma unroll
+      for (int k = 0; k < kReleaseFlight; ++k)
+        if (held[k] < 0) atomicMin(p.page_shares_out + page[k], s - kReleaseMark);
+    });
+  cluster_barrier();
+  const uint32_t counts_addr = smem_u32(counts);
+  for (int u = first_unit; u < units; u += stride) {
+    int n = 0;
+    walk(u, [&](int s, const int32_t(&page)[kReleaseFlight]) {
+      int32_t held[kReleaseFlight];
+#pragma unroll
+      for (int k = 0; k < kReleaseFlight; ++k)
+        held[k] = page[k] >= 0 ? __ldcg(p.page_shares_out + page[k]) : 0;
+#pragma unroll
+      for (int k = 0; k < kReleaseFlight; ++k)
+        n += __popc(__ballot_sync(0xffffffffu, held[k] == s - kReleaseMark));
+    });
+    if (lane < ctas) st_cluster(counts_addr + 4u * static_cast<uint32_t>(u), lane, n);
+  }
+  cluster_barrier();
+
+  int64_t all = 0;
+  for (int u0 = 0; u0 < units; u0 += kPlanThreads) {
+    const int u = u0 + tid;
+    const int64_t to = block_scan(u < units ? counts[u] : 0, all, sums);
+    if (u < units) counts[u] = static_cast<int32_t>(to);  // at most num_blocks
+  }
+  __syncthreads();
+  const int64_t top = free_now + all;  // stack height if nothing is dropped
+  if (rank == 0 && tid == 0) {
+    *p.free_count_out = static_cast<int32_t>(min(top, static_cast<int64_t>(p.free_capacity)));
+    if (p.dropped_count != nullptr && top > p.free_capacity)
+      atomicAdd(p.dropped_count, static_cast<int32_t>(top - p.free_capacity));
+  }
+  for (int u = first_unit; u < units; u += stride) {
+    int64_t at = top - (u > 0 ? counts[u - 1] : 0);  // one above the unit's first page
+    walk(u, [&](int s, const int32_t(&page)[kReleaseFlight]) {
+      int32_t held[kReleaseFlight];
+#pragma unroll
+      for (int k = 0; k < kReleaseFlight; ++k)
+        held[k] = page[k] >= 0 ? __ldcg(p.page_shares_out + page[k]) : 0;
+#pragma unroll
+      for (int k = 0; k < kReleaseFlight; ++k) {
+        const bool mine = held[k] == s - kReleaseMark;
+        const uint32_t live = __ballot_sync(0xffffffffu, mine);
+        const int64_t slot = at - 1 - __popc(live & ((1u << lane) - 1));
+        if (mine && slot < p.free_capacity) p.free_pages[slot] = page[k];
+        // nobody else takes the 0 for its mark
+        if (mine) p.page_shares_out[page[k]] = 0;
+        at -= __popc(live);
+      }
+    });
+  }
+  cluster_barrier();  // every length has been read
+  for (int s = static_cast<int>(rank) * kPlanThreads + tid; s < p.num_seqs;
+       s += static_cast<int>(ctas) * kPlanThreads)
+    p.seq_lens_out[s] = begin[s] >= 0 ? __ldg(p.keep_lens + s) : p.seq_lens[s];
+}
+
+// ---------------------------------------------------------------------- compact
+struct CompactParams {
+  const int32_t* seq_lens;
+  int32_t num_seqs;
+  const int32_t* block_table;
+  int32_t max_blocks;
+  PageSize page;
+  const int32_t* page_shares;
+  int32_t num_blocks;
+  const int32_t* free_pages;
+  int32_t free_capacity;
+  const int32_t* free_count;
+  int32_t max_moves;
+  int32_t* block_table_out;
+  int32_t* page_shares_out;
+  int32_t* free_pages_out;
+  int32_t* free_count_out;
+  int32_t* copy_src;
+  int32_t* copy_dst;
+  int32_t* pages_end;
+  // workspace
+  uint32_t* used;   // a bit a page: in a table
+  uint32_t* idle;   // a bit a page: on the stack
+  int32_t* moved;   // [num_blocks] the page's new id
+  int32_t words;    // of a bit map
+};
+
+// Every pass over the tables and the pools' metadata is a launch over the whole
+// device; the ranks between them are one CTA's.
+__global__ void __launch_bounds__(kPlanThreads) compact_clear_kernel(const CompactParams p) {
+  cudaTriggerProgrammaticLaunchCompletion();
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kPlanThreads + threadIdx.x;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kPlanThreads;
+  for (int64_t w = first; w < p.words; w += stride) p.used[w] = p.idle[w] = 0u;
+  for (int64_t i = first; i < p.num_blocks; i += stride) p.moved[i] = static_cast<int32_t>(i);
+  if (p.page_shares_out != p.page_shares)
+    copy_ints(p.page_shares, p.page_shares_out, p.num_blocks, first, stride);
+}
+
+__global__ void __launch_bounds__(kRowThreads) compact_mark_kernel(const CompactParams p, int32_t chunks) {
+  cudaGridDependencySynchronize();
+  cudaTriggerProgrammaticLaunchCompletion();
+  const int32_t count = min(max(__ldg(p.free_count), 0), p.free_capacity);
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x; i < count;
+       i += static_cast<int64_t>(gridDim.x) * kRowThreads) {
+    const int32_t page = __ldg(p.free_pages + i);
+    if (page >= 0 && page < p.num_blocks) atomicOr(p.idle + (page >> 5), 1u << (page & 31));
+  }
+  const int64_t units = static_cast<int64_t>(p.num_seqs) * chunks;
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int32_t s = static_cast<int32_t>(u / chunks);
+    const int32_t b0 = static_cast<int32_t>(u - static_cast<int64_t>(s) * chunks) * kRowChunk;
+    const int32_t end = min(p.page.blocks(__ldg(p.seq_lens + s)), p.max_blocks);
+    const int32_t* row = p.block_table + static_cast<int64_t>(s) * p.max_blocks;
+    int32_t page[kRowChunk / kRowThreads];
+#pragma unroll
+    for (int k = 0; k < kRowChunk / kRowThreads; ++k) {
+      const int32_t b = b0 + k * kRowThreads + threadIdx.x;
+      page[k] = b < end ? __ldg(row + b) : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kRowChunk / kRowThreads; ++k)
+      if (page[k] >= 0 && page[k] < p.num_blocks)
+        atomicOr(p.used + (page[k] >> 5), 1u << (page[k] & 31));
+  }
+}
+
+// The moves: used page number i from the top to free page number i from the
+// bottom, as long as that is downwards. One CTA; a thread has consecutive words
+// of the bit maps, and its first ranks are those of two prefix sums.
+__global__ void __launch_bounds__(kPlanThreads) compact_rank_kernel(const CompactParams p) {
+  __shared__ int64_t sums[32];
+  __shared__ int32_t sh_moves, sh_end;
+  cudaGridDependencySynchronize();
+  cudaTriggerProgrammaticLaunchCompletion();
+  const int tid = threadIdx.x;
+  const int32_t per = (p.words + kPlanThreads - 1) / kPlanThreads;
+  const int32_t w0 = min(tid * static_cast<int64_t>(per), static_cast<int64_t>(p.words));
+  const int32_t w1 = min(w0 + static_cast<int64_t>(per), static_cast<int64_t>(p.words));
+  int64_t n_used = 0, n_idle = 0;
+  for (int32_t w = w0; w < w1; ++w) {
+    const uint32_t a = __ldcg(p.used + w);
+    n_used += __popc(a);
+    n_idle += __popc(__ldcg(p.idle + w) & ~a);  // a page of a table is not free
+  }
+  int64_t all_used = 0, all_idle = 0;
+  const int32_t used_before = static_cast<int32_t>(block_scan(n_used, all_used, sums) - n_used);
+  const int32_t idle_before = static_cast<int32_t>(block_scan(n_idle, all_idle, sums) - n_idle);
+  const int32_t U = static_cast<int32_t>(all_used), F = static_cast<int32_t>(all_idle);
+  const int32_t most = min(min(U, F), p.max_moves);
+  if (tid == 0) sh_moves = sh_end = 0;
+  {
+    int32_t f = idle_before, t = U - 1 - used_before;  // rank from the bottom, from the top
+    for (int32_t w = w0; w < w1 && (f < most || t >= 0); ++w) {
+      const uint32_t a = __ldcg(p.used + w);
+      for (uint32_t bits = __ldcg(p.idle + w) & ~a; bits != 0; bits &= bits - 1, ++f)
+        if (f < most) p.copy_dst[f] = 32 * w + __ffs(bits) - 1;
+      for (uint32_t bits = a; bits != 0; bits &= bits - 1, --t)
+        if (t < most) p.copy_src[t] = 32 * w + __ffs(bits) - 1;
+    }
+  }
+  __syncthreads();
+  int down = 0;
+  for (int32_t i = tid; i < most; i += kPlanThreads) down += p.copy_dst[i] < p.copy_src[i];
+  if (down > 0) atomicAdd(&sh_moves, down);
+  __syncthreads();
+  const int32_t m = sh_moves;
+  {  // the stack: all free pages, the lowest on top
+    int32_t f = idle_before, t = U - 1 - used_before, end = 0;
+    for (int32_t w = w0; w < w1; ++w) {
+      const uint32_t a = __ldcg(p.used + w);
+      const uint32_t any = a | __ldcg(p.idle + w);
+      for (uint32_t bits = any; bits != 0; bits &= bits - 1) {
+        const uint32_t bit = bits & (0u - bits);
+        const int32_t page = 32 * w + __ffs(bits) - 1;
+        if ((a & bit) != 0) {
+          // above it: t used pages, F - f free ones
+          if (t < m) p.free_pages_out[t + min(F - m, F - f)] = page;
+          else end = page + 1;
+          --t;
+        } else {
+          // above it: t + 1 used pages, F - 1 - f free ones
+          if (f >= m) p.free_pages_out[F - 1 - f + min(m, t + 1)] = page;
+          else end = page + 1;
+          ++f;
+        }
+      }
+    }
+    if (end > 0) atomicMax(&sh_end, end);
+  }
+  for (int32_t i = tid; i < p.max_moves; i += kPlanThreads) {
+    if (i < m) {
+      const int32_t from = p.copy_src[i], to = p.copy_dst[i];
+      p.moved[from] = to;
+      p.page_shares_out[to] = p.page_shares_out[from];
+      p.page_shares_out[from] = 0;
+    } else {
+      p.copy_src[i] = p.copy_dst[i] = -1;
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    *p.free_count_out = F;
+    if (p.pages_end != nullptr) *p.pages_end = sh_end;
+  }
+}
+
+__global__ void __launch_bounds__(kRowThreads) compact_table_kernel(const CompactParams p, int32_t chunks) {
+  cudaGridDependencySynchronize();
+  const bool same = p.block_table_out == p.block_table;
+  const int64_t units = static_cast<int64_t>(p.num_seqs) * chunks;
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int32_t s = static_cast<int32_t>(u / chunks);
+    const int32_t b0 = static_cast<int32_t>(u - static_cast<int64_t>(s) * chunks) * kRowChunk;
+    const int32_t end = min(p.page.blocks(__ldg(p.seq_lens + s)), p.max_blocks);
+    const int64_t row = static_cast<int64_t>(s) * p.max_blocks;
+    int32_t page[kRowChunk / kRowThreads], to[kRowChunk / kRowThreads];
+#pragma unroll
+    for (int k = 0; k < kRowChunk / kRowThreads; ++k) {
+      const int32_t b = b0 + k * kRowThreads + threadIdx.x;
+      page[k] = b < p.max_blocks ? p.block_table[row + b] : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kRowChunk / kRowThreads; ++k) {
+      const int32_t b = b0 + k * kRowThreads + threadIdx.x;
+      const bool live = b < end && page[k] >= 0 && page[k] < p.num_blocks;
+      to[k] = live ? __ldcg(p.moved + page[k]) : page[k];
+    }
+#pragma unroll
+    for (int k = 0; k < kRowChunk / kRowThreads; ++k) {
+      const int32_t b = b0 + k * kRowThreads + threadIdx.x;
+      if (b < p.max_blocks && (!same || to[k] != page[k])) p.block_table_out[row + b] = to[k];
+    }
+  }
+}
+
+// ------------------------------------------------------------------------- copy
+// Pages are cut into equal segments of at most 16 KB, a CTA's at a time: each
+// thread has four 16-byte loads under way, eight CTAs an SM. A CTA reads the
+// page ids of all its units ahead (256 at a time), so that units without a page
+// cost no memory latency each.
+__global__ void __launch_bounds__(kRowThreads)
+    copy_pages_kernel(const int32_t* __restrict__ src, const int32_t* __restrict__ dst,
+                      int32_t num_copies, uint8_t* cache, int64_t num_blocks, int64_t stride,
+                      int64_t page_bytes, int32_t segments, int64_t segment_bytes,
+                      int32_t* invalid_count) {
+  __shared__ int32_t from[kRowThreads], to[kRowThreads];
+  const int64_t units = static_cast<int64_t>(num_copies) * segments;
+  for (int64_t u0 = blockIdx.x; u0 < units; u0 += static_cast<int64_t>(gridDim.x) * kRowThreads) {
+    const int64_t mine = u0 + static_cast<int64_t>(threadIdx.x) * gridDim.x;
+    int32_t a = -1, b = -1;
+    if (mine < units) {
+      const int64_t i = mine / segments;
+      a = __ldg(src + i);
+      b = __ldg(dst + i);
+      const bool skip = a == -1 || b == -1;
+      if (!skip && (a < 0 || b < 0 || a >= num_blocks || b >= num_blocks)) {
+        if (invalid_count != nullptr && mine - i * segments == 0) atomicAdd(invalid_count, 1);
+        a = -1;
+      }
+      if (skip || a == b) a = -1;
+    }
+    __syncthreads();
+    from[threadIdx.x] = a;
+    to[threadIdx.x] = b;
+    const int any = __syncthreads_count(a >= 0);
+    if (any == 0) continue;
+    for (int k = 0; k < kRowThreads; ++k) {
+      if (from[k] < 0) continue;
+      const int64_t unit = u0 + static_cast<int64_t>(k) * gridDim.x;
+      const int64_t lo = (unit % segments) * segment_bytes;
+      const int64_t hi = min(lo + segment_bytes, page_bytes);
+      const uint8_t* s = cache + static_cast<int64_t>(from[k]) * stride;
+      uint8_t* d = cache + static_cast<int64_t>(to[k]) * stride;
+      for (int64_t at = lo + 16 * threadIdx.x; at < hi; at += 16 * kRowThreads * kCopyVecs) {
+        uint4 v[kCopyVecs];
+#pragma unroll
+        for (int x = 0; x < kCopyVecs; ++x)
+          if (at + 16 * kRowThreads * x < hi)
+            v[x] = *reinterpret_cast<const uint4*>(s + at + 16 * kRowThreads * x);
+#pragma unroll
+        for (int x = 0; x < kCopyVecs; ++x)
+          if (at + 16 * kRowThreads * x < hi)
+            *reinterpret_cast<uint4*>(d + at + 16 * kRowThreads * x) = v[x];
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------------- host
+// A launch that may start while the one before it still runs, and waits for it itself.
+template <typename... Args>
+int32_t launch_after(void (*kernel)(Args...), unsigned grid, unsigned threads, cudaStream_t stream,
+                     Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return NVFP4_MLA_ERR_LAUNCH;
+  }
+  return NVFP4_MLA_OK;
+}
+
+unsigned row_grid(int64_t rows, int32_t chunks, int sms) {
+  const int64_t units = rows * chunks, most = static_cast<int64_t>(sms) * 8;
+  return static_cast<unsigned>(units < 1 ? 1 : units < most ? units : most);
+}
+int32_t row_chunks(int32_t max_blocks) { return (max_blocks + kRowChunk - 1) / kRowChunk; }
+
+size_t bitmap_words(int64_t num_blocks) { return static_cast<size_t>((num_blocks + 127) / 128 * 4); }
+
+}  // namespace
+}  // namespace nvfp4_mla
+
+using namespace nvfp4_mla;
+
+extern "C" int32_t nvfp4_mla_fork(const int32_t* src_seqs, const int32_t* dst_seqs,
+                                  const int32_t* fork_lens, int32_t num_forks,
+                                  const int32_t* seq_lens, int32_t num_seqs, int32_t* block_table,
+                                  int32_t max_blocks_per_seq, int32_t page_size,
+                                  const int32_t* page_shares, int32_t num_blocks,
+                                  const int32_t* free_pages, int32_t free_capacity,
+                                  const int32_t* free_count, int32_t* seq_lens_out,
+                                  int32_t* page_shares_out, int32_t* free_count_out,
+                                  int32_t* shared_blocks, int32_t* copy_src, int32_t* copy_dst,
+                                  int32_t* refused_count, void* stream) {
+  if (!plan_shape_ok(num_seqs, max_blocks_per_seq, page_size, free_capacity) || num_forks < 0 ||
+      num_forks > NVFP4_MLA_MAX_PLAN_SEQS || num_blocks < 1)
+    return NVFP4_MLA_ERR_SHAPE;
+  if (!seq_lens || !block_table || !page_shares || !free_count || !seq_lens_out ||
+      !page_shares_out || !free_count_out || (free_capacity > 0 && !free_pages) ||
+      (num_forks > 0 && (!src_seqs || !dst_seqs || !fork_lens || !shared_blocks || !copy_src || !copy_dst)))
+    return NVFP4_MLA_ERR_NULL;
+  int dev = 0, sms = 0;
+  if (int32_t st = current_device_checked(&dev, &sms)) return st;
+  const ForkParams p = {src_seqs,    dst_seqs,  fork_lens,  num_forks,      seq_lens,
+                        num_seqs,    block_table, max_blocks_per_seq, page_division(page_size),
+                        page_shares, num_blocks, free_pages, free_capacity, free_count,
+                        seq_lens_out, page_shares_out, free_count_out, shared_blocks, copy_src,
+                        copy_dst,    refused_count};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const size_t smem = 4 * static_cast<size_t>(num_seqs);
+  // the same limit in every call (it is the process's)
+  if (smem > 40 * 1024 &&
+      cudaFuncSetAttribute(reinterpret_cast<const void*>(fork_plan_kernel),
+                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           4 * NVFP4_MLA_MAX_PLAN_SEQS) != cudaSuccess) {
+    cudaGetLastError();
+    return NVFP4_MLA_ERR_LAUNCH;
+  }
+  unsigned grid = 1;
+  if (page_shares_out != page_shares) {
+    const int64_t copying = (static_cast<int64_t>(num_blocks) + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
+    grid += static_cast<unsigned>(copying < sms ? copying : sms);
+  }
+  fork_plan_kernel<<<grid, kPlanThreads, smem, s>>>(p);
+  if (int32_t st = launch_status()) return st;
+  if (num_forks == 0) return NVFP4_MLA_OK;
+  const int32_t chunks = row_chunks(max_blocks_per_seq);
+  return launch_after(fork_share_kernel, row_grid(num_forks, chunks, sms), kRowThreads, s, p, chunks);
+}
+
+extern "C" int32_t nvfp4_mla_release(const int32_t* keep_lens, const int32_t* seq_lens,
+                                     int32_t num_seqs, const int32_t* block_table,
+                                     int32_t max_blocks_per_seq, int32_t page_size,
+                                     const int32_t* page_shares, int32_t num_blocks,
+                                     int32_t* free_pages, int32_t free_capacity,
+                                     const int32_t* free_count, int32_t* seq_lens_out,
+                                     int32_t* page_shares_out, int32_t* free_count_out,
+                                     int32_t* dropped_count, int32_t* refused_count, void* stream) {
+  if (!plan_shape_ok(num_seqs, max_blocks_per_seq, page_size, free_capacity) || num_blocks < 1)
+    return NVFP4_MLA_ERR_SHAPE;
+  if (!keep_lens || !seq_lens || !block_table || !page_shares || !free_count || !seq_lens_out ||
+      !page_shares_out || !free_count_out || (free_capacity > 0 && !free_pages))
+    return NVFP4_MLA_ERR_NULL;
+  int dev = 0, sms = 0;
+  if (int32_t st = current_device_checked(&dev, &sms)) return st;
+  const ReleaseParams p = {keep_lens,   seq_lens,   num_seqs,   block_table,   max_blocks_per_seq,
+                           page_division(page_size), page_shares, num_blocks, free_pages,
+                           free_capacity, free_count, seq_lens_out, page_shares_out, free_count_out,
+                           dropped_count, refused_count};
+  const size_t smem = kReleaseBytes * static_cast<size_t>(num_seqs) + 4 * kReleaseUnits;
+  // a table that 32 warps walk in one round needs no cluster
+  const bool small = static_cast<int64_t>(num_seqs) * row_chunks(max_blocks_per_seq) <= kPlanWarps / 4 &&
+                     page_shares_out == page_shares;
+  return launch_cluster_smem(release_kernel, p, small ? 1 : kMaxCluster, smem,
+                             kReleaseBytes * NVFP4_MLA_MAX_PLAN_SEQS + 4 * kReleaseUnits,
+                             static_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t nvfp4_mla_compact_workspace_size(int32_t num_blocks) {
+  if (num_blocks < 1) return SIZE_MAX;
+  return 2 * 4 * bitmap_words(num_blocks) + 4 * static_cast<size_t>(num_blocks);
+}
+
+extern "C" int32_t nvfp4_mla_compact(const int32_t* seq_lens, int32_t num_seqs,
+                                     const int32_t* block_table, int32_t max_blocks_per_seq,
+                                     int32_t page_size, const int32_t* page_shares,
+                                     int32_t num_blocks, const int32_t* free_pages,
+                                     int32_t free_capacity, const int32_t* free_count,
+                                     int32_t max_moves, int32_t* block_table_out,
+                                     int32_t* page_shares_out, int32_t* free_pages_out,
+                                     int32_t* free_count_out, int32_t* copy_src, int32_t* copy_dst,
+                                     int32_t* pages_end, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+  if (!plan_shape_ok(num_seqs, max_blocks_per_seq, page_size, free_capacity) || num_blocks < 1 ||
+      max_moves < 0)
+    return NVFP4_MLA_ERR_SHAPE;
+  if (!seq_lens || !block_table || !page_shares || !free_count || !block_table_out ||
+      !page_shares_out || !free_count_out || (free_capacity > 0 && (!free_pages || !free_pages_out)) ||
+      (max_moves > 0 && (!copy_src || !copy_dst)))
+    return NVFP4_MLA_ERR_NULL;
+  if (!workspace || workspace_bytes < nvfp4_mla_compact_workspace_size(num_blocks))
+    return NVFP4_MLA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return NVFP4_MLA_ERR_ALIGN;
+  int dev = 0, sms = 0;
+  if (int32_t st = current_device_checked(&dev, &sms)) return st;
+  const size_t words = bitmap_words(num_blocks);
+  uint32_t* used = static_cast<uint32_t*>(workspace);
+  const CompactParams p = {seq_lens,       num_seqs,        block_table,    max_blocks_per_seq,
+                           page_division(page_size), page_shares, num_blocks, free_pages,
+                           free_capacity,  free_count,      max_moves,      block_table_out,
+                           page_shares_out, free_pages_out, free_count_out, copy_src,
+                           copy_dst,       pages_end,       used,           used + words,
+                           reinterpret_cast<int32_t*>(used + 2 * words), static_cast<int32_t>(words)};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int64_t clearing = (static_cast<int64_t>(num_blocks) + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
+  compact_clear_kernel<<<static_cast<unsigned>(clearing < sms ? clearing : sms), kPlanThreads, 0, s>>>(p);
+  if (int32_t st = launch_status()) return st;
+  const int32_t chunks = row_chunks(max_blocks_per_seq);
+  const unsigned grid = row_grid(num_seqs, chunks, sms);
+  if (int32_t st = launch_after(compact_mark_kernel, grid, kRowThreads, s, p, chunks)) return st;
+  if (int32_t st = launch_after(compact_rank_kernel, 1, kPlanThreads, s, p)) return st;
+  return launch_after(compact_table_kernel, grid, kRowThreads, s, p, chunks);
+}
+
+extern "C" int32_t nvfp4_mla_copy_pages(const int32_t* copy_src, const int32_t* copy_dst,
+                                        int32_t num_copies, void* cache, int64_t num_blocks,
+                                        int64_t block_stride_bytes, int64_t page_bytes,
+                                        int32_t* invalid_count, void* stream) {
+  if (num_copies < 0) return NVFP4_MLA_ERR_SHAPE;
+  if (num_copies == 0) return NVFP4_MLA_OK;
+  if (!copy_src || !copy_dst || !cache) return NVFP4_MLA_ERR_NULL;
+  if (num_blocks < 1 || num_blocks > INT32_MAX || page_bytes < 1 || block_stride_bytes < page_bytes ||
+      block_stride_bytes > INT64_MAX / num_blocks)
+    return NVFP4_MLA_ERR_SHAPE;
+  if (!aligned16(cache) || (block_stride_bytes & 15) || (page_bytes & 15)) return NVFP4_MLA_ERR_ALIGN;
+  int dev = 0, sms = 0;
+  if (int32_t st = current_device_checked(&dev, &sms)) return st;
+  constexpr int64_t kRound = 16 * kRowThreads * kCopyVecs;  // what a CTA has under way
+  const int64_t segments = (page_bytes + kRound - 1) / kRound;
+  if (segments > INT32_MAX) return NVFP4_MLA_ERR_SHAPE;
+  const int64_t segment_bytes = ((page_bytes + segments - 1) / segments + 15) / 16 * 16;
+  copy_pages_kernel<<<row_grid(num_copies, static_cast<int32_t>(segments), sms), kRowThreads, 0,
+                      static_cast<cudaStream_t>(stream)>>>(
+      copy_src, copy_dst, num_copies, static_cast<uint8_t*>(cache), num_blocks, block_stride_bytes,
+      page_bytes, static_cast<int32_t>(segments), segment_bytes, invalid_count);
+  return launch_status();
+}
