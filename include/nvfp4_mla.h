@@ -480,6 +480,62 @@ int32_t sparse_mla_select(const void* q_index, const float* weights, const int32
                           void* stream);
 
 /* ------------------------------------------------------------------------
+ * Dense causal absorbed-MLA attention of a step's new tokens over the cache:
+ * prompt chunks, drafts and single tokens, in any mixture. The step's tokens
+ * are packed by sequence, as nvfp4_mla_plan_step packs them, and their rows
+ * are in the cache already (nvfp4_mla_append). With n = cu_tokens[s + 1] -
+ * cu_tokens[s] new tokens and length L = seq_lens[s] (after the step), token
+ * i of sequence s sees the keys at positions 0 .. L - n + i, and for head h
+ *   z_j = sm_scale * (q_latent[t,h,:] . latent_j + q_rope[t,h,:] . rope_j)
+ *   out[t,h,:] = sum_j softmax(z)_j * latent_j      (512 values)
+ *   lse[t,h]   = ln(sum_j exp(z_j))                  (natural log)
+ * with latent_j / rope_j as for sparse_mla_decode. Scores and the weighted
+ * sum use FP16 operands (rows are exact in FP16; weights are rounded) with
+ * FP32 accumulation, the sum of the weights is FP32. The partial states of
+ * sparse_mla_merge_states may come from here (out_fp32).
+ *
+ *   q_latent     device bf16 [num_q, num_heads, 512], 16-byte aligned
+ *   q_rope       device bf16 [num_q, num_heads, 64], 16-byte aligned
+ *                (operands are FP16: |q_latent|, and |q_rope| * rope_scale /
+ *                latent_scale, must stay below 65504; latent_scale counts
+ *                for FP8 rows)
+ *   cu_tokens    device int32 [num_seqs + 1], ascending, at most num_q; rows
+ *                of out and lse from cu_tokens[num_seqs] on are left as they
+ *                were
+ *   num_q        rows of q_latent; 0 is a no-op; num_q * num_heads < 2^31
+ *   num_heads    1..128
+ *   num_seqs     1..NVFP4_MLA_MAX_PLAN_SEQS
+ *   block_table  device int32 [num_seqs, max_blocks_per_seq];
+ *                max_blocks_per_seq * page_size <= 2^31 - 512
+ *   seq_lens     device int32 [num_seqs]
+ *   cache, num_blocks, block_stride_bytes, row_format, the scales, out,
+ *   out_fp32, lse  as for sparse_mla_decode
+ *   workspace    device, 16-byte aligned, >= dense_mla_chunk_workspace_size
+ *                bytes for the same sizes; contents need not be initialised.
+ *                Calls that can run at the same time need one each
+ *   invalid_count nullable device int32: += visible positions whose page id
+ *                is outside [0, num_blocks) (their keys are skipped; a token
+ *                that is left with none gets out = 0 and lse = -inf), and 1
+ *                for each malformed sequence (offsets that descend or leave
+ *                0..num_q, a length below its new tokens or beyond its
+ *                table), whose rows are left as they were
+ * Where a kernel's wait runs out (nvfp4_mla_set_wait_limit), all rows of the
+ * step are NaN. dense_mla_chunk_workspace_size returns SIZE_MAX for an
+ * invalid shape and 0 for num_q = 0. Results do not depend on what else runs,
+ * and are the same for the same arguments on the same kind of device.
+ */
+size_t dense_mla_chunk_workspace_size(int32_t num_q, int32_t num_heads, int32_t num_seqs);
+
+int32_t dense_mla_chunk(const void* q_latent, const void* q_rope, const int32_t* cu_tokens,
+                        int32_t num_q, int32_t num_heads, const int32_t* block_table,
+                        int32_t num_seqs, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                        int32_t page_size, const void* cache, int64_t num_blocks,
+                        int64_t block_stride_bytes, int32_t row_format, float sm_scale,
+                        float latent_scale, float rope_scale, void* out, int32_t out_fp32,
+                        float* lse, void* workspace, size_t workspace_bytes,
+                        int32_t* invalid_count, void* stream);
+
+/* ------------------------------------------------------------------------
  * Pages that several sequences share: parallel samples, beams, common
  * prompts. page_shares[p] (device int32 [num_blocks]) is the number of
  * sequences that hold page p beyond the first: 0 for a free page and for a

@@ -37,7 +37,8 @@ __all__ = [
     "sparse_mla_merge_states", "nvfp4_mla_staged_rows_per_q", "nvfp4_mla_stage_fp8",
     "staged_fp8_tables", "INDEX_DIM", "INDEX_ROW_BYTES", "nvfp4_mla_plan_step",
     "nvfp4_mla_truncate", "nvfp4_mla_index_append", "nvfp4_mla_index_read",
-    "sparse_mla_select_workspace_size", "sparse_mla_select", "nvfp4_mla_fork", "nvfp4_mla_release",
+    "sparse_mla_select_workspace_size", "sparse_mla_select",
+    "dense_mla_chunk_workspace_size", "dense_mla_chunk", "nvfp4_mla_fork", "nvfp4_mla_release",
     "nvfp4_mla_compact_workspace_size", "nvfp4_mla_compact", "nvfp4_mla_copy_pages", "library_path",
 ]
 
@@ -440,6 +441,59 @@ def sparse_mla_select(q_index: torch.Tensor, weights: torch.Tensor, q_seq: torch
         ws or 0, _stream(stream))
     _check(st, "sparse_mla_select")
     return topk_idx
+
+
+# ------------------------------------------------------- dense attention of a step
+def dense_mla_chunk_workspace_size(num_q: int, num_heads: int, num_seqs: int) -> int:
+    n = int(_lib().dense_mla_chunk_workspace_size(num_q, num_heads, num_seqs))
+    if n == (1 << 64) - 1:
+        raise ValueError("invalid chunk shape")
+    return n
+
+
+def dense_mla_chunk(q_latent: torch.Tensor, q_rope: torch.Tensor, cu_tokens: torch.Tensor,
+                    block_table: torch.Tensor, seq_lens: torch.Tensor, page_size: int,
+                    cache: torch.Tensor, num_blocks: int, block_stride_bytes: int,
+                    row_format: int, sm_scale: float, latent_scale: float = 1.0,
+                    rope_scale: float = 1.0, out: Optional[torch.Tensor] = None,
+                    out_fp32: bool = False, lse: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None,
+                    invalid_count: Optional[torch.Tensor] = None, stream=None):
+    """Causal attention of a step's new tokens (``cu_tokens`` int32 [num_seqs + 1], the tokens of
+    sequence s are its last ones of ``seq_lens``) to everything in the cache; returns
+    (out [num_q,H,512], lse [num_q,H]).
+
+    ``out`` / ``lse`` / ``workspace`` are allocated with torch when not given; rows behind the last
+    token are not written.
+    """
+    dev, i32, bf16 = torch.cuda.current_device(), torch.int32, torch.bfloat16
+    if q_latent.dim() != 3 or q_latent.shape[2] != LATENT_DIM:
+        raise ValueError("q_latent must be bf16 [num_q, num_heads, 512]")
+    num_q, H = q_latent.shape[0], q_latent.shape[1]
+    table, num_seqs, max_blocks = _table(block_table, dev)
+    out_type = torch.float32 if out_fp32 else bf16
+    if out is None:
+        out = _result((num_q, H, LATENT_DIM), out_type, dev, stream)
+    if lse is None:
+        lse = _result((num_q, H), torch.float32, dev, stream)
+    if workspace is None:
+        need = int(_lib().dense_mla_chunk_workspace_size(num_q, H, num_seqs))
+        if need < 1 << 63:  # an invalid shape is refused below
+            workspace = _scratch(need, torch.uint8, dev, stream)
+    st = _lib().dense_mla_chunk(
+        _arg(q_latent, "q_latent", bf16, 0, dev),
+        _arg(q_rope, "q_rope", bf16, num_q * H * ROPE_DIM, dev),
+        _arg(cu_tokens, "cu_tokens", i32, num_seqs + 1, dev), num_q, H, table, num_seqs, max_blocks,
+        _arg(seq_lens, "seq_lens", i32, num_seqs, dev), page_size,
+        _pool(cache, num_blocks, block_stride_bytes, page_size, dev,
+              ROW_BYTES.get(row_format, 0)), num_blocks, block_stride_bytes, row_format, sm_scale,
+        latent_scale, rope_scale, _arg(out, "out", out_type, num_q * H * LATENT_DIM, dev),
+        1 if out_fp32 else 0, _arg(lse, "lse", torch.float32, num_q * H, dev),
+        None if workspace is None else _arg(workspace, "workspace", workspace.dtype, 0, dev),
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _opt(invalid_count, "invalid_count", i32, 1, dev), _stream(stream))
+    _check(st, "dense_mla_chunk")
+    return out, lse
 
 
 # --------------------------------------------------------------- shared pages

@@ -39,6 +39,9 @@ SIGNATURES = {
     "sparse_mla_select_workspace_size": (SZ, [I32, I32, I32, I32, I32]),
     "sparse_mla_select": (I32, [P, P, P, P, I32, I32, P, I32, I32, I32, P, I64, I64, I32, I32, I32,
                                 I32, P, P, SZ, P]),
+    "dense_mla_chunk_workspace_size": (SZ, [I32, I32, I32]),
+    "dense_mla_chunk": (I32, [P, P, P, I32, I32, P, I32, I32, P, I32, P, I64, I64, I32, F32, F32, F32,
+                              P, I32, P, P, SZ, P, P]),
     "nvfp4_mla_fork": (I32, [P, P, P, I32, P, I32, P, I32, I32, P, I32, P, I32, P, P, P, P, P, P, P,
                              P, P]),
     "nvfp4_mla_release": (I32, [P, P, I32, P, I32, I32, P, I32, P, I32, P, P, P, P, P, P, P]),
