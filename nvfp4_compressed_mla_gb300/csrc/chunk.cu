@@ -44,10 +44,14 @@ namespace nvfp4_mla {
 namespace {
 
 constexpr int kPieceKeys = 64;                // keys of a P piece and of a V slot
-constexpr int kSoftWarps = 4;                 // softmax / rescale and output
-constexpr int kExpandWarp0 = 4, kExpandWarps = 8;
-constexpr int kIssueWarp = 12;
-constexpr int kChunkThreads = 13 * 32;
+constexpr int kSoftWarps = 8;                 // softmax / rescaling and output: two groups of four
+constexpr int kExpandWarp0 = 8, kExpandWarps = 8;
+constexpr int kIssueWarp = 16, kSendWarp = 17;
+constexpr int kChunkThreads = 20 * 32;        // the last four warps leave registers to the others
+// Registers of a thread of the softmax, the expanding and the last warps; as
+// many in all as at the launch.
+constexpr int kSoftRegs = 112, kExpandRegs = 112, kIssueRegs = 32;
+static_assert(2 * kSoftRegs + 2 * kExpandRegs + kIssueRegs == 5 * 96, "registers");
 constexpr int kMaxClusters = 80;              // of two CTAs; half as many of four
 constexpr int kPSlots = 4;                    // P pieces in flight
 constexpr uint32_t kPBytes = 128 * kPieceKeys * 2;
@@ -247,6 +251,13 @@ __device__ __forceinline__ void arrive_tx_release_cluster(uint32_t cluster_bar, 
                "r"(bytes)
                : "memory");
 }
+// The same where only copied bytes are to be seen behind the barrier.
+__device__ __forceinline__ void arrive_tx_relaxed_cluster(uint32_t cluster_bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::
+                   "r"(cluster_bar),
+               "r"(bytes)
+               : "memory");
+}
 // shared (this CTA) -> shared (another CTA of the cluster), counted on that CTA's mbarrier
 __device__ __forceinline__ void bulk_s2s(uint32_t dst_cluster, uint32_t src, uint32_t bytes,
                                          uint32_t bar_cluster) {
@@ -256,19 +267,13 @@ __device__ __forceinline__ void bulk_s2s(uint32_t dst_cluster, uint32_t src, uin
       "r"(src), "r"(bytes), "r"(bar_cluster)
       : "memory");
 }
-__device__ __forceinline__ void st_cluster_u8(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
-// The AND of `v` over the 128 threads of warps 0-3 (barrier 1).
-__device__ __forceinline__ bool group_and(bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\n"
-      "bar.red.and.pred q, 1, 128, p;\nselp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"(v ? 1u : 0u)
-      : "memory");
-  return r != 0;
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 template <int kPair>
 __device__ __forceinline__ void alloc_tmem(uint32_t dst_smem) {
@@ -348,7 +353,7 @@ __device__ __forceinline__ uint32_t swizzled(uint32_t row, uint32_t col) {
 template <bool kCluster = false>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t abort_addr,
                                           long long limit) {
-  return __all_sync(0xffffffffu, wait_bar<kCluster>(bar, parity, abort_addr, limit));
+  return __all_sync(0xffffffffu, wait_bar_hot<kCluster>(bar, parity, abort_addr, limit));
 }
 __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
   const long long t0 = clock64();
@@ -409,30 +414,41 @@ struct ChunkLayout {
   static constexpr uint32_t kK = 0;                        // two key tiles
   static constexpr uint32_t kQRope = 2 * kKTileBytes;
   static constexpr uint32_t kStaged = kQRope + 16384;      // P pieces on their way out
-  static constexpr uint32_t kEndScore = kStaged + kPSlots * kPBytes;
+  static constexpr uint32_t kRef = kStaged + kPSlots * kPBytes;  // references of the rows, two pieces
+  static constexpr uint32_t kSums = kRef + 1024;                 // sums of weights, two results
+  static constexpr uint32_t kEndScore = kSums + 1024;
   // output CTA
   static constexpr uint32_t kVSlot = 65536 / kPair;        // 64 keys x 512 / kPair dimensions
   static constexpr int kVSlots = 2 * kPair;
   static constexpr uint32_t kV = 0;
   static constexpr uint32_t kP = kV + kVSlots * kVSlot;
-  static constexpr uint32_t kNote = kP + kPSlots * kPBytes;  // what comes with a P piece:
-  static constexpr uint32_t kFactor = 0, kFinal = 512, kFlag = 1024;  // per row, per row, per warp
-  static constexpr uint32_t kNoteBytes = 1040;
-  static constexpr uint32_t kEndOut = kNote + kPSlots * kNoteBytes;
+  static constexpr uint32_t kFactor = kP + kPSlots * kPBytes;  // rescale factor of each row, a P slot
+  static constexpr uint32_t kTag = kFactor + kPSlots * 512;    // per warp and P slot: 1 + piece to rescale at
+  static constexpr uint32_t kFinal = kTag + kPSlots * 16;      // output factor of each row, a result
+  static constexpr uint32_t kFinals = 8;  // more results than there are P pieces in flight
+  static constexpr uint32_t kEndOut = kFinal + kFinals * 512;
   static constexpr uint32_t kCtl = kEndScore > kEndOut ? kEndScore : kEndOut;
-  static constexpr uint32_t kBytes = kCtl + 320;
+  static constexpr uint32_t kCtlBytes = 1024;
+  static constexpr uint32_t kBytes = kCtl + kCtlBytes;
   // score CTA's tensor memory: Q's latent part in columns 0 .. 255, then S
   static constexpr uint32_t kSCol = 256;
+  static constexpr uint32_t kSBufs = 4 / kPair;
   static_assert(kBytes <= kMaxSharedBytes && kCtl % 16 == 0, "shared memory");
-  static_assert(kSCol + 2 * kPieceKeys * kPair <= kTmemCols, "tensor memory");
+  static_assert(kSCol + kSBufs * kPieceKeys * kPair <= kTmemCols, "tensor memory");
 };
 struct ChunkCtl {  // barriers and words, at the same offsets in every CTA of the cluster
-  static constexpr uint32_t kKFull = 0, kSFull = 16, kSEmpty = 32, kQFull = 48, kPFull = 56,
-                            kPReady = 88, kVFull = 120, kPvDone = 152, kTmem = 184, kAbort = 188,
-                            kSent = 192, kScored = 196, kSummed = 200, kValid = 208;
-  static constexpr uint32_t kValidTiles = 4;  // 16 bytes each: bits of the keys that exist
+  static constexpr uint32_t kKFull = 0, kSFull = 16, kSEmpty = 48, kQFull = 80, kPFull = 88,
+                            kPReady = 136, kVFull = 184, kPvDone = 216, kTask = 264, kTaskDone = 272,
+                            kStaged = 280, kRefDone = 328, kSumDone = 392, kTmem = 456, kAbort = 460,
+                            kSent = 464, kScored = 468, kSummed = 472, kTaskWord = 476, kNoted = 480,
+                            kMissing = 512;
+  // a word for each of the expanding warps of a tile, 8 tiles: (1 + tile) << 8 and
+  // the bits of its keys that exist, where some page does not resolve
+  static constexpr uint32_t kMissingTiles = 8, kMissingBytes = 64;
 };
-static_assert(ChunkCtl::kValid + 16 * ChunkCtl::kValidTiles <= 320, "control block");
+static_assert(kPSlots <= 6 && ChunkCtl::kNoted + 4 * kPSlots <= ChunkCtl::kMissing &&
+                  ChunkCtl::kMissing + 512 == ChunkLayout<1>::kCtlBytes,
+              "control block");
 
 // ------------------------------------------------------------------ expansion
 // Warp w of the eight expands keys 8 w .. 8 w + 7 of each 64. kItems 16-byte
@@ -450,65 +466,124 @@ struct RowItems {
   uint4 rope;
 };
 
-// Row addresses of the eight keys from `key` on (lane j < 8 has key + j): the
-// page of a table entry that was loaded before, or -1.
-struct RowEntry {
-  int32_t page;    // -1: no such key
-  int32_t in_page;
-};
-__device__ __forceinline__ RowEntry load_entry(const ChunkParams& p, int32_t seq, int32_t key,
-                                               int32_t len, int lane) {
-  RowEntry e = {-1, 0};
-  const int32_t k = key + lane;
-  if (lane < 8 && k < len) {
-    const int32_t b = p.page.block(k);
-    e.in_page = k - b * p.page.size;
-    e.page = __ldg(p.block_table + static_cast<int64_t>(seq) * p.max_blocks + b);
+// Where a lane's first latent item lies from the warp's first key on, in bytes.
+// An output CTA of a pair (kHalves) expands dimensions 128 part .. + 127 of each
+// half of the 512.
+template <int kFmt, bool kHalves>
+__device__ __forceinline__ uint32_t first_item(int lane, int part) {
+  if constexpr (kFmt == NVFP4_MLA_ROW_NVFP4_352) {
+    const uint32_t c = (lane & 1) + 2 * (lane >> 3);  // 32 dimensions each
+    return ((lane >> 1) & 3) * kNvfp4Row + (kHalves ? 128 * (c >> 2) + 64 * part + 16 * (c & 3) : 16 * c);
+  } else {
+    return (lane >> 2) * kFp8Row + (kHalves ? 128 * part : 0) + 16 * (lane & 3);
   }
-  return e;
 }
-__device__ __forceinline__ int64_t entry_offset(const ChunkParams& p, const RowEntry& e,
-                                                int32_t row_bytes) {
-  return e.page >= 0 && e.page < p.num_blocks
-             ? e.page * p.block_stride + static_cast<int64_t>(e.in_page) * row_bytes
-             : -1;
+// The distance from there to item i, and (NVFP4) the distance of its two scales.
+template <int kFmt, bool kHalves>
+__device__ __forceinline__ constexpr uint32_t item_step(int i) {
+  if (kFmt == NVFP4_MLA_ROW_NVFP4_352) return (i & 1) * 4 * kNvfp4Row + (i >> 1) * 128;
+  return kHalves ? 256 * (i >> 1) + 64 * (i & 1) : 64 * i;
+}
+__device__ __forceinline__ constexpr uint32_t scale_step(int i) {
+  return (i & 1) * 4 * kNvfp4Row + (i >> 1) * 16;
+}
+__device__ __forceinline__ uint32_t first_scale(uint32_t item) {  // of the item at this distance
+  const uint32_t key = item / kNvfp4Row;
+  return key * kNvfp4Row + kScaleOff + (item - key * kNvfp4Row) / 8;
+}
+template <int kFmt>
+__device__ __forceinline__ uint32_t rope_item(int lane) {
+  return kFmt == NVFP4_MLA_ROW_NVFP4_352 ? (lane >> 2) * kNvfp4Row + kRopeOff + 16 * (lane & 3)
+                                         : (lane >> 2) * kFp8Row + kLatent + 16 * (lane & 3);
 }
 
-// Where a lane's latent items lie: `half_step` is the distance in a row's codes
-// (bytes) between the two halves of 128 dimensions that an output CTA of a pair
-// expands, 0 where all 512 are expanded.
-template <int kFmt, int kLatItems, bool kRopeToo, bool kHalves>
-__device__ __forceinline__ void load_items(const ChunkParams& p, int64_t mine, int lane, int part,
-                                           RowItems<kFmt, kLatItems, kRopeToo>& r) {
-  using R = RowItems<kFmt, kLatItems, kRopeToo>;
-  const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-  if constexpr (R::kNv) {
-    const int ka = (lane >> 1) & 3;
-    const int64_t at[2] = {__shfl_sync(0xffffffffu, mine, ka), __shfl_sync(0xffffffffu, mine, ka + 4)};
-#pragma unroll
-    for (int i = 0; i < kLatItems; ++i) {
-      const int64_t off = at[i & 1];
-      const int c = (lane & 1) + 2 * (lane >> 3) + 8 * (i >> 1);
-      // dimensions 32 c .. + 31 of the row, or of this CTA's two halves
-      const int code = kHalves ? 128 * (c >> 2) + 64 * part + 16 * (c & 3) : 16 * c;
-      r.lat[i] = off >= 0 ? ld_row_v4(p.cache + off + code) : z;
-      r.scale[i] = off >= 0 ? ld_row_u16(p.cache + off + kScaleOff + code / 8) : 0u;
-    }
-    if constexpr (kRopeToo) {
-      const int64_t off = __shfl_sync(0xffffffffu, mine, lane >> 2);
-      r.rope = off >= 0 ? ld_row_v4(p.cache + off + kRopeOff + 16 * (lane & 3)) : z;
-    }
-  } else {
-    const int64_t off = __shfl_sync(0xffffffffu, mine, lane >> 2);
-#pragma unroll
-    for (int i = 0; i < kLatItems; ++i) {
-      const int c = 4 * i + (lane & 3);  // dimensions 16 c .. + 15
-      const int byte = kHalves ? 256 * (c >> 3) + 128 * part + 16 * (c & 7) : 16 * c;
-      r.lat[i] = off >= 0 ? ld_row_v4(p.cache + off + byte) : z;
-    }
-    if constexpr (kRopeToo) r.rope = off >= 0 ? ld_row_v4(p.cache + off + kLatent + 16 * (lane & 3)) : z;
+// The keys of a warp at a time: where the first one lies, or all eight.
+// kRuns (pages of a multiple of 64 rows): one page holds them, and a lane's items
+// lie at fixed distances; rows of the page behind the length are read as they
+// are (no row sees them, and as values they are numbers). Otherwise lane j has
+// the address of key j.
+template <int kFmt, bool kRuns, bool kHalves>
+struct KeyRows {
+  static constexpr int kRowBytes = kFmt == NVFP4_MLA_ROW_NVFP4_352 ? kNvfp4Row : kFp8Row;
+  uint32_t lat0, scale0, rope0;  // of the lane, from the warp's first key on
+  int part;
+  int32_t page, in_page;  // of the next keys: the entry is on its way
+  bool some;              // they are below the length
+
+  __device__ KeyRows(int lane, int part_) : part(part_) {
+    lat0 = first_item<kFmt, kHalves>(lane, part);
+    scale0 = first_scale(lat0);
+    rope0 = rope_item<kFmt>(lane);
   }
-}
+  __device__ __forceinline__ void none() {
+    page = -1;
+    some = false;
+  }
+  // the entry of keys first_key + 8 w .. + 7 of 64, on its way
+  __device__ __forceinline__ void next(const ChunkParams& p, int32_t seq, int32_t first_key, int w, int32_t len,
+                                       int lane) {
+    const int32_t key = first_key + (kRuns ? 0 : 8 * w + (lane & 7));
+    some = key < len && (kRuns || lane < 8);
+    page = -1;
+    if (some) {
+      const int32_t b = p.page.block(key);
+      in_page = key - b * p.page.size + (kRuns ? 8 * w : 0);
+      page = __ldg(p.block_table + static_cast<int64_t>(seq) * p.max_blocks + b);
+    }
+  }
+  // loads them; `exist` and `missing` are bits of the eight keys
+  template <int kLatItems, bool kRopeToo>
+  __device__ __forceinline__ void load(const ChunkParams& p, int lane, RowItems<kFmt, kLatItems, kRopeToo>& r,
+                                       uint32_t& exist, uint32_t& missing) const {
+    using R = RowItems<kFmt, kLatItems, kRopeToo>;
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    const bool ok = page >= 0 && page < p.num_blocks;
+    const int64_t mine = page * p.block_stride + static_cast<int64_t>(in_page) * kRowBytes;
+    if constexpr (kRuns) {
+      exist = ok ? 0xffu : 0u;
+      missing = some && !ok ? 0xffu : 0u;
+      const uint8_t* lat = p.cache + mine + lat0;
+      if (ok) {
+#pragma unroll
+        for (int i = 0; i < kLatItems; ++i) r.lat[i] = ld_row_v4(lat + item_step<kFmt, kHalves>(i));
+        if constexpr (R::kNv) {
+          const uint8_t* sc = p.cache + mine + scale0;
+#pragma unroll
+          for (int i = 0; i < kLatItems; ++i) r.scale[i] = ld_row_u16(sc + scale_step(i));
+        }
+        if constexpr (kRopeToo) r.rope = ld_row_v4(p.cache + mine + rope0);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kLatItems; ++i) r.lat[i] = z;
+        if constexpr (R::kNv) {
+#pragma unroll
+          for (int i = 0; i < kLatItems; ++i) r.scale[i] = 0u;
+        }
+        if constexpr (kRopeToo) r.rope = z;
+      }
+    } else {
+      exist = __ballot_sync(0xffffffffu, ok);
+      missing = __ballot_sync(0xffffffffu, some && !ok);
+      const int64_t off = ok ? mine : -1;
+      const uint32_t key0 = lat0 / kRowBytes;  // of the lane's items; the same for the scales
+      const uint32_t in_row = lat0 - key0 * kRowBytes, scale_in_row = scale0 - key0 * kRowBytes;
+      const int64_t at[2] = {__shfl_sync(0xffffffffu, off, key0),
+                             R::kNv ? __shfl_sync(0xffffffffu, off, (key0 + 4) & 31) : 0};
+#pragma unroll
+      for (int i = 0; i < kLatItems; ++i) {
+        const int64_t a = at[R::kNv ? i & 1 : 0];
+        const uint32_t step = item_step<kFmt, kHalves>(i) - (R::kNv ? (i & 1) * 4 * kNvfp4Row : 0);
+        r.lat[i] = a >= 0 ? ld_row_v4(p.cache + a + in_row + step) : z;
+        if constexpr (R::kNv)
+          r.scale[i] = a >= 0 ? ld_row_u16(p.cache + a + scale_in_row + (scale_step(i) - (i & 1) * 4 * kNvfp4Row)) : 0u;
+      }
+      if constexpr (kRopeToo) {
+        const int64_t a = __shfl_sync(0xffffffffu, off, lane >> 2);
+        r.rope = a >= 0 ? ld_row_v4(p.cache + a + (rope0 - (lane >> 2) * kRowBytes)) : z;
+      }
+    }
+  }
+};
 
 __device__ __forceinline__ void store_e4m3x16(uint4 v, uint32_t block, uint32_t key, uint32_t col,
                                               bool numbers) {
@@ -587,11 +662,10 @@ struct KeyWalk {
 };
 
 // ------------------------------------------------------------------ kernel
-template <int kFmt, int kPair>
+template <int kFmt, int kPair, bool kRuns>
 __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const ChunkParams p) {
   using L = ChunkLayout<kPair>;
   using C = ChunkCtl;
-  constexpr int kRowBytes = kFmt == NVFP4_MLA_ROW_NVFP4_352 ? kNvfp4Row : kFp8Row;
   constexpr bool kNv = kFmt == NVFP4_MLA_ROW_NVFP4_352;
   constexpr int kTileKeys = kPieceKeys * kPair;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -606,27 +680,42 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const ChunkPara
   const long long lim = p.wait_cycles;
   const uint32_t abort_addr = ctl + C::kAbort;
   auto bar = [&](uint32_t off, uint32_t i) { return ctl + off + 8u * i; };
-  auto leader_bar = [&](uint32_t off, uint32_t i) { return map_rank(bar(off, i), leader); };
+  // an arrival at the leader of this CTA's pair, behind this thread's writes
+  const uint32_t leader_ctl = map_rank(ctl, leader);
+  auto tell_leader = [&](uint32_t off, uint32_t i) {
+    if constexpr (kPair == 1) mbar_arrive(bar(off, i));
+    else mbar_arrive_cluster(leader_ctl + off + 8u * i);
+  };
 
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(C::kKFull, i), kExpandWarps * kPair);
+    for (int i = 0; i < 2; ++i) mbar_init(bar(C::kKFull, i), kExpandWarps * kPair);
+    for (uint32_t i = 0; i < L::kSBufs; ++i) {
       mbar_init(bar(C::kSFull, i), 1);
-      mbar_init(bar(C::kSEmpty, i), kSoftWarps * kPair);
+      mbar_init(bar(C::kSEmpty, i), 4 * kPair * kPair);  // the warps that read a tile, of each CTA
     }
     mbar_init(bar(C::kQFull, 0), kSoftWarps * kPair);
     for (int i = 0; i < kPSlots; ++i) {
       mbar_init(bar(C::kPFull, i), 1);
-      mbar_init(bar(C::kPReady, i), kSoftWarps * kPair);
-      mbar_init(bar(C::kVFull, i), kExpandWarps * kPair);
+      mbar_init(bar(C::kPReady, i), 1);
       mbar_init(bar(C::kPvDone, i), 1);
+      mbar_init(bar(C::kStaged, i), 4);
     }
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(bar(C::kRefDone, i), 1);
+      mbar_init(bar(C::kSumDone, i), 1);
+    }
+    for (int i = 0; i < L::kVSlots; ++i) mbar_init(bar(C::kVFull, i), kExpandWarps * kPair);
+    mbar_init(bar(C::kTask, 0), 1);
+    mbar_init(bar(C::kTaskDone, 0), kSoftWarps);
     st_shared_u32(ctl + C::kSent, 0u);
     st_shared_u32(ctl + C::kScored, 0u);
     st_shared_u32(ctl + C::kSummed, 0u);
+    for (int i = 0; i < kPSlots; ++i) st_shared_u32(ctl + C::kNoted + 4 * i, 0u);
     st_shared_u32(abort_addr, (sbase & 1023u) != 0 ? 1u : 0u);
     fence_mbar_init();
   }
+  if (tid < 128) st_shared_u32(ctl + C::kMissing + 4 * tid, 0u);
+  if (!scoring && tid < 4 * kPSlots) st_shared_u32(sbase + L::kTag + 4 * tid, 0u);
   if (warp == kIssueWarp) alloc_tmem<kPair>(ctl + C::kTmem);
   tc_fence_before();
   __syncthreads();
@@ -637,399 +726,505 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const ChunkPara
   cudaGridDependencySynchronize();  // the plan is there
   cudaTriggerProgrammaticLaunchCompletion();
 
-  if (warp >= kExpandWarp0 && warp < kIssueWarp && scoring) {
-    // ------------------------------------------------ keys of a score CTA
-    // Tile i goes into slot i % 2, once the MMAs of tile i - 2 are done. Table
-    // entries are loaded kAhead + 1 tiles ahead and rows kAhead.
-    constexpr int kLat = kNv ? 4 : 8, kAhead = kNv ? 2 : 1;
-    using R = RowItems<kFmt, kLat, true>;
-    const int w = warp - kExpandWarp0;
-    KeyWalk<kPair> walk(p, cluster, 1);
-    auto entry = [&]() -> RowEntry {
-      if (!walk.live) return {-1, 0};
-      const int32_t key = walk.at * kTileKeys + kPieceKeys * static_cast<int32_t>(part) + 8 * w;
-      const RowEntry e = load_entry(p, walk.pieces.seq, key, walk.pieces.len, lane);
-      walk.step();
-      return e;
-    };
-    R items[kAhead + 1];
-    uint32_t valid[kAhead + 1];
-    bool live[kAhead + 2];
-    live[0] = walk.live;
-    RowEntry e = entry();
-    auto fetch = [&](R& r, uint32_t& v) {  // the rows of entry e, and the next entry
-      const int64_t off = entry_offset(p, e, kRowBytes);
-      e = entry();
-      v = __ballot_sync(0xffffffffu, off >= 0) & 0xFFu;
-      load_items<kFmt, kLat, true, false>(p, off, lane, 0, r);
-    };
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      live[k + 1] = walk.live;
-      fetch(items[k], valid[k]);
-    }
-    for (uint32_t i = 0; live[0]; ++i) {
-      live[kAhead + 1] = walk.live;
-      fetch(items[kAhead], valid[kAhead]);
-      if (!warp_wait(bar(C::kSFull, i & 1), ((i >> 1) & 1) ^ 1, abort_addr, lim)) break;
-      store_items<kFmt, kLat, true, false>(items[0], sbase + L::kK + (i & 1) * kKTileBytes, w, lane);
-      fence_proxy_async_cta();
-      // the softmax of both CTAs reads which keys exist
-      const uint32_t at = ctl + C::kValid + 16 * (i % C::kValidTiles) + 8 * part + w;
-      if (lane < kPair) st_cluster_u8(map_rank(at, lane), valid[0]);
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(leader_bar(C::kKFull, i & 1));
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        items[k] = items[k + 1];
-        valid[k] = valid[k + 1];
-      }
-#pragma unroll
-      for (int k = 0; k <= kAhead; ++k) live[k] = live[k + 1];
-    }
-  } else if (warp >= kExpandWarp0 && warp < kIssueWarp) {
-    // ------------------------------------------------ values of an output CTA
-    // Piece u goes into slot u % kVSlots, once the MMAs of piece u - kVSlots are done.
-    constexpr int kLat = (kNv ? 4 : 8) / kPair, kAhead = 2;
-    using R = RowItems<kFmt, kLat, false>;
-    const int w = warp - kExpandWarp0;
-    KeyWalk<kPair> walk(p, cluster, kPair);
-    auto entry = [&]() -> RowEntry {
-      if (!walk.live) return {-1, 0};
-      const RowEntry e = load_entry(p, walk.pieces.seq, walk.at * kPieceKeys + 8 * w, walk.pieces.len, lane);
-      walk.step();
-      return e;
-    };
-    R items[kAhead + 1];
-    bool live[kAhead + 2];
-    live[0] = walk.live;
-    RowEntry e = entry();
-    auto fetch = [&](R& r) {
-      const int64_t off = entry_offset(p, e, kRowBytes);
-      e = entry();
-      load_items<kFmt, kLat, false, kPair == 2>(p, off, lane, static_cast<int>(part), r);
-    };
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      live[k + 1] = walk.live;
-      fetch(items[k]);
-    }
-    for (uint32_t u = 0; live[0]; ++u) {
-      live[kAhead + 1] = walk.live;
-      fetch(items[kAhead]);
-      const uint32_t vs = u % L::kVSlots;
-      if (u >= L::kVSlots) {
-        const uint32_t v = u - L::kVSlots;
-        if (!warp_wait<true>(bar(C::kPvDone, v % kPSlots), (v / kPSlots) & 1, abort_addr, lim)) break;
-      }
-      store_items<kFmt, kLat, false, true>(items[0], sbase + L::kV + vs * L::kVSlot, w, lane);
-      fence_proxy_async_cta();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(leader_bar(C::kVFull, vs));
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) items[k] = items[k + 1];
-#pragma unroll
-      for (int k = 0; k <= kAhead; ++k) live[k] = live[k + 1];
-    }
-  } else if (warp == kIssueWarp && scoring) {
-    // ------------------------------------------------ S = Q K^T (one thread of the leader)
-    if (lane == 0 && rank == leader) {
-      constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(kTileKeys >> 3) << 17) |
-                                  (static_cast<uint32_t>(128 * kPair >> 4) << 24);
-      const uint64_t qr = operand_desc(sbase + L::kQRope);
-      uint32_t i = 0;
-      bool run = true;
-      Pieces<kPair> pieces(p, cluster);
-      for (uint32_t item = 0; run && pieces.next(); ++item) {
-        if (!wait_bar_hot<true>(bar(C::kQFull, 0), item & 1, abort_addr, lim)) break;
-        for (int32_t kt = pieces.begin; kt < pieces.end; ++kt, ++i) {
-          const uint32_t b = i & 1, ph = (i >> 1) & 1;
-          if (!wait_bar_hot<true>(bar(C::kSEmpty, b), ph ^ 1, abort_addr, lim) ||
-              !wait_bar_hot<true>(bar(C::kKFull, b), ph, abort_addr, lim)) {
-            run = false;
-            break;
+  // All warps of a warpgroup change their registers together.
+  if (warp >= kIssueWarp) {
+    fewer_registers<kIssueRegs>();
+    if (warp == kSendWarp && scoring) {
+      // ------------------------------------------------ P pieces to the output CTA
+      if (lane == 0) {
+        const uint32_t out_rank = kPair + part;
+        const uint32_t out_p = map_rank(sbase + L::kP, out_rank), out_full = map_rank(bar(C::kPFull, 0), out_rank);
+        uint32_t u = 0;
+        bool run = true;
+        Pieces<kPair> pieces(p, cluster);
+        while (run && pieces.next()) {
+          const uint32_t n = static_cast<uint32_t>(pieces.end - pieces.begin) * kPair;
+          for (uint32_t x = 0; x < n; ++x, ++u) {
+            const uint32_t ps = u % kPSlots;
+            run = wait_bar_hot(bar(C::kStaged, ps), (u / kPSlots) & 1, abort_addr, lim);
+            if (!run) break;
+            const uint32_t full = out_full + 8u * ps;
+            if (ld_shared_u32(ctl + C::kNoted + 4 * ps) == u + 1) arrive_tx_release_cluster(full, kPBytes);
+            else arrive_tx_relaxed_cluster(full, kPBytes);
+            bulk_s2s(out_p + ps * kPBytes, sbase + L::kStaged + ps * kPBytes, kPBytes, full);
           }
-          tc_fence_after();
-          const uint32_t d = L::kSCol + kTileKeys * b;
-          const uint64_t kd = operand_desc(sbase + L::kK + b * kKTileBytes);
-#pragma unroll
-          for (int x = 0; x < 32; ++x)
-            pair_mma_ts<kPair>(d, 8u * x, kd + (x >> 2) * (kKBlock >> 4) + 2 * (x & 3), kIdesc,
-                               x != 0 ? 1u : 0u);
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            pair_mma_ss<kPair>(d, qr + 2 * x, kd + 8 * (kKBlock >> 4) + 2 * x, kIdesc, 1u);
-          commit_to<kPair>(bar(C::kSFull, b), static_cast<uint16_t>((1u << kPair) - 1));
         }
+        st_cluster_u32(map_rank(ctl + C::kSent, out_rank), u);
       }
-      for (uint32_t r = 0; r < kPair; ++r) st_cluster_u32(map_rank(ctl + C::kScored, r), i);
-    }
-  } else if (warp == kIssueWarp) {
-    // ------------------------------------------------ O += P V (one thread of the leader)
-    if (lane == 0 && rank == leader) {
-      constexpr uint32_t kIdesc = (1u << 4) | (1u << 16) | ((256u >> 3) << 17) |
-                                  (static_cast<uint32_t>(128 * kPair >> 4) << 24);
-      uint32_t u = 0;
-      bool run = true;
-      Pieces<kPair> pieces(p, cluster);
-      while (run && pieces.next()) {
-        const uint32_t n = static_cast<uint32_t>(pieces.end - pieces.begin) * kPair;
-        for (uint32_t x = 0; x < n; ++x, ++u) {
-          const uint32_t ps = u % kPSlots, vs = u % L::kVSlots;
-          if (!wait_bar_hot<true>(bar(C::kPReady, ps), (u / kPSlots) & 1, abort_addr, lim) ||
-              !wait_bar_hot<true>(bar(C::kVFull, vs), (u / L::kVSlots) & 1, abort_addr, lim)) {
-            run = false;
-            break;
+    } else if (warp == kIssueWarp && scoring) {
+      // ------------------------------------------------ S = Q K^T (one thread of the leader)
+      if (lane == 0 && rank == leader) {
+        constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(kTileKeys >> 3) << 17) |
+                                    (static_cast<uint32_t>(128 * kPair >> 4) << 24);
+        const uint64_t qr = operand_desc(sbase + L::kQRope);
+        uint32_t i = 0;
+        bool run = true;
+        Pieces<kPair> pieces(p, cluster);
+        for (uint32_t item = 0; run && pieces.next(); ++item) {
+          if (!wait_bar_hot<true>(bar(C::kQFull, 0), item & 1, abort_addr, lim)) break;
+          for (int32_t kt = pieces.begin; kt < pieces.end; ++kt, ++i) {
+            const uint32_t b = i % L::kSBufs, slot = i & 1;
+            if (!wait_bar_hot<true>(bar(C::kSEmpty, b), ((i / L::kSBufs) & 1) ^ 1, abort_addr, lim) ||
+                !wait_bar_hot<true>(bar(C::kKFull, slot), (i >> 1) & 1, abort_addr, lim)) {
+              run = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t d = L::kSCol + kTileKeys * b;
+            const uint64_t kd = operand_desc(sbase + L::kK + slot * kKTileBytes);
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              pair_mma_ts<kPair>(d, 8u * x, kd + (x >> 2) * (kKBlock >> 4) + 2 * (x & 3), kIdesc,
+                                 x != 0 ? 1u : 0u);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              pair_mma_ss<kPair>(d, qr + 2 * x, kd + 8 * (kKBlock >> 4) + 2 * x, kIdesc, 1u);
+            commit_to<kPair>(bar(C::kSFull, b), static_cast<uint16_t>((1u << kPair) - 1));
           }
-          tc_fence_after();
-          const uint64_t pd = operand_desc(sbase + L::kP + ps * kPBytes);
-          const uint64_t vd = operand_desc(sbase + L::kV + vs * L::kVSlot, kKBlock);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-            for (int nh = 0; nh < 2; ++nh)
-              pair_mma_ss<kPair>(256u * nh, pd + 2 * kk,
-                                 vd + nh * (L::kVSlot >> 5) + kk * (2048 >> 4), kIdesc,
-                                 (x | kk) != 0 ? 1u : 0u);
-          commit_to<kPair>(bar(C::kPvDone, ps), static_cast<uint16_t>((1u << (2 * kPair)) - 1));
         }
+        for (uint32_t r = 0; r < kPair; ++r) st_cluster_u32(map_rank(ctl + C::kScored, r), i);
       }
-      for (uint32_t r = 0; r < 2 * kPair; ++r) st_cluster_u32(map_rank(ctl + C::kSummed, r), u);
-    }
-  } else if (scoring) {
-    // ------------------------------------------------ Q, softmax (thread = row)
-    const uint32_t lane_base = static_cast<uint32_t>(32 * warp) << 16;
-    const int row = 128 * static_cast<int>(part) + tid;  // of the row tile
-    const uint32_t out_rank = kPair + part;
-    const uint32_t note0 = map_rank(sbase + L::kNote, out_rank);
-    const float c = p.score_scale;
-    const uint64_t c2 = f32x2(c, c);
-    uint32_t i = 0, u = 0;
-    bool ok = true;
-    Pieces<kPair> pieces(p, cluster);
-    while (ok && pieces.next()) {
-      {  // the MMAs that read the Q before are done: this warp has waited for their S
-        const bool mine = row < pieces.rows;
-        const uint4* ql = reinterpret_cast<const uint4*>(p.q_lat + (pieces.row0 + row) * kLatent);
-        const uint4* qr = reinterpret_cast<const uint4*>(p.q_rope + (pieces.row0 + row) * kRope);
-        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll 2
-        for (int x = 0; x < 8; ++x) {
-          uint4 v[8];
-#pragma unroll
-          for (int y = 0; y < 8; ++y) v[y] = mine ? __ldg(ql + 8 * x + y) : z;
-          uint32_t h[32];
-#pragma unroll
-          for (int y = 0; y < 8; ++y) {
-            const uint4 f = to_f16x8(v[y], p.lat_mult);
-            h[4 * y] = f.x, h[4 * y + 1] = f.y, h[4 * y + 2] = f.z, h[4 * y + 3] = f.w;
-          }
-          tmem_st32(tmem + lane_base + 32u * x, h);
-        }
-#pragma unroll
-        for (int y = 0; y < 8; ++y) {
-          const uint4 f = to_f16x8(mine ? __ldg(qr + y) : z, p.rope_mult);
-          st_shared_v4(sbase + L::kQRope + swizzled(tid, y), f.x, f.y, f.z, f.w);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        fence_proxy_async_cta();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(leader_bar(C::kQFull, 0));
-      }
-      // keys that the row sees
-      const int32_t sees = pieces.base + 1 +
-                           static_cast<int32_t>((pieces.row0 - pieces.first_row + min(row, pieces.rows - 1)) /
-                                                p.num_heads);
-      float m = -INFINITY, l = 0.f;
-      for (int32_t kt = pieces.begin; kt < pieces.end && ok; ++kt, ++i) {
-        const uint32_t b = i & 1;
-        const bool last = kt + 1 == pieces.end;
-        ok = warp_wait(bar(C::kSFull, b), (i >> 1) & 1, abort_addr, lim);
-        if (ok) tc_fence_after();
-        const uint32_t s_addr = tmem + lane_base + L::kSCol + kTileKeys * b;
-        const uint4 vw = ld_shared_v4(ctl + C::kValid + 16 * (i % C::kValidTiles));
-        const int32_t room = sees - kt * kTileKeys;  // of this tile's keys
-        const bool all = __all_sync(0xffffffffu, room >= kTileKeys) &&
-                         (kPair == 1 ? (vw.x & vw.y) : (vw.x & vw.y & vw.z & vw.w)) == 0xffffffffu;
-        const uint32_t words[4] = {vw.x, vw.y, vw.z, vw.w};
-        // the bits of word x that the row sees
-        auto seen = [&](int x) -> uint32_t {
-          const int32_t n = room - 32 * x;
-          return n >= 32 ? words[x] : n <= 0 ? 0u : words[x] & ((1u << n) - 1u);
+    } else if (warp == kIssueWarp) {
+      // ------------------------------------------------ O += P V (one thread of the leader)
+      // A thread of each output CTA follows the P pieces that land there. It has O
+      // rescaled where a piece comes with factors and written behind the last piece
+      // of a row tile (tasks of warps 0-3), then the leader's issues the MMAs and the
+      // other one tells it that its piece is there.
+      if (lane == 0) {
+        constexpr uint32_t kIdesc = (1u << 4) | (1u << 16) | ((256u >> 3) << 17) |
+                                    (static_cast<uint32_t>(128 * kPair >> 4) << 24);
+        uint32_t u = 0, tasks = 0;
+        bool run = true;
+        auto post = [&](uint32_t word) {
+          st_shared_u32(ctl + C::kTaskWord, word);
+          mbar_arrive(bar(C::kTask, 0));
+          ++tasks;
         };
-        float mx = -INFINITY;
-        if (ok) {
+        auto task_done = [&]() { return wait_bar_hot(bar(C::kTaskDone, 0), (tasks - 1) & 1, abort_addr, lim); };
+        Pieces<kPair> pieces(p, cluster);
+        while (run && pieces.next()) {
+          const uint32_t n = static_cast<uint32_t>(pieces.end - pieces.begin) * kPair;
+          if (tasks > 0 && !task_done()) break;  // O before has been read
+          for (uint32_t x = 0; x < n; ++x, ++u) {
+            const uint32_t ps = u % kPSlots, vs = u % L::kVSlots;
+            run = wait_bar_hot<true>(bar(C::kPFull, ps), (u / kPSlots) & 1, abort_addr, lim);
+            if (!run) break;
+            const uint4 tag = ld_shared_v4(sbase + L::kTag + 16 * ps);
+            if (tag.x == u + 1 || tag.y == u + 1 || tag.z == u + 1 || tag.w == u + 1) {
+              post(2 * u);
+              run = task_done();
+              if (!run) break;
+            }
+            tc_fence_after();
+            if (rank != leader) {
+              tc_fence_before();
+              mbar_arrive_cluster(map_rank(bar(C::kPReady, ps), leader));
+              continue;
+            }
+            run = (kPair == 1 || wait_bar_hot<true>(bar(C::kPReady, ps), (u / kPSlots) & 1, abort_addr, lim)) &&
+                  wait_bar_hot<true>(bar(C::kVFull, vs), (u / L::kVSlots) & 1, abort_addr, lim);
+            if (!run) break;
+            tc_fence_after();
+            const uint64_t pd = operand_desc(sbase + L::kP + ps * kPBytes);
+            const uint64_t vd = operand_desc(sbase + L::kV + vs * L::kVSlot, kKBlock);
 #pragma unroll
-          for (int x = 0; x < kTileKeys / 32; ++x) {
-            uint32_t s[32];
-            tmem_ld32(s_addr + 32u * x, s);
-            tmem_ld_wait();
-            if (!all) {
-              const uint32_t bits = seen(x);
+            for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+              for (int nh = 0; nh < 2; ++nh)
+                pair_mma_ss<kPair>(256u * nh, pd + 2 * kk,
+                                   vd + nh * (L::kVSlot >> 5) + kk * (2048 >> 4), kIdesc,
+                                   (x | kk) != 0 ? 1u : 0u);
+            commit_to<kPair>(bar(C::kPvDone, ps), static_cast<uint16_t>((1u << (2 * kPair)) - 1));
+          }
+          if (run) post(2 * (u - 1) + 1);
+        }
+        if (rank == leader)
+          for (uint32_t r = 0; r < 2 * kPair; ++r) st_cluster_u32(map_rank(ctl + C::kSummed, r), u);
+      }
+    }
+  } else if (warp >= kExpandWarp0) {
+    more_registers<kExpandRegs>();
+    if (scoring) {
+      // ------------------------------------------------ keys of a score CTA
+      // Tile i goes into slot i % 2, once the MMAs of tile i - 2 are done. Rows are
+      // loaded kAhead tiles ahead and table entries one more; the loop is unrolled
+      // over the kAhead + 1 sets of registers, so that no copy waits for a load.
+      constexpr int kLat = kNv ? 4 : 8, kAhead = kNv ? 2 : 1, kSets = kAhead + 1;
+      using R = RowItems<kFmt, kLat, true>;
+      const int w = warp - kExpandWarp0;
+      KeyWalk<kPair> walk(p, cluster, 1);
+      KeyRows<kFmt, kRuns, false> rows(lane, 0);
+      auto entry = [&]() {
+        if (!walk.live) {
+          rows.none();
+          return;
+        }
+        rows.next(p, walk.pieces.seq, walk.at * kTileKeys + kPieceKeys * static_cast<int32_t>(part), w,
+                  walk.pieces.len, lane);
+        walk.step();
+      };
+      R items[kSets];
+      uint32_t exist[kSets], missing[kSets];  // bits of the warp's keys
+      bool live[kSets];
+      bool next_live = walk.live;
+      entry();
+      auto fetch = [&](int k) {  // rows into set k, and the next table entry
+        live[k] = next_live;
+        rows.load(p, lane, items[k], exist[k], missing[k]);
+        next_live = walk.live;
+        entry();
+      };
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) fetch(k);
+      bool run = true;
+      for (uint32_t i = 0; run;) {
+#pragma unroll
+        for (int k = 0; k < kSets; ++k) {
+          if (!run || !live[k]) {
+            run = false;
+            break;
+          }
+          fetch((k + kAhead) % kSets);
+          if (i >= 2 && !warp_wait(bar(C::kSFull, (i - 2) % L::kSBufs), ((i - 2) / L::kSBufs) & 1, abort_addr, lim)) {
+            run = false;
+            break;
+          }
+          store_items<kFmt, kLat, true, false>(items[k], sbase + L::kK + (i & 1) * kKTileBytes, w, lane);
+          fence_proxy_async_cta();
+          if (missing[k] != 0u) {  // the softmax of both CTAs has to know
+            if (lane < kPair)
+              st_cluster_u32(map_rank(ctl + C::kMissing + C::kMissingBytes * (i % C::kMissingTiles) + 4 * (8 * part + w), lane),
+                             ((i + 1) << 8) | exist[k]);
+            asm volatile("fence.acq_rel.cluster;" ::: "memory");
+          }
+          __syncwarp();
+          if (lane == 0) tell_leader(C::kKFull, i & 1);
+          ++i;
+        }
+      }
+    } else {
+      // ------------------------------------------------ values of an output CTA
+      // Piece u goes into slot u % kVSlots, once the MMAs of piece u - kVSlots are done.
+      constexpr int kLat = (kNv ? 4 : 8) / kPair, kAhead = kLat > 4 ? 1 : 2, kSets = kAhead + 1;
+      using R = RowItems<kFmt, kLat, false>;
+      const int w = warp - kExpandWarp0;
+      KeyWalk<kPair> walk(p, cluster, kPair);
+      KeyRows<kFmt, kRuns, kPair == 2> rows(lane, static_cast<int>(part));
+      auto entry = [&]() {
+        if (!walk.live) {
+          rows.none();
+          return;
+        }
+        rows.next(p, walk.pieces.seq, walk.at * kPieceKeys, w, walk.pieces.len, lane);
+        walk.step();
+      };
+      R items[kSets];
+      bool live[kSets];
+      bool next_live = walk.live;
+      entry();
+      auto fetch = [&](int k) {
+        uint32_t exist, missing;
+        live[k] = next_live;
+        rows.load(p, lane, items[k], exist, missing);
+        next_live = walk.live;
+        entry();
+      };
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) fetch(k);
+      bool run = true;
+      for (uint32_t u = 0; run;) {
+#pragma unroll
+        for (int k = 0; k < kSets; ++k) {
+          if (!run || !live[k]) {
+            run = false;
+            break;
+          }
+          fetch((k + kAhead) % kSets);
+          const uint32_t vs = u % L::kVSlots;
+          if (u >= L::kVSlots) {
+            const uint32_t v = u - L::kVSlots;
+            if (!warp_wait<true>(bar(C::kPvDone, v % kPSlots), (v / kPSlots) & 1, abort_addr, lim)) {
+              run = false;
+              break;
+            }
+          }
+          store_items<kFmt, kLat, false, true>(items[k], sbase + L::kV + vs * L::kVSlot, w, lane);
+          fence_proxy_async_cta();
+          __syncwarp();
+          if (lane == 0) tell_leader(C::kVFull, vs);
+          ++u;
+        }
+      }
+    }
+  } else {
+    more_registers<kSoftRegs>();
+    if (scoring) {
+      // ------------------------------------------------ Q, softmax (thread = row)
+      // The two groups of four warps take the pieces in turn. A row's reference goes
+      // from piece to piece through shared memory; each group has a sum of its own.
+      const uint32_t group = warp >> 2, quad = warp & 3;
+      const uint32_t t = tid & 127;
+      const uint32_t lane_base = (32 * quad) << 16;
+      const int row = 128 * static_cast<int>(part) + static_cast<int>(t);  // of the row tile
+      const uint32_t out_rank = kPair + part;
+      const float c = p.score_scale;
+      const uint64_t c2 = f32x2(c, c);
+      uint32_t i0 = 0, u0 = 0, joined = 0;  // tiles, pieces and results of two groups before
+      bool ok = true;
+      Pieces<kPair> pieces(p, cluster);
+      for (uint32_t item = 0; ok && pieces.next(); ++item) {
+        const uint32_t n = static_cast<uint32_t>(pieces.end - pieces.begin) * kPair;
+        // the MMAs that read the Q before are done
+        if (i0 > 0) ok = warp_wait(bar(C::kSFull, (i0 - 1) % L::kSBufs), ((i0 - 1) / L::kSBufs) & 1, abort_addr, lim);
+        if (!ok) break;
+        tc_fence_after();
+        {  // each group writes half of Q
+          const bool mine = row < pieces.rows;
+          const uint4* ql = reinterpret_cast<const uint4*>(p.q_lat + (pieces.row0 + row) * kLatent) + 32 * group;
+          const uint4* qr = reinterpret_cast<const uint4*>(p.q_rope + (pieces.row0 + row) * kRope) + 4 * group;
+          const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+          for (int x = 0; x < 4; ++x) {
+            uint4 v[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y) v[y] = mine ? __ldg(ql + 8 * x + y) : z;
+            uint32_t h[32];
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              const uint4 f = to_f16x8(v[y], p.lat_mult);
+              h[4 * y] = f.x, h[4 * y + 1] = f.y, h[4 * y + 2] = f.z, h[4 * y + 3] = f.w;
+            }
+            tmem_st32(tmem + lane_base + 128u * group + 32u * x, h);
+          }
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const uint4 f = to_f16x8(mine ? __ldg(qr + y) : z, p.rope_mult);
+            st_shared_v4(sbase + L::kQRope + swizzled(t, 4 * group + y), f.x, f.y, f.z, f.w);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          fence_proxy_async_cta();
+          __syncwarp();
+          if (lane == 0) tell_leader(C::kQFull, 0);
+        }
+        // keys that the row sees
+        const int32_t sees = pieces.base + 1 +
+                             static_cast<int32_t>((pieces.row0 - pieces.first_row + min(row, pieces.rows - 1)) /
+                                                  p.num_heads);
+        float m = -INFINITY, l = 0.f;  // the reference that l is relative to
+        for (uint32_t x = (u0 ^ group) & 1; x < n; x += 2) {
+          const uint32_t u = u0 + x, ps = u % kPSlots, i = i0 + x / kPair, h = x % kPair, b = i % L::kSBufs;
+          ok = warp_wait(bar(C::kSFull, b), (i / L::kSBufs) & 1, abort_addr, lim);
+          if (!ok) break;
+          tc_fence_after();
+          uint32_t s[2][32];
+          const uint32_t s_addr = tmem + lane_base + L::kSCol + kTileKeys * b + kPieceKeys * h;
+          tmem_ld32(s_addr, s[0]);
+          tmem_ld32(s_addr + 32u, s[1]);
+          // keys of the piece that the row could see, and (lane j) of keys 8 j .. 8 j + 7 those that exist
+          const int32_t room = sees - ((pieces.begin + static_cast<int32_t>(x / kPair)) * kTileKeys +
+                                       kPieceKeys * static_cast<int32_t>(h));
+          uint32_t exist = 0xffu;
+          if (lane < 8) {
+            const uint32_t v =
+                ld_shared_u32(ctl + C::kMissing + C::kMissingBytes * (i % C::kMissingTiles) + 32 * h + 4 * lane);
+            if ((v >> 8) == ((i + 1) & 0xffffffu)) exist = v & 0xffu;
+          }
+          const bool all = __all_sync(0xffffffffu, room >= kPieceKeys && exist == 0xffu);
+          tmem_ld_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tell_leader(C::kSEmpty, b);  // S is read
+          uint32_t bits[2] = {0xffffffffu, 0xffffffffu};  // the keys that the row sees
+          if (!all) {
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+              uint32_t word = 0;
+#pragma unroll
+              for (int y = 0; y < 4; ++y) word |= __shfl_sync(0xffffffffu, exist, 4 * a + y) << (8 * y);
+              const int32_t seen = room - 32 * a;
+              bits[a] = seen >= 32 ? word : seen <= 0 ? 0u : word & ((1u << seen) - 1u);
 #pragma unroll
               for (int y = 0; y < 32; ++y)
-                if (!((bits >> y) & 1u)) s[y] = 0xff800000u;  // -inf
+                if (!((bits[a] >> y) & 1u)) s[a][y] = 0xff800000u;  // -inf
             }
-            float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll
-            for (int y = 0; y < 32; y += 4) {
-              t0 = fmax3(t0, __uint_as_float(s[y]), __uint_as_float(s[y + 1]));
-              t1 = fmax3(t1, __uint_as_float(s[y + 2]), __uint_as_float(s[y + 3]));
-            }
-            mx = fmax3(mx, t0, t1);
           }
-        }
-        const float top = mx == -INFINITY ? -INFINITY : mx * c;
-        float alpha = 1.f;
-        bool moved = false;
-        if (top > m + kTau) {  // also the first score that the row sees
-          const float to = top - kHeadroom;
-          moved = m != -INFINITY;
-          alpha = moved ? ex2(m - to) : 0.f;
-          l *= alpha;
-          m = to;
-        }
-        const bool rescale = __any_sync(0xffffffffu, moved);
-        const float nm = m == -INFINITY ? 0.f : -m;
-        const uint64_t nm2 = f32x2(nm, nm);
-#pragma unroll 1
-        for (int h = 0; h < kPair; ++h, ++u) {
-          const uint32_t ps = u % kPSlots;
-          if (ok && u >= kPSlots)
+          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int y = 0; y < 32; y += 4) {
+            tops[0] = fmax3(tops[0], __uint_as_float(s[0][y]), __uint_as_float(s[0][y + 1]));
+            tops[1] = fmax3(tops[1], __uint_as_float(s[0][y + 2]), __uint_as_float(s[0][y + 3]));
+            tops[2] = fmax3(tops[2], __uint_as_float(s[1][y]), __uint_as_float(s[1][y + 1]));
+            tops[3] = fmax3(tops[3], __uint_as_float(s[1][y + 2]), __uint_as_float(s[1][y + 3]));
+          }
+          const float mx = fmaxf(fmax3(tops[0], tops[1], tops[2]), tops[3]);
+          const float top = mx == -INFINITY ? -INFINITY : mx * c;
+          // the reference behind the piece before, and behind this one
+          if (u > 0) {
+            const uint32_t v = u - 1;
+            ok = warp_wait(bar(C::kRefDone, 4 * (v & 1) + quad), (v >> 1) & 1, abort_addr, lim);
+            if (!ok) break;
+          }
+          const float before =
+              x > 0 ? __uint_as_float(ld_shared_u32(sbase + L::kRef + 512 * ((u - 1) & 1) + 4 * t)) : -INFINITY;
+          const bool moves = top > before + kTau;  // also the first score that the row sees
+          const float ref = moves ? top - kHeadroom : before;
+          st_shared_u32(sbase + L::kRef + 512 * (u & 1) + 4 * t, __float_as_uint(ref));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::kRefDone, 4 * (u & 1) + quad));
+          if (ref != m) {
+            l *= m == -INFINITY ? 0.f : ex2(m - ref);
+            m = ref;
+          }
+          const float nm = m == -INFINITY ? 0.f : -m;
+          const uint64_t nm2 = f32x2(nm, nm);
+          if (u >= kPSlots)
             ok = warp_wait<true>(bar(C::kPvDone, ps), ((u / kPSlots) & 1) ^ 1, abort_addr, lim);
+          if (!ok) break;
+          const uint32_t dst = sbase + L::kStaged + ps * kPBytes;
           uint64_t sum[2] = {0ull, 0ull};
-          if (ok) {
-            const uint32_t dst = sbase + L::kStaged + ps * kPBytes;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              uint32_t s[32];
-              tmem_ld32(s_addr + kPieceKeys * h + 32u * x, s);
-              tmem_ld_wait();
-              const uint32_t bits = all ? 0xffffffffu : seen(2 * h + x);
-              uint32_t pk[16];
+          for (int a = 0; a < 2; ++a)
 #pragma unroll
-              for (int y = 0; y < 16; ++y) {
+            for (int q = 0; q < 4; ++q) {
+              uint32_t pk[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const int at = 8 * q + 2 * y;
                 float e0, e1;
-                split_f32x2(fma_f32x2(f32x2(__uint_as_float(s[2 * y]), __uint_as_float(s[2 * y + 1])), c2, nm2),
+                split_f32x2(fma_f32x2(f32x2(__uint_as_float(s[a][at]), __uint_as_float(s[a][at + 1])), c2, nm2),
                             e0, e1);
                 e0 = ex2(e0);
                 e1 = ex2(e1);
                 if (!all) {
-                  if (!((bits >> (2 * y)) & 1u)) e0 = 0.f;
-                  if (!((bits >> (2 * y + 1)) & 1u)) e1 = 0.f;
+                  if (!((bits[a] >> at) & 1u)) e0 = 0.f;
+                  if (!((bits[a] >> (at + 1)) & 1u)) e1 = 0.f;
                 }
                 sum[y & 1] = add_f32x2(sum[y & 1], f32x2(e0, e1));
                 pk[y] = pack_f16x2(e0, e1);
               }
-#pragma unroll
-              for (int y = 0; y < 4; ++y)
-                st_shared_v4(dst + swizzled(tid, 4 * x + y), pk[4 * y], pk[4 * y + 1], pk[4 * y + 2],
-                             pk[4 * y + 3]);
+              st_shared_v4(dst + swizzled(t, 4 * a + q), pk[0], pk[1], pk[2], pk[3]);
             }
+          {
             float e0, e1;
             split_f32x2(add_f32x2(sum[0], sum[1]), e0, e1);
             l += e0 + e1;
           }
-          if (h == kPair - 1) {  // S is read
-            tc_fence_before();
+          if (x + 2 == n) {  // the other group ends the result
+            st_shared_u32(sbase + L::kSums + 512 * (joined & 1) + 4 * t, __float_as_uint(l));
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(leader_bar(C::kSEmpty, b));
+            if (lane == 0) mbar_arrive(bar(C::kSumDone, 4 * (joined & 1) + quad));
           }
-          const uint32_t note = note0 + ps * L::kNoteBytes;
-          if (ok) {
-            if (h == 0 && rescale) st_cluster_u32(note + L::kFactor + 4 * tid, __float_as_uint(alpha));
-            if (last && h == kPair - 1)
-              st_cluster_u32(note + L::kFinal + 4 * tid, __float_as_uint(l == 0.f ? 0.f : p.out_mult / l));
-            if (lane == 0) st_cluster_u32(note + L::kFlag + 4 * warp, h == 0 && rescale ? 1u : 0u);
+          // What goes with the piece, rarely: factors, and behind the last one what the
+          // output is to be multiplied by
+          const bool last = x + 1 == n;
+          const bool rescale = __any_sync(0xffffffffu, moves && before != -INFINITY);
+          if (rescale || last) {
+            if (rescale) {
+              const float alpha = !moves ? 1.f : before == -INFINITY ? 0.f : ex2(before - ref);
+              st_cluster_u32(map_rank(sbase + L::kFactor + 512 * ps + 4 * t, out_rank), __float_as_uint(alpha));
+              if (lane == 0) st_cluster_u32(map_rank(sbase + L::kTag + 16 * ps + 4 * quad, out_rank), u + 1);
+            }
+            if (last) {
+              if (n > 1) {
+                ok = warp_wait(bar(C::kSumDone, 4 * (joined & 1) + quad), (joined >> 1) & 1, abort_addr, lim);
+                if (!ok) break;
+                const float other = __uint_as_float(ld_shared_u32(sbase + L::kSums + 512 * (joined & 1) + 4 * t));
+                l += before == -INFINITY ? 0.f : other * ex2(before - ref);
+              }
+              st_cluster_u32(map_rank(sbase + L::kFinal + 512 * (item % L::kFinals) + 4 * t, out_rank),
+                             __float_as_uint(l == 0.f ? 0.f : p.out_mult / l));
+            }
+            if (lane == 0) st_shared_u32(ctl + C::kNoted + 4 * ps, u + 1);
           }
           fence_proxy_async_cta();
-          ok = group_and(ok);  // the piece is staged, its note is written
-          if (!ok) break;
-          if (tid == 0) {
-            const uint32_t full = map_rank(bar(C::kPFull, ps), out_rank);
-            arrive_tx_release_cluster(full, kPBytes);
-            bulk_s2s(map_rank(sbase + L::kP + ps * kPBytes, out_rank), sbase + L::kStaged + ps * kPBytes,
-                     kPBytes, full);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::kStaged, ps));
+          if (last && row < pieces.rows) {
+            const float lse = l == 0.f ? -INFINITY : (m + lg2(l)) * kLn2;
+            if (!pieces.whole) p.part_lse[static_cast<int64_t>(pieces.slot) * (128 * kPair) + row] = lse;
+            else if (p.lse != nullptr) p.lse[pieces.row0 + row] = lse;
           }
         }
+        if (n > 1) ++joined;
+        i0 += n / kPair;
+        u0 += n;
       }
-      if (ok && row < pieces.rows) {
-        const float lse = l == 0.f ? -INFINITY : (m + lg2(l)) * kLn2;
-        if (!pieces.whole) p.part_lse[static_cast<int64_t>(pieces.slot) * (128 * kPair) + row] = lse;
-        else if (p.lse != nullptr) p.lse[pieces.row0 + row] = lse;
-      }
-    }
-    if (tid == 0) st_cluster_u32(map_rank(ctl + C::kSent, out_rank), u);
-  } else {
-    // ------------------------------------------------ rescaling and output (thread = row)
-    const uint32_t lane_base = static_cast<uint32_t>(32 * warp) << 16;
-    const int row = 128 * static_cast<int>(part) + tid;
-    uint32_t u = 0;
-    bool ok = true;
-    Pieces<kPair> pieces(p, cluster);
-    while (ok && pieces.next()) {
-      const uint32_t n = static_cast<uint32_t>(pieces.end - pieces.begin) * kPair;
-      float fin = 0.f;
-      for (uint32_t x = 0; x < n; ++x, ++u) {
-        const uint32_t ps = u % kPSlots;
-        ok = warp_wait<true>(bar(C::kPFull, ps), (u / kPSlots) & 1, abort_addr, lim);
-        if (!ok) break;
-        const uint32_t note = sbase + L::kNote + ps * L::kNoteBytes;
-        if (ld_shared_u32(note + L::kFlag + 4 * warp) != 0u) {
-          // after a piece of the same rows, whose MMAs (and all before) have to be done
-          ok = warp_wait<true>(bar(C::kPvDone, (u - 1) % kPSlots), ((u - 1) / kPSlots) & 1, abort_addr, lim);
+    } else {
+      // ------------------------------------------------ rescaling and output (thread = row)
+      // Each group of four warps has half of the columns.
+      const uint32_t group = warp >> 2, quad = warp & 3, t = tid & 127;
+      const uint32_t o_addr = tmem + ((32 * quad) << 16) + 256u * group;
+      const int row = 128 * static_cast<int>(part) + static_cast<int>(t);
+      uint32_t tasks = 0;
+      bool ok = true;
+      Pieces<kPair> pieces(p, cluster);
+      for (uint32_t item = 0; ok && pieces.next(); ++item) {
+        for (bool rescaling = true; rescaling;) {
+          ok = warp_wait(bar(C::kTask, 0), tasks & 1, abort_addr, lim);
           if (!ok) break;
-          tc_fence_after();
-          const float alpha = __uint_as_float(ld_shared_u32(note + L::kFactor + 4 * tid));
+          ++tasks;
+          const uint32_t word = ld_shared_u32(ctl + C::kTaskWord);
+          const uint32_t u = word >> 1, ps = u % kPSlots;
+          rescaling = (word & 1u) == 0u;
+          if (rescaling) {
+            if (ld_shared_u32(sbase + L::kTag + 16 * ps + 4 * quad) == u + 1) {
+              // after a piece of the same rows, whose MMAs (and all before) have to be done
+              ok = warp_wait<true>(bar(C::kPvDone, (u - 1) % kPSlots), ((u - 1) / kPSlots) & 1, abort_addr, lim);
+              if (!ok) break;
+              tc_fence_after();
+              const float alpha = __uint_as_float(ld_shared_u32(sbase + L::kFactor + 512 * ps + 4 * t));
 #pragma unroll 1
-          for (int y = 0; y < 16; ++y) {
-            uint32_t r[32];
-            tmem_ld32(tmem + lane_base + 32u * y, r);
-            tmem_ld_wait();
+              for (int y = 0; y < 8; ++y) {
+                uint32_t r[32];
+                tmem_ld32(o_addr + 32u * y, r);
+                tmem_ld_wait();
 #pragma unroll
-            for (int q = 0; q < 32; ++q) r[q] = __float_as_uint(__uint_as_float(r[q]) * alpha);
-            tmem_st32(tmem + lane_base + 32u * y, r);
+                for (int q = 0; q < 32; ++q) r[q] = __float_as_uint(__uint_as_float(r[q]) * alpha);
+                tmem_st32(o_addr + 32u * y, r);
+              }
+              tmem_st_wait();
+            }
+          } else {
+            ok = warp_wait<true>(bar(C::kPvDone, ps), (u / kPSlots) & 1, abort_addr, lim);
+            if (!ok) break;
+            tc_fence_after();
+            const float fin = __uint_as_float(ld_shared_u32(sbase + L::kFinal + 512 * (item % L::kFinals) + 4 * t));
+            const bool mine = row < pieces.rows;
+            const bool f32 = !pieces.whole || p.out_fp32;
+            float* wide = pieces.whole
+                              ? static_cast<float*>(p.out) + (pieces.row0 + row) * kLatent
+                              : p.part_out + (static_cast<int64_t>(pieces.slot) * (128 * kPair) + row) * kLatent;
+            wide += 256 * group;
+            uint16_t* narrow = static_cast<uint16_t*>(p.out) + (pieces.row0 + row) * kLatent + 256 * group;
+#pragma unroll 1
+            for (int y = 0; y < 8; ++y) {
+              uint32_t r[32];
+              tmem_ld32(o_addr + 32u * y, r);
+              tmem_ld_wait();
+              float v[32];
+#pragma unroll
+              for (int q = 0; q < 32; ++q) v[q] = __uint_as_float(r[q]) * fin;
+              if (!mine) continue;
+              if (f32) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                  *reinterpret_cast<float4*>(wide + 32 * y + 4 * q) =
+                      make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+              } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  *reinterpret_cast<uint4*>(narrow + 32 * y + 8 * q) =
+                      make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                                 pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+              }
+            }
           }
-          tmem_st_wait();
-        }
-        if (x + 1 == n) fin = __uint_as_float(ld_shared_u32(note + L::kFinal + 4 * tid));
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(leader_bar(C::kPReady, ps));
-      }
-      if (ok) ok = warp_wait<true>(bar(C::kPvDone, (u - 1) % kPSlots), ((u - 1) / kPSlots) & 1, abort_addr, lim);
-      if (!ok) break;
-      tc_fence_after();
-      const bool mine = row < pieces.rows;
-      const bool f32 = !pieces.whole || p.out_fp32;
-      float* wide = pieces.whole
-                        ? static_cast<float*>(p.out) + (pieces.row0 + row) * kLatent
-                        : p.part_out + (static_cast<int64_t>(pieces.slot) * (128 * kPair) + row) * kLatent;
-      uint16_t* narrow = static_cast<uint16_t*>(p.out) + (pieces.row0 + row) * kLatent;
-#pragma unroll 1
-      for (int y = 0; y < 16; ++y) {
-        uint32_t r[32];
-        tmem_ld32(tmem + lane_base + 32u * y, r);
-        tmem_ld_wait();
-        float v[32];
-#pragma unroll
-        for (int q = 0; q < 32; ++q) v[q] = __uint_as_float(r[q]) * fin;
-        if (!mine) continue;
-        if (f32) {
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            *reinterpret_cast<float4*>(wide + 32 * y + 4 * q) =
-                make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-        } else {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<uint4*>(narrow + 32 * y + 8 * q) =
-                make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
-                           pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::kTaskDone, 0));
         }
       }
-      tc_fence_before();
     }
   }
 
@@ -1043,7 +1238,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(const ChunkPara
   if (tid == 0) {
     const uint32_t scored = ld_shared_u32(ctl + C::kScored), summed = ld_shared_u32(ctl + C::kSummed);
     const uint32_t sent = ld_shared_u32(ctl + C::kSent);
-    if (scored > 0) drain(bar(C::kSFull, (scored - 1) & 1), ((scored - 1) >> 1) & 1);
+    if (scored > 0) drain(bar(C::kSFull, (scored - 1) % L::kSBufs), ((scored - 1) / L::kSBufs) & 1);
     if (sent > 0) drain(bar(C::kPFull, (sent - 1) % kPSlots), ((sent - 1) / kPSlots) & 1);
     if (summed > 0) drain(bar(C::kPvDone, (summed - 1) % kPSlots), ((summed - 1) / kPSlots) & 1);
   }
@@ -1187,14 +1382,14 @@ bool chunk_shape_ok(int32_t num_q, int32_t num_heads, int32_t num_seqs) {
 }
 
 // Clusters of a kernel that the device holds at once, asked once a device.
-template <int kFmt, int kPair>
+template <int kFmt, int kPair, bool kRuns>
 int32_t resident_clusters(int device, cudaLaunchConfig_t cfg, int sms, int* clusters) {
   constexpr int kDevices = 64;
   static std::atomic<int> known[kDevices];
   int n = device < kDevices ? known[device].load(std::memory_order_relaxed) : 0;
   if (n == 0) {
     cfg.gridDim = dim3(static_cast<unsigned>(sms / (2 * kPair) * (2 * kPair)));
-    if (cudaOccupancyMaxActiveClusters(&n, chunk_kernel<kFmt, kPair>, &cfg) != cudaSuccess || n < 1) {
+    if (cudaOccupancyMaxActiveClusters(&n, chunk_kernel<kFmt, kPair, kRuns>, &cfg) != cudaSuccess || n < 1) {
       cudaGetLastError();
       return NVFP4_MLA_ERR_LAUNCH;
     }
@@ -1205,12 +1400,12 @@ int32_t resident_clusters(int device, cudaLaunchConfig_t cfg, int sms, int* clus
   return NVFP4_MLA_OK;
 }
 
-template <int kFmt, int kPair>
+template <int kFmt, int kPair, bool kRuns>
 int32_t launch_chunk(ChunkParams p, int device, int sms, cudaStream_t stream) {
   constexpr size_t smem = ChunkLayout<kPair>::kBytes;
   const size_t plan_smem = 4 * static_cast<size_t>(p.num_seqs);
   // limits of the process: the same in every call
-  if (cudaFuncSetAttribute(reinterpret_cast<const void*>(chunk_kernel<kFmt, kPair>),
+  if (cudaFuncSetAttribute(reinterpret_cast<const void*>(chunk_kernel<kFmt, kPair, kRuns>),
                            cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess ||
       (plan_smem > 40 * 1024 &&
        cudaFuncSetAttribute(reinterpret_cast<const void*>(chunk_plan_kernel<kPair>),
@@ -1229,7 +1424,7 @@ int32_t launch_chunk(ChunkParams p, int device, int sms, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (int32_t st = resident_clusters<kFmt, kPair>(device, cfg, sms, &p.clusters)) return st;
+  if (int32_t st = resident_clusters<kFmt, kPair, kRuns>(device, cfg, sms, &p.clusters)) return st;
   if (p.invalid_count != nullptr) {
     chunk_check_kernel<<<p.num_seqs < 4 * sms ? p.num_seqs : 4 * sms, 256, 0, stream>>>(p);
     if (int32_t st = launch_status()) return st;
@@ -1240,7 +1435,7 @@ int32_t launch_chunk(ChunkParams p, int device, int sms, cudaStream_t stream) {
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, chunk_kernel<kFmt, kPair>, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, chunk_kernel<kFmt, kPair, kRuns>, p) != cudaSuccess) {
     cudaGetLastError();
     return NVFP4_MLA_ERR_LAUNCH;
   }
@@ -1255,6 +1450,12 @@ int32_t launch_chunk(ChunkParams p, int device, int sms, cudaStream_t stream) {
     return NVFP4_MLA_ERR_LAUNCH;
   }
   return NVFP4_MLA_OK;
+}
+
+template <int kFmt, int kPair>
+int32_t launch_pages(const ChunkParams& p, bool runs, int device, int sms, cudaStream_t stream) {
+  return runs ? launch_chunk<kFmt, kPair, true>(p, device, sms, stream)
+              : launch_chunk<kFmt, kPair, false>(p, device, sms, stream);
 }
 
 }  // namespace
@@ -1333,9 +1534,10 @@ extern "C" int32_t dense_mla_chunk(const void* q_latent, const void* q_rope, con
   p.wait_cycles = decode_wait_cycles();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int pair = pair_of(num_q, num_heads, num_seqs);
+  const bool runs = page_size % kPieceKeys == 0;
   if (fp8)
-    return pair == 2 ? launch_chunk<NVFP4_MLA_ROW_FP8_576, 2>(p, dev, sms, s)
-                     : launch_chunk<NVFP4_MLA_ROW_FP8_576, 1>(p, dev, sms, s);
-  return pair == 2 ? launch_chunk<NVFP4_MLA_ROW_NVFP4_352, 2>(p, dev, sms, s)
-                   : launch_chunk<NVFP4_MLA_ROW_NVFP4_352, 1>(p, dev, sms, s);
+    return pair == 2 ? launch_pages<NVFP4_MLA_ROW_FP8_576, 2>(p, runs, dev, sms, s)
+                     : launch_pages<NVFP4_MLA_ROW_FP8_576, 1>(p, runs, dev, sms, s);
+  return pair == 2 ? launch_pages<NVFP4_MLA_ROW_NVFP4_352, 2>(p, runs, dev, sms, s)
+                   : launch_pages<NVFP4_MLA_ROW_NVFP4_352, 1>(p, runs, dev, sms, s);
 }
