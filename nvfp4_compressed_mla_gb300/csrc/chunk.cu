@@ -62,8 +62,11 @@ constexpr long long kDrainLimit = 1ll << 31;
 // The reference of a row moves when a score exceeds it by more than kTau (log2
 // units), to kHeadroom below that score. P <= 2^15 fits FP16 (largest finite
 // value 65504) and P of the largest score is at least 2^kHeadroom then, so that
-// weights down to 2^-21 of it are normal FP16 numbers.
-constexpr float kTau = 15.f, kHeadroom = 7.f;
+// weights down to 2^-16 of it are normal FP16 numbers and smaller ones are off by
+// 2^-27 of it at most. A move stops the pipeline for an O in tensor memory to be
+// read and written, so that room for scores to grow is worth more than precision
+// of small weights: with kHeadroom 7 a third of the pieces had one.
+constexpr float kTau = 15.f, kHeadroom = 2.f;
 // Key tiles' time that a row tile costs beside its own (loading Q, the first
 // score tile before P V can begin, writing O), and the least share of a cluster.
 constexpr int kTileOverhead = 3, kLeastShare = 6;
@@ -264,6 +267,19 @@ __device__ __forceinline__ void bulk_s2s(uint32_t dst_cluster, uint32_t src, uin
       "r"(src), "r"(bytes), "r"(bar_cluster)
       : "memory");
 }
+// An arrival at another CTA's barrier. What it reports lies in this CTA's own
+// memories, where the tensor core of this SM reads it, and this thread has seen it
+// complete; so release at CTA scope is enough. At cluster scope the arrival takes
+// about 1000 cycles.
+__device__ __forceinline__ void arrive_remote(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
 template <int kRegs>
 __device__ __forceinline__ void set_registers() {  // of all warps of a warpgroup
   if constexpr (kRegs > kLaunchRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
@@ -382,12 +398,15 @@ struct ChunkLayout {
   static constexpr uint32_t kP = kV + kVSlots * kVSlotBytes;
   static constexpr uint32_t kRawOut = kP + kPSlots * kPBytes;
   static constexpr uint32_t kRawsOut = 2;
-  static constexpr uint32_t kFactor = kRawOut + kRawsOut * kRawBytes;  // rescale factor of each row, a P slot
-  static constexpr uint32_t kTag = kFactor + kPSlots * 512;  // per 32 rows and P slot: 1 + piece to rescale at
-  static constexpr uint32_t kFinal = kTag + kPSlots * 16;    // output factor of each row, a result
-  static constexpr uint32_t kFinals = 8;  // more results than there are pieces under way
-  static constexpr uint32_t kEndOut = kFinal + kFinals * 512;
-  static_assert(kFinals > kPSlots + kStages + 1, "final factors");
+  // what may come with a piece: rescale factors of the rows, 1 + the piece for
+  // each 32 of them that it is for; output factors of the rows, a result
+  static constexpr uint32_t kNotes = 8;  // pieces (results) that may be noted and not yet done
+  static constexpr uint32_t kFactor = kRawOut + kRawsOut * kRawBytes;
+  static constexpr uint32_t kTag = kFactor + kNotes * 512;
+  static constexpr uint32_t kFinal = kTag + kNotes * 16;
+  static constexpr uint32_t kEndOut = kFinal + kNotes * 512;
+  // a piece is noted once its stage is free: those that are staged or have a slot
+  static_assert(kNotes > kPSlots + kStages, "notes");
   static constexpr uint32_t kCtl = kEndScore > kEndOut ? kEndScore : kEndOut;
   static constexpr uint32_t kCtlBytes = 704;
   static constexpr uint32_t kBytes = kCtl + kCtlBytes;
@@ -550,7 +569,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
     fence_mbar_init();
   }
   if (tid < 8 * C::kMissingTiles) st_shared_u32(ctl + C::kMissing + 4 * tid, 0u);
-  if (!scoring && tid < 4 * L::kPSlots) st_shared_u32(sbase + L::kTag + 4 * tid, 0u);
+  if (!scoring && tid < 4 * L::kNotes) st_shared_u32(sbase + L::kTag + 4 * tid, 0u);
   if (warp == kIssueWarp) alloc_tmem_pair(ctl + C::kTmem);
   tc_fence_before();
   __syncthreads();
@@ -640,56 +659,75 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
       if (lane == 0) st_shared_u32(ctl + C::kLoaded, u);
     } else if (warp == kSendWarp && scoring) {
       // ---------------------------------------------- P pieces to the output CTA
-      if (lane == 0) {
-        const uint32_t out_p = map_rank(sbase + L::kP, 2 + part), out_full = map_rank(bar(C::kPFull, 0), 2 + part);
-        uint32_t u = 0;
-        bool run = true;
-        Pieces pieces(p, cluster);
-        while (run && pieces.next()) {
-          const uint32_t n = static_cast<uint32_t>(pieces.end - pieces.begin) * 2;
-          for (uint32_t x = 0; x < n; ++x, ++u) {
-            const uint32_t ps = u % L::kPSlots, st = u % L::kStages;
-            run = wait_bar_hot(bar(C::kStaged, st), (u / L::kStages) & 1, abort_addr, lim) &&
-                  (u < L::kPSlots ||
-                   wait_bar_hot<true>(bar(C::kPvDone, ps), ((u / L::kPSlots) & 1) ^ 1, abort_addr, lim));
-            if (!run) break;
+      const uint32_t out_p = map_rank(sbase + L::kP, 2 + part), out_full = map_rank(bar(C::kPFull, 0), 2 + part);
+      uint32_t u = 0;
+      bool run = true;
+      Pieces pieces(p, cluster);
+      while (run && pieces.next()) {
+        const uint32_t n = static_cast<uint32_t>(pieces.end - pieces.begin) * 2;
+        for (uint32_t x = 0; x < n; ++x, ++u) {
+          const uint32_t ps = u % L::kPSlots, st = u % L::kStages;
+          run = warp_wait(bar(C::kStaged, st), (u / L::kStages) & 1, abort_addr, lim) &&
+                (u < L::kPSlots ||
+                 warp_wait<true>(bar(C::kPvDone, ps), ((u / L::kPSlots) & 1) ^ 1, abort_addr, lim));
+          if (!run) break;
+          const bool noted = ld_shared_u32(ctl + C::kNoted + 4 * (u & 3)) == u + 1;
+          if (elect_one()) {
             const uint32_t full = out_full + 8u * ps;
-            if (ld_shared_u32(ctl + C::kNoted + 4 * (u & 3)) == u + 1) arrive_tx_release_cluster(full, kPBytes);
+            if (noted) arrive_tx_release_cluster(full, kPBytes);
             else arrive_tx_relaxed_cluster(full, kPBytes);
             bulk_s2s(out_p + ps * kPBytes, sbase + L::kStaged + st * kPBytes, kPBytes, full);
           }
+          __syncwarp();
         }
-        st_cluster_u32(map_rank(ctl + C::kSent, 2 + part), u);
+      }
+      if (lane == 0) st_cluster_u32(map_rank(ctl + C::kSent, 2 + part), u);
+    } else if (warp == kSendWarp) {
+      // ---------------------------------------------- P pieces have left their stage
+      const uint32_t freed = map_rank(bar(C::kStageFree, 0), part);
+      uint32_t u = 0;
+      bool run = true;
+      Pieces pieces(p, cluster);
+      while (run && pieces.next()) {
+        const uint32_t n = static_cast<uint32_t>(pieces.end - pieces.begin) * 2;
+        for (uint32_t x = 0; x < n; ++x, ++u) {
+          run = warp_wait<true>(bar(C::kPFull, u % L::kPSlots), (u / L::kPSlots) & 1, abort_addr, lim);
+          if (!run) break;
+          if (elect_one()) mbar_arrive_cluster_relaxed(freed + 8u * (u & 1));
+          __syncwarp();
+        }
       }
     } else if (warp == kIssueWarp && scoring) {
-      // ---------------------------------------------- S = Q K^T (one thread a CTA)
-      // The leader's issues the MMAs, the other one tells it what its CTA has ready.
-      if (lane == 0) {
-        constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(kTileKeys >> 3) << 17) |
-                                    (static_cast<uint32_t>(kTileRows >> 4) << 24);
-        const uint64_t qr = operand_desc(sbase + L::kQRope);
-        const uint32_t peer = map_rank(bar(C::kPeer, 0), 0);
-        uint32_t i = 0;
-        bool run = true;
-        Pieces pieces(p, cluster);
-        for (uint32_t item = 0; run && pieces.next(); ++item) {
-          if (!wait_bar_hot(bar(C::kQFull, 0), item & 1, abort_addr, lim)) break;
-          for (int32_t kt = pieces.begin; kt < pieces.end; ++kt, ++i) {
-            const uint32_t b = i & 1, ph = (i >> 1) & 1;
-            run = wait_bar_hot(bar(C::kSEmpty, b), ph ^ 1, abort_addr, lim) &&
-                  wait_bar_hot(bar(C::kKFull, b), ph, abort_addr, lim);
-            if (!run) break;
-            if (part != 0) {
-              tc_fence_after();
-              tc_fence_before();
-              mbar_arrive_cluster(peer + 8u * b);
-              continue;
-            }
-            run = wait_bar_hot<true>(bar(C::kPeer, b), ph, abort_addr, lim);
-            if (!run) break;
-            tc_fence_after();
-            const uint32_t d = kSCol + kTileKeys * b;
-            const uint64_t kd = operand_desc(sbase + L::kK + b * kKTileBytes);
+      // ---------------------------------------------- S = Q K^T
+      // The leader's warp issues the MMAs, the other one tells it what its CTA has
+      // ready. The whole warp goes through the loop, so that operands stay uniform.
+      constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(kTileKeys >> 3) << 17) |
+                                  (static_cast<uint32_t>(kTileRows >> 4) << 24);
+      const uint64_t qr = operand_desc(sbase + L::kQRope);
+      const uint32_t peer = map_rank(bar(C::kPeer, 0), 0);
+      uint32_t i = 0;
+      bool run = true;
+      Pieces pieces(p, cluster);
+      for (uint32_t item = 0; run && pieces.next(); ++item) {
+        if (!warp_wait(bar(C::kQFull, 0), item & 1, abort_addr, lim)) break;
+        for (int32_t kt = pieces.begin; kt < pieces.end; ++kt, ++i) {
+          const uint32_t b = i & 1, ph = (i >> 1) & 1;
+          run = warp_wait(bar(C::kSEmpty, b), ph ^ 1, abort_addr, lim) &&
+                warp_wait(bar(C::kKFull, b), ph, abort_addr, lim);
+          if (!run) break;
+          tc_fence_after();
+          if (part != 0) {
+            tc_fence_before();
+            if (elect_one()) arrive_remote(peer + 8u * b);
+            __syncwarp();
+            continue;
+          }
+          run = warp_wait<true>(bar(C::kPeer, b), ph, abort_addr, lim);
+          if (!run) break;
+          tc_fence_after();
+          const uint32_t d = kSCol + kTileKeys * b;
+          const uint64_t kd = operand_desc(sbase + L::kK + b * kKTileBytes);
+          if (elect_one()) {
 #pragma unroll
             for (int x = 0; x < 32; ++x)
               pair_mma_ts(d, 8u * x, kd + (x >> 2) * (kKBlock >> 4) + 2 * (x & 3), kIdesc, x != 0 ? 1u : 0u);
@@ -698,55 +736,59 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
               pair_mma_ss(d, qr + 2 * x, kd + 8 * (kKBlock >> 4) + 2 * x, kIdesc, 1u);
             commit_to(bar(C::kSFull, b), 0x3);
           }
+          __syncwarp();
         }
-        if (part == 0)
-          for (uint32_t r = 0; r < 2; ++r) st_cluster_u32(map_rank(ctl + C::kScored, r), i);
       }
+      if (part == 0 && lane < 2) st_cluster_u32(map_rank(ctl + C::kScored, lane), i);
     } else if (warp == kIssueWarp) {
-      // ---------------------------------------------- O += P V (one thread a CTA)
-      // It follows the P pieces that land in its CTA, has O rescaled where a piece
-      // comes with factors and written behind the last piece of a row tile (tasks of
-      // warps 0-7); then the leader's issues the MMAs and the other one tells it.
-      if (lane == 0) {
-        constexpr uint32_t kIdesc = (1u << 4) | (1u << 16) | ((256u >> 3) << 17) |
-                                    (static_cast<uint32_t>(kTileRows >> 4) << 24);
-        const uint32_t peer = map_rank(bar(C::kPReady, 0), 2), freed = map_rank(bar(C::kStageFree, 0), part);
-        uint32_t u = 0, tasks = 0;
-        bool run = true;
-        auto post = [&](uint32_t word) {
+      // ---------------------------------------------- O += P V
+      // The warp follows the P pieces that land in its CTA, has O rescaled where a
+      // piece comes with factors and written behind the last piece of a row tile
+      // (tasks of warps 0-7); then the leader's issues the MMAs and the other one
+      // tells it.
+      constexpr uint32_t kIdesc = (1u << 4) | (1u << 16) | ((256u >> 3) << 17) |
+                                  (static_cast<uint32_t>(kTileRows >> 4) << 24);
+      const uint32_t peer = map_rank(bar(C::kPReady, 0), 2);
+      uint32_t u = 0, tasks = 0;
+      bool run = true;
+      auto post = [&](uint32_t word) {
+        if (lane == 0) {
           st_shared_u32(ctl + C::kTaskWord, word);
           mbar_arrive(bar(C::kTask, 0));
-          ++tasks;
-        };
-        auto task_done = [&]() { return wait_bar_hot(bar(C::kTaskDone, 0), (tasks - 1) & 1, abort_addr, lim); };
-        Pieces pieces(p, cluster);
-        while (run && pieces.next()) {
-          const uint32_t n = static_cast<uint32_t>(pieces.end - pieces.begin) * 2;
-          if (tasks > 0 && !task_done()) break;  // O before has been read
-          for (uint32_t x = 0; x < n; ++x, ++u) {
-            const uint32_t ps = u % L::kPSlots, vs = u % L::kVSlots;
-            run = wait_bar_hot<true>(bar(C::kPFull, ps), (u / L::kPSlots) & 1, abort_addr, lim);
+        }
+        __syncwarp();
+        ++tasks;
+      };
+      auto task_done = [&]() { return warp_wait(bar(C::kTaskDone, 0), (tasks - 1) & 1, abort_addr, lim); };
+      Pieces pieces(p, cluster);
+      while (run && pieces.next()) {
+        const uint32_t n = static_cast<uint32_t>(pieces.end - pieces.begin) * 2;
+        if (tasks > 0 && !task_done()) break;  // O before has been read
+        for (uint32_t x = 0; x < n; ++x, ++u) {
+          const uint32_t ps = u % L::kPSlots, vs = u % L::kVSlots;
+          run = warp_wait<true>(bar(C::kPFull, ps), (u / L::kPSlots) & 1, abort_addr, lim);
+          if (!run) break;
+          const uint4 tag = ld_shared_v4(sbase + L::kTag + 16 * (u % L::kNotes));
+          if (tag.x == u + 1 || tag.y == u + 1 || tag.z == u + 1 || tag.w == u + 1) {
+            post(2 * u);
+            run = task_done();
             if (!run) break;
-            mbar_arrive_cluster_relaxed(freed + 8u * (u & 1));  // the piece has left its stage
-            const uint4 tag = ld_shared_v4(sbase + L::kTag + 16 * ps);
-            if (tag.x == u + 1 || tag.y == u + 1 || tag.z == u + 1 || tag.w == u + 1) {
-              post(2 * u);
-              run = task_done();
-              if (!run) break;
-            }
-            run = wait_bar_hot(bar(C::kVFull, vs), (u / L::kVSlots) & 1, abort_addr, lim);
-            if (!run) break;
-            tc_fence_after();
-            if (part != 0) {
-              tc_fence_before();
-              mbar_arrive_cluster(peer + 8u * ps);
-              continue;
-            }
-            run = wait_bar_hot<true>(bar(C::kPReady, ps), (u / L::kPSlots) & 1, abort_addr, lim);
-            if (!run) break;
-            tc_fence_after();
-            const uint64_t pd = operand_desc(sbase + L::kP + ps * kPBytes);
-            const uint64_t vd = operand_desc(sbase + L::kV + vs * kVSlotBytes, kKBlock);
+          }
+          run = warp_wait(bar(C::kVFull, vs), (u / L::kVSlots) & 1, abort_addr, lim);
+          if (!run) break;
+          tc_fence_after();
+          if (part != 0) {
+            tc_fence_before();
+            if (elect_one()) arrive_remote(peer + 8u * ps);
+            __syncwarp();
+            continue;
+          }
+          run = warp_wait<true>(bar(C::kPReady, ps), (u / L::kPSlots) & 1, abort_addr, lim);
+          if (!run) break;
+          tc_fence_after();
+          const uint64_t pd = operand_desc(sbase + L::kP + ps * kPBytes);
+          const uint64_t vd = operand_desc(sbase + L::kV + vs * kVSlotBytes, kKBlock);
+          if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
@@ -755,11 +797,11 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
                             (x | kk) != 0 ? 1u : 0u);
             commit_to(bar(C::kPvDone, ps), 0xF);
           }
-          if (run) post(2 * (u - 1) + 1);
+          __syncwarp();
         }
-        if (part == 0)
-          for (uint32_t r = 0; r < 4; ++r) st_cluster_u32(map_rank(ctl + C::kSummed, r), u);
+        if (run) post(2 * (u - 1) + 1);
       }
+      if (part == 0 && lane < 4) st_cluster_u32(map_rank(ctl + C::kSummed, lane), u);
     }
   } else if (warp >= kExpandWarp0) {
     set_registers<kExpandRegs>();
@@ -972,17 +1014,17 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
           }
           if (rescale || last) {
             if (rescale) {
-              const uint32_t ps = u % L::kPSlots;
+              const uint32_t note = u % L::kNotes;
               const float alpha = !moves ? 1.f : before == -INFINITY ? 0.f : ex2(before - ref);
-              st_cluster_u32(map_rank(sbase + L::kFactor + 512 * ps + 4 * t, out_rank), __float_as_uint(alpha));
-              if (lane == 0) st_cluster_u32(map_rank(sbase + L::kTag + 16 * ps + 4 * quad, out_rank), u + 1);
+              st_cluster_u32(map_rank(sbase + L::kFactor + 512 * note + 4 * t, out_rank), __float_as_uint(alpha));
+              if (lane == 0) st_cluster_u32(map_rank(sbase + L::kTag + 16 * note + 4 * quad, out_rank), u + 1);
             }
             if (last) {
               ok = warp_wait(bar(C::kSumDone, 4 * (item & 1) + quad), (item >> 1) & 1, abort_addr, lim);
               if (!ok) break;
               const float other = __uint_as_float(ld_shared_u32(sbase + L::kSums + 512 * (item & 1) + 4 * t));
               l += before == -INFINITY ? 0.f : other * ex2(before - ref);
-              st_cluster_u32(map_rank(sbase + L::kFinal + 512 * (item % L::kFinals) + 4 * t, out_rank),
+              st_cluster_u32(map_rank(sbase + L::kFinal + 512 * (item % L::kNotes) + 4 * t, out_rank),
                              __float_as_uint(l == 0.f ? 0.f : p.out_mult / l));
             }
             if (lane == 0) st_shared_u32(ctl + C::kNoted + 4 * (u & 3), u + 1);
@@ -1009,16 +1051,16 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
           if (!ok) break;
           ++tasks;
           const uint32_t word = ld_shared_u32(ctl + C::kTaskWord);
-          const uint32_t u = word >> 1, ps = u % L::kPSlots;
+          const uint32_t u = word >> 1, ps = u % L::kPSlots, note = u % L::kNotes;
           rescaling = (word & 1u) == 0u;
           if (rescaling) {
-            if (ld_shared_u32(sbase + L::kTag + 16 * ps + 4 * quad) == u + 1) {
+            if (ld_shared_u32(sbase + L::kTag + 16 * note + 4 * quad) == u + 1) {
               // behind a piece of the same rows, whose MMAs (and all before) have to be done
               const uint32_t v = u - 1;
               ok = warp_wait<true>(bar(C::kPvDone, v % L::kPSlots), (v / L::kPSlots) & 1, abort_addr, lim);
               if (!ok) break;
               tc_fence_after();
-              const float alpha = __uint_as_float(ld_shared_u32(sbase + L::kFactor + 512 * ps + 4 * t));
+              const float alpha = __uint_as_float(ld_shared_u32(sbase + L::kFactor + 512 * note + 4 * t));
 #pragma unroll 1
               for (int y = 0; y < 8; ++y) {
                 uint32_t r[32];
@@ -1034,7 +1076,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
             ok = warp_wait<true>(bar(C::kPvDone, ps), (u / L::kPSlots) & 1, abort_addr, lim);
             if (!ok) break;
             tc_fence_after();
-            const float fin = __uint_as_float(ld_shared_u32(sbase + L::kFinal + 512 * (item % L::kFinals) + 4 * t));
+            const float fin = __uint_as_float(ld_shared_u32(sbase + L::kFinal + 512 * (item % L::kNotes) + 4 * t));
             const bool mine = row < pieces.rows;
             const bool f32 = !pieces.whole || p.out_fp32;
             float* wide = pieces.whole

@@ -75,8 +75,9 @@ class Case:
     def reference(self, tokens=None):
         """(out, lse, bound of |out error|, bound of |lse error|) of all tokens, or of some rows.
 
-        The kernel's roundings: FP16 weights, off by 2^-11 of themselves (half a step) or by 2^-25
-        where subnormal, beside a largest weight of at least 2^7; scores accumulated in fp32 over 36
+        The kernel's roundings: FP16 weights, off by 2^-11 of themselves (half a step) or, where
+        subnormal, by half of their step of 2^-24; the largest weight is at least 2^2 then, so that
+        relative to it that is 2^-25 / 2^2 = 2^-27; scores accumulated in fp32 over 36
         steps of 16 products, each off by at most 2^-23 of the magnitudes' sum; q_rope times the ratio
         of the scales in FP16 (2^-11) where that is no power of two; exponentials and sums in fp32,
         2^-20 in all; the bf16 result, 2^-8 (half a step) of itself."""
@@ -109,7 +110,7 @@ class Case:
                 out[t] = w @ k
                 lse[t] = (top + np.log(tot))[:, 0]
                 ltol[t] = dz.max(1) + 2.0 ** -20 * (1 + np.abs(lse[t]))
-                dw = w * (2.0 ** -11 + 2 * dz + 2.0 ** -20) + 2.0 ** -32 / tot
+                dw = w * (2.0 ** -11 + 2 * dz + 2.0 ** -20) + 2.0 ** -27 / tot
                 tol[t] = dw @ np.abs(k) + 1e-30
         return out, lse, tol, ltol
 
