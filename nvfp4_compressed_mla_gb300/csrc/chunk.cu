@@ -245,19 +245,6 @@ struct Pieces {
 };
 
 // ------------------------------------------------------------------ PTX
-__device__ __forceinline__ void arrive_tx_release_cluster(uint32_t cluster_bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::
-                   "r"(cluster_bar),
-               "r"(bytes)
-               : "memory");
-}
-// The same where only copied bytes are to be seen behind the barrier.
-__device__ __forceinline__ void arrive_tx_relaxed_cluster(uint32_t cluster_bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::
-                   "r"(cluster_bar),
-               "r"(bytes)
-               : "memory");
-}
 // shared (this CTA) -> shared (another CTA of the cluster), counted on that CTA's mbarrier
 __device__ __forceinline__ void bulk_s2s(uint32_t dst_cluster, uint32_t src, uint32_t bytes,
                                          uint32_t bar_cluster) {
@@ -672,18 +659,19 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
                  warp_wait<true>(bar(C::kPvDone, ps), ((u / L::kPSlots) & 1) ^ 1, abort_addr, lim));
           if (!run) break;
           const bool noted = ld_shared_u32(ctl + C::kNoted + 4 * (u & 3)) == u + 1;
-          if (elect_one()) {
-            const uint32_t full = out_full + 8u * ps;
-            if (noted) arrive_tx_release_cluster(full, kPBytes);
-            else arrive_tx_relaxed_cluster(full, kPBytes);
-            bulk_s2s(out_p + ps * kPBytes, sbase + L::kStaged + st * kPBytes, kPBytes, full);
-          }
+          if (noted) asm volatile("fence.acq_rel.cluster;" ::: "memory");  // the notes are there first
+          if (elect_one())
+            bulk_s2s(out_p + ps * kPBytes, sbase + L::kStaged + st * kPBytes, kPBytes, out_full + 8u * ps);
           __syncwarp();
         }
       }
       if (lane == 0) st_cluster_u32(map_rank(ctl + C::kSent, 2 + part), u);
     } else if (warp == kSendWarp) {
       // ---------------------------------------------- P pieces have left their stage
+      // and their slots' barriers take the next one, in this CTA: an arrival from the
+      // score CTA would cost its sender 300 cycles a piece.
+      if (lane == 0)
+        for (uint32_t i = 0; i < L::kPSlots; ++i) mbar_arrive_tx(bar(C::kPFull, i), kPBytes);
       const uint32_t freed = map_rank(bar(C::kStageFree, 0), part);
       uint32_t u = 0;
       bool run = true;
@@ -693,7 +681,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
         for (uint32_t x = 0; x < n; ++x, ++u) {
           run = warp_wait<true>(bar(C::kPFull, u % L::kPSlots), (u / L::kPSlots) & 1, abort_addr, lim);
           if (!run) break;
-          if (elect_one()) mbar_arrive_cluster_relaxed(freed + 8u * (u & 1));
+          if (elect_one()) {
+            mbar_arrive_cluster_relaxed(freed + 8u * (u & 1));
+            mbar_arrive_tx(bar(C::kPFull, u % L::kPSlots), kPBytes);
+          }
           __syncwarp();
         }
       }
