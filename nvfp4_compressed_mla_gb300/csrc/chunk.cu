@@ -45,14 +45,15 @@ namespace {
 
 constexpr int kTileRows = 256, kTileKeys = 128;
 constexpr int kPieceKeys = 64;                // keys of a P piece and of a V slot
-constexpr int kSoftWarps = 8;                 // softmax / rescaling and output: two groups of four
-constexpr int kExpandWarp0 = 8, kExpandWarps = 8;
-constexpr int kIssueWarp = 16, kSendWarp = 17, kLoadWarp = 18;
-constexpr int kChunkThreads = 20 * 32;        // the last four warps leave registers to the others
+constexpr uint32_t kGroups = 3;               // of four warps: softmax / rescaling and output
+constexpr int kSoftWarps = 4 * kGroups;
+constexpr int kExpandWarp0 = kSoftWarps, kExpandWarps = 8;
+constexpr int kIssueWarp = kExpandWarp0 + kExpandWarps, kSendWarp = kIssueWarp + 1, kLoadWarp = kIssueWarp + 2;
+constexpr int kChunkThreads = (kIssueWarp + 4) * 32;  // the last four warps leave registers to the others
 // Registers of a thread of the softmax, the expanding and the last warps; as
 // many in all as at the launch.
-constexpr int kLaunchRegs = 96, kSoftRegs = 128, kExpandRegs = 88, kIssueRegs = 48;
-static_assert(2 * kSoftRegs + 2 * kExpandRegs + kIssueRegs == 5 * kLaunchRegs, "registers");
+constexpr int kLaunchRegs = 80, kSoftRegs = 104, kExpandRegs = 64, kIssueRegs = 40;
+static_assert(kGroups * kSoftRegs + 2 * kExpandRegs + kIssueRegs == 6 * kLaunchRegs, "registers");
 constexpr int kMaxClusters = 40;
 constexpr uint32_t kPBytes = 128 * kPieceKeys * 2;
 constexpr uint32_t kKBlock = kPieceKeys * 128;   // 64 keys x 64 dimensions, FP16
@@ -389,9 +390,9 @@ struct ChunkLayout {
   static constexpr uint32_t kStaged = kQRope + 16384;
   static constexpr uint32_t kRawScore = kStaged + kStages * kPBytes;
   static constexpr uint32_t kRawsScore = 1;
-  static constexpr uint32_t kRef = kRawScore + kRawsScore * kRawBytes;  // references of the rows, two pieces
-  static constexpr uint32_t kSums = kRef + 1024;                        // sums of weights, two results
-  static constexpr uint32_t kEndScore = kSums + 1024;
+  static constexpr uint32_t kRef = kRawScore + kRawsScore * kRawBytes;  // references of the rows, a group
+  static constexpr uint32_t kSums = kRef + kGroups * 512;               // sums of weights, a group and 4 results
+  static constexpr uint32_t kEndScore = kSums + 4 * kGroups * 512;
   // output CTA
   static constexpr uint32_t kVSlots = 3, kPSlots = kNv ? 4 : 3;
   static constexpr uint32_t kV = 0;
@@ -408,7 +409,7 @@ struct ChunkLayout {
   // a piece is noted once its stage is free: those that are staged or have a slot
   static_assert(kNotes > kPSlots + kStages, "notes");
   static constexpr uint32_t kCtl = kEndScore > kEndOut ? kEndScore : kEndOut;
-  static constexpr uint32_t kCtlBytes = 704;
+  static constexpr uint32_t kCtlBytes = 1072;
   static constexpr uint32_t kBytes = kCtl + kCtlBytes;
   static_assert(kBytes <= kMaxSharedBytes && kCtl % 16 == 0 && kTag % 16 == 0, "shared memory");
   static_assert(kStaged % 1024 == 0 && kP % 1024 == 0 && kRawScore % 16 == 0 && kRawOut % 16 == 0, "operands");
@@ -417,10 +418,10 @@ constexpr uint32_t kSCol = 256;  // score CTA's tensor memory: Q's latent part, 
 static_assert(kSCol + 2 * kTileKeys <= kTmemCols, "tensor memory");
 struct ChunkCtl {  // barriers and words, at the same offsets in every CTA of the cluster
   static constexpr uint32_t kRawFull = 0, kRawEmpty = 16, kKFull = 32, kPeer = 48, kSFull = 64, kSEmpty = 80,
-                            kQFull = 96, kStaged = 104, kStageFree = 120, kRefDone = 136, kSumDone = 200,
-                            kPFull = 264, kPReady = 296, kPvDone = 328, kVFull = 360, kTask = 384,
-                            kTaskDone = 392, kTmem = 400, kAbort = 404, kSent = 408, kScored = 412,
-                            kSummed = 416, kLoaded = 420, kTaskWord = 424, kNoted = 428, kMissing = 448;
+                            kQFull = 96, kStaged = 104, kStageFree = 120, kRefDone = 152, kSumDone = 248,
+                            kPFull = 632, kPReady = 664, kPvDone = 696, kVFull = 728, kTask = 752,
+                            kTaskDone = 760, kTmem = 768, kAbort = 772, kSent = 776, kScored = 780,
+                            kSummed = 784, kLoaded = 788, kTaskWord = 792, kNoted = 796, kMissing = 816;
   // 1 + tile and the bits of its 64 keys that exist, a CTA of the pair, 8 tiles:
   // written where some page does not resolve
   static constexpr uint32_t kMissingTiles = 8;
@@ -543,15 +544,13 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
       mbar_init(bar(C::kKFull, i), kExpandWarps);
       mbar_init(bar(C::kPeer, i), 1);
       mbar_init(bar(C::kSFull, i), 1);
-      mbar_init(bar(C::kSEmpty, i), kSoftWarps);
-      mbar_init(bar(C::kStaged, i), kSoftWarps / 2);
-      mbar_init(bar(C::kStageFree, i), 1);
+      mbar_init(bar(C::kSEmpty, i), 8);  // four warps a piece
+      mbar_init(bar(C::kStaged, i), 4);
     }
     mbar_init(bar(C::kQFull, 0), kSoftWarps);
-    for (uint32_t i = 0; i < 8; ++i) {
-      mbar_init(bar(C::kRefDone, i), 1);
-      mbar_init(bar(C::kSumDone, i), 1);
-    }
+    for (uint32_t i = 0; i < 4 * kGroups; ++i) mbar_init(bar(C::kRefDone, i), 1);
+    for (uint32_t i = 0; i < 16 * kGroups; ++i) mbar_init(bar(C::kSumDone, i), 1);
+    for (uint32_t i = 0; i < 4; ++i) mbar_init(bar(C::kStageFree, i), 1);
     for (uint32_t i = 0; i < L::kPSlots; ++i) {
       mbar_init(bar(C::kPFull, i), 1);
       mbar_init(bar(C::kPReady, i), 1);
@@ -695,7 +694,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
           run = warp_wait<true>(bar(C::kPFull, u % L::kPSlots), (u / L::kPSlots) & 1, abort_addr, lim);
           if (!run) break;
           if (elect_one()) {
-            mbar_arrive_cluster_relaxed(freed + 8u * (u & 1));
+            mbar_arrive_cluster_relaxed(freed + 8u * (u & 3));
             mbar_arrive_tx(bar(C::kPFull, u % L::kPSlots), kPBytes);
           }
           __syncwarp();
@@ -867,26 +866,26 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
     Pieces pieces(p, cluster);
     if (scoring) {
       // ---------------------------------------------- Q, softmax (thread = row)
-      // The two groups of four warps take the pieces in turn, group 0 the first 64
-      // keys of each tile. A row's reference goes from piece to piece through shared
+      // The groups of four warps take the pieces in turn: one has the time of three
+      // pieces for each. A row's reference goes from piece to piece through shared
       // memory; each group has a sum of its own.
       const uint32_t out_rank = 2 + part;
       const float c = p.score_scale;
       const uint64_t c2 = f32x2(c, c);
       uint32_t i0 = 0;  // tiles before
       for (uint32_t item = 0; ok && pieces.next(); ++item) {
-        const uint32_t n = static_cast<uint32_t>(pieces.end - pieces.begin);
+        const uint32_t n = static_cast<uint32_t>(pieces.end - pieces.begin) * 2;
         // the MMAs that read the Q before are done
         if (i0 > 0) ok = warp_wait(bar(C::kSFull, (i0 - 1) & 1), ((i0 - 1) >> 1) & 1, abort_addr, lim);
         if (!ok) break;
         tc_fence_after();
-        {  // each group writes half of Q
+        {  // each group writes a third of Q's nine blocks of 64 dimensions
           const bool mine = row < pieces.rows;
-          const uint4* ql = reinterpret_cast<const uint4*>(p.q_lat + (pieces.row0 + row) * kLatent) + 32 * group;
-          const uint4* qr = reinterpret_cast<const uint4*>(p.q_rope + (pieces.row0 + row) * kRope) + 4 * group;
+          const uint4* ql = reinterpret_cast<const uint4*>(p.q_lat + (pieces.row0 + row) * kLatent);
+          const uint4* qr = reinterpret_cast<const uint4*>(p.q_rope + (pieces.row0 + row) * kRope);
           const uint4 z = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll 1
-          for (int x = 0; x < 4; ++x) {
+          for (uint32_t x = group; x < 8; x += kGroups) {
             uint4 v[8];
 #pragma unroll
             for (int y = 0; y < 8; ++y) v[y] = mine ? __ldg(ql + 8 * x + y) : z;
@@ -896,12 +895,14 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
               const uint4 f = to_f16x8(v[y], p.lat_mult);
               h[4 * y] = f.x, h[4 * y + 1] = f.y, h[4 * y + 2] = f.z, h[4 * y + 3] = f.w;
             }
-            tmem_st32(tmem + lane_base + 128u * group + 32u * x, h);
+            tmem_st32(tmem + lane_base + 32u * x, h);
           }
+          if (group == kGroups - 1) {
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const uint4 f = to_f16x8(mine ? __ldg(qr + y) : z, p.rope_mult);
-            st_shared_v4(sbase + L::kQRope + swizzled(t, 4 * group + y), f.x, f.y, f.z, f.w);
+            for (int y = 0; y < 8; ++y) {
+              const uint4 f = to_f16x8(mine ? __ldg(qr + y) : z, p.rope_mult);
+              st_shared_v4(sbase + L::kQRope + swizzled(t, y), f.x, f.y, f.z, f.w);
+            }
           }
           tmem_st_wait();
           tc_fence_before();
@@ -914,21 +915,20 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
                              static_cast<int32_t>((pieces.row0 - pieces.first_row + min(row, pieces.rows - 1)) /
                                                   p.num_heads);
         float m = -INFINITY, l = 0.f;  // the reference that l is relative to
-        for (uint32_t x = 0; x < n; ++x) {
-          const uint32_t i = i0 + x, b = i & 1, u = 2 * i + group, st = u % L::kStages;
+        for (uint32_t x = (group + kGroups - 2 * i0 % kGroups) % kGroups; x < n; x += kGroups) {
+          const uint32_t u = 2 * i0 + x, i = u >> 1, b = i & 1, half = u & 1, st = u % L::kStages;
           ok = warp_wait(bar(C::kSFull, b), (i >> 1) & 1, abort_addr, lim);
           if (!ok) break;
           tc_fence_after();
           uint32_t s[2][32];
-          const uint32_t s_addr = tmem + lane_base + kSCol + kTileKeys * b + kPieceKeys * group;
+          const uint32_t s_addr = tmem + lane_base + kSCol + kTileKeys * b + kPieceKeys * half;
           tmem_ld32(s_addr, s[0]);
           tmem_ld32(s_addr + 32u, s[1]);
           // keys of the piece that the row could see, and those that exist
-          const int32_t room = sees - ((pieces.begin + static_cast<int32_t>(x)) * kTileKeys +
-                                       kPieceKeys * static_cast<int32_t>(group));
-          uint4 have = ld_shared_v4(ctl + C::kMissing + 32 * (i % C::kMissingTiles) + 16 * group);
+          const int32_t room = sees - pieces.begin * kTileKeys - kPieceKeys * static_cast<int32_t>(x);
+          uint4 have = ld_shared_v4(ctl + C::kMissing + 32 * (i % C::kMissingTiles) + 16 * half);
           if (have.x != i + 1) have.y = have.z = 0xffffffffu;
-          const bool all = __all_sync(0xffffffffu, room >= kPieceKeys && (have.y & have.z) == 0xffffffffu);
+          const bool all = room >= kPieceKeys && (have.y & have.z) == 0xffffffffu;
           tmem_ld_wait();
           tc_fence_before();
           __syncwarp();
@@ -956,14 +956,18 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
           const float top = mx == -INFINITY ? -INFINITY : mx * c;
           // the reference behind the piece before, and behind this one
           if (u > 0) {
-            ok = warp_wait(bar(C::kRefDone, 4 * (group ^ 1) + quad), ((u - 1) >> 1) & 1, abort_addr, lim);
+            const uint32_t v = u - 1;
+            ok = warp_wait(bar(C::kRefDone, 4 * (v % kGroups) + quad), (v / kGroups) & 1, abort_addr, lim);
             if (!ok) break;
           }
-          const float before =
-              x + group > 0 ? __uint_as_float(ld_shared_u32(sbase + L::kRef + 512 * (group ^ 1) + 4 * t)) : -INFINITY;
+          const uint32_t ref_at = sbase + L::kRef + 4 * t;
+          auto ref_of = [&](uint32_t v) { return __uint_as_float(ld_shared_u32(ref_at + 512 * (v % kGroups))); };
+          const float before = x > 0 ? ref_of(u - 1) : -INFINITY;
+          const bool last = x + 1 == n;
+          const float earlier = last && x > 1 ? ref_of(u - 2) : -INFINITY;  // while it is there
           const bool moves = top > before + kTau;  // also the first score that the row sees
           const float ref = moves ? top - kHeadroom : before;
-          st_shared_u32(sbase + L::kRef + 512 * group + 4 * t, __float_as_uint(ref));
+          st_shared_u32(ref_at + 512 * group, __float_as_uint(ref));
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(C::kRefDone, 4 * group + quad));
           if (ref != m) {
@@ -997,7 +1001,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
           }
           if (u >= L::kStages) {  // the stage's piece before has left it
             const uint32_t v = u - L::kStages;
-            ok = warp_wait<true>(bar(C::kStageFree, v & 1), (v >> 1) & 1, abort_addr, lim);
+            ok = warp_wait<true>(bar(C::kStageFree, v & 3), (v >> 2) & 1, abort_addr, lim);
             if (!ok) break;
           }
           const uint32_t dst = sbase + L::kStaged + st * kPBytes;
@@ -1009,13 +1013,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
                            pk[a][4 * q + 3]);
           // What goes with the piece, rarely: factors, and behind the last one what the
           // output is to be multiplied by
-          const bool last = x + 1 == n && group == 1;
           const bool rescale = __any_sync(0xffffffffu, moves && before != -INFINITY);
-          if (x + 1 == n && group == 0) {  // the other group ends the result
-            st_shared_u32(sbase + L::kSums + 512 * (item & 1) + 4 * t, __float_as_uint(l));
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(C::kSumDone, 4 * (item & 1) + quad));
-          }
           if (rescale || last) {
             if (rescale) {
               const uint32_t note = u % L::kNotes;
@@ -1024,10 +1022,15 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
               if (lane == 0) st_cluster_u32(map_rank(sbase + L::kTag + 16 * note + 4 * quad, out_rank), u + 1);
             }
             if (last) {
-              ok = warp_wait(bar(C::kSumDone, 4 * (item & 1) + quad), (item >> 1) & 1, abort_addr, lim);
+              for (uint32_t d = 1; d < kGroups && ok; ++d) {  // the group of piece u - d
+                const uint32_t g = (group + kGroups - d) % kGroups;
+                ok = warp_wait(bar(C::kSumDone, 4 * kGroups * (item & 3) + 4 * g + quad), (item >> 2) & 1,
+                               abort_addr, lim);
+                const float other =
+                    __uint_as_float(ld_shared_u32(sbase + L::kSums + 512 * (kGroups * (item & 3) + g) + 4 * t));
+                if (other != 0.f) l += other * ex2((d == 1 ? before : earlier) - ref);
+              }
               if (!ok) break;
-              const float other = __uint_as_float(ld_shared_u32(sbase + L::kSums + 512 * (item & 1) + 4 * t));
-              l += before == -INFINITY ? 0.f : other * ex2(before - ref);
               st_cluster_u32(map_rank(sbase + L::kFinal + 512 * (item % L::kNotes) + 4 * t, out_rank),
                              __float_as_uint(l == 0.f ? 0.f : p.out_mult / l));
             }
@@ -1042,12 +1045,17 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
             else if (p.lse != nullptr) p.lse[pieces.row0 + row] = lse;
           }
         }
-        i0 += n;
+        if (!ok) break;
+        // for the group that ends the result (nobody waits for that one's own)
+        st_shared_u32(sbase + L::kSums + 512 * (kGroups * (item & 3) + group) + 4 * t, __float_as_uint(l));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::kSumDone, 4 * kGroups * (item & 3) + 4 * group + quad));
+        i0 += n / 2;
       }
     } else {
       // ---------------------------------------------- rescaling and output (thread = row)
-      // Each group of four warps has half of the columns.
-      const uint32_t o_addr = tmem + lane_base + 256u * group;
+      // The groups of four warps take blocks of 32 columns in turn.
+      const uint32_t o_addr = tmem + lane_base;
       uint32_t tasks = 0;
       for (uint32_t item = 0; ok && pieces.next(); ++item) {
         for (bool rescaling = true; rescaling;) {
@@ -1066,7 +1074,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
               tc_fence_after();
               const float alpha = __uint_as_float(ld_shared_u32(sbase + L::kFactor + 512 * note + 4 * t));
 #pragma unroll 1
-              for (int y = 0; y < 8; ++y) {
+              for (uint32_t y = group; y < 16; y += kGroups) {
                 uint32_t r[32];
                 tmem_ld32(o_addr + 32u * y, r);
                 tmem_ld_wait();
@@ -1086,10 +1094,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
             float* wide = pieces.whole
                               ? static_cast<float*>(p.out) + (pieces.row0 + row) * kLatent
                               : p.part_out + (static_cast<int64_t>(pieces.slot) * kTileRows + row) * kLatent;
-            wide += 256 * group;
-            uint16_t* narrow = static_cast<uint16_t*>(p.out) + (pieces.row0 + row) * kLatent + 256 * group;
+            uint16_t* narrow = static_cast<uint16_t*>(p.out) + (pieces.row0 + row) * kLatent;
 #pragma unroll 1
-            for (int y = 0; y < 8; ++y) {
+            for (uint32_t y = group; y < 16; y += kGroups) {
               uint32_t r[32];
               tmem_ld32(o_addr + 32u * y, r);
               tmem_ld_wait();
