@@ -54,7 +54,7 @@ def library_path() -> str:
 
 
 def _lib():
-    return _native.load()
+    return _native._lib or _native.load()
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:

@@ -9,6 +9,8 @@
 // All four work on metadata of a few kilobytes to a few megabytes and are bound
 // by latency (dependent loads, launches, barriers), but for the copy of pages,
 // which is bound by HBM: it reads and writes each page once.
+#include <atomic>
+
 #include "plan_common.cuh"
 
 namespace nvfp4_mla {
@@ -239,71 +241,108 @@ __global__ void __launch_bounds__(kPlanThreads) release_kernel(const ReleasePara
     copy_ints(p.page_shares, p.page_shares_out, p.num_blocks,
               static_cast<int64_t>(rank) * kPlanThreads + tid, static_cast<int64_t>(ctas) * kPlanThreads);
   if (rank == 0 && p.refused_count != nullptr && refused > 0) atomicAdd(p.refused_count, refused);
-  cluster_barrier();  // the counts may change now; the units are in every CTA's shared memory
+  __syncthreads();  // the units are in shared memory
 
-  // f(s, pages of 8 x 32 entries (-1: none)) for each round of a unit
-  auto walk = [&](int u, auto&& f) {
-    int s;
-    {  // the sequence: the first whose units end behind u
-      int lo = 0, hi = p.num_seqs;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (unit_end[mid] <= u) lo = mid + 1;
-        else hi = mid;
-      }
-      s = lo;
-    }
-    const int32_t first = s > 0 ? unit_end[s - 1] : 0;
-    const int64_t b1 = min(p.page.blocks(p.seq_lens[s]), p.max_blocks);
-    int64_t b = begin[s] + (u - first) * chunk;
-    const int64_t end = min(b + chunk, b1);
-    const int32_t* row = p.block_table + static_cast<int64_t>(s) * p.max_blocks;
-    for (; b < end; b += kReleaseChunk) {
-      int32_t page[kReleaseFlight];
-#pragma unroll
-      for (int k = 0; k < kReleaseFlight; ++k) {
-        const int64_t at = b + 32 * k + lane;
-        page[k] = at < end ? __ldg(row + at) : -1;
-        if (page[k] >= p.num_blocks) page[k] = -1;
-      }
-      f(s, page);
-    }
-  };
   const int first_unit = static_cast<int>(rank) * kPlanWarps + warp;
   const int stride = static_cast<int>(ctas) * kPlanWarps;
+  // the sequence of a unit, its next block and the block behind its last
+  auto locate = [&](int u, int& s, int64_t& b, int64_t& end) {
+    int lo = 0, hi = p.num_seqs;  // the first sequence whose units end behind u
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (unit_end[mid] <= u) lo = mid + 1;
+      else hi = mid;
+    }
+    s = lo;
+    b = begin[s] + (u - (s > 0 ? unit_end[s - 1] : 0)) * chunk;
+    end = min(b + chunk, static_cast<int64_t>(min(p.page.blocks(p.seq_lens[s]), p.max_blocks)));
+  };
+  auto load = [&](int s, int64_t b, int64_t end, int32_t (&page)[kReleaseFlight]) {
+    const int32_t* row = p.block_table + static_cast<int64_t>(s) * p.max_blocks;
+#pragma unroll
+    for (int k = 0; k < kReleaseFlight; ++k) {
+      const int64_t at = b + 32 * k + lane;
+      page[k] = at < end ? __ldg(row + at) : -1;
+      if (page[k] >= p.num_blocks) page[k] = -1;
+    }
+  };
+  // The warp's first two units stay in registers through the passes, if they are of
+  // one round each.
+  constexpr int kKept = 2;
+  int kept_seq[kKept];
+  int32_t kept[kKept][kReleaseFlight];
+  const bool keeps = chunk == kReleaseChunk;
+  if (keeps) {
+#pragma unroll
+    for (int x = 0; x < kKept; ++x) {
+      const int u = first_unit + x * stride;
+      int64_t b = 0, end = 0;
+      kept_seq[x] = 0;
+      if (u < units) locate(u, kept_seq[x], b, end);
+      load(kept_seq[x], b, end, kept[x]);
+    }
+  }
+  // begin(u) and f(s, pages of 8 x 32 entries (-1: none)) for each round of the warp's units
+  auto walk = [&](auto&& start, auto&& f, auto&& stop) {
+    if (keeps) {
+#pragma unroll
+      for (int x = 0; x < kKept; ++x) {
+        const int u = first_unit + x * stride;
+        if (u < units) {
+          start(u);
+          f(kept_seq[x], kept[x]);
+          stop(u);
+        }
+      }
+    }
+    for (int u = first_unit + (keeps ? kKept * stride : 0); u < units; u += stride) {
+      int s;
+      int64_t b, end;
+      locate(u, s, b, end);
+      start(u);
+      for (; b < end; b += kReleaseChunk) {
+        int32_t page[kReleaseFlight];
+        load(s, b, end, page);
+        f(s, page);
+      }
+      stop(u);
+    }
+  };
+  auto nothing = [](int) {};
+  auto held_by = [&](const int32_t(&page)[kReleaseFlight], int32_t (&held)[kReleaseFlight]) {
+#pragma unroll
+    for (int k = 0; k < kReleaseFlight; ++k)
+      held[k] = page[k] >= 0 ? __ldcg(p.page_shares_out + page[k]) : 0;
+  };
 
-  for (int u = first_unit; u < units; u += stride)
-    walk(u, [&](int, const int32_t(&page)[kReleaseFlight]) {
+  cluster_barrier();  // the counts may change now
+  walk(nothing, [&](int, const int32_t(&page)[kReleaseFlight]) {
 #pragma unroll
-      for (int k = 0; k < kReleaseFlight; ++k)
-        if (page[k] >= 0) atomicAdd(p.page_shares_out + page[k], -1);
-    });
+    for (int k = 0; k < kReleaseFlight; ++k)
+      if (page[k] >= 0) atomicAdd(p.page_shares_out + page[k], -1);
+  }, nothing);
   cluster_barrier();
-  for (int u = first_unit; u < units; u += stride)
-    walk(u, [&](int s, const int32_t(&page)[kReleaseFlight]) {
-      int32_t held[kReleaseFlight];
+  walk(nothing, [&](int s, const int32_t(&page)[kReleaseFlight]) {
+    int32_t held[kReleaseFlight];
+    held_by(page, held);
 #pragma unroll
-      for (int k = 0; k < kReleaseFlight; ++k)
-        held[k] = page[k] >= 0 ? __ldcg(p.page_shares_out + page[k]) : 0;
-#pragma unroll
-      for (int k = 0; k < kReleaseFlight; ++k)
-        if (held[k] < 0) atomicMin(p.page_shares_out + page[k], s - kReleaseMark);
-    });
+    for (int k = 0; k < kReleaseFlight; ++k)
+      if (held[k] < 0) atomicMin(p.page_shares_out + page[k], s - kReleaseMark);
+  }, nothing);
   cluster_barrier();
   const uint32_t counts_addr = smem_u32(counts);
-  for (int u = first_unit; u < units; u += stride) {
-    int n = 0;
-    walk(u, [&](int s, const int32_t(&page)[kReleaseFlight]) {
-      int32_t held[kReleaseFlight];
+  int n = 0;
+  walk([&](int) { n = 0; },
+       [&](int s, const int32_t(&page)[kReleaseFlight]) {
+         int32_t held[kReleaseFlight];
+         held_by(page, held);
 #pragma unroll
-      for (int k = 0; k < kReleaseFlight; ++k)
-        held[k] = page[k] >= 0 ? __ldcg(p.page_shares_out + page[k]) : 0;
-#pragma unroll
-      for (int k = 0; k < kReleaseFlight; ++k)
-        n += __popc(__ballot_sync(0xffffffffu, held[k] == s - kReleaseMark));
-    });
-    if (lane < ctas) st_cluster(counts_addr + 4u * static_cast<uint32_t>(u), lane, n);
-  }
+         for (int k = 0; k < kReleaseFlight; ++k)
+           n += __popc(__ballot_sync(0xffffffffu, held[k] == s - kReleaseMark));
+       },
+       [&](int u) {
+         if (lane < ctas) st_cluster(counts_addr + 4u * static_cast<uint32_t>(u), lane, n);
+       });
   cluster_barrier();
 
   int64_t all = 0;
@@ -319,25 +358,23 @@ __global__ void __launch_bounds__(kPlanThreads) release_kernel(const ReleasePara
     if (p.dropped_count != nullptr && top > p.free_capacity)
       atomicAdd(p.dropped_count, static_cast<int32_t>(top - p.free_capacity));
   }
-  for (int u = first_unit; u < units; u += stride) {
-    int64_t at = top - (u > 0 ? counts[u - 1] : 0);  // one above the unit's first page
-    walk(u, [&](int s, const int32_t(&page)[kReleaseFlight]) {
-      int32_t held[kReleaseFlight];
+  int64_t at = 0;  // one above the next page's slot
+  walk([&](int u) { at = top - (u > 0 ? counts[u - 1] : 0); },
+       [&](int s, const int32_t(&page)[kReleaseFlight]) {
+         int32_t held[kReleaseFlight];
+         held_by(page, held);
 #pragma unroll
-      for (int k = 0; k < kReleaseFlight; ++k)
-        held[k] = page[k] >= 0 ? __ldcg(p.page_shares_out + page[k]) : 0;
-#pragma unroll
-      for (int k = 0; k < kReleaseFlight; ++k) {
-        const bool mine = held[k] == s - kReleaseMark;
-        const uint32_t live = __ballot_sync(0xffffffffu, mine);
-        const int64_t slot = at - 1 - __popc(live & ((1u << lane) - 1));
-        if (mine && slot < p.free_capacity) p.free_pages[slot] = page[k];
-        // nobody else takes the 0 for its mark
-        if (mine) p.page_shares_out[page[k]] = 0;
-        at -= __popc(live);
-      }
-    });
-  }
+         for (int k = 0; k < kReleaseFlight; ++k) {
+           const bool mine = held[k] == s - kReleaseMark;
+           const uint32_t live = __ballot_sync(0xffffffffu, mine);
+           const int64_t slot = at - 1 - __popc(live & ((1u << lane) - 1));
+           if (mine && slot < p.free_capacity) p.free_pages[slot] = page[k];
+           // nobody else takes the 0 for its mark
+           if (mine) p.page_shares_out[page[k]] = 0;
+           at -= __popc(live);
+         }
+       },
+       nothing);
   cluster_barrier();  // every length has been read
   for (int s = static_cast<int>(rank) * kPlanThreads + tid; s < p.num_seqs;
        s += static_cast<int>(ctas) * kPlanThreads)
@@ -368,6 +405,7 @@ struct CompactParams {
   uint32_t* used;   // a bit a page: in a table
   uint32_t* idle;   // a bit a page: on the stack
   int32_t* moved;   // [num_blocks] the page's new id
+  int2* ranks;      // used and free pages before a word of the bit maps
   int32_t words;    // of a bit map
 };
 
@@ -378,6 +416,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_clear_kernel(const Compa
   const int64_t first = static_cast<int64_t>(blockIdx.x) * kPlanThreads + threadIdx.x;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kPlanThreads;
   for (int64_t w = first; w < p.words; w += stride) p.used[w] = p.idle[w] = 0u;
+  if (first == 0 && p.pages_end != nullptr) *p.pages_end = 0;
   for (int64_t i = first; i < p.num_blocks; i += stride) p.moved[i] = static_cast<int32_t>(i);
   if (p.page_shares_out != p.page_shares)
     copy_ints(p.page_shares, p.page_shares_out, p.num_blocks, first, stride);
@@ -412,71 +451,97 @@ __global__ void __launch_bounds__(kRowThreads) compact_mark_kernel(const Compact
 }
 
 // The moves: used page number i from the top to free page number i from the
-// bottom, as long as that is downwards. One CTA; a thread has consecutive words
-// of the bit maps, and its first ranks are those of two prefix sums.
+// bottom, as long as that is downwards. One cluster. Every CTA sums up all words
+// of the bit maps (a thread has consecutive ones) and keeps the sums before each
+// 32 words of its share; then a warp takes a word at a time, a lane a page.
 __global__ void __launch_bounds__(kPlanThreads) compact_rank_kernel(const CompactParams p) {
   __shared__ int64_t sums[32];
   __shared__ int32_t sh_moves, sh_end;
   cudaGridDependencySynchronize();
   cudaTriggerProgrammaticLaunchCompletion();
-  const int tid = threadIdx.x;
-  const int32_t per = (p.words + kPlanThreads - 1) / kPlanThreads;
-  const int32_t w0 = min(tid * static_cast<int64_t>(per), static_cast<int64_t>(p.words));
-  const int32_t w1 = min(w0 + static_cast<int64_t>(per), static_cast<int64_t>(p.words));
-  int64_t n_used = 0, n_idle = 0;
-  for (int32_t w = w0; w < w1; ++w) {
-    const uint32_t a = __ldcg(p.used + w);
-    n_used += __popc(a);
-    n_idle += __popc(__ldcg(p.idle + w) & ~a);  // a page of a table is not free
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = cta_rank(), ctas = cluster_size();
+  // the CTA's share of the words, in whole warps' turns
+  const int32_t share = (p.words + static_cast<int32_t>(ctas) - 1) / static_cast<int32_t>(ctas);
+  const int32_t own0 = min(static_cast<int64_t>(rank) * share, static_cast<int64_t>(p.words));
+  const int32_t own1 = min(own0 + static_cast<int64_t>(share), static_cast<int64_t>(p.words));
+  auto words_at = [&](int32_t w, uint32_t& used, uint32_t& idle) {
+    used = __ldcg(p.used + w);
+    idle = __ldcg(p.idle + w) & ~used;  // a page of a table is not free
+  };
+  // sums over the words before the share, in it and behind it, in one pass: first
+  // the two others' totals, then the share's running sums, written per word
+  int64_t before_used = 0, before_idle = 0, all_used = 0, all_idle = 0;
+  {
+    int64_t bu = 0, bi = 0, au = 0, ai = 0;
+    for (int32_t w = tid; w < p.words; w += kPlanThreads) {
+      uint32_t used, idle;
+      words_at(w, used, idle);
+      const int u = __popc(used), i = __popc(idle);
+      au += u;
+      ai += i;
+      if (w < own0) {
+        bu += u;
+        bi += i;
+      }
+    }
+    block_scan(bu, before_used, sums);
+    block_scan(bi, before_idle, sums);
+    block_scan(au, all_used, sums);
+    block_scan(ai, all_idle, sums);
   }
-  int64_t all_used = 0, all_idle = 0;
-  const int32_t used_before = static_cast<int32_t>(block_scan(n_used, all_used, sums) - n_used);
-  const int32_t idle_before = static_cast<int32_t>(block_scan(n_idle, all_idle, sums) - n_idle);
   const int32_t U = static_cast<int32_t>(all_used), F = static_cast<int32_t>(all_idle);
   const int32_t most = min(min(U, F), p.max_moves);
   if (tid == 0) sh_moves = sh_end = 0;
-  {
-    int32_t f = idle_before, t = U - 1 - used_before;  // rank from the bottom, from the top
-    for (int32_t w = w0; w < w1 && (f < most || t >= 0); ++w) {
-      const uint32_t a = __ldcg(p.used + w);
-      for (uint32_t bits = __ldcg(p.idle + w) & ~a; bits != 0; bits &= bits - 1, ++f)
-        if (f < most) p.copy_dst[f] = 32 * w + __ffs(bits) - 1;
-      for (uint32_t bits = a; bits != 0; bits &= bits - 1, --t)
-        if (t < most) p.copy_src[t] = 32 * w + __ffs(bits) - 1;
-    }
+  // ranks of the first pages of each word of the share
+  for (int32_t w0 = own0; w0 < own1; w0 += kPlanThreads) {
+    const int32_t w = w0 + tid;
+    uint32_t used = 0, idle = 0;
+    if (w < own1) words_at(w, used, idle);
+    const int64_t tu = block_scan(__popc(used), before_used, sums) - __popc(used);
+    const int64_t ti = block_scan(__popc(idle), before_idle, sums) - __popc(idle);
+    if (w < own1) p.ranks[w] = make_int2(static_cast<int32_t>(tu), static_cast<int32_t>(ti));
   }
   __syncthreads();
+  // f(page, whether it is used or free, its rank among those from the top or the bottom, the others' rank)
+  auto each = [&](auto&& f) {
+    for (int32_t w = own0 + warp; w < own1; w += kPlanWarps) {
+      uint32_t used, idle;
+      words_at(w, used, idle);
+      const int2 r = p.ranks[w];
+      const uint32_t below = (1u << lane) - 1u;
+      const int32_t nu = r.x + __popc(used & below), ni = r.y + __popc(idle & below);
+      // used pages from this one up, free pages below this one
+      f(32 * w + lane, (used >> lane) & 1u, (idle >> lane) & 1u, U - nu, ni);
+    }
+  };
+  each([&](int32_t page, bool used, bool idle, int32_t up, int32_t below) {
+    if (idle && below < most) p.copy_dst[below] = page;
+    if (used && up - 1 < most) p.copy_src[up - 1] = page;
+  });
+  cluster_barrier();
   int down = 0;
-  for (int32_t i = tid; i < most; i += kPlanThreads) down += p.copy_dst[i] < p.copy_src[i];
+  for (int32_t i = tid; i < most; i += kPlanThreads) down += __ldcg(p.copy_dst + i) < __ldcg(p.copy_src + i);
   if (down > 0) atomicAdd(&sh_moves, down);
   __syncthreads();
   const int32_t m = sh_moves;
-  {  // the stack: all free pages, the lowest on top
-    int32_t f = idle_before, t = U - 1 - used_before, end = 0;
-    for (int32_t w = w0; w < w1; ++w) {
-      const uint32_t a = __ldcg(p.used + w);
-      const uint32_t any = a | __ldcg(p.idle + w);
-      for (uint32_t bits = any; bits != 0; bits &= bits - 1) {
-        const uint32_t bit = bits & (0u - bits);
-        const int32_t page = 32 * w + __ffs(bits) - 1;
-        if ((a & bit) != 0) {
-          // above it: t used pages, F - f free ones
-          if (t < m) p.free_pages_out[t + min(F - m, F - f)] = page;
-          else end = page + 1;
-          --t;
-        } else {
-          // above it: t + 1 used pages, F - 1 - f free ones
-          if (f >= m) p.free_pages_out[F - 1 - f + min(m, t + 1)] = page;
-          else end = page + 1;
-          ++f;
-        }
-      }
+  cluster_barrier();  // every CTA has counted: the list may end now
+  int32_t end = 0;
+  each([&](int32_t page, bool used, bool idle, int32_t up, int32_t below) {
+    // the stack: all free pages, the lowest on top
+    if (used) {
+      if (up - 1 < m) p.free_pages_out[up - 1 + min(F - m, F - below)] = page;
+      else end = page + 1;
+    } else if (idle) {
+      if (below >= m) p.free_pages_out[F - 1 - below + min(m, up)] = page;
+      else end = page + 1;
     }
-    if (end > 0) atomicMax(&sh_end, end);
-  }
-  for (int32_t i = tid; i < p.max_moves; i += kPlanThreads) {
+  });
+  if (end > 0) atomicMax(&sh_end, end);
+  for (int32_t i = static_cast<int32_t>(rank) * kPlanThreads + tid; i < p.max_moves;
+       i += static_cast<int32_t>(ctas) * kPlanThreads) {
     if (i < m) {
-      const int32_t from = p.copy_src[i], to = p.copy_dst[i];
+      const int32_t from = __ldcg(p.copy_src + i), to = __ldcg(p.copy_dst + i);
       p.moved[from] = to;
       p.page_shares_out[to] = p.page_shares_out[from];
       p.page_shares_out[from] = 0;
@@ -486,8 +551,8 @@ __global__ void __launch_bounds__(kPlanThreads) compact_rank_kernel(const Compac
   }
   __syncthreads();
   if (tid == 0) {
-    *p.free_count_out = F;
-    if (p.pages_end != nullptr) *p.pages_end = sh_end;
+    if (rank == 0) *p.free_count_out = F;
+    if (p.pages_end != nullptr && sh_end > 0) atomicMax(p.pages_end, sh_end);
   }
 }
 
@@ -523,41 +588,42 @@ __global__ void __launch_bounds__(kRowThreads) compact_table_kernel(const Compac
 // ------------------------------------------------------------------------- copy
 // Pages are cut into equal segments of at most 16 KB, a CTA's at a time: each
 // thread has four 16-byte loads under way, eight CTAs an SM. A CTA reads the
-// page ids of all its units ahead (256 at a time), so that units without a page
-// cost no memory latency each.
+// page ids of all its units ahead (256 at a time) and keeps those that have a
+// page to copy, so that the others cost no memory latency each.
 __global__ void __launch_bounds__(kRowThreads)
     copy_pages_kernel(const int32_t* __restrict__ src, const int32_t* __restrict__ dst,
                       int32_t num_copies, uint8_t* cache, int64_t num_blocks, int64_t stride,
                       int64_t page_bytes, int32_t segments, int64_t segment_bytes,
                       int32_t* invalid_count) {
-  __shared__ int32_t from[kRowThreads], to[kRowThreads];
+  __shared__ int32_t from[kRowThreads], to[kRowThreads], part[kRowThreads];
+  __shared__ int32_t live;
   const int64_t units = static_cast<int64_t>(num_copies) * segments;
   for (int64_t u0 = blockIdx.x; u0 < units; u0 += static_cast<int64_t>(gridDim.x) * kRowThreads) {
     const int64_t mine = u0 + static_cast<int64_t>(threadIdx.x) * gridDim.x;
-    int32_t a = -1, b = -1;
+    if (threadIdx.x == 0) live = 0;
+    __syncthreads();  // also: the units before have been read
     if (mine < units) {
       const int64_t i = mine / segments;
-      a = __ldg(src + i);
-      b = __ldg(dst + i);
-      const bool skip = a == -1 || b == -1;
-      if (!skip && (a < 0 || b < 0 || a >= num_blocks || b >= num_blocks)) {
-        if (invalid_count != nullptr && mine - i * segments == 0) atomicAdd(invalid_count, 1);
-        a = -1;
+      const int32_t seg = static_cast<int32_t>(mine - i * segments);
+      const int32_t a = __ldg(src + i), b = __ldg(dst + i);
+      if (a != -1 && b != -1) {
+        if (a < 0 || b < 0 || a >= num_blocks || b >= num_blocks) {
+          if (invalid_count != nullptr && seg == 0) atomicAdd(invalid_count, 1);
+        } else if (a != b) {
+          const int at = atomicAdd(&live, 1);  // in any order: the copies are independent
+          from[at] = a;
+          to[at] = b;
+          part[at] = seg;
+        }
       }
-      if (skip || a == b) a = -1;
     }
     __syncthreads();
-    from[threadIdx.x] = a;
-    to[threadIdx.x] = b;
-    const int any = __syncthreads_count(a >= 0);
-    if (any == 0) continue;
-    for (int k = 0; k < kRowThreads; ++k) {
-      if (from[k] < 0) continue;
-      const int64_t unit = u0 + static_cast<int64_t>(k) * gridDim.x;
-      const int64_t lo = (unit % segments) * segment_bytes;
+    const int n = live;
+    for (int k = 0; k < n; ++k) {
+      const int64_t lo = part[k] * segment_bytes;
       const int64_t hi = min(lo + segment_bytes, page_bytes);
-      const uint8_t* s = cache + static_cast<int64_t>(from[k]) * stride;
-      uint8_t* d = cache + static_cast<int64_t>(to[k]) * stride;
+      const uint8_t* s = cache + from[k] * stride;
+      uint8_t* d = cache + to[k] * stride;
       for (int64_t at = lo + 16 * threadIdx.x; at < hi; at += 16 * kRowThreads * kCopyVecs) {
         uint4 v[kCopyVecs];
 #pragma unroll
@@ -570,6 +636,7 @@ __global__ void __launch_bounds__(kRowThreads)
             *reinterpret_cast<uint4*>(d + at + 16 * kRowThreads * x) = v[x];
       }
     }
+    __syncthreads();
   }
 }
 
@@ -577,21 +644,56 @@ __global__ void __launch_bounds__(kRowThreads)
 // A launch that may start while the one before it still runs, and waits for it itself.
 template <typename... Args>
 int32_t launch_after(void (*kernel)(Args...), unsigned grid, unsigned threads, cudaStream_t stream,
-                     Args... args) {
+                     unsigned cluster, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
     cudaGetLastError();
     return NVFP4_MLA_ERR_LAUNCH;
   }
   return NVFP4_MLA_OK;
+}
+
+// 16 where the device runs clusters of 16 of this kernel (with `smem` bytes of
+// shared memory a CTA), else 8; asked once a device.
+int large_cluster(const void* kernel, int device, size_t smem) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];
+  int n = device < kDevices ? known[device].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    n = kMaxCluster;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(16);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 16;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int fit = 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) ==
+            cudaSuccess &&
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg) == cudaSuccess && fit > 0)
+      n = 16;
+    cudaGetLastError();
+    if (device < kDevices) known[device].store(n, std::memory_order_relaxed);
+  }
+  return n;
 }
 
 unsigned row_grid(int64_t rows, int32_t chunks, int sms) {
@@ -650,7 +752,7 @@ extern "C" int32_t nvfp4_mla_fork(const int32_t* src_seqs, const int32_t* dst_se
   if (int32_t st = launch_status()) return st;
   if (num_forks == 0) return NVFP4_MLA_OK;
   const int32_t chunks = row_chunks(max_blocks_per_seq);
-  return launch_after(fork_share_kernel, row_grid(num_forks, chunks, sms), kRowThreads, s, p, chunks);
+  return launch_after(fork_share_kernel, row_grid(num_forks, chunks, sms), kRowThreads, s, 1, p, chunks);
 }
 
 extern "C" int32_t nvfp4_mla_release(const int32_t* keep_lens, const int32_t* seq_lens,
@@ -676,14 +778,16 @@ extern "C" int32_t nvfp4_mla_release(const int32_t* keep_lens, const int32_t* se
   // a table that 32 warps walk in one round needs no cluster
   const bool small = static_cast<int64_t>(num_seqs) * row_chunks(max_blocks_per_seq) <= kPlanWarps / 4 &&
                      page_shares_out == page_shares;
-  return launch_cluster_smem(release_kernel, p, small ? 1 : kMaxCluster, smem,
-                             kReleaseBytes * NVFP4_MLA_MAX_PLAN_SEQS + 4 * kReleaseUnits,
-                             static_cast<cudaStream_t>(stream));
+  // Its scattered accesses to the counts are what the SMs of a cluster take their
+  // time for: sixteen CTAs, where the device holds such a cluster.
+  constexpr size_t kMost = kReleaseBytes * NVFP4_MLA_MAX_PLAN_SEQS + 4 * kReleaseUnits;
+  const int ctas = small ? 1 : large_cluster(reinterpret_cast<const void*>(release_kernel), dev, kMost);
+  return launch_cluster_smem(release_kernel, p, ctas, smem, kMost, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" size_t nvfp4_mla_compact_workspace_size(int32_t num_blocks) {
   if (num_blocks < 1) return SIZE_MAX;
-  return 2 * 4 * bitmap_words(num_blocks) + 4 * static_cast<size_t>(num_blocks);
+  return (2 * 4 + sizeof(int2)) * bitmap_words(num_blocks) + 4 * static_cast<size_t>(num_blocks);
 }
 
 extern "C" int32_t nvfp4_mla_compact(const int32_t* seq_lens, int32_t num_seqs,
@@ -715,16 +819,19 @@ extern "C" int32_t nvfp4_mla_compact(const int32_t* seq_lens, int32_t num_seqs,
                            free_capacity,  free_count,      max_moves,      block_table_out,
                            page_shares_out, free_pages_out, free_count_out, copy_src,
                            copy_dst,       pages_end,       used,           used + words,
-                           reinterpret_cast<int32_t*>(used + 2 * words), static_cast<int32_t>(words)};
+                           reinterpret_cast<int32_t*>(used + 4 * words),
+                           reinterpret_cast<int2*>(used + 2 * words), static_cast<int32_t>(words)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t clearing = (static_cast<int64_t>(num_blocks) + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
   compact_clear_kernel<<<static_cast<unsigned>(clearing < sms ? clearing : sms), kPlanThreads, 0, s>>>(p);
   if (int32_t st = launch_status()) return st;
   const int32_t chunks = row_chunks(max_blocks_per_seq);
   const unsigned grid = row_grid(num_seqs, chunks, sms);
-  if (int32_t st = launch_after(compact_mark_kernel, grid, kRowThreads, s, p, chunks)) return st;
-  if (int32_t st = launch_after(compact_rank_kernel, 1, kPlanThreads, s, p)) return st;
-  return launch_after(compact_table_kernel, grid, kRowThreads, s, p, chunks);
+  if (int32_t st = launch_after(compact_mark_kernel, grid, kRowThreads, s, 1, p, chunks)) return st;
+  // a CTA for each 32 warps' words, as far as a cluster goes
+  const unsigned ranks = words <= kPlanWarps ? 1 : kMaxCluster;
+  if (int32_t st = launch_after(compact_rank_kernel, ranks, kPlanThreads, s, ranks, p)) return st;
+  return launch_after(compact_table_kernel, grid, kRowThreads, s, 1, p, chunks);
 }
 
 extern "C" int32_t nvfp4_mla_copy_pages(const int32_t* copy_src, const int32_t* copy_dst,

@@ -86,7 +86,7 @@ def test_sizes_and_nothing_to_copy(lib):
     assert _copy(lib, n=0, copy_src=None) == 0
     size = lib.nvfp4_mla_compact_workspace_size
     assert size(0) == size(-1) == (1 << 64) - 1
-    assert size(1) == 32 + 4 and size(1000) == 2 * 128 + 4000
+    assert 36 <= size(1) <= 128 and 2 * 128 + 4000 <= size(1000) <= 8000
     assert size(2 ** 31 - 1) > 2 ** 33
 
 
