@@ -72,9 +72,12 @@ constexpr float kTau = 15.f, kHeadroom = 2.f;
 // score tile before P V can begin, writing O), and the least share of a cluster.
 constexpr int kTileOverhead = 3, kLeastShare = 6;
 
-struct RowTile {       // 256 rows of a sequence
-  int32_t seq, index;  // of the sequence's row tiles
-  int64_t unit;        // first unit: kTileOverhead units, then one a key tile
+struct alignas(16) RowTile {  // 256 rows of a sequence
+  int32_t seq, rows;     // its rows, 1 .. 256
+  int32_t base, len;     // tokens before the new ones; length
+  int64_t unit, end;     // its units: kTileOverhead, then one a key tile
+  int64_t row0;          // its first row of all
+  int32_t offset, pad;   // and of the sequence's
 };
 struct Plan {
   int64_t units, share;  // of all row tiles, of a cluster
@@ -101,7 +104,7 @@ struct ChunkParams {
   int32_t* invalid_count;
   // workspace
   Plan* plan;
-  RowTile* tiles;     // [max_tiles + 1]
+  RowTile* tiles;     // [max_tiles]
   int32_t* first;     // [clusters] the row tile of a cluster's first unit
   int32_t* failed;    // [clusters]
   float* part_lse;    // [2 clusters][rows]
@@ -144,7 +147,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   for (int t0 = 0; t0 < n_tiles; t0 += kPlanThreads) {
     const int t = t0 + tid;
     int64_t n = 0;
-    int s = 0, index = 0;
+    int s = 0;
+    RowTile tile = {};
     if (t < n_tiles) {
       int hi = p.num_seqs - 1;
       while (s < hi) {
@@ -152,15 +156,21 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
         if (upto[mid] <= t) s = mid + 1;
         else hi = mid;
       }
-      index = t - (s > 0 ? upto[s - 1] : 0);
+      const int64_t offset = static_cast<int64_t>(t - (s > 0 ? upto[s - 1] : 0)) * kTileRows;
       int32_t start, len;
       const int32_t tokens = new_tokens(p, s, start, len);
-      const int64_t last = min((static_cast<int64_t>(index) * kTileRows + kTileRows - 1) / p.num_heads,
-                               static_cast<int64_t>(tokens - 1));
-      n = kTileOverhead + (len - tokens + last + kTileKeys) / kTileKeys;  // sees len - tokens + last + 1
+      const int64_t rows = min(static_cast<int64_t>(tokens) * p.num_heads - offset, int64_t{kTileRows});
+      const int64_t last = (offset + rows - 1) / p.num_heads;  // token: it sees len - tokens + last + 1 keys
+      n = kTileOverhead + (len - tokens + last + kTileKeys) / kTileKeys;
+      tile = {s, static_cast<int32_t>(rows), len - tokens, len, 0, 0,
+              static_cast<int64_t>(start) * p.num_heads + offset, static_cast<int32_t>(offset), 0};
     }
     const int64_t to = block_scan(n, units, sums);
-    if (t < n_tiles) p.tiles[t] = {s, index, to - n};
+    if (t < n_tiles) {
+      tile.unit = to - n;
+      tile.end = to;
+      p.tiles[t] = tile;
+    }
   }
   const int64_t share = max((units + p.clusters - 1) / p.clusters, int64_t{kLeastShare});
   for (int c = tid; c < p.clusters; c += kPlanThreads) {
@@ -168,12 +178,11 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
     p.failed[c] = 0;
   }
   if (tid == 0) {
-    p.tiles[n_tiles] = {-1, 0, units};
     *p.plan = {units, share, n_tiles, 0};
   }
   __syncthreads();
   for (int t = tid; t < n_tiles; t += kPlanThreads) {
-    const int64_t a = p.tiles[t].unit, b = p.tiles[t + 1].unit;
+    const int64_t a = p.tiles[t].unit, b = p.tiles[t].end;
     for (int64_t c = (a + share - 1) / share; c * share < b; ++c) p.first[c] = t;
   }
 }
@@ -197,48 +206,37 @@ __global__ void __launch_bounds__(256) chunk_check_kernel(const ChunkParams p) {
   if (bad > 0) atomicAdd(p.invalid_count, bad);
 }
 
-// The pieces of row tiles that make up a cluster's share, one after the other.
+// The pieces of row tiles that make up a cluster's share, one after the other. The
+// plan is read through L1: the warps of a CTA follow one another through it.
 struct Pieces {
   const ChunkParams& p;
   int64_t u0, u1;     // the cluster's units
   int32_t t, tiles;   // the next row tile
   int32_t cluster;
   // the current piece
-  int32_t seq, rows, base, len;  // rows of the tile; tokens before the new ones; length
-  int64_t row0, first_row;       // first row of the tile, of the sequence's first token
-  int32_t begin, end;            // key tiles
-  bool whole;                    // all that the row tile sees
-  int32_t slot;                  // of a partial result
+  RowTile tile;
+  int32_t begin, end;  // key tiles
+  bool whole;          // all that the row tile sees
+  int32_t slot;        // of a partial result
 
   __device__ Pieces(const ChunkParams& params, int c) : p(params), cluster(c) {
-    const int64_t units = __ldcg(&p.plan->units), share = __ldcg(&p.plan->share);
+    const int64_t units = p.plan->units, share = p.plan->share;
     u0 = c * share;
     u1 = min(u0 + share, units);
-    tiles = __ldcg(&p.plan->tiles);
-    t = u0 < units ? __ldcg(p.first + c) : tiles;
+    tiles = p.plan->tiles;
+    t = u0 < units ? p.first[c] : tiles;
   }
   __device__ __forceinline__ bool next() {
     while (t < tiles) {
-      const int4 x = __ldcg(reinterpret_cast<const int4*>(p.tiles + t));
-      const int4 y = __ldcg(reinterpret_cast<const int4*>(p.tiles + t + 1));
-      const int64_t a = static_cast<int64_t>(static_cast<uint32_t>(x.z)) | (static_cast<int64_t>(x.w) << 32);
-      const int64_t b = static_cast<int64_t>(static_cast<uint32_t>(y.z)) | (static_cast<int64_t>(y.w) << 32);
-      if (a >= u1) break;
+      tile = p.tiles[t];
+      if (tile.unit >= u1) break;
       ++t;
-      const int64_t k0 = a + kTileOverhead;  // unit of key tile 0
+      const int64_t k0 = tile.unit + kTileOverhead;  // unit of key tile 0
       begin = static_cast<int32_t>(max(u0 - k0, int64_t{0}));
-      end = static_cast<int32_t>(max(min(u1, b) - k0, int64_t{0}));
+      end = static_cast<int32_t>(max(min(u1, tile.end) - k0, int64_t{0}));
       if (end <= begin) continue;
-      whole = begin == 0 && end == b - k0;
-      slot = 2 * cluster + (a >= u0 ? 1 : 0);
-      seq = x.x;
-      int32_t start;
-      const int32_t n = new_tokens(p, seq, start, len);
-      base = len - n;
-      first_row = static_cast<int64_t>(start) * p.num_heads;
-      row0 = first_row + static_cast<int64_t>(x.y) * (kTileRows);
-      rows = static_cast<int32_t>(
-          min(static_cast<int64_t>(n) * p.num_heads - (row0 - first_row), int64_t{kTileRows}));
+      whole = begin == 0 && end == tile.end - k0;
+      slot = 2 * cluster + (tile.unit >= u0 ? 1 : 0);
       return true;
     }
     return false;
@@ -365,16 +363,34 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+__device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
 __device__ __forceinline__ uint32_t hmin2(uint32_t a, uint32_t b) {  // of a NaN and a number: the number
   uint32_t r;
   asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ uint4 to_f16x8(uint4 x, float m) {  // 8 bf16 values times m
-  return make_uint4(pack_f16x2(bf16_lo(x.x) * m, bf16_hi(x.x) * m),
-                    pack_f16x2(bf16_lo(x.y) * m, bf16_hi(x.y) * m),
-                    pack_f16x2(bf16_lo(x.z) * m, bf16_hi(x.z) * m),
-                    pack_f16x2(bf16_lo(x.w) * m, bf16_hi(x.w) * m));
+__device__ __forceinline__ uint32_t to_f16x2(uint32_t x, float m) {  // 2 bf16 values times m
+  return pack_f16x2(bf16_lo(x) * m, bf16_hi(x) * m);
+}
+__device__ __forceinline__ uint4 to_f16x8(uint4 x, float m) {
+  return make_uint4(to_f16x2(x.x, m), to_f16x2(x.y, m), to_f16x2(x.z, m), to_f16x2(x.w, m));
+}
+__device__ __forceinline__ void ld_32_bytes(const void* p, uint32_t (&v)[8]) {  // 16-byte aligned
+  const uint4 a = ld_nc_v4(p), b = ld_nc_v4(static_cast<const uint8_t*>(p) + 16);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+// Sixteen lanes of tensor memory, 32 columns: of a thread, registers 4 j + {0, 1}
+// are columns 8 j + 2 (lane % 4) + {0, 1} of row lane / 4, and 4 j + {2, 3} of row lane / 4 + 8.
+__device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 
 // ------------------------------------------------------------------ memory plan
@@ -432,11 +448,12 @@ static_assert(ChunkCtl::kMissing + 32 * ChunkCtl::kMissingTiles == ChunkLayout<0
 // Warp w of the eight expands keys 8 w .. 8 w + 7 of each 64, kItems 16-byte
 // pieces of their rows a lane:
 //   NVFP4 rows: 32 codes (64 bytes of FP16) and their two scales; a lane has two
-//     keys, (lane / 2) % 4 and that + 4; rope: key lane / 4, bytes 16 (lane % 4);
+//     keys, 2 ((lane / 2) % 4) and the next; rope: key lane / 4, bytes 16 (lane % 4);
 //   FP8 rows: 16 values of key lane / 4.
-// Both ways the eight lanes of a load's or a store's phase touch eight different
-// 16-byte columns of shared memory. A CTA of the output pair (kHalves) expands
-// dimensions 128 part .. + 127 of each half of the 512.
+// The eight lanes of a store's phase touch eight different 16-byte columns of
+// shared memory. A CTA of the output pair (kHalves) expands dimensions 128 part ..
+// + 127 of each half of the 512. Latent blocks of a score CTA (kKeys) are in the
+// order in which Q is stored: dimensions 16 q + 4 j + e of 64 at 16 j + 4 q + e.
 template <int kFmt, int kItems, bool kRopeToo, bool kHalves>
 struct RowItems {
   static constexpr bool kNv = kFmt == NVFP4_MLA_ROW_NVFP4_352;
@@ -450,11 +467,11 @@ struct RowItems {
     if constexpr (kNv) {
       const uint32_t c = (lane & 1) + 2 * (lane >> 3);  // of 32 dimensions
       const uint32_t code = kHalves ? 128 * (c >> 2) + 64 * part + 16 * (c & 3) : 16 * c;
-      const uint32_t key = raw + (8 * w + ((lane >> 1) & 3)) * kRow;
+      const uint32_t key = raw + (8 * w + 2 * ((lane >> 1) & 3)) * kRow;
 #pragma unroll
       for (int i = 0; i < kItems; ++i) {
-        lat[i] = ld_shared_v4(key + code + (i & 1) * 4 * kRow + (i >> 1) * 128);
-        scale[i] = ld_shared_u16(key + kScaleOff + code / 8 + (i & 1) * 4 * kRow + (i >> 1) * 16);
+        lat[i] = ld_shared_v4(key + code + (i & 1) * kRow + (i >> 1) * 128);
+        scale[i] = ld_shared_u16(key + kScaleOff + code / 8 + (i & 1) * kRow + (i >> 1) * 16);
       }
       if constexpr (kRopeToo)
         rope = ld_shared_v4(raw + (8 * w + (lane >> 2)) * kRow + kRopeOff + 16 * (lane & 3));
@@ -467,7 +484,9 @@ struct RowItems {
     }
   }
 
-  __device__ static __forceinline__ void store_e4m3(uint4 v, uint32_t block, uint32_t key, uint32_t col,
+  // 16 values of a key, column pair `pair` (0 .. 3) of a block; kOrder: in Q's order
+  template <bool kOrder>
+  __device__ static __forceinline__ void store_e4m3(uint4 v, uint32_t block, uint32_t key, uint32_t pair,
                                                     bool numbers) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t h[8];
@@ -480,32 +499,45 @@ struct RowItems {
 #pragma unroll
       for (int q = 0; q < 8; ++q) h[q] = hmin2(h[q], 0x5F005F00u);  // 448
     }
-    st_shared_v4(block + swizzled(key, col), h[0], h[1], h[2], h[3]);
-    st_shared_v4(block + swizzled(key, col + 1), h[4], h[5], h[6], h[7]);
+    if constexpr (kOrder) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        st_shared_v2(block + swizzled(key, 2 * j + (pair >> 1)) + 8 * (pair & 1), h[2 * j], h[2 * j + 1]);
+    } else {
+      st_shared_v4(block + swizzled(key, 2 * pair), h[0], h[1], h[2], h[3]);
+      st_shared_v4(block + swizzled(key, 2 * pair + 1), h[4], h[5], h[6], h[7]);
+    }
   }
-  // Into blocks of 64 keys x 64 dimensions from `dst` on. kNumbers (values): a NaN
+  // Into blocks of 64 keys x 64 dimensions from `dst` on. As a value (not kKeys) a NaN
   // becomes a number. A row's scores are NaN for every token that sees it then; the
   // others weigh it with 0, which a NaN would not survive. The same holds for what
   // lies in the place of a key that does not exist.
-  template <bool kNumbers>
+  template <bool kKeys>
   __device__ __forceinline__ void store(uint32_t dst, int w, int lane) const {
     if constexpr (kNv) {
 #pragma unroll
       for (int i = 0; i < kItems; ++i) {
-        const uint32_t key = 8u * w + ((lane >> 1) & 3) + 4u * (i & 1);
+        const uint32_t key = 8u * w + 2 * ((lane >> 1) & 3) + (i & 1);
         const uint32_t c = (lane & 1) + 2 * (lane >> 3) + 8 * (i >> 1);
         uint32_t s = e4m3x2_to_f16x2(static_cast<uint16_t>(scale[i]));
-        if (kNumbers) s = hmin2(s, 0x5F005F00u);
+        if (!kKeys) s = hmin2(s, 0x5F005F00u);
         const uint32_t s0 = __byte_perm(s, s, 0x1010), s1 = __byte_perm(s, s, 0x3232);
         const uint32_t words[4] = {lat[i].x, lat[i].y, lat[i].z, lat[i].w};
         const uint32_t block = dst + (c >> 1) * kKBlock;
+        uint32_t f[4][4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          uint32_t f[4];
-          e2m1x8_to_f16x8(words[x], f);
+          e2m1x8_to_f16x8(words[x], f[x]);
 #pragma unroll
-          for (int y = 0; y < 4; ++y) f[y] = hmul2_u32(f[y], x < 2 ? s0 : s1);
-          st_shared_v4(block + swizzled(key, (c & 1) * 4 + x), f[0], f[1], f[2], f[3]);
+          for (int y = 0; y < 4; ++y) f[x][y] = hmul2_u32(f[x][y], x < 2 ? s0 : s1);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          if (kKeys)
+            st_shared_v4(block + swizzled(key, 2 * x + (c & 1)), f[x >> 1][2 * (x & 1)], f[x >> 1][2 * (x & 1) + 1],
+                         f[2 + (x >> 1)][2 * (x & 1)], f[2 + (x >> 1)][2 * (x & 1) + 1]);
+          else
+            st_shared_v4(block + swizzled(key, (c & 1) * 4 + x), f[x][0], f[x][1], f[x][2], f[x][3]);
         }
       }
     } else {
@@ -513,10 +545,10 @@ struct RowItems {
 #pragma unroll
       for (int i = 0; i < kItems; ++i) {
         const uint32_t c = 4 * i + (lane & 3);
-        store_e4m3(lat[i], dst + (c >> 2) * kKBlock, key, 2 * (c & 3), kNumbers);
+        store_e4m3<kKeys>(lat[i], dst + (c >> 2) * kKBlock, key, c & 3, !kKeys);
       }
     }
-    if constexpr (kRopeToo) store_e4m3(rope, dst + 8 * kKBlock, 8u * w + (lane >> 2), 2 * (lane & 3), false);
+    if constexpr (kRopeToo) store_e4m3<false>(rope, dst + 8 * kKBlock, 8u * w + (lane >> 2), lane & 3, false);
   }
 };
 
@@ -594,11 +626,11 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
       bool run = true;
       Pieces pieces(p, cluster);
       while (run && pieces.next()) {
-        const int32_t* table = p.block_table + static_cast<int64_t>(pieces.seq) * p.max_blocks;
+        const int32_t* table = p.block_table + static_cast<int64_t>(pieces.tile.seq) * p.max_blocks;
         const int32_t step = scoring ? kTileKeys : kPieceKeys;
         const int32_t stop = pieces.end * kTileKeys;
         int32_t key = pieces.begin * kTileKeys + (scoring ? kPieceKeys * static_cast<int32_t>(part) : 0);
-        auto page_of = [&](int32_t k) { return k < pieces.len && k < stop ? __ldg(table + p.page.block(k)) : -1; };
+        auto page_of = [&](int32_t k) { return k < pieces.tile.len && k < stop ? __ldg(table + p.page.block(k)) : -1; };
         int32_t page = runs ? page_of(key) : 0;
         for (; key < stop; key += step, ++u) {
           const uint32_t s = u % raws;
@@ -613,7 +645,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
           int64_t off[2];
           if (runs) {
             const bool ok = page >= 0 && page < p.num_blocks;
-            const int32_t left = pieces.len - key;
+            const int32_t left = pieces.tile.len - key;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               have[x] = ok ? 0xffffffffu : 0u;
@@ -625,7 +657,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               const int32_t k = key + 32 * x + lane;
-              const bool some = k < pieces.len;
+              const bool some = k < pieces.tile.len;
               const int32_t b = some ? p.page.block(k) : 0;
               const int32_t id = some ? __ldg(table + b) : -1;
               const bool ok = id >= 0 && id < p.num_blocks;
@@ -826,7 +858,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
           if (lane == 0) mbar_arrive(bar(C::kRawEmpty, s));
           run = u < 2 || warp_wait(bar(C::kSFull, u & 1), ((u >> 1) & 1) ^ 1, abort_addr, lim);
           if (!run) break;
-          items.template store<false>(sbase + L::kK + (u & 1) * kKTileBytes, w, lane);
+          items.template store<true>(sbase + L::kK + (u & 1) * kKTileBytes, w, lane);
           fence_proxy_async_cta();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(C::kKFull, u & 1));
@@ -849,7 +881,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
           run = u < L::kVSlots ||
                 warp_wait<true>(bar(C::kPvDone, v % L::kPSlots), (v / L::kPSlots) & 1, abort_addr, lim);
           if (!run) break;
-          items.template store<true>(sbase + L::kV + vs * kVSlotBytes, w, lane);
+          items.template store<false>(sbase + L::kV + vs * kVSlotBytes, w, lane);
           fence_proxy_async_cta();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(C::kVFull, vs));
@@ -875,35 +907,57 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
       uint32_t i0 = 0;  // tiles before
       for (uint32_t item = 0; ok && pieces.next(); ++item) {
         const uint32_t n = static_cast<uint32_t>(pieces.end - pieces.begin) * 2;
-        // the MMAs that read the Q before are done
-        if (i0 > 0) ok = warp_wait(bar(C::kSFull, (i0 - 1) & 1), ((i0 - 1) >> 1) & 1, abort_addr, lim);
-        if (!ok) break;
-        tc_fence_after();
-        {  // each group writes a third of Q's nine blocks of 64 dimensions
-          const bool mine = row < pieces.rows;
-          const uint4* ql = reinterpret_cast<const uint4*>(p.q_lat + (pieces.row0 + row) * kLatent);
-          const uint4* qr = reinterpret_cast<const uint4*>(p.q_rope + (pieces.row0 + row) * kRope);
-          const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll 1
-          for (uint32_t x = group; x < 8; x += kGroups) {
-            uint4 v[8];
+        {
+          // Each group loads a third of Q's nine blocks of 64 dimensions. A warp has 32
+          // rows; a lane loads 16 dimensions (32 bytes) of rows lane / 4 + 8 y, so that a
+          // load takes whole lines, and stores them as the 16 x 256 bit shape has them:
+          // dimensions 16 q + 4 j + e of a block (q = lane % 4) become 16 j + 4 q + e, which
+          // is the order that the keys are expanded to.
+          const uint32_t rows = pieces.tile.rows, r0 = 128 * part + 32 * quad + (lane >> 2);
+          const uint16_t* ql = p.q_lat + (pieces.tile.row0 + r0) * kLatent + 16 * (lane & 3);
+          const uint16_t* qr = p.q_rope + (pieces.tile.row0 + row) * kRope;
+          auto load = [&](uint32_t block, uint32_t (&v)[4][8]) {
 #pragma unroll
-            for (int y = 0; y < 8; ++y) v[y] = mine ? __ldg(ql + 8 * x + y) : z;
-            uint32_t h[32];
+            for (int y = 0; y < 4; ++y) {
 #pragma unroll
-            for (int y = 0; y < 8; ++y) {
-              const uint4 f = to_f16x8(v[y], p.lat_mult);
-              h[4 * y] = f.x, h[4 * y + 1] = f.y, h[4 * y + 2] = f.z, h[4 * y + 3] = f.w;
+              for (int z = 0; z < 8; ++z) v[y][z] = 0u;
+              if (block < 8 && r0 + 8 * y < rows) ld_32_bytes(ql + 8 * y * kLatent + 64 * block, v[y]);
             }
-            tmem_st32(tmem + lane_base + 32u * x, h);
-          }
+          };
+          auto store = [&](uint32_t block, const uint32_t (&v)[4][8]) {
+            if (block >= 8) return;
+#pragma unroll
+            for (int y = 0; y < 4; y += 2) {
+              uint32_t h[16];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  h[4 * j + z] = to_f16x2(v[y][2 * j + z], p.lat_mult);
+                  h[4 * j + 2 + z] = to_f16x2(v[y + 1][2 * j + z], p.lat_mult);
+                }
+              tmem_st_16x256b_x4(tmem + ((32 * quad + 8 * y) << 16) + 32u * block, h);
+            }
+          };
+          uint32_t first[4][8], second[4][8];
+          load(group, first);
+          load(group + kGroups, second);
+          // the MMAs that read the Q before are done
+          if (i0 > 0) ok = warp_wait(bar(C::kSFull, (i0 - 1) & 1), ((i0 - 1) >> 1) & 1, abort_addr, lim);
+          if (!ok) break;
+          tc_fence_after();
+          store(group, first);
+          load(group + 2 * kGroups, first);
+          store(group + kGroups, second);
           if (group == kGroups - 1) {
 #pragma unroll
             for (int y = 0; y < 8; ++y) {
-              const uint4 f = to_f16x8(mine ? __ldg(qr + y) : z, p.rope_mult);
+              uint4 f = make_uint4(0u, 0u, 0u, 0u);
+              if (row < pieces.tile.rows) f = to_f16x8(__ldg(reinterpret_cast<const uint4*>(qr) + y), p.rope_mult);
               st_shared_v4(sbase + L::kQRope + swizzled(t, y), f.x, f.y, f.z, f.w);
             }
           }
+          store(group + 2 * kGroups, first);
           tmem_st_wait();
           tc_fence_before();
           fence_proxy_async_cta();
@@ -911,9 +965,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
           if (lane == 0) mbar_arrive(bar(C::kQFull, 0));
         }
         // keys that the row sees
-        const int32_t sees = pieces.base + 1 +
-                             static_cast<int32_t>((pieces.row0 - pieces.first_row + min(row, pieces.rows - 1)) /
-                                                  p.num_heads);
+        const int32_t sees =
+            pieces.tile.base + 1 + (pieces.tile.offset + min(row, pieces.tile.rows - 1)) / p.num_heads;
         float m = -INFINITY, l = 0.f;  // the reference that l is relative to
         for (uint32_t x = (group + kGroups - 2 * i0 % kGroups) % kGroups; x < n; x += kGroups) {
           const uint32_t u = 2 * i0 + x, i = u >> 1, b = i & 1, half = u & 1, st = u % L::kStages;
@@ -1039,10 +1092,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
           fence_proxy_async_cta();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(C::kStaged, st));
-          if (last && row < pieces.rows) {
+          if (last && row < pieces.tile.rows) {
             const float lse = l == 0.f ? -INFINITY : (m + lg2(l)) * kLn2;
             if (!pieces.whole) p.part_lse[static_cast<int64_t>(pieces.slot) * kTileRows + row] = lse;
-            else if (p.lse != nullptr) p.lse[pieces.row0 + row] = lse;
+            else if (p.lse != nullptr) p.lse[pieces.tile.row0 + row] = lse;
           }
         }
         if (!ok) break;
@@ -1089,12 +1142,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
             if (!ok) break;
             tc_fence_after();
             const float fin = __uint_as_float(ld_shared_u32(sbase + L::kFinal + 512 * (item % L::kNotes) + 4 * t));
-            const bool mine = row < pieces.rows;
+            const bool mine = row < pieces.tile.rows;
             const bool f32 = !pieces.whole || p.out_fp32;
             float* wide = pieces.whole
-                              ? static_cast<float*>(p.out) + (pieces.row0 + row) * kLatent
+                              ? static_cast<float*>(p.out) + (pieces.tile.row0 + row) * kLatent
                               : p.part_out + (static_cast<int64_t>(pieces.slot) * kTileRows + row) * kLatent;
-            uint16_t* narrow = static_cast<uint16_t*>(p.out) + (pieces.row0 + row) * kLatent;
+            uint16_t* narrow = static_cast<uint16_t*>(p.out) + (pieces.tile.row0 + row) * kLatent;
 #pragma unroll 1
             for (uint32_t y = group; y < 16; y += kGroups) {
               uint32_t r[32];
@@ -1185,12 +1238,8 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkParams p) {
     const int t = __ldcg(p.first + c);  // whose units reach to c's first one, or begin there
     // first[c] is the last row tile that begins at or before `at`
     const RowTile tile = p.tiles[t];
-    const int64_t a = tile.unit, b = p.tiles[t + 1].unit;
-    if (a == at || a < at - share) continue;  // not cut here, or before
-    int32_t start, len;
-    const int64_t n = static_cast<int64_t>(new_tokens(p, tile.seq, start, len)) * p.num_heads;
-    const int64_t first_row = static_cast<int64_t>(tile.index) * kTileRows;
-    if (row >= n - first_row) continue;
+    const int64_t a = tile.unit, b = tile.end;
+    if (a == at || a < at - share || row >= tile.rows) continue;  // not cut here, or before
     const int64_t k0 = a + kTileOverhead;
     const int c1 = static_cast<int>((b - 1) / share);
     // the parts: cluster c - 1 to c1, those that have key tiles
@@ -1231,7 +1280,7 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkParams p) {
       }
     }
     const float inv = nan ? NAN : tot > 0.f ? 1.f / tot : 0.f;
-    const int64_t to = static_cast<int64_t>(start) * p.num_heads + first_row + row;
+    const int64_t to = tile.row0 + row;
 #pragma unroll
     for (int y = 0; y < 4; ++y) {
       const float v0 = acc[4 * y] * inv, v1 = acc[4 * y + 1] * inv, v2 = acc[4 * y + 2] * inv,
@@ -1259,14 +1308,14 @@ ChunkSpace chunk_space(int32_t num_q, int32_t num_heads, int32_t num_seqs) {
       static_cast<int64_t>(num_q) * num_heads / kTileRows + (num_seqs < num_q ? num_seqs : num_q);
   s.max_tiles = static_cast<int32_t>(tiles);
   s.tiles = 64;
-  s.first = s.tiles + sizeof(RowTile) * static_cast<size_t>(tiles + 1);
+  s.first = s.tiles + sizeof(RowTile) * static_cast<size_t>(tiles);
   s.failed = s.first + 4 * kMaxClusters;
   s.lse = s.failed + 4 * kMaxClusters;
   s.out = s.lse + 4 * 2 * kMaxClusters * kTileRows;
   s.bytes = s.out + size_t{4} * 2 * kMaxClusters * kTileRows * kLatent;
   return s;
 }
-static_assert(sizeof(RowTile) == 16 && sizeof(Plan) <= 64 && (4 * kMaxClusters) % 16 == 0, "workspace");
+static_assert(sizeof(RowTile) == 48 && sizeof(Plan) <= 64 && (4 * kMaxClusters) % 16 == 0, "workspace");
 
 bool chunk_shape_ok(int32_t num_q, int32_t num_heads, int32_t num_seqs) {
   return num_q >= 0 && num_heads >= 1 && num_heads <= NVFP4_MLA_MAX_HEADS && num_seqs >= 1 &&
