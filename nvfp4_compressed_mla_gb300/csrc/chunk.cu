@@ -382,6 +382,13 @@ __device__ __forceinline__ void ld_32_bytes(const void* p, uint32_t (&v)[8]) {  
   v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
   v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
+// The same lanes' 64 columns the other way.
+__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 " NVFP4_TMEM_REGS ", [%32];"
+               : NVFP4_TMEM_OUTS(r)
+               : "r"(taddr)
+               : "memory");
+}
 // Sixteen lanes of tensor memory, 32 columns: of a thread, registers 4 j + {0, 1}
 // are columns 8 j + 2 (lane % 4) + {0, 1} of row lane / 4, and 4 j + {2, 3} of row lane / 4 + 8.
 __device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -445,110 +452,153 @@ struct ChunkCtl {  // barriers and words, at the same offsets in every CTA of th
 static_assert(ChunkCtl::kMissing + 32 * ChunkCtl::kMissingTiles == ChunkLayout<0>::kCtlBytes, "control block");
 
 // ------------------------------------------------------------------ expansion
-// Warp w of the eight expands keys 8 w .. 8 w + 7 of each 64, kItems 16-byte
-// pieces of their rows a lane:
-//   NVFP4 rows: 32 codes (64 bytes of FP16) and their two scales; a lane has two
-//     keys, 2 ((lane / 2) % 4) and the next; rope: key lane / 4, bytes 16 (lane % 4);
-//   FP8 rows: 16 values of key lane / 4.
-// The eight lanes of a store's phase touch eight different 16-byte columns of
-// shared memory. A CTA of the output pair (kHalves) expands dimensions 128 part ..
-// + 127 of each half of the 512. Latent blocks of a score CTA (kKeys) are in the
-// order in which Q is stored: dimensions 16 q + 4 j + e of 64 at 16 j + 4 q + e.
-template <int kFmt, int kItems, bool kRopeToo, bool kHalves>
+// Warp w of the eight expands keys 8 w .. 8 w + 7 of each 64: a lane key lane % 8
+// and, of its latent part, kBlocks blocks of 64 dimensions; of its rope part 16
+// values of key lane / 4. The eight lanes of a store's phase have different keys,
+// so they touch different 16-byte columns of shared memory.
+//
+// What the matrix products call a dimension need not be the row's. Within each
+// block of 64 the order is such that what a thread loads, or writes, of Q and O
+// through the 16 x 256 bit shape of tensor memory is contiguous in global memory
+// (q = 0 .. 3 is lane % 4 there):
+//   keys (and Q): dimension 16 q + 4 j + e is at 16 j + 4 q + e  (j, e = 0 .. 3)
+//   values (and O): dimension 16 q + 2 j + e is at 8 j + 2 q + e  (j = 0 .. 7, e = 0, 1)
+// A score CTA expands all 512 dimensions of its keys, a CTA of the output pair
+// dimensions 128 part .. + 127 of each half.
+template <int kFmt, bool kKeys>
 struct RowItems {
   static constexpr bool kNv = kFmt == NVFP4_MLA_ROW_NVFP4_352;
   static constexpr uint32_t kRow = kNv ? kNvfp4Row : kFp8Row;
-  uint4 lat[kItems];
-  uint32_t scale[kNv ? kItems : 1];
+  static constexpr int kBlocks = kKeys ? 2 : 1, kVecs = kNv ? 2 : 4;  // 16 bytes each of a block
+  uint4 lat[kBlocks][kVecs];
+  uint32_t scale[kBlocks];
   uint4 rope;
 
   // From the rows at `raw` (of 64 keys).
   __device__ __forceinline__ void load(uint32_t raw, int w, int lane, uint32_t part) {
-    if constexpr (kNv) {
-      const uint32_t c = (lane & 1) + 2 * (lane >> 3);  // of 32 dimensions
-      const uint32_t code = kHalves ? 128 * (c >> 2) + 64 * part + 16 * (c & 3) : 16 * c;
-      const uint32_t key = raw + (8 * w + 2 * ((lane >> 1) & 3)) * kRow;
+    const uint32_t key = raw + (8 * w + (lane & 7)) * kRow;
 #pragma unroll
-      for (int i = 0; i < kItems; ++i) {
-        lat[i] = ld_shared_v4(key + code + (i & 1) * kRow + (i >> 1) * 128);
-        scale[i] = ld_shared_u16(key + kScaleOff + code / 8 + (i & 1) * kRow + (i >> 1) * 16);
-      }
-      if constexpr (kRopeToo)
-        rope = ld_shared_v4(raw + (8 * w + (lane >> 2)) * kRow + kRopeOff + 16 * (lane & 3));
-    } else {
-      const uint32_t key = raw + (8 * w + (lane >> 2)) * kRow + 16 * (lane & 3);
+    for (int i = 0; i < kBlocks; ++i) {
+      const uint32_t b = (lane >> 3) + 4 * i;
+      const uint32_t dim = kKeys ? 64 * b : 256 * (b >> 1) + 128 * part + 64 * (b & 1);
 #pragma unroll
-      for (int i = 0; i < kItems; ++i)
-        lat[i] = ld_shared_v4(key + (kHalves ? 128 * part + 256 * (i >> 1) + 64 * (i & 1) : 64u * i));
-      if constexpr (kRopeToo) rope = ld_shared_v4(key + kLatent);
+      for (int v = 0; v < kVecs; ++v) lat[i][v] = ld_shared_v4(key + (kNv ? dim / 2 : dim) + 16 * v);
+      if constexpr (kNv) scale[i] = ld_shared_u32(key + kScaleOff + dim / 16);
     }
+    if constexpr (kKeys)
+      rope = ld_shared_v4(raw + (8 * w + (lane >> 2)) * kRow + (kNv ? kRopeOff : kLatent) + 16 * (lane & 3));
   }
 
-  // 16 values of a key, column pair `pair` (0 .. 3) of a block; kOrder: in Q's order
-  template <bool kOrder>
-  __device__ static __forceinline__ void store_e4m3(uint4 v, uint32_t block, uint32_t key, uint32_t pair,
-                                                    bool numbers) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t h[8];
+  // Into blocks of 64 keys x 64 dimensions from `dst` on. As a value a NaN becomes a
+  // number: a row's scores are NaN for every token that sees it then, and the others
+  // weigh it with 0, which a NaN would not survive. The same holds for what lies in
+  // the place of a key that does not exist.
+  __device__ __forceinline__ void store(uint32_t dst, int w, int lane) const {
+    const uint32_t key = 8u * w + (lane & 7);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      h[2 * q] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[q] & 0xFFFFu));
-      h[2 * q + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[q] >> 16));
+    for (int i = 0; i < kBlocks; ++i) {
+      const uint32_t block = dst + ((lane >> 3) + 4 * i) * kKBlock;
+      auto put = [&](uint32_t col, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+        st_shared_v4(block + swizzled(key, col), a, b, c, d);
+      };
+      if constexpr (kNv) {
+        uint32_t s01 = e4m3x2_to_f16x2(static_cast<uint16_t>(scale[i] & 0xFFFFu));
+        uint32_t s23 = e4m3x2_to_f16x2(static_cast<uint16_t>(scale[i] >> 16));
+        if (!kKeys) {
+          s01 = hmin2(s01, 0x5F005F00u);  // 448
+          s23 = hmin2(s23, 0x5F005F00u);
+        }
+        const uint32_t s[4] = {__byte_perm(s01, s01, 0x1010), __byte_perm(s01, s01, 0x3232),
+                               __byte_perm(s23, s23, 0x1010), __byte_perm(s23, s23, 0x3232)};
+        const uint32_t words[8] = {lat[i][0].x, lat[i][0].y, lat[i][0].z, lat[i][0].w,
+                                   lat[i][1].x, lat[i][1].y, lat[i][1].z, lat[i][1].w};
+        // the eight dimensions 16 q + 8 a .. + 7
+        auto eight = [&](int q, int a, uint32_t (&f)[4]) {
+          e2m1x8_to_f16x8(words[2 * q + a], f);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) f[y] = hmul2_u32(f[y], s[q]);
+        };
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          if constexpr (kKeys) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t f[4], g[4];
+              eight(2 * h, a, f);
+              eight(2 * h + 1, a, g);
+              put(4 * a + h, f[0], f[1], g[0], g[1]);
+              put(4 * a + 2 + h, f[2], f[3], g[2], g[3]);
+            }
+          } else {
+            uint32_t f[4][4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) eight(q, a, f[q]);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) put(4 * a + y, f[0][y], f[1][y], f[2][y], f[3][y]);
+          }
+        }
+      } else {
+        uint32_t words[4][4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          words[q][0] = lat[i][q].x, words[q][1] = lat[i][q].y;
+          words[q][2] = lat[i][q].z, words[q][3] = lat[i][q].w;
+        }
+        auto two = [&](int q, int y, int half) {  // dimensions 16 q + 4 y + 2 half, + 1
+          const uint32_t h = e4m3x2_to_f16x2(static_cast<uint16_t>(words[q][y] >> (16 * half)));
+          return kKeys ? h : hmin2(h, 0x5F005F00u);  // 448
+        };
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+          if constexpr (kKeys) {
+            const int q = 2 * (m & 1), y = m >> 1;
+            put(m, two(q, y, 0), two(q, y, 1), two(q + 1, y, 0), two(q + 1, y, 1));
+          } else {
+            const int y = m >> 1, h = m & 1;
+            put(m, two(0, y, h), two(1, y, h), two(2, y, h), two(3, y, h));
+          }
+        }
+      }
     }
-    if (numbers) {
+    if constexpr (kKeys) {
+      const uint32_t w4[4] = {rope.x, rope.y, rope.z, rope.w};
+      uint32_t h[8];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) h[q] = hmin2(h[q], 0x5F005F00u);  // 448
-    }
-    if constexpr (kOrder) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        st_shared_v2(block + swizzled(key, 2 * j + (pair >> 1)) + 8 * (pair & 1), h[2 * j], h[2 * j + 1]);
-    } else {
-      st_shared_v4(block + swizzled(key, 2 * pair), h[0], h[1], h[2], h[3]);
-      st_shared_v4(block + swizzled(key, 2 * pair + 1), h[4], h[5], h[6], h[7]);
+      for (int q = 0; q < 4; ++q) {
+        h[2 * q] = e4m3x2_to_f16x2(static_cast<uint16_t>(w4[q] & 0xFFFFu));
+        h[2 * q + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w4[q] >> 16));
+      }
+      const uint32_t k = 8u * w + (lane >> 2), col = 2 * (lane & 3);
+      st_shared_v4(dst + 8 * kKBlock + swizzled(k, col), h[0], h[1], h[2], h[3]);
+      st_shared_v4(dst + 8 * kKBlock + swizzled(k, col + 1), h[4], h[5], h[6], h[7]);
     }
   }
-  // Into blocks of 64 keys x 64 dimensions from `dst` on. As a value (not kKeys) a NaN
-  // becomes a number. A row's scores are NaN for every token that sees it then; the
-  // others weigh it with 0, which a NaN would not survive. The same holds for what
-  // lies in the place of a key that does not exist.
-  template <bool kKeys>
-  __device__ __forceinline__ void store(uint32_t dst, int w, int lane) const {
-    if constexpr (kNv) {
+};
+
+// Q of a score CTA's 128 rows (from row r0 of all, `rows` of them exist), as FP16: the
+// latent part into tensor memory, the rope part into shared memory. Two of the
+// eight warps share a quarter of the rows: `half` of the blocks each. A lane loads
+// 32 bytes of a row, so that a load takes whole lines.
+struct QLoad {
+  const uint16_t* lat;   // the lane's first row and dimensions
+  const uint16_t* rope;
+  int32_t left;          // rows from the lane's first one on
+  uint32_t v[2][8];      // of two rows, 8 apart
+
+  __device__ __forceinline__ QLoad(const ChunkParams& p, int64_t row0, int32_t rows, int first, int lane) {
+    const int r = first + (lane >> 2);
+    lat = p.q_lat + (row0 + r) * kLatent + 16 * (lane & 3);
+    rope = p.q_rope + (row0 + r) * kRope + 16 * (lane & 3);
+    left = rows - r;
+  }
+  // rows 16 y + {0, 8} of 64 dimensions
+  __device__ __forceinline__ void load(const uint16_t* from, int width, int y) {
 #pragma unroll
-      for (int i = 0; i < kItems; ++i) {
-        const uint32_t key = 8u * w + 2 * ((lane >> 1) & 3) + (i & 1);
-        const uint32_t c = (lane & 1) + 2 * (lane >> 3) + 8 * (i >> 1);
-        uint32_t s = e4m3x2_to_f16x2(static_cast<uint16_t>(scale[i]));
-        if (!kKeys) s = hmin2(s, 0x5F005F00u);
-        const uint32_t s0 = __byte_perm(s, s, 0x1010), s1 = __byte_perm(s, s, 0x3232);
-        const uint32_t words[4] = {lat[i].x, lat[i].y, lat[i].z, lat[i].w};
-        const uint32_t block = dst + (c >> 1) * kKBlock;
-        uint32_t f[4][4];
+    for (int z = 0; z < 2; ++z) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          e2m1x8_to_f16x8(words[x], f[x]);
-#pragma unroll
-          for (int y = 0; y < 4; ++y) f[x][y] = hmul2_u32(f[x][y], x < 2 ? s0 : s1);
-        }
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          if (kKeys)
-            st_shared_v4(block + swizzled(key, 2 * x + (c & 1)), f[x >> 1][2 * (x & 1)], f[x >> 1][2 * (x & 1) + 1],
-                         f[2 + (x >> 1)][2 * (x & 1)], f[2 + (x >> 1)][2 * (x & 1) + 1]);
-          else
-            st_shared_v4(block + swizzled(key, (c & 1) * 4 + x), f[x][0], f[x][1], f[x][2], f[x][3]);
-        }
-      }
-    } else {
-      const uint32_t key = 8u * w + (lane >> 2);
-#pragma unroll
-      for (int i = 0; i < kItems; ++i) {
-        const uint32_t c = 4 * i + (lane & 3);
-        store_e4m3<kKeys>(lat[i], dst + (c >> 2) * kKBlock, key, c & 3, !kKeys);
-      }
+      for (int k = 0; k < 8; ++k) v[z][k] = 0u;
+      if (left > 16 * y + 8 * z) ld_32_bytes(from + (16 * y + 8 * z) * width, v[z]);
     }
-    if constexpr (kRopeToo) store_e4m3<false>(rope, dst + 8 * kKBlock, 8u * w + (lane >> 2), lane & 3, false);
   }
 };
 
@@ -579,7 +629,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
       mbar_init(bar(C::kSEmpty, i), 8);  // four warps a piece
       mbar_init(bar(C::kStaged, i), 4);
     }
-    mbar_init(bar(C::kQFull, 0), kSoftWarps);
+    mbar_init(bar(C::kQFull, 0), kExpandWarps);
     for (uint32_t i = 0; i < 4 * kGroups; ++i) mbar_init(bar(C::kRefDone, i), 1);
     for (uint32_t i = 0; i < 16 * kGroups; ++i) mbar_init(bar(C::kSumDone, i), 1);
     for (uint32_t i = 0; i < 4; ++i) mbar_init(bar(C::kStageFree, i), 1);
@@ -852,16 +902,59 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
           const uint32_t s = u % L::kRawsScore;
           run = warp_wait(bar(C::kRawFull, s), (u / L::kRawsScore) & 1, abort_addr, lim);
           if (!run) break;
-          RowItems<kFmt, L::kNv ? 4 : 8, true, false> items;
+          RowItems<kFmt, true> items;
           items.load(sbase + L::kRawScore + s * L::kRawBytes, w, lane, 0);
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(C::kRawEmpty, s));
           run = u < 2 || warp_wait(bar(C::kSFull, u & 1), ((u >> 1) & 1) ^ 1, abort_addr, lim);
           if (!run) break;
-          items.template store<true>(sbase + L::kK + (u & 1) * kKTileBytes, w, lane);
+          items.store(sbase + L::kK + (u & 1) * kKTileBytes, w, lane);
           fence_proxy_async_cta();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(C::kKFull, u & 1));
+          if (kt == pieces.begin) {  // Q, once the MMAs of the row tile before are done with its
+            const uint32_t quad = w & 3, half = w >> 2;
+            QLoad a(p, pieces.tile.row0, pieces.tile.rows, 128 * part + 32 * quad, lane), b = a;
+            const uint32_t q_addr = tmem + ((32 * quad) << 16) + 128 * half;
+            auto put = [&](const QLoad& q, int x) {  // rows 16 (x % 2) .. + 15 of block 4 half + x / 2
+              uint32_t h[16];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  h[4 * j + z] = to_f16x2(q.v[0][2 * j + z], p.lat_mult);
+                  h[4 * j + 2 + z] = to_f16x2(q.v[1][2 * j + z], p.lat_mult);
+                }
+              tmem_st_16x256b_x4(q_addr + ((16 * (x & 1)) << 16) + 32u * (x >> 1), h);
+            };
+            a.load(a.lat + 256 * half, kLatent, 0);
+            b.load(b.lat + 256 * half, kLatent, 1);
+            if (u > 0) run = warp_wait(bar(C::kSFull, (u - 1) & 1), ((u - 1) >> 1) & 1, abort_addr, lim);
+            if (!run) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int x = 0; x < 8; x += 2) {
+              put(a, x);
+              if (x < 6) a.load(a.lat + 256 * half + 32 * (x + 2), kLatent, 0);
+              else a.load(a.rope, kRope, half);
+              put(b, x + 1);
+              if (x < 6) b.load(b.lat + 256 * half + 32 * (x + 2), kLatent, 1);
+            }
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const uint32_t r = 32 * quad + 16 * half + 8 * z + (lane >> 2), col = 2 * (lane & 3);
+              uint32_t h[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) h[k] = to_f16x2(a.v[z][k], p.rope_mult);
+              st_shared_v4(sbase + L::kQRope + swizzled(r, col), h[0], h[1], h[2], h[3]);
+              st_shared_v4(sbase + L::kQRope + swizzled(r, col + 1), h[4], h[5], h[6], h[7]);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            fence_proxy_async_cta();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::kQFull, 0));
+          }
         }
       }
     } else {
@@ -873,7 +966,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
           const uint32_t s = u % L::kRawsOut, vs = u % L::kVSlots;
           run = warp_wait(bar(C::kRawFull, s), (u / L::kRawsOut) & 1, abort_addr, lim);
           if (!run) break;
-          RowItems<kFmt, L::kNv ? 2 : 4, false, true> items;
+          RowItems<kFmt, false> items;
           items.load(sbase + L::kRawOut + s * L::kRawBytes, w, lane, part);
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(C::kRawEmpty, s));
@@ -881,7 +974,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
           run = u < L::kVSlots ||
                 warp_wait<true>(bar(C::kPvDone, v % L::kPSlots), (v / L::kPSlots) & 1, abort_addr, lim);
           if (!run) break;
-          items.template store<false>(sbase + L::kV + vs * kVSlotBytes, w, lane);
+          items.store(sbase + L::kV + vs * kVSlotBytes, w, lane);
           fence_proxy_async_cta();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(C::kVFull, vs));
@@ -897,7 +990,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
     bool ok = true;
     Pieces pieces(p, cluster);
     if (scoring) {
-      // ---------------------------------------------- Q, softmax (thread = row)
+      // ---------------------------------------------- softmax (thread = row)
       // The groups of four warps take the pieces in turn: one has the time of three
       // pieces for each. A row's reference goes from piece to piece through shared
       // memory; each group has a sum of its own.
@@ -907,63 +1000,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
       uint32_t i0 = 0;  // tiles before
       for (uint32_t item = 0; ok && pieces.next(); ++item) {
         const uint32_t n = static_cast<uint32_t>(pieces.end - pieces.begin) * 2;
-        {
-          // Each group loads a third of Q's nine blocks of 64 dimensions. A warp has 32
-          // rows; a lane loads 16 dimensions (32 bytes) of rows lane / 4 + 8 y, so that a
-          // load takes whole lines, and stores them as the 16 x 256 bit shape has them:
-          // dimensions 16 q + 4 j + e of a block (q = lane % 4) become 16 j + 4 q + e, which
-          // is the order that the keys are expanded to.
-          const uint32_t rows = pieces.tile.rows, r0 = 128 * part + 32 * quad + (lane >> 2);
-          const uint16_t* ql = p.q_lat + (pieces.tile.row0 + r0) * kLatent + 16 * (lane & 3);
-          const uint16_t* qr = p.q_rope + (pieces.tile.row0 + row) * kRope;
-          auto load = [&](uint32_t block, uint32_t (&v)[4][8]) {
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-#pragma unroll
-              for (int z = 0; z < 8; ++z) v[y][z] = 0u;
-              if (block < 8 && r0 + 8 * y < rows) ld_32_bytes(ql + 8 * y * kLatent + 64 * block, v[y]);
-            }
-          };
-          auto store = [&](uint32_t block, const uint32_t (&v)[4][8]) {
-            if (block >= 8) return;
-#pragma unroll
-            for (int y = 0; y < 4; y += 2) {
-              uint32_t h[16];
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                  h[4 * j + z] = to_f16x2(v[y][2 * j + z], p.lat_mult);
-                  h[4 * j + 2 + z] = to_f16x2(v[y + 1][2 * j + z], p.lat_mult);
-                }
-              tmem_st_16x256b_x4(tmem + ((32 * quad + 8 * y) << 16) + 32u * block, h);
-            }
-          };
-          uint32_t first[4][8], second[4][8];
-          load(group, first);
-          load(group + kGroups, second);
-          // the MMAs that read the Q before are done
-          if (i0 > 0) ok = warp_wait(bar(C::kSFull, (i0 - 1) & 1), ((i0 - 1) >> 1) & 1, abort_addr, lim);
-          if (!ok) break;
-          tc_fence_after();
-          store(group, first);
-          load(group + 2 * kGroups, first);
-          store(group + kGroups, second);
-          if (group == kGroups - 1) {
-#pragma unroll
-            for (int y = 0; y < 8; ++y) {
-              uint4 f = make_uint4(0u, 0u, 0u, 0u);
-              if (row < pieces.tile.rows) f = to_f16x8(__ldg(reinterpret_cast<const uint4*>(qr) + y), p.rope_mult);
-              st_shared_v4(sbase + L::kQRope + swizzled(t, y), f.x, f.y, f.z, f.w);
-            }
-          }
-          store(group + 2 * kGroups, first);
-          tmem_st_wait();
-          tc_fence_before();
-          fence_proxy_async_cta();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(C::kQFull, 0));
-        }
         // keys that the row sees
         const int32_t sees =
             pieces.tile.base + 1 + (pieces.tile.offset + min(row, pieces.tile.rows - 1)) / p.num_heads;
@@ -1141,33 +1177,45 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
             ok = warp_wait<true>(bar(C::kPvDone, ps), (u / L::kPSlots) & 1, abort_addr, lim);
             if (!ok) break;
             tc_fence_after();
-            const float fin = __uint_as_float(ld_shared_u32(sbase + L::kFinal + 512 * (item % L::kNotes) + 4 * t));
-            const bool mine = row < pieces.tile.rows;
+            // 16 rows x 64 dimensions at a time: a lane has 16 dimensions of two rows
+            const uint32_t finals = sbase + L::kFinal + 512 * (item % L::kNotes) + 4 * (32 * quad + (lane >> 2));
+            const int r0 = 128 * static_cast<int>(part) + 32 * static_cast<int>(quad) + (lane >> 2);
             const bool f32 = !pieces.whole || p.out_fp32;
-            float* wide = pieces.whole
-                              ? static_cast<float*>(p.out) + (pieces.tile.row0 + row) * kLatent
-                              : p.part_out + (static_cast<int64_t>(pieces.slot) * kTileRows + row) * kLatent;
-            uint16_t* narrow = static_cast<uint16_t*>(p.out) + (pieces.tile.row0 + row) * kLatent;
+            float* wide = (pieces.whole ? static_cast<float*>(p.out) + (pieces.tile.row0 + r0) * kLatent
+                                        : p.part_out +
+                                              (static_cast<int64_t>(pieces.slot) * kTileRows + r0) * kLatent) +
+                          16 * (lane & 3);
+            uint16_t* narrow = static_cast<uint16_t*>(p.out) + (pieces.tile.row0 + r0) * kLatent + 16 * (lane & 3);
 #pragma unroll 1
             for (uint32_t y = group; y < 16; y += kGroups) {
+              const uint32_t block = y >> 1, rows = 16 * (y & 1);
               uint32_t r[32];
-              tmem_ld32(o_addr + 32u * y, r);
+              tmem_ld_16x256b_x8(o_addr + (rows << 16) + 64u * block, r);
               tmem_ld_wait();
-              float v[32];
 #pragma unroll
-              for (int q = 0; q < 32; ++q) v[q] = __uint_as_float(r[q]) * fin;
-              if (!mine) continue;
-              if (f32) {
+              for (int z = 0; z < 2; ++z) {
+                const int at = static_cast<int>(rows) + 8 * z;
+                const float fin = __uint_as_float(ld_shared_u32(finals + 4 * at));
+                float v[16];
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                  *reinterpret_cast<float4*>(wide + 32 * y + 4 * q) =
-                      make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-              } else {
+                for (int j = 0; j < 8; ++j) {
+                  v[2 * j] = __uint_as_float(r[4 * j + 2 * z]) * fin;
+                  v[2 * j + 1] = __uint_as_float(r[4 * j + 2 * z + 1]) * fin;
+                }
+                if (r0 + at >= pieces.tile.rows) continue;
+                const int64_t to = static_cast<int64_t>(at) * kLatent + 64 * block;
+                if (f32) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                  *reinterpret_cast<uint4*>(narrow + 32 * y + 8 * q) =
-                      make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
-                                 pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+                  for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<float4*>(wide + to + 4 * q) =
+                        make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                } else {
+#pragma unroll
+                  for (int q = 0; q < 2; ++q)
+                    *reinterpret_cast<uint4*>(narrow + to + 8 * q) =
+                        make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                                   pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+                }
               }
             }
           }
