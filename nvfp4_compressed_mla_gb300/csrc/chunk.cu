@@ -260,6 +260,9 @@ __device__ __forceinline__ void bulk_s2s(uint32_t dst_cluster, uint32_t src, uin
 __device__ __forceinline__ void arrive_remote(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {  // multiples of 16
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 // One lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -363,9 +366,6 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
-  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
-}
 __device__ __forceinline__ uint32_t hmin2(uint32_t a, uint32_t b) {  // of a NaN and a number: the number
   uint32_t r;
   asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -374,11 +374,9 @@ __device__ __forceinline__ uint32_t hmin2(uint32_t a, uint32_t b) {  // of a NaN
 __device__ __forceinline__ uint32_t to_f16x2(uint32_t x, float m) {  // 2 bf16 values times m
   return pack_f16x2(bf16_lo(x) * m, bf16_hi(x) * m);
 }
-__device__ __forceinline__ uint4 to_f16x8(uint4 x, float m) {
-  return make_uint4(to_f16x2(x.x, m), to_f16x2(x.y, m), to_f16x2(x.z, m), to_f16x2(x.w, m));
-}
-__device__ __forceinline__ void ld_32_bytes(const void* p, uint32_t (&v)[8]) {  // 16-byte aligned
-  const uint4 a = ld_nc_v4(p), b = ld_nc_v4(static_cast<const uint8_t*>(p) + 16);
+// Two pieces of 16 bytes, 64 bytes apart.
+__device__ __forceinline__ void ld_two_v4(const uint16_t* p, uint32_t (&v)[8]) {
+  const uint4 a = ld_nc_v4(p), b = ld_nc_v4(p + 32);
   v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
   v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
@@ -458,11 +456,11 @@ static_assert(ChunkCtl::kMissing + 32 * ChunkCtl::kMissingTiles == ChunkLayout<0
 // so they touch different 16-byte columns of shared memory.
 //
 // What the matrix products call a dimension need not be the row's. Within each
-// block of 64 the order is such that what a thread loads, or writes, of Q and O
-// through the 16 x 256 bit shape of tensor memory is contiguous in global memory
-// (q = 0 .. 3 is lane % 4 there):
-//   keys (and Q): dimension 16 q + 4 j + e is at 16 j + 4 q + e  (j, e = 0 .. 3)
-//   values (and O): dimension 16 q + 2 j + e is at 8 j + 2 q + e  (j = 0 .. 7, e = 0, 1)
+// block of 64 the order is such that what four lanes load of a row of Q, or write
+// of O, with one 16-byte access each through the 16 x 256 bit shape of tensor
+// memory is contiguous in global memory (q = 0 .. 3 is lane % 4 there):
+//   keys (and Q): dimension 32 h + 8 q + 4 j + e is at 32 h + 16 j + 4 q + e  (h, j = 0, 1; e = 0 .. 3)
+//   values (and O): dimension 32 h + 8 q + 2 j + e is at 32 h + 8 j + 2 q + e  (h, e = 0, 1; j = 0 .. 3)
 // A score CTA expands all 512 dimensions of its keys, a CTA of the output pair
 // dimensions 128 part .. + 127 of each half.
 template <int kFmt, bool kKeys>
@@ -512,52 +510,50 @@ struct RowItems {
                                __byte_perm(s23, s23, 0x1010), __byte_perm(s23, s23, 0x3232)};
         const uint32_t words[8] = {lat[i][0].x, lat[i][0].y, lat[i][0].z, lat[i][0].w,
                                    lat[i][1].x, lat[i][1].y, lat[i][1].z, lat[i][1].w};
-        // the eight dimensions 16 q + 8 a .. + 7
-        auto eight = [&](int q, int a, uint32_t (&f)[4]) {
-          e2m1x8_to_f16x8(words[2 * q + a], f);
+        // the eight dimensions 32 h + 8 q .. + 7
+        auto eight = [&](int h, int q, uint32_t (&f)[4]) {
+          e2m1x8_to_f16x8(words[4 * h + q], f);
 #pragma unroll
-          for (int y = 0; y < 4; ++y) f[y] = hmul2_u32(f[y], s[q]);
+          for (int y = 0; y < 4; ++y) f[y] = hmul2_u32(f[y], s[2 * h + (q >> 1)]);
         };
 #pragma unroll
-        for (int a = 0; a < 2; ++a) {
+        for (int h = 0; h < 2; ++h) {
           if constexpr (kKeys) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int q = 0; q < 4; q += 2) {
               uint32_t f[4], g[4];
-              eight(2 * h, a, f);
-              eight(2 * h + 1, a, g);
-              put(4 * a + h, f[0], f[1], g[0], g[1]);
-              put(4 * a + 2 + h, f[2], f[3], g[2], g[3]);
+              eight(h, q, f);
+              eight(h, q + 1, g);
+              put(4 * h + (q >> 1), f[0], f[1], g[0], g[1]);
+              put(4 * h + 2 + (q >> 1), f[2], f[3], g[2], g[3]);
             }
           } else {
             uint32_t f[4][4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) eight(q, a, f[q]);
+            for (int q = 0; q < 4; ++q) eight(h, q, f[q]);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) put(4 * a + y, f[0][y], f[1][y], f[2][y], f[3][y]);
+            for (int y = 0; y < 4; ++y) put(4 * h + y, f[0][y], f[1][y], f[2][y], f[3][y]);
           }
         }
       } else {
-        uint32_t words[4][4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          words[q][0] = lat[i][q].x, words[q][1] = lat[i][q].y;
-          words[q][2] = lat[i][q].z, words[q][3] = lat[i][q].w;
-        }
-        auto two = [&](int q, int y, int half) {  // dimensions 16 q + 4 y + 2 half, + 1
-          const uint32_t h = e4m3x2_to_f16x2(static_cast<uint16_t>(words[q][y] >> (16 * half)));
-          return kKeys ? h : hmin2(h, 0x5F005F00u);  // 448
+        // dimensions 32 h + 8 q + 2 y, + 1
+        auto two = [&](int h, int q, int y) {
+          const uint4 v = lat[i][2 * h + (q >> 1)];
+          const uint32_t word = (q & 1) ? ((y >> 1) ? v.w : v.z) : ((y >> 1) ? v.y : v.x);
+          const uint32_t f = e4m3x2_to_f16x2(static_cast<uint16_t>(word >> (16 * (y & 1))));
+          return kKeys ? f : hmin2(f, 0x5F005F00u);  // 448
         };
 #pragma unroll
-        for (int m = 0; m < 8; ++m) {
-          if constexpr (kKeys) {
-            const int q = 2 * (m & 1), y = m >> 1;
-            put(m, two(q, y, 0), two(q, y, 1), two(q + 1, y, 0), two(q + 1, y, 1));
-          } else {
-            const int y = m >> 1, h = m & 1;
-            put(m, two(0, y, h), two(1, y, h), two(2, y, h), two(3, y, h));
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            if constexpr (kKeys) {
+              const int q = 2 * (m & 1), y = 2 * (m >> 1);
+              put(4 * h + m, two(h, q, y), two(h, q, y + 1), two(h, q + 1, y), two(h, q + 1, y + 1));
+            } else {
+              put(4 * h + m, two(h, 0, m), two(h, 1, m), two(h, 2, m), two(h, 3, m));
+            }
           }
-        }
       }
     }
     if constexpr (kKeys) {
@@ -577,8 +573,8 @@ struct RowItems {
 
 // Q of a score CTA's 128 rows (from row r0 of all, `rows` of them exist), as FP16: the
 // latent part into tensor memory, the rope part into shared memory. Two of the
-// eight warps share a quarter of the rows: `half` of the blocks each. A lane loads
-// 32 bytes of a row, so that a load takes whole lines.
+// eight warps share a quarter of the rows: half of the blocks each. Four lanes load
+// 64 bytes of a row at a time.
 struct QLoad {
   const uint16_t* lat;   // the lane's first row and dimensions
   const uint16_t* rope;
@@ -587,8 +583,8 @@ struct QLoad {
 
   __device__ __forceinline__ QLoad(const ChunkParams& p, int64_t row0, int32_t rows, int first, int lane) {
     const int r = first + (lane >> 2);
-    lat = p.q_lat + (row0 + r) * kLatent + 16 * (lane & 3);
-    rope = p.q_rope + (row0 + r) * kRope + 16 * (lane & 3);
+    lat = p.q_lat + (row0 + r) * kLatent + 8 * (lane & 3);
+    rope = p.q_rope + (row0 + r) * kRope + 8 * (lane & 3);
     left = rows - r;
   }
   // rows 16 y + {0, 8} of 64 dimensions
@@ -597,7 +593,7 @@ struct QLoad {
     for (int z = 0; z < 2; ++z) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[z][k] = 0u;
-      if (left > 16 * y + 8 * z) ld_32_bytes(from + (16 * y + 8 * z) * width, v[z]);
+      if (left > 16 * y + 8 * z) ld_two_v4(from + (16 * y + 8 * z) * width, v[z]);
     }
   }
 };
@@ -676,6 +672,16 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
       bool run = true;
       Pieces pieces(p, cluster);
       while (run && pieces.next()) {
+        // the next row tile's Q, into L2
+        if (scoring && lane < 2 && pieces.t < pieces.tiles && p.tiles[pieces.t].unit < pieces.u1) {
+          const RowTile& after = p.tiles[pieces.t];
+          const int32_t rows = min(after.rows - 128 * static_cast<int32_t>(part), 128);
+          const int64_t first = after.row0 + 128 * part;
+          if (rows > 0)
+            prefetch_l2(lane == 0 ? p.q_lat + first * kLatent : p.q_rope + first * kRope,
+                        static_cast<uint32_t>(rows) * 2u * (lane == 0 ? kLatent : kRope));
+        }
+        __syncwarp();
         const int32_t* table = p.block_table + static_cast<int64_t>(pieces.tile.seq) * p.max_blocks;
         const int32_t step = scoring ? kTileKeys : kPieceKeys;
         const int32_t stop = pieces.end * kTileKeys;
@@ -942,12 +948,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
             }
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
-              const uint32_t r = 32 * quad + 16 * half + 8 * z + (lane >> 2), col = 2 * (lane & 3);
+              const uint32_t r = 32 * quad + 16 * half + 8 * z + (lane >> 2), col = lane & 3;
               uint32_t h[8];
 #pragma unroll
               for (int k = 0; k < 8; ++k) h[k] = to_f16x2(a.v[z][k], p.rope_mult);
               st_shared_v4(sbase + L::kQRope + swizzled(r, col), h[0], h[1], h[2], h[3]);
-              st_shared_v4(sbase + L::kQRope + swizzled(r, col + 1), h[4], h[5], h[6], h[7]);
+              st_shared_v4(sbase + L::kQRope + swizzled(r, col + 4), h[4], h[5], h[6], h[7]);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -1177,15 +1183,15 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
             ok = warp_wait<true>(bar(C::kPvDone, ps), (u / L::kPSlots) & 1, abort_addr, lim);
             if (!ok) break;
             tc_fence_after();
-            // 16 rows x 64 dimensions at a time: a lane has 16 dimensions of two rows
+            // 16 rows x 64 dimensions at a time: a lane has twice 8 dimensions of two rows
             const uint32_t finals = sbase + L::kFinal + 512 * (item % L::kNotes) + 4 * (32 * quad + (lane >> 2));
             const int r0 = 128 * static_cast<int>(part) + 32 * static_cast<int>(quad) + (lane >> 2);
             const bool f32 = !pieces.whole || p.out_fp32;
             float* wide = (pieces.whole ? static_cast<float*>(p.out) + (pieces.tile.row0 + r0) * kLatent
                                         : p.part_out +
                                               (static_cast<int64_t>(pieces.slot) * kTileRows + r0) * kLatent) +
-                          16 * (lane & 3);
-            uint16_t* narrow = static_cast<uint16_t*>(p.out) + (pieces.tile.row0 + r0) * kLatent + 16 * (lane & 3);
+                          8 * (lane & 3);
+            uint16_t* narrow = static_cast<uint16_t*>(p.out) + (pieces.tile.row0 + r0) * kLatent + 8 * (lane & 3);
 #pragma unroll 1
             for (uint32_t y = group; y < 16; y += kGroups) {
               const uint32_t block = y >> 1, rows = 16 * (y & 1);
@@ -1207,12 +1213,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
                 if (f32) {
 #pragma unroll
                   for (int q = 0; q < 4; ++q)
-                    *reinterpret_cast<float4*>(wide + to + 4 * q) =
+                    *reinterpret_cast<float4*>(wide + to + 32 * (q >> 1) + 4 * (q & 1)) =
                         make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
                 } else {
 #pragma unroll
                   for (int q = 0; q < 2; ++q)
-                    *reinterpret_cast<uint4*>(narrow + to + 8 * q) =
+                    *reinterpret_cast<uint4*>(narrow + to + 32 * q) =
                         make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
                                    pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
                 }
