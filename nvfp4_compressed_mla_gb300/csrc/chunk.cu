@@ -57,7 +57,7 @@ static_assert(kGroups * kSoftRegs + 2 * kExpandRegs + kIssueRegs == 6 * kLaunchR
 constexpr int kMaxClusters = 40;
 constexpr uint32_t kPBytes = 128 * kPieceKeys * 2;
 constexpr uint32_t kKBlock = kPieceKeys * 128;   // 64 keys x 64 dimensions, FP16
-constexpr uint32_t kKTileBytes = 9 * kKBlock;    // 8 latent blocks and the rope
+constexpr uint32_t kTileBlocks = 9;              // 8 latent blocks and the rope
 constexpr uint32_t kVSlotBytes = 4 * kKBlock;    // 64 keys x 256 dimensions
 constexpr long long kDrainLimit = 1ll << 31;
 // The reference of a row moves when a score exceeds it by more than kTau (log2
@@ -405,9 +405,15 @@ struct ChunkLayout {
   static constexpr uint32_t kRow = kNv ? kNvfp4Row : kFp8Row;
   static constexpr uint32_t kRawBytes = kPieceKeys * kRow;  // cache rows of 64 keys
   // score CTA
-  static constexpr uint32_t kK = 0;                        // two key tiles
-  static constexpr uint32_t kQRope = 2 * kKTileBytes;
-  static constexpr uint32_t kStages = kNv ? 2 : 1;         // P pieces on their way out
+  // A ring of blocks of keys, two tiles. The wider FP8 rows leave no room for that
+  // and more than one stage of P (a prompt's tile took 1.4 times as long): there a
+  // tile's first four blocks have room beside the tile before, and the others
+  // where the MMAs are done with that one's first four. For NVFP4 rows that ring
+  // and a third stage are 3 % slower than two tiles and two stages.
+  static constexpr uint32_t kK = 0, kKBlocks = kNv ? 2 * kTileBlocks : kTileBlocks + 5;
+  static constexpr bool kHalves = kKBlocks < 2 * kTileBlocks;
+  static constexpr uint32_t kQRope = kKBlocks * kKBlock;
+  static constexpr uint32_t kStages = kNv ? 2 : 3;         // P pieces on their way out
   static constexpr uint32_t kStaged = kQRope + 16384;
   static constexpr uint32_t kRawScore = kStaged + kStages * kPBytes;
   static constexpr uint32_t kRawsScore = 1;
@@ -430,7 +436,7 @@ struct ChunkLayout {
   // a piece is noted once its stage is free: those that are staged or have a slot
   static_assert(kNotes > kPSlots + kStages, "notes");
   static constexpr uint32_t kCtl = kEndScore > kEndOut ? kEndScore : kEndOut;
-  static constexpr uint32_t kCtlBytes = 1072;
+  static constexpr uint32_t kCtlBytes = 1104;
   static constexpr uint32_t kBytes = kCtl + kCtlBytes;
   static_assert(kBytes <= kMaxSharedBytes && kCtl % 16 == 0 && kTag % 16 == 0, "shared memory");
   static_assert(kStaged % 1024 == 0 && kP % 1024 == 0 && kRawScore % 16 == 0 && kRawOut % 16 == 0, "operands");
@@ -439,10 +445,11 @@ constexpr uint32_t kSCol = 256;  // score CTA's tensor memory: Q's latent part, 
 static_assert(kSCol + 2 * kTileKeys <= kTmemCols, "tensor memory");
 struct ChunkCtl {  // barriers and words, at the same offsets in every CTA of the cluster
   static constexpr uint32_t kRawFull = 0, kRawEmpty = 16, kKFull = 32, kPeer = 48, kSFull = 64, kSEmpty = 80,
-                            kQFull = 96, kStaged = 104, kStageFree = 120, kRefDone = 152, kSumDone = 248,
-                            kPFull = 632, kPReady = 664, kPvDone = 696, kVFull = 728, kTask = 752,
-                            kTaskDone = 760, kTmem = 768, kAbort = 772, kSent = 776, kScored = 780,
-                            kSummed = 784, kLoaded = 788, kTaskWord = 792, kNoted = 796, kMissing = 816;
+                            kQFull = 96, kStaged = 104, kStageFree = 128, kRefDone = 160, kSumDone = 256,
+                            kPFull = 640, kPReady = 672, kPvDone = 704, kVFull = 736, kTask = 760,
+                            kTaskDone = 768, kKHalf = 776, kTmem = 792, kAbort = 796, kSent = 800,
+                            kScored = 804, kSummed = 808, kLoaded = 812, kTaskWord = 816, kNoted = 820,
+                            kMissing = 848;
   // 1 + tile and the bits of its 64 keys that exist, a CTA of the pair, 8 tiles:
   // written where some page does not resolve
   static constexpr uint32_t kMissingTiles = 8;
@@ -487,87 +494,83 @@ struct RowItems {
       rope = ld_shared_v4(raw + (8 * w + (lane >> 2)) * kRow + (kNv ? kRopeOff : kLatent) + 16 * (lane & 3));
   }
 
-  // Into blocks of 64 keys x 64 dimensions from `dst` on. As a value a NaN becomes a
-  // number: a row's scores are NaN for every token that sees it then, and the others
-  // weigh it with 0, which a NaN would not survive. The same holds for what lies in
-  // the place of a key that does not exist.
-  __device__ __forceinline__ void store(uint32_t dst, int w, int lane) const {
+  // The lane's block number i into the 64 keys x 64 dimensions at `block`. As a value a
+  // NaN becomes a number: a row's scores are NaN for every token that sees it then,
+  // and the others weigh it with 0, which a NaN would not survive. The same holds
+  // for what lies in the place of a key that does not exist.
+  __device__ __forceinline__ void store_block(int i, uint32_t block, int w, int lane) const {
     const uint32_t key = 8u * w + (lane & 7);
+    auto put = [&](uint32_t col, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+      st_shared_v4(block + swizzled(key, col), a, b, c, d);
+    };
+    if constexpr (kNv) {
+      uint32_t s01 = e4m3x2_to_f16x2(static_cast<uint16_t>(scale[i] & 0xFFFFu));
+      uint32_t s23 = e4m3x2_to_f16x2(static_cast<uint16_t>(scale[i] >> 16));
+      if (!kKeys) {
+        s01 = hmin2(s01, 0x5F005F00u);  // 448
+        s23 = hmin2(s23, 0x5F005F00u);
+      }
+      const uint32_t s[4] = {__byte_perm(s01, s01, 0x1010), __byte_perm(s01, s01, 0x3232),
+                             __byte_perm(s23, s23, 0x1010), __byte_perm(s23, s23, 0x3232)};
+      const uint32_t words[8] = {lat[i][0].x, lat[i][0].y, lat[i][0].z, lat[i][0].w,
+                                 lat[i][1].x, lat[i][1].y, lat[i][1].z, lat[i][1].w};
+      // the eight dimensions 32 h + 8 q .. + 7
+      auto eight = [&](int h, int q, uint32_t (&f)[4]) {
+        e2m1x8_to_f16x8(words[4 * h + q], f);
 #pragma unroll
-    for (int i = 0; i < kBlocks; ++i) {
-      const uint32_t block = dst + ((lane >> 3) + 4 * i) * kKBlock;
-      auto put = [&](uint32_t col, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-        st_shared_v4(block + swizzled(key, col), a, b, c, d);
+        for (int y = 0; y < 4; ++y) f[y] = hmul2_u32(f[y], s[2 * h + (q >> 1)]);
       };
-      if constexpr (kNv) {
-        uint32_t s01 = e4m3x2_to_f16x2(static_cast<uint16_t>(scale[i] & 0xFFFFu));
-        uint32_t s23 = e4m3x2_to_f16x2(static_cast<uint16_t>(scale[i] >> 16));
-        if (!kKeys) {
-          s01 = hmin2(s01, 0x5F005F00u);  // 448
-          s23 = hmin2(s23, 0x5F005F00u);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if constexpr (kKeys) {
+#pragma unroll
+          for (int q = 0; q < 4; q += 2) {
+            uint32_t f[4], g[4];
+            eight(h, q, f);
+            eight(h, q + 1, g);
+            put(4 * h + (q >> 1), f[0], f[1], g[0], g[1]);
+            put(4 * h + 2 + (q >> 1), f[2], f[3], g[2], g[3]);
+          }
+        } else {
+          uint32_t f[4][4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) eight(h, q, f[q]);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) put(4 * h + y, f[0][y], f[1][y], f[2][y], f[3][y]);
         }
-        const uint32_t s[4] = {__byte_perm(s01, s01, 0x1010), __byte_perm(s01, s01, 0x3232),
-                               __byte_perm(s23, s23, 0x1010), __byte_perm(s23, s23, 0x3232)};
-        const uint32_t words[8] = {lat[i][0].x, lat[i][0].y, lat[i][0].z, lat[i][0].w,
-                                   lat[i][1].x, lat[i][1].y, lat[i][1].z, lat[i][1].w};
-        // the eight dimensions 32 h + 8 q .. + 7
-        auto eight = [&](int h, int q, uint32_t (&f)[4]) {
-          e2m1x8_to_f16x8(words[4 * h + q], f);
+      }
+    } else {
+      // dimensions 32 h + 8 q + 2 y, + 1
+      auto two = [&](int h, int q, int y) {
+        const uint4 v = lat[i][2 * h + (q >> 1)];
+        const uint32_t word = (q & 1) ? ((y >> 1) ? v.w : v.z) : ((y >> 1) ? v.y : v.x);
+        const uint32_t f = e4m3x2_to_f16x2(static_cast<uint16_t>(word >> (16 * (y & 1))));
+        return kKeys ? f : hmin2(f, 0x5F005F00u);  // 448
+      };
 #pragma unroll
-          for (int y = 0; y < 4; ++y) f[y] = hmul2_u32(f[y], s[2 * h + (q >> 1)]);
-        };
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int m = 0; m < 4; ++m) {
           if constexpr (kKeys) {
-#pragma unroll
-            for (int q = 0; q < 4; q += 2) {
-              uint32_t f[4], g[4];
-              eight(h, q, f);
-              eight(h, q + 1, g);
-              put(4 * h + (q >> 1), f[0], f[1], g[0], g[1]);
-              put(4 * h + 2 + (q >> 1), f[2], f[3], g[2], g[3]);
-            }
+            const int q = 2 * (m & 1), y = 2 * (m >> 1);
+            put(4 * h + m, two(h, q, y), two(h, q, y + 1), two(h, q + 1, y), two(h, q + 1, y + 1));
           } else {
-            uint32_t f[4][4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) eight(h, q, f[q]);
-#pragma unroll
-            for (int y = 0; y < 4; ++y) put(4 * h + y, f[0][y], f[1][y], f[2][y], f[3][y]);
+            put(4 * h + m, two(h, 0, m), two(h, 1, m), two(h, 2, m), two(h, 3, m));
           }
         }
-      } else {
-        // dimensions 32 h + 8 q + 2 y, + 1
-        auto two = [&](int h, int q, int y) {
-          const uint4 v = lat[i][2 * h + (q >> 1)];
-          const uint32_t word = (q & 1) ? ((y >> 1) ? v.w : v.z) : ((y >> 1) ? v.y : v.x);
-          const uint32_t f = e4m3x2_to_f16x2(static_cast<uint16_t>(word >> (16 * (y & 1))));
-          return kKeys ? f : hmin2(f, 0x5F005F00u);  // 448
-        };
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            if constexpr (kKeys) {
-              const int q = 2 * (m & 1), y = 2 * (m >> 1);
-              put(4 * h + m, two(h, q, y), two(h, q, y + 1), two(h, q + 1, y), two(h, q + 1, y + 1));
-            } else {
-              put(4 * h + m, two(h, 0, m), two(h, 1, m), two(h, 2, m), two(h, 3, m));
-            }
-          }
-      }
     }
-    if constexpr (kKeys) {
-      const uint32_t w4[4] = {rope.x, rope.y, rope.z, rope.w};
-      uint32_t h[8];
+  }
+  __device__ __forceinline__ void store_rope(uint32_t block, int w, int lane) const {
+    const uint32_t words[4] = {rope.x, rope.y, rope.z, rope.w};
+    uint32_t h[8];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        h[2 * q] = e4m3x2_to_f16x2(static_cast<uint16_t>(w4[q] & 0xFFFFu));
-        h[2 * q + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w4[q] >> 16));
-      }
-      const uint32_t k = 8u * w + (lane >> 2), col = 2 * (lane & 3);
-      st_shared_v4(dst + 8 * kKBlock + swizzled(k, col), h[0], h[1], h[2], h[3]);
-      st_shared_v4(dst + 8 * kKBlock + swizzled(k, col + 1), h[4], h[5], h[6], h[7]);
+    for (int q = 0; q < 4; ++q) {
+      h[2 * q] = e4m3x2_to_f16x2(static_cast<uint16_t>(words[q] & 0xFFFFu));
+      h[2 * q + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(words[q] >> 16));
     }
+    const uint32_t key = 8u * w + (lane >> 2), col = 2 * (lane & 3);
+    st_shared_v4(block + swizzled(key, col), h[0], h[1], h[2], h[3]);
+    st_shared_v4(block + swizzled(key, col + 1), h[4], h[5], h[6], h[7]);
   }
 };
 
@@ -623,11 +626,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
       mbar_init(bar(C::kPeer, i), 1);
       mbar_init(bar(C::kSFull, i), 1);
       mbar_init(bar(C::kSEmpty, i), 8);  // four warps a piece
-      mbar_init(bar(C::kStaged, i), 4);
+      mbar_init(bar(C::kKHalf, i), 1);
     }
     mbar_init(bar(C::kQFull, 0), kExpandWarps);
     for (uint32_t i = 0; i < 4 * kGroups; ++i) mbar_init(bar(C::kRefDone, i), 1);
     for (uint32_t i = 0; i < 16 * kGroups; ++i) mbar_init(bar(C::kSumDone, i), 1);
+    for (uint32_t i = 0; i < L::kStages; ++i) mbar_init(bar(C::kStaged, i), 4);
     for (uint32_t i = 0; i < 4; ++i) mbar_init(bar(C::kStageFree, i), 1);
     for (uint32_t i = 0; i < L::kPSlots; ++i) {
       mbar_init(bar(C::kPFull, i), 1);
@@ -796,7 +800,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
                                   (static_cast<uint32_t>(kTileRows >> 4) << 24);
       const uint64_t qr = operand_desc(sbase + L::kQRope);
       const uint32_t peer = map_rank(bar(C::kPeer, 0), 0);
-      uint32_t i = 0;
+      const uint64_t k0 = operand_desc(sbase + L::kK);
+      uint32_t i = 0, first = 0;  // ring position of the tile's first block
       bool run = true;
       Pieces pieces(p, cluster);
       for (uint32_t item = 0; run && pieces.next(); ++item) {
@@ -817,17 +822,23 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
           if (!run) break;
           tc_fence_after();
           const uint32_t d = kSCol + kTileKeys * b;
-          const uint64_t kd = operand_desc(sbase + L::kK + b * kKTileBytes);
           if (elect_one()) {
+            uint32_t at = first;
 #pragma unroll
-            for (int x = 0; x < 32; ++x)
-              pair_mma_ts(d, 8u * x, kd + (x >> 2) * (kKBlock >> 4) + 2 * (x & 3), kIdesc, x != 0 ? 1u : 0u);
+            for (uint32_t block = 0; block < kTileBlocks; ++block) {
+              const uint64_t kd = k0 + at * (kKBlock >> 4);
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              pair_mma_ss(d, qr + 2 * x, kd + 8 * (kKBlock >> 4) + 2 * x, kIdesc, 1u);
+              for (uint32_t x = 0; x < 4; ++x) {
+                if (block < 8) pair_mma_ts(d, 32 * block + 8 * x, kd + 2 * x, kIdesc, (block | x) != 0 ? 1u : 0u);
+                else pair_mma_ss(d, qr + 2 * x, kd + 2 * x, kIdesc, 1u);
+              }
+              if (L::kHalves && block == 3) commit_to(bar(C::kKHalf, b), 0x3);
+              if (++at == L::kKBlocks) at = 0;
+            }
             commit_to(bar(C::kSFull, b), 0x3);
           }
           __syncwarp();
+          first = (first + kTileBlocks) % L::kKBlocks;
         }
       }
       if (part == 0 && lane < 2) st_cluster_u32(map_rank(ctl + C::kScored, lane), i);
@@ -902,7 +913,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
     Pieces pieces(p, cluster);
     if (scoring) {
       // ---------------------------------------------- keys of a score CTA
-      // Tile u goes into slot u % 2, once the MMAs of tile u - 2 are done.
+      // Tile u goes into the ring once the MMAs of tile u - 2 are done (kHalves: its
+      // first four blocks do, the others once those of tile u - 1's first four are).
+      uint32_t first = 0;  // ring position of the tile's first block
       while (run && pieces.next()) {
         for (int32_t kt = pieces.begin; kt < pieces.end; ++kt, ++u) {
           const uint32_t s = u % L::kRawsScore;
@@ -914,7 +927,18 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
           if (lane == 0) mbar_arrive(bar(C::kRawEmpty, s));
           run = u < 2 || warp_wait(bar(C::kSFull, u & 1), ((u >> 1) & 1) ^ 1, abort_addr, lim);
           if (!run) break;
-          items.store(sbase + L::kK + (u & 1) * kKTileBytes, w, lane);
+          auto block_at = [&](uint32_t block) {
+            const uint32_t at = first + block;
+            return sbase + L::kK + (at < L::kKBlocks ? at : at - L::kKBlocks) * kKBlock;
+          };
+          items.store_block(0, block_at(lane >> 3), w, lane);
+          if (L::kHalves && u > 0) {
+            run = warp_wait(bar(C::kKHalf, (u - 1) & 1), ((u - 1) >> 1) & 1, abort_addr, lim);
+            if (!run) break;
+          }
+          items.store_block(1, block_at(4 + (lane >> 3)), w, lane);
+          items.store_rope(block_at(8), w, lane);
+          first = (first + kTileBlocks) % L::kKBlocks;
           fence_proxy_async_cta();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(C::kKFull, u & 1));
@@ -980,7 +1004,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
           run = u < L::kVSlots ||
                 warp_wait<true>(bar(C::kPvDone, v % L::kPSlots), (v / L::kPSlots) & 1, abort_addr, lim);
           if (!run) break;
-          items.store(sbase + L::kV + vs * kVSlotBytes, w, lane);
+          items.store_block(0, sbase + L::kV + vs * kVSlotBytes + (lane >> 3) * kKBlock, w, lane);
           fence_proxy_async_cta();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(C::kVFull, vs));
