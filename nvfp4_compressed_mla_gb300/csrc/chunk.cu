@@ -173,13 +173,12 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
     }
   }
   const int64_t share = max((units + p.clusters - 1) / p.clusters, int64_t{kLeastShare});
+  // the row tile of each cluster's first unit
   for (int c = tid; c < p.clusters; c += kPlanThreads) {
     p.first[c] = n_tiles;
     p.failed[c] = 0;
   }
-  if (tid == 0) {
-    *p.plan = {units, share, n_tiles, 0};
-  }
+  if (tid == 0) *p.plan = {units, share, n_tiles, 0};
   __syncthreads();
   for (int t = tid; t < n_tiles; t += kPlanThreads) {
     const int64_t a = p.tiles[t].unit, b = p.tiles[t].end;
@@ -600,6 +599,13 @@ struct QLoad {
     }
   }
 };
+
+// Partial results lie in the order in which a warp has them: of 8 rows and 64
+// dimensions four times 32 lanes' 16 bytes; lane 4 (row % 8) + c of number q has
+// dimensions 32 (q / 2) + 8 c + 4 (q % 2) .. + 3. Here the place of 8 rows' first.
+__device__ __forceinline__ int64_t part_at(int32_t slot, int row) {
+  return (static_cast<int64_t>(slot) * kTileRows + row) * (kLatent / 4);
+}
 
 // ------------------------------------------------------------------ kernel
 template <int kFmt>
@@ -1210,11 +1216,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
             // 16 rows x 64 dimensions at a time: a lane has twice 8 dimensions of two rows
             const uint32_t finals = sbase + L::kFinal + 512 * (item % L::kNotes) + 4 * (32 * quad + (lane >> 2));
             const int r0 = 128 * static_cast<int>(part) + 32 * static_cast<int>(quad) + (lane >> 2);
-            const bool f32 = !pieces.whole || p.out_fp32;
-            float* wide = (pieces.whole ? static_cast<float*>(p.out) + (pieces.tile.row0 + r0) * kLatent
-                                        : p.part_out +
-                                              (static_cast<int64_t>(pieces.slot) * kTileRows + r0) * kLatent) +
-                          8 * (lane & 3);
+            float* wide = static_cast<float*>(p.out) + (pieces.tile.row0 + r0) * kLatent + 8 * (lane & 3);
+            float4* parts = reinterpret_cast<float4*>(p.part_out) +
+                            part_at(pieces.slot, 128 * static_cast<int>(part) + 32 * static_cast<int>(quad)) + lane;
             uint16_t* narrow = static_cast<uint16_t*>(p.out) + (pieces.tile.row0 + r0) * kLatent + 8 * (lane & 3);
 #pragma unroll 1
             for (uint32_t y = group; y < 16; y += kGroups) {
@@ -1234,7 +1238,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
                 }
                 if (r0 + at >= pieces.tile.rows) continue;
                 const int64_t to = static_cast<int64_t>(at) * kLatent + 64 * block;
-                if (f32) {
+                if (!pieces.whole) {
+#pragma unroll
+                  for (int q = 0; q < 4; ++q)
+                    parts[128 * (8 * (at >> 3) + block) + 32 * q] =
+                        make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                } else if (p.out_fp32) {
 #pragma unroll
                   for (int q = 0; q < 4; ++q)
                     *reinterpret_cast<float4*>(wide + to + 32 * (q >> 1) + 4 * (q & 1)) =
@@ -1290,7 +1299,7 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkParams p) {
   cudaGridDependencySynchronize();
   const int lane = threadIdx.x & 31;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
-  const int64_t me = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int64_t me = static_cast<int64_t>(threadIdx.x >> 5) * gridDim.x + blockIdx.x;  // few rows: an SM each
   bool failed = false;
   for (int c = lane; c < p.clusters; c += 32) failed |= __ldcg(p.failed + c) != 0;
   if (__any_sync(0xffffffffu, failed)) {  // a wait ran out: no row is to be trusted
@@ -1331,43 +1340,66 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkParams p) {
     int q0 = c - 1;
     while (q0 < c1 && !has(q0)) ++q0;
     if (q0 == c1) continue;  // all key tiles in one cluster: it wrote the result
-    float top = -INFINITY;
+    // a lane reads the sums of parts lane and lane + 32 of the row, then all parts' outputs
+    // come four at a time: read one after the other they took a microsecond each
+    const int parts = c1 - q0 + 1;
+    float z[2], top = -INFINITY;
     bool nan = false;
-    for (int q = q0; q <= c1; ++q) {
-      const float z = __ldcg(lse_at(q));
-      nan |= z != z;
-      top = fmaxf(top, z);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      z[i] = lane + 32 * i < parts ? __ldcg(lse_at(q0 + lane + 32 * i)) : -INFINITY;
+      nan |= z[i] != z[i];
+      top = fmaxf(top, z[i]);
     }
+    nan = __any_sync(0xffffffffu, nan);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
     float acc[16] = {};
     float tot = 0.f;
     if (top != -INFINITY) {
-      for (int q = q0; q <= c1; ++q) {
-        const float w = ex2((__ldcg(lse_at(q)) - top) * kLog2e);
-        tot += w;
-        if (w == 0.f) continue;
-        const float* from =
-            p.part_out + (static_cast<int64_t>(2 * q + (a >= q * share ? 1 : 0)) * kTileRows + row) * kLatent;
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(from + 128 * y + 4 * lane));
-          acc[4 * y] += w * v.x;
-          acc[4 * y + 1] += w * v.y;
-          acc[4 * y + 2] += w * v.z;
-          acc[4 * y + 3] += w * v.w;
+      for (int i = 0; i < 2; ++i) z[i] = ex2((z[i] - top) * kLog2e);
+      for (int i0 = 0; i0 < parts; i0 += 4) {
+        float4 v[4][4];
+        float w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float mine = i0 + i < 32 ? z[0] : z[1];
+          w[i] = __shfl_sync(0xffffffffu, mine, (i0 + i) & 31);  // 0 behind the last part
+          const int q = q0 + i0 + i;
+          const float4* from = reinterpret_cast<const float4*>(p.part_out) +
+                               part_at(2 * q + (a >= q * share ? 1 : 0), row & ~7) + 4 * (row & 7) + (lane & 3);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            v[i][y] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (w[i] != 0.f) v[i][y] = __ldcg(from + 128 * (2 * y + (lane >> 4)) + 32 * ((lane >> 2) & 3));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          tot += w[i];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            acc[4 * y] += w[i] * v[i][y].x;
+            acc[4 * y + 1] += w[i] * v[i][y].y;
+            acc[4 * y + 2] += w[i] * v[i][y].z;
+            acc[4 * y + 3] += w[i] * v[i][y].w;
+          }
         }
       }
     }
     const float inv = nan ? NAN : tot > 0.f ? 1.f / tot : 0.f;
     const int64_t to = tile.row0 + row;
+    const int dim = 64 * (lane >> 4) + 32 * ((lane >> 3) & 1) + 8 * (lane & 3) + 4 * ((lane >> 2) & 1);
 #pragma unroll
     for (int y = 0; y < 4; ++y) {
       const float v0 = acc[4 * y] * inv, v1 = acc[4 * y + 1] * inv, v2 = acc[4 * y + 2] * inv,
                   v3 = acc[4 * y + 3] * inv;
       if (p.out_fp32)
-        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + to * kLatent + 128 * y + 4 * lane) =
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + to * kLatent + 128 * y + dim) =
             make_float4(v0, v1, v2, v3);
       else
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + to * kLatent + 128 * y + 4 * lane) =
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + to * kLatent + 128 * y + dim) =
             make_uint2(pack_bf16x2(v0, v1), pack_bf16x2(v2, v3));
     }
     if (lane == 0 && p.lse != nullptr)
