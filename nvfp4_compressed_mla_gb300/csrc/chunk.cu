@@ -404,18 +404,22 @@ struct ChunkLayout {
   static constexpr uint32_t kRow = kNv ? kNvfp4Row : kFp8Row;
   static constexpr uint32_t kRawBytes = kPieceKeys * kRow;  // cache rows of 64 keys
   // score CTA
-  // A ring of blocks of keys, two tiles. The wider FP8 rows leave no room for that
-  // and more than one stage of P (a prompt's tile took 1.4 times as long): there a
-  // tile's first four blocks have room beside the tile before, and the others
-  // where the MMAs are done with that one's first four. For NVFP4 rows that ring
-  // and a third stage are 3 % slower than two tiles and two stages.
-  static constexpr uint32_t kK = 0, kKBlocks = kNv ? 2 * kTileBlocks : kTileBlocks + 5;
-  static constexpr bool kHalves = kKBlocks < 2 * kTileBlocks;
+  // A ring of blocks of keys. Two whole tiles of them would leave room for one stage
+  // of P beside FP8 rows, and for one tile of rows on its way beside NVFP4 rows. So a
+  // tile's first kKBlocks - 9 blocks (at least four) have room beside the tile before,
+  // the others where the MMAs are done with that one's first ones. Measured, of 512
+  // tokens of a prompt of 16384 (128 heads) and 66 decoding sequences of up to 32768:
+  // FP8 rows 2179 us with two tiles and one stage, 1552 with 14 blocks and three;
+  // NVFP4 rows 1324 and 557 us with two tiles and one slot of rows, 1305 and 529 with
+  // 15 blocks and two, 1329 and 540 with 14.
+  static constexpr uint32_t kK = 0, kKBlocks = kNv ? kTileBlocks + 6 : kTileBlocks + 5;
+  static constexpr uint32_t kKShared = 2 * kTileBlocks - kKBlocks;  // blocks that wait for the tile before
+  static_assert(kKBlocks >= kTileBlocks + 4 && kKShared > 0, "the expanding warps write four blocks at first");
   static constexpr uint32_t kQRope = kKBlocks * kKBlock;
   static constexpr uint32_t kStages = kNv ? 2 : 3;         // P pieces on their way out
   static constexpr uint32_t kStaged = kQRope + 16384;
   static constexpr uint32_t kRawScore = kStaged + kStages * kPBytes;
-  static constexpr uint32_t kRawsScore = 1;
+  static constexpr uint32_t kRawsScore = kNv ? 2 : 1;
   static constexpr uint32_t kRef = kRawScore + kRawsScore * kRawBytes;  // references of the rows, a group
   static constexpr uint32_t kSums = kRef + kGroups * 512;               // sums of weights, a group and 4 results
   static constexpr uint32_t kEndScore = kSums + 4 * kGroups * 512;
@@ -838,7 +842,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
                 if (block < 8) pair_mma_ts(d, 32 * block + 8 * x, kd + 2 * x, kIdesc, (block | x) != 0 ? 1u : 0u);
                 else pair_mma_ss(d, qr + 2 * x, kd + 2 * x, kIdesc, 1u);
               }
-              if (L::kHalves && block == 3) commit_to(bar(C::kKHalf, b), 0x3);
+              if (block + 1 == L::kKShared) commit_to(bar(C::kKHalf, b), 0x3);
               if (++at == L::kKBlocks) at = 0;
             }
             commit_to(bar(C::kSFull, b), 0x3);
@@ -919,8 +923,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
     Pieces pieces(p, cluster);
     if (scoring) {
       // ---------------------------------------------- keys of a score CTA
-      // Tile u goes into the ring once the MMAs of tile u - 2 are done (kHalves: its
-      // first four blocks do, the others once those of tile u - 1's first four are).
+      // Tile u goes into the ring once the MMAs of tile u - 2 are done, its last blocks
+      // once those of tile u - 1's first kKShared are.
       uint32_t first = 0;  // ring position of the tile's first block
       while (run && pieces.next()) {
         for (int32_t kt = pieces.begin; kt < pieces.end; ++kt, ++u) {
@@ -938,7 +942,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
             return sbase + L::kK + (at < L::kKBlocks ? at : at - L::kKBlocks) * kKBlock;
           };
           items.store_block(0, block_at(lane >> 3), w, lane);
-          if (L::kHalves && u > 0) {
+          if (u > 0) {
             run = warp_wait(bar(C::kKHalf, (u - 1) & 1), ((u - 1) >> 1) & 1, abort_addr, lim);
             if (!run) break;
           }
