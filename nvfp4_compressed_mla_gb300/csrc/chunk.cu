@@ -474,108 +474,151 @@ static_assert(ChunkCtl::kMissing + 32 * ChunkCtl::kMissingTiles == ChunkLayout<0
 // A score CTA expands all 512 dimensions of its keys, a CTA of the output pair
 // dimensions 128 part .. + 127 of each half.
 template <int kFmt, bool kKeys>
-struct RowItems {
-  static constexpr bool kNv = kFmt == NVFP4_MLA_ROW_NVFP4_352;
-  static constexpr uint32_t kRow = kNv ? kNvfp4Row : kFp8Row;
-  static constexpr int kBlocks = kKeys ? 2 : 1, kVecs = kNv ? 2 : 4;  // 16 bytes each of a block
-  uint4 lat[kBlocks][kVecs];
+struct RowItems;
+
+// 448, the largest E4M3 value, in place of a NaN.
+__device__ __forceinline__ uint32_t as_number(uint32_t f) { return hmin2(f, 0x5F005F00u); }
+
+template <bool kKeys>
+struct RowItems<NVFP4_MLA_ROW_NVFP4_352, kKeys> {
+  static constexpr uint32_t kRow = kNvfp4Row;
+  static constexpr int kBlocks = kKeys ? 2 : 1;  // of a lane: lane / 8, and 4 more
+  uint4 lat[kBlocks][2];
   uint32_t scale[kBlocks];
   uint4 rope;
 
-  // From the rows at `raw` (of 64 keys).
+  // From the rows at `raw` (of 64 keys). Rows are 88 banks apart, so that keys 4 apart
+  // meet in theirs: the later four lanes of eight read their halves the other way round.
   __device__ __forceinline__ void load(uint32_t raw, int w, int lane, uint32_t part) {
     const uint32_t key = raw + (8 * w + (lane & 7)) * kRow;
+    const bool turned = (lane & 4) != 0;
 #pragma unroll
     for (int i = 0; i < kBlocks; ++i) {
       const uint32_t b = (lane >> 3) + 4 * i;
       const uint32_t dim = kKeys ? 64 * b : 256 * (b >> 1) + 128 * part + 64 * (b & 1);
-#pragma unroll
-      for (int v = 0; v < kVecs; ++v) lat[i][v] = ld_shared_v4(key + (kNv ? dim / 2 : dim) + 16 * v);
-      if constexpr (kNv) scale[i] = ld_shared_u32(key + kScaleOff + dim / 16);
+      const uint4 x = ld_shared_v4(key + dim / 2 + (turned ? 16 : 0));
+      const uint4 y = ld_shared_v4(key + dim / 2 + (turned ? 0 : 16));
+      lat[i][0] = turned ? y : x;
+      lat[i][1] = turned ? x : y;
+      scale[i] = ld_shared_u32(key + kScaleOff + dim / 16);
     }
-    if constexpr (kKeys)
-      rope = ld_shared_v4(raw + (8 * w + (lane >> 2)) * kRow + (kNv ? kRopeOff : kLatent) + 16 * (lane & 3));
+    if constexpr (kKeys) rope = ld_shared_v4(raw + (8 * w + (lane >> 2)) * kRow + kRopeOff + 16 * (lane & 3));
   }
 
-  // The lane's block number i into the 64 keys x 64 dimensions at `block`. As a value a
-  // NaN becomes a number: a row's scores are NaN for every token that sees it then,
-  // and the others weigh it with 0, which a NaN would not survive. The same holds
-  // for what lies in the place of a key that does not exist.
-  __device__ __forceinline__ void store_block(int i, uint32_t block, int w, int lane) const {
-    const uint32_t key = 8u * w + (lane & 7);
+  // Blocks 4 i .. 4 i + 3 of the keys; at(block) is a block's 64 keys x 64 dimensions.
+  template <typename At>
+  __device__ __forceinline__ void store_blocks(int i, At&& at, int w, int lane) const {
+    const uint32_t key = 8u * w + (lane & 7), block = at(4u * i + (lane >> 3));
     auto put = [&](uint32_t col, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
       st_shared_v4(block + swizzled(key, col), a, b, c, d);
     };
-    if constexpr (kNv) {
-      uint32_t s01 = e4m3x2_to_f16x2(static_cast<uint16_t>(scale[i] & 0xFFFFu));
-      uint32_t s23 = e4m3x2_to_f16x2(static_cast<uint16_t>(scale[i] >> 16));
-      if (!kKeys) {
-        s01 = hmin2(s01, 0x5F005F00u);  // 448
-        s23 = hmin2(s23, 0x5F005F00u);
-      }
-      const uint32_t s[4] = {__byte_perm(s01, s01, 0x1010), __byte_perm(s01, s01, 0x3232),
-                             __byte_perm(s23, s23, 0x1010), __byte_perm(s23, s23, 0x3232)};
-      const uint32_t words[8] = {lat[i][0].x, lat[i][0].y, lat[i][0].z, lat[i][0].w,
-                                 lat[i][1].x, lat[i][1].y, lat[i][1].z, lat[i][1].w};
-      // the eight dimensions 32 h + 8 q .. + 7
-      auto eight = [&](int h, int q, uint32_t (&f)[4]) {
-        e2m1x8_to_f16x8(words[4 * h + q], f);
-#pragma unroll
-        for (int y = 0; y < 4; ++y) f[y] = hmul2_u32(f[y], s[2 * h + (q >> 1)]);
-      };
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if constexpr (kKeys) {
-#pragma unroll
-          for (int q = 0; q < 4; q += 2) {
-            uint32_t f[4], g[4];
-            eight(h, q, f);
-            eight(h, q + 1, g);
-            put(4 * h + (q >> 1), f[0], f[1], g[0], g[1]);
-            put(4 * h + 2 + (q >> 1), f[2], f[3], g[2], g[3]);
-          }
-        } else {
-          uint32_t f[4][4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) eight(h, q, f[q]);
-#pragma unroll
-          for (int y = 0; y < 4; ++y) put(4 * h + y, f[0][y], f[1][y], f[2][y], f[3][y]);
-        }
-      }
-    } else {
-      // dimensions 32 h + 8 q + 2 y, + 1
-      auto two = [&](int h, int q, int y) {
-        const uint4 v = lat[i][2 * h + (q >> 1)];
-        const uint32_t word = (q & 1) ? ((y >> 1) ? v.w : v.z) : ((y >> 1) ? v.y : v.x);
-        const uint32_t f = e4m3x2_to_f16x2(static_cast<uint16_t>(word >> (16 * (y & 1))));
-        return kKeys ? f : hmin2(f, 0x5F005F00u);  // 448
-      };
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          if constexpr (kKeys) {
-            const int q = 2 * (m & 1), y = 2 * (m >> 1);
-            put(4 * h + m, two(h, q, y), two(h, q, y + 1), two(h, q + 1, y), two(h, q + 1, y + 1));
-          } else {
-            put(4 * h + m, two(h, 0, m), two(h, 1, m), two(h, 2, m), two(h, 3, m));
-          }
-        }
+    uint32_t s01 = e4m3x2_to_f16x2(static_cast<uint16_t>(scale[i] & 0xFFFFu));
+    uint32_t s23 = e4m3x2_to_f16x2(static_cast<uint16_t>(scale[i] >> 16));
+    if (!kKeys) {
+      s01 = as_number(s01);
+      s23 = as_number(s23);
     }
-  }
-  __device__ __forceinline__ void store_rope(uint32_t block, int w, int lane) const {
-    const uint32_t words[4] = {rope.x, rope.y, rope.z, rope.w};
-    uint32_t h[8];
+    const uint32_t s[4] = {__byte_perm(s01, s01, 0x1010), __byte_perm(s01, s01, 0x3232),
+                           __byte_perm(s23, s23, 0x1010), __byte_perm(s23, s23, 0x3232)};
+    const uint32_t words[8] = {lat[i][0].x, lat[i][0].y, lat[i][0].z, lat[i][0].w,
+                               lat[i][1].x, lat[i][1].y, lat[i][1].z, lat[i][1].w};
+    // the eight dimensions 32 h + 8 q .. + 7
+    auto eight = [&](int h, int q, uint32_t (&f)[4]) {
+      e2m1x8_to_f16x8(words[4 * h + q], f);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      h[2 * q] = e4m3x2_to_f16x2(static_cast<uint16_t>(words[q] & 0xFFFFu));
-      h[2 * q + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(words[q] >> 16));
+      for (int y = 0; y < 4; ++y) f[y] = hmul2_u32(f[y], s[2 * h + (q >> 1)]);
+    };
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if constexpr (kKeys) {
+#pragma unroll
+        for (int q = 0; q < 4; q += 2) {
+          uint32_t f[4], g[4];
+          eight(h, q, f);
+          eight(h, q + 1, g);
+          put(4 * h + (q >> 1), f[0], f[1], g[0], g[1]);
+          put(4 * h + 2 + (q >> 1), f[2], f[3], g[2], g[3]);
+        }
+      } else {
+        uint32_t f[4][4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) eight(h, q, f[q]);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) put(4 * h + y, f[0][y], f[1][y], f[2][y], f[3][y]);
+      }
     }
-    const uint32_t key = 8u * w + (lane >> 2), col = 2 * (lane & 3);
-    st_shared_v4(block + swizzled(key, col), h[0], h[1], h[2], h[3]);
-    st_shared_v4(block + swizzled(key, col + 1), h[4], h[5], h[6], h[7]);
   }
 };
+
+// A lane has half a block: 32 dimensions of key 4 (lane / 8 % 2) + 2 (lane / 4 % 2) +
+// lane % 2, half lane / 2 % 2 of every second block. Rows are 144 banks apart, so that
+// keys 2 apart meet in theirs: of eight lanes those with the later keys read their two
+// 16 bytes the other way round, and neither their reads nor their stores conflict.
+template <bool kKeys>
+struct RowItems<NVFP4_MLA_ROW_FP8_576, kKeys> {
+  static constexpr uint32_t kRow = kFp8Row;
+  static constexpr int kItems = kKeys ? 4 : 2;
+  uint4 lat[kItems][2];
+  uint4 rope;
+
+  static __device__ __forceinline__ uint32_t key_of(int w, int lane) {
+    return 8u * w + ((lane >> 1) & 6) + (lane & 1);
+  }
+  __device__ __forceinline__ void load(uint32_t raw, int w, int lane, uint32_t part) {
+    const uint32_t half = (lane >> 1) & 1, turned = (lane >> 2) & 1;
+    const uint32_t from = raw + key_of(w, lane) * kRow + 32 * half;
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const uint32_t b = (lane >> 4) + 2 * i;
+      const uint32_t dim = kKeys ? 64 * b : 256 * (b >> 1) + 128 * part + 64 * (b & 1);
+      const uint4 x = ld_shared_v4(from + dim + 16 * turned), y = ld_shared_v4(from + dim + 16 * (turned ^ 1));
+      lat[i][0] = kKeys || turned == 0 ? x : y;
+      lat[i][1] = kKeys || turned == 0 ? y : x;
+    }
+    if constexpr (kKeys) rope = ld_shared_v4(raw + (8 * w + (lane >> 2)) * kRow + kLatent + 16 * (lane & 3));
+  }
+
+  // Blocks 4 i .. 4 i + 3 of the keys; at(block) is a block's 64 keys x 64 dimensions.
+  template <typename At>
+  __device__ __forceinline__ void store_blocks(int i, At&& at, int w, int lane) const {
+    const uint32_t key = key_of(w, lane), half = (lane >> 1) & 1, turned = (lane >> 2) & 1;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const uint4(&v)[2] = lat[2 * i + x];
+      const uint32_t block = at(4u * i + 2 * x + (lane >> 4));
+      // dimensions 16 z + 8 q + 2 y, + 1 of the half (of its turned parts, for keys)
+      auto two = [&](int z, int q, int y) {
+        const uint32_t word = q ? ((y >> 1) ? v[z].w : v[z].z) : ((y >> 1) ? v[z].y : v[z].x);
+        const uint32_t f = e4m3x2_to_f16x2(static_cast<uint16_t>(word >> (16 * (y & 1))));
+        return kKeys ? f : as_number(f);
+      };
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        if constexpr (kKeys) {
+          const int z = m & 1, y = m & 2;
+          st_shared_v4(block + swizzled(key, 4 * half + (z ^ turned) + y), two(z, 0, y), two(z, 0, y + 1),
+                       two(z, 1, y), two(z, 1, y + 1));
+        } else {
+          st_shared_v4(block + swizzled(key, 4 * half + m), two(0, 0, m), two(0, 1, m), two(1, 0, m), two(1, 1, m));
+        }
+      }
+    }
+  }
+};
+
+// The rope part of a lane, 16 values of key lane / 4, into the 64 keys x 64 dimensions at `block`.
+__device__ __forceinline__ void store_rope(const uint4& rope, uint32_t block, int w, int lane) {
+  const uint32_t words[4] = {rope.x, rope.y, rope.z, rope.w};
+  uint32_t h[8];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    h[2 * q] = e4m3x2_to_f16x2(static_cast<uint16_t>(words[q] & 0xFFFFu));
+    h[2 * q + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(words[q] >> 16));
+  }
+  const uint32_t key = 8u * w + (lane >> 2), col = 2 * (lane & 3);
+  st_shared_v4(block + swizzled(key, col), h[0], h[1], h[2], h[3]);
+  st_shared_v4(block + swizzled(key, col + 1), h[4], h[5], h[6], h[7]);
+}
 
 // Q of a score CTA's 128 rows (from row r0 of all, `rows` of them exist), as FP16: the
 // latent part into tensor memory, the rope part into shared memory. Two of the
@@ -941,13 +984,13 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
             const uint32_t at = first + block;
             return sbase + L::kK + (at < L::kKBlocks ? at : at - L::kKBlocks) * kKBlock;
           };
-          items.store_block(0, block_at(lane >> 3), w, lane);
+          items.store_blocks(0, block_at, w, lane);
           if (u > 0) {
             run = warp_wait(bar(C::kKHalf, (u - 1) & 1), ((u - 1) >> 1) & 1, abort_addr, lim);
             if (!run) break;
           }
-          items.store_block(1, block_at(4 + (lane >> 3)), w, lane);
-          items.store_rope(block_at(8), w, lane);
+          items.store_blocks(1, block_at, w, lane);
+          store_rope(items.rope, block_at(8), w, lane);
           first = (first + kTileBlocks) % L::kKBlocks;
           fence_proxy_async_cta();
           __syncwarp();
@@ -1014,7 +1057,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
           run = u < L::kVSlots ||
                 warp_wait<true>(bar(C::kPvDone, v % L::kPSlots), (v / L::kPSlots) & 1, abort_addr, lim);
           if (!run) break;
-          items.store_block(0, sbase + L::kV + vs * kVSlotBytes + (lane >> 3) * kKBlock, w, lane);
+          items.store_blocks(0, [&](uint32_t block) { return sbase + L::kV + vs * kVSlotBytes + block * kKBlock; },
+                             w, lane);
           fence_proxy_async_cta();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(C::kVFull, vs));
