@@ -188,7 +188,8 @@ int32_t sparse_mla_decode(const void* q_latent, const void* q_rope, const int32_
  * partials), so a stalled launch ends with a visible result instead of
  * holding its SMs. 0 restores the default of 2^31 cycles (about a second).
  * Process-wide; applies to decode launches enqueued after the call, and to
- * those of sparse_mla_select, whose rows are then -2. A bound
+ * those of sparse_mla_select, whose rows are then -2, and of dense_mla_chunk,
+ * whose rows are then all NaN. A bound
  * shorter than a healthy launch's waits makes healthy launches fail, which
  * is how the failure path is tested. Returns NVFP4_MLA_ERR_VALUE if
  * cycles < 0. This is this library's choice; the post has no counterpart.
@@ -522,7 +523,9 @@ int32_t sparse_mla_select(const void* q_index, const float* weights, const int32
  * Where a kernel's wait runs out (nvfp4_mla_set_wait_limit), all rows of the
  * step are NaN. dense_mla_chunk_workspace_size returns SIZE_MAX for an
  * invalid shape and 0 for num_q = 0. Results do not depend on what else runs,
- * and are the same for the same arguments on the same kind of device.
+ * and are the same for the same arguments on the same kind of device; with
+ * other sequences beside it in the step, a sequence's rows may differ by
+ * their roundings.
  */
 size_t dense_mla_chunk_workspace_size(int32_t num_q, int32_t num_heads, int32_t num_seqs);
 

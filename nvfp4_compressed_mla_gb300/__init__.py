@@ -140,7 +140,7 @@ def sparse_mla_decode_num_splits(num_q: int, num_heads: int, topk: int) -> int:
 
 
 def nvfp4_mla_set_wait_limit(cycles: int) -> None:
-    """Bound (SM clock cycles) of the decode and selection kernels' internal waits; 0 = default."""
+    """Bound (SM clock cycles) of the decode, selection and chunk kernels' internal waits; 0 = default."""
     _check(_lib().nvfp4_mla_set_wait_limit(int(cycles)), "nvfp4_mla_set_wait_limit")
 
 
