@@ -282,7 +282,10 @@ __global__ void __launch_bounds__(kPlanThreads) release_kernel(const ReleasePara
       load(kept_seq[x], b, end, kept[x]);
     }
   }
-  // begin(u) and f(s, pages of 8 x 32 entries (-1: none)) for each round of the warp's units
+  // which of the kept entries return their page: a bit each, known behind the third pass
+  uint32_t ours[kKept] = {};
+  // start(u), f(s, pages of 8 x 32 entries (-1: none), their place in `ours` or null) for each
+  // round of the warp's units, and stop(u)
   auto walk = [&](auto&& start, auto&& f, auto&& stop) {
     if (keeps) {
 #pragma unroll
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(kPlanThreads) release_kernel(const ReleasePara
         const int u = first_unit + x * stride;
         if (u < units) {
           start(u);
-          f(kept_seq[x], kept[x]);
+          f(kept_seq[x], kept[x], ours + x);
           stop(u);
         }
       }
@@ -303,7 +306,7 @@ __global__ void __launch_bounds__(kPlanThreads) release_kernel(const ReleasePara
       for (; b < end; b += kReleaseChunk) {
         int32_t page[kReleaseFlight];
         load(s, b, end, page);
-        f(s, page);
+        f(s, page, static_cast<uint32_t*>(nullptr));
       }
       stop(u);
     }
@@ -316,13 +319,13 @@ __global__ void __launch_bounds__(kPlanThreads) release_kernel(const ReleasePara
   };
 
   cluster_barrier();  // the counts may change now
-  walk(nothing, [&](int, const int32_t(&page)[kReleaseFlight]) {
+  walk(nothing, [&](int, const int32_t(&page)[kReleaseFlight], uint32_t*) {
 #pragma unroll
     for (int k = 0; k < kReleaseFlight; ++k)
       if (page[k] >= 0) atomicAdd(p.page_shares_out + page[k], -1);
   }, nothing);
   cluster_barrier();
-  walk(nothing, [&](int s, const int32_t(&page)[kReleaseFlight]) {
+  walk(nothing, [&](int s, const int32_t(&page)[kReleaseFlight], uint32_t*) {
     int32_t held[kReleaseFlight];
     held_by(page, held);
 #pragma unroll
@@ -333,12 +336,15 @@ __global__ void __launch_bounds__(kPlanThreads) release_kernel(const ReleasePara
   const uint32_t counts_addr = smem_u32(counts);
   int n = 0;
   walk([&](int) { n = 0; },
-       [&](int s, const int32_t(&page)[kReleaseFlight]) {
+       [&](int s, const int32_t(&page)[kReleaseFlight], uint32_t* out) {
          int32_t held[kReleaseFlight];
          held_by(page, held);
 #pragma unroll
-         for (int k = 0; k < kReleaseFlight; ++k)
-           n += __popc(__ballot_sync(0xffffffffu, held[k] == s - kReleaseMark));
+         for (int k = 0; k < kReleaseFlight; ++k) {
+           const bool mine = held[k] == s - kReleaseMark;
+           n += __popc(__ballot_sync(0xffffffffu, mine));
+           if (out != nullptr && mine) *out |= 1u << k;
+         }
        },
        [&](int u) {
          if (lane < ctas) st_cluster(counts_addr + 4u * static_cast<uint32_t>(u), lane, n);
@@ -360,12 +366,12 @@ __global__ void __launch_bounds__(kPlanThreads) release_kernel(const ReleasePara
   }
   int64_t at = 0;  // one above the next page's slot
   walk([&](int u) { at = top - (u > 0 ? counts[u - 1] : 0); },
-       [&](int s, const int32_t(&page)[kReleaseFlight]) {
-         int32_t held[kReleaseFlight];
-         held_by(page, held);
+       [&](int s, const int32_t(&page)[kReleaseFlight], uint32_t* known) {
+         int32_t held[kReleaseFlight] = {};
+         if (known == nullptr) held_by(page, held);
 #pragma unroll
          for (int k = 0; k < kReleaseFlight; ++k) {
-           const bool mine = held[k] == s - kReleaseMark;
+           const bool mine = known != nullptr ? (*known >> k) & 1u : held[k] == s - kReleaseMark;
            const uint32_t live = __ballot_sync(0xffffffffu, mine);
            const int64_t slot = at - 1 - __popc(live & ((1u << lane) - 1));
            if (mine && slot < p.free_capacity) p.free_pages[slot] = page[k];
