@@ -7,27 +7,47 @@
 // 2 x 1088 flop a row and key. A cache row of 352 bytes serves 128 heads with 279 kflop a token,
 // 791 flop a byte: tensor-bound from one token of 128 heads on.
 //
-// The rows (token, head) of a sequence are consecutive in memory, and a tile takes 128 kPair of
-// them, whatever the number of heads. One cluster works on a tile, and 512 columns of fp32 output
-// for 128 rows are all of an SM's tensor memory, so that the two products live on different SMs:
+// The rows (token, head) of a sequence are consecutive in memory, and a row tile takes 256 of
+// them, whatever the number of heads. One cluster of four CTAs works on a tile. 512 columns of fp32
+// output for 128 rows are all of an SM's tensor memory, so that the two products live on different
+// SMs, each as one MMA over a pair of them (cta_group::2, M = 256): an SM expands half of the keys,
+// or half of the dimensions, and the pair shares them, which halves the work of expanding a key for
+// a row. On one SM with 64 keys at a time an MMA whose A operand is in tensor memory takes as long
+// as one with 128 (70 cycles), so that sequences of up to 128 rows gain nothing from M = 128.
 //
-//   score CTAs (ranks 0 .. kPair - 1): 128 rows each. Q stays in tensor memory (latent part, 256
-//     columns, the MMA's A operand) and shared memory (rope part). Eight warps expand 64 keys a
-//     CTA and tile into FP16 (exact: a code times its scale has 6 significant bits) in shared
-//     memory; S of 64 kPair keys goes into one of two buffers. Four softmax warps (thread = row)
-//     turn it into P = 2^(s c - m) against a lazy reference m, in FP16, and copy it in pieces of
-//     64 keys into the output CTA of the same rows.
-//   output CTAs (ranks kPair .. 2 kPair - 1): O (128 rows x 512, fp32) in tensor memory. Eight
-//     warps expand the keys' latent part, each CTA 512 / kPair of the dimensions; four warps
-//     (thread = row) rescale O when a row's reference moved, and write the output.
-//
-// With kPair = 2 each product is one MMA over a pair of SMs (cta_group::2, M = 256): an SM expands
-// half of the keys or half of the dimensions and the pair shares them, which halves the work of
-// expanding a key for a row. kPair = 1 wastes less on sequences with few rows.
+//   score CTAs (ranks 0, 1): 128 rows each. Q stays in tensor memory (latent part, 256 columns, the
+//     MMA's A operand) and shared memory (rope part). Eight warps expand 64 keys a CTA and key tile
+//     (128 keys) into FP16 (exact: a code times its scale has 6 significant bits) in shared memory;
+//     S of 128 keys goes into one of two buffers. Three groups of four softmax warps (thread = row)
+//     take its pieces of 64 keys in turn, make P = 2^(s c - m) of them against a lazy reference m,
+//     in FP16, and a warp copies it into the output CTA of the same rows.
+//   output CTAs (ranks 2, 3): O (128 rows x 512, fp32) in tensor memory. Eight warps expand the
+//     keys' latent part, each CTA 256 of the dimensions; twelve warps rescale O when a row's
+//     reference moved, and write the output.
+//   In both a warp loads the cache's rows and a warp issues the MMAs; the issuing warp of a pair's
+//     second CTA tells the leader's what its CTA has ready.
 //
 // Work is dealt out in key tiles: a planning kernel lists the row tiles of the step with the key
-// tiles that each sees, and every cluster takes an equal, contiguous share of all of them. A row
-// tile that is cut by the shares' borders is merged by a last kernel from fp32 partial results.
+// tiles that each sees, and every cluster (36 of them fit the device's 152 SMs) takes an equal,
+// contiguous share of all of them. A row tile that is cut by the shares' borders is merged by a last
+// kernel from fp32 partial results. Which row is cut, and so a result's last bits, depends on the
+// whole step, but on nothing outside of it: the same arguments give the same bits.
+//
+// Measured (bf16 output, one call of the three kernels; a device's bf16 product of two large
+// matrices: 1906 TFLOP/s at best, 1709 for seconds on end):
+//   NVFP4, 512 tokens of a prompt of 16384, 128 heads      1.30 ms  1767 TFLOP/s
+//   FP8, the same                                          1.30 ms  1766
+//   NVFP4, 5 prompts of up to 5000 tokens, 32 heads        1.18 ms  1475
+//   NVFP4, 61 sequences: prompts, drafts, single tokens    3.69 ms  1617
+//   NVFP4, 66 tokens of 66 contexts of up to 32768         0.53 ms   850 (half of each MMA's rows are empty)
+//   NVFP4, 1 token of 128 heads, 8192 keys                   39 us  (bound by latency)
+//   NVFP4, 7 tokens of 16 heads, 307 keys                    28 us
+// The first two are bound by the MMAs: they take 2520 of about 2650 cycles of a key tile. Without
+// the MMAs' time the same pipelines (rows, expansion, softmax) take 1.23 ms, with neither that nor
+// exponentials 1.11 ms, so that nothing is left idle for long. What a row tile costs beside its key
+// tiles is loading Q and the first tile before P V can begin (8 us, most of it beside the tile
+// before) and writing O (2.6 us). A short call is a chain: plan 3.7 us, rows and Q 5, first scores
+// 2.5, first weights 3, a key tile 1.2 us each, output 2 to 4.5, teardown 2, merge 4 to 9.
 //
 // Every wait is bounded. A cluster whose wait runs out drains what it has in flight and reports
 // it; the last kernel then writes NaN to all rows of the step.
@@ -69,8 +89,14 @@ constexpr long long kDrainLimit = 1ll << 31;
 // of small weights: with kHeadroom 7 a third of the pieces had one.
 constexpr float kTau = 15.f, kHeadroom = 2.f;
 // Key tiles' time that a row tile costs beside its own (loading Q, the first
-// score tile before P V can begin, writing O), and the least share of a cluster.
-constexpr int kTileOverhead = 3, kLeastShare = 6;
+// score tile before P V can begin, writing O), and the least share of a cluster:
+// a cluster more costs its start and a merge. With 1 / 2 / 3 / 4 / 5 key tiles
+// five prompts of 5000 tokens take 1353 / 1292 / 1231 / 1203 / 1210 us (FP8 rows)
+// and 61 sequences of all kinds 3826 / 3772 / 3700 / 3690 / 3714. With a least share
+// of 4 / 6 / 8 (and 3 key tiles) a token over 8192 keys takes 38.6 / 38.9 / 42.2 us,
+// four over 2048 keys 38.4 / 42.5 / 45.1, 7 tokens over 307 keys 30.7 / 28.8 / 28.7:
+// those need no merge from 6 on (7 with 4 key tiles).
+constexpr int kTileOverhead = 4, kLeastShare = 7;
 
 struct alignas(16) RowTile {  // 256 rows of a sequence
   int32_t seq, rows;     // its rows, 1 .. 256
@@ -460,10 +486,11 @@ struct ChunkCtl {  // barriers and words, at the same offsets in every CTA of th
 static_assert(ChunkCtl::kMissing + 32 * ChunkCtl::kMissingTiles == ChunkLayout<0>::kCtlBytes, "control block");
 
 // ------------------------------------------------------------------ expansion
-// Warp w of the eight expands keys 8 w .. 8 w + 7 of each 64: a lane key lane % 8
-// and, of its latent part, kBlocks blocks of 64 dimensions; of its rope part 16
-// values of key lane / 4. The eight lanes of a store's phase have different keys,
-// so they touch different 16-byte columns of shared memory.
+// Warp w of the eight expands keys 8 w .. 8 w + 7 of each 64; of the rope part a lane
+// has 16 values of key lane / 4. Shared memory carries these reads and stores, the
+// MMAs' operands and the copies of rows and P at once, so that no eight lanes' 16-byte
+// accesses may meet in a bank: with FP8 rows read as a key a lane (four meet) 512
+// tokens of a prompt took 1553 us in place of 1300.
 //
 // What the matrix products call a dimension need not be the row's. Within each
 // block of 64 the order is such that what four lanes load of a row of Q, or write
@@ -487,7 +514,7 @@ struct RowItems<NVFP4_MLA_ROW_NVFP4_352, kKeys> {
   uint32_t scale[kBlocks];
   uint4 rope;
 
-  // From the rows at `raw` (of 64 keys). Rows are 88 banks apart, so that keys 4 apart
+  // A lane has key lane % 8 and blocks of 64 dimensions. Rows are 88 banks apart, so that keys 4 apart
   // meet in theirs: the later four lanes of eight read their halves the other way round.
   __device__ __forceinline__ void load(uint32_t raw, int w, int lane, uint32_t part) {
     const uint32_t key = raw + (8 * w + (lane & 7)) * kRow;
@@ -647,7 +674,8 @@ struct QLoad {
   }
 };
 
-// Partial results lie in the order in which a warp has them: of 8 rows and 64
+// Partial results lie in the order in which a warp has them (as rows of 512 values they took
+// 8.4 us to write, 128 rows a CTA, and 4.4 in this order): of 8 rows and 64
 // dimensions four times 32 lanes' 16 bytes; lane 4 (row % 8) + c of number q has
 // dimensions 32 (q / 2) + 8 c + 4 (q % 2) .. + 3. Here the place of 8 rows' first.
 __device__ __forceinline__ int64_t part_at(int32_t slot, int row) {
@@ -1389,7 +1417,8 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkParams p) {
     while (q0 < c1 && !has(q0)) ++q0;
     if (q0 == c1) continue;  // all key tiles in one cluster: it wrote the result
     // a lane reads the sums of parts lane and lane + 32 of the row, then all parts' outputs
-    // come four at a time: read one after the other they took a microsecond each
+    // come four at a time: read one after the other, a token of 128 heads over 8192 keys
+    // (12 parts) took 9 us more
     const int parts = c1 - q0 + 1;
     float z[2], top = -INFINITY;
     bool nan = false;
@@ -1473,6 +1502,7 @@ ChunkSpace chunk_space(int32_t num_q, int32_t num_heads, int32_t num_seqs) {
   s.bytes = s.out + size_t{4} * 2 * kMaxClusters * kTileRows * kLatent;
   return s;
 }
+static_assert(kMaxClusters <= 64, "a lane of the merge has two parts");
 static_assert(sizeof(RowTile) == 48 && sizeof(Plan) <= 64 && (4 * kMaxClusters) % 16 == 0, "workspace");
 
 bool chunk_shape_ok(int32_t num_q, int32_t num_heads, int32_t num_seqs) {
