@@ -52,6 +52,7 @@
 // Every wait is bounded. A cluster whose wait runs out drains what it has in flight and reports
 // it; the last kernel then writes NaN to all rows of the step.
 #include <cuda.h>
+#include <float.h>
 #include <math.h>
 
 #include <atomic>
@@ -1134,8 +1135,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(C::kSEmpty, b));  // S is read
-          uint32_t bits[2] = {have.y, have.z};  // the keys that the row sees
-          if (!all) {
+          // one branch for the warp: a test at each score cost more than the exponentials
+          if (!__all_sync(0xffffffffu, all)) {
+            uint32_t bits[2] = {have.y, have.z};  // the keys that the row sees
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
               const int32_t seen = room - 32 * a;
@@ -1188,10 +1190,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
                   fma_f32x2(f32x2(__uint_as_float(s[a][2 * y]), __uint_as_float(s[a][2 * y + 1])), c2, nm2), e0, e1);
               e0 = ex2(e0);
               e1 = ex2(e1);
-              if (!all) {
-                if (!((bits[a] >> (2 * y)) & 1u)) e0 = 0.f;
-                if (!((bits[a] >> (2 * y + 1)) & 1u)) e1 = 0.f;
-              }
               sum[y & 1] = add_f32x2(sum[y & 1], f32x2(e0, e1));
               pk[a][y] = pack_f16x2(e0, e1);
             }
@@ -1634,7 +1632,9 @@ extern "C" int32_t dense_mla_chunk(const void* q_latent, const void* q_rope, con
   p.block_stride = block_stride_bytes;
   const bool fp8 = row_format == NVFP4_MLA_ROW_FP8_576;
   const float lat = fp8 ? latent_scale : 1.f, sign = sm_scale < 0.f ? -1.f : 1.f;
-  p.score_scale = fabsf(sm_scale) * lat * kLog2e;
+  // never 0, so that the scale times -inf (a key that is not seen) stays -inf: times 2^-126 any
+  // score of FP16 operands has an exponential of 1 too
+  p.score_scale = fmaxf(fabsf(sm_scale) * lat * kLog2e, FLT_MIN);
   p.lat_mult = sign;
   p.rope_mult = sign * (rope_scale / lat);
   p.out_mult = lat;
