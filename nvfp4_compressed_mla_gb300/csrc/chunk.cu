@@ -35,18 +35,18 @@
 //
 // Measured (bf16 output, one call of the three kernels; a device's bf16 product of two large
 // matrices: 1906 TFLOP/s at best, 1709 for seconds on end):
-//   NVFP4, 512 tokens of a prompt of 16384, 128 heads      1.30 ms  1767 TFLOP/s
-//   FP8, the same                                          1.30 ms  1766
-//   NVFP4, 5 prompts of up to 5000 tokens, 32 heads        1.18 ms  1475
-//   NVFP4, 61 sequences: prompts, drafts, single tokens    3.69 ms  1617
-//   NVFP4, 66 tokens of 66 contexts of up to 32768         0.53 ms   850 (half of each MMA's rows are empty)
-//   NVFP4, 1 token of 128 heads, 8192 keys                   39 us  (bound by latency)
-//   NVFP4, 7 tokens of 16 heads, 307 keys                    28 us
-// The first two are bound by the MMAs: they take 2520 of about 2650 cycles of a key tile. Without
-// the MMAs' time the same pipelines (rows, expansion, softmax) take 1.23 ms, with neither that nor
-// exponentials 1.11 ms, so that nothing is left idle for long. What a row tile costs beside its key
-// tiles is loading Q and the first tile before P V can begin (8 us, most of it beside the tile
-// before) and writing O (2.6 us). A short call is a chain: plan 3.7 us, rows and Q 5, first scores
+//   NVFP4, 512 tokens of a prompt of 16384, 128 heads      1.21 ms  1896 TFLOP/s
+//   FP8, the same                                          1.23 ms  1873
+//   NVFP4, 5 prompts of up to 5000 tokens, 32 heads        1.09 ms  1594
+//   NVFP4, 61 sequences: prompts, drafts, single tokens    3.42 ms  1745
+//   NVFP4, 66 tokens of 66 contexts of up to 32768         0.49 ms   917 (half of each MMA's rows are empty)
+//   NVFP4, 1 token of 128 heads, 8192 keys                   40 us  (bound by latency)
+//   NVFP4, 7 tokens of 16 heads, 307 keys                    29 us
+// The first two are bound by the MMAs (the score SMs' tensor cores are active 96.5 % of the cycles
+// with NVFP4 rows). With a third of the MMAs the same pipelines (rows, expansion, softmax) take 1.13
+// and 1.19 ms, the 66 tokens 0.46: an MMA of 128 rows would not help those much. What a row tile
+// costs beside its key tiles is loading Q and the first tile before P V can begin (8 us, most of it
+// beside the tile before) and writing O (2.6 us). A short call is a chain: plan 3.7 us, rows and Q 5, first scores
 // 2.5, first weights 3, a key tile 1.2 us each, output 2 to 4.5, teardown 2, merge 4 to 9.
 //
 // Every wait is bounded. A cluster whose wait runs out drains what it has in flight and reports
@@ -431,19 +431,20 @@ struct ChunkLayout {
   static constexpr uint32_t kRow = kNv ? kNvfp4Row : kFp8Row;
   static constexpr uint32_t kRawBytes = kPieceKeys * kRow;  // cache rows of 64 keys
   // score CTA
-  // A ring of blocks of keys. Two whole tiles of them would leave room for one stage
-  // of P beside FP8 rows, and for one tile of rows on its way beside NVFP4 rows. So a
-  // tile's first kKBlocks - 9 blocks (at least four) have room beside the tile before,
-  // the others where the MMAs are done with that one's first ones. Measured, of 512
-  // tokens of a prompt of 16384 (128 heads) and 66 decoding sequences of up to 32768:
-  // FP8 rows 2179 us with two tiles and one stage, 1552 with 14 blocks and three;
-  // NVFP4 rows 1324 and 557 us with two tiles and one slot of rows, 1305 and 529 with
-  // 15 blocks and two, 1329 and 540 with 14.
-  static constexpr uint32_t kK = 0, kKBlocks = kNv ? kTileBlocks + 6 : kTileBlocks + 5;
+  // A ring of blocks of keys. Two whole tiles of them would leave no room for what else
+  // is worth more: two slots of NVFP4 rows on their way, two stages of P beside the one
+  // slot of FP8 rows. So a tile's first kKBlocks - 9 blocks have room beside the tile
+  // before, the others where the MMAs are done with that one's first ones. Measured, of
+  // 512 tokens of a prompt of 16384 (128 heads) and 66 decoding sequences of up to 32768:
+  // NVFP4 rows 1324 and 557 us with two tiles and one slot of rows, 1305 and 529 with 15
+  // blocks and two; later 1216 and 495 with 15, 1336 and 547 with 14. The prompt with FP8
+  // rows 2179 us with two tiles and one stage, 1552 with 14 blocks and three stages; later
+  // 1334 with those, 1311 with 14 and two, 1249 with 16 and two, 1269 with 17.
+  static constexpr uint32_t kK = 0, kKBlocks = kNv ? kTileBlocks + 6 : kTileBlocks + 7;
   static constexpr uint32_t kKShared = 2 * kTileBlocks - kKBlocks;  // blocks that wait for the tile before
   static_assert(kKBlocks >= kTileBlocks + 4 && kKShared > 0, "the expanding warps write four blocks at first");
   static constexpr uint32_t kQRope = kKBlocks * kKBlock;
-  static constexpr uint32_t kStages = kNv ? 2 : 3;         // P pieces on their way out
+  static constexpr uint32_t kStages = 2;                   // P pieces on their way out
   static constexpr uint32_t kStaged = kQRope + 16384;
   static constexpr uint32_t kRawScore = kStaged + kStages * kPBytes;
   static constexpr uint32_t kRawsScore = kNv ? 2 : 1;
