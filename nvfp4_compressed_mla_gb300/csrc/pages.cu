@@ -74,22 +74,31 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkParam
   }
   // an ordinary load: the count may be replaced below
   const int32_t free_now = min(max(*p.free_count, 0), p.free_capacity);
-  for (int s = tid; s < p.num_seqs; s += kPlanThreads) claim[s] = p.num_forks;
+  int32_t src, dst, len;
+  auto load = [&](int i) {
+    const bool here = i < p.num_forks;
+    src = here ? __ldg(p.src_seqs + i) : -1;
+    dst = here ? __ldg(p.dst_seqs + i) : -1;
+    len = here ? __ldg(p.fork_lens + i) : 0;
+  };
+  load(tid);  // one round's forks stay in registers
+  const bool one = p.num_forks <= kPlanThreads;
+  for (int s = tid; s < p.num_seqs; s += kPlanThreads) {
+    claim[s] = p.num_forks;
+    if (p.seq_lens_out != p.seq_lens) p.seq_lens_out[s] = p.seq_lens[s];
+  }
   __syncthreads();
   for (int i = tid; i < p.num_forks; i += kPlanThreads) {
-    const int32_t dst = __ldg(p.dst_seqs + i);
-    if (__ldg(p.src_seqs + i) != -1 && dst >= 0 && dst < p.num_seqs) atomicMin(claim + dst, i);
+    if (!one) load(i);
+    if (src != -1 && dst >= 0 && dst < p.num_seqs) atomicMin(claim + dst, i);
   }
   __syncthreads();
   const int64_t room = static_cast<int64_t>(p.max_blocks) * p.page.size;
   int64_t asked = 0;
-  int taken = 0, refused = 0;
+  int refused = 0;
   for (int i0 = 0; i0 < p.num_forks; i0 += kPlanThreads) {
     const int i = i0 + tid;
-    const bool here = i < p.num_forks;
-    const int32_t src = here ? __ldg(p.src_seqs + i) : -1;
-    const int32_t dst = here ? __ldg(p.dst_seqs + i) : -1;
-    const int32_t len = here ? __ldg(p.fork_lens + i) : 0;
+    if (!one) load(i);
     bool ok = src >= 0 && src < p.num_seqs && dst >= 0 && dst < p.num_seqs && len >= 0 &&
               len <= room && claim[min(max(dst, 0), p.num_seqs - 1)] == i;
     // ordinary loads: the lengths may be replaced below
@@ -100,30 +109,26 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkParam
     ok = ok && (!need || rank <= free_now);
     int32_t from = -1, to = -1;
     if (ok && need) {
-      ++taken;
       to = __ldg(p.free_pages + (free_now - rank));
       from = p.block_table[static_cast<int64_t>(src) * p.max_blocks + full];
       p.block_table[static_cast<int64_t>(dst) * p.max_blocks + full] = to;
     }
     if (from < 0 || from >= p.num_blocks || to < 0 || to >= p.num_blocks) from = to = -1;
-    if (here) {
+    if (i < p.num_forks) {
       p.shared_blocks[i] = ok ? full : -1;
       p.copy_src[i] = from;
       p.copy_dst[i] = to;
+      if (ok && one) p.seq_lens_out[dst] = len;  // every length was read before the sum
       if (!ok && src != -1) ++refused;
     }
   }
+  // the forks up to the first one without a page have one each
+  if (tid == 0) *p.free_count_out = free_now - static_cast<int32_t>(min(asked, static_cast<int64_t>(free_now)));
+  if (p.refused_count != nullptr && refused > 0) atomicAdd(p.refused_count, refused);
+  if (one) return;
   __syncthreads();  // every length has been read
-  if (p.seq_lens_out != p.seq_lens) {
-    for (int s = tid; s < p.num_seqs; s += kPlanThreads) p.seq_lens_out[s] = p.seq_lens[s];
-    __syncthreads();
-  }
   for (int i = tid; i < p.num_forks; i += kPlanThreads)  // a thread's own results
     if (p.shared_blocks[i] >= 0) p.seq_lens_out[__ldg(p.dst_seqs + i)] = __ldg(p.fork_lens + i);
-  int64_t all = 0;
-  block_scan(taken, all, sums);
-  if (tid == 0) *p.free_count_out = free_now - static_cast<int32_t>(all);
-  if (p.refused_count != nullptr && refused > 0) atomicAdd(p.refused_count, refused);
 }
 
 // The shared entries, 1024 of a fork at a time, and their pages' holders.
@@ -475,28 +480,23 @@ __global__ void __launch_bounds__(kPlanThreads) compact_rank_kernel(const Compac
     used = __ldcg(p.used + w);
     idle = __ldcg(p.idle + w) & ~used;  // a page of a table is not free
   };
-  // sums over the words before the share, in it and behind it, in one pass: first
-  // the two others' totals, then the share's running sums, written per word
-  int64_t before_used = 0, before_idle = 0, all_used = 0, all_idle = 0;
+  // used and free pages before the share, and in all words
+  // (a pair of sums below 2^31 in one word: a block's sum takes half a microsecond)
+  auto both = [](int used, int idle) { return (static_cast<int64_t>(used) << 32) + idle; };
+  int64_t before = 0, all = 0;
   {
-    int64_t bu = 0, bi = 0, au = 0, ai = 0;
+    int64_t b = 0, a = 0;
     for (int32_t w = tid; w < p.words; w += kPlanThreads) {
       uint32_t used, idle;
       words_at(w, used, idle);
-      const int u = __popc(used), i = __popc(idle);
-      au += u;
-      ai += i;
-      if (w < own0) {
-        bu += u;
-        bi += i;
-      }
+      const int64_t n = both(__popc(used), __popc(idle));
+      a += n;
+      if (w < own0) b += n;
     }
-    block_scan(bu, before_used, sums);
-    block_scan(bi, before_idle, sums);
-    block_scan(au, all_used, sums);
-    block_scan(ai, all_idle, sums);
+    if (ctas > 1) block_scan(b, before, sums);
+    block_scan(a, all, sums);
   }
-  const int32_t U = static_cast<int32_t>(all_used), F = static_cast<int32_t>(all_idle);
+  const int32_t U = static_cast<int32_t>(all >> 32), F = static_cast<int32_t>(all);
   const int32_t most = min(min(U, F), p.max_moves);
   if (tid == 0) sh_moves = sh_end = 0;
   // ranks of the first pages of each word of the share
@@ -504,9 +504,8 @@ __global__ void __launch_bounds__(kPlanThreads) compact_rank_kernel(const Compac
     const int32_t w = w0 + tid;
     uint32_t used = 0, idle = 0;
     if (w < own1) words_at(w, used, idle);
-    const int64_t tu = block_scan(__popc(used), before_used, sums) - __popc(used);
-    const int64_t ti = block_scan(__popc(idle), before_idle, sums) - __popc(idle);
-    if (w < own1) p.ranks[w] = make_int2(static_cast<int32_t>(tu), static_cast<int32_t>(ti));
+    const int64_t n = both(__popc(used), __popc(idle)), to = block_scan(n, before, sums) - n;
+    if (w < own1) p.ranks[w] = make_int2(static_cast<int32_t>(to >> 32), static_cast<int32_t>(to));
   }
   __syncthreads();
   // f(page, whether it is used or free, its rank among those from the top or the bottom, the others' rank)
