@@ -84,7 +84,8 @@ PageSize page_division(int32_t size) {
 template <typename Params>
 int32_t launch_cluster_smem(void (*kernel)(Params), const Params& p, int ctas, size_t smem,
                             size_t most, cudaStream_t stream) {
-  if (smem > 48 * 1024 &&
+  // what a kernel has beside it counts towards the 48 KB that need no setting
+  if (smem > 40 * 1024 &&
       cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(most)) != cudaSuccess) {
