@@ -289,6 +289,30 @@ def test_against_the_sparse_decode_over_the_same_rows():
     assert float((lse - ref_lse).abs().max()) < 1e-3
 
 
+def test_thousands_of_sequences():
+    """More sequences and row tiles than the plan takes at a time, among them idle ones."""
+    rng = np.random.default_rng(29)
+    lens = rng.integers(0, 60, 2600)
+    new = np.minimum(lens, rng.choice([0, 1, 1, 1, 3], 2600))
+    c = Case(29, lens, new, 16, page=16)
+    c.check(*run(c))
+
+
+@pytest.mark.parametrize("heads,fmt", [(16, NVFP4), (128, FP8)])
+def test_queries_that_are_no_numbers_stay_in_their_rows(heads, fmt):
+    c = Case(30, [300, 90], [20, 3], heads, fmt)
+    ref = c.reference()
+    c.ql[3, 2, 17], c.qr[21, 1, 5] = 0x7FC0, 0x7FC0  # NaN
+    c.ql[7, 4, 0], c.qr[9, 0, 63] = 0x7F80, 0xFF80   # infinities
+    out, lse = run(c)
+    for t, h in ((3, 2), (21, 1)):
+        assert bool(torch.isnan(out[t, h].float()).all()) and bool(torch.isnan(lse[t, h]))
+    for t, h in ((3, 2), (21, 1), (7, 4), (9, 0)):
+        out[t, h] = dev(ref[0][t, h]).to(out.dtype)
+        lse[t, h] = float(ref[1][t, h])
+    c.check(out, lse, ref=ref)
+
+
 def test_bindings_refuse_what_they_can_see():
     import nvfp4_compressed_mla_gb300 as nm
     c = Case(28, [100], [2], 16)
