@@ -553,8 +553,9 @@ __global__ void __launch_bounds__(kPlanThreads) compact_rank_kernel(const Compac
     }
   });
   if (end > 0) atomicMax(&sh_end, end);
-  for (int32_t i = static_cast<int32_t>(rank) * kPlanThreads + tid; i < p.max_moves;
-       i += static_cast<int32_t>(ctas) * kPlanThreads) {
+  // 64 bits: the lists may be as long as an int32 counts
+  for (int64_t i = static_cast<int64_t>(rank) * kPlanThreads + tid; i < p.max_moves;
+       i += static_cast<int64_t>(ctas) * kPlanThreads) {
     if (i < m) {
       const int32_t from = __ldcg(p.copy_src + i), to = __ldcg(p.copy_dst + i);
       p.moved[from] = to;
