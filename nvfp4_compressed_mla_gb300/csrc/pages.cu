@@ -716,7 +716,9 @@ unsigned row_grid(int64_t rows, int32_t chunks, int sms) {
   const int64_t units = rows * chunks, most = static_cast<int64_t>(sms) * 8;
   return static_cast<unsigned>(units < 1 ? 1 : units < most ? units : most);
 }
-int32_t row_chunks(int32_t max_blocks) { return (max_blocks + kRowChunk - 1) / kRowChunk; }
+int32_t row_chunks(int32_t max_blocks) {  // of up to 2^31 - 1 entries
+  return static_cast<int32_t>((int64_t{max_blocks} + kRowChunk - 1) / kRowChunk);
+}
 
 size_t bitmap_words(int64_t num_blocks) { return static_cast<size_t>((num_blocks + 127) / 128 * 4); }
 
