@@ -286,6 +286,15 @@ __device__ __forceinline__ void bulk_s2s(uint32_t dst_cluster, uint32_t src, uin
 __device__ __forceinline__ void arrive_remote(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
+__device__ __forceinline__ void st_relaxed_cluster(uint32_t addr, uint32_t v) {
+  asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_relaxed_cluster(uint32_t addr) {  // of this CTA's memory
+  uint32_t v;
+  asm volatile("ld.relaxed.cluster.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {  // multiples of 16
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
@@ -357,6 +366,21 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_
   const uint32_t hint = suspend_ns(limit);
   while (true) {
     if (__all_sync(0xffffffffu, mbar_wait_suspend<kCluster>(bar, parity, hint))) return true;
+    const bool late = clock64() - t0 > limit;
+    if (__any_sync(0xffffffffu, late || ld_shared_u32(abort_addr) != 0u)) {
+      if (late) st_shared_u32(abort_addr, 1u);
+      return false;
+    }
+  }
+}
+// The same for a word of another CTA to become that of a tile; `word` is what was read last.
+__device__ __forceinline__ bool warp_wait_word(uint32_t addr, uint32_t tile, uint32_t& word, uint32_t abort_addr,
+                                               long long limit) {
+  if (__all_sync(0xffffffffu, (word >> 1) == tile + 1)) return true;
+  const long long t0 = clock64();
+  while (true) {
+    word = ld_relaxed_cluster(addr);
+    if (__all_sync(0xffffffffu, (word >> 1) == tile + 1)) return true;
     const bool late = clock64() - t0 > limit;
     if (__any_sync(0xffffffffu, late || ld_shared_u32(abort_addr) != 0u)) {
       if (late) st_shared_u32(abort_addr, 1u);
@@ -481,11 +505,18 @@ struct ChunkCtl {  // barriers and words, at the same offsets in every CTA of th
                             kTaskDone = 768, kKHalf = 776, kTmem = 792, kAbort = 796, kSent = 800,
                             kScored = 804, kSummed = 808, kLoaded = 812, kTaskWord = 816, kNoted = 820,
                             kMissing = 848;
-  // 1 + tile and the bits of its 64 keys that exist, a CTA of the pair, 8 tiles:
-  // written where some page does not resolve
+  // A CTA of the pair and 8 tiles: 2 (1 + tile), + 1 where one of its 64 keys has no page,
+  // and then the bits of those that have one. The loader of the CTA writes it into both,
+  // and no barrier says that it has arrived: whoever reads the word waits for its tile's.
   static constexpr uint32_t kMissingTiles = 8;
 };
 static_assert(ChunkCtl::kMissing + 32 * ChunkCtl::kMissingTiles == ChunkLayout<0>::kCtlBytes, "control block");
+// The loader has the place of tile u - kMissingTiles for tile u: the expanding warps have left the rows
+// of tile u - raws, so the MMAs of tile u - raws - 3 are done, and for those both CTAs' softmax warps
+// have read the scores, and before them the word, of tile u - raws - 5.
+static_assert(ChunkCtl::kMissingTiles >= ChunkLayout<0>::kRawsScore + 5 &&
+                  ChunkCtl::kMissingTiles >= ChunkLayout<1>::kRawsScore + 5,
+              "missing keys");
 
 // ------------------------------------------------------------------ expansion
 // Warp w of the eight expands keys 8 w .. 8 w + 7 of each 64; of the rope part a lane
@@ -813,9 +844,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
           if (scoring && (lost[0] | lost[1]) != 0u) {  // the softmax of both CTAs has to know
             if (lane < 2) {
               const uint32_t to = map_rank(ctl + C::kMissing + 32 * (u % C::kMissingTiles) + 16 * part, lane);
-              st_cluster_v4(to, u + 1, ~lost[0], ~lost[1], 0u);
+              st_cluster_u32(to + 4, ~lost[0]);
+              st_cluster_u32(to + 8, ~lost[1]);
             }
-            asm volatile("fence.acq_rel.cluster;" ::: "memory");
+            fence_cluster();
             __syncwarp();
           }
           if (lane == 0) mbar_arrive_tx(full, static_cast<uint32_t>(__popc(have[0]) + __popc(have[1])) * L::kRow);
@@ -827,6 +859,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
             for (int x = 0; x < 2; ++x)
               if ((have[x] >> lane) & 1u) bulk_g2s(dst + (32 * x + lane) * L::kRow, p.cache + off[x], L::kRow, full);
           }
+          // Behind the copies: the next arrival waits until the word has landed. In front of them
+          // 66 single tokens with FP8 rows took 641 us, in place of 561.
+          if (scoring && lane < 2)
+            st_relaxed_cluster(map_rank(ctl + C::kMissing + 32 * (u % C::kMissingTiles) + 16 * part, lane),
+                               2 * (u + 1) + ((lost[0] | lost[1]) != 0u ? 1u : 0u));
+          __syncwarp();
           page = next;
         }
       }
@@ -846,7 +884,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
                  warp_wait<true>(bar(C::kPvDone, ps), ((u / L::kPSlots) & 1) ^ 1, abort_addr, lim));
           if (!run) break;
           const bool noted = ld_shared_u32(ctl + C::kNoted + 4 * (u & 3)) == u + 1;
-          if (noted) asm volatile("fence.acq_rel.cluster;" ::: "memory");  // the notes are there first
+          if (noted) fence_cluster();  // the notes are there first
           if (elect_one())
             bulk_s2s(out_p + ps * kPBytes, sbase + L::kStaged + st * kPBytes, kPBytes, out_full + 8u * ps);
           __syncwarp();
@@ -1129,16 +1167,25 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
           tmem_ld32(s_addr + 32u, s[1]);
           // keys of the piece that the row could see, and those that exist
           const int32_t room = sees - pieces.begin * kTileKeys - kPieceKeys * static_cast<int32_t>(x);
-          uint4 have = ld_shared_v4(ctl + C::kMissing + 32 * (i % C::kMissingTiles) + 16 * half);
-          if (have.x != i + 1) have.y = have.z = 0xffffffffu;
-          const bool all = room >= kPieceKeys && (have.y & have.z) == 0xffffffffu;
+          const uint32_t word_at = ctl + C::kMissing + 32 * (i % C::kMissingTiles) + 16 * half;
+          uint32_t word = ld_relaxed_cluster(word_at);
           tmem_ld_wait();
+          // one branch for the warp: a test at each score cost more than the exponentials
+          const bool all = __all_sync(0xffffffffu, room >= kPieceKeys && word == 2 * (i + 1));
+          uint32_t bits[2] = {0xffffffffu, 0xffffffffu};
+          if (!all) {
+            ok = warp_wait_word(word_at, i, word, abort_addr, lim);
+            if (!ok) break;
+            if (word & 1u) {
+              fence_cluster();
+              bits[0] = ld_shared_u32(word_at + 4);
+              bits[1] = ld_shared_u32(word_at + 8);
+            }
+          }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(C::kSEmpty, b));  // S is read
-          // one branch for the warp: a test at each score cost more than the exponentials
-          if (!__all_sync(0xffffffffu, all)) {
-            uint32_t bits[2] = {have.y, have.z};  // the keys that the row sees
+          if (!all) {  // the keys that the row sees
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
               const int32_t seen = room - 32 * a;
