@@ -1305,8 +1305,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
       const uint32_t o_addr = tmem + lane_base;
       uint32_t tasks = 0;
       for (uint32_t item = 0; ok && pieces.next(); ++item) {
+        // A result may come with its last piece only: the wait for it is as long as those of
+        // all pieces, each of which other warps wait for.
+        const long long n = 2ll * (pieces.end - pieces.begin);
+        const long long all = lim < (1ll << 62) / n ? lim * n : 1ll << 62;
         for (bool rescaling = true; rescaling;) {
-          ok = warp_wait(bar(C::kTask, 0), tasks & 1, abort_addr, lim);
+          ok = warp_wait(bar(C::kTask, 0), tasks & 1, abort_addr, all);
           if (!ok) break;
           ++tasks;
           const uint32_t word = ld_shared_u32(ctl + C::kTaskWord);

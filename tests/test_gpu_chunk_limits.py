@@ -1,4 +1,4 @@
-"""GPU: the dense attention of a step where keys are missing."""
+"""GPU: the dense attention of a step where keys are missing, and where a result takes long."""
 import numpy as np
 import pytest
 import torch
@@ -54,3 +54,44 @@ def test_missing_pages_of_a_context_that_many_clusters_share(page, fmt):
     for _ in range(3):  # the words of an earlier call must not matter
         out, lse = nm.dense_mla_chunk(*c.device(), out_fp32=True)
         c.check(out, lse, True)
+
+
+@pytest.mark.parametrize("fmt", [NVFP4, FP8])
+def test_results_that_take_longer_than_a_wait_may(fmt):
+    """72 tokens behind a million: 36 row tiles of 8192 key tiles, about 10 ms each, under a limit of 2 million
+    cycles (1 ms; a wait for one key tile is a microsecond). All of the context is one page."""
+    import nvfp4_compressed_mla_gb300 as nm
+    c = Case(55, [64], [1], 128, fmt, spare=0)
+    rng = np.random.default_rng(55)
+    n, length = 72, 1 << 20
+    q = torch.from_numpy(rng.standard_normal((n, 128, 576)).astype(np.float32)).to("cuda:0").bfloat16()
+    args = c.device()
+    args[0], args[1] = q[..., :512].contiguous(), q[..., 512:].contiguous()
+    args[2] = torch.tensor([0, n], dtype=I32, device="cuda:0")
+    args[3] = torch.zeros((1, length // 64), dtype=I32, device="cuda:0")
+    args[4] = torch.tensor([length], dtype=I32, device="cuda:0")
+    nm.nvfp4_mla_set_wait_limit(2_000_000)
+    try:
+        out, lse = nm.dense_mla_chunk(*args, out_fp32=True)
+        torch.cuda.synchronize()
+    finally:
+        nm.nvfp4_mla_set_wait_limit(0)
+    lat, rope, _ = c.keys(0)
+    keys = np.concatenate([lat, rope], 1)
+    for t in (0, 35, 71):
+        seen = length - n + t + 1
+        often = seen // 64 + (np.arange(64) < seen % 64)  # so many of the keys that the token sees are this row
+        x = q[t].double().cpu().numpy()
+        z = x @ keys.T * c.sm_scale
+        top = z.max(1, keepdims=True)
+        w = often * np.exp(z - top)
+        total = w.sum(1, keepdims=True)
+        w /= total
+        # scores over 37 steps in fp32; the sum of weights over a third of the pieces of 64 keys, and a few more;
+        # the output over 65536 steps of 16 keys, each off by 2^-23 of the magnitudes' sum, and FP16 weights
+        dz = (np.abs(x) @ np.abs(keys).T).max(1) * c.sm_scale * 37 * 2.0 ** -23
+        dsum = (seen / 64 / 3 + 40) * 2.0 ** -24 + 2.0 ** -20
+        bound = (w @ np.abs(lat)) * (2.0 ** -11 + seen / 16 * 2.0 ** -23 + dsum + 2 * dz)[:, None]
+        assert (np.abs(out[t].double().cpu().numpy() - w @ lat) <= bound).all()
+        error = np.abs(lse[t].double().cpu().numpy() - (top + np.log(total))[:, 0])
+        assert (error <= dz + dsum + 2.0 ** -20 * np.abs(top[:, 0] + np.log(total[:, 0]))).all()
