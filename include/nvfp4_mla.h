@@ -519,7 +519,8 @@ int32_t sparse_mla_select(const void* q_index, const float* weights, const int32
  *                that is left with none gets out = 0 and lse = -inf), and 1
  *                for each malformed sequence (offsets that descend or leave
  *                0..num_q, a length below its new tokens or beyond its
- *                table), whose rows are left as they were
+ *                table), whose rows are left as they were; it stays at
+ *                2^31 - 1 where it would pass that
  * Where a kernel's wait runs out (nvfp4_mla_set_wait_limit), all rows of the
  * step are NaN. dense_mla_chunk_workspace_size returns SIZE_MAX for an
  * invalid shape and 0 for num_q = 0. Results do not depend on what else runs,

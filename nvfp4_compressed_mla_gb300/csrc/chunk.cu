@@ -213,9 +213,23 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   }
 }
 
+// Adds n to a counter that stays at 2^31 - 1 where it would pass that.
+__device__ __forceinline__ void add_saturating(int32_t* count, int64_t n) {
+  int32_t was = *count;
+  while (true) {
+    const int32_t to = static_cast<int32_t>(min(was + n, int64_t{INT32_MAX}));
+    const int32_t seen = atomicCAS(count, was, to);
+    if (seen == was) return;
+    was = seen;
+  }
+}
+
 // Positions without a page, and malformed sequences; launched where they are counted.
 __global__ void __launch_bounds__(256) chunk_check_kernel(const ChunkParams p) {
-  int bad = 0;
+  __shared__ unsigned long long total;
+  if (threadIdx.x == 0) total = 0;
+  __syncthreads();
+  int64_t bad = 0;
   for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x) {
     int32_t start, len;
     if (new_tokens(p, s, start, len) == 0) {
@@ -229,7 +243,9 @@ __global__ void __launch_bounds__(256) chunk_check_kernel(const ChunkParams p) {
       if (page < 0 || page >= p.num_blocks) bad += min(p.page.size, len - b * p.page.size);
     }
   }
-  if (bad > 0) atomicAdd(p.invalid_count, bad);
+  if (bad > 0) atomicAdd(&total, static_cast<unsigned long long>(bad));
+  __syncthreads();
+  if (threadIdx.x == 0 && total > 0) add_saturating(p.invalid_count, static_cast<int64_t>(total));
 }
 
 // The pieces of row tiles that make up a cluster's share, one after the other. The

@@ -1,9 +1,10 @@
-"""GPU: the dense attention of a step where keys are missing, and where a result takes long."""
+"""GPU: the dense attention of a step where keys are missing, where their count and the time that a result takes
+reach their limits."""
 import numpy as np
 import pytest
 import torch
 
-from tests.chunk_cases import FP8, NVFP4, Case
+from tests.chunk_cases import FP8, NVFP4, ROW, Case
 
 pytestmark = pytest.mark.gpu
 
@@ -95,3 +96,30 @@ def test_results_that_take_longer_than_a_wait_may(fmt):
         assert (np.abs(out[t].double().cpu().numpy() - w @ lat) <= bound).all()
         error = np.abs(lse[t].double().cpu().numpy() - (top + np.log(total))[:, 0])
         assert (error <= dz + dsum + 2.0 ** -20 * np.abs(top[:, 0] + np.log(total[:, 0]))).all()
+
+
+def test_count_of_missing_positions_that_passes_32_bits():
+    """Two sequences of pages that do not exist, 2146435072 positions each (about two seconds)."""
+    import nvfp4_compressed_mla_gb300 as nm
+    page, width = 1 << 20, 2047
+    c = Case(60, [5, 5], [1, 1], 1, page=64)
+    args = c.device()
+    args[3] = torch.full((2, width), -1, dtype=I32, device="cuda:0")
+    args[4] = torch.full((2,), page * width, dtype=I32, device="cuda:0")
+    args[6] = torch.zeros(page * ROW[NVFP4], dtype=torch.uint8, device="cuda:0")
+    args[5], args[7], args[8] = page, 1, page * ROW[NVFP4]
+    bad = zero()
+    out, lse = nm.dense_mla_chunk(*args, invalid_count=bad)
+    assert not out.any() and bool(torch.isneginf(lse).all())
+    assert int(bad) == 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("before,after", [(0, 200), (-50, 150), (2 ** 31 - 201, 2 ** 31 - 1), (2 ** 31 - 200, 2 ** 31 - 1),
+                                          (2 ** 31 - 1, 2 ** 31 - 1)])
+def test_count_of_missing_positions_is_added(before, after):
+    import nvfp4_compressed_mla_gb300 as nm
+    c = Case(61, [300, 120, 40], [2, 1, 1], 16, page=16)
+    c.table[0, :5], c.table[1, :] = -1, c.blocks  # 80 positions and 120
+    bad = torch.tensor([before], dtype=I32, device="cuda:0")
+    nm.dense_mla_chunk(*c.device(), invalid_count=bad)
+    assert int(bad) == after
