@@ -499,7 +499,10 @@ int32_t sparse_mla_select(const void* q_index, const float* weights, const int32
  *   q_rope       device bf16 [num_q, num_heads, 64], 16-byte aligned
  *                (operands are FP16: |q_latent|, and |q_rope| * rope_scale /
  *                latent_scale, must stay below 65504; latent_scale counts
- *                for FP8 rows)
+ *                for FP8 rows. Below 2^-14 they are off by 2^-25 at most, and
+ *                a score by 2^-25 * |sm_scale| * latent_scale times the sum of
+ *                the row's magnitudes in those dimensions, as they are before
+ *                latent_scale and rope_scale)
  *   cu_tokens    device int32 [num_seqs + 1], ascending, at most num_q; rows
  *                of out and lse from cu_tokens[num_seqs] on are left as they
  *                were

@@ -1,10 +1,11 @@
 """GPU: the dense attention of a step where keys are missing, where their count and the time that a result takes
-reach their limits."""
+reach their limits, and where operands leave FP16's normal range."""
 import numpy as np
 import pytest
 import torch
 
 from tests.chunk_cases import FP8, NVFP4, ROW, Case
+from workloads.gen import f32_from_bf16
 
 pytestmark = pytest.mark.gpu
 
@@ -123,3 +124,56 @@ def test_count_of_missing_positions_is_added(before, after):
     bad = torch.tensor([before], dtype=I32, device="cuda:0")
     nm.dense_mla_chunk(*c.device(), invalid_count=bad)
     assert int(bad) == after
+
+
+def small_operands(c, tokens):
+    """The case's reference, its bounds widened for operands below FP16's normal range.
+
+    The kernel's operands are q_latent and q_rope * rope_scale (/ latent_scale for FP8 rows) in FP16. Below 2^-14
+    the step is 2^-24, so that an operand is off by 2^-25 at most, and a score by |sm_scale| (times latent_scale
+    for FP8 rows) 2^-25 sum |k_d|, k being a row's values before the scales and d the dimensions of such
+    operands. A score that is off by dz moves its weight by a factor of exp(dz) and the sum of weights by one of
+    exp(max dz) at most, lse by max dz."""
+    out, lse, tol, ltol = c.reference(tokens)
+    lat_scale = c.latent_scale if c.fmt == FP8 else 1.0
+    tiny = lambda q: (np.abs(q) < 2.0 ** -14) & (q != 0)
+    for s in range(c.S):
+        lat, rope, ok = c.keys(s)
+        base = int(c.lens[s]) - int(c.new[s])
+        for i in range(int(c.new[s])):
+            t = int(c.cu[s]) + i
+            if t not in tokens:
+                continue
+            k, r = lat[:base + i + 1], rope[:base + i + 1]
+            ql, qr = f32_from_bf16(c.ql[t]).astype(np.float64), f32_from_bf16(c.qr[t]).astype(np.float64)
+            z = c.sm_scale * (ql @ k.T + qr @ r.T)
+            dz = abs(c.sm_scale) * lat_scale * 2.0 ** -25 * (
+                tiny(ql) @ np.abs(k / lat_scale).T + tiny(qr * c.rope_scale / lat_scale) @ np.abs(r / c.rope_scale).T)
+            w = np.exp(z - lse[t][:, None])
+            tol[t] += (w * np.expm1(dz + dz.max(1, keepdims=True))) @ np.abs(k)
+            ltol[t] += dz.max(1)
+    return out, lse, tol, ltol
+
+
+@pytest.mark.parametrize("heads", [16, 128])
+@pytest.mark.parametrize("fmt,latent_scale,rope_scale,sm_scale,part", [
+    (FP8, 1.0, 2.0 ** -14, 64.0, "rope"),       # the ratio of the scales makes q_rope's operand subnormal
+    (FP8, 2.0 ** 10, 2.0 ** -4, 1.0, "rope"),
+    (FP8, 2.0 ** 10, 2.0 ** -10, 8.0, "rope"),
+    (NVFP4, 1.0, 2.0 ** -14, 64.0, "rope"),
+    (NVFP4, 1.0, 1.0, 2048.0, "latent"),        # small q_latent
+    (FP8, 2.0 ** -3, 1.0, 4096.0, "latent"),
+    (FP8, 1.0, 2.0 ** -14, 1 / 24, "both"),
+])
+def test_operands_below_the_normal_range_of_fp16(heads, fmt, latent_scale, rope_scale, sm_scale, part):
+    import nvfp4_compressed_mla_gb300 as nm
+    c = Case(70, [150, 80], [6, 1], heads, fmt, latent_scale=latent_scale, rope_scale=rope_scale, sm_scale=sm_scale)
+    if part == "rope":
+        c.ql[:] = 0
+    if part == "latent":
+        c.ql -= np.where(c.ql & 0x7F80, 17 << 7, 0).astype(np.uint16)  # times 2^-17
+        c.qr[:] = 0
+    tokens = range(c.n)
+    ref = small_operands(c, tokens)
+    out, lse = nm.dense_mla_chunk(*c.device(), out_fp32=True)
+    c.check(out, lse, True, ref=ref)
