@@ -681,9 +681,12 @@ int32_t launch_after(void (*kernel)(Args...), unsigned grid, unsigned threads, c
   return NVFP4_MLA_OK;
 }
 
-// 16 where the device runs clusters of 16 of this kernel (with `smem` bytes of
-// shared memory a CTA), else 8; asked once a device.
-int large_cluster(const void* kernel, int device, size_t smem) {
+// CTAs of a release's cluster: 16 where the device runs such a cluster with the most shared
+// memory that a call asks for, else 8; asked once a device.
+constexpr size_t kReleaseMost = kReleaseBytes * NVFP4_MLA_MAX_PLAN_SEQS + 4 * kReleaseUnits;
+int release_cluster(int device) {
+  const void* kernel = reinterpret_cast<const void*>(release_kernel);
+  constexpr size_t smem = kReleaseMost;
   constexpr int kDevices = 64;
   static std::atomic<int> known[kDevices];
   int n = device < kDevices ? known[device].load(std::memory_order_relaxed) : 0;
@@ -798,9 +801,8 @@ extern "C" int32_t nvfp4_mla_release(const int32_t* keep_lens, const int32_t* se
                      page_shares_out == page_shares;
   // Its scattered accesses to the counts are what the SMs of a cluster take their
   // time for: sixteen CTAs, where the device holds such a cluster.
-  constexpr size_t kMost = kReleaseBytes * NVFP4_MLA_MAX_PLAN_SEQS + 4 * kReleaseUnits;
-  const int ctas = small ? 1 : large_cluster(reinterpret_cast<const void*>(release_kernel), dev, kMost);
-  return launch_cluster_smem(release_kernel, p, ctas, smem, kMost, static_cast<cudaStream_t>(stream));
+  const int ctas = small ? 1 : release_cluster(dev);
+  return launch_cluster_smem(release_kernel, p, ctas, smem, kReleaseMost, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" size_t nvfp4_mla_compact_workspace_size(int32_t num_blocks) {
