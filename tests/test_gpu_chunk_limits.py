@@ -1,10 +1,11 @@
-"""GPU: the dense attention of a step where keys are missing, where their count and the time that a result takes
-reach their limits, and where operands leave FP16's normal range."""
+"""GPU: the dense attention of a step where keys are missing, where its planning's shared memory, the count of
+missing positions and the time that a result takes reach their limits, and where operands leave FP16's normal range."""
 import numpy as np
 import pytest
 import torch
 
 from tests.chunk_cases import FP8, NVFP4, ROW, Case
+from tests.gpu_cases import dev_tensor as dev
 from workloads.gen import f32_from_bf16
 
 pytestmark = pytest.mark.gpu
@@ -177,3 +178,23 @@ def test_operands_below_the_normal_range_of_fp16(heads, fmt, latent_scale, rope_
     ref = small_operands(c, tokens)
     out, lse = nm.dense_mla_chunk(*c.device(), out_fp32=True)
     c.check(out, lse, True, ref=ref)
+
+
+@pytest.mark.parametrize("seqs", [10240, 10241, 12225, 12288, 16384])
+def test_sequences_around_the_plan_s_shared_memory(seqs):
+    """4 bytes a sequence; most of them are idle."""
+    import nvfp4_compressed_mla_gb300 as nm
+    rng = np.random.default_rng(seqs)
+    new = np.where(rng.random(seqs) < 150 / seqs, rng.integers(1, 6, seqs), 0)
+    new[[0, seqs - 1]] = 1
+    lens = np.where(rng.random(seqs) < 0.1, rng.integers(0, 60, seqs), 0)
+    lens = np.maximum(lens, new)
+    c = Case(seqs, lens, new, 16, page=16)
+    c.table[seqs - 1, 0] = -1
+    args, lens = c.device(), c.lens.copy()
+    lens[np.nonzero(c.new == 0)[0][::7]] = -1  # of a sequence without new tokens nothing is read
+    args[4] = dev(lens)
+    bad = zero()
+    out, lse = nm.dense_mla_chunk(*args, invalid_count=bad)
+    c.check(out, lse)
+    assert int(bad) == unresolved(c) > 0
