@@ -90,14 +90,17 @@ constexpr long long kDrainLimit = 1ll << 31;
 // of small weights: with kHeadroom 7 a third of the pieces had one.
 constexpr float kTau = 15.f, kHeadroom = 2.f;
 // Key tiles' time that a row tile costs beside its own (loading Q, the first
-// score tile before P V can begin, writing O), and the least share of a cluster:
-// a cluster more costs its start and a merge. With 1 / 2 / 3 / 4 / 5 key tiles
-// five prompts of 5000 tokens take 1353 / 1292 / 1231 / 1203 / 1210 us (FP8 rows)
-// and 61 sequences of all kinds 3826 / 3772 / 3700 / 3690 / 3714. With a least share
-// of 4 / 6 / 8 (and 3 key tiles) a token over 8192 keys takes 38.6 / 38.9 / 42.2 us,
-// four over 2048 keys 38.4 / 42.5 / 45.1, 7 tokens over 307 keys 30.7 / 28.8 / 28.7:
-// those need no merge from 6 on (7 with 4 key tiles).
-constexpr int kTileOverhead = 4, kLeastShare = 7;
+// score tile before P V can begin, writing O). With 1 / 2 / 3 / 4 / 5 key tiles
+// five prompts of 5000 tokens take 1312 / 1241 / 1195 / 1155 / 1152 us (FP8 rows)
+// and 61 sequences of all kinds 3730 / 3670 / 3617 / 3613 / 3626.
+// The least share of a cluster is that overhead: a cluster more costs its start
+// and a merge (4 us), a key tile 1.2 us. In a graph, a token of 128 heads over 384 /
+// 768 / 2048 / 8192 keys takes 24.2 / 28.6 / 29.5 / 32.4 us with a least share of 4;
+// 26.0 / 27.8 / 28.5 / 33.6 with 3, 23.8 / 27.0 / 32.3 / 34.1 with 7, 23.7 / 28.2 / 33.5 /
+// 36.9 with 8. Over 97 short steps (1 to 32 sequences of 128 to 16384 tokens, 1 to
+// 20 new ones) 3 is 0.5 % below 4 in the mean (9 % above and below it at the ends),
+// 7 is 3 % above 4, 8 is 6 % and 12 is 11 %.
+constexpr int kTileOverhead = 4, kLeastShare = kTileOverhead;
 
 struct alignas(16) RowTile {  // 256 rows of a sequence
   int32_t seq, rows;     // its rows, 1 .. 256

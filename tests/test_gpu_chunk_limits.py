@@ -198,3 +198,14 @@ def test_sequences_around_the_plan_s_shared_memory(seqs):
     out, lse = nm.dense_mla_chunk(*args, invalid_count=bad)
     c.check(out, lse)
     assert int(bad) == unresolved(c) > 0
+
+
+@pytest.mark.parametrize("heads,new", [(16, 1), (128, 1), (64, 20)])
+def test_a_few_row_tiles_over_any_number_of_key_tiles(heads, new):
+    """Wherever the clusters' shares cut them: 1 to 20 key tiles, and a border beside a multiple of 128 keys."""
+    import nvfp4_compressed_mla_gb300 as nm
+    for k in range(1, 21):
+        for length in (128 * k - 1, 128 * k, 128 * k + 1 + (k % 5) * 20):
+            c = Case(80 + k, [length], [new], heads)
+            out, lse = nm.dense_mla_chunk(*c.device(), out_fp32=True)
+            c.check(out, lse, True, tokens=sorted({0, new // 2, new - 1}))
