@@ -33,21 +33,28 @@
 // kernel from fp32 partial results. Which row is cut, and so a result's last bits, depends on the
 // whole step, but on nothing outside of it: the same arguments give the same bits.
 //
-// Measured (bf16 output, one call of the three kernels; a device's bf16 product of two large
-// matrices: 1906 TFLOP/s at best, 1709 for seconds on end):
-//   NVFP4, 512 tokens of a prompt of 16384, 128 heads      1.21 ms  1896 TFLOP/s
-//   FP8, the same                                          1.23 ms  1873
-//   NVFP4, 5 prompts of up to 5000 tokens, 32 heads        1.09 ms  1594
-//   NVFP4, 61 sequences: prompts, drafts, single tokens    3.42 ms  1745
-//   NVFP4, 66 tokens of 66 contexts of up to 32768         0.49 ms   917 (half of each MMA's rows are empty)
-//   NVFP4, 1 token of 128 heads, 8192 keys                   40 us  (bound by latency)
-//   NVFP4, 7 tokens of 16 heads, 307 keys                    29 us
-// The first two are bound by the MMAs (the score SMs' tensor cores are active 96.5 % of the cycles
-// with NVFP4 rows). With a third of the MMAs the same pipelines (rows, expansion, softmax) take 1.13
-// and 1.19 ms, the 66 tokens 0.46: an MMA of 128 rows would not help those much. What a row tile
+// Measured (bf16 output, one call of the three kernels behind the other; a device's bf16 product of
+// two large matrices: 1906 TFLOP/s at best, 1709 for seconds on end; the first two by the power left):
+//   NVFP4, 512 tokens of a prompt of 16384, 128 heads      1.24 - 1.31 ms  1760 - 1855 TFLOP/s
+//   FP8, the same                                          1.26 - 1.30 ms  1770 - 1820
+//   NVFP4, 5 prompts of up to 5000 tokens, 32 heads        1.12 ms  1560
+//   FP8, the same                                          1.15 ms  1525
+//   NVFP4, 61 sequences: prompts, drafts, single tokens    3.63 ms  1690 (6.1 PFLOP; others by their pairing)
+//   NVFP4, 66 tokens of 66 contexts of up to 32768         0.50 ms   903 (half of each MMA's rows are empty)
+//   FP8, the same                                          0.56 ms   800
+//   NVFP4, the same with 8 / 32 / 64 heads                 0.48 / 0.49 / 0.49 ms
+//   the same with pages of 16, 32 or 48 tokens             1.86 - 1.89 ms; the prompt above 4.59
+//   NVFP4, 1 token of 128 heads, 8192 keys                   37 us  (bound by latency)
+//   NVFP4, 7 tokens of 16 heads, 307 keys                    28 us
+// The prompts are bound by the MMAs (the score SMs' tensor cores are active 95 % of the cycles). With a
+// third of the MMAs the same pipelines (rows, expansion, softmax) took 1.13 and 1.19 ms for the first
+// two, the 66 tokens 0.46: an MMA of 128 rows would not help those much. They do not depend on the
+// rows either, so that fewer heads gain nothing. What a row tile
 // costs beside its key tiles is loading Q and the first tile before P V can begin (8 us, most of it
 // beside the tile before) and writing O (2.6 us). A short call is a chain: plan 3.7 us, rows and Q 5, first scores
 // 2.5, first weights 3, a key tile 1.2 us each, output 2 to 4.5, teardown 2, merge 4 to 9.
+// Pages that are no multiple of 64 tokens are copied row by row, 64 small copies in place of one, behind
+// a lookup of the table that waits for a free slot.
 //
 // Every wait is bounded. A cluster whose wait runs out drains what it has in flight and reports
 // it; the last kernel then writes NaN to all rows of the step.
@@ -477,12 +484,11 @@ struct ChunkLayout {
   // A ring of blocks of keys. Two whole tiles of them would leave no room for what else
   // is worth more: two slots of NVFP4 rows on their way, two stages of P beside the one
   // slot of FP8 rows. So a tile's first kKBlocks - 9 blocks have room beside the tile
-  // before, the others where the MMAs are done with that one's first ones. Measured, of
-  // 512 tokens of a prompt of 16384 (128 heads) and 66 decoding sequences of up to 32768:
-  // NVFP4 rows 1324 and 557 us with two tiles and one slot of rows, 1305 and 529 with 15
-  // blocks and two; later 1216 and 495 with 15, 1336 and 547 with 14. The prompt with FP8
-  // rows 2179 us with two tiles and one stage, 1552 with 14 blocks and three stages; later
-  // 1334 with those, 1311 with 14 and two, 1249 with 16 and two, 1269 with 17.
+  // before, the others where the MMAs are done with that one's first ones. Of 512 tokens
+  // of a prompt of 16384 (128 heads) and 66 single tokens over up to 32768 keys:
+  // NVFP4 rows 1243 and 499 us with 15 blocks and two slots of rows, 1323 and 526 with 14
+  // and two, 1248 and 543 with 16 and one. FP8 rows 1287 and 561 us with 16 blocks and two
+  // stages, 1336 and 568 with 14 and two, 1319 and 570 with 14 and three.
   static constexpr uint32_t kK = 0, kKBlocks = kNv ? kTileBlocks + 6 : kTileBlocks + 7;
   static constexpr uint32_t kKShared = 2 * kTileBlocks - kKBlocks;  // blocks that wait for the tile before
   static_assert(kKBlocks >= kTileBlocks + 4 && kKShared > 0, "the expanding warps write four blocks at first");
@@ -986,8 +992,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kChunkThreads, 1) ch
       // ---------------------------------------------- O += P V
       // The warp follows the P pieces that land in its CTA, has O rescaled where a
       // piece comes with factors and written behind the last piece of a row tile
-      // (tasks of warps 0-7); then the leader's issues the MMAs and the other one
-      // tells it.
+      // (tasks of the twelve rescaling warps); then the leader's issues the MMAs and
+      // the other one tells it.
       constexpr uint32_t kIdesc = (1u << 4) | (1u << 16) | ((256u >> 3) << 17) |
                                   (static_cast<uint32_t>(kTileRows >> 4) << 24);
       const uint32_t peer = map_rank(bar(C::kPReady, 0), 2);
